@@ -17,7 +17,9 @@ const char *const kTraceNames[TR_COUNT] = {
     "kda_conv_tail_checkpoints", "kda_decode_step", "kda_decode_step_fused",
     "kda_decode_step_fused_fp8", "kda_conv_state_update", "kda_decode_multi", "kda_state_accept",
     "kda_prefill_host", "mla_decode_latent", "mla_decode_latent_noalloc", "mla_decode",
-    "kda_check_device_error", "kda_wait_probe"};
+    "kda_check_device_error", "kda_wait_probe", "kda_tree_verify", "kda_tree_accept",
+    "mla_tree_mask", "mla_tree_latent", "mla_tree_decode", "mla_cache_append", "mla_cache_accept",
+    "mla_pages_copy", "mla_pages_free", "mla_pages_fork", "mla_pages_reserve"};
 }  // namespace kda
 
 namespace {
@@ -82,9 +84,10 @@ kda::RecArgs base_args(const kda_params *p) {
 }  // namespace
 
 namespace kda {
-// for the other host-side entry points of the library (kda_host_stream.cu)
+// for the other host-side entry points of the library (kda_host_stream.cu, kda_tree_api.cu)
 kda_status validate_params(const kda_params *p) { return check_params(p); }
 void note_launches(int n) { g_launches += (uint64_t)n; }
+int *device_error() { return device_error_ptr(); }
 }  // namespace kda
 
 extern "C" {
@@ -114,6 +117,7 @@ const char *kda_status_string(kda_status s) {
     case KDA_ERR_BAD_INDEX: return "KDA_ERR_BAD_INDEX: a device-side index was out of range";
     case KDA_ERR_BAD_SEQLENS:
       return "KDA_ERR_BAD_SEQLENS: device-side sequence offsets outside the token rows";
+    case KDA_ERR_NO_PAGES: return "KDA_ERR_NO_PAGES: the cache has too few free pages";
   }
   return "unknown kda_status";
 }
@@ -586,7 +590,8 @@ kda_status kda_check_device_error(cudaStream_t stream) {
     if (cudaMemcpy(ptr, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
       return KDA_ERR_CUDA;
     if (host & kda::ERR_MBAR_TIMEOUT) return KDA_ERR_TIMEOUT;
-    return (host & kda::ERR_BAD_INDEX) ? KDA_ERR_BAD_INDEX : KDA_ERR_BAD_SEQLENS;
+    if (host & kda::ERR_BAD_INDEX) return KDA_ERR_BAD_INDEX;
+    return (host & kda::ERR_BAD_SEQLEN) ? KDA_ERR_BAD_SEQLENS : KDA_ERR_NO_PAGES;
   }
   return KDA_OK;
 }

@@ -8,7 +8,7 @@
 namespace kda {
 
 // bits of the library's sticky device error flag
-enum : int { ERR_MBAR_TIMEOUT = 1, ERR_BAD_SEQLEN = 2, ERR_BAD_INDEX = 4 };
+enum : int { ERR_MBAR_TIMEOUT = 1, ERR_BAD_SEQLEN = 2, ERR_BAD_INDEX = 4, ERR_NO_PAGES = 8 };
 
 // Token-serial recurrence (decode, and the exact-fp32 prefill path).
 struct RecArgs {
@@ -56,6 +56,52 @@ struct MlaArgs {
   int n_split;                 // splits of each sequence's positions (1: none)
   float *part;                 // split partials: [n_split, B, 64, 512] Z, then [.., 64, 2] (m, l)
   void *out;                   // [B, 64, 128] bf16 gated head outputs
+  int *err;
+};
+
+// The KDA layer over trees of drafted tokens (kda_tree.cu).
+struct TreeArgs {
+  int H, n_seqs, n_slots;
+  int max_nodes;               // verify: most nodes of a sequence (sizes the shared memory)
+  int64_t total;               // rows of x_raw, g, beta, gate, out
+  float scale, l2_eps, norm_eps, g_min;
+  int qk_l2norm;
+  const void *x_raw, *conv_w;  // [total, 3HD] io, [3HD, 4] io
+  void *conv_state;            // [slots, 3, 3HD] io (accept updates it)
+  const float *g, *beta;       // [total, H, D], [total, H]
+  void *state;                 // [slots, H, D, D] (accept updates it)
+  const int32_t *slot_idx;     // [n_seqs] or nullptr
+  const int32_t *cu_nodes;     // [n_seqs + 1] nodes of sequence n: rows cu_nodes[n] .. [n + 1]
+  const int32_t *parent;       // [total] earlier node of the same sequence, or -1
+  const int32_t *accept;       // accept: [n_seqs] last accepted node, or -1
+  const void *gate;            // verify: [total, H, D] io or nullptr
+  const float *norm_w;         // [D] or nullptr
+  void *out;                   // verify: [total, H, D] io
+  int *err;
+};
+
+// A pool of cache pages and the sequences' page tables (mla_pages.cu, mla_tree.cu).
+struct PagedCache {
+  void *pool;                  // [n_layers, n_pages, page_size, 576] bf16
+  int n_layers, n_pages, page_size;
+  const int32_t *table;        // [n_seqs, max_pages]
+  int max_pages;
+  const int32_t *lengths;      // [n_seqs] cached positions
+  int *err;
+};
+
+// Latent attention of drafted trees over the paged cache (mla_tree.cu).
+struct TreeAttnArgs {
+  PagedCache c;                // one layer
+  int n_seqs, H;
+  int64_t total;               // drafted nodes of the batch
+  float scale_log2;            // score scale x log2(e)
+  const void *q;               // [total, H, 576] bf16
+  const int32_t *cu_nodes;     // [n_seqs + 1]
+  const int64_t *mask;         // [total] bit j: drafted node j is visible; nullptr: a chain
+  void *z;                     // [total, H, 512]
+  int z_bf16;
+  void *ws;                    // partial sums and the plan
   int *err;
 };
 
@@ -112,5 +158,29 @@ cudaError_t launch_conv_ckpt(const void *x, const void *conv_state, const int32_
                              const int32_t *ckpt_pos, int n_ckpt, int channels, void *out,
                              bool io_bf16, int *err, cudaStream_t s);
 cudaError_t launch_conv_update(const ConvArgs &a, bool io_bf16, cudaStream_t s);
+// outputs of every node of the drafted trees, or (accept) the accepted paths into the state
+cudaError_t launch_tree(const TreeArgs &a, bool accept, int D, bool io_bf16, bool st_bf16,
+                        cudaStream_t s);
+size_t mla_tree_ws_bytes(int n_seqs, int64_t total, int H);
+cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s);
+cudaError_t launch_tree_mask(const int32_t *parent, const int32_t *cu, int n_seqs, int64_t total,
+                             int64_t *mask, int *err, cudaStream_t s);
+cudaError_t launch_cache_append(const PagedCache &c, const int32_t *cu, int n_seqs, int64_t total,
+                                const void *rows, cudaStream_t s);
+cudaError_t launch_cache_accept(const PagedCache &c, const int32_t *cu, int n_seqs, int64_t total,
+                                const int32_t *parent, const int32_t *accept, int32_t *new_lengths,
+                                cudaStream_t s);
+cudaError_t launch_pages_copy(const PagedCache &c, const int32_t *src, const int32_t *dst, int n,
+                              cudaStream_t s);
+// page bookkeeping: refs [n_pages]; table, held, lengths are written
+cudaError_t launch_pages_free(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots,
+                              const int32_t *slots, int n, cudaStream_t s);
+size_t pages_ws_bytes(int n);
+cudaError_t launch_pages_fork(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots,
+                              const int32_t *src, const int32_t *dst, int n, void *ws,
+                              cudaStream_t s);
+cudaError_t launch_pages_reserve(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots,
+                                 const int32_t *slots, const int32_t *extra, int n, void *ws,
+                                 cudaStream_t s);
 
 }  // namespace kda

@@ -12,7 +12,9 @@ enum TraceId {
   TR_PROLOGUE, TR_PREFILL, TR_PREFILL_FP8, TR_PREFILL_CKPT, TR_CONV_TAIL_CKPT, TR_DECODE,
   TR_DECODE_FUSED, TR_DECODE_FUSED_FP8, TR_CONV_UPDATE, TR_DECODE_MULTI, TR_STATE_ACCEPT,
   TR_PREFILL_HOST, TR_MLA_LATENT, TR_MLA_LATENT_NOALLOC, TR_MLA_DECODE, TR_CHECK_ERROR,
-  TR_WAIT_PROBE, TR_COUNT
+  TR_WAIT_PROBE, TR_TREE_VERIFY, TR_TREE_ACCEPT, TR_MLA_TREE_MASK, TR_MLA_TREE_LATENT,
+  TR_MLA_TREE_DECODE, TR_MLA_CACHE_APPEND, TR_MLA_CACHE_ACCEPT, TR_MLA_PAGES_COPY, TR_MLA_PAGES_FREE,
+  TR_MLA_PAGES_FORK, TR_MLA_PAGES_RESERVE, TR_COUNT
 };
 extern const char *const kTraceNames[TR_COUNT];
 

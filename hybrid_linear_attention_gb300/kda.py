@@ -18,7 +18,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libkda.so")
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_WORKSPACE, \
-    KDA_ERR_TIMEOUT, KDA_ERR_BAD_INDEX, KDA_ERR_BAD_SEQLENS = 0, -1, -2, -3, -4, -5, -6, -7
+    KDA_ERR_TIMEOUT, KDA_ERR_BAD_INDEX, KDA_ERR_BAD_SEQLENS, KDA_ERR_NO_PAGES = \
+    0, -1, -2, -3, -4, -5, -6, -7, -8
 KDA_F32, KDA_BF16 = 0, 1
 
 _TORCH_OF = {KDA_F32: torch.float32, KDA_BF16: torch.bfloat16}
@@ -33,6 +34,10 @@ EXPORTS = (
     "kda_check_device_error", "kda_launch_count", "kda_trace_ranges", "kda_wait_probe",
     "mla_decode_workspace_size", "mla_set_split_override", "mla_decode_latent",
     "mla_decode_latent_noalloc", "mla_decode",
+    "kda_tree_verify", "kda_tree_accept", "mla_tree_mask", "mla_tree_workspace_size",
+    "mla_tree_latent", "mla_tree_decode", "mla_cache_append", "mla_cache_accept",
+    "mla_pages_copy", "mla_pages_workspace_size", "mla_pages_free", "mla_pages_fork",
+    "mla_pages_reserve",
 )
 
 
@@ -123,6 +128,29 @@ def load():
             "mla_decode": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, ctypes.c_float,
                                   _vp, _vp, _vp, _vp, _sz, _vp]),
         }
+        tree = [_P, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i64]
+        paged = [_vp, _i32, _i32, _vp, _i32, _vp]  # pool .. lengths of one layer
+        layers = [_vp, _i32, _i32, _i32, _vp, _i32, _vp]  # the same of all layers
+        sig.update({
+            "kda_tree_verify": (_i32, tree + [_i32, _vp, _vp, _vp, _vp]),
+            "kda_tree_accept": (_i32, tree + [_vp, _vp]),
+            "mla_tree_mask": (_i32, [_vp, _vp, _i32, _i64, _vp, _vp]),
+            "mla_tree_workspace_size": (_sz, [_i32, _i64, _i32]),
+            "mla_tree_latent": (_i32, [_vp, _i32] + paged + [_vp, _i32, _i64, _vp, ctypes.c_float,
+                                                             _vp, _i32, _vp, _sz, _vp]),
+            "mla_tree_decode": (_i32, [_vp] * 4 + paged + [_vp, _i32, _i64, _vp, _vp,
+                                                           ctypes.c_float, _vp, _vp, _vp, _vp, _sz,
+                                                           _vp]),
+            "mla_cache_append": (_i32, layers + [_vp, _i32, _i64, _vp, _vp]),
+            "mla_cache_accept": (_i32, layers + [_vp, _i32, _i64, _vp, _vp, _vp, _vp]),
+            "mla_pages_copy": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp]),
+            "mla_pages_workspace_size": (_sz, [_i32]),
+            "mla_pages_free": (_i32, [_i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp]),
+            "mla_pages_fork": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp,
+                                      _vp, _i32, _vp, _sz, _vp]),
+            "mla_pages_reserve": (_i32, [_i32, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp,
+                                         _i32, _vp, _sz, _vp]),
+        })
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
             fn.restype = res
@@ -472,3 +500,207 @@ def mla_decode(q_nope, q_rope, w_uk, w_uv, cache, lengths, gate_logit, q_cat, z,
         float(scale), _ptr(q_cat, bf, "q_cat"), _ptr(z, torch.float32, "z"), _ptr(out, bf, "out"),
         *_ws(workspace), _stream(stream))
     _check(st, "mla_decode")
+
+
+# ---- verifying a tree of drafted tokens -------------------------------------------------------
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+
+
+def _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, slot_idx):
+    io, i32, f32 = p.io_torch, torch.int32, torch.float32
+    total, H, d, n = parent.shape[0], p.H, p.d_k, cu_nodes.numel() - 1
+    _shape(x_raw, (total, 3 * H * d), "x_raw")
+    _shape(conv_w, (3 * H * d, 4), "conv_w")
+    _shape(conv_state, (state.shape[0], 3, 3 * H * d), "conv_state")
+    _shape(g, (total, H, d), "g")
+    _shape(beta, (total, H), "beta")
+    _shape(state, (state.shape[0], H, d, d), "state")
+    _shape(slot_idx, (n,), "slot_idx")
+    return [ctypes.byref(p), _ptr(x_raw, io, "x_raw"), _ptr(conv_w, io, "conv_w"),
+            _ptr(conv_state, io, "conv_state"), _ptr(g, f32, "g"), _ptr(beta, f32, "beta"),
+            _ptr(state, p.state_torch, "state"), state.shape[0], _ptr(slot_idx, i32, "slot_idx"),
+            _ptr(cu_nodes, i32, "cu_nodes"), _ptr(parent, i32, "parent"), n, total]
+
+
+def kda_tree_verify(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, out, *,
+                    max_nodes=64, slot_idx=None, gate_logit=None, norm_w=None, stream=None):
+    """Outputs of every node of the drafted trees: x_raw [nodes, 3*H*d], g [nodes, H, d], beta
+    [nodes, H], parent [nodes] and out [nodes, H, d] packed by cu_nodes [n_seqs + 1]; the pool
+    state and the conv tails are only read."""
+    io = p.io_torch
+    args = _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, slot_idx)
+    _shape(out, g.shape, "out")
+    _shape(gate_logit, g.shape, "gate_logit")
+    _shape(norm_w, (p.d_k,), "norm_w")
+    st = load().kda_tree_verify(*args, int(max_nodes), _ptr(gate_logit, io, "gate_logit"),
+                                _ptr(norm_w, torch.float32, "norm_w"), _ptr(out, io, "out"),
+                                _stream(stream))
+    _check(st, "kda_tree_verify")
+
+
+def kda_tree_accept(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, accept_node, *,
+                    slot_idx=None, stream=None):
+    """The path to accept_node [n_seqs] (-1: none) replayed into the pool state and conv tail."""
+    args = _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, slot_idx)
+    _shape(accept_node, (cu_nodes.numel() - 1,), "accept_node")
+    st = load().kda_tree_accept(*args, _ptr(accept_node, torch.int32, "accept_node"),
+                                _stream(stream))
+    _check(st, "kda_tree_accept")
+
+
+def mla_tree_mask(parent, cu_nodes, mask, *, stream=None):
+    """mask [nodes] int64: bit j = the node itself or its ancestor j, from parent [nodes]."""
+    _shape(mask, parent.shape, "mask")
+    st = load().mla_tree_mask(_ptr(parent, torch.int32, "parent"),
+                              _ptr(cu_nodes, torch.int32, "cu_nodes"), cu_nodes.numel() - 1,
+                              parent.shape[0], _ptr(mask, torch.int64, "mask"), _stream(stream))
+    _check(st, "mla_tree_mask")
+
+
+def mla_tree_workspace_size(n_seqs, total_nodes, H=64):
+    return int(load().mla_tree_workspace_size(int(n_seqs), int(total_nodes), int(H)))
+
+
+def _paged(pool, page_table, lengths, n_seqs):
+    """pool .. lengths of one layer ([n_pages, page_size, 576])."""
+    _shape(pool, (pool.shape[0], pool.shape[1], 576), "pool")
+    if page_table.shape[0] < n_seqs or lengths.shape[0] < n_seqs:
+        raise ValueError("page_table, lengths: fewer rows than sequences")
+    return [_ptr(pool, torch.bfloat16, "pool"), pool.shape[0], pool.shape[1],
+            _ptr(page_table, torch.int32, "page_table"), page_table.shape[1],
+            _ptr(lengths, torch.int32, "lengths")]
+
+
+def _paged_layers(pool, page_table, lengths, n_seqs):
+    """pool .. lengths of all layers ([n_layers, n_pages, page_size, 576])."""
+    if pool.dim() != 4:
+        raise ValueError("pool: expected [n_layers, n_pages, page_size, 576]")
+    one = _paged(pool[0], page_table, lengths, n_seqs)
+    return [_ptr(pool, torch.bfloat16, "pool"), pool.shape[0]] + one[1:]
+
+
+_DTYPE = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
+
+
+def mla_tree_latent(q_cat, pool, page_table, lengths, cu_nodes, z, *, mask=None, scale=MLA_SCALE,
+                    workspace=None, stream=None):
+    """q_cat [nodes, H, 576] bf16, pool [n_pages, page_size, 576] bf16, page_table [n_seqs,
+    max_pages], lengths [n_seqs], cu_nodes [n_seqs + 1], z [nodes, H, 512] fp32 or bf16, mask
+    [nodes] int64 (None: a chain), workspace of mla_tree_workspace_size bytes."""
+    total, H, n = q_cat.shape[0], q_cat.shape[1], cu_nodes.numel() - 1
+    _shape(q_cat, (total, H, 576), "q_cat")
+    _shape(z, (total, H, 512), "z")
+    _shape(mask, (total,), "mask")
+    if z.dtype not in _DTYPE:
+        raise TypeError(f"z: expected float32 or bfloat16, got {z.dtype}")
+    cache = _paged(pool, page_table, lengths, n)
+    st = load().mla_tree_latent(
+        _ptr(q_cat, torch.bfloat16, "q_cat"), H, *cache,
+        _ptr(cu_nodes, torch.int32, "cu_nodes"), n, total, _ptr(mask, torch.int64, "mask"),
+        float(scale), _ptr(z, None, "z"), _DTYPE[z.dtype], *_ws(workspace), _stream(stream))
+    _check(st, "mla_tree_latent")
+
+
+def mla_tree_decode(q_nope, q_rope, w_uk, w_uv, pool, page_table, lengths, cu_nodes, gate_logit,
+                    q_cat, z, out, *, mask=None, scale=MLA_SCALE, workspace=None, stream=None):
+    """One absorbed gated-MLA step for the nodes of drafted trees; q_cat and z are caller-owned
+    intermediates."""
+    bf = torch.bfloat16
+    total, n = q_nope.shape[0], cu_nodes.numel() - 1
+    for t, tail, name in ((q_nope, (64, 128), "q_nope"), (q_rope, (64, 64), "q_rope"),
+                          (gate_logit, (64,), "gate_logit"), (q_cat, (64, 576), "q_cat"),
+                          (z, (64, 512), "z"), (out, (64, 128), "out")):
+        _shape(t, (total,) + tail, name)
+    _shape(w_uk, (64, 128, 512), "w_uk")
+    _shape(w_uv, (64, 128, 512), "w_uv")
+    _shape(mask, (total,), "mask")
+    st = load().mla_tree_decode(
+        _ptr(q_nope, bf, "q_nope"), _ptr(q_rope, bf, "q_rope"), _ptr(w_uk, bf, "w_uk"),
+        _ptr(w_uv, bf, "w_uv"), *_paged(pool, page_table, lengths, n),
+        _ptr(cu_nodes, torch.int32, "cu_nodes"), n, total, _ptr(mask, torch.int64, "mask"),
+        _ptr(gate_logit, bf, "gate_logit"), float(scale), _ptr(q_cat, bf, "q_cat"),
+        _ptr(z, torch.float32, "z"), _ptr(out, bf, "out"), *_ws(workspace), _stream(stream))
+    _check(st, "mla_tree_decode")
+
+
+def mla_cache_append(pool, page_table, lengths, cu_rows, rows, *, stream=None):
+    """rows [n_layers, total, 576] written behind each sequence in pool [n_layers, n_pages,
+    page_size, 576]; lengths stay."""
+    n = cu_rows.numel() - 1
+    _shape(rows, (pool.shape[0], rows.shape[1], 576), "rows")
+    st = load().mla_cache_append(
+        *_paged_layers(pool, page_table, lengths, n), _ptr(cu_rows, torch.int32, "cu_rows"), n,
+        rows.shape[1], _ptr(rows, torch.bfloat16, "rows"), _stream(stream))
+    _check(st, "mla_cache_append")
+
+
+def mla_cache_accept(pool, page_table, lengths, cu_nodes, parent, accept_node, new_lengths, *,
+                     stream=None):
+    """The accepted paths' rows compacted; new_lengths [n_seqs] may be lengths."""
+    n, i32 = cu_nodes.numel() - 1, torch.int32
+    _shape(accept_node, (n,), "accept_node")
+    if new_lengths.shape[0] < n:
+        raise ValueError("new_lengths: fewer rows than sequences")
+    st = load().mla_cache_accept(
+        *_paged_layers(pool, page_table, lengths, n), _ptr(cu_nodes, i32, "cu_nodes"), n,
+        parent.shape[0], _ptr(parent, i32, "parent"), _ptr(accept_node, i32, "accept_node"),
+        _ptr(new_lengths, i32, "new_lengths"), _stream(stream))
+    _check(st, "mla_cache_accept")
+
+
+def mla_pages_copy(pool, src, dst, *, stream=None):
+    """Pages src[i] copied to dst[i] in every layer of pool [n_layers, n_pages, page_size, 576]."""
+    _shape(pool, (pool.shape[0], pool.shape[1], pool.shape[2], 576), "pool")
+    _shape(dst, src.shape, "dst")
+    st = load().mla_pages_copy(_ptr(pool, torch.bfloat16, "pool"), *pool.shape[:3],
+                               _ptr(src, torch.int32, "src"), _ptr(dst, torch.int32, "dst"),
+                               src.numel(), _stream(stream))
+    _check(st, "mla_pages_copy")
+
+
+def mla_pages_workspace_size(n):
+    return int(load().mla_pages_workspace_size(int(n)))
+
+
+def _book(refcount, page_table, held, lengths):
+    i32 = torch.int32
+    _shape(held, (page_table.shape[0],), "held")
+    _shape(lengths, (page_table.shape[0],), "lengths")
+    return [_ptr(refcount, i32, "refcount"), _ptr(page_table, i32, "page_table"),
+            page_table.shape[1], _ptr(held, i32, "held"), _ptr(lengths, i32, "lengths"),
+            page_table.shape[0]]
+
+
+def mla_pages_free(refcount, page_table, held, lengths, slots, *, stream=None):
+    """All pages of the sequences in slots released."""
+    st = load().mla_pages_free(refcount.numel(), *_book(refcount, page_table, held, lengths),
+                               _ptr(slots, torch.int32, "slots"), slots.numel(), _stream(stream))
+    _check(st, "mla_pages_free")
+
+
+def mla_pages_fork(pool, refcount, page_table, held, lengths, src, dst, *, workspace=None,
+                   stream=None):
+    """Sequences dst become copies of src: full pages shared, a partly filled last one copied."""
+    i32 = torch.int32
+    _shape(pool, (pool.shape[0], refcount.numel(), pool.shape[2], 576), "pool")
+    _shape(dst, src.shape, "dst")
+    st = load().mla_pages_fork(
+        _ptr(pool, torch.bfloat16, "pool"), *pool.shape[:3],
+        *_book(refcount, page_table, held, lengths), _ptr(src, i32, "src"), _ptr(dst, i32, "dst"),
+        src.numel(), *_ws(workspace), _stream(stream))
+    _check(st, "mla_pages_fork")
+
+
+def mla_pages_reserve(page_size, refcount, page_table, held, lengths, slots, extra, *,
+                      workspace=None, stream=None):
+    """The pages that sequences `slots` lack for lengths + extra positions."""
+    i32 = torch.int32
+    _shape(extra, slots.shape, "extra")
+    st = load().mla_pages_reserve(
+        refcount.numel(), int(page_size), *_book(refcount, page_table, held, lengths),
+        _ptr(slots, i32, "slots"), _ptr(extra, i32, "extra"), slots.numel(), *_ws(workspace),
+        _stream(stream))
+    _check(st, "mla_pages_reserve")

@@ -62,7 +62,8 @@ typedef enum {
   KDA_ERR_WORKSPACE = -4,
   KDA_ERR_TIMEOUT = -5,
   KDA_ERR_BAD_INDEX = -6,
-  KDA_ERR_BAD_SEQLENS = -7
+  KDA_ERR_BAD_SEQLENS = -7,
+  KDA_ERR_NO_PAGES = -8
 } kda_status;
 
 typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
@@ -333,6 +334,57 @@ kda_status kda_state_accept(const kda_params* p, const void* step_states, int n_
                             const int32_t* slot_idx, cudaStream_t stream);
 
 /*
+ * kda_tree_verify -- a KDA layer's outputs for every node of a tree of drafted tokens, from the
+ * raw projections.  A draft may branch: node i of a sequence follows its parent, an earlier node
+ * of the same sequence, or the sequence itself (parent -1; there may be several such roots).  The
+ * output of a node equals that of kda_decode_step_fused run token by token along its path from
+ * the pool state; the pool state and the conv tail are read and left as they are, and no node's
+ * state is stored.  kda_decode_multi does the same for a chain and keeps every step's state.
+ *
+ *   x_raw       [total_nodes, 3*H*d] io_dtype: raw q|k|v projections of the nodes; the
+ *               convolution runs along each node's path, then into the tail.
+ *   conv_w      [3*H*d, 4]; conv_state [n_slots, 3, 3*H*d] io_dtype (read only).
+ *   g           [total_nodes, H, d] fp32 log-retention; beta [total_nodes, H] fp32.
+ *   state       [n_slots, H, d, d] state_dtype pool (read only); slot_idx [n_seqs] or NULL as in
+ *               kda_decode_step (here two sequences may share a slot).
+ *   cu_nodes    [n_seqs + 1] int32 (device): the nodes of sequence n are rows cu_nodes[n] ..
+ *               cu_nodes[n+1]-1.  A sequence whose offsets fall outside [0, total_nodes], run
+ *               backwards or hold more than max_nodes nodes is skipped (its output rows stay as
+ *               they were) and reported (KDA_ERR_BAD_SEQLENS).
+ *   parent      [total_nodes] int32 (device): index of the parent within the sequence, smaller
+ *               than the node's own, or -1.  Another value is taken as -1 and reported
+ *               (KDA_ERR_BAD_INDEX).
+ *   max_nodes   1..64: the most nodes of any sequence (a smaller value lets more of them run at
+ *               a time).
+ *   gate_logit  [total_nodes, H, d] io_dtype or NULL; norm_w [d] fp32 or NULL, as kda_prefill.
+ *   out         [total_nodes, H, d] io_dtype.  Rows of no sequence stay as they were.
+ * total_nodes at most 2^22.  No counterpart interface is printed on the pages.
+ */
+kda_status kda_tree_verify(const kda_params* p, const void* x_raw, const void* conv_w,
+                           const void* conv_state, const float* g, const float* beta,
+                           const void* state, int n_slots, const int32_t* slot_idx,
+                           const int32_t* cu_nodes, const int32_t* parent, int n_seqs,
+                           int64_t total_nodes, int max_nodes, const void* gate_logit,
+                           const float* norm_w, void* out, cudaStream_t stream);
+
+/*
+ * kda_tree_accept -- writes the accepted path of each verified tree into the pool: the state and
+ * the conv tail in slot(n) become what kda_decode_step_fused run along the path from the root to
+ * node accept_node[n] leaves.  accept_node[n] = -1: nothing was accepted, state and tail stay
+ * bit for bit.  The path's tokens are replayed from the same x_raw, g and beta as the verify call's,
+ * so a state is read once and written once whatever the tree's size.
+ *   accept_node [n_seqs] int32 (device), -1 .. nodes - 1.  Another value is skipped and reported
+ *               (KDA_ERR_BAD_INDEX).
+ *   Other arguments as kda_tree_verify; up to 64 nodes a sequence; slots must be distinct.  The
+ *   tail is a bit-exact copy of the last three raw inputs.
+ */
+kda_status kda_tree_accept(const kda_params* p, const void* x_raw, const void* conv_w,
+                           void* conv_state, const float* g, const float* beta, void* state,
+                           int n_slots, const int32_t* slot_idx, const int32_t* cu_nodes,
+                           const int32_t* parent, int n_seqs, int64_t total_nodes,
+                           const int32_t* accept_node, cudaStream_t stream);
+
+/*
  * kda_prefill_host_workspace_size -- device bytes kda_prefill_host needs for n_seqs sequences
  * cut into segments of at most segment_tokens rows (a positive multiple of 64, at most 2^24),
  * with gate logits when with_gate is nonzero: two sets of segment buffers (raw projections,
@@ -409,9 +461,10 @@ int64_t kda_prefill_host_plan(const int32_t* cu_seqlens, int n_seqs, int64_t tot
                               int64_t segment_tokens, int64_t* bounds, int64_t max_segments);
 
 /* Synchronises `stream`, then reads and clears the library's sticky device error flag
- * (set when a bounded device wait ran out, a device-side index was out of range, or a
- * sequence's offsets fell outside the token rows).  Returns KDA_OK, KDA_ERR_TIMEOUT,
- * KDA_ERR_BAD_INDEX, KDA_ERR_BAD_SEQLENS (in that order of precedence) or KDA_ERR_CUDA. */
+ * (set when a bounded device wait ran out, a device-side index was out of range, a
+ * sequence's offsets fell outside the token rows, or a paged cache had too few free pages).
+ * Returns KDA_OK, KDA_ERR_TIMEOUT, KDA_ERR_BAD_INDEX, KDA_ERR_BAD_SEQLENS, KDA_ERR_NO_PAGES (in
+ * that order of precedence) or KDA_ERR_CUDA. */
 kda_status kda_check_device_error(cudaStream_t stream);
 
 /* Failure detection without a GPU fault: launches a one-thread kernel that waits, with the
