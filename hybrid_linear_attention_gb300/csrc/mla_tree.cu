@@ -7,92 +7,721 @@
 // len + j, is a key of node i where bit j of i's mask is set:
 //     s_t = scale q . [c_t ; r_t],  z = sum_t softmax(s)_t c_t  over the visible positions
 // (z = 0 where none is).
+//
+// What bounds it: a sequence of len positions and R = nodes x heads query rows costs 2176 R len
+// flop over 1152 len bytes, so beyond two nodes of 64 heads the tensor cores are the floor, not
+// the cache's bytes.  z of R rows is 512 fp32 wide: tensor memory (256 KB) holds 64 rows of it
+// beside the scores, and a 64-row product runs the tensor cores at half rate on one SM
+// (measured: 2048 of 4096 multiply-adds a cycle).  So a pair of CTAs works on 128 rows with
+// cta_group::2 products, M = 128 (64 rows each) and N = 256, which run at the full rate
+// (measured: 64 cycles a K = 16 step; N = 128 takes 44 instead of 32):
+//     S[128 x 256 positions] = Q C^T    each CTA holds its 64 query rows and 128 of the
+//                                       positions, all 576 channels, in nine 64-channel blocks;
+//     Z[128 x 512 latents] += P C       each CTA holds its 64 rows of weights and all 256
+//                                       positions of its half of the latents, in eight
+//                                       [64 positions x 128 latents] chunks.
+// The blocks and chunks stream through one ring of seven 16 KB slots in the order in which the
+// products use them (S of tile t + 1 before Z of tile t, so the softmax of t + 1 has a whole Z
+// and S to hide behind).  That loads 272 KB a CTA and 256 positions; TMA brings 41 bytes a cycle
+// and SM from L2 (measured, 12 TB/s), the products need 64, so L2 is the bound, near 64 % of the
+// tensor peak.
+//
+// Work is dealt in tiles of 256 positions: clusters form groups of G that take G row tiles of a
+// sequence side by side (they read the same positions at the same time, so HBM sees them once),
+// and every group takes an equal run of the batch's tiles.  A run that begins or ends inside a
+// sequence leaves partial sums, which tree_combine_kernel merges in a fixed order.
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "kda_tc_ptx.cuh"
+
+#include <atomic>
+#include <cstring>
 
 namespace kda {
 namespace {
 
-constexpr int TL = 512, TK = 576;
+using namespace tc;
 
-__global__ void __launch_bounds__(128) tree_attn_kernel(const TreeAttnArgs a) {
-  __shared__ float s_q[TK], s_p[128], s_red[4];
-  __shared__ int64_t s_at[128];
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = seq_of_token(a.cu_nodes, a.n_seqs, t);
-  const int64_t lo = a.cu_nodes[n], hi = a.cu_nodes[n + 1];
-  if (t < lo || t >= hi) return;  // a row of no sequence
-  if (lo < 0 || hi > a.total || hi - lo > 64) {
-    if (tid == 0 && a.err) atomicOr(a.err, ERR_BAD_SEQLEN);
-    return;
+constexpr int TL = 512, TK = 576, KB = TK / 64;
+constexpr int TILE = 256;            // positions of a tile
+constexpr int RC = 64;               // query rows of a CTA (a pair: 128)
+constexpr int NSLOT = 7;
+constexpr uint32_t SLOT = 16384;
+constexpr uint32_t OFF_Q = 0;                        // [KB][64 rows][128 B]
+constexpr uint32_t OFF_P = KB * RC * 128;            // [4][64 rows][128 B]: 64 positions each
+constexpr uint32_t OFF_R = OFF_P + 4 * RC * 128;     // the ring
+constexpr uint32_t SMEM = OFF_R + NSLOT * SLOT + 1024;
+constexpr uint32_t TM_Z = 0, TM_S = 256;  // Z: two products of 128 columns; S: two buffers of 128
+// warps 0-7 softmax and output, 8 loads, 9-10 help it at a sequence's end, 11 issues products
+constexpr int W_LOAD = 8, W_HELP = 9, W_MMA = 11, NT = 384;
+constexpr int MAX_CLUSTERS = 80;     // of two CTAs (152 SMs: 76)
+constexpr float LAZY = 8.f;          // log2 of how far a row's scores may rise above its reference
+
+// barriers; L: the leading CTA's are used by both
+enum {
+  B_FULL = 0,               // L  a slot's data is there in both CTAs
+  B_EMPTY = B_FULL + NSLOT, //    the products have read a slot
+  B_QFULL = B_EMPTY + NSLOT, B_QEMPTY,  // L, -: the queries
+  B_SFULL, B_SEMPTY = B_SFULL + 2,      // -, L: the two score buffers
+  B_PFULL = B_SEMPTY + 2,   // L  the weights are written, Z is rescaled
+  B_ZFULL,                  //    a tile's value product is done
+  B_ZFREE,                  // L  the output has read Z
+  B_DRAIN, B_N
+};
+
+struct TreeMaps {
+  CUtensorMap q, c;
+};
+// What the clusters leave for the combine kernel: partial sums [2 x clusters][128][512], their
+// (reference, normaliser) [..][128][2], and for every cluster the rows it completes.
+struct Merge {
+  int64_t tiles;            // of the batch
+  int row0, rows;           // rows that this cluster's first run completes (0: none)
+  int first, last;          // workers that hold parts of them
+  int workers, group;
+};
+
+__device__ __forceinline__ float ex2(float x) {  // 2^x, relative error about 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc));
+}
+// arrive on this barrier in both CTAs once the products issued so far are done
+__device__ __forceinline__ void commit2(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// tile load into this CTA, completing on a barrier of the pair (shared::cluster address)
+__device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+// A sequence as the kernel sees it: rows of its nodes, visible positions, tiles.
+struct Seq {
+  int lo, W, len, end, tiles, row_tiles;
+};
+__device__ __forceinline__ Seq seq_of(const TreeAttnArgs &a, int n, bool tell) {
+  Seq s;
+  s.lo = a.cu_nodes[n];
+  const int hi = a.cu_nodes[n + 1];
+  s.W = hi - s.lo;
+  if (s.lo < 0 || hi < s.lo || hi > a.total || s.W > 64) {
+    if (tell && a.err) atomicOr(a.err, ERR_BAD_SEQLEN);
+    s.W = 0;
   }
-  const int W = (int)(hi - lo), i = (int)(t - lo);
-  int64_t len = a.c.lengths[n], end = len + W;
-  if (len < 0 || end > (int64_t)a.c.max_pages * a.c.page_size) {
-    if (tid == 0 && a.err) atomicOr(a.err, ERR_BAD_INDEX);
-    len = end = 0;
+  s.len = a.c.lengths[n];
+  if (s.W > 0 && (s.len < 0 || (int64_t)s.len + s.W > (int64_t)a.c.max_pages * a.c.page_size)) {
+    if (tell && a.err) atomicOr(a.err, ERR_BAD_INDEX);
+    s.len = s.end = 0;  // nothing visible
+  } else {
+    s.end = s.len + s.W;
   }
-  const unsigned long long mask = a.mask ? (unsigned long long)a.mask[t] : (2ull << i) - 1;
-  const bf16 *q = reinterpret_cast<const bf16 *>(a.q) + (t * a.H + h) * TK;
-  for (int c = tid; c < TK; c += 128) s_q[c] = to_f(q[c]);
-  const bf16 *pool = reinterpret_cast<const bf16 *>(a.c.pool);
-  float m = -INFINITY, l = 0.f, z[4] = {0.f, 0.f, 0.f, 0.f};
+  s.tiles = s.W > 0 ? (s.end > 0 ? (s.end - 1) / TILE + 1 : 1) : 0;
+  s.row_tiles = (s.W * a.H + 2 * RC - 1) / (2 * RC);
+  return s;
+}
+
+// This cluster's run of tiles, cut at the sequences' ends; every warp role walks it on its own.
+struct Walk {
+  int n;
+  int64_t off, left;  // place in sequence n's (pass, tile) order, tiles left
+  int group, member;
+  Seq s;
+  int rt, t0, t1;     // the current segment: row tile, tiles t0 .. t1 - 1
+  __device__ __forceinline__ bool next(const TreeAttnArgs &a) {
+    while (left > 0) {
+      s = seq_of(a, n, false);
+      const int64_t all = (int64_t)((s.row_tiles + group - 1) / group) * s.tiles;
+      if (off >= all) {
+        ++n;
+        off = 0;
+        continue;
+      }
+      t0 = (int)(off % s.tiles);
+      rt = (int)(off / s.tiles) * group + member;
+      t1 = s.tiles - t0 < left ? s.tiles : t0 + (int)left;
+      off += t1 - t0;
+      left -= t1 - t0;
+      if (rt < s.row_tiles) return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ int64_t run_start(int64_t tiles, int w, int workers) { return tiles * w / workers; }
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
+    tree_attn_kernel(const TreeAttnArgs a, const __grid_constant__ TreeMaps maps, float *part, float *part_ml,
+                     Merge *merge) {
+  extern __shared__ uint8_t dyn[];
+  __shared__ __align__(8) uint64_t s_bar[B_N];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile uint32_t s_abort;
+  __shared__ unsigned long long s_cost[4];
+  __shared__ int64_t s_scan[NT / 32];
+  __shared__ int s_n;
+  __shared__ int64_t s_off;
+  __shared__ float s_max[4][RC], s_sum[4][RC];
+  const uint32_t raw = smem_u32(dyn);
+  const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+  uint8_t *sm = dyn + pad;
+  const uint32_t sb = raw + pad;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int cid = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  auto bar = [&](int i) { return smem_u32(&s_bar[i]); };
+  if (tid == 0) {
+    for (int i = 0; i < B_N; ++i)
+      mbar_init(bar(i), (i < B_EMPTY || i == B_QFULL || i == B_SEMPTY || i == B_SEMPTY + 1 || i == B_PFULL || i == B_ZFREE)
+                            ? 2 : 1);
+    mbar_fence_init();
+    s_abort = 0;
+    s_n = 0;
+    s_off = 0;
+  }
+  if (tid < 4) s_cost[tid] = 0;
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
   __syncthreads();
-  for (int64_t p0 = 0; p0 < end; p0 += 128) {
-    const int64_t pos = p0 + tid;
-    float s = -INFINITY;
-    s_at[tid] = -1;
-    if (pos < end && (pos < len || ((mask >> (pos - len)) & 1))) {
-      const int page = a.c.table[(int64_t)n * a.c.max_pages + pos / a.c.page_size];
-      if (page >= 0 && page < a.c.n_pages) {
-        const int64_t row = ((int64_t)page * a.c.page_size + pos % a.c.page_size) * TK;
-        s_at[tid] = row;
-        s = 0.f;
-        for (int c = 0; c < TK; c += 4) {
-          const float4 x = load4(pool + row + c);
-          s = fmaf(x.x, s_q[c], fmaf(x.y, s_q[c + 1], fmaf(x.z, s_q[c + 2], fmaf(x.w, s_q[c + 3], s))));
+
+  // ---- the batch's tiles for groups of 1, 2, 4 and 8 clusters, and this cluster's run ----------
+  {
+    unsigned long long c[4] = {0, 0, 0, 0};
+    for (int n = tid; n < a.n_seqs; n += NT) {
+      const Seq s = seq_of(a, n, blockIdx.x == 0);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) c[g] += (unsigned long long)((s.row_tiles + (1 << g) - 1) >> g) * s.tiles;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c[g] += __shfl_xor_sync(0xffffffffu, c[g], o);
+      if (lane == 0 && c[g]) atomicAdd(&s_cost[g], c[g]);
+    }
+  }
+  __syncthreads();
+  // the largest group whose run is within 3 % of the shortest: larger groups read the cache from
+  // HBM fewer times, and lose where row tiles do not divide by them
+  int group = 1, workers = clusters;
+  {
+    float best = INFINITY;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (clusters >> g) best = fminf(best, (float)s_cost[g] / (float)(clusters >> g));
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if ((clusters >> g) && (float)s_cost[g] / (float)(clusters >> g) <= 1.03f * best) group = 1 << g, workers = clusters >> g;
+  }
+  const int64_t tiles = (int64_t)s_cost[31 - __clz(group)];
+  const int worker = cid / group, member = cid % group;
+  const int64_t begin = worker < workers ? run_start(tiles, worker, workers) : 0;
+  const int64_t stop = worker < workers ? run_start(tiles, worker + 1, workers) : 0;
+  if (stop > begin) {  // the sequence that tile `begin` falls in
+    int64_t before = 0;
+    for (int n0 = 0; n0 < a.n_seqs && before <= begin; n0 += NT) {
+      int64_t cost = 0;
+      if (n0 + tid < a.n_seqs) {
+        const Seq s = seq_of(a, n0 + tid, false);
+        cost = (int64_t)((s.row_tiles + group - 1) / group) * s.tiles;
+      }
+      int64_t x = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) s_scan[warp] = x;
+      __syncthreads();
+      int64_t at = before;
+      for (int w = 0; w < warp; ++w) at += s_scan[w];
+      at += x - cost;
+      if (at <= begin && begin < at + cost) s_n = n0 + tid, s_off = begin - at;
+      for (int w = 0; w < NT / 32; ++w) before += s_scan[w];
+      __syncthreads();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tm = s_tmem;
+  Walk walk;
+  walk.n = s_n, walk.off = s_off, walk.left = stop - begin, walk.group = group, walk.member = member;
+  // A wait that runs out raises s_abort; from then on waits fail at once.  The softmax and load
+  // warps then walk on to the end without waiting (they meet on named barriers, which all of them
+  // have to reach), and the loader issues nothing more.
+  auto wait = [&](int i, uint32_t parity) {
+#pragma unroll 1
+    for (long it = 0; it < kWaitLimit; ++it) {
+      if (mbar_try_wait_cluster(bar(i), parity & 1)) return true;
+      if (s_abort) return false;
+    }
+    s_abort = 1;
+    return false;
+  };
+  const int box = a.c.page_size < 64 ? a.c.page_size : 64;  // rows of a tile load
+
+  if (warp == W_LOAD || (warp >= W_HELP && warp < W_MMA)) {
+    // ---- loads: S(0) S(1) Z(0) S(2) Z(1) ..., a slot at a time.  Where a chunk of Z's operand
+    //      reaches past the cached positions, warps 9-10 fill it: rows behind the last drafted
+    //      node and drafted rows with a value that is not finite become zeros there (their weight
+    //      is 0 or NaN, and 0 x NaN must not reach the rows that do not see them).
+    const uint32_t full0 = map_shared_rank(bar(B_FULL), 0), qfull0 = map_shared_rank(bar(B_QFULL), 0);
+    const bool loader = warp == W_LOAD;
+    int fill = 0, segs = 0;
+    struct Tile {
+      Seq s;
+      int n, t, page;  // page: lane e's page of the positions 256 t + e box ..
+    } cur, prev;
+    bool have_prev = false;
+    auto pages = [&](Tile &x) {
+      x.page = a.c.n_pages;  // past the pool: zeros
+      const int pos = TILE * x.t + lane * box;
+      if (lane * box < TILE && pos < x.s.end) {
+        const int p = a.c.table[(size_t)x.n * a.c.max_pages + pos / a.c.page_size];
+        if (p >= 0 && p < a.c.n_pages) x.page = p;
+        else if (a.err) atomicOr(a.err, ERR_BAD_INDEX);
+      }
+    };
+    auto warp_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
+    auto slot_free = [&]() { return fill < NSLOT || warp_wait(B_EMPTY + fill % NSLOT, (uint32_t)(fill / NSLOT - 1)); };
+    auto load_s = [&](const Tile &x) {
+      if (!loader) {
+        fill += KB;
+        return;
+      }
+      const int boxes = 128 / box, e = (int)(128 * rank) / box + (lane < boxes ? lane : 0);
+      const int page = __shfl_sync(0xffffffffu, x.page, e), row = (TILE * x.t + e * box) % a.c.page_size;
+      for (int kb = 0; kb < KB; ++kb, ++fill) {
+        const int j = fill % NSLOT;
+        if (!slot_free()) continue;
+        if (lane == 0) mbar_arrive_expect_tx_remote(bar(B_FULL + j), 0, SLOT);
+        __syncwarp();
+        if (lane < boxes)
+          tma_pair_3d(sb + OFF_R + j * SLOT + lane * box * 128, &maps.c, 64 * kb, row, page, full0 + 8 * j);
+      }
+    };
+    auto load_z = [&](const Tile &x) {
+      const int per = 64 / box, boxes = 2 * per, blk = lane / per, sub = lane % per;
+      for (int h = 0; h < 2; ++h)
+        for (int pc = 0; pc < 4; ++pc, ++fill) {
+          const int j = fill % NSLOT, g0 = TILE * x.t + 64 * pc;
+          if (g0 + 64 > x.s.len && g0 < x.s.end) {
+            uint8_t *slot = sm + OFF_R + j * SLOT;
+            const int ht = tid - 32 * W_HELP, piece = ht & 15;
+            uint4 v[16];
+            bool ok = true;
+            if (!loader) {
+#pragma unroll
+              for (int y = 0; y < 16; ++y) {
+                const int pos = g0 + (ht >> 4) + 4 * y;
+                v[y] = make_uint4(0, 0, 0, 0);
+                if (pos < x.s.end) {
+                  const int p = a.c.table[(size_t)x.n * a.c.max_pages + pos / a.c.page_size];
+                  if (p >= 0 && p < a.c.n_pages)
+                    v[y] = *(reinterpret_cast<const uint4 *>(a.c.pool) +
+                             ((size_t)p * a.c.page_size + pos % a.c.page_size) * (TK / 8) + 32 * rank + 16 * h + piece);
+                }
+              }
+            } else {
+              ok = slot_free();
+            }
+            bar_sync(2, 96);  // the slot is free
+            if (!loader) {
+#pragma unroll
+              for (int y = 0; y < 16; ++y) {
+                const int r = (ht >> 4) + 4 * y;
+                auto odd = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
+                const bool bad = g0 + r >= x.s.len && (odd(v[y].x) || odd(v[y].y) || odd(v[y].z) || odd(v[y].w));
+                const uint32_t any = __ballot_sync(0xffffffffu, bad) & (lane < 16 ? 0xffffu : 0xffff0000u);
+                if (any) v[y] = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(slot + (piece >> 3) * 8192 + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v[y];
+              }
+              fence_proxy_async();
+            }
+            bar_sync(2, 96);  // the slot is written
+            if (loader && lane == 0 && ok) mbar_arrive_remote(bar(B_FULL + j), 0);
+            continue;
+          }
+          if (!loader || !slot_free()) continue;
+          const int e = 64 * pc / box + sub, src = lane < boxes ? e : 0;
+          const int page = __shfl_sync(0xffffffffu, x.page, src), row = (TILE * x.t + src * box) % a.c.page_size;
+          if (lane == 0) mbar_arrive_expect_tx_remote(bar(B_FULL + j), 0, SLOT);
+          __syncwarp();
+          if (lane < boxes)
+            tma_pair_3d(sb + OFF_R + j * SLOT + blk * 8192 + sub * box * 128, &maps.c, 256 * (int)rank + 128 * h + 64 * blk, row,
+                        page, full0 + 8 * j);
         }
-        s *= a.scale_log2;
-      } else if (a.err) {
-        atomicOr(a.err, ERR_BAD_INDEX);
+    };
+    while (walk.next(a)) {
+      if (loader && (segs == 0 || warp_wait(B_QEMPTY, (uint32_t)(segs - 1)))) {
+        const int64_t row = (int64_t)walk.s.lo * a.H + 2 * RC * walk.rt + RC * (int)rank;
+        const int rows = a.total * a.H < RC ? (int)(a.total * a.H) : RC;  // of a box
+        if (lane == 0) mbar_arrive_expect_tx_remote(bar(B_QFULL), 0, KB * rows * 128);
+        __syncwarp();
+        if (lane < KB) tma_pair_3d(sb + OFF_Q + lane * RC * 128, &maps.q, 64 * lane, (int)row, 0, qfull0);
+      }
+      ++segs;
+      for (int t = walk.t0; t < walk.t1; ++t) {
+        cur.s = walk.s, cur.n = walk.n, cur.t = t;
+        if (loader) pages(cur);
+        load_s(cur);
+        if (have_prev) load_z(prev);
+        prev = cur;
+        have_prev = true;
       }
     }
-    const float wm = warp_max(s);
-    if (lane == 0) s_red[warp] = wm;
-    __syncthreads();
-    const float mn = fmaxf(m, fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3])));
-    const float base = mn == -INFINITY ? 0.f : mn, al = exp2f(m - base);
-    s_p[tid] = exp2f(s - base);
-    __syncthreads();
-    float ls = 0.f;
-#pragma unroll
-    for (int y = 0; y < 4; ++y) z[y] *= al;
-    for (int j = 0; j < 128; ++j) {
-      if (s_at[j] < 0) continue;
-      const float p = s_p[j];
-      const float4 x = load4(pool + s_at[j] + 4 * tid);
-      z[0] = fmaf(p, x.x, z[0]), z[1] = fmaf(p, x.y, z[1]), z[2] = fmaf(p, x.z, z[2]), z[3] = fmaf(p, x.w, z[3]);
-      ls += p;
+    if (have_prev) load_z(prev);
+    if (loader) {
+      // every slot and the queries read before the CTA may end
+      for (int j = 0; j < NSLOT; ++j) {
+        const int uses = (fill - j + NSLOT - 1) / NSLOT;
+        if (fill > j) wait(B_EMPTY + j, (uint32_t)(uses - 1));
+      }
+      if (segs > 0) wait(B_QEMPTY, (uint32_t)(segs - 1));
+      if (s_abort && rank == 0)  // a wait ran out: let the copies in flight land
+        for (int j = 0; j < NSLOT; ++j)
+          if (fill > j) mbar_wait_cluster(bar(B_FULL + j), (uint32_t)((fill - j + NSLOT - 1) / NSLOT - 1) & 1);
     }
-    l = l * al + ls;
-    m = mn;
-    __syncthreads();
+  } else if (warp == W_MMA) {
+    // ---- products (one thread of the leading CTA) --------------------------------------------
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t ID_S = idesc(1, 128, 256, 0, 0), ID_Z = idesc(1, 128, 256, 0, 1);
+      int used = 0, segs = 0, i = 0;
+      bool ok = true;
+      auto value = [&](int t, bool first, int seg) {
+        if (!(ok = wait(B_PFULL, (uint32_t)t))) return;
+        if (first && seg > 0 && !(ok = wait(B_ZFREE, (uint32_t)(seg - 1)))) return;
+        for (int h = 0; h < 2; ++h)
+          for (int pc = 0; pc < 4; ++pc, ++used) {
+            const int j = used % NSLOT;
+            if (!(ok = wait(B_FULL + j, (uint32_t)(used / NSLOT)))) return;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma2(tm + TM_Z + 128 * h, sdesc_sw128(sb + OFF_P + pc * RC * 128 + ks * 32, 16, 1024),
+                   sdesc_sw128(sb + OFF_R + j * SLOT + ks * 2048, 8192, 1024), ID_Z, !(first && pc == 0 && ks == 0));
+            commit2(bar(B_EMPTY + j));
+          }
+        commit2(bar(B_ZFULL));
+      };
+      bool prev_first = false;
+      int prev_seg = 0;
+      while (ok && walk.next(a)) {
+        for (int t = walk.t0; t < walk.t1 && ok; ++t, ++i) {
+          const int buf = i & 1;
+          if (t == walk.t0 && !(ok = wait(B_QFULL, (uint32_t)segs))) break;
+          if (i >= 2 && !(ok = wait(B_SEMPTY + buf, (uint32_t)((i >> 1) - 1)))) break;
+          for (int kb = 0; kb < KB; ++kb, ++used) {
+            const int j = used % NSLOT;
+            if (!(ok = wait(B_FULL + j, (uint32_t)(used / NSLOT)))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma2(tm + TM_S + 128 * buf, sdesc_sw128(sb + OFF_Q + kb * RC * 128 + ks * 32, 16, 1024),
+                   sdesc_sw128(sb + OFF_R + j * SLOT + ks * 32, 16, 1024), ID_S, kb > 0 || ks > 0);
+            commit2(bar(B_EMPTY + j));
+          }
+          if (!ok) break;
+          commit2(bar(B_SFULL + buf));
+          if (t == walk.t1 - 1) commit2(bar(B_QEMPTY));
+          if (i > 0) value(i - 1, prev_first, prev_seg);
+          prev_first = t == walk.t0;
+          prev_seg = segs;
+        }
+        ++segs;
+      }
+      if (ok && i > 0) value(i - 1, prev_first, prev_seg);
+      if (!ok) {  // a wait ran out: let the products in flight end
+        commit2(bar(B_DRAIN));
+        mbar_wait_cluster(bar(B_DRAIN), 0);
+      }
+    }
+  } else {
+    // ---- softmax and output: TMEM lane l of S and Z is row l % 64; lanes 64-127 hold the upper
+    //      128 positions of S and the upper 256 latents of Z.  Warp w reads lanes 32 (w & 3) ..,
+    //      and of their 128 columns (positions; of Z's two products the one) half w >> 2.
+    const int qw = warp & 3, hf = warp >> 2, ph = qw >> 1;
+    const int row = (32 * qw + lane) & 63, quarter = 2 * ph + hf;  // this thread's 64 positions of a tile
+    const uint32_t lanes = (uint32_t)(32 * qw) << 16;
+    uint8_t *prow = sm + OFF_P + quarter * RC * 128 + row * 128;
+    int i = 0, segs = 0;
+    while (walk.next(a)) {
+      const int r0 = 2 * RC * walk.rt + RC * (int)rank;  // this CTA's first row of the sequence
+      const int rows = walk.s.W * a.H - r0;              // and how many are there (may be <= 0)
+      const Seq s = walk.s;
+      unsigned long long seen = 0;
+      if (row < rows) {
+        const int node = (r0 + row) / a.H;
+        seen = a.mask ? (unsigned long long)a.mask[s.lo + node] : (2ull << node) - 1;
+        if (s.W < 64) seen &= (1ull << s.W) - 1;
+        if (s.end == 0) seen = 0;  // a bad length: nothing is there
+      }
+      float ref = -INFINITY, sum = 0.f;
+      for (int t = walk.t0; t < walk.t1; ++t, ++i) {
+        const int buf = i & 1;
+        const int p0 = TILE * t + 64 * quarter;  // this thread's first position
+        // the visible ones of its 64 positions, as bits
+        unsigned long long vis = ~0ull;
+        if (p0 + 64 > s.len) {
+          const int d = s.len - p0;  // cached ones among them
+          vis = d >= 0 ? (((1ull << d) - 1) | (seen << d)) : (d > -64 ? seen >> -d : 0ull);
+        }
+        for (int x = 0; x < 64; x += box) {
+          if (p0 + x >= s.end) break;
+          const int p = a.c.table[(size_t)walk.n * a.c.max_pages + (p0 + x) / a.c.page_size];
+          if (p < 0 || p >= a.c.n_pages) vis &= ~((box == 64 ? ~0ull : ((1ull << box) - 1)) << x);
+        }
+        if (rows <= 0) {  // a row tile of one CTA: this one only keeps the pair in step
+          if (tid == 0) {
+            wait(B_SFULL + buf, (uint32_t)(i >> 1));
+            mbar_arrive_remote(bar(B_SEMPTY + buf), 0);
+            if (i > 0) wait(B_ZFULL, (uint32_t)(i - 1));
+            mbar_arrive_remote(bar(B_PFULL), 0);
+          }
+          continue;
+        }
+        wait(B_SFULL + buf, (uint32_t)(i >> 1));
+        tc_fence_after();
+        float v[64];
+        {
+          float x[32], y[32];
+          tmem_ld32(tm + lanes + TM_S + 128 * buf + 64 * hf, x);
+          tmem_ld32(tm + lanes + TM_S + 128 * buf + 64 * hf + 32, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = x[c], v[32 + c] = y[c];
+        }
+        if (vis != ~0ull) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) v[c] = (vis >> c) & 1 ? v[c] : -INFINITY;
+        }
+        float m = fmaxf(v[0], v[1]);
+#pragma unroll
+        for (int c = 2; c < 64; c += 2) m = fmaxf(m, fmaxf(v[c], v[c + 1]));
+        s_max[quarter][row] = m;
+        tc_fence_before();
+        bar_sync(1, 256);
+        if (tid == 0) mbar_arrive_remote(bar(B_SEMPTY + buf), 0);
+        m = fmaxf(fmaxf(s_max[0][row], s_max[1][row]), fmaxf(s_max[2][row], s_max[3][row])) * a.scale_log2;
+        // the reference follows the maximum only when it is passed by 2^8: the weights keep their
+        // relative precision up to there, and Z is rescaled seldom
+        float al = 1.f;
+        if (m > ref + LAZY || ref == -INFINITY) {
+          al = ref == -INFINITY ? 1.f : ex2(ref - m);
+          ref = m;
+        }
+        const float base = ref == -INFINITY ? 0.f : ref;
+        float ls = 0.f;
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float e0 = ex2(fmaf(v[2 * c], a.scale_log2, -base)), e1 = ex2(fmaf(v[2 * c + 1], a.scale_log2, -base));
+          const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
+          w[c] = *reinterpret_cast<const uint32_t *>(&b);
+          // the normaliser sums the weights that the product uses
+          ls += __uint_as_float(w[c] << 16) + __uint_as_float(w[c] & 0xffff0000u);
+        }
+        sum = sum * al + ls;
+        if (i > 0) wait(B_ZFULL, (uint32_t)(i - 1));  // the last tile's weights are read
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4 *>(prow + ((c ^ (row & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        if (__any_sync(0xffffffffu, al != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float z[32];
+            const uint32_t at = tm + lanes + TM_Z + 128 * hf + 32 * c;
+            tmem_ld32(at, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) z[y] *= al;
+            tmem_st32(at, z);
+          }
+          tmem_wait_st();
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        bar_sync(1, 256);
+        if (tid == 0) mbar_arrive_remote(bar(B_PFULL), 0);
+      }
+      // the segment's output
+      const bool whole = walk.t0 == 0 && walk.t1 == s.tiles;
+      const int slot = 2 * cid + (walk.t0 == 0 ? 1 : 0);
+      if (rows > 0 || tid == 0) wait(B_ZFULL, (uint32_t)(i - 1));
+      if (rows > 0) {
+        s_sum[quarter][row] = sum;
+        bar_sync(1, 256);
+        const float l = (s_sum[0][row] + s_sum[1][row]) + (s_sum[2][row] + s_sum[3][row]);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        tc_fence_after();
+        const int64_t out = ((int64_t)s.lo * a.H + r0 + row) * TL + 256 * ph + 128 * hf;
+        float *p = part + ((size_t)slot * 2 * RC + RC * rank + row) * TL + 256 * ph + 128 * hf;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float z[32];
+          tmem_ld32(tm + lanes + TM_Z + 128 * hf + 32 * c, z);
+          tmem_wait_ld();
+          if (row < rows) {
+            if (!whole) {
+#pragma unroll
+              for (int y = 0; y < 32; y += 4) store4(p + 32 * c + y, make_float4(z[y], z[y + 1], z[y + 2], z[y + 3]));
+            } else if (a.z_bf16) {
+              uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<bf16 *>(a.z) + out + 32 * c);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                uint32_t u[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const __nv_bfloat162 b = __floats2bfloat162_rn(z[8 * y + 2 * x] * inv, z[8 * y + 2 * x + 1] * inv);
+                  u[x] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+                dst[y] = make_uint4(u[0], u[1], u[2], u[3]);
+              }
+            } else {
+              float *dst = reinterpret_cast<float *>(a.z) + out + 32 * c;
+#pragma unroll
+              for (int y = 0; y < 32; y += 4)
+                store4(dst + y, make_float4(z[y] * inv, z[y + 1] * inv, z[y + 2] * inv, z[y + 3] * inv));
+            }
+          }
+        }
+        if (!whole && quarter == 0) {
+          float *ml = part_ml + ((size_t)slot * 2 * RC + RC * rank + row) * 2;
+          ml[0] = ref;
+          ml[1] = l;
+        }
+        tc_fence_before();
+      }
+      bar_sync(1, 256);
+      if (tid == 0) mbar_arrive_remote(bar(B_ZFREE), 0);
+      // what the combine kernel merges: a sequence's rows whose last tile is in this run and
+      // whose first is not
+      if (segs == 0 && rank == 0 && tid == 0 && walk.t0 > 0) {
+        Merge g;
+        g.tiles = tiles, g.workers = workers, g.group = group, g.rows = 0, g.row0 = 0, g.first = g.last = 0;
+        if (walk.t1 == s.tiles) {
+          const int64_t first_tile = begin - walk.t0;
+          g.row0 = s.lo * a.H + 2 * RC * walk.rt;
+          g.rows = s.W * a.H - 2 * RC * walk.rt < 2 * RC ? s.W * a.H - 2 * RC * walk.rt : 2 * RC;
+          g.first = (int)(((first_tile + 1) * workers - 1) / tiles);
+          g.last = worker;
+        }
+        merge[cid] = g;
+      } else if (segs == 0 && rank == 0 && tid == 0) {
+        merge[cid].rows = 0;
+      }
+      ++segs;
+    }
+    if (segs == 0 && rank == 0 && tid == 0) merge[cid].rows = 0;
   }
-  const float r = l == 0.f ? 0.f : 1.f / l;
-  const int64_t at = (t * a.H + h) * TL + 4 * tid;
+  if (lane == 0 && s_abort && a.err) atomicOr(a.err, ERR_MBAR_TIMEOUT);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u));
+}
+
+// z = sum_w 2^(m_w - M) Z_w / sum_w 2^(m_w - M) l_w over the workers w that hold parts of a row;
+// 128 threads a row, the parts' loads independent of the running sums.
+__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeAttnArgs a, const float *part, const float *part_ml,
+                                                           const Merge *merge) {
+  const Merge g = merge[blockIdx.x];
+  const int row = 2 * blockIdx.y + (threadIdx.x >> 7), t = threadIdx.x & 127;
+  if (row >= g.rows) return;
+  const int member = blockIdx.x % g.group;
+  // the first worker's part is its last run, the others' their first; a worker without tiles
+  // (more workers than tiles) has none
+  auto slot = [&](int w) { return (size_t)(2 * (w * g.group + member) + (w == g.first ? 1 : 0)) * 2 * RC + row; };
+  auto has = [&](int w) { return run_start(g.tiles, w, g.workers) < run_start(g.tiles, w + 1, g.workers); };
+  float M = -INFINITY;
+  for (int w = g.first; w <= g.last; ++w)
+    if (has(w)) M = fmaxf(M, part_ml[slot(w) * 2]);
+  float z[4] = {0.f, 0.f, 0.f, 0.f}, L = 0.f;
+#pragma unroll 4
+  for (int w = g.first; w <= g.last; ++w) {
+    if (!has(w)) continue;
+    const size_t s = slot(w);
+    const float m = part_ml[s * 2], l = part_ml[s * 2 + 1];
+    const float4 x = load4(part + s * TL + 4 * t);
+    const float f = m == -INFINITY ? (l == 0.f ? 0.f : l) : exp2f(m - M);  // l NaN: the row is NaN
+    L = fmaf(f, l, L);
+    z[0] = fmaf(f, x.x, z[0]), z[1] = fmaf(f, x.y, z[1]), z[2] = fmaf(f, x.z, z[2]), z[3] = fmaf(f, x.w, z[3]);
+  }
+  const float r = L == 0.f ? 0.f : 1.f / L;
   const float4 v = make_float4(z[0] * r, z[1] * r, z[2] * r, z[3] * r);
+  const int64_t at = ((int64_t)g.row0 + row) * TL + 4 * t;
   if (a.z_bf16) store4(reinterpret_cast<bf16 *>(a.z) + at, v);
   else store4(reinterpret_cast<float *>(a.z) + at, v);
 }
 
+bool tree_map(CUtensorMap *m, const void *ptr, int64_t d1, int64_t d2, int box_rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)TK, (cuuint64_t)d1, (cuuint64_t)d2};
+  cuuint64_t strides[2] = {(cuuint64_t)TK * 2, (cuuint64_t)d1 * TK * 2};
+  cuuint32_t bx[3] = {64, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t PART = (size_t)MAX_CLUSTERS * 2 * 2 * RC * TL * sizeof(float);
+constexpr size_t PART_ML = (size_t)MAX_CLUSTERS * 2 * 2 * RC * 2 * sizeof(float);
+
 }  // namespace
 
-size_t mla_tree_ws_bytes(int, int64_t, int) { return 256; }
+size_t mla_tree_ws_bytes(int, int64_t, int) { return PART + PART_ML + MAX_CLUSTERS * sizeof(Merge); }
 
 cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s) {
-  *launches = 1;
-  tree_attn_kernel<<<dim3((unsigned)a.total, a.H), 128, 0, s>>>(a);
+  *launches = 0;
+  TreeMaps maps;
+  memset(&maps, 0, sizeof maps);
+  const int64_t rows = a.total * a.H;
+  const int box = a.c.page_size < 64 ? a.c.page_size : 64;
+  if (!tree_map(&maps.q, a.q, rows, 1, rows < RC ? (int)rows : RC) ||
+      !tree_map(&maps.c, a.c.pool, a.c.page_size, a.c.n_pages, box))
+    return cudaErrorInvalidValue;
+  int dev = 0, nsm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<bool> attr_set[64];  // the opt-in done, per device (idempotent if raced)
+  if (dev >= 64 || !attr_set[dev].load()) {
+    e = cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set[dev].store(true);
+  }
+  const int clusters = nsm / 2 < 1 ? 1 : (nsm / 2 < MAX_CLUSTERS ? nsm / 2 : MAX_CLUSTERS);
+  float *part = reinterpret_cast<float *>(a.ws);
+  float *part_ml = reinterpret_cast<float *>(reinterpret_cast<char *>(a.ws) + PART);
+  Merge *merge = reinterpret_cast<Merge *>(reinterpret_cast<char *>(a.ws) + PART + PART_ML);
+  tree_attn_kernel<<<2 * clusters, NT, SMEM, s>>>(a, maps, part, part_ml, merge);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  tree_combine_kernel<<<dim3(clusters, RC), 256, 0, s>>>(a, part, part_ml, merge);
+  ++*launches;
   return cudaGetLastError();
 }
 
