@@ -52,8 +52,9 @@ constexpr uint32_t OFF_P = KB * RC * 128;            // [4][64 rows][128 B]: 64 
 constexpr uint32_t OFF_R = OFF_P + 4 * RC * 128;     // the ring
 constexpr uint32_t SMEM = OFF_R + NSLOT * SLOT + 1024;
 constexpr uint32_t TM_Z = 0, TM_S = 256;  // Z: two products of 128 columns; S: two buffers of 128
-// warps 0-7 softmax and output, 8 loads, 9-10 help it at a sequence's end, 11 issues products
-constexpr int W_LOAD = 8, W_HELP = 9, W_MMA = 11, NT = 384;
+// warps 0-7 softmax and output, 8 loads, 9 helps it at a sequence's end, 10 tells the leading CTA
+// what the softmax warps have done, 11 issues products
+constexpr int W_LOAD = 8, W_HELP = 9, W_TELL = 10, W_MMA = 11, NT = 384;
 constexpr int MAX_CLUSTERS = 80;     // of two CTAs (152 SMs: 76)
 constexpr float LAZY = 8.f;          // log2 of how far a row's scores may rise above its reference
 
@@ -62,8 +63,8 @@ enum {
   B_FULL = 0,               // L  a slot's data is there in both CTAs
   B_EMPTY = B_FULL + NSLOT, //    the products have read a slot
   B_QFULL = B_EMPTY + NSLOT, B_QEMPTY,  // L, -: the queries
-  B_SFULL, B_SEMPTY = B_SFULL + 2,      // -, L: the two score buffers
-  B_PFULL = B_SEMPTY + 2,   // L  the weights are written, Z is rescaled
+  B_SFULL,                  //    a score buffer is written (two)
+  B_PFULL = B_SFULL + 2,    // L  the scores are read, the weights written, Z is rescaled
   B_ZFULL,                  //    a tile's value product is done
   B_ZFREE,                  // L  the output has read Z
   B_DRAIN, B_N
@@ -106,6 +107,14 @@ __device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
+}
+// arrive on the leading CTA's barrier without ordering anything (a release there costs the thread
+// a cluster-wide fence, about a thousand cycles)
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int n) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 __device__ __forceinline__ void bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -176,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   __shared__ int64_t s_scan[NT / 32];
   __shared__ int s_n;
   __shared__ int64_t s_off;
-  __shared__ float s_max[4][RC], s_sum[4][RC];
+  __shared__ float s_max[2][4][RC], s_sum[4][RC];
   const uint32_t raw = smem_u32(dyn);
   const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
   uint8_t *sm = dyn + pad;
@@ -187,7 +196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   auto bar = [&](int i) { return smem_u32(&s_bar[i]); };
   if (tid == 0) {
     for (int i = 0; i < B_N; ++i)
-      mbar_init(bar(i), (i < B_EMPTY || i == B_QFULL || i == B_SEMPTY || i == B_SEMPTY + 1 || i == B_PFULL || i == B_ZFREE)
+      mbar_init(bar(i), (i < B_EMPTY || i == B_QFULL || i == B_PFULL || i == B_ZFREE)
                             ? 2 : 1);
     mbar_fence_init();
     s_abort = 0;
@@ -266,11 +275,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   walk.n = s_n, walk.off = s_off, walk.left = stop - begin, walk.group = group, walk.member = member;
   // A wait that runs out raises s_abort; from then on waits fail at once.  The softmax and load
   // warps then walk on to the end without waiting (they meet on named barriers, which all of them
-  // have to reach), and the loader issues nothing more.
-  auto wait = [&](int i, uint32_t parity) {
+  // have to reach), and the loader issues nothing more.  `far`: what the other CTA's threads wrote
+  // before they arrived is to be seen too.
+  auto wait = [&](int i, uint32_t parity, bool far = false) {
 #pragma unroll 1
     for (long it = 0; it < kWaitLimit; ++it) {
-      if (mbar_try_wait_cluster(bar(i), parity & 1)) return true;
+      if (far ? mbar_try_wait_cluster(bar(i), parity & 1) : mbar_try_wait(bar(i), parity & 1)) return true;
       if (s_abort) return false;
     }
     s_abort = 1;
@@ -278,9 +288,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   };
   const int box = a.c.page_size < 64 ? a.c.page_size : 64;  // rows of a tile load
 
-  if (warp == W_LOAD || (warp >= W_HELP && warp < W_MMA)) {
+  if (warp == W_LOAD || warp == W_HELP) {
     // ---- loads: S(0) S(1) Z(0) S(2) Z(1) ..., a slot at a time.  Where a chunk of Z's operand
-    //      reaches past the cached positions, warps 9-10 fill it: rows behind the last drafted
+    //      reaches past the cached positions, warp 9 fills it: rows behind the last drafted
     //      node and drafted rows with a value that is not finite become zeros there (their weight
     //      is 0 or NaN, and 0 x NaN must not reach the rows that do not see them).
     const uint32_t full0 = map_shared_rank(bar(B_FULL), 0), qfull0 = map_shared_rank(bar(B_QFULL), 0);
@@ -302,6 +312,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     };
     auto warp_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
     auto slot_free = [&]() { return fill < NSLOT || warp_wait(B_EMPTY + fill % NSLOT, (uint32_t)(fill / NSLOT - 1)); };
+    // the leading CTA's barrier expects both CTAs' bytes; the other CTA only arrives (its bytes
+    // cannot come before the phase they belong to: its slot was freed by that phase's products)
+    auto announce = [&](int i, uint32_t bytes) {
+      if (lane == 0) {
+        if (rank == 0) mbar_expect_tx(bar(i), bytes);
+        else arrive_relaxed(map_shared_rank(bar(i), 0));
+      }
+      __syncwarp();
+    };
     auto load_s = [&](const Tile &x) {
       if (!loader) {
         fill += KB;
@@ -312,8 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       for (int kb = 0; kb < KB; ++kb, ++fill) {
         const int j = fill % NSLOT;
         if (!slot_free()) continue;
-        if (lane == 0) mbar_arrive_expect_tx_remote(bar(B_FULL + j), 0, SLOT);
-        __syncwarp();
+        announce(B_FULL + j, 2 * SLOT);
         if (lane < boxes)
           tma_pair_3d(sb + OFF_R + j * SLOT + lane * box * 128, &maps.c, 64 * kb, row, page, full0 + 8 * j);
       }
@@ -325,13 +343,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           const int j = fill % NSLOT, g0 = TILE * x.t + 64 * pc;
           if (g0 + 64 > x.s.len && g0 < x.s.end) {
             uint8_t *slot = sm + OFF_R + j * SLOT;
-            const int ht = tid - 32 * W_HELP, piece = ht & 15;
+            const int piece = lane & 15;
             uint4 v[16];
             bool ok = true;
-            if (!loader) {
+            auto fetch = [&](int half) {
 #pragma unroll
               for (int y = 0; y < 16; ++y) {
-                const int pos = g0 + (ht >> 4) + 4 * y;
+                const int pos = g0 + 32 * half + (lane >> 4) + 2 * y;
                 v[y] = make_uint4(0, 0, 0, 0);
                 if (pos < x.s.end) {
                   const int p = a.c.table[(size_t)x.n * a.c.max_pages + pos / a.c.page_size];
@@ -340,31 +358,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
                              ((size_t)p * a.c.page_size + pos % a.c.page_size) * (TK / 8) + 32 * rank + 16 * h + piece);
                 }
               }
-            } else {
-              ok = slot_free();
-            }
-            bar_sync(2, 96);  // the slot is free
-            if (!loader) {
+            };
+            auto put = [&](int half) {
 #pragma unroll
               for (int y = 0; y < 16; ++y) {
-                const int r = (ht >> 4) + 4 * y;
+                const int r = 32 * half + (lane >> 4) + 2 * y;
                 auto odd = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
                 const bool bad = g0 + r >= x.s.len && (odd(v[y].x) || odd(v[y].y) || odd(v[y].z) || odd(v[y].w));
                 const uint32_t any = __ballot_sync(0xffffffffu, bad) & (lane < 16 ? 0xffffu : 0xffff0000u);
                 if (any) v[y] = make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4 *>(slot + (piece >> 3) * 8192 + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v[y];
               }
+            };
+            if (loader) ok = slot_free();
+            else fetch(0);
+            bar_sync(2, 64);  // the slot is free
+            if (!loader) {
+              put(0);
+              fetch(1);
+              put(1);
               fence_proxy_async();
             }
-            bar_sync(2, 96);  // the slot is written
+            bar_sync(2, 64);  // the slot is written
             if (loader && lane == 0 && ok) mbar_arrive_remote(bar(B_FULL + j), 0);
             continue;
           }
           if (!loader || !slot_free()) continue;
           const int e = 64 * pc / box + sub, src = lane < boxes ? e : 0;
           const int page = __shfl_sync(0xffffffffu, x.page, src), row = (TILE * x.t + src * box) % a.c.page_size;
-          if (lane == 0) mbar_arrive_expect_tx_remote(bar(B_FULL + j), 0, SLOT);
-          __syncwarp();
+          announce(B_FULL + j, 2 * SLOT);
           if (lane < boxes)
             tma_pair_3d(sb + OFF_R + j * SLOT + blk * 8192 + sub * box * 128, &maps.c, 256 * (int)rank + 128 * h + 64 * blk, row,
                         page, full0 + 8 * j);
@@ -374,8 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       if (loader && (segs == 0 || warp_wait(B_QEMPTY, (uint32_t)(segs - 1)))) {
         const int64_t row = (int64_t)walk.s.lo * a.H + 2 * RC * walk.rt + RC * (int)rank;
         const int rows = a.total * a.H < RC ? (int)(a.total * a.H) : RC;  // of a box
-        if (lane == 0) mbar_arrive_expect_tx_remote(bar(B_QFULL), 0, KB * rows * 128);
-        __syncwarp();
+        announce(B_QFULL, 2 * KB * rows * 128);
         if (lane < KB) tma_pair_3d(sb + OFF_Q + lane * RC * 128, &maps.q, 64 * lane, (int)row, 0, qfull0);
       }
       ++segs;
@@ -406,13 +427,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       constexpr uint32_t ID_S = idesc(1, 128, 256, 0, 0), ID_Z = idesc(1, 128, 256, 0, 1);
       int used = 0, segs = 0, i = 0;
       bool ok = true;
-      auto value = [&](int t, bool first, int seg) {
-        if (!(ok = wait(B_PFULL, (uint32_t)t))) return;
-        if (first && seg > 0 && !(ok = wait(B_ZFREE, (uint32_t)(seg - 1)))) return;
+      // `tail`: the tile reaches past the cached positions (chunks of it are written by threads)
+      auto value = [&](int t, bool first, int seg, bool tail) {
+        if (!(ok = wait(B_PFULL, (uint32_t)t, true))) return;
+        if (first && seg > 0 && !(ok = wait(B_ZFREE, (uint32_t)(seg - 1), true))) return;
         for (int h = 0; h < 2; ++h)
           for (int pc = 0; pc < 4; ++pc, ++used) {
             const int j = used % NSLOT;
-            if (!(ok = wait(B_FULL + j, (uint32_t)(used / NSLOT)))) return;
+            if (!(ok = wait(B_FULL + j, (uint32_t)(used / NSLOT), tail))) return;
             tc_fence_after();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
@@ -422,13 +444,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           }
         commit2(bar(B_ZFULL));
       };
-      bool prev_first = false;
+      bool prev_first = false, prev_tail = false;
       int prev_seg = 0;
       while (ok && walk.next(a)) {
         for (int t = walk.t0; t < walk.t1 && ok; ++t, ++i) {
           const int buf = i & 1;
           if (t == walk.t0 && !(ok = wait(B_QFULL, (uint32_t)segs))) break;
-          if (i >= 2 && !(ok = wait(B_SEMPTY + buf, (uint32_t)((i >> 1) - 1)))) break;
+          // (the scores of tile i - 2 in this buffer are read: Z(i - 2) has waited for that)
           for (int kb = 0; kb < KB; ++kb, ++used) {
             const int j = used % NSLOT;
             if (!(ok = wait(B_FULL + j, (uint32_t)(used / NSLOT)))) break;
@@ -442,17 +464,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           if (!ok) break;
           commit2(bar(B_SFULL + buf));
           if (t == walk.t1 - 1) commit2(bar(B_QEMPTY));
-          if (i > 0) value(i - 1, prev_first, prev_seg);
+          if (i > 0) value(i - 1, prev_first, prev_seg, prev_tail);
           prev_first = t == walk.t0;
+          prev_tail = TILE * (t + 1) > walk.s.len;
           prev_seg = segs;
         }
         ++segs;
       }
-      if (ok && i > 0) value(i - 1, prev_first, prev_seg);
+      if (ok && i > 0) value(i - 1, prev_first, prev_seg, prev_tail);
       if (!ok) {  // a wait ran out: let the products in flight end
         commit2(bar(B_DRAIN));
         mbar_wait_cluster(bar(B_DRAIN), 0);
       }
+    }
+  } else if (warp == W_TELL) {
+    // ---- arrivals on the leading CTA's barriers for the softmax warps, whose next work need not
+    //      wait for the cluster-wide release
+    int i = 0;
+    while (walk.next(a)) {
+      const bool idle = walk.s.W * a.H <= 2 * RC * walk.rt + RC * (int)rank;  // no rows of this CTA
+      for (int t = walk.t0; t < walk.t1; ++t, ++i) {
+        // (the softmax warps come to barrier 3 again only after Z of this tile, so after this)
+        if (!idle) bar_sync(3, 288);
+        else if (i > 0) wait(B_ZFULL, (uint32_t)(i - 1));
+        if (lane == 0) mbar_arrive_remote(bar(B_PFULL), 0);
+      }
+      if (idle) wait(B_ZFULL, (uint32_t)(i - 1));
+      bar_sync(4, 288);
+      if (lane == 0) mbar_arrive_remote(bar(B_ZFREE), 0);
     }
   } else {
     // ---- softmax and output: TMEM lane l of S and Z is row l % 64; lanes 64-127 hold the upper
@@ -475,7 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         if (s.end == 0) seen = 0;  // a bad length: nothing is there
       }
       float ref = -INFINITY, sum = 0.f;
-      for (int t = walk.t0; t < walk.t1; ++t, ++i) {
+      if (rows <= 0) i += walk.t1 - walk.t0;  // a row tile of one CTA: this one's products are not used
+      for (int t = walk.t0; t < walk.t1 && rows > 0; ++t, ++i) {
         const int buf = i & 1;
         const int p0 = TILE * t + 64 * quarter;  // this thread's first position
         // the visible ones of its 64 positions, as bits
@@ -488,15 +528,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           if (p0 + x >= s.end) break;
           const int p = a.c.table[(size_t)walk.n * a.c.max_pages + (p0 + x) / a.c.page_size];
           if (p < 0 || p >= a.c.n_pages) vis &= ~((box == 64 ? ~0ull : ((1ull << box) - 1)) << x);
-        }
-        if (rows <= 0) {  // a row tile of one CTA: this one only keeps the pair in step
-          if (tid == 0) {
-            wait(B_SFULL + buf, (uint32_t)(i >> 1));
-            mbar_arrive_remote(bar(B_SEMPTY + buf), 0);
-            if (i > 0) wait(B_ZFULL, (uint32_t)(i - 1));
-            mbar_arrive_remote(bar(B_PFULL), 0);
-          }
-          continue;
         }
         wait(B_SFULL + buf, (uint32_t)(i >> 1));
         tc_fence_after();
@@ -516,11 +547,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         float m = fmaxf(v[0], v[1]);
 #pragma unroll
         for (int c = 2; c < 64; c += 2) m = fmaxf(m, fmaxf(v[c], v[c + 1]));
-        s_max[quarter][row] = m;
-        tc_fence_before();
+        s_max[buf][quarter][row] = m;  // two buffers: this barrier is a tile's only one
         bar_sync(1, 256);
-        if (tid == 0) mbar_arrive_remote(bar(B_SEMPTY + buf), 0);
-        m = fmaxf(fmaxf(s_max[0][row], s_max[1][row]), fmaxf(s_max[2][row], s_max[3][row])) * a.scale_log2;
+        m = fmaxf(fmaxf(s_max[buf][0][row], s_max[buf][1][row]), fmaxf(s_max[buf][2][row], s_max[buf][3][row])) *
+            a.scale_log2;
         // the reference follows the maximum only when it is passed by 2^8: the weights keep their
         // relative precision up to there, and Z is rescaled seldom
         float al = 1.f;
@@ -560,14 +590,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         }
         fence_proxy_async();
         tc_fence_before();
-        bar_sync(1, 256);
-        if (tid == 0) mbar_arrive_remote(bar(B_PFULL), 0);
+        bar_arrive(3, 288);
       }
       // the segment's output
       const bool whole = walk.t0 == 0 && walk.t1 == s.tiles;
       const int slot = 2 * cid + (walk.t0 == 0 ? 1 : 0);
-      if (rows > 0 || tid == 0) wait(B_ZFULL, (uint32_t)(i - 1));
       if (rows > 0) {
+        wait(B_ZFULL, (uint32_t)(i - 1));
         s_sum[quarter][row] = sum;
         bar_sync(1, 256);
         const float l = (s_sum[0][row] + s_sum[1][row]) + (s_sum[2][row] + s_sum[3][row]);
@@ -610,9 +639,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           ml[1] = l;
         }
         tc_fence_before();
+        bar_arrive(4, 288);
+      } else {
+        bar_sync(4, 288);  // not ahead of the products: a barrier's phases are told apart by parity
       }
-      bar_sync(1, 256);
-      if (tid == 0) mbar_arrive_remote(bar(B_ZFREE), 0);
       // what the combine kernel merges: a sequence's rows whose last tile is in this run and
       // whose first is not
       if (segs == 0 && rank == 0 && tid == 0 && walk.t0 > 0) {

@@ -140,6 +140,15 @@ def test_many_short_sequences():
     case.check(case.run())
 
 
+def test_many_sequences_with_odd_node_counts():
+    """Row tiles of one CTA's rows between full ones, several sequences in every cluster's run."""
+    rng = np.random.default_rng(6)
+    case = Case([int(x) for x in rng.integers(0, 700, 240)], [int(x) for x in rng.integers(1, 5, 240)], seed=192)
+    for _ in range(3):
+        case.check(case.run())
+    kda.kda_check_device_error()
+
+
 def test_same_bits_every_time():
     case = Case([3000, 200], [4, 9], seed=93)
     a, b = case.run(), case.run()
