@@ -67,7 +67,8 @@ enum {
   B_PFULL = B_SFULL + 2,    // L  the scores are read, the weights written, Z is rescaled
   B_ZFULL,                  //    a tile's value product is done
   B_ZFREE,                  // L  the output has read Z
-  B_DRAIN, B_N
+  B_TAIL,                   //    a slot that threads have to look over has landed
+  B_DRAIN = B_TAIL + NSLOT, B_N
 };
 
 struct TreeMaps {
@@ -76,10 +77,9 @@ struct TreeMaps {
 // What the clusters leave for the combine kernel: partial sums [2 x clusters][128][512], their
 // (reference, normaliser) [..][128][2], and for every cluster the rows it completes.
 struct Merge {
-  int64_t tiles;            // of the batch
   int row0, rows;           // rows that this cluster's first run completes (0: none)
   int first, last;          // workers that hold parts of them
-  int workers, group;
+  int group, pad[3];
 };
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, relative error about 2^-22
@@ -147,22 +147,21 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnArgs &a, int n, bool tell) {
 
 // This cluster's run of tiles, cut at the sequences' ends; every warp role walks it on its own.
 struct Walk {
-  int n;
-  int64_t off, left;  // place in sequence n's (pass, tile) order, tiles left
+  int n, off;    // place in sequence n's (pass, tile) order (at most 2^26 tiles)
+  int64_t left;  // tiles left
   int group, member;
   Seq s;
   int rt, t0, t1;     // the current segment: row tile, tiles t0 .. t1 - 1
   __device__ __forceinline__ bool next(const TreeAttnArgs &a) {
     while (left > 0) {
       s = seq_of(a, n, false);
-      const int64_t all = (int64_t)((s.row_tiles + group - 1) / group) * s.tiles;
-      if (off >= all) {
+      if (off >= (s.row_tiles + group - 1) / group * s.tiles) {
         ++n;
         off = 0;
         continue;
       }
-      t0 = (int)(off % s.tiles);
-      rt = (int)(off / s.tiles) * group + member;
+      t0 = off % s.tiles;
+      rt = off / s.tiles * group + member;
       t1 = s.tiles - t0 < left ? s.tiles : t0 + (int)left;
       off += t1 - t0;
       left -= t1 - t0;
@@ -183,8 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   __shared__ volatile uint32_t s_abort;
   __shared__ unsigned long long s_cost[4];
   __shared__ int64_t s_scan[NT / 32];
-  __shared__ int s_n;
-  __shared__ int64_t s_off;
+  __shared__ int s_n, s_off;
   __shared__ float s_max[2][4][RC], s_sum[4][RC];
   const uint32_t raw = smem_u32(dyn);
   const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
@@ -239,6 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       if ((clusters >> g) && (float)s_cost[g] / (float)(clusters >> g) <= 1.03f * best) group = 1 << g, workers = clusters >> g;
   }
   const int64_t tiles = (int64_t)s_cost[31 - __clz(group)];
+  if (tiles < workers) workers = (int)tiles;  // so every worker has a run
   const int worker = cid / group, member = cid % group;
   const int64_t begin = worker < workers ? run_start(tiles, worker, workers) : 0;
   const int64_t stop = worker < workers ? run_start(tiles, worker + 1, workers) : 0;
@@ -261,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       int64_t at = before;
       for (int w = 0; w < warp; ++w) at += s_scan[w];
       at += x - cost;
-      if (at <= begin && begin < at + cost) s_n = n0 + tid, s_off = begin - at;
+      if (at <= begin && begin < at + cost) s_n = n0 + tid, s_off = (int)(begin - at);
       for (int w = 0; w < NT / 32; ++w) before += s_scan[w];
       __syncthreads();
     }
@@ -290,22 +289,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 
   if (warp == W_LOAD || warp == W_HELP) {
     // ---- loads: S(0) S(1) Z(0) S(2) Z(1) ..., a slot at a time.  Where a chunk of Z's operand
-    //      reaches past the cached positions, warp 9 fills it: rows behind the last drafted
-    //      node and drafted rows with a value that is not finite become zeros there (their weight
-    //      is 0 or NaN, and 0 x NaN must not reach the rows that do not see them).
+    //      reaches past the cached positions, warp 9 looks it over before the products may use
+    //      it: rows behind the last drafted node and drafted rows with a value that is not finite
+    //      become zeros there (their weight is 0 or NaN, and 0 x NaN must not reach the rows that
+    //      do not see them).
     const uint32_t full0 = map_shared_rank(bar(B_FULL), 0), qfull0 = map_shared_rank(bar(B_QFULL), 0);
     const bool loader = warp == W_LOAD;
+    const int boxes = 128 / box;             // tile loads of a slot, one lane each
+    const int lb = 31 - __clz(box), lp = 31 - __clz(a.c.page_size);
+    const int sub = lane & (64 / box - 1), blk = (lane * box) >> 6;  // of a value chunk: rows, latents
     int fill = 0, segs = 0;
+    uint32_t looked = 0;                     // parity of B_TAIL + j
     struct Tile {
-      Seq s;
-      int n, t, page;  // page: lane e's page of the positions 256 t + e box ..
+      int len, end, n, t, page;  // page: lane e's page of the positions 256 t + e box ..
     } cur, prev;
     bool have_prev = false;
     auto pages = [&](Tile &x) {
       x.page = a.c.n_pages;  // past the pool: zeros
       const int pos = TILE * x.t + lane * box;
-      if (lane * box < TILE && pos < x.s.end) {
-        const int p = a.c.table[(size_t)x.n * a.c.max_pages + pos / a.c.page_size];
+      if (lane * box < TILE && pos < x.end) {
+        const int p = a.c.table[(size_t)x.n * a.c.max_pages + (pos >> lp)];
         if (p >= 0 && p < a.c.n_pages) x.page = p;
         else if (a.err) atomicOr(a.err, ERR_BAD_INDEX);
       }
@@ -326,8 +329,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         fill += KB;
         return;
       }
-      const int boxes = 128 / box, e = (int)(128 * rank) / box + (lane < boxes ? lane : 0);
-      const int page = __shfl_sync(0xffffffffu, x.page, e), row = (TILE * x.t + e * box) % a.c.page_size;
+      const int e = ((128 * (int)rank) >> lb) + (lane < boxes ? lane : 0);
+      const int page = __shfl_sync(0xffffffffu, x.page, e), row = (TILE * x.t + (e << lb)) & (a.c.page_size - 1);
       for (int kb = 0; kb < KB; ++kb, ++fill) {
         const int j = fill % NSLOT;
         if (!slot_free()) continue;
@@ -337,60 +340,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       }
     };
     auto load_z = [&](const Tile &x) {
-      const int per = 64 / box, boxes = 2 * per, blk = lane / per, sub = lane % per;
-      for (int h = 0; h < 2; ++h)
-        for (int pc = 0; pc < 4; ++pc, ++fill) {
-          const int j = fill % NSLOT, g0 = TILE * x.t + 64 * pc;
-          if (g0 + 64 > x.s.len && g0 < x.s.end) {
-            uint8_t *slot = sm + OFF_R + j * SLOT;
-            const int piece = lane & 15;
-            uint4 v[16];
-            bool ok = true;
-            auto fetch = [&](int half) {
-#pragma unroll
-              for (int y = 0; y < 16; ++y) {
-                const int pos = g0 + 32 * half + (lane >> 4) + 2 * y;
-                v[y] = make_uint4(0, 0, 0, 0);
-                if (pos < x.s.end) {
-                  const int p = a.c.table[(size_t)x.n * a.c.max_pages + pos / a.c.page_size];
-                  if (p >= 0 && p < a.c.n_pages)
-                    v[y] = *(reinterpret_cast<const uint4 *>(a.c.pool) +
-                             ((size_t)p * a.c.page_size + pos % a.c.page_size) * (TK / 8) + 32 * rank + 16 * h + piece);
-                }
-              }
-            };
-            auto put = [&](int half) {
-#pragma unroll
-              for (int y = 0; y < 16; ++y) {
-                const int r = 32 * half + (lane >> 4) + 2 * y;
-                auto odd = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
-                const bool bad = g0 + r >= x.s.len && (odd(v[y].x) || odd(v[y].y) || odd(v[y].z) || odd(v[y].w));
-                const uint32_t any = __ballot_sync(0xffffffffu, bad) & (lane < 16 ? 0xffffu : 0xffff0000u);
-                if (any) v[y] = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(slot + (piece >> 3) * 8192 + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = v[y];
-              }
-            };
-            if (loader) ok = slot_free();
-            else fetch(0);
-            bar_sync(2, 64);  // the slot is free
-            if (!loader) {
-              put(0);
-              fetch(1);
-              put(1);
-              fence_proxy_async();
-            }
-            bar_sync(2, 64);  // the slot is written
-            if (loader && lane == 0 && ok) mbar_arrive_remote(bar(B_FULL + j), 0);
-            continue;
-          }
-          if (!loader || !slot_free()) continue;
-          const int e = 64 * pc / box + sub, src = lane < boxes ? e : 0;
-          const int page = __shfl_sync(0xffffffffu, x.page, src), row = (TILE * x.t + src * box) % a.c.page_size;
-          announce(B_FULL + j, 2 * SLOT);
+#pragma unroll 1
+      for (int hp = 0; hp < 8; ++hp, ++fill) {
+        const int j = fill % NSLOT, h = hp >> 2, pc = hp & 3, g0 = TILE * x.t + 64 * pc;
+        const bool tail = g0 + 64 > x.len && g0 < x.end;
+        if (loader) {
+          const int e = ((64 * pc) >> lb) + sub;
+          const int page = __shfl_sync(0xffffffffu, x.page, e), row = (TILE * x.t + (e << lb)) & (a.c.page_size - 1);
+          if (!slot_free()) continue;
+          if (!tail) announce(B_FULL + j, 2 * SLOT);
+          else if (lane == 0) mbar_expect_tx(bar(B_TAIL + j), SLOT);
+          __syncwarp();
           if (lane < boxes)
-            tma_pair_3d(sb + OFF_R + j * SLOT + blk * 8192 + sub * box * 128, &maps.c, 256 * (int)rank + 128 * h + 64 * blk, row,
-                        page, full0 + 8 * j);
+            tma_pair_3d(sb + OFF_R + j * SLOT + blk * 8192 + sub * box * 128, &maps.c, 256 * (int)rank + 128 * h + 64 * blk,
+                        row, page, tail ? map_shared_rank(bar(B_TAIL + j), rank) : full0 + 8 * j);
+        } else if (tail) {
+          const bool ok = warp_wait(B_TAIL + j, (looked >> j) & 1);
+          looked ^= 1u << j;
+          uint8_t *slot = sm + OFF_R + j * SLOT;
+          const int piece = lane & 15;
+          // two rows at a time, 16 lanes each
+          for (int r0 = x.len > g0 ? x.len - g0 : 0; r0 < 64; r0 += 2) {
+            const int r = r0 + (lane >> 4);
+            uint4 *at = reinterpret_cast<uint4 *>(slot + (piece >> 3) * 8192 + (r & 63) * 128 + (((piece & 7) ^ (r & 7)) << 4));
+            bool bad = false;
+            if (g0 + r0 < x.end) {
+              auto odd = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
+              const uint4 v = *at;
+              bad = odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w);
+            }
+            const uint32_t any = __ballot_sync(0xffffffffu, bad) & (lane < 16 ? 0xffffu : 0xffff0000u);
+            if (r < 64 && (any || g0 + r >= x.end)) *at = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive_remote(bar(B_FULL + j), 0);
         }
+      }
     };
     while (walk.next(a)) {
       if (loader && (segs == 0 || warp_wait(B_QEMPTY, (uint32_t)(segs - 1)))) {
@@ -401,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       }
       ++segs;
       for (int t = walk.t0; t < walk.t1; ++t) {
-        cur.s = walk.s, cur.n = walk.n, cur.t = t;
+        cur.len = walk.s.len, cur.end = walk.s.end, cur.n = walk.n, cur.t = t;
         if (loader) pages(cur);
         load_s(cur);
         if (have_prev) load_z(prev);
@@ -417,9 +403,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         if (fill > j) wait(B_EMPTY + j, (uint32_t)(uses - 1));
       }
       if (segs > 0) wait(B_QEMPTY, (uint32_t)(segs - 1));
-      if (s_abort && rank == 0)  // a wait ran out: let the copies in flight land
-        for (int j = 0; j < NSLOT; ++j)
-          if (fill > j) mbar_wait_cluster(bar(B_FULL + j), (uint32_t)((fill - j + NSLOT - 1) / NSLOT - 1) & 1);
+      if (s_abort)  // a wait ran out: let the copies in flight land
+        for (int y = 0; y < 100; ++y) __nanosleep(10000);
     }
   } else if (warp == W_MMA) {
     // ---- products (one thread of the leading CTA) --------------------------------------------
@@ -500,6 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     const int qw = warp & 3, hf = warp >> 2, ph = qw >> 1;
     const int row = (32 * qw + lane) & 63, quarter = 2 * ph + hf;  // this thread's 64 positions of a tile
     const uint32_t lanes = (uint32_t)(32 * qw) << 16;
+    const int lp = 31 - __clz(a.c.page_size);
     uint8_t *prow = sm + OFF_P + quarter * RC * 128 + row * 128;
     int i = 0, segs = 0;
     while (walk.next(a)) {
@@ -526,8 +512,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         }
         for (int x = 0; x < 64; x += box) {
           if (p0 + x >= s.end) break;
-          const int p = a.c.table[(size_t)walk.n * a.c.max_pages + (p0 + x) / a.c.page_size];
-          if (p < 0 || p >= a.c.n_pages) vis &= ~((box == 64 ? ~0ull : ((1ull << box) - 1)) << x);
+          const int p = a.c.table[(size_t)walk.n * a.c.max_pages + ((p0 + x) >> lp)];
+          if (__builtin_expect(p < 0 || p >= a.c.n_pages, 0)) vis &= ~((box == 64 ? ~0ull : ((1ull << box) - 1)) << x);
         }
         wait(B_SFULL + buf, (uint32_t)(i >> 1));
         tc_fence_after();
@@ -647,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       // whose first is not
       if (segs == 0 && rank == 0 && tid == 0 && walk.t0 > 0) {
         Merge g;
-        g.tiles = tiles, g.workers = workers, g.group = group, g.rows = 0, g.row0 = 0, g.first = g.last = 0;
+        g.group = group, g.rows = 0, g.row0 = 0, g.first = g.last = 0;
         if (walk.t1 == s.tiles) {
           const int64_t first_tile = begin - walk.t0;
           g.row0 = s.lo * a.H + 2 * RC * walk.rt;
@@ -680,17 +666,13 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeAttnArgs a,
   const int row = 2 * blockIdx.y + (threadIdx.x >> 7), t = threadIdx.x & 127;
   if (row >= g.rows) return;
   const int member = blockIdx.x % g.group;
-  // the first worker's part is its last run, the others' their first; a worker without tiles
-  // (more workers than tiles) has none
+  // the first worker's part is the end of its run, the others' the beginning of theirs
   auto slot = [&](int w) { return (size_t)(2 * (w * g.group + member) + (w == g.first ? 1 : 0)) * 2 * RC + row; };
-  auto has = [&](int w) { return run_start(g.tiles, w, g.workers) < run_start(g.tiles, w + 1, g.workers); };
   float M = -INFINITY;
-  for (int w = g.first; w <= g.last; ++w)
-    if (has(w)) M = fmaxf(M, part_ml[slot(w) * 2]);
+  for (int w = g.first; w <= g.last; ++w) M = fmaxf(M, part_ml[slot(w) * 2]);
   float z[4] = {0.f, 0.f, 0.f, 0.f}, L = 0.f;
 #pragma unroll 4
   for (int w = g.first; w <= g.last; ++w) {
-    if (!has(w)) continue;
     const size_t s = slot(w);
     const float m = part_ml[s * 2], l = part_ml[s * 2 + 1];
     const float4 x = load4(part + s * TL + 4 * t);
