@@ -21,8 +21,11 @@
 //                                       positions of its half of the latents, in eight
 //                                       [64 positions x 128 latents] chunks.
 // The blocks and chunks stream through one ring of seven 16 KB slots in the order in which the
-// products use them (S of tile t + 1 before Z of tile t, so the softmax of t + 1 has a whole Z
-// and S to hide behind).  That loads 272 KB a CTA and 256 positions; TMA brings 41 bytes a cycle
+// products use them: while the softmax of tile t runs, S of t + 1 and Z of t - 1 are built side by
+// side, Z's chunks first, so that the weights of t can be written over those of t - 1 behind the
+// last blocks of S.  One thread's products leave gaps (measured: a wait and a commit every four of
+// them, 101 to 149 cycles a product instead of 64), two threads' fill each other's (64 cycles), so
+// S and Z are issued from two warps.  That loads 272 KB a CTA and 256 positions; TMA brings 41 bytes a cycle
 // and SM from L2 (measured, 12 TB/s), the products need 64, so L2 is the bound, near 64 % of the
 // tensor peak.
 //
@@ -52,23 +55,26 @@ constexpr uint32_t OFF_P = KB * RC * 128;            // [4][64 rows][128 B]: 64 
 constexpr uint32_t OFF_R = OFF_P + 4 * RC * 128;     // the ring
 constexpr uint32_t SMEM = OFF_R + NSLOT * SLOT + 1024;
 constexpr uint32_t TM_Z = 0, TM_S = 256;  // Z: two products of 128 columns; S: two buffers of 128
-// warps 0-7 softmax and output, 8 loads, 9 helps it at a sequence's end, 10 tells the leading CTA
-// what the softmax warps have done, 11 issues products
-constexpr int W_LOAD = 8, W_HELP = 9, W_TELL = 10, W_MMA = 11, NT = 384;
+// warps 0-7 softmax and output, 8 loads the ring, 9 the queries and looks over a sequence's last
+// chunks, 10 tells the leading CTA what the softmax warps have done, 11 and 12 issue the score and
+// the value products
+constexpr int W_LOAD = 8, W_HELP = 9, W_TELL = 10, W_SCORE = 11, W_VALUE = 12, NT = 416;
 constexpr int MAX_CLUSTERS = 80;     // of two CTAs (152 SMs: 76)
 constexpr float LAZY = 8.f;          // log2 of how far a row's scores may rise above its reference
 
 // barriers; L: the leading CTA's are used by both
 enum {
-  B_FULL = 0,               // L  a slot's data is there in both CTAs
-  B_EMPTY = B_FULL + NSLOT, //    the products have read a slot
+  B_FULL_S = 0,             // L  a slot's score block is there in both CTAs
+  B_FULL_Z = B_FULL_S + NSLOT,   // L  a slot's value chunk is (a barrier of its own: a warp that
+                                 //    waits by parity must have seen the phase before)
+  B_EMPTY = B_FULL_Z + NSLOT,    //    the products have read a slot
   B_QFULL = B_EMPTY + NSLOT, B_QEMPTY,  // L, -: the queries
   B_SFULL,                  //    a score buffer is written (two)
   B_PFULL = B_SFULL + 2,    // L  the scores are read, the weights written, Z is rescaled
   B_ZFULL,                  //    a tile's value product is done
   B_ZFREE,                  // L  the output has read Z
   B_TAIL,                   //    a slot that threads have to look over has landed
-  B_DRAIN = B_TAIL + NSLOT, B_N
+  B_DRAIN = B_TAIL + NSLOT, B_N = B_DRAIN + 2
 };
 
 struct TreeMaps {
@@ -82,6 +88,11 @@ struct Merge {
   int group, pad[3];
 };
 
+__device__ __forceinline__ bool elect() {  // one lane of the (whole) warp
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ float ex2(float x) {  // 2^x, relative error about 2^-22
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -171,6 +182,11 @@ struct Walk {
   }
 };
 
+// Places in the ring of a phase's slots: score block kb and value chunk c, where the phase has
+// both (z z s four times, then the other five s), or the one alone.
+__device__ __forceinline__ int place_s(int kb, bool both) { return both ? (kb < 4 ? 3 * kb + 2 : kb + 8) : kb; }
+__device__ __forceinline__ int place_z(int c, bool both) { return both ? c + (c >> 1) : c; }
+
 __device__ __forceinline__ int64_t run_start(int64_t tiles, int w, int workers) { return tiles * w / workers; }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
@@ -182,7 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   __shared__ volatile uint32_t s_abort;
   __shared__ unsigned long long s_cost[4];
   __shared__ int64_t s_scan[NT / 32];
-  __shared__ int s_n, s_off;
+  __shared__ int s_n, s_off, s_page[3][16];
   __shared__ float s_max[2][4][RC], s_sum[4][RC];
   const uint32_t raw = smem_u32(dyn);
   const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
@@ -287,179 +303,241 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   };
   const int box = a.c.page_size < 64 ? a.c.page_size : 64;  // rows of a tile load
 
-  if (warp == W_LOAD || warp == W_HELP) {
-    // ---- loads: S(0) S(1) Z(0) S(2) Z(1) ..., a slot at a time.  Where a chunk of Z's operand
-    //      reaches past the cached positions, warp 9 looks it over before the products may use
-    //      it: rows behind the last drafted node and drafted rows with a value that is not finite
-    //      become zeros there (their weight is 0 or NaN, and 0 x NaN must not reach the rows that
-    //      do not see them).
-    const uint32_t full0 = map_shared_rank(bar(B_FULL), 0), qfull0 = map_shared_rank(bar(B_QFULL), 0);
-    const bool loader = warp == W_LOAD;
-    const int boxes = 128 / box;             // tile loads of a slot, one lane each
+  auto warp_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
+
+  if (warp == W_LOAD) {
+    // ---- the ring: S(0), then phase by phase S(t + 1) with Z(t - 1) ------------------------------
+    const uint32_t fulls0 = map_shared_rank(bar(B_FULL_S), 0), fullz0 = map_shared_rank(bar(B_FULL_Z), 0), tail0 = map_shared_rank(bar(B_TAIL), rank);
     const int lb = 31 - __clz(box), lp = 31 - __clz(a.c.page_size);
-    const int sub = lane & (64 / box - 1), blk = (lane * box) >> 6;  // of a value chunk: rows, latents
-    int fill = 0, segs = 0;
-    uint32_t looked = 0;                     // parity of B_TAIL + j
-    struct Tile {
-      int len, end, n, t, page;  // page: lane e's page of the positions 256 t + e box ..
-    } cur, prev;
-    bool have_prev = false;
-    auto pages = [&](Tile &x) {
-      x.page = a.c.n_pages;  // past the pool: zeros
-      const int pos = TILE * x.t + lane * box;
-      if (lane * box < TILE && pos < x.end) {
-        const int p = a.c.table[(size_t)x.n * a.c.max_pages + (pos >> lp)];
-        if (p >= 0 && p < a.c.n_pages) x.page = p;
-        else if (a.err) atomicOr(a.err, ERR_BAD_INDEX);
-      }
-    };
-    auto warp_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
-    auto slot_free = [&]() { return fill < NSLOT || warp_wait(B_EMPTY + fill % NSLOT, (uint32_t)(fill / NSLOT - 1)); };
+    const int per = 64 >> lb;  // tile loads of 64 positions
+    int fill = 0;
+    // one thread loads; s_page[tile % 3][e] is the page of the positions 256 t + e box ..
+    auto slot_free = [&](int j) { return fill < NSLOT || wait(B_EMPTY + j, (uint32_t)(fill / NSLOT - 1)); };
     // the leading CTA's barrier expects both CTAs' bytes; the other CTA only arrives (its bytes
     // cannot come before the phase they belong to: its slot was freed by that phase's products)
-    auto announce = [&](int i, uint32_t bytes) {
-      if (lane == 0) {
-        if (rank == 0) mbar_expect_tx(bar(i), bytes);
-        else arrive_relaxed(map_shared_rank(bar(i), 0));
-      }
-      __syncwarp();
+    auto announce = [&](int i, uint32_t far) {
+      if (rank == 0) mbar_expect_tx(bar(i), 2 * SLOT);
+      else arrive_relaxed(far);
     };
-    auto load_s = [&](const Tile &x) {
-      if (!loader) {
-        fill += KB;
-        return;
-      }
-      const int e = ((128 * (int)rank) >> lb) + (lane < boxes ? lane : 0);
-      const int page = __shfl_sync(0xffffffffu, x.page, e), row = (TILE * x.t + (e << lb)) & (a.c.page_size - 1);
-      for (int kb = 0; kb < KB; ++kb, ++fill) {
-        const int j = fill % NSLOT;
-        if (!slot_free()) continue;
-        announce(B_FULL + j, 2 * SLOT);
-        if (lane < boxes)
-          tma_pair_3d(sb + OFF_R + j * SLOT + lane * box * 128, &maps.c, 64 * kb, row, page, full0 + 8 * j);
-      }
-    };
-    auto load_z = [&](const Tile &x) {
+    auto load_s = [&](int i, int t, int kb) {
+      const int j = fill % NSLOT;
+      if (slot_free(j)) {
+        announce(B_FULL_S + j, fulls0 + 8 * j);
+        const int e0 = (128 * (int)rank) >> lb;
 #pragma unroll 1
-      for (int hp = 0; hp < 8; ++hp, ++fill) {
-        const int j = fill % NSLOT, h = hp >> 2, pc = hp & 3, g0 = TILE * x.t + 64 * pc;
-        const bool tail = g0 + 64 > x.len && g0 < x.end;
-        if (loader) {
-          const int e = ((64 * pc) >> lb) + sub;
-          const int page = __shfl_sync(0xffffffffu, x.page, e), row = (TILE * x.t + (e << lb)) & (a.c.page_size - 1);
-          if (!slot_free()) continue;
-          if (!tail) announce(B_FULL + j, 2 * SLOT);
-          else if (lane == 0) mbar_expect_tx(bar(B_TAIL + j), SLOT);
-          __syncwarp();
-          if (lane < boxes)
-            tma_pair_3d(sb + OFF_R + j * SLOT + blk * 8192 + sub * box * 128, &maps.c, 256 * (int)rank + 128 * h + 64 * blk,
-                        row, page, tail ? map_shared_rank(bar(B_TAIL + j), rank) : full0 + 8 * j);
-        } else if (tail) {
-          const bool ok = warp_wait(B_TAIL + j, (looked >> j) & 1);
-          looked ^= 1u << j;
-          uint8_t *slot = sm + OFF_R + j * SLOT;
-          const int piece = lane & 15;
-          // two rows at a time, 16 lanes each
-          for (int r0 = x.len > g0 ? x.len - g0 : 0; r0 < 64; r0 += 2) {
-            const int r = r0 + (lane >> 4);
-            uint4 *at = reinterpret_cast<uint4 *>(slot + (piece >> 3) * 8192 + (r & 63) * 128 + (((piece & 7) ^ (r & 7)) << 4));
-            bool bad = false;
-            if (g0 + r0 < x.end) {
-              auto odd = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
-              const uint4 v = *at;
-              bad = odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w);
-            }
-            const uint32_t any = __ballot_sync(0xffffffffu, bad) & (lane < 16 ? 0xffffu : 0xffff0000u);
-            if (r < 64 && (any || g0 + r >= x.end)) *at = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0 && ok) mbar_arrive_remote(bar(B_FULL + j), 0);
+        for (int y = 0; y < 2 * per; ++y)
+          tma_pair_3d(sb + OFF_R + j * SLOT + y * box * 128, &maps.c, 64 * kb, (TILE * t + ((e0 + y) << lb)) & (a.c.page_size - 1),
+                      s_page[i][e0 + y], fulls0 + 8 * j);
+      }
+      ++fill;
+    };
+    auto load_z = [&](int i, int t, int len, int end, int c) {
+      const int j = fill % NSLOT, h = c >> 2, pc = c & 3, g0 = TILE * t + 64 * pc;
+      const bool tail = g0 + 64 > len && g0 < end;
+      if (slot_free(j)) {
+        if (!tail) announce(B_FULL_Z + j, fullz0 + 8 * j);
+        else mbar_expect_tx(bar(B_TAIL + j), SLOT);
+        const uint32_t done = (tail ? tail0 : fullz0) + 8 * j;
+        const int e0 = (64 * pc) >> lb;
+#pragma unroll 1
+        for (int y = 0; y < per; ++y) {
+          const int row = (TILE * t + ((e0 + y) << lb)) & (a.c.page_size - 1), page = s_page[i][e0 + y];
+          const uint32_t dst = sb + OFF_R + j * SLOT + y * box * 128;
+          tma_pair_3d(dst, &maps.c, 256 * (int)rank + 128 * h, row, page, done);
+          tma_pair_3d(dst + 8192, &maps.c, 256 * (int)rank + 128 * h + 64, row, page, done);
         }
+      }
+      ++fill;
+    };
+    int i = 0;                                                   // tiles so far
+    int t1 = 0, len1 = 0, end1 = 0, t2 = 0, len2 = 0, end2 = 0;  // the last tile and the one before
+    auto lookup = [&](int t) {
+      const int pos = TILE * t + lane * box;
+      return lane * box < TILE && pos < walk.s.end ? a.c.table[(size_t)walk.n * a.c.max_pages + (pos >> lp)] : -2;
+    };
+    while (walk.next(a)) {
+      int ahead = lookup(walk.t0);
+      for (int t = walk.t0; t < walk.t1; ++t, ++i) {
+        const int page = ahead;
+        if (t + 1 < walk.t1) ahead = lookup(t + 1);
+        if ((page < 0 || page >= a.c.n_pages) && page != -2 && a.err) atomicOr(a.err, ERR_BAD_INDEX);
+        // no page, or behind the last node: past the pool, where loads give zeros
+        if (lane < 16) s_page[i % 3][lane] = page >= 0 && page < a.c.n_pages ? page : a.c.n_pages;
+        __syncwarp();
+        if (elect()) {
+          if (i < 2) {
+#pragma unroll 1
+            for (int kb = 0; kb < KB; ++kb) load_s(i % 3, t, kb);
+          } else {
+#pragma unroll 1
+            for (int y = 0; y < 12; ++y)
+              if (y % 3 == 2) load_s(i % 3, t, y / 3);
+              else load_z((i + 1) % 3, t2, len2, end2, y - y / 3);
+#pragma unroll 1
+            for (int kb = 4; kb < KB; ++kb) load_s(i % 3, t, kb);
+          }
+        } else {
+          fill += i < 2 ? KB : KB + 8;
+        }
+        __syncwarp();
+        t2 = t1, len2 = len1, end2 = end1;
+        t1 = t, len1 = walk.s.len, end1 = walk.s.end;
+      }
+    }
+    if (elect()) {  // the last two tiles' value products
+#pragma unroll 1
+      for (int c = 0; c < 8 && i >= 2; ++c) load_z((i + 1) % 3, t2, len2, end2, c);
+#pragma unroll 1
+      for (int c = 0; c < 8 && i >= 1; ++c) load_z((i + 2) % 3, t1, len1, end1, c);
+    } else {
+      fill += i >= 2 ? 16 : 8 * i;
+    }
+    __syncwarp();
+    // every slot read before the CTA may end
+    for (int j = 0; j < NSLOT; ++j)
+      if (fill > j) wait(B_EMPTY + j, (uint32_t)((fill - j + NSLOT - 1) / NSLOT - 1));
+    if (s_abort)  // a wait ran out: let the copies in flight land
+      for (int y = 0; y < 100; ++y) __nanosleep(10000);
+  } else if (warp == W_HELP) {
+    // ---- the queries of a segment, and the chunks of Z's operand that reach past the cached
+    //      positions: rows behind the last drafted node and drafted rows with a value that is not
+    //      finite become zeros there before the products may use them (their weight is 0 or NaN,
+    //      and 0 x NaN must not reach the rows that do not see them).
+    const uint32_t qfull0 = map_shared_rank(bar(B_QFULL), 0);
+    int base = 0, i = 0, segs = 0;  // ring places before the phase, tiles so far
+    uint32_t looked = 0;            // parity of B_TAIL + j
+    int len1 = 0, end1 = 0, t1 = 0, len2 = 0, end2 = 0, t2 = 0;  // tiles t and t - 1 of the phase
+    auto look = [&](int len, int end, int t, bool both) {
+      if (TILE * (t + 1) <= len) return;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        const int g0 = TILE * t + 64 * (c & 3), j = (base + place_z(c, both)) % NSLOT;
+        if (g0 + 64 <= len || g0 >= end) continue;
+        const bool ok = warp_wait(B_TAIL + j, (looked >> j) & 1);
+        looked ^= 1u << j;
+        uint8_t *slot = sm + OFF_R + j * SLOT;
+        const int piece = lane & 15;
+        // two rows at a time, 16 lanes each
+        for (int r0 = len > g0 ? len - g0 : 0; r0 < 64; r0 += 2) {
+          const int r = r0 + (lane >> 4);
+          uint4 *at = reinterpret_cast<uint4 *>(slot + (piece >> 3) * 8192 + (r & 63) * 128 + (((piece & 7) ^ (r & 7)) << 4));
+          bool bad = false;
+          if (g0 + r0 < end) {
+            auto odd = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
+            const uint4 v = *at;
+            bad = odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w);
+          }
+          const uint32_t any = __ballot_sync(0xffffffffu, bad) & (lane < 16 ? 0xffffu : 0xffff0000u);
+          if (r < 64 && (any || g0 + r >= end)) *at = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive_remote(bar(B_FULL_Z + j), 0);
       }
     };
     while (walk.next(a)) {
-      if (loader && (segs == 0 || warp_wait(B_QEMPTY, (uint32_t)(segs - 1)))) {
+      if (segs == 0 || warp_wait(B_QEMPTY, (uint32_t)(segs - 1))) {
         const int64_t row = (int64_t)walk.s.lo * a.H + 2 * RC * walk.rt + RC * (int)rank;
         const int rows = a.total * a.H < RC ? (int)(a.total * a.H) : RC;  // of a box
-        announce(B_QFULL, 2 * KB * rows * 128);
+        if (lane == 0) {
+          if (rank == 0) mbar_expect_tx(bar(B_QFULL), 2 * KB * rows * 128);
+          else arrive_relaxed(qfull0);
+        }
+        __syncwarp();
         if (lane < KB) tma_pair_3d(sb + OFF_Q + lane * RC * 128, &maps.q, 64 * lane, (int)row, 0, qfull0);
       }
       ++segs;
-      for (int t = walk.t0; t < walk.t1; ++t) {
-        cur.len = walk.s.len, cur.end = walk.s.end, cur.n = walk.n, cur.t = t;
-        if (loader) pages(cur);
-        load_s(cur);
-        if (have_prev) load_z(prev);
-        prev = cur;
-        have_prev = true;
+      for (int t = walk.t0; t < walk.t1; ++t, ++i) {
+        if (i >= 2) look(len2, end2, t2, true);
+        base += KB + (i >= 2 ? 8 : 0);
+        len2 = len1, end2 = end1, t2 = t1;
+        len1 = walk.s.len, end1 = walk.s.end, t1 = t;
       }
     }
-    if (have_prev) load_z(prev);
-    if (loader) {
-      // every slot and the queries read before the CTA may end
-      for (int j = 0; j < NSLOT; ++j) {
-        const int uses = (fill - j + NSLOT - 1) / NSLOT;
-        if (fill > j) wait(B_EMPTY + j, (uint32_t)(uses - 1));
-      }
-      if (segs > 0) wait(B_QEMPTY, (uint32_t)(segs - 1));
-      if (s_abort)  // a wait ran out: let the copies in flight land
-        for (int y = 0; y < 100; ++y) __nanosleep(10000);
-    }
-  } else if (warp == W_MMA) {
-    // ---- products (one thread of the leading CTA) --------------------------------------------
-    if (rank == 0 && lane == 0) {
-      constexpr uint32_t ID_S = idesc(1, 128, 256, 0, 0), ID_Z = idesc(1, 128, 256, 0, 1);
-      int used = 0, segs = 0, i = 0;
+    if (i >= 2) look(len2, end2, t2, false), base += 8;
+    if (i >= 1) look(len1, end1, t1, false);
+    if (segs > 0) wait(B_QEMPTY, (uint32_t)(segs - 1));
+  } else if (warp == W_SCORE) {
+    // ---- score products (one thread of the leading CTA) ---------------------------------------
+    if (rank == 0 && elect()) {
+      constexpr uint32_t ID_S = idesc(1, 128, 256, 0, 0);
+      int base = 0, segs = 0, i = 0;
+      uint32_t full = 0;  // parities of the slots
       bool ok = true;
-      // `tail`: the tile reaches past the cached positions (chunks of it are written by threads)
-      auto value = [&](int t, bool first, int seg, bool tail) {
-        if (!(ok = wait(B_PFULL, (uint32_t)t, true))) return;
-        if (first && seg > 0 && !(ok = wait(B_ZFREE, (uint32_t)(seg - 1), true))) return;
-        for (int h = 0; h < 2; ++h)
-          for (int pc = 0; pc < 4; ++pc, ++used) {
-            const int j = used % NSLOT;
-            if (!(ok = wait(B_FULL + j, (uint32_t)(used / NSLOT), tail))) return;
-            tc_fence_after();
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma2(tm + TM_Z + 128 * h, sdesc_sw128(sb + OFF_P + pc * RC * 128 + ks * 32, 16, 1024),
-                   sdesc_sw128(sb + OFF_R + j * SLOT + ks * 2048, 8192, 1024), ID_Z, !(first && pc == 0 && ks == 0));
-            commit2(bar(B_EMPTY + j));
-          }
-        commit2(bar(B_ZFULL));
-      };
-      bool prev_first = false, prev_tail = false;
-      int prev_seg = 0;
       while (ok && walk.next(a)) {
         for (int t = walk.t0; t < walk.t1 && ok; ++t, ++i) {
-          const int buf = i & 1;
+          const bool both = i >= 2;
           if (t == walk.t0 && !(ok = wait(B_QFULL, (uint32_t)segs))) break;
-          // (the scores of tile i - 2 in this buffer are read: Z(i - 2) has waited for that)
-          for (int kb = 0; kb < KB; ++kb, ++used) {
-            const int j = used % NSLOT;
-            if (!(ok = wait(B_FULL + j, (uint32_t)(used / NSLOT)))) break;
-            tc_fence_after();
+          // this buffer's scores (tile i - 2) are read
+          if (both && !(ok = wait(B_PFULL, (uint32_t)(i - 2), true))) break;
+          tc_fence_after();
+          const uint32_t d = tm + TM_S + 128 * (i & 1);
+#pragma unroll 1
+          for (int kb = 0; kb < KB; ++kb) {
+            const int f = base + place_s(kb, both), j = f % NSLOT;
+            if (!(ok = wait(B_FULL_S + j, full >> j))) break;
+            full ^= 1u << j;
+            const uint64_t ad = sdesc_sw128(sb + OFF_Q + kb * RC * 128, 16, 1024);
+            const uint64_t bd = sdesc_sw128(sb + OFF_R + j * SLOT, 16, 1024);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma2(tm + TM_S + 128 * buf, sdesc_sw128(sb + OFF_Q + kb * RC * 128 + ks * 32, 16, 1024),
-                   sdesc_sw128(sb + OFF_R + j * SLOT + ks * 32, 16, 1024), ID_S, kb > 0 || ks > 0);
+            for (int ks = 0; ks < 4; ++ks) mma2(d, ad + 2 * ks, bd + 2 * ks, ID_S, kb > 0 || ks > 0);
             commit2(bar(B_EMPTY + j));
           }
           if (!ok) break;
-          commit2(bar(B_SFULL + buf));
+          commit2(bar(B_SFULL + (i & 1)));
           if (t == walk.t1 - 1) commit2(bar(B_QEMPTY));
-          if (i > 0) value(i - 1, prev_first, prev_seg, prev_tail);
-          prev_first = t == walk.t0;
-          prev_tail = TILE * (t + 1) > walk.s.len;
-          prev_seg = segs;
+          base += KB + (both ? 8 : 0);
         }
         ++segs;
       }
-      if (ok && i > 0) value(i - 1, prev_first, prev_seg, prev_tail);
       if (!ok) {  // a wait ran out: let the products in flight end
         commit2(bar(B_DRAIN));
-        mbar_wait_cluster(bar(B_DRAIN), 0);
+        mbar_wait(bar(B_DRAIN), 0);
+      }
+    }
+  } else if (warp == W_VALUE) {
+    // ---- value products (one thread of the leading CTA) ---------------------------------------
+    if (rank == 0 && elect()) {
+      constexpr uint32_t ID_Z = idesc(1, 128, 256, 0, 1);
+      int base = 0, segs = 0, i = 0;
+      uint32_t full = 0;  // parities of the slots
+      bool ok = true;
+      // `first`: of a segment; `tail`: the tile reaches past the cached positions (threads have
+      // looked over chunks of it)
+      auto value = [&](int t, bool first, int seg, bool tail, bool both) {
+        if (!(ok = wait(B_PFULL, (uint32_t)t, true))) return;
+        if (first && seg > 0 && !(ok = wait(B_ZFREE, (uint32_t)(seg - 1), true))) return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          const int f = base + place_z(c, both), j = f % NSLOT, h = c >> 2, pc = c & 3;
+          if (!(ok = wait(B_FULL_Z + j, full >> j, tail))) return;
+          full ^= 1u << j;
+          const uint64_t ad = sdesc_sw128(sb + OFF_P + pc * RC * 128, 16, 1024);
+          const uint64_t bd = sdesc_sw128(sb + OFF_R + j * SLOT, 8192, 1024);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma2(tm + TM_Z + 128 * h, ad + 2 * ks, bd + 128 * ks, ID_Z, !(first && pc == 0 && ks == 0));
+          commit2(bar(B_EMPTY + j));
+        }
+        commit2(bar(B_ZFULL));
+      };
+      bool first1 = false, tail1 = false, first2 = false, tail2 = false;  // tiles t and t - 1 of the phase
+      int seg1 = 0, seg2 = 0;
+      while (ok && walk.next(a)) {
+        for (int t = walk.t0; t < walk.t1 && ok; ++t, ++i) {
+          if (i >= 2) value(i - 2, first2, seg2, tail2, true);
+          base += KB + (i >= 2 ? 8 : 0);
+          first2 = first1, tail2 = tail1, seg2 = seg1;
+          first1 = t == walk.t0, tail1 = TILE * (t + 1) > walk.s.len, seg1 = segs;
+        }
+        ++segs;
+      }
+      if (ok && i >= 2) value(i - 2, first2, seg2, tail2, false), base += 8;
+      if (ok && i >= 1) value(i - 1, first1, seg1, tail1, false);
+      if (!ok) {
+        commit2(bar(B_DRAIN + 1));
+        mbar_wait(bar(B_DRAIN + 1), 0);
       }
     }
   } else if (warp == W_TELL) {
