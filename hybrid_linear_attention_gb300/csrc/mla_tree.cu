@@ -20,14 +20,13 @@
 //     Z[128 x 512 latents] += P C       each CTA holds its 64 rows of weights and all 256
 //                                       positions of its half of the latents, in eight
 //                                       [64 positions x 128 latents] chunks.
-// The blocks and chunks stream through one ring of seven 16 KB slots in the order in which the
-// products use them: while the softmax of tile t runs, S of t + 1 and Z of t - 1 are built side by
-// side, Z's chunks first, so that the weights of t can be written over those of t - 1 behind the
-// last blocks of S.  One thread's products leave gaps (measured: a wait and a commit every four of
-// them, 101 to 149 cycles a product instead of 64), two threads' fill each other's (64 cycles), so
-// S and Z are issued from two warps.  That loads 272 KB a CTA and 256 positions; TMA brings 41 bytes a cycle
-// and SM from L2 (measured, 12 TB/s), the products need 64, so L2 is the bound, near 64 % of the
-// tensor peak.
+// Blocks and chunks stream through a ring of 16 KB slots each (four and three), with a loading and
+// an issuing warp each: while the softmax of tile t runs, S of t + 1 and Z of t - 1 are built side
+// by side.  One thread's products leave gaps (measured: with a wait and a commit every four of
+// them, 101 to 149 cycles a product instead of 64), two threads' fill each other's (64 cycles); one
+// thread's loads cost it about 450 cycles a slot, so two load.
+// That brings 272 KB to a CTA for 256 positions; TMA moves 41 bytes a cycle and SM from L2
+// (measured, 12 TB/s), the products need 64, so L2 is the bound, near 64 % of the tensor peak.
 //
 // Work is dealt in tiles of 256 positions: clusters form groups of G that take G row tiles of a
 // sequence side by side (they read the same positions at the same time, so HBM sees them once),
@@ -48,33 +47,35 @@ using namespace tc;
 constexpr int TL = 512, TK = 576, KB = TK / 64;
 constexpr int TILE = 256;            // positions of a tile
 constexpr int RC = 64;               // query rows of a CTA (a pair: 128)
-constexpr int NSLOT = 7;
+constexpr int NS = 4, NZ = 3;        // slots of the score and value operands' rings
 constexpr uint32_t SLOT = 16384;
 constexpr uint32_t OFF_Q = 0;                        // [KB][64 rows][128 B]
 constexpr uint32_t OFF_P = KB * RC * 128;            // [4][64 rows][128 B]: 64 positions each
-constexpr uint32_t OFF_R = OFF_P + 4 * RC * 128;     // the ring
-constexpr uint32_t SMEM = OFF_R + NSLOT * SLOT + 1024;
+constexpr uint32_t OFF_S = OFF_P + 4 * RC * 128;     // score blocks [128 positions][128 B]
+constexpr uint32_t OFF_Z = OFF_S + NS * SLOT;        // value chunks [2][64 positions][128 B]
+constexpr uint32_t SMEM = OFF_Z + NZ * SLOT + 1024;
 constexpr uint32_t TM_Z = 0, TM_S = 256;  // Z: two products of 128 columns; S: two buffers of 128
-// warps 0-7 softmax and output, 8 loads the ring, 9 the queries and looks over a sequence's last
-// chunks, 10 tells the leading CTA what the softmax warps have done, 11 and 12 issue the score and
-// the value products
-constexpr int W_LOAD = 8, W_HELP = 9, W_TELL = 10, W_SCORE = 11, W_VALUE = 12, NT = 416;
+// warps 0-7 softmax and output, 8 and 9 load score blocks and value chunks, 10 loads the queries
+// and looks over a sequence's last chunks, 11 tells the leading CTA what the softmax warps have
+// done, 12 and 13 issue the score and the value products
+constexpr int W_LOAD_S = 8, W_LOAD_Z = 9, W_HELP = 10, W_TELL = 11, W_SCORE = 12, W_VALUE = 13, NT = 448;
 constexpr int MAX_CLUSTERS = 80;     // of two CTAs (152 SMs: 76)
 constexpr float LAZY = 8.f;          // log2 of how far a row's scores may rise above its reference
 
 // barriers; L: the leading CTA's are used by both
 enum {
-  B_FULL_S = 0,             // L  a slot's score block is there in both CTAs
-  B_FULL_Z = B_FULL_S + NSLOT,   // L  a slot's value chunk is (a barrier of its own: a warp that
-                                 //    waits by parity must have seen the phase before)
-  B_EMPTY = B_FULL_Z + NSLOT,    //    the products have read a slot
-  B_QFULL = B_EMPTY + NSLOT, B_QEMPTY,  // L, -: the queries
+  B_FULL_S = 0,                 // L  a slot's data is there in both CTAs
+  B_FULL_Z = B_FULL_S + NS,     // L
+  B_EMPTY_S = B_FULL_Z + NZ,    //    the products have read a slot
+  B_EMPTY_Z = B_EMPTY_S + NS,
+  B_QFULL = B_EMPTY_Z + NZ, B_QEMPTY,  // L, -: the queries
   B_SFULL,                  //    a score buffer is written (two)
-  B_PFULL = B_SFULL + 2,    // L  the scores are read, the weights written, Z is rescaled
+  B_SFREE = B_SFULL + 2,    // L  and read (two)
+  B_PFULL = B_SFREE + 2,    // L  the weights are written, Z is rescaled
   B_ZFULL,                  //    a tile's value product is done
   B_ZFREE,                  // L  the output has read Z
-  B_TAIL,                   //    a slot that threads have to look over has landed
-  B_DRAIN = B_TAIL + NSLOT, B_N = B_DRAIN + 2
+  B_TAIL,                   //    a value slot that threads have to look over has landed
+  B_DRAIN = B_TAIL + NZ, B_N = B_DRAIN + 2
 };
 
 struct TreeMaps {
@@ -182,11 +183,6 @@ struct Walk {
   }
 };
 
-// Places in the ring of a phase's slots: score block kb and value chunk c, where the phase has
-// both (z z s four times, then the other five s), or the one alone.
-__device__ __forceinline__ int place_s(int kb, bool both) { return both ? (kb < 4 ? 3 * kb + 2 : kb + 8) : kb; }
-__device__ __forceinline__ int place_z(int c, bool both) { return both ? c + (c >> 1) : c; }
-
 __device__ __forceinline__ int64_t run_start(int64_t tiles, int w, int workers) { return tiles * w / workers; }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
@@ -198,7 +194,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   __shared__ volatile uint32_t s_abort;
   __shared__ unsigned long long s_cost[4];
   __shared__ int64_t s_scan[NT / 32];
-  __shared__ int s_n, s_off, s_page[3][16];
+  __shared__ int s_n, s_off, s_page[2][16];
   __shared__ float s_max[2][4][RC], s_sum[4][RC];
   const uint32_t raw = smem_u32(dyn);
   const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
@@ -210,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   auto bar = [&](int i) { return smem_u32(&s_bar[i]); };
   if (tid == 0) {
     for (int i = 0; i < B_N; ++i)
-      mbar_init(bar(i), (i < B_EMPTY || i == B_QFULL || i == B_PFULL || i == B_ZFREE)
+      mbar_init(bar(i), (i < B_EMPTY_S || i == B_QFULL || i == B_SFREE || i == B_SFREE + 1 || i == B_PFULL || i == B_ZFREE)
                             ? 2 : 1);
     mbar_fence_init();
     s_abort = 0;
@@ -305,97 +301,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 
   auto warp_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
 
-  if (warp == W_LOAD) {
-    // ---- the ring: S(0), then phase by phase S(t + 1) with Z(t - 1) ------------------------------
-    const uint32_t fulls0 = map_shared_rank(bar(B_FULL_S), 0), fullz0 = map_shared_rank(bar(B_FULL_Z), 0), tail0 = map_shared_rank(bar(B_TAIL), rank);
-    const int lb = 31 - __clz(box), lp = 31 - __clz(a.c.page_size);
+  if (warp == W_LOAD_S || warp == W_LOAD_Z) {
+    // ---- the rings, a tile at a time; one thread loads, s_page[which][e] is the page of the
+    //      positions 256 t + e box ..
+    const bool scores = warp == W_LOAD_S;
+    const int which = scores ? 0 : 1, full = scores ? B_FULL_S : B_FULL_Z, empty = scores ? B_EMPTY_S : B_EMPTY_Z;
+    const int slots = scores ? NS : NZ;
+    const uint32_t full0 = map_shared_rank(bar(full), 0), tail0 = map_shared_rank(bar(B_TAIL), rank);
+    const uint32_t ring = sb + (scores ? OFF_S : OFF_Z);
+    const int lb = 31 - __clz(box), lp = 31 - __clz(a.c.page_size), in_page = a.c.page_size - 1;
     const int per = 64 >> lb;  // tile loads of 64 positions
-    int fill = 0;
-    // one thread loads; s_page[tile % 3][e] is the page of the positions 256 t + e box ..
-    auto slot_free = [&](int j) { return fill < NSLOT || wait(B_EMPTY + j, (uint32_t)(fill / NSLOT - 1)); };
+    int j = 0;                 // the next slot
+    uint32_t par = 1;          // parity that its last use ends (a fresh barrier counts as ended)
+    auto step = [&]() {
+      if (++j == slots) j = 0, par ^= 1;
+    };
     // the leading CTA's barrier expects both CTAs' bytes; the other CTA only arrives (its bytes
     // cannot come before the phase they belong to: its slot was freed by that phase's products)
-    auto announce = [&](int i, uint32_t far) {
-      if (rank == 0) mbar_expect_tx(bar(i), 2 * SLOT);
-      else arrive_relaxed(far);
+    auto announce = [&]() {
+      if (rank == 0) mbar_expect_tx(bar(full + j), 2 * SLOT);
+      else arrive_relaxed(full0 + 8 * j);
     };
-    auto load_s = [&](int i, int t, int kb) {
-      const int j = fill % NSLOT;
-      if (slot_free(j)) {
-        announce(B_FULL_S + j, fulls0 + 8 * j);
-        const int e0 = (128 * (int)rank) >> lb;
-#pragma unroll 1
-        for (int y = 0; y < 2 * per; ++y)
-          tma_pair_3d(sb + OFF_R + j * SLOT + y * box * 128, &maps.c, 64 * kb, (TILE * t + ((e0 + y) << lb)) & (a.c.page_size - 1),
-                      s_page[i][e0 + y], fulls0 + 8 * j);
-      }
-      ++fill;
-    };
-    auto load_z = [&](int i, int t, int len, int end, int c) {
-      const int j = fill % NSLOT, h = c >> 2, pc = c & 3, g0 = TILE * t + 64 * pc;
-      const bool tail = g0 + 64 > len && g0 < end;
-      if (slot_free(j)) {
-        if (!tail) announce(B_FULL_Z + j, fullz0 + 8 * j);
-        else mbar_expect_tx(bar(B_TAIL + j), SLOT);
-        const uint32_t done = (tail ? tail0 : fullz0) + 8 * j;
-        const int e0 = (64 * pc) >> lb;
-#pragma unroll 1
-        for (int y = 0; y < per; ++y) {
-          const int row = (TILE * t + ((e0 + y) << lb)) & (a.c.page_size - 1), page = s_page[i][e0 + y];
-          const uint32_t dst = sb + OFF_R + j * SLOT + y * box * 128;
-          tma_pair_3d(dst, &maps.c, 256 * (int)rank + 128 * h, row, page, done);
-          tma_pair_3d(dst + 8192, &maps.c, 256 * (int)rank + 128 * h + 64, row, page, done);
-        }
-      }
-      ++fill;
-    };
-    int i = 0;                                                   // tiles so far
-    int t1 = 0, len1 = 0, end1 = 0, t2 = 0, len2 = 0, end2 = 0;  // the last tile and the one before
     auto lookup = [&](int t) {
       const int pos = TILE * t + lane * box;
       return lane * box < TILE && pos < walk.s.end ? a.c.table[(size_t)walk.n * a.c.max_pages + (pos >> lp)] : -2;
     };
     while (walk.next(a)) {
       int ahead = lookup(walk.t0);
-      for (int t = walk.t0; t < walk.t1; ++t, ++i) {
+      for (int t = walk.t0; t < walk.t1; ++t) {
         const int page = ahead;
         if (t + 1 < walk.t1) ahead = lookup(t + 1);
-        if ((page < 0 || page >= a.c.n_pages) && page != -2 && a.err) atomicOr(a.err, ERR_BAD_INDEX);
+        if (scores && (page < 0 || page >= a.c.n_pages) && page != -2 && a.err) atomicOr(a.err, ERR_BAD_INDEX);
         // no page, or behind the last node: past the pool, where loads give zeros
-        if (lane < 16) s_page[i % 3][lane] = page >= 0 && page < a.c.n_pages ? page : a.c.n_pages;
+        if (lane < 16) s_page[which][lane] = page >= 0 && page < a.c.n_pages ? page : a.c.n_pages;
         __syncwarp();
         if (elect()) {
-          if (i < 2) {
+          const int p0 = TILE * t;
+          if (scores) {
+            const int e0 = (128 * (int)rank) >> lb;
 #pragma unroll 1
-            for (int kb = 0; kb < KB; ++kb) load_s(i % 3, t, kb);
+            for (int kb = 0; kb < KB; ++kb) {
+              if (wait(empty + j, par)) {
+                announce();
+#pragma unroll 1
+                for (int y = 0; y < 2 * per; ++y)
+                  tma_pair_3d(ring + j * SLOT + y * box * 128, &maps.c, 64 * kb, (p0 + ((e0 + y) << lb)) & in_page,
+                              s_page[which][e0 + y], full0 + 8 * j);
+              }
+              step();
+            }
           } else {
 #pragma unroll 1
-            for (int y = 0; y < 12; ++y)
-              if (y % 3 == 2) load_s(i % 3, t, y / 3);
-              else load_z((i + 1) % 3, t2, len2, end2, y - y / 3);
+            for (int c = 0; c < 8; ++c) {
+              const int g0 = p0 + 64 * (c & 3), e0 = (64 * (c & 3)) >> lb, ch = 256 * (int)rank + 128 * (c >> 2);
+              const bool tail = g0 + 64 > walk.s.len && g0 < walk.s.end;  // warp 10 looks it over
+              if (wait(empty + j, par)) {
+                if (!tail) announce();
+                else mbar_expect_tx(bar(B_TAIL + j), SLOT);
+                const uint32_t done = (tail ? tail0 : full0) + 8 * j;
 #pragma unroll 1
-            for (int kb = 4; kb < KB; ++kb) load_s(i % 3, t, kb);
+                for (int y = 0; y < per; ++y) {
+                  const int row = (p0 + ((e0 + y) << lb)) & in_page, pg = s_page[which][e0 + y];
+                  tma_pair_3d(ring + j * SLOT + y * box * 128, &maps.c, ch, row, pg, done);
+                  tma_pair_3d(ring + j * SLOT + 8192 + y * box * 128, &maps.c, ch + 64, row, pg, done);
+                }
+              }
+              step();
+            }
           }
         } else {
-          fill += i < 2 ? KB : KB + 8;
+          for (int y = 0; y < (scores ? KB : 8); ++y) step();
         }
         __syncwarp();
-        t2 = t1, len2 = len1, end2 = end1;
-        t1 = t, len1 = walk.s.len, end1 = walk.s.end;
       }
     }
-    if (elect()) {  // the last two tiles' value products
-#pragma unroll 1
-      for (int c = 0; c < 8 && i >= 2; ++c) load_z((i + 1) % 3, t2, len2, end2, c);
-#pragma unroll 1
-      for (int c = 0; c < 8 && i >= 1; ++c) load_z((i + 2) % 3, t1, len1, end1, c);
-    } else {
-      fill += i >= 2 ? 16 : 8 * i;
-    }
-    __syncwarp();
     // every slot read before the CTA may end
-    for (int j = 0; j < NSLOT; ++j)
-      if (fill > j) wait(B_EMPTY + j, (uint32_t)((fill - j + NSLOT - 1) / NSLOT - 1));
+    for (int y = 0; y < slots; ++y) {
+      wait(empty + j, par);
+      step();
+    }
     if (s_abort)  // a wait ran out: let the copies in flight land
       for (int y = 0; y < 100; ++y) __nanosleep(10000);
   } else if (warp == W_HELP) {
@@ -404,18 +388,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     //      finite become zeros there before the products may use them (their weight is 0 or NaN,
     //      and 0 x NaN must not reach the rows that do not see them).
     const uint32_t qfull0 = map_shared_rank(bar(B_QFULL), 0);
-    int base = 0, i = 0, segs = 0;  // ring places before the phase, tiles so far
-    uint32_t looked = 0;            // parity of B_TAIL + j
-    int len1 = 0, end1 = 0, t1 = 0, len2 = 0, end2 = 0, t2 = 0;  // tiles t and t - 1 of the phase
-    auto look = [&](int len, int end, int t, bool both) {
+    int segs = 0, j0 = 0;      // the tile's first value slot
+    uint32_t looked = 0;       // parity of B_TAIL + j
+    int len1 = -1, end1 = 0, t1 = 0;
+    auto look = [&](int len, int end, int t) {
+      const int first = j0;
+      j0 = (j0 + 8) % NZ;
       if (TILE * (t + 1) <= len) return;
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {
-        const int g0 = TILE * t + 64 * (c & 3), j = (base + place_z(c, both)) % NSLOT;
+        const int g0 = TILE * t + 64 * (c & 3), j = (first + c) % NZ;
         if (g0 + 64 <= len || g0 >= end) continue;
         const bool ok = warp_wait(B_TAIL + j, (looked >> j) & 1);
         looked ^= 1u << j;
-        uint8_t *slot = sm + OFF_R + j * SLOT;
+        uint8_t *slot = sm + OFF_Z + j * SLOT;
         const int piece = lane & 15;
         // two rows at a time, 16 lanes each
         for (int r0 = len > g0 ? len - g0 : 0; r0 < 64; r0 += 2) {
@@ -447,46 +433,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         if (lane < KB) tma_pair_3d(sb + OFF_Q + lane * RC * 128, &maps.q, 64 * lane, (int)row, 0, qfull0);
       }
       ++segs;
-      for (int t = walk.t0; t < walk.t1; ++t, ++i) {
-        if (i >= 2) look(len2, end2, t2, true);
-        base += KB + (i >= 2 ? 8 : 0);
-        len2 = len1, end2 = end1, t2 = t1;
+      for (int t = walk.t0; t < walk.t1; ++t) {
+        if (len1 >= 0) look(len1, end1, t1);  // a tile late: a segment's queries go first
         len1 = walk.s.len, end1 = walk.s.end, t1 = t;
       }
     }
-    if (i >= 2) look(len2, end2, t2, false), base += 8;
-    if (i >= 1) look(len1, end1, t1, false);
+    if (len1 >= 0) look(len1, end1, t1);
     if (segs > 0) wait(B_QEMPTY, (uint32_t)(segs - 1));
   } else if (warp == W_SCORE) {
     // ---- score products (one thread of the leading CTA) ---------------------------------------
     if (rank == 0 && elect()) {
       constexpr uint32_t ID_S = idesc(1, 128, 256, 0, 0);
-      int base = 0, segs = 0, i = 0;
-      uint32_t full = 0;  // parities of the slots
+      int segs = 0, i = 0, j = 0;
+      uint32_t par = 0;
       bool ok = true;
       while (ok && walk.next(a)) {
         for (int t = walk.t0; t < walk.t1 && ok; ++t, ++i) {
-          const bool both = i >= 2;
           if (t == walk.t0 && !(ok = wait(B_QFULL, (uint32_t)segs))) break;
           // this buffer's scores (tile i - 2) are read
-          if (both && !(ok = wait(B_PFULL, (uint32_t)(i - 2), true))) break;
+          if (i >= 2 && !(ok = wait(B_SFREE + (i & 1), (uint32_t)((i >> 1) - 1), true))) break;
           tc_fence_after();
           const uint32_t d = tm + TM_S + 128 * (i & 1);
 #pragma unroll 1
           for (int kb = 0; kb < KB; ++kb) {
-            const int f = base + place_s(kb, both), j = f % NSLOT;
-            if (!(ok = wait(B_FULL_S + j, full >> j))) break;
-            full ^= 1u << j;
+            if (!(ok = wait(B_FULL_S + j, par))) break;
             const uint64_t ad = sdesc_sw128(sb + OFF_Q + kb * RC * 128, 16, 1024);
-            const uint64_t bd = sdesc_sw128(sb + OFF_R + j * SLOT, 16, 1024);
+            const uint64_t bd = sdesc_sw128(sb + OFF_S + j * SLOT, 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) mma2(d, ad + 2 * ks, bd + 2 * ks, ID_S, kb > 0 || ks > 0);
-            commit2(bar(B_EMPTY + j));
+            commit2(bar(B_EMPTY_S + j));
+            if (++j == NS) j = 0, par ^= 1;
           }
           if (!ok) break;
           commit2(bar(B_SFULL + (i & 1)));
           if (t == walk.t1 - 1) commit2(bar(B_QEMPTY));
-          base += KB + (both ? 8 : 0);
         }
         ++segs;
       }
@@ -499,42 +479,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     // ---- value products (one thread of the leading CTA) ---------------------------------------
     if (rank == 0 && elect()) {
       constexpr uint32_t ID_Z = idesc(1, 128, 256, 0, 1);
-      int base = 0, segs = 0, i = 0;
-      uint32_t full = 0;  // parities of the slots
+      int segs = 0, i = 0, j = 0;
+      uint32_t par = 0;
       bool ok = true;
-      // `first`: of a segment; `tail`: the tile reaches past the cached positions (threads have
-      // looked over chunks of it)
-      auto value = [&](int t, bool first, int seg, bool tail, bool both) {
-        if (!(ok = wait(B_PFULL, (uint32_t)t, true))) return;
-        if (first && seg > 0 && !(ok = wait(B_ZFREE, (uint32_t)(seg - 1), true))) return;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          const int f = base + place_z(c, both), j = f % NSLOT, h = c >> 2, pc = c & 3;
-          if (!(ok = wait(B_FULL_Z + j, full >> j, tail))) return;
-          full ^= 1u << j;
-          const uint64_t ad = sdesc_sw128(sb + OFF_P + pc * RC * 128, 16, 1024);
-          const uint64_t bd = sdesc_sw128(sb + OFF_R + j * SLOT, 8192, 1024);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma2(tm + TM_Z + 128 * h, ad + 2 * ks, bd + 128 * ks, ID_Z, !(first && pc == 0 && ks == 0));
-          commit2(bar(B_EMPTY + j));
-        }
-        commit2(bar(B_ZFULL));
-      };
-      bool first1 = false, tail1 = false, first2 = false, tail2 = false;  // tiles t and t - 1 of the phase
-      int seg1 = 0, seg2 = 0;
       while (ok && walk.next(a)) {
         for (int t = walk.t0; t < walk.t1 && ok; ++t, ++i) {
-          if (i >= 2) value(i - 2, first2, seg2, tail2, true);
-          base += KB + (i >= 2 ? 8 : 0);
-          first2 = first1, tail2 = tail1, seg2 = seg1;
-          first1 = t == walk.t0, tail1 = TILE * (t + 1) > walk.s.len, seg1 = segs;
+          const bool first = t == walk.t0;
+          const bool tail = TILE * (t + 1) > walk.s.len;  // threads may have looked over a chunk
+          if (!(ok = wait(B_PFULL, (uint32_t)i, true))) break;
+          if (first && segs > 0 && !(ok = wait(B_ZFREE, (uint32_t)(segs - 1), true))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            if (!(ok = wait(B_FULL_Z + j, par, tail))) break;
+            const uint64_t ad = sdesc_sw128(sb + OFF_P + (c & 3) * RC * 128, 16, 1024);
+            const uint64_t bd = sdesc_sw128(sb + OFF_Z + j * SLOT, 8192, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma2(tm + TM_Z + 128 * (c >> 2), ad + 2 * ks, bd + 128 * ks, ID_Z, !(first && (c & 3) == 0 && ks == 0));
+            commit2(bar(B_EMPTY_Z + j));
+            if (++j == NZ) j = 0, par ^= 1;
+          }
+          if (!ok) break;
+          commit2(bar(B_ZFULL));
         }
         ++segs;
       }
-      if (ok && i >= 2) value(i - 2, first2, seg2, tail2, false), base += 8;
-      if (ok && i >= 1) value(i - 1, first1, seg1, tail1, false);
       if (!ok) {
         commit2(bar(B_DRAIN + 1));
         mbar_wait(bar(B_DRAIN + 1), 0);
@@ -550,7 +520,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         // (the softmax warps come to barrier 3 again only after Z of this tile, so after this)
         if (!idle) bar_sync(3, 288);
         else if (i > 0) wait(B_ZFULL, (uint32_t)(i - 1));
-        if (lane == 0) mbar_arrive_remote(bar(B_PFULL), 0);
+        if (lane == 0) {
+          fence_cluster();
+          arrive_relaxed(map_shared_rank(bar(B_PFULL), 0));
+          arrive_relaxed(map_shared_rank(bar(B_SFREE + (i & 1)), 0));
+        }
       }
       if (idle) wait(B_ZFULL, (uint32_t)(i - 1));
       bar_sync(4, 288);
@@ -666,36 +640,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         const float l = (s_sum[0][row] + s_sum[1][row]) + (s_sum[2][row] + s_sum[3][row]);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         tc_fence_after();
-        const int64_t out = ((int64_t)s.lo * a.H + r0 + row) * TL + 256 * ph + 128 * hf;
-        float *p = part + ((size_t)slot * 2 * RC + RC * rank + row) * TL + 256 * ph + 128 * hf;
+        // the warp's [32 rows][128 latents], 128 bytes of each row at a time: through shared memory
+        // (the weights' place, free now), so that eight lanes write a row's 128 bytes together
+        // (a thread writing its own row's 16 bytes at a time took 10,000 cycles)
+        uint8_t *stage = sm + OFF_P + warp * 4096;
+        const bool bits = whole && a.z_bf16;
+        const int col0 = 256 * ph + 128 * hf, first = 32 * (qw & 1);  // of the warp: latents, rows
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 128; c += bits ? 64 : 32) {
           float z[32];
-          tmem_ld32(tm + lanes + TM_Z + 128 * hf + 32 * c, z);
+          tmem_ld32(tm + lanes + TM_Z + 128 * hf + c, z);
           tmem_wait_ld();
-          if (row < rows) {
-            if (!whole) {
+          if (bits) {
+            float y[32];
+            tmem_ld32(tm + lanes + TM_Z + 128 * hf + c + 32, y);
+            tmem_wait_ld();
+            auto pack = [&](float lo, float hi) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(lo * inv, hi * inv);
+              return *reinterpret_cast<const uint32_t *>(&b);
+            };
 #pragma unroll
-              for (int y = 0; y < 32; y += 4) store4(p + 32 * c + y, make_float4(z[y], z[y + 1], z[y + 2], z[y + 3]));
-            } else if (a.z_bf16) {
-              uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<bf16 *>(a.z) + out + 32 * c);
+            for (int x = 0; x < 4; ++x) {
+              *reinterpret_cast<uint4 *>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) = make_uint4(
+                  pack(z[8 * x], z[8 * x + 1]), pack(z[8 * x + 2], z[8 * x + 3]), pack(z[8 * x + 4], z[8 * x + 5]),
+                  pack(z[8 * x + 6], z[8 * x + 7]));
+              *reinterpret_cast<uint4 *>(stage + lane * 128 + (((x + 4) ^ (lane & 7)) << 4)) = make_uint4(
+                  pack(y[8 * x], y[8 * x + 1]), pack(y[8 * x + 2], y[8 * x + 3]), pack(y[8 * x + 4], y[8 * x + 5]),
+                  pack(y[8 * x + 6], y[8 * x + 7]));
+            }
+          } else {
+            const float f = whole ? inv : 1.f;
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                uint32_t u[4];
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<float4 *>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) =
+                  make_float4(z[4 * x] * f, z[4 * x + 1] * f, z[4 * x + 2] * f, z[4 * x + 3] * f);
+          }
+          __syncwarp();
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  const __nv_bfloat162 b = __floats2bfloat162_rn(z[8 * y + 2 * x] * inv, z[8 * y + 2 * x + 1] * inv);
-                  u[x] = *reinterpret_cast<const uint32_t *>(&b);
-                }
-                dst[y] = make_uint4(u[0], u[1], u[2], u[3]);
-              }
-            } else {
-              float *dst = reinterpret_cast<float *>(a.z) + out + 32 * c;
-#pragma unroll
-              for (int y = 0; y < 32; y += 4)
-                store4(dst + y, make_float4(z[y] * inv, z[y + 1] * inv, z[y + 2] * inv, z[y + 3] * inv));
+          for (int x = 0; x < 8; ++x) {
+            const int r = 4 * x + (lane >> 3), piece = lane & 7;
+            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+            if (first + r < rows) {
+              const int64_t g = (int64_t)s.lo * a.H + r0 + first + r;  // row of the batch
+              char *dst = bits ? reinterpret_cast<char *>(reinterpret_cast<bf16 *>(a.z) + g * TL + col0 + c)
+                         : whole ? reinterpret_cast<char *>(reinterpret_cast<float *>(a.z) + g * TL + col0 + c)
+                                 : reinterpret_cast<char *>(part + ((size_t)slot * 2 * RC + RC * rank + first + r) * TL + col0 + c);
+              *reinterpret_cast<uint4 *>(dst + 16 * piece) = v;
             }
           }
+          __syncwarp();
         }
         if (!whole && quarter == 0) {
           float *ml = part_ml + ((size_t)slot * 2 * RC + RC * rank + row) * 2;
