@@ -56,8 +56,8 @@ constexpr uint32_t OFF_Z = OFF_S + NS * SLOT;        // value chunks [2][64 posi
 constexpr uint32_t SMEM = OFF_Z + NZ * SLOT + 1024;
 constexpr uint32_t TM_Z = 0, TM_S = 256;  // Z: two products of 128 columns; S: two buffers of 128
 // warps 0-7 softmax and output, 8 and 9 load score blocks and value chunks, 10 loads the queries
-// and looks over a sequence's last chunks, 11 tells the leading CTA what the softmax warps have
-// done, 12 and 13 issue the score and the value products
+// and looks over a sequence's last chunks, 11 arrives for the softmax warps of a CTA without rows, 12
+// and 13 issue the score and the value products
 constexpr int W_LOAD_S = 8, W_LOAD_Z = 9, W_HELP = 10, W_TELL = 11, W_SCORE = 12, W_VALUE = 13, NT = 448;
 constexpr int MAX_CLUSTERS = 80;     // of two CTAs (152 SMs: 76)
 constexpr float LAZY = 8.f;          // log2 of how far a row's scores may rise above its reference
@@ -71,8 +71,10 @@ enum {
   B_QFULL = B_EMPTY_Z + NZ, B_QEMPTY,  // L, -: the queries
   B_SFULL,                  //    a score buffer is written (two)
   B_SFREE = B_SFULL + 2,    // L  and read (two)
-  B_PFULL = B_SFREE + 2,    // L  the weights are written, Z is rescaled
-  B_ZFULL,                  //    a tile's value product is done
+  B_SCALED = B_SFREE + 2,   // L  Z is scaled to a tile's reference
+  B_PFULL,                  // L  64 positions' weights are written (four)
+  B_PFREE = B_PFULL + 4,    //    and read (four)
+  B_ZFULL = B_PFREE + 4,    //    a tile's value product is done
   B_ZFREE,                  // L  the output has read Z
   B_TAIL,                   //    a value slot that threads have to look over has landed
   B_DRAIN = B_TAIL + NZ, B_N = B_DRAIN + 2
@@ -120,13 +122,11 @@ __device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
-// arrive on the leading CTA's barrier without ordering anything (a release there costs the thread
-// a cluster-wide fence, about a thousand cycles)
-__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(int id, int n) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+// Arrive n times on a barrier of the pair (shared::cluster address).  What a thread wrote before is
+// in its own SM's shared and tensor memory, where the products read it: a CTA-scope release is
+// enough (a cluster-scope one costs the thread a fence of about a thousand cycles).
+__device__ __forceinline__ void arrive_pair(uint32_t cluster_bar, uint32_t n = 1) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(n) : "memory");
 }
 __device__ __forceinline__ void bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -205,9 +205,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   const int cid = blockIdx.x >> 1, clusters = gridDim.x >> 1;
   auto bar = [&](int i) { return smem_u32(&s_bar[i]); };
   if (tid == 0) {
-    for (int i = 0; i < B_N; ++i)
-      mbar_init(bar(i), (i < B_EMPTY_S || i == B_QFULL || i == B_SFREE || i == B_SFREE + 1 || i == B_PFULL || i == B_ZFREE)
-                            ? 2 : 1);
+    for (int i = 0; i < B_N; ++i) {
+      int n = 1;
+      if (i < B_EMPTY_S || i == B_QFULL) n = 2;                                        // a loader of each CTA
+      if (i == B_SFREE || i == B_SFREE + 1 || i == B_SCALED || i == B_ZFREE) n = 16;  // the softmax warps
+      if (i >= B_PFULL && i < B_PFREE) n = 4;                                         // two of each CTA
+      mbar_init(bar(i), n);
+    }
     mbar_fence_init();
     s_abort = 0;
     s_n = 0;
@@ -286,12 +290,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   walk.n = s_n, walk.off = s_off, walk.left = stop - begin, walk.group = group, walk.member = member;
   // A wait that runs out raises s_abort; from then on waits fail at once.  The softmax and load
   // warps then walk on to the end without waiting (they meet on named barriers, which all of them
-  // have to reach), and the loader issues nothing more.  `far`: what the other CTA's threads wrote
-  // before they arrived is to be seen too.
-  auto wait = [&](int i, uint32_t parity, bool far = false) {
+  // have to reach), and the loader issues nothing more.
+  auto wait = [&](int i, uint32_t parity) {
 #pragma unroll 1
     for (long it = 0; it < kWaitLimit; ++it) {
-      if (far ? mbar_try_wait_cluster(bar(i), parity & 1) : mbar_try_wait(bar(i), parity & 1)) return true;
+      if (mbar_try_wait(bar(i), parity & 1)) return true;
       if (s_abort) return false;
     }
     s_abort = 1;
@@ -320,7 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     // cannot come before the phase they belong to: its slot was freed by that phase's products)
     auto announce = [&]() {
       if (rank == 0) mbar_expect_tx(bar(full + j), 2 * SLOT);
-      else arrive_relaxed(full0 + 8 * j);
+      else arrive_pair(full0 + 8 * j);
     };
     auto lookup = [&](int t) {
       const int pos = TILE * t + lane * box;
@@ -353,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           } else {
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
-              const int g0 = p0 + 64 * (c & 3), e0 = (64 * (c & 3)) >> lb, ch = 256 * (int)rank + 128 * (c >> 2);
+              const int g0 = p0 + 64 * (c >> 1), e0 = (64 * (c >> 1)) >> lb, ch = 256 * (int)rank + 128 * (c & 1);
               const bool tail = g0 + 64 > walk.s.len && g0 < walk.s.end;  // warp 10 looks it over
               if (wait(empty + j, par)) {
                 if (!tail) announce();
@@ -397,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       if (TILE * (t + 1) <= len) return;
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {
-        const int g0 = TILE * t + 64 * (c & 3), j = (first + c) % NZ;
+        const int g0 = TILE * t + 64 * (c >> 1), j = (first + c) % NZ;
         if (g0 + 64 <= len || g0 >= end) continue;
         const bool ok = warp_wait(B_TAIL + j, (looked >> j) & 1);
         looked ^= 1u << j;
@@ -418,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         }
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0 && ok) mbar_arrive_remote(bar(B_FULL_Z + j), 0);
+        if (lane == 0 && ok) arrive_pair(map_shared_rank(bar(B_FULL_Z + j), 0));
       }
     };
     while (walk.next(a)) {
@@ -427,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         const int rows = a.total * a.H < RC ? (int)(a.total * a.H) : RC;  // of a box
         if (lane == 0) {
           if (rank == 0) mbar_expect_tx(bar(B_QFULL), 2 * KB * rows * 128);
-          else arrive_relaxed(qfull0);
+          else arrive_pair(qfull0);
         }
         __syncwarp();
         if (lane < KB) tma_pair_3d(sb + OFF_Q + lane * RC * 128, &maps.q, 64 * lane, (int)row, 0, qfull0);
@@ -451,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         for (int t = walk.t0; t < walk.t1 && ok; ++t, ++i) {
           if (t == walk.t0 && !(ok = wait(B_QFULL, (uint32_t)segs))) break;
           // this buffer's scores (tile i - 2) are read
-          if (i >= 2 && !(ok = wait(B_SFREE + (i & 1), (uint32_t)((i >> 1) - 1), true))) break;
+          if (i >= 2 && !(ok = wait(B_SFREE + (i & 1), (uint32_t)((i >> 1) - 1)))) break;
           tc_fence_after();
           const uint32_t d = tm + TM_S + 128 * (i & 1);
 #pragma unroll 1
@@ -485,19 +488,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       while (ok && walk.next(a)) {
         for (int t = walk.t0; t < walk.t1 && ok; ++t, ++i) {
           const bool first = t == walk.t0;
-          const bool tail = TILE * (t + 1) > walk.s.len;  // threads may have looked over a chunk
-          if (!(ok = wait(B_PFULL, (uint32_t)i, true))) break;
-          if (first && segs > 0 && !(ok = wait(B_ZFREE, (uint32_t)(segs - 1), true))) break;
-          tc_fence_after();
+          if (!(ok = wait(B_SCALED, (uint32_t)i))) break;
+          if (first && segs > 0 && !(ok = wait(B_ZFREE, (uint32_t)(segs - 1)))) break;
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            if (!(ok = wait(B_FULL_Z + j, par, tail))) break;
-            const uint64_t ad = sdesc_sw128(sb + OFF_P + (c & 3) * RC * 128, 16, 1024);
+          for (int c = 0; c < 8; ++c) {  // 64 positions, one half of the latents and then the other
+            const int pc = c >> 1, h = c & 1;
+            if (h == 0 && !(ok = wait(B_PFULL + pc, (uint32_t)i))) break;
+            if (!(ok = wait(B_FULL_Z + j, par))) break;
+            tc_fence_after();
+            const uint64_t ad = sdesc_sw128(sb + OFF_P + pc * RC * 128, 16, 1024);
             const uint64_t bd = sdesc_sw128(sb + OFF_Z + j * SLOT, 8192, 1024);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma2(tm + TM_Z + 128 * (c >> 2), ad + 2 * ks, bd + 128 * ks, ID_Z, !(first && (c & 3) == 0 && ks == 0));
+              mma2(tm + TM_Z + 128 * h, ad + 2 * ks, bd + 128 * ks, ID_Z, !(first && pc == 0 && ks == 0));
             commit2(bar(B_EMPTY_Z + j));
+            if (h == 1) commit2(bar(B_PFREE + pc));
             if (++j == NZ) j = 0, par ^= 1;
           }
           if (!ok) break;
@@ -511,24 +516,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       }
     }
   } else if (warp == W_TELL) {
-    // ---- arrivals on the leading CTA's barriers for the softmax warps, whose next work need not
-    //      wait for the cluster-wide release
+    // ---- the softmax warps' arrivals where this CTA has no rows (the upper half of a row tile)
     int i = 0;
+    const uint32_t lead = map_shared_rank(bar(0), 0);
     while (walk.next(a)) {
-      const bool idle = walk.s.W * a.H <= 2 * RC * walk.rt + RC * (int)rank;  // no rows of this CTA
-      for (int t = walk.t0; t < walk.t1; ++t, ++i) {
-        // (the softmax warps come to barrier 3 again only after Z of this tile, so after this)
-        if (!idle) bar_sync(3, 288);
-        else if (i > 0) wait(B_ZFULL, (uint32_t)(i - 1));
-        if (lane == 0) {
-          fence_cluster();
-          arrive_relaxed(map_shared_rank(bar(B_PFULL), 0));
-          arrive_relaxed(map_shared_rank(bar(B_SFREE + (i & 1)), 0));
+      if (walk.s.W * a.H <= 2 * RC * walk.rt + RC * (int)rank) {
+        for (int t = walk.t0; t < walk.t1; ++t, ++i) {
+          wait(B_SFULL + (i & 1), (uint32_t)(i >> 1));
+          if (lane == 0) arrive_pair(lead + 8 * (B_SFREE + (i & 1)), 8);
+          for (int q = 0; q < 4; ++q) {
+            if (i > 0) wait(B_PFREE + q, (uint32_t)(i - 1));
+            if (lane == 0 && q == 0) arrive_pair(lead + 8 * B_SCALED, 8);
+            if (lane == 0) arrive_pair(lead + 8 * (B_PFULL + q), 2);
+          }
+          __syncwarp();
         }
+        wait(B_ZFULL, (uint32_t)(i - 1));
+        if (lane == 0) arrive_pair(lead + 8 * B_ZFREE, 8);
+      } else {
+        i += walk.t1 - walk.t0;
       }
-      if (idle) wait(B_ZFULL, (uint32_t)(i - 1));
-      bar_sync(4, 288);
-      if (lane == 0) mbar_arrive_remote(bar(B_ZFREE), 0);
+      // in step with the softmax warps: a barrier's phases are told apart by parity only
+      bar_sync(2, 288);
     }
   } else {
     // ---- softmax and output: TMEM lane l of S and Z is row l % 64; lanes 64-127 hold the upper
@@ -538,6 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     const int row = (32 * qw + lane) & 63, quarter = 2 * ph + hf;  // this thread's 64 positions of a tile
     const uint32_t lanes = (uint32_t)(32 * qw) << 16;
     const int lp = 31 - __clz(a.c.page_size);
+    const uint32_t lead = map_shared_rank(bar(0), 0);
     uint8_t *prow = sm + OFF_P + quarter * RC * 128 + row * 128;
     int i = 0, segs = 0;
     while (walk.next(a)) {
@@ -578,6 +588,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 #pragma unroll
           for (int c = 0; c < 32; ++c) v[c] = x[c], v[32 + c] = y[c];
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_pair(lead + 8 * (B_SFREE + buf));
         if (vis != ~0ull) {
 #pragma unroll
           for (int c = 0; c < 64; ++c) v[c] = (vis >> c) & 1 ? v[c] : -INFINITY;
@@ -608,12 +621,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           ls += __uint_as_float(w[c] << 16) + __uint_as_float(w[c] & 0xffff0000u);
         }
         sum = sum * al + ls;
-        if (i > 0) wait(B_ZFULL, (uint32_t)(i - 1));  // the last tile's weights are read
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4 *>(prow + ((c ^ (row & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        // the last tile's first products are done, so both CTAs have scaled Z for it: this tile's turn
+        if (i > 0) wait(B_PFREE, (uint32_t)(i - 1));
         if (__any_sync(0xffffffffu, al != 1.f)) {
+          wait(B_ZFULL, (uint32_t)(i - 1));
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             float z[32];
@@ -625,10 +637,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
             tmem_st32(at, z);
           }
           tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
         }
+        if (lane == 0) arrive_pair(lead + 8 * B_SCALED);
+        if (i > 0) wait(B_PFREE + quarter, (uint32_t)(i - 1));  // the last tile's weights are read
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4 *>(prow + ((c ^ (row & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         fence_proxy_async();
-        tc_fence_before();
-        bar_arrive(3, 288);
+        __syncwarp();
+        if (lane == 0) arrive_pair(lead + 8 * (B_PFULL + quarter));
       }
       // the segment's output
       const bool whole = walk.t0 == 0 && walk.t1 == s.tiles;
@@ -696,10 +715,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           ml[1] = l;
         }
         tc_fence_before();
-        bar_arrive(4, 288);
-      } else {
-        bar_sync(4, 288);  // not ahead of the products: a barrier's phases are told apart by parity
+        __syncwarp();
+        if (lane == 0) arrive_pair(lead + 8 * B_ZFREE);
       }
+      bar_sync(2, 288);  // (see warp 11)
       // what the combine kernel merges: a sequence's rows whose last tile is in this run and
       // whose first is not
       if (segs == 0 && rank == 0 && tid == 0 && walk.t0 > 0) {
