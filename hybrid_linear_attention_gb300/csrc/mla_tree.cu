@@ -122,6 +122,15 @@ __device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
+// the same with an L2 eviction policy
+__device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
 // Arrive n times on a barrier of the pair (shared::cluster address).  What a thread wrote before is
 // in its own SM's shared and tensor memory, where the products read it: a CTA-scope release is
 // enough (a cluster-scope one costs the thread a fence of about a thousand cycles).
@@ -240,17 +249,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     }
   }
   __syncthreads();
-  // the largest group whose run is within 3 % of the shortest: larger groups read the cache from
-  // HBM fewer times, and lose where row tiles do not divide by them
+  // The group whose run takes the least time.  A larger one idles where row tiles do not divide by
+  // it, but its clusters' tiles take less: they share HBM's reads (measured: 0.93 of a lone cluster's
+  // time for two, 0.87 for four; 64 sequences x 6 to 8 nodes x 4096: 202 us alone, 180 in fours;
+  // 100 x 4 to 5 nodes: 132 alone, 139 in twos).
   int group = 1, workers = clusters;
   {
     float best = INFINITY;
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-      if (clusters >> g) best = fminf(best, (float)s_cost[g] / (float)(clusters >> g));
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      if ((clusters >> g) && (float)s_cost[g] / (float)(clusters >> g) <= 1.03f * best) group = 1 << g, workers = clusters >> g;
+    for (int g = 0; g < 4; ++g) {
+      const float cost = (clusters >> g) ? (float)s_cost[g] / (float)(clusters >> g) * (g == 0 ? 1.f : g == 1 ? 0.93f : 0.87f) : INFINITY;
+      if (cost <= best) best = cost, group = 1 << g, workers = clusters >> g;
+    }
   }
   const int64_t tiles = (int64_t)s_cost[31 - __clz(group)];
   if (tiles < workers) workers = (int)tiles;  // so every worker has a run
@@ -312,6 +322,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     const int slots = scores ? NS : NZ;
     const uint32_t full0 = map_shared_rank(bar(full), 0), tail0 = map_shared_rank(bar(B_TAIL), rank);
     const uint32_t ring = sb + (scores ? OFF_S : OFF_Z);
+    // A lone cluster reads a position's row twice, its scores' loads and one or two tiles later its
+    // values'; then L2 may drop it.  (By default L2 kept rows that were done with: 1.35 GB came from
+    // HBM for 0.95 GB of cache at 256 sequences x 1 node, 252 us; so, 212.)  In a group the others
+    // still need it.
+    uint64_t policy;
+    if (group > 1) asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+    else if (scores) asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+    else asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     const int lb = 31 - __clz(box), lp = 31 - __clz(a.c.page_size), in_page = a.c.page_size - 1;
     const int per = 64 >> lb;  // tile loads of 64 positions
     int j = 0;                 // the next slot
@@ -349,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 #pragma unroll 1
                 for (int y = 0; y < 2 * per; ++y)
                   tma_pair_3d(ring + j * SLOT + y * box * 128, &maps.c, 64 * kb, (p0 + ((e0 + y) << lb)) & in_page,
-                              s_page[which][e0 + y], full0 + 8 * j);
+                              s_page[which][e0 + y], full0 + 8 * j, policy);
               }
               step();
             }
@@ -365,8 +383,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 #pragma unroll 1
                 for (int y = 0; y < per; ++y) {
                   const int row = (p0 + ((e0 + y) << lb)) & in_page, pg = s_page[which][e0 + y];
-                  tma_pair_3d(ring + j * SLOT + y * box * 128, &maps.c, ch, row, pg, done);
-                  tma_pair_3d(ring + j * SLOT + 8192 + y * box * 128, &maps.c, ch + 64, row, pg, done);
+                  tma_pair_3d(ring + j * SLOT + y * box * 128, &maps.c, ch, row, pg, done, policy);
+                  tma_pair_3d(ring + j * SLOT + 8192 + y * box * 128, &maps.c, ch + 64, row, pg, done, policy);
                 }
               }
               step();
