@@ -26,8 +26,34 @@ namespace {
 __device__ __forceinline__ void l2_prefetch(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
-__device__ __forceinline__ float dot4(float4 a, float4 b) {
-  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
+// 2^x, 1/x and the sigmoid on the special-function unit (relative errors about 2^-22)
+__device__ __forceinline__ float ex2_(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float exp_(float x) { return ex2_(x * LOG2E); }
+__device__ __forceinline__ float sigmoid_(float x) { return __fdividef(1.f, 1.f + exp_(-x)); }
+__device__ __forceinline__ float silu_(float x) { return x * sigmoid_(x); }
+
+// fp32 -> tf32 (10 mantissa bits, to nearest), and the warp's 16 x 8 x 8 product
+__device__ __forceinline__ uint32_t tf32_(float x) {
+  uint32_t y;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_16x8x8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// four 8 x 4 blocks of 32-bit values: lane l gets row l / 4, column l % 4 of each
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void *row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"((uint32_t)__cvta_generic_to_shared(row)));
 }
 
 // The nodes of sequence n: first row and count; an offset pair that is out of range, runs
@@ -49,61 +75,87 @@ __device__ __forceinline__ const IO *tap_row(const TreeArgs &a, int row0, int sl
                 : reinterpret_cast<const IO *>(a.conv_state) + ((size_t)slot * 3 + (3 + j)) * C;
 }
 
-// SiLU of the width-4 causal convolution for four neighbouring channels, taps oldest first.
-template <typename IO>
-__device__ __forceinline__ float4 conv4(const IO *t0, const IO *t1, const IO *t2, const IO *t3,
-                                        const IO *w, size_t ch) {
-  const float4 x0 = load4(t0 + ch), x1 = load4(t1 + ch), x2 = load4(t2 + ch), x3 = load4(t3 + ch);
-  const float4 wa = load4(w + 4 * ch), wb = load4(w + 4 * ch + 4), wc = load4(w + 4 * ch + 8),
-               wd = load4(w + 4 * ch + 12);
-  float4 y;
-  y.x = siluf_(wa.x * x0.x + wa.y * x1.x + wa.z * x2.x + wa.w * x3.x);
-  y.y = siluf_(wb.x * x0.y + wb.y * x1.y + wb.z * x2.y + wb.w * x3.y);
-  y.z = siluf_(wc.x * x0.z + wc.y * x1.z + wc.z * x2.z + wc.w * x3.z);
-  y.w = siluf_(wd.x * x0.w + wd.y * x1.w + wd.z * x2.w + wd.w * x3.w);
-  return y;
+// Four neighbouring channels' weights of the width-4 convolution, and its SiLU for taps t0 (oldest)
+// to t3.
+struct Conv4 {
+  float4 a, b, c, d;
+  template <typename IO>
+  __device__ __forceinline__ void load(const IO *w, size_t ch) {
+    a = load4(w + 4 * ch), b = load4(w + 4 * ch + 4), c = load4(w + 4 * ch + 8), d = load4(w + 4 * ch + 12);
+  }
+  __device__ __forceinline__ float4 operator()(float4 t0, float4 t1, float4 t2, float4 t3) const {
+    return make_float4(silu_(fmaf(a.x, t0.x, fmaf(a.y, t1.x, fmaf(a.z, t2.x, a.w * t3.x)))),
+                       silu_(fmaf(b.x, t0.y, fmaf(b.y, t1.y, fmaf(b.z, t2.y, b.w * t3.y)))),
+                       silu_(fmaf(c.x, t0.z, fmaf(c.y, t1.z, fmaf(c.z, t2.z, c.w * t3.z)))),
+                       silu_(fmaf(d.x, t0.w, fmaf(d.y, t1.w, fmaf(d.z, t2.w, d.w * t3.w)))));
+  }
+};
+
+// `bytes` from p on into L2, a line a thread
+__device__ __forceinline__ void ask_l2(const void *p, size_t bytes, int th, int nth) {
+  for (size_t off = (size_t)th * 128; off < bytes; off += (size_t)nth * 128)
+    l2_prefetch(reinterpret_cast<const char *>(p) + off);
 }
 
-// shared memory of the verify kernel for at most W nodes (floats): q, k, v, G / accK [W][D]
-// each, accQ [W][D], A and B [W][W]
+// shared memory of the verify kernel for at most W nodes (floats): k over q [2 W, whole tiles of
+// 16][D + 4], v, G (then S^T k), S^T q [W][D] each, A and B [W][W]
 __host__ __device__ constexpr size_t verify_smem_floats(int W, int D) {
-  return (size_t)5 * W * D + (size_t)2 * W * W;
+  return (size_t)((2 * W + 15) / 16 * 16) * (D + 4) + (size_t)3 * W * D + (size_t)2 * W * W;
 }
 
-// One CTA per (sequence, head) at a time; lane 4 rg + cq of warp w holds rows
-// (D/8) rg .. of columns 16 w + 4 cq .. + 3 of the state, so a column's sum over the key rows
-// closes inside its warp.
+// columns of the state that a warp of the verify kernel owns, and its threads: four warps of 32
+// columns (one of 16 at D = 16)
+template <int D>
+struct VerifyShape {
+  static constexpr int CW = D < 32 ? D : 32, NT = D / CW * 32, NJ = CW / 8;
+};
+template <int N>
+struct Cols {
+  float v[N];
+};
+__device__ __forceinline__ void load_cols(Cols<4> &c, const float *p) {
+  const float4 x = __ldcs(reinterpret_cast<const float4 *>(p));
+  c.v[0] = x.x, c.v[1] = x.y, c.v[2] = x.z, c.v[3] = x.w;
+}
+__device__ __forceinline__ void load_cols(Cols<4> &c, const bf16 *p) {
+  const float4 x = load4_stream(p);
+  c.v[0] = x.x, c.v[1] = x.y, c.v[2] = x.z, c.v[3] = x.w;
+}
+template <typename ST>
+__device__ __forceinline__ void load_cols(Cols<2> &c, const ST *p) {
+  const float2 x = load2(p);
+  c.v[0] = x.x, c.v[1] = x.y;
+}
+
+// One CTA per (sequence, head) at a time.  With X the 2 W rows k_i e^{G_i} and q_i e^{G_i}, the
+// product X S is what the state is read for; it runs on the tensor cores (mma.sync, 16 rows of X by
+// 8 columns by 8 channels: there are too few rows for the 128-row tcgen05 forms, and the kernel is
+// bound by the state's bytes).  Lane (g, t) = (l / 4, l % 4) of warp w loads columns 32 w + 4 g .. + 3
+// of rows t, t + 4, ..., which are its parts of the products' B operands, straight from memory into
+// registers, and gets columns 32 w + 8 t .. + 7 of X S.  Both operands are split into two tf32 parts
+// and three products are added, good to about 2^-21.  The CTA is small (four warps, no state held)
+// so that five of them share an SM, each in another of the phases that a unit's few barriers cut.
 template <int D, typename IO, typename ST>
-__global__ void __launch_bounds__(2 * D) tree_verify_kernel(const TreeArgs a) {
-  constexpr int NT = 2 * D, R = D / 8, NW = NT / 32;
+__global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 5 : 1) tree_verify_kernel(const TreeArgs a) {
+  constexpr int CW = VerifyShape<D>::CW, NT = VerifyShape<D>::NT, NJ = VerifyShape<D>::NJ, NW = NT / 32, XS = D + 4;
+  constexpr int CT = 3 * D / 4;  // threads of the convolution, four channels each
   extern __shared__ __align__(16) float smem[];
   __shared__ int s_par[64], s_up[64][3];
   __shared__ unsigned long long s_anc[64];
-  __shared__ float s_beta[64];
+  __shared__ float s_beta[64], s_rn[128];
   const int WM = a.max_nodes;
-  float *s_q = smem, *s_k = s_q + WM * D, *s_v = s_k + WM * D, *s_g = s_v + WM * D;
-  float *s_o = s_g + WM * D, *s_A = s_o + WM * D, *s_B = s_A + WM * WM;
+  float *s_x = smem, *s_v = s_x + (2 * WM + 15) / 16 * 16 * XS, *s_g = s_v + WM * D, *s_o = s_g + WM * D,
+        *s_A = s_o + WM * D, *s_B = s_A + WM * WM;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cq = lane & 3, rg = lane >> 2, col = 16 * warp + 4 * cq;
+  const int g = lane >> 2, t = lane & 3;
   const int H = a.H;
   const int64_t units = (int64_t)a.n_seqs * H;
   const size_t C = (size_t)3 * H * D;
+  const IO *x_raw = reinterpret_cast<const IO *>(a.x_raw);
 
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int h = (int)(unit % H), n = (int)(unit / H);
     const int slot = a.slot_idx ? a.slot_idx[n] : n;
-    {  // the next unit's state into L2
-      const int64_t nx = unit + gridDim.x;
-      if (nx < units) {
-        const int nn = (int)(nx / H), sn = a.slot_idx ? a.slot_idx[nn] : nn;
-        if (sn >= 0 && sn < a.n_slots) {
-          const char *p = reinterpret_cast<const char *>(a.state) +
-                          ((size_t)sn * H + (int)(nx % H)) * D * D * sizeof(ST);
-          for (size_t off = (size_t)tid * 128; off < (size_t)D * D * sizeof(ST); off += (size_t)NT * 128)
-            l2_prefetch(p + off);
-        }
-      }
-    }
     int row0;
     const int W = tree_nodes(a, n, WM, row0, tid == 0 && h == 0);
     if (slot < 0 || slot >= a.n_slots) {
@@ -111,16 +163,10 @@ __global__ void __launch_bounds__(2 * D) tree_verify_kernel(const TreeArgs a) {
       continue;
     }
     if (W == 0) continue;
+    const ST *src = reinterpret_cast<const ST *>(a.state) + ((size_t)slot * H + h) * (size_t)D * D;
+    ask_l2(src, sizeof(ST) * D * D, tid, NT);  // needed two phases on
 
-    float S[R][4];
-    {
-      const ST *src = reinterpret_cast<const ST *>(a.state) + ((size_t)slot * H + h) * (size_t)D * D + col;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float4 x = load4_stream(src + (size_t)(R * rg + r) * D);
-        S[r][0] = x.x, S[r][1] = x.y, S[r][2] = x.z, S[r][3] = x.w;
-      }
-    }
+    // ---- the sequence's tree ---------------------------------------------------------------------
     __syncthreads();  // the previous unit's shared memory has been read
     for (int i = tid; i < W; i += NT) {
       int p = a.parent[row0 + i];
@@ -134,246 +180,345 @@ __global__ void __launch_bounds__(2 * D) tree_verify_kernel(const TreeArgs a) {
     __syncthreads();
     for (int i = tid; i < W; i += NT) {
       unsigned long long m = 0;
-      int up[3], u = i;
+      int u = i;
 #pragma unroll
       for (int y = 0; y < 3; ++y) {
         u = u >= 0 ? s_par[u] : (u > -3 ? u - 1 : -3);
-        up[y] = u;
+        s_up[i][y] = u;
       }
       for (int j = s_par[i]; j >= 0; j = s_par[j]) m |= 1ull << j;
       s_anc[i] = m;
-      s_up[i][0] = up[0], s_up[i][1] = up[1], s_up[i][2] = up[2];
     }
-    // G: the log-retention summed along each node's path
+    __syncthreads();
+
+    // ---- q, k, v of every node after the convolution along its path (a thread four channels of a
+    //      stream), beside them the retentions summed along the paths (the other threads, four
+    //      channels each), as powers of two
+    if (tid < CT) {
+      const int c4 = tid % (D / 4), st = tid / (D / 4);
+      const size_t ch = (size_t)st * H * D + (size_t)h * D + 4 * c4;
+      Conv4 cw;
+      cw.load(reinterpret_cast<const IO *>(a.conv_w), ch);
+      float *dst = st == 2 ? s_v : s_x + (st == 0 ? W * XS : 0);
+      const int ld = st == 2 ? D : XS;
+      for (int i = 0; i < W; ++i) {
+        const float4 y = cw(load4(tap_row<IO>(a, row0, slot, s_up[i][2], C) + ch),
+                            load4(tap_row<IO>(a, row0, slot, s_up[i][1], C) + ch),
+                            load4(tap_row<IO>(a, row0, slot, s_up[i][0], C) + ch), load4(x_raw + (size_t)(row0 + i) * C + ch));
+        *reinterpret_cast<float4 *>(dst + i * ld + 4 * c4) = y;
+      }
+    } else if (tid - CT < D / 4) {
+      const int c = 4 * (tid - CT);
+#pragma unroll 4
+      for (int i = 0; i < W; ++i) {
+        const float4 x = load4(a.g + ((size_t)(row0 + i) * H + h) * D + c);
+        const int p = s_par[i];
+        float4 y = make_float4(fmaxf(x.x, a.g_min) * LOG2E, fmaxf(x.y, a.g_min) * LOG2E, fmaxf(x.z, a.g_min) * LOG2E,
+                               fmaxf(x.w, a.g_min) * LOG2E);
+        if (p >= 0) {
+          const float4 z = *reinterpret_cast<const float4 *>(s_g + p * D + c);
+          y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+        }
+        *reinterpret_cast<float4 *>(s_g + i * D + c) = y;
+      }
+    }
+    __syncthreads();
+    // ---- the norms of k and q (a warp a row), kept as factors
+    for (int x = warp; x < 2 * W; x += NW) {
+      float rn = 1.f;
+      if (a.qk_l2norm) {
+        float ss = 0.f;
+        for (int c = lane; c < D; c += 32) ss = fmaf(s_x[x * XS + c], s_x[x * XS + c], ss);
+        rn = rsqrtf(warp_sum(ss) + a.l2_eps);
+      }
+      if (lane == 0) s_rn[x] = rn;
+    }
+    __syncthreads();
+    // ---- A and B over the (node, ancestor or itself) pairs: eight lanes a pair, D / 8 channels each
+    {
+      const int grp = tid >> 3, sub = tid & 7;
+      int at = grp;
+      for (int i = 0; i < W; ++i) {
+        unsigned long long m = s_anc[i] | (1ull << i);
+        const int cnt = __popcll(m);
+        // this group's pairs of node i: every NT/8-th of the running count
+        int k = at;
+        for (int skipped = 0; k < cnt; k += NT / 8) {
+          for (; skipped < k; ++skipped) m &= m - 1;
+          const int j = __ffsll((long long)m) - 1;
+          float pa = 0.f, pb = 0.f;
+          // channels sub, sub + 8, ..: neighbouring lanes on neighbouring banks
+#pragma unroll 4
+          for (int c = sub; c < D; c += 8) {
+            const float e = ex2_(s_g[i * D + c] - s_g[j * D + c]) * s_x[j * XS + c];
+            pa = fmaf(s_x[i * XS + c], e, pa);
+            pb = fmaf(s_x[(W + i) * XS + c], e, pb);
+          }
+          const unsigned grp_mask = 0xffu << (lane & 24);
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) {
+            pa += __shfl_xor_sync(grp_mask, pa, o);
+            pb += __shfl_xor_sync(grp_mask, pb, o);
+          }
+          if (sub == 0) {
+            s_A[i * WM + j] = pa * s_rn[i] * s_rn[j];
+            s_B[i * WM + j] = pb * s_rn[W + i] * s_rn[j];
+          }
+        }
+        at = k - cnt;
+      }
+    }
+    __syncthreads();
+    // ---- X = k e^G over q e^G
+    for (int x = tid; x < W * D / 4; x += NT) {
+      const int i = x / (D / 4), c = 4 * (x % (D / 4));
+      const float4 G = *reinterpret_cast<const float4 *>(s_g + i * D + c);
+      const float4 e = make_float4(ex2_(G.x), ex2_(G.y), ex2_(G.z), ex2_(G.w));
+      float4 *k = reinterpret_cast<float4 *>(s_x + i * XS + c), *q = reinterpret_cast<float4 *>(s_x + (W + i) * XS + c);
+      const float rk = s_rn[i], rq = s_rn[W + i];
+      float4 y = *k, z = *q;
+      y.x *= e.x * rk, y.y *= e.y * rk, y.z *= e.z * rk, y.w *= e.w * rk;
+      z.x *= e.x * rq, z.y *= e.y * rq, z.z *= e.z * rq, z.w *= e.w * rq;
+      *k = y, *q = z;
+    }
+    __syncthreads();
+    // ---- X S: k's rows over G's place, q's into s_o
+    for (int m0 = 0; m0 < 2 * W; m0 += 16) {
+      float acc[NJ][4] = {};
+      // lane l of ldmatrix names row l % 8 of block l / 8: rows 0-7 | 8-15, channels 0-3 | 4-7
+      const float *rows = s_x + (m0 + (lane & 7) + (lane >> 3 & 1) * 8) * XS + (lane >> 4) * 4;
+      const ST *mine = src + (size_t)t * D + CW * warp + NJ * g;
+      constexpr int AHEAD = D / 8 < 4 ? D / 8 : 4;  // steps whose state is on its way
+      Cols<NJ> b[AHEAD][2];
+#pragma unroll
+      for (int s = 0; s < AHEAD; ++s)
+        load_cols(b[s][0], mine + (size_t)8 * s * D), load_cols(b[s][1], mine + (size_t)(8 * s + 4) * D);
+#pragma unroll
+      for (int s = 0; s < D / 8; ++s) {
+        const Cols<NJ> b0 = b[s % AHEAD][0], b1 = b[s % AHEAD][1];
+        if (s + AHEAD < D / 8) {
+          load_cols(b[s % AHEAD][0], mine + (size_t)8 * (s + AHEAD) * D);
+          load_cols(b[s % AHEAD][1], mine + (size_t)(8 * (s + AHEAD) + 4) * D);
+        }
+        uint32_t x[4], hi[4], lo[4];
+        ldmatrix4(x, rows + 8 * s);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          hi[y] = tf32_(__uint_as_float(x[y]));
+          lo[y] = tf32_(__uint_as_float(x[y]) - __uint_as_float(hi[y]));
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const uint32_t p1 = tf32_(b0.v[j]), q1 = tf32_(b1.v[j]);
+          mma_16x8x8(acc[j], lo, p1, q1);
+          mma_16x8x8(acc[j], hi, tf32_(b0.v[j] - __uint_as_float(p1)), tf32_(b1.v[j] - __uint_as_float(q1)));
+          mma_16x8x8(acc[j], hi, p1, q1);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = m0 + g + 8 * y;
+        if (r < 2 * W) {
+          float *dst = (r < W ? s_g + r * D : s_o + (r - W) * D) + CW * warp + 2 * NJ * t;
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) dst[NJ * z + j] = acc[j][2 * y + z];
+        }
+      }
+    }
+    __syncthreads();
+    // ---- the corrected writes, by substitution down the tree (u over v's place): a thread a column
     for (int c = tid; c < D; c += NT)
       for (int i = 0; i < W; ++i) {
-        const float g = fmaxf(a.g[((size_t)(row0 + i) * H + h) * D + c], a.g_min);
-        const int p = s_par[i];
-        s_g[i * D + c] = p >= 0 ? s_g[p * D + c] + g : g;
-      }
-    __syncthreads();
-    // q, k, v of every node after the convolution along its path
-    for (int t = tid; t < W * 3 * (D / 4); t += NT) {
-      const int c4 = t % (D / 4), st = t / (D / 4) % 3, i = t / (3 * (D / 4));
-      const size_t ch = (size_t)st * H * D + (size_t)h * D + 4 * c4;
-      const float4 y = conv4(tap_row<IO>(a, row0, slot, s_up[i][2], C), tap_row<IO>(a, row0, slot, s_up[i][1], C),
-                             tap_row<IO>(a, row0, slot, s_up[i][0], C), tap_row<IO>(a, row0, slot, i, C),
-                             reinterpret_cast<const IO *>(a.conv_w), ch);
-      float *dst = (st == 0 ? s_q : st == 1 ? s_k : s_v) + i * D + 4 * c4;
-      *reinterpret_cast<float4 *>(dst) = y;
-    }
-    __syncthreads();
-    if (a.qk_l2norm) {
-      for (int t = warp; t < 2 * W; t += NW) {
-        float *x = (t & 1 ? s_k : s_q) + (t >> 1) * D;
-        float ss = 0.f;
-        for (int c = lane; c < D; c += 32) ss = fmaf(x[c], x[c], ss);
-        const float r = rsqrtf(warp_sum(ss) + a.l2_eps);
-        for (int c = lane; c < D; c += 32) x[c] *= r;
-      }
-      __syncthreads();
-    }
-    // A and B over the (node, ancestor or itself) pairs: a warp per pair
-    for (int t = warp; t < W * W; t += NW) {
-      const int i = t / W, j = t % W;
-      if (j > i || !(j == i || ((s_anc[i] >> j) & 1))) continue;
-      float pa = 0.f, pb = 0.f;
-      for (int c = lane; c < D; c += 32) {
-        const float e = expf(s_g[i * D + c] - s_g[j * D + c]) * s_k[j * D + c];
-        pa = fmaf(s_k[i * D + c], e, pa);
-        pb = fmaf(s_q[i * D + c], e, pb);
-      }
-      pa = warp_sum(pa);
-      pb = warp_sum(pb);
-      if (lane == 0) s_A[i * WM + j] = pa, s_B[i * WM + j] = pb;
-    }
-    __syncthreads();
-    for (int t = tid; t < W * D; t += NT) {
-      const float e = expf(s_g[t]);
-      s_q[t] *= e;
-      s_k[t] *= e;
-    }
-    __syncthreads();
-    // S^T (k e^G) over G's place, S^T (q e^G) into s_o
-    for (int x = 0; x < 2 * W; ++x) {
-      const float *vec = (x < W ? s_k + x * D : s_q + (x - W) * D) + R * rg;
-      float p[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) p[c] = fmaf(S[r][c], vec[r], p[c]);
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) p[c] += __shfl_xor_sync(0xffffffffu, p[c], off);
-      float *dst = (x < W ? s_g + x * D : s_o + (x - W) * D) + col;
-      if (rg == 0) *reinterpret_cast<float4 *>(dst) = make_float4(p[0], p[1], p[2], p[3]);
-    }
-    __syncthreads();
-    // the corrected writes, by substitution down the tree (u over v's place), then the reads
-    if (tid < D)
-      for (int i = 0; i < W; ++i) {
-        float u = s_v[i * D + tid] - s_g[i * D + tid];
+        float u = s_v[i * D + c] - s_g[i * D + c];
         for (unsigned long long m = s_anc[i]; m; m &= m - 1) {
           const int j = __ffsll((long long)m) - 1;
-          u = fmaf(-s_A[i * WM + j], s_v[j * D + tid], u);
+          u = fmaf(-s_A[i * WM + j], s_v[j * D + c], u);
         }
-        s_v[i * D + tid] = s_beta[i] * u;
+        s_v[i * D + c] = s_beta[i] * u;
       }
     __syncthreads();
-    for (int t = tid; t < W * D; t += NT) {
-      const int i = t / D, c = t % D;
-      float o = s_o[t];
-      for (unsigned long long m = s_anc[i] | (1ull << i); m; m &= m - 1) {
-        const int j = __ffsll((long long)m) - 1;
-        o = fmaf(s_B[i * WM + j], s_v[j * D + c], o);
-      }
-      s_o[t] = a.scale * o;
-    }
-    __syncthreads();
+    // ---- the reads, norm and gate: a warp a node, a lane four neighbouring columns
     for (int i = warp; i < W; i += NW) {
-      const size_t row = ((size_t)(row0 + i) * H + h) * D;
-      float rn = 1.f;
+      const int c = 4 * lane;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < D) {
+        o = *reinterpret_cast<const float4 *>(s_o + i * D + c);
+        for (unsigned long long m = s_anc[i] | (1ull << i); m; m &= m - 1) {
+          const int j = __ffsll((long long)m) - 1;
+          const float b = s_B[i * WM + j];
+          const float4 u = *reinterpret_cast<const float4 *>(s_v + j * D + c);
+          o.x = fmaf(b, u.x, o.x), o.y = fmaf(b, u.y, o.y), o.z = fmaf(b, u.z, o.z), o.w = fmaf(b, u.w, o.w);
+        }
+        o.x *= a.scale, o.y *= a.scale, o.z *= a.scale, o.w *= a.scale;
+      }
+      const size_t row = ((size_t)(row0 + i) * H + h) * D + c;
       if (a.gate) {
-        float ss = 0.f;
-        for (int c = lane; c < D; c += 32) ss = fmaf(s_o[i * D + c], s_o[i * D + c], ss);
-        rn = rsqrtf(warp_sum(ss) / D + a.norm_eps);
+        const float rn = rsqrtf(warp_sum(o.x * o.x + o.y * o.y + o.z * o.z + o.w * o.w) / D + a.norm_eps);
+        if (c < D) {
+          const float4 z = load4(reinterpret_cast<const IO *>(a.gate) + row);
+          const float4 w = a.norm_w ? load4(a.norm_w + c) : make_float4(1.f, 1.f, 1.f, 1.f);
+          o.x *= rn * w.x * sigmoid_(z.x), o.y *= rn * w.y * sigmoid_(z.y), o.z *= rn * w.z * sigmoid_(z.z),
+              o.w *= rn * w.w * sigmoid_(z.w);
+        }
       }
-      for (int c = lane; c < D; c += 32) {
-        float o = s_o[i * D + c];
-        if (a.gate)
-          o = o * rn * (a.norm_w ? a.norm_w[c] : 1.f) *
-              sigmoidf_(to_f(reinterpret_cast<const IO *>(a.gate)[row + c]));
-        reinterpret_cast<IO *>(a.out)[row + c] = from_f<IO>(o);
-      }
+      if (c < D) store4(reinterpret_cast<IO *>(a.out) + row, o);
     }
   }
 }
 
 // The accepted path replayed: state read once, every path token's decay and corrected write in
-// registers, state written once; then the conv tail of the unit's channels.
-constexpr int AT = 8;  // path tokens staged at a time
+// registers, state written once; then the conv tail.  Lane 4 rg + cq of warp w holds rows (D/8) rg ..
+// of columns 16 w + 4 cq .. + 3, so a column's sum over the key rows closes inside its warp, and once
+// the tokens are staged in shared memory (k normalised, v, retention, strength) the warps need
+// nothing from each other.  A CTA takes `group` heads of a sequence at a time and stages all their
+// tokens together: the path is worked out once, and the warps go through the heads' states without
+// a barrier.  Bound by the state's bytes, read and written.
+constexpr int AT = 8;  // path tokens staged at a time; a longer path goes head by head
+template <int D>
+constexpr size_t accept_smem(int group) {
+  return (size_t)group * AT * (3 * D + 1) * sizeof(float);
+}
 template <int D, typename IO, typename ST>
-__global__ void __launch_bounds__(2 * D) tree_accept_kernel(const TreeArgs a) {
-  constexpr int NT = 2 * D, R = D / 8, NW = NT / 32;
-  __shared__ __align__(16) float s_k[AT][D], s_v[AT][D], s_a[AT][D];
-  __shared__ float s_beta[AT];
+__global__ void __launch_bounds__(2 * D, 2) tree_accept_kernel(const TreeArgs a, int group) {
+  constexpr int NT = 2 * D, R = D / 8;
+  extern __shared__ __align__(16) float smem[];
   __shared__ int s_par[64], s_path[64], s_m;
+  // [head of the group][token][k | v | retention][D], then the strengths
+  float *s_beta = smem + (size_t)group * AT * 3 * D;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cq = lane & 3, rg = lane >> 2, col = 16 * warp + 4 * cq;
   const int H = a.H;
-  const int64_t units = (int64_t)a.n_seqs * H;
+  const int64_t groups = (int64_t)a.n_seqs * H / group;
   const size_t C = (size_t)3 * H * D;
 
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int h = (int)(unit % H), n = (int)(unit / H);
+  for (int64_t unit = blockIdx.x; unit < groups; unit += gridDim.x) {
+    const int h0 = (int)(unit * group % H), n = (int)(unit * group / H);
     const int slot = a.slot_idx ? a.slot_idx[n] : n;
-    {
-      const int64_t nx = unit + gridDim.x;
-      if (nx < units) {
-        const int nn = (int)(nx / H), sn = a.slot_idx ? a.slot_idx[nn] : nn;
-        if (sn >= 0 && sn < a.n_slots && a.accept[nn] >= 0) {
-          const char *p = reinterpret_cast<const char *>(a.state) +
-                          ((size_t)sn * H + (int)(nx % H)) * D * D * sizeof(ST);
-          for (size_t off = (size_t)tid * 128; off < (size_t)D * D * sizeof(ST); off += (size_t)NT * 128)
-            l2_prefetch(p + off);
-        }
-      }
-    }
     int row0;
-    const int W = tree_nodes(a, n, 64, row0, tid == 0 && h == 0);
+    const int W = tree_nodes(a, n, 64, row0, tid == 0 && h0 == 0);
     const int last = a.accept[n];
     if (slot < 0 || slot >= a.n_slots || last < -1 || last >= W) {
       if (tid == 0 && a.err) atomicOr(a.err, ERR_BAD_INDEX);
       continue;
     }
     if (last < 0) continue;  // nothing accepted: state and tail stay
-
-    float S[R][4];
-    ST *st = reinterpret_cast<ST *>(a.state) + ((size_t)slot * H + h) * (size_t)D * D + col;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float4 x = load4_stream(st + (size_t)(R * rg + r) * D);
-      S[r][0] = x.x, S[r][1] = x.y, S[r][2] = x.z, S[r][3] = x.w;
-    }
-    __syncthreads();  // the previous unit's shared memory has been read
+    ST *state = reinterpret_cast<ST *>(a.state) + ((size_t)slot * H + h0) * (size_t)D * D;
+    ask_l2(state, sizeof(ST) * D * D, tid, NT);
+    __syncthreads();  // the previous group's shared memory has been read
     for (int i = tid; i <= last; i += NT) {
       int p = a.parent[row0 + i];
       if (p < -1 || p >= i) {
-        if (h == 0 && a.err) atomicOr(a.err, ERR_BAD_INDEX);
+        if (h0 == 0 && a.err) atomicOr(a.err, ERR_BAD_INDEX);
         p = -1;
       }
       s_par[i] = p;
     }
     __syncthreads();
     if (tid == 0) {
-      int m = 0;
-      for (int j = last; j >= 0; j = s_par[j]) ++m;
-      s_m = m;
-      for (int j = last; j >= 0; j = s_par[j]) s_path[--m] = j;
+      int x = 0;
+      for (int j = last; j >= 0; j = s_par[j]) ++x;
+      s_m = x;
+      for (int j = last; j >= 0; j = s_par[j]) s_path[--x] = j;
     }
     __syncthreads();
     const int m = s_m;
     auto at = [&](int d) { return d >= 0 ? s_path[d] : d; };  // path position -> node or tail
-    for (int d0 = 0; d0 < m; d0 += AT) {
-      const int nt = m - d0 < AT ? m - d0 : AT;
-      if (d0) __syncthreads();
-      for (int t = tid; t < nt * 2 * (D / 4); t += NT) {
-        const int c4 = t % (D / 4), s = 1 + t / (D / 4) % 2, i = t / (2 * (D / 4)), d = d0 + i;
-        const size_t ch = (size_t)s * H * D + (size_t)h * D + 4 * c4;
-        const float4 y = conv4(tap_row<IO>(a, row0, slot, at(d - 3), C), tap_row<IO>(a, row0, slot, at(d - 2), C),
-                               tap_row<IO>(a, row0, slot, at(d - 1), C), tap_row<IO>(a, row0, slot, at(d), C),
-                               reinterpret_cast<const IO *>(a.conv_w), ch);
-        *reinterpret_cast<float4 *>((s == 1 ? s_k[i] : s_v[i]) + 4 * c4) = y;
-      }
-      for (int t = tid; t < nt * D; t += NT) {
-        const int i = t / D, c = t % D;
-        s_a[i][c] = expf(fmaxf(a.g[((size_t)(row0 + s_path[d0 + i]) * H + h) * D + c], a.g_min));
-      }
-      if (tid < nt) s_beta[tid] = a.beta[(size_t)(row0 + s_path[d0 + tid]) * H + h];
-      __syncthreads();
-      if (a.qk_l2norm) {
-        for (int t = warp; t < nt; t += NW) {
-          float ss = 0.f;
-          for (int c = lane; c < D; c += 32) ss = fmaf(s_k[t][c], s_k[t][c], ss);
-          const float r = rsqrtf(warp_sum(ss) + a.l2_eps);
-          for (int c = lane; c < D; c += 32) s_k[t][c] *= r;
+    // tokens d0 .. d0 + nt - 1 of heads h .. h + heads - 1
+    auto stage = [&](int h, int heads, int d0, int nt) {
+      const int total = heads * nt * 2 * (D / 4);
+      for (int x = tid; x - lane < total; x += NT) {  // D / 4 neighbouring lanes a row
+        const int c4 = x % (D / 4), s = x / (D / 4) % 2, i = x / (D / 2) % nt, y = x / (D / 2 * nt), d = d0 + i;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < total) {
+          const size_t ch = (size_t)(1 + s) * H * D + (size_t)(h + y) * D + 4 * c4;
+          Conv4 cw;
+          cw.load(reinterpret_cast<const IO *>(a.conv_w), ch);
+          v = cw(load4(tap_row<IO>(a, row0, slot, at(d - 3), C) + ch), load4(tap_row<IO>(a, row0, slot, at(d - 2), C) + ch),
+                 load4(tap_row<IO>(a, row0, slot, at(d - 1), C) + ch), load4(tap_row<IO>(a, row0, slot, at(d), C) + ch));
         }
-        __syncthreads();
-      }
-      for (int i = 0; i < nt; ++i) {
-        float p[4] = {0.f, 0.f, 0.f, 0.f};
+        if (a.qk_l2norm) {
+          float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float al = s_a[i][R * rg + r], k = s_k[i][R * rg + r];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            S[r][c] *= al;
-            p[c] = fmaf(S[r][c], k, p[c]);
+          for (int o = 1; o < D / 4; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (s == 0) {
+            const float rk = rsqrtf(ss + a.l2_eps);
+            v.x *= rk, v.y *= rk, v.z *= rk, v.w *= rk;
           }
         }
+        if (x < total) *reinterpret_cast<float4 *>(smem + ((size_t)(y * AT + i) * 3 + s) * D + 4 * c4) = v;
+      }
+      for (int x = tid; x < heads * nt * (D / 4); x += NT) {
+        const int c4 = x % (D / 4), i = x / (D / 4) % nt, y = x / (D / 4 * nt);
+        const float4 g = load4(a.g + ((size_t)(row0 + s_path[d0 + i]) * H + h + y) * D + 4 * c4);
+        *reinterpret_cast<float4 *>(smem + ((size_t)(y * AT + i) * 3 + 2) * D + 4 * c4) = make_float4(
+            expf(fmaxf(g.x, a.g_min)), expf(fmaxf(g.y, a.g_min)), expf(fmaxf(g.z, a.g_min)), expf(fmaxf(g.w, a.g_min)));
+      }
+      for (int x = tid; x < heads * nt; x += NT)
+        s_beta[x / nt * AT + x % nt] = a.beta[(size_t)(row0 + s_path[d0 + x % nt]) * H + h + x / nt];
+    };
+    const bool together = m <= AT;
+    if (together) {
+      stage(h0, group, 0, m);
+      __syncthreads();
+    }
+    for (int y = 0; y < group; ++y) {
+      ST *st = state + (size_t)y * D * D + col;
+      float S[R][4];
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1)
+      for (int r = 0; r < R; ++r) {
+        const float4 x = load4_stream(st + (size_t)(R * rg + r) * D);
+        S[r][0] = x.x, S[r][1] = x.y, S[r][2] = x.z, S[r][3] = x.w;
+      }
+      if (y + 1 < group) ask_l2(state + (size_t)(y + 1) * D * D, sizeof(ST) * D * D, tid, NT);
+      for (int d0 = 0; d0 < m; d0 += AT) {
+        const int nt = m - d0 < AT ? m - d0 : AT, at0 = together ? y * AT : 0;
+        if (!together) {
+          __syncthreads();  // the tokens of before have been read
+          stage(h0 + y, 1, d0, nt);
+          __syncthreads();
+        }
+        for (int i = 0; i < nt; ++i) {
+          const float *tok = smem + (size_t)(at0 + i) * 3 * D, *kr = tok + R * rg, *ar = tok + 2 * D + R * rg;
+          float p[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) p[c] += __shfl_xor_sync(0xffffffffu, p[c], off);
-        const float4 v = *reinterpret_cast<const float4 *>(&s_v[i][col]);
-        const float b = s_beta[i];
-        const float u[4] = {b * (v.x - p[0]), b * (v.y - p[1]), b * (v.z - p[2]), b * (v.w - p[3])};
+          for (int r2 = 0; r2 < R; r2 += 2) {
+            const float2 k2 = *reinterpret_cast<const float2 *>(kr + r2), a2 = *reinterpret_cast<const float2 *>(ar + r2);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float k = s_k[i][R * rg + r];
+            for (int c = 0; c < 4; ++c) {
+              S[r2][c] *= a2.x;
+              p[c] = fmaf(S[r2][c], k2.x, p[c]);
+              S[r2 + 1][c] *= a2.y;
+              p[c] = fmaf(S[r2 + 1][c], k2.y, p[c]);
+            }
+          }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) S[r][c] = fmaf(k, u[c], S[r][c]);
+          for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) p[c] += __shfl_xor_sync(0xffffffffu, p[c], off);
+          const float4 v = *reinterpret_cast<const float4 *>(tok + D + col);
+          const float b = s_beta[at0 + i];
+          const float u[4] = {b * (v.x - p[0]), b * (v.y - p[1]), b * (v.z - p[2]), b * (v.w - p[3])};
+#pragma unroll
+          for (int r2 = 0; r2 < R; r2 += 2) {
+            const float2 k2 = *reinterpret_cast<const float2 *>(kr + r2);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              S[r2][c] = fmaf(k2.x, u[c], S[r2][c]);
+              S[r2 + 1][c] = fmaf(k2.y, u[c], S[r2 + 1][c]);
+            }
+          }
         }
       }
-    }
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      store4_stream(st + (size_t)(R * rg + r) * D, make_float4(S[r][0], S[r][1], S[r][2], S[r][3]));
-    // the last three raw inputs of the path (bit-exact copies; every convolution has read the
-    // old tail: the last staging barrier is behind)
-    for (int t = tid; t < 3 * D; t += NT) {
-      const size_t ch = (size_t)(t / D) * H * D + (size_t)h * D + t % D;
+      for (int r = 0; r < R; ++r)
+        store4_stream(st + (size_t)(R * rg + r) * D, make_float4(S[r][0], S[r][1], S[r][2], S[r][3]));
+    }
+    // the last three raw inputs of the path (bit-exact copies; every convolution has read the old
+    // tail: the staging barriers are behind)
+    for (int x = tid; x < 3 * group * D; x += NT) {
+      const size_t ch = (size_t)(x / (group * D)) * H * D + (size_t)h0 * D + x % (group * D);
       const IO x0 = tap_row<IO>(a, row0, slot, at(m - 3), C)[ch], x1 = tap_row<IO>(a, row0, slot, at(m - 2), C)[ch],
                x2 = tap_row<IO>(a, row0, slot, at(m - 1), C)[ch];
       IO *tail = reinterpret_cast<IO *>(a.conv_state) + (size_t)slot * 3 * C + ch;
@@ -384,29 +529,53 @@ __global__ void __launch_bounds__(2 * D) tree_accept_kernel(const TreeArgs a) {
   }
 }
 
-template <typename K>
-cudaError_t launch_units(K kernel, const TreeArgs &a, int threads, size_t smem, size_t smem_most,
-                         cudaStream_t s) {
-  int dev = 0, nsm = 0, per_sm = 0;
+// CTAs of `kernel` that fit on the current device, kept per kernel and device for the last shared
+// memory size asked (a query costs the host more than a launch).
+template <auto kernel>
+cudaError_t fitting(int threads, size_t smem, size_t smem_most, int64_t *ctas) {
+  static std::atomic<int64_t> known[64];  // size and count + 1 in one word
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int64_t have = dev < 64 ? known[dev].load() : 0;
+  if (have && (size_t)(have >> 32) == smem) {
+    *ctas = (have & 0xffffffff) - 1;
+    return cudaSuccess;
+  }
+  int nsm = 0, per_sm = 0;
   // always the largest tree's size: a smaller one set by another host thread could come
   // between this call's opt-in and its launch
-  if (e == cudaSuccess && smem_most > 0)
+  if (smem_most > 0)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_most);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
   if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)a.n_seqs * a.H;
-  const int64_t fit = (int64_t)nsm * (per_sm > 0 ? per_sm : 1);
-  kernel<<<(unsigned)(units < fit ? units : fit), threads, smem, s>>>(a);
-  return cudaGetLastError();
+  *ctas = (int64_t)nsm * (per_sm > 0 ? per_sm : 1);
+  if (dev < 64) known[dev].store((int64_t)smem << 32 | (*ctas + 1));
+  return cudaSuccess;
 }
 
 template <int D, typename IO, typename ST>
 cudaError_t launch_typed(const TreeArgs &a, bool accept, cudaStream_t s) {
-  if (accept) return launch_units(tree_accept_kernel<D, IO, ST>, a, 2 * D, 0, 0, s);
-  return launch_units(tree_verify_kernel<D, IO, ST>, a, 2 * D, verify_smem_floats(a.max_nodes, D) * sizeof(float),
-                      verify_smem_floats(64, D) * sizeof(float), s);
+  const int64_t units = (int64_t)a.n_seqs * a.H;
+  int64_t fit = 0;
+  if (accept) {
+    constexpr auto kernel = tree_accept_kernel<D, IO, ST>;
+    cudaError_t e = fitting<kernel>(2 * D, accept_smem<D>(4), accept_smem<D>(4), &fit);
+    if (e != cudaSuccess) return e;
+    // heads staged together while that leaves every CTA several groups
+    int group = 1;
+    while (group < 4 && a.H % (2 * group) == 0 && units / (2 * group) >= 4 * fit) group *= 2;
+    const int64_t groups = units / group;
+    kernel<<<(unsigned)(groups < fit ? groups : fit), 2 * D, accept_smem<D>(group), s>>>(a, group);
+  } else {
+    constexpr auto kernel = tree_verify_kernel<D, IO, ST>;
+    const size_t smem = verify_smem_floats(a.max_nodes, D) * sizeof(float);
+    cudaError_t e = fitting<kernel>(VerifyShape<D>::NT, smem, verify_smem_floats(64, D) * sizeof(float), &fit);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(units < fit ? units : fit), VerifyShape<D>::NT, smem, s>>>(a);
+  }
+  return cudaGetLastError();
 }
 
 template <int D>

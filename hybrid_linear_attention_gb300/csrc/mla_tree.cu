@@ -824,13 +824,14 @@ cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s
     return cudaErrorInvalidValue;
   int dev = 0, nsm = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  static std::atomic<bool> attr_set[64];  // the opt-in done, per device (idempotent if raced)
-  if (dev >= 64 || !attr_set[dev].load()) {
+  static std::atomic<int> sms[64];  // SMs of a device once the kernel is opted in there (idempotent if raced)
+  if (dev < 64) nsm = sms[dev].load();
+  if (nsm == 0) {
     e = cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    if (dev < 64) attr_set[dev].store(true);
+    if (dev < 64) sms[dev].store(nsm);
   }
   const int clusters = nsm / 2 < 1 ? 1 : (nsm / 2 < MAX_CLUSTERS ? nsm / 2 : MAX_CLUSTERS);
   float *part = reinterpret_cast<float *>(a.ws);

@@ -217,7 +217,13 @@ def _hptr(t, dtype=None, name="tensor"):
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object (which costs more than a launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
 
