@@ -32,9 +32,13 @@ __device__ __forceinline__ float ex2_(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp_(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 constexpr float LOG2E = 1.4426950408889634f;
-__device__ __forceinline__ float exp_(float x) { return ex2_(x * LOG2E); }
-__device__ __forceinline__ float sigmoid_(float x) { return __fdividef(1.f, 1.f + exp_(-x)); }
+__device__ __forceinline__ float sigmoid_(float x) { return rcp_(1.f + ex2_(x * -LOG2E)); }
 __device__ __forceinline__ float silu_(float x) { return x * sigmoid_(x); }
 
 // fp32 -> tf32 (10 mantissa bits, to nearest), and the warp's 16 x 8 x 8 product
@@ -49,7 +53,22 @@ __device__ __forceinline__ void mma_16x8x8(float (&d)[4], const uint32_t (&a)[4]
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// four 8 x 4 blocks of 32-bit values: lane l gets row l / 4, column l % 4 of each
+// the same of bf16 operands, 16 x 8 x 16, two values a register
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two values as bf16 pairs hi + lo, good to about 2^-17 of each
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  hi = *reinterpret_cast<const uint32_t *>(&h);
+  const __nv_bfloat162 l =
+      __floats2bfloat162_rn(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+  lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+// four 8 x 16-byte blocks: lane l gets the 32-bit word l % 4 of row l / 4 of each
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void *row) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -97,10 +116,42 @@ __device__ __forceinline__ void ask_l2(const void *p, size_t bytes, int th, int 
     l2_prefetch(reinterpret_cast<const char *>(p) + off);
 }
 
+// What a CTA will read of heads h .. h + HEADS - 1 of `rows` nodes of sequence n, into L2: the raw
+// inputs' streams FIRST .. 2, the retentions, the gates and the conv tail (a line or more a thread).
+template <int D, typename IO, int HEADS, int FIRST>
+__device__ __forceinline__ void ask_inputs(const TreeArgs &a, int row0, int rows, int slot, int h, int th, int nth) {
+  const size_t C = (size_t)3 * a.H * D;
+  constexpr int first = FIRST, xl = (HEADS * D * (int)sizeof(IO) + 127) / 128, gl = (HEADS * D * 4 + 127) / 128;  // lines
+  constexpr int nx = (3 - FIRST) * xl, per = nx + gl + (FIRST == 0 ? xl : 0);
+  const IO *x_raw = reinterpret_cast<const IO *>(a.x_raw);
+  for (int x = th; x < rows * per + 3 * nx; x += nth) {
+    const char *p;
+    if (x < rows * per) {
+      const int i = row0 + x / per, y = x % per;
+      const size_t at = ((size_t)i * a.H + h) * D;
+      if (y < nx) p = reinterpret_cast<const char *>(x_raw + (size_t)i * C + ((size_t)(first + y / xl) * a.H + h) * D) + y % xl * 128;
+      else if (y < nx + gl) p = reinterpret_cast<const char *>(a.g + at) + (y - nx) * 128;
+      else if (a.gate) p = reinterpret_cast<const char *>(reinterpret_cast<const IO *>(a.gate) + at) + (y - nx - gl) * 128;
+      else continue;
+    } else {
+      const int y = x - rows * per;
+      p = reinterpret_cast<const char *>(reinterpret_cast<const IO *>(a.conv_state) + ((size_t)slot * 3 + y / nx) * C +
+                                         ((size_t)(first + y % nx / xl) * a.H + h) * D) + y % xl * 128;
+    }
+    l2_prefetch(p);
+  }
+}
+
 // shared memory of the verify kernel for at most W nodes (floats): k over q [2 W, whole tiles of
-// 16][D + 4], v, G (then S^T k), S^T q [W][D] each, A and B [W][W]
-__host__ __device__ constexpr size_t verify_smem_floats(int W, int D) {
-  return (size_t)((2 * W + 15) / 16 * 16) * (D + 4) + (size_t)3 * W * D + (size_t)2 * W * W;
+// 16][D + 4], v, G (then S^T k) [W][D] each, then S^T q [W][D], A and B [W][W], which take the place of
+// the raw inputs [W + 3][3 D] where those are staged (bf16)
+__host__ __device__ constexpr size_t verify_smem_floats(int W, int D, bool staged) {
+  const size_t late = (size_t)W * D + (size_t)2 * W * W, raw = staged ? ((size_t)(W + 3) * 3 * D + 1) / 2 : 0;
+  return (size_t)((2 * W + 15) / 16 * 16) * (D + 4) + (size_t)2 * W * D + (late > raw ? late : raw);
+}
+__device__ __forceinline__ void copy_async16(void *smem, const void *global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global)
+               : "memory");
 }
 
 // columns of the state that a warp of the verify kernel owns, and its threads: four warps of 32
@@ -127,34 +178,37 @@ __device__ __forceinline__ void load_cols(Cols<2> &c, const ST *p) {
   c.v[0] = x.x, c.v[1] = x.y;
 }
 
-// One CTA per (sequence, head) at a time.  With X the 2 W rows k_i e^{G_i} and q_i e^{G_i}, the
-// product X S is what the state is read for; it runs on the tensor cores (mma.sync, 16 rows of X by
-// 8 columns by 8 channels: there are too few rows for the 128-row tcgen05 forms, and the kernel is
-// bound by the state's bytes).  Lane (g, t) = (l / 4, l % 4) of warp w loads columns 32 w + 4 g .. + 3
-// of rows t, t + 4, ..., which are its parts of the products' B operands, straight from memory into
-// registers, and gets columns 32 w + 8 t .. + 7 of X S.  Both operands are split into two tf32 parts
-// and three products are added, good to about 2^-21.  The CTA is small (four warps, no state held)
-// so that five of them share an SM, each in another of the phases that a unit's few barriers cut.
+// With X the 2 W rows k_i e^{G_i} and q_i e^{G_i}, the product X S is what the state is read for; it
+// runs on the tensor cores (mma.sync, 16 rows of X at a time: there are too few rows for the 128-row
+// tcgen05 forms, and the kernel is bound by the state's bytes).  Lane (g, t) = (l / 4, l % 4) of warp
+// w loads columns 32 w + 4 g .. + 3 of its rows of S, which are its parts of the products' B operands,
+// straight from memory into registers, and gets columns 32 w + 8 t .. + 7 of X S.  With bf16 I/O both
+// operands are split into two bf16 parts and three products are added, good to about 2^-16 (an output
+// is rounded to 2^-9); with fp32 I/O into two tf32 parts, about 2^-21.
+// A CTA is small (four warps, no state held), so that seven share an SM, each in another of the phases
+// that the few barriers of a unit cut.  bf16 inputs come into shared memory by asynchronous copies
+// that run while the tree is worked out.
 template <int D, typename IO, typename ST>
-__global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 5 : 1) tree_verify_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 7 : 1) tree_verify_kernel(const TreeArgs a) {
   constexpr int CW = VerifyShape<D>::CW, NT = VerifyShape<D>::NT, NJ = VerifyShape<D>::NJ, NW = NT / 32, XS = D + 4;
   constexpr int CT = 3 * D / 4;  // threads of the convolution, four channels each
+  constexpr bool EXACT = sizeof(IO) == 4;
   extern __shared__ __align__(16) float smem[];
-  __shared__ int s_par[64], s_up[64][3];
+  __shared__ int s_par[64];
+  __shared__ __align__(16) int s_tap[64][4];  // a node's taps, oldest first: nodes, or -1 (newest) .. -3 of the tail
   __shared__ unsigned long long s_anc[64];
   __shared__ float s_beta[64], s_rn[128];
   const int WM = a.max_nodes;
   float *s_x = smem, *s_v = s_x + (2 * WM + 15) / 16 * 16 * XS, *s_g = s_v + WM * D, *s_o = s_g + WM * D,
         *s_A = s_o + WM * D, *s_B = s_A + WM * WM;
+  IO *s_raw = reinterpret_cast<IO *>(s_o);  // row 3 + i: node i, rows 0 .. 2 the tail
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int H = a.H;
-  const int64_t units = (int64_t)a.n_seqs * H;
+  const uint32_t H = a.H, units = (uint32_t)a.n_seqs * H;  // at most 65535 x 21845
   const size_t C = (size_t)3 * H * D;
-  const IO *x_raw = reinterpret_cast<const IO *>(a.x_raw);
 
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int h = (int)(unit % H), n = (int)(unit / H);
+  for (uint32_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int n = (int)(unit / H), h = (int)(unit % H);
     const int slot = a.slot_idx ? a.slot_idx[n] : n;
     int row0;
     const int W = tree_nodes(a, n, WM, row0, tid == 0 && h == 0);
@@ -164,10 +218,19 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 5 : 1) tree_ver
     }
     if (W == 0) continue;
     const ST *src = reinterpret_cast<const ST *>(a.state) + ((size_t)slot * H + h) * (size_t)D * D;
-    ask_l2(src, sizeof(ST) * D * D, tid, NT);  // needed two phases on
+    __syncthreads();  // the previous unit's shared memory has been read
+    if (!EXACT) {
+      constexpr int P = D * (int)sizeof(IO) / 16;  // pieces of a head's channels
+      for (int x = tid; x < (W + 3) * 3 * P; x += NT) {
+        const int i = x / (3 * P) - 3, st = x / P % 3, y = x % P * (16 / (int)sizeof(IO));
+        copy_async16(s_raw + (size_t)(i + 3) * 3 * D + st * D + y, tap_row<IO>(a, row0, slot, i, C) + ((size_t)st * H + h) * D + y);
+      }
+    }
+    for (int x = tid; x < W * (D / 4); x += NT)
+      copy_async16(s_g + 4 * x, a.g + ((size_t)(row0 + x / (D / 4)) * H + h) * D + 4 * (x % (D / 4)));
+    ask_l2(src, sizeof(ST) * D * D, tid, NT);  // needed a few phases on (any earlier, and L2 drops it again)
 
     // ---- the sequence's tree ---------------------------------------------------------------------
-    __syncthreads();  // the previous unit's shared memory has been read
     for (int i = tid; i < W; i += NT) {
       int p = a.parent[row0 + i];
       if (p < -1 || p >= i) {  // not an earlier node: flagged, taken as a root
@@ -182,13 +245,14 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 5 : 1) tree_ver
       unsigned long long m = 0;
       int u = i;
 #pragma unroll
-      for (int y = 0; y < 3; ++y) {
+      for (int y = 3; y >= 0; --y) {
+        s_tap[i][y] = u;
         u = u >= 0 ? s_par[u] : (u > -3 ? u - 1 : -3);
-        s_up[i][y] = u;
       }
       for (int j = s_par[i]; j >= 0; j = s_par[j]) m |= 1ull << j;
       s_anc[i] = m;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
 
     // ---- q, k, v of every node after the convolution along its path (a thread four channels of a
@@ -199,19 +263,18 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 5 : 1) tree_ver
       const size_t ch = (size_t)st * H * D + (size_t)h * D + 4 * c4;
       Conv4 cw;
       cw.load(reinterpret_cast<const IO *>(a.conv_w), ch);
-      float *dst = st == 2 ? s_v : s_x + (st == 0 ? W * XS : 0);
+      float *dst = (st == 2 ? s_v : s_x + (st == 0 ? W * XS : 0)) + 4 * c4;
       const int ld = st == 2 ? D : XS;
-      for (int i = 0; i < W; ++i) {
-        const float4 y = cw(load4(tap_row<IO>(a, row0, slot, s_up[i][2], C) + ch),
-                            load4(tap_row<IO>(a, row0, slot, s_up[i][1], C) + ch),
-                            load4(tap_row<IO>(a, row0, slot, s_up[i][0], C) + ch), load4(x_raw + (size_t)(row0 + i) * C + ch));
-        *reinterpret_cast<float4 *>(dst + i * ld + 4 * c4) = y;
+      const IO *raw = s_raw + 9 * D + st * D + 4 * c4;
+      for (int i = 0; i < W; ++i, dst += ld) {
+        const int4 tap = *reinterpret_cast<const int4 *>(s_tap[i]);
+        auto at = [&](int j) { return EXACT ? load4(tap_row<IO>(a, row0, slot, j, C) + ch) : load4(raw + j * 3 * D); };
+        *reinterpret_cast<float4 *>(dst) = cw(at(tap.x), at(tap.y), at(tap.z), at(tap.w));
       }
     } else if (tid - CT < D / 4) {
       const int c = 4 * (tid - CT);
-#pragma unroll 4
       for (int i = 0; i < W; ++i) {
-        const float4 x = load4(a.g + ((size_t)(row0 + i) * H + h) * D + c);
+        const float4 x = *reinterpret_cast<const float4 *>(s_g + i * D + c);
         const int p = s_par[i];
         float4 y = make_float4(fmaxf(x.x, a.g_min) * LOG2E, fmaxf(x.y, a.g_min) * LOG2E, fmaxf(x.z, a.g_min) * LOG2E,
                                fmaxf(x.w, a.g_min) * LOG2E);
@@ -222,43 +285,60 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 5 : 1) tree_ver
         *reinterpret_cast<float4 *>(s_g + i * D + c) = y;
       }
     }
-    __syncthreads();
-    // ---- the norms of k and q (a warp a row), kept as factors
-    for (int x = warp; x < 2 * W; x += NW) {
-      float rn = 1.f;
-      if (a.qk_l2norm) {
-        float ss = 0.f;
-        for (int c = lane; c < D; c += 32) ss = fmaf(s_x[x * XS + c], s_x[x * XS + c], ss);
-        rn = rsqrtf(warp_sum(ss) + a.l2_eps);
-      }
-      if (lane == 0) s_rn[x] = rn;
+    if (unit + gridDim.x < units) {  // the next unit's inputs
+      const uint32_t nu = unit + gridDim.x;
+      const int nn = (int)(nu / H), ns = a.slot_idx ? a.slot_idx[nn] : nn;
+      int nrow0;
+      const int nw = tree_nodes(a, nn, WM, nrow0, false);
+      if (ns >= 0 && ns < a.n_slots && nw > 0) ask_inputs<D, IO, 1, 0>(a, nrow0, nw, ns, (int)(nu % H), tid, NT);
     }
     __syncthreads();
-    // ---- A and B over the (node, ancestor or itself) pairs: eight lanes a pair, D / 8 channels each
+    // ---- the norms of k and q (eight lanes a row), kept as factors
+    for (int x = tid >> 3; x < 2 * W; x += NT / 8) {
+      float ss = 0.f;
+      for (int c = 4 * (tid & 7); c < D; c += 32) {
+        const float4 y = *reinterpret_cast<const float4 *>(s_x + x * XS + c);
+        ss = fmaf(y.x, y.x, fmaf(y.y, y.y, fmaf(y.z, y.z, fmaf(y.w, y.w, ss))));
+      }
+      const unsigned eight = 0xffu << (lane & 24);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(eight, ss, o);
+      if ((tid & 7) == 0) s_rn[x] = a.qk_l2norm ? rsqrtf(ss + a.l2_eps) : 1.f;
+    }
+    __syncthreads();
+    // ---- A and B over the (node, ancestor or itself) pairs: eight lanes a pair, every NT/8-th of
+    //      the running count of pairs to a group of lanes
     {
-      const int grp = tid >> 3, sub = tid & 7;
-      int at = grp;
+      const int sub = 4 * (tid & 7);
+      const unsigned eight = 0xffu << (lane & 24);
+      int at = tid >> 3;
       for (int i = 0; i < W; ++i) {
         unsigned long long m = s_anc[i] | (1ull << i);
         const int cnt = __popcll(m);
-        // this group's pairs of node i: every NT/8-th of the running count
         int k = at;
         for (int skipped = 0; k < cnt; k += NT / 8) {
           for (; skipped < k; ++skipped) m &= m - 1;
           const int j = __ffsll((long long)m) - 1;
           float pa = 0.f, pb = 0.f;
-          // channels sub, sub + 8, ..: neighbouring lanes on neighbouring banks
-#pragma unroll 4
-          for (int c = sub; c < D; c += 8) {
-            const float e = ex2_(s_g[i * D + c] - s_g[j * D + c]) * s_x[j * XS + c];
-            pa = fmaf(s_x[i * XS + c], e, pa);
-            pb = fmaf(s_x[(W + i) * XS + c], e, pb);
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            const int c = c0 + sub;
+            if (c < D) {
+              const float4 gi = *reinterpret_cast<const float4 *>(s_g + i * D + c),
+                           gj = *reinterpret_cast<const float4 *>(s_g + j * D + c);
+              const float4 kj = *reinterpret_cast<const float4 *>(s_x + j * XS + c),
+                           ki = *reinterpret_cast<const float4 *>(s_x + i * XS + c),
+                           qi = *reinterpret_cast<const float4 *>(s_x + (W + i) * XS + c);
+              const float e0 = ex2_(gi.x - gj.x) * kj.x, e1 = ex2_(gi.y - gj.y) * kj.y, e2 = ex2_(gi.z - gj.z) * kj.z,
+                          e3 = ex2_(gi.w - gj.w) * kj.w;
+              pa = fmaf(ki.x, e0, fmaf(ki.y, e1, fmaf(ki.z, e2, fmaf(ki.w, e3, pa))));
+              pb = fmaf(qi.x, e0, fmaf(qi.y, e1, fmaf(qi.z, e2, fmaf(qi.w, e3, pb))));
+            }
           }
-          const unsigned grp_mask = 0xffu << (lane & 24);
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) {
-            pa += __shfl_xor_sync(grp_mask, pa, o);
-            pb += __shfl_xor_sync(grp_mask, pb, o);
+            pa += __shfl_xor_sync(eight, pa, o);
+            pb += __shfl_xor_sync(eight, pb, o);
           }
           if (sub == 0) {
             s_A[i * WM + j] = pa * s_rn[i] * s_rn[j];
@@ -269,50 +349,84 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 5 : 1) tree_ver
       }
     }
     __syncthreads();
-    // ---- X = k e^G over q e^G
-    for (int x = tid; x < W * D / 4; x += NT) {
-      const int i = x / (D / 4), c = 4 * (x % (D / 4));
-      const float4 G = *reinterpret_cast<const float4 *>(s_g + i * D + c);
-      const float4 e = make_float4(ex2_(G.x), ex2_(G.y), ex2_(G.z), ex2_(G.w));
-      float4 *k = reinterpret_cast<float4 *>(s_x + i * XS + c), *q = reinterpret_cast<float4 *>(s_x + (W + i) * XS + c);
-      const float rk = s_rn[i], rq = s_rn[W + i];
-      float4 y = *k, z = *q;
-      y.x *= e.x * rk, y.y *= e.y * rk, y.z *= e.z * rk, y.w *= e.w * rk;
-      z.x *= e.x * rq, z.y *= e.y * rq, z.z *= e.z * rq, z.w *= e.w * rq;
-      *k = y, *q = z;
+    // ---- X = k e^G over q e^G, a warp a row; with bf16 I/O as [D] high parts, then [D] low parts
+    for (int x = warp; x < 2 * W; x += NW) {
+      float *row = s_x + x * XS;
+      const float *G = s_g + (x < W ? x : x - W) * D;
+      const float rn = s_rn[x];
+      const int c = 4 * lane;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < D) {
+        const float4 e = *reinterpret_cast<const float4 *>(G + c);
+        y = *reinterpret_cast<const float4 *>(row + c);
+        y.x *= ex2_(e.x) * rn, y.y *= ex2_(e.y) * rn, y.z *= ex2_(e.z) * rn, y.w *= ex2_(e.w) * rn;
+      }
+      if (EXACT) {
+        if (c < D) *reinterpret_cast<float4 *>(row + c) = y;
+      } else {
+        uint2 hi, lo;
+        split2(y.x, y.y, hi.x, lo.x);
+        split2(y.z, y.w, hi.y, lo.y);
+        __syncwarp();  // the row has been read
+        if (c < D) {
+          *reinterpret_cast<uint2 *>(row + c / 2) = hi;
+          *reinterpret_cast<uint2 *>(row + D / 2 + c / 2) = lo;
+        }
+      }
     }
     __syncthreads();
     // ---- X S: k's rows over G's place, q's into s_o
     for (int m0 = 0; m0 < 2 * W; m0 += 16) {
       float acc[NJ][4] = {};
-      // lane l of ldmatrix names row l % 8 of block l / 8: rows 0-7 | 8-15, channels 0-3 | 4-7
+      const ST *mine = src + CW * warp + NJ * g;
+      // lane l of ldmatrix names row l % 8 of block l / 8: rows 0-7 | 8-15, then 16 bytes on
       const float *rows = s_x + (m0 + (lane & 7) + (lane >> 3 & 1) * 8) * XS + (lane >> 4) * 4;
-      const ST *mine = src + (size_t)t * D + CW * warp + NJ * g;
-      constexpr int AHEAD = D / 8 < 4 ? D / 8 : 4;  // steps whose state is on its way
-      Cols<NJ> b[AHEAD][2];
+      if (EXACT) {
+#pragma unroll 4
+        for (int s = 0; s < D / 8; ++s) {  // rows 8 s + t and 8 s + 4 + t
+          Cols<NJ> b0, b1;
+          load_cols(b0, mine + (size_t)(8 * s + t) * D);
+          load_cols(b1, mine + (size_t)(8 * s + 4 + t) * D);
+          uint32_t x[4], hi[4], lo[4];
+          ldmatrix4(x, rows + 8 * s);
 #pragma unroll
-      for (int s = 0; s < AHEAD; ++s)
-        load_cols(b[s][0], mine + (size_t)8 * s * D), load_cols(b[s][1], mine + (size_t)(8 * s + 4) * D);
+          for (int y = 0; y < 4; ++y) {
+            hi[y] = tf32_(__uint_as_float(x[y]));
+            lo[y] = tf32_(__uint_as_float(x[y]) - __uint_as_float(hi[y]));
+          }
 #pragma unroll
-      for (int s = 0; s < D / 8; ++s) {
-        const Cols<NJ> b0 = b[s % AHEAD][0], b1 = b[s % AHEAD][1];
-        if (s + AHEAD < D / 8) {
-          load_cols(b[s % AHEAD][0], mine + (size_t)8 * (s + AHEAD) * D);
-          load_cols(b[s % AHEAD][1], mine + (size_t)(8 * (s + AHEAD) + 4) * D);
+          for (int j = 0; j < NJ; ++j) {
+            const uint32_t p1 = tf32_(b0.v[j]), q1 = tf32_(b1.v[j]);
+            mma_16x8x8(acc[j], lo, p1, q1);
+            mma_16x8x8(acc[j], hi, tf32_(b0.v[j] - __uint_as_float(p1)), tf32_(b1.v[j] - __uint_as_float(q1)));
+            mma_16x8x8(acc[j], hi, p1, q1);
+          }
         }
-        uint32_t x[4], hi[4], lo[4];
-        ldmatrix4(x, rows + 8 * s);
+      } else {
+        constexpr int STEPS = D / 16;
+        Cols<NJ> b0[4];  // rows 16 s + 2 t, + 1, + 8, + 9 of this step and the next
+        auto fetch = [&](Cols<NJ> (&x)[4], int s) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          hi[y] = tf32_(__uint_as_float(x[y]));
-          lo[y] = tf32_(__uint_as_float(x[y]) - __uint_as_float(hi[y]));
-        }
+          for (int y = 0; y < 4; ++y) load_cols(x[y], mine + (size_t)(16 * s + 2 * t + (y & 1) + (y >> 1) * 8) * D);
+        };
+        auto multiply = [&](const Cols<NJ> (&x)[4], int s) {
+          uint32_t hi[4], lo[4];
+          ldmatrix4(hi, rows + 8 * s);
+          ldmatrix4(lo, rows + D / 2 + 8 * s);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const uint32_t p1 = tf32_(b0.v[j]), q1 = tf32_(b1.v[j]);
-          mma_16x8x8(acc[j], lo, p1, q1);
-          mma_16x8x8(acc[j], hi, tf32_(b0.v[j] - __uint_as_float(p1)), tf32_(b1.v[j] - __uint_as_float(q1)));
-          mma_16x8x8(acc[j], hi, p1, q1);
+          for (int j = 0; j < NJ; ++j) {
+            uint32_t p1, q1, p2, q2;
+            split2(x[0].v[j], x[1].v[j], p1, p2);
+            split2(x[2].v[j], x[3].v[j], q1, q2);
+            mma_16x8x16(acc[j], lo, p1, q1);
+            mma_16x8x16(acc[j], hi, p2, q2);
+            mma_16x8x16(acc[j], hi, p1, q1);
+          }
+        };
+#pragma unroll 1
+        for (int s = 0; s < STEPS; ++s) {
+          fetch(b0, s);
+          multiply(b0, s);
         }
       }
 #pragma unroll
@@ -342,8 +456,11 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 5 : 1) tree_ver
     // ---- the reads, norm and gate: a warp a node, a lane four neighbouring columns
     for (int i = warp; i < W; i += NW) {
       const int c = 4 * lane;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      const size_t row = ((size_t)(row0 + i) * H + h) * D + c;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f), z = o, w = make_float4(1.f, 1.f, 1.f, 1.f);
       if (c < D) {
+        if (a.gate) z = load4(reinterpret_cast<const IO *>(a.gate) + row);
+        if (a.gate && a.norm_w) w = load4(a.norm_w + c);
         o = *reinterpret_cast<const float4 *>(s_o + i * D + c);
         for (unsigned long long m = s_anc[i] | (1ull << i); m; m &= m - 1) {
           const int j = __ffsll((long long)m) - 1;
@@ -353,15 +470,10 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 5 : 1) tree_ver
         }
         o.x *= a.scale, o.y *= a.scale, o.z *= a.scale, o.w *= a.scale;
       }
-      const size_t row = ((size_t)(row0 + i) * H + h) * D + c;
       if (a.gate) {
         const float rn = rsqrtf(warp_sum(o.x * o.x + o.y * o.y + o.z * o.z + o.w * o.w) / D + a.norm_eps);
-        if (c < D) {
-          const float4 z = load4(reinterpret_cast<const IO *>(a.gate) + row);
-          const float4 w = a.norm_w ? load4(a.norm_w + c) : make_float4(1.f, 1.f, 1.f, 1.f);
-          o.x *= rn * w.x * sigmoid_(z.x), o.y *= rn * w.y * sigmoid_(z.y), o.z *= rn * w.z * sigmoid_(z.z),
-              o.w *= rn * w.w * sigmoid_(z.w);
-        }
+        o.x *= rn * w.x * sigmoid_(z.x), o.y *= rn * w.y * sigmoid_(z.y), o.z *= rn * w.z * sigmoid_(z.z),
+            o.w *= rn * w.w * sigmoid_(z.w);
       }
       if (c < D) store4(reinterpret_cast<IO *>(a.out) + row, o);
     }
@@ -390,10 +502,10 @@ __global__ void __launch_bounds__(2 * D, 2) tree_accept_kernel(const TreeArgs a,
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cq = lane & 3, rg = lane >> 2, col = 16 * warp + 4 * cq;
   const int H = a.H;
-  const int64_t groups = (int64_t)a.n_seqs * H / group;
+  const uint32_t groups = (uint32_t)a.n_seqs * (uint32_t)H / group;  // at most 65535 x 21845
   const size_t C = (size_t)3 * H * D;
 
-  for (int64_t unit = blockIdx.x; unit < groups; unit += gridDim.x) {
+  for (uint32_t unit = blockIdx.x; unit < groups; unit += gridDim.x) {
     const int h0 = (int)(unit * group % H), n = (int)(unit * group / H);
     const int slot = a.slot_idx ? a.slot_idx[n] : n;
     int row0;
@@ -405,7 +517,7 @@ __global__ void __launch_bounds__(2 * D, 2) tree_accept_kernel(const TreeArgs a,
     }
     if (last < 0) continue;  // nothing accepted: state and tail stay
     ST *state = reinterpret_cast<ST *>(a.state) + ((size_t)slot * H + h0) * (size_t)D * D;
-    ask_l2(state, sizeof(ST) * D * D, tid, NT);
+    if (unit == blockIdx.x) ask_l2(state, sizeof(ST) * D * D, tid, NT);
     __syncthreads();  // the previous group's shared memory has been read
     for (int i = tid; i <= last; i += NT) {
       int p = a.parent[row0 + i];
@@ -471,7 +583,19 @@ __global__ void __launch_bounds__(2 * D, 2) tree_accept_kernel(const TreeArgs a,
         const float4 x = load4_stream(st + (size_t)(R * rg + r) * D);
         S[r][0] = x.x, S[r][1] = x.y, S[r][2] = x.z, S[r][3] = x.w;
       }
-      if (y + 1 < group) ask_l2(state + (size_t)(y + 1) * D * D, sizeof(ST) * D * D, tid, NT);
+      if (y + 1 < group) {
+        ask_l2(state + (size_t)(y + 1) * D * D, sizeof(ST) * D * D, tid, NT);
+      } else if (unit + gridDim.x < groups) {  // the next group's first head
+        const uint32_t nu = (unit + gridDim.x) * group;
+        const int nn = (int)(nu / H), ns = a.slot_idx ? a.slot_idx[nn] : nn;
+        int nrow0;
+        const int nw = tree_nodes(a, nn, 64, nrow0, false), nl = a.accept[nn];
+        if (ns >= 0 && ns < a.n_slots && nl >= 0 && nl < nw) {
+          ask_l2(reinterpret_cast<const ST *>(a.state) + ((size_t)ns * H + nu % H) * (size_t)D * D, sizeof(ST) * D * D, tid, NT);
+          if (group == 2) ask_inputs<D, IO, 2, 1>(a, nrow0, nl + 1, ns, (int)(nu % H), tid, NT);
+          else ask_inputs<D, IO, 1, 1>(a, nrow0, nl + 1, ns, (int)(nu % H), tid, NT);
+        }
+      }
       for (int d0 = 0; d0 < m; d0 += AT) {
         const int nt = m - d0 < AT ? m - d0 : AT, at0 = together ? y * AT : 0;
         if (!together) {
@@ -561,17 +685,18 @@ cudaError_t launch_typed(const TreeArgs &a, bool accept, cudaStream_t s) {
   int64_t fit = 0;
   if (accept) {
     constexpr auto kernel = tree_accept_kernel<D, IO, ST>;
-    cudaError_t e = fitting<kernel>(2 * D, accept_smem<D>(4), accept_smem<D>(4), &fit);
+    cudaError_t e = fitting<kernel>(2 * D, accept_smem<D>(2), accept_smem<D>(2), &fit);
     if (e != cudaSuccess) return e;
-    // heads staged together while that leaves every CTA several groups
-    int group = 1;
-    while (group < 4 && a.H % (2 * group) == 0 && units / (2 * group) >= 4 * fit) group *= 2;
+    // two heads staged together where that leaves every CTA several groups (measured at 256 sequences
+    // x 64 heads: 568 us one head at a time, 468 two, 505 four, whose paths differ too much in length)
+    const int group = a.H % 2 == 0 && units / 2 >= 4 * fit ? 2 : 1;
     const int64_t groups = units / group;
     kernel<<<(unsigned)(groups < fit ? groups : fit), 2 * D, accept_smem<D>(group), s>>>(a, group);
   } else {
     constexpr auto kernel = tree_verify_kernel<D, IO, ST>;
-    const size_t smem = verify_smem_floats(a.max_nodes, D) * sizeof(float);
-    cudaError_t e = fitting<kernel>(VerifyShape<D>::NT, smem, verify_smem_floats(64, D) * sizeof(float), &fit);
+    constexpr bool staged = sizeof(IO) == 2;
+    const size_t smem = verify_smem_floats(a.max_nodes, D, staged) * sizeof(float);
+    cudaError_t e = fitting<kernel>(VerifyShape<D>::NT, smem, verify_smem_floats(64, D, staged) * sizeof(float), &fit);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)(units < fit ? units : fit), VerifyShape<D>::NT, smem, s>>>(a);
   }
