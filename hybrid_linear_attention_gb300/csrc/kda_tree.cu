@@ -147,7 +147,8 @@ __device__ __forceinline__ void ask_inputs(const TreeArgs &a, int row0, int rows
 // the raw inputs [W + 3][3 D] where those are staged (bf16)
 __host__ __device__ constexpr size_t verify_smem_floats(int W, int D, bool staged) {
   const size_t late = (size_t)W * D + (size_t)2 * W * W, raw = staged ? ((size_t)(W + 3) * 3 * D + 1) / 2 : 0;
-  return (size_t)((2 * W + 15) / 16 * 16) * (D + 4) + (size_t)2 * W * D + (late > raw ? late : raw);
+  const size_t all = (size_t)((2 * W + 15) / 16 * 16) * (D + 4) + (size_t)2 * W * D + (late > raw ? late : raw);
+  return (all + 3) / 4 * 4;  // what follows starts on 16 bytes
 }
 __device__ __forceinline__ void copy_async16(void *smem, const void *global) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global)
@@ -177,6 +178,20 @@ __device__ __forceinline__ void load_cols(Cols<2> &c, const ST *p) {
   const float2 x = load2(p);
   c.v[0] = x.x, c.v[1] = x.y;
 }
+template <typename ST>
+__device__ __forceinline__ void load_cols_shared(Cols<4> &c, const ST *p) {
+  const float4 x = load4(p);
+  c.v[0] = x.x, c.v[1] = x.y, c.v[2] = x.z, c.v[3] = x.w;
+}
+template <typename ST>
+__device__ __forceinline__ void load_cols_shared(Cols<2> &c, const ST *p) {
+  load_cols(c, p);
+}
+// floats that a state kept in shared memory takes (rows padded by 16 bytes)
+template <int D, typename ST>
+constexpr size_t resident_floats() {
+  return (size_t)D * (D * sizeof(ST) + 16) / 4;
+}
 
 // With X the 2 W rows k_i e^{G_i} and q_i e^{G_i}, the product X S is what the state is read for; it
 // runs on the tensor cores (mma.sync, 16 rows of X at a time: there are too few rows for the 128-row
@@ -188,8 +203,10 @@ __device__ __forceinline__ void load_cols(Cols<2> &c, const ST *p) {
 // A CTA is small (four warps, no state held), so that seven share an SM, each in another of the phases
 // that the few barriers of a unit cut.  bf16 inputs come into shared memory by asynchronous copies
 // that run while the tree is worked out.
-template <int D, typename IO, typename ST>
-__global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 7 : 1) tree_verify_kernel(const TreeArgs a) {
+// RESIDENT: with few units the state comes into shared memory the same way, all at once; read step by
+// step from L2 it would be most of a lone unit's time (one sequence x 12 nodes x 64 heads: MEASURED).
+template <int D, typename IO, typename ST, bool RESIDENT>
+__global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 : 7) : 1) tree_verify_kernel(const TreeArgs a) {
   constexpr int CW = VerifyShape<D>::CW, NT = VerifyShape<D>::NT, NJ = VerifyShape<D>::NJ, NW = NT / 32, XS = D + 4;
   constexpr int CT = 3 * D / 4;  // threads of the convolution, four channels each
   constexpr bool EXACT = sizeof(IO) == 4;
@@ -202,6 +219,8 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 7 : 1) tree_ver
   float *s_x = smem, *s_v = s_x + (2 * WM + 15) / 16 * 16 * XS, *s_g = s_v + WM * D, *s_o = s_g + WM * D,
         *s_A = s_o + WM * D, *s_B = s_A + WM * WM;
   IO *s_raw = reinterpret_cast<IO *>(s_o);  // row 3 + i: node i, rows 0 .. 2 the tail
+  constexpr int SS = D + 16 / (int)sizeof(ST);
+  ST *s_S = reinterpret_cast<ST *>(smem + verify_smem_floats(WM, D, !EXACT));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t H = a.H, units = (uint32_t)a.n_seqs * H;  // at most 65535 x 21845
@@ -228,7 +247,14 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 7 : 1) tree_ver
     }
     for (int x = tid; x < W * (D / 4); x += NT)
       copy_async16(s_g + 4 * x, a.g + ((size_t)(row0 + x / (D / 4)) * H + h) * D + 4 * (x % (D / 4)));
-    ask_l2(src, sizeof(ST) * D * D, tid, NT);  // needed a few phases on (any earlier, and L2 drops it again)
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (RESIDENT) {
+      constexpr int P = 16 / (int)sizeof(ST);
+      for (int x = tid; x < D * D / P; x += NT) copy_async16(s_S + x / (D / P) * SS + x % (D / P) * P, src + (size_t)x * P);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else {
+      ask_l2(src, sizeof(ST) * D * D, tid, NT);  // needed a few phases on (any earlier, and L2 drops it again)
+    }
 
     // ---- the sequence's tree ---------------------------------------------------------------------
     for (int i = tid; i < W; i += NT) {
@@ -252,7 +278,7 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 7 : 1) tree_ver
       for (int j = s_par[i]; j >= 0; j = s_par[j]) m |= 1ull << j;
       s_anc[i] = m;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(RESIDENT ? 1 : 0) : "memory");
     __syncthreads();
 
     // ---- q, k, v of every node after the convolution along its path (a thread four channels of a
@@ -349,6 +375,7 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 7 : 1) tree_ver
       }
     }
     __syncthreads();
+    if (RESIDENT) asm volatile("cp.async.wait_group 0;" ::: "memory");
     // ---- X = k e^G over q e^G, a warp a row; with bf16 I/O as [D] high parts, then [D] low parts
     for (int x = warp; x < 2 * W; x += NW) {
       float *row = s_x + x * XS;
@@ -378,15 +405,20 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 7 : 1) tree_ver
     // ---- X S: k's rows over G's place, q's into s_o
     for (int m0 = 0; m0 < 2 * W; m0 += 16) {
       float acc[NJ][4] = {};
-      const ST *mine = src + CW * warp + NJ * g;
+      const ST *mine = (RESIDENT ? s_S : src) + CW * warp + NJ * g;
+      constexpr int LD = RESIDENT ? SS : D;
+      auto rows_of = [&](Cols<NJ> &x, int r) {
+        if (RESIDENT) load_cols_shared(x, mine + r * LD);
+        else load_cols(x, mine + (size_t)r * LD);
+      };
       // lane l of ldmatrix names row l % 8 of block l / 8: rows 0-7 | 8-15, then 16 bytes on
       const float *rows = s_x + (m0 + (lane & 7) + (lane >> 3 & 1) * 8) * XS + (lane >> 4) * 4;
       if (EXACT) {
 #pragma unroll 4
         for (int s = 0; s < D / 8; ++s) {  // rows 8 s + t and 8 s + 4 + t
           Cols<NJ> b0, b1;
-          load_cols(b0, mine + (size_t)(8 * s + t) * D);
-          load_cols(b1, mine + (size_t)(8 * s + 4 + t) * D);
+          rows_of(b0, 8 * s + t);
+          rows_of(b1, 8 * s + 4 + t);
           uint32_t x[4], hi[4], lo[4];
           ldmatrix4(x, rows + 8 * s);
 #pragma unroll
@@ -407,7 +439,7 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? 7 : 1) tree_ver
         Cols<NJ> b0[4];  // rows 16 s + 2 t, + 1, + 8, + 9 of this step and the next
         auto fetch = [&](Cols<NJ> (&x)[4], int s) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) load_cols(x[y], mine + (size_t)(16 * s + 2 * t + (y & 1) + (y >> 1) * 8) * D);
+          for (int y = 0; y < 4; ++y) rows_of(x[y], 16 * s + 2 * t + (y & 1) + (y >> 1) * 8);
         };
         auto multiply = [&](const Cols<NJ> (&x)[4], int s) {
           uint32_t hi[4], lo[4];
@@ -679,6 +711,7 @@ cudaError_t fitting(int threads, size_t smem, size_t smem_most, int64_t *ctas) {
   return cudaSuccess;
 }
 
+constexpr size_t SMEM_MOST = 220 * 1024;  // of a CTA, beside the kernels' static part
 template <int D, typename IO, typename ST>
 cudaError_t launch_typed(const TreeArgs &a, bool accept, cudaStream_t s) {
   const int64_t units = (int64_t)a.n_seqs * a.H;
@@ -693,12 +726,23 @@ cudaError_t launch_typed(const TreeArgs &a, bool accept, cudaStream_t s) {
     const int64_t groups = units / group;
     kernel<<<(unsigned)(groups < fit ? groups : fit), 2 * D, accept_smem<D>(group), s>>>(a, group);
   } else {
-    constexpr auto kernel = tree_verify_kernel<D, IO, ST>;
     constexpr bool staged = sizeof(IO) == 2;
     const size_t smem = verify_smem_floats(a.max_nodes, D, staged) * sizeof(float);
-    cudaError_t e = fitting<kernel>(VerifyShape<D>::NT, smem, verify_smem_floats(64, D, staged) * sizeof(float), &fit);
+    const size_t most = verify_smem_floats(64, D, staged) * sizeof(float), extra = resident_floats<D, ST>() * sizeof(float);
+    constexpr int NT = VerifyShape<D>::NT;
+    if (smem + extra <= SMEM_MOST) {
+      constexpr auto kernel = tree_verify_kernel<D, IO, ST, true>;
+      cudaError_t e = fitting<kernel>(NT, smem + extra, SMEM_MOST, &fit);
+      if (e != cudaSuccess) return e;
+      if (units <= fit) {
+        kernel<<<(unsigned)units, NT, smem + extra, s>>>(a);
+        return cudaGetLastError();
+      }
+    }
+    constexpr auto kernel = tree_verify_kernel<D, IO, ST, false>;
+    cudaError_t e = fitting<kernel>(NT, smem, most, &fit);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(units < fit ? units : fit), VerifyShape<D>::NT, smem, s>>>(a);
+    kernel<<<(unsigned)(units < fit ? units : fit), NT, smem, s>>>(a);
   }
   return cudaGetLastError();
 }
