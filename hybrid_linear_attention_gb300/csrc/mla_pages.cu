@@ -40,38 +40,58 @@ __device__ __forceinline__ void flag(int *err, int bit) {
 
 // ---- rows ------------------------------------------------------------------------------------
 
-// Row t of sequence n's new rows goes to position lengths[n] + t.  A CTA takes four rows; 72
-// threads copy a row's 72 pieces in up to eight layers at a time.
-constexpr int AP_ROWS = 4, AP_NT = AP_ROWS * ROW16;
+// Row t of sequence n's new rows goes to position lengths[n] + t.  A CTA takes four rows: 72 threads
+// read a row's 72 pieces of up to nine layers while a warp looks up where the row goes (32 sequences'
+// offsets at a step), then write them.
+constexpr int AP_ROWS = 4, AP_NT = AP_ROWS * ROW16, AP_LAYERS = 9;
 __global__ void __launch_bounds__(AP_NT) cache_append_kernel(const PagedCache c, const int32_t *cu,
                                                              int n_seqs, int64_t total,
                                                              const uint4 *rows) {
+  __shared__ int s_page[AP_ROWS], s_row[AP_ROWS];
   if (blockIdx.x == 0)
     for (int n = threadIdx.x; n < n_seqs; n += AP_NT)
       if (cu[n] < 0 || cu[n + 1] < cu[n] || cu[n + 1] > total) flag(c.err, ERR_BAD_SEQLEN);
   const int64_t t = (int64_t)blockIdx.x * AP_ROWS + threadIdx.x / ROW16;
   const int piece = threadIdx.x % ROW16;
+  uint4 x[AP_LAYERS];
+#pragma unroll
+  for (int y = 0; y < AP_LAYERS; ++y)
+    if (t < total && y < c.n_layers) x[y] = __ldcs(rows + ((size_t)y * total + t) * ROW16 + piece);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t mine = (int64_t)blockIdx.x * AP_ROWS + warp;
+  if (warp < AP_ROWS && mine < total) {
+    // the last sequence whose first row is at most this one, among lo .. hi - 1
+    int lo = 0, hi = n_seqs;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, at < hi && (int64_t)cu[at] <= mine);
+      const int k = m ? 31 - __clz(m) : 0;  // offsets that do not rise give some place, inside all the same
+      hi = lo + (k + 1) * step < hi ? lo + (k + 1) * step : hi;
+      lo += k * step;
+    }
+    if (lane == 0) {
+      const int64_t first = cu[lo], end = cu[lo + 1];
+      int page = -2, row = 0;  // no sequence's row: not written
+      if (first >= 0 && mine >= first && mine < end && end <= total) {
+        const int len = c.lengths[lo];
+        const int64_t pos = (int64_t)len + (mine - first);
+        page = len < 0 ? -1 : page_of(c, lo, pos);
+        row = (int)(pos % c.page_size);
+        if (page < 0) flag(c.err, ERR_BAD_INDEX);
+      }
+      s_page[warp] = page;
+      s_row[warp] = row;
+    }
+  }
+  __syncthreads();
   if (t >= total) return;
-  const int n = seq_of_token(cu, n_seqs, t);
-  const int64_t lo = cu[n], hi = cu[n + 1];
-  if (lo < 0 || t < lo || t >= hi || hi > total) return;  // no sequence's row: not written
-  const int len = c.lengths[n];
-  const int64_t pos = (int64_t)len + (t - lo);
-  const int page = len < 0 ? -1 : page_of(c, n, pos);
-  if (page < 0) {
-    if (piece == 0) flag(c.err, ERR_BAD_INDEX);
-    return;
-  }
-  const int row = (int)(pos % c.page_size);
-  for (int l0 = 0; l0 < c.n_layers; l0 += 8) {
-    uint4 x[8];
+  const int page = s_page[threadIdx.x / ROW16], row = s_row[threadIdx.x / ROW16];
+  if (page < 0) return;
 #pragma unroll
-    for (int y = 0; y < 8; ++y)
-      if (l0 + y < c.n_layers) x[y] = __ldcs(rows + ((size_t)(l0 + y) * total + t) * ROW16 + piece);
-#pragma unroll
-    for (int y = 0; y < 8; ++y)
-      if (l0 + y < c.n_layers) pool_row(c, l0 + y, page, row)[piece] = x[y];
-  }
+  for (int y = 0; y < AP_LAYERS; ++y)
+    if (y < c.n_layers) pool_row(c, y, page, row)[piece] = x[y];
+  for (int l = AP_LAYERS; l < c.n_layers; ++l)
+    pool_row(c, l, page, row)[piece] = __ldcs(rows + ((size_t)l * total + t) * ROW16 + piece);
 }
 
 // The accepted path's rows moved up to lengths[n], lengths[n] + 1, ..: step d of the path is

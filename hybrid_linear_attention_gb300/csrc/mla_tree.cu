@@ -227,6 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     s_off = 0;
   }
   if (tid < 4) s_cost[tid] = 0;
+  if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(tid ? &maps.c : &maps.q) : "memory");
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -766,33 +767,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u));
 }
 
-// z = sum_w 2^(m_w - M) Z_w / sum_w 2^(m_w - M) l_w over the workers w that hold parts of a row;
-// 128 threads a row, the parts' loads independent of the running sums.
-__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeAttnArgs a, const float *part, const float *part_ml,
+// z = sum_w 2^(m_w - M) Z_w / sum_w 2^(m_w - M) l_w over the workers w that hold parts of a row; a warp
+// a row, the parts' loads independent of the running sums.
+constexpr int CNT = 256, CROWS = CNT / 32;
+__global__ void __launch_bounds__(CNT) tree_combine_kernel(const TreeAttnArgs a, const float *part, const float *part_ml,
                                                            const Merge *merge) {
+  // launched while the attention kernel runs out: its results are there once this returns
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Merge g = merge[blockIdx.x];
-  const int row = 2 * blockIdx.y + (threadIdx.x >> 7), t = threadIdx.x & 127;
+  const int row = CROWS * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= g.rows) return;
   const int member = blockIdx.x % g.group;
   // the first worker's part is the end of its run, the others' the beginning of theirs
   auto slot = [&](int w) { return (size_t)(2 * (w * g.group + member) + (w == g.first ? 1 : 0)) * 2 * RC + row; };
   float M = -INFINITY;
-  for (int w = g.first; w <= g.last; ++w) M = fmaxf(M, part_ml[slot(w) * 2]);
-  float z[4] = {0.f, 0.f, 0.f, 0.f}, L = 0.f;
-#pragma unroll 4
+  for (int w = g.first + lane; w <= g.last; w += 32) M = fmaxf(M, part_ml[slot(w) * 2]);
+  M = warp_max(M);
+  float4 z[4] = {};
+  float L = 0.f;
+#pragma unroll 2
   for (int w = g.first; w <= g.last; ++w) {
     const size_t s = slot(w);
     const float m = part_ml[s * 2], l = part_ml[s * 2 + 1];
-    const float4 x = load4(part + s * TL + 4 * t);
+    float4 x[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) x[y] = load4(part + s * TL + 128 * y + 4 * lane);
     const float f = m == -INFINITY ? (l == 0.f ? 0.f : l) : exp2f(m - M);  // l NaN: the row is NaN
     L = fmaf(f, l, L);
-    z[0] = fmaf(f, x.x, z[0]), z[1] = fmaf(f, x.y, z[1]), z[2] = fmaf(f, x.z, z[2]), z[3] = fmaf(f, x.w, z[3]);
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      z[y].x = fmaf(f, x[y].x, z[y].x), z[y].y = fmaf(f, x[y].y, z[y].y), z[y].z = fmaf(f, x[y].z, z[y].z),
+      z[y].w = fmaf(f, x[y].w, z[y].w);
   }
   const float r = L == 0.f ? 0.f : 1.f / L;
-  const float4 v = make_float4(z[0] * r, z[1] * r, z[2] * r, z[3] * r);
-  const int64_t at = ((int64_t)g.row0 + row) * TL + 4 * t;
-  if (a.z_bf16) store4(reinterpret_cast<bf16 *>(a.z) + at, v);
-  else store4(reinterpret_cast<float *>(a.z) + at, v);
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const float4 v = make_float4(z[y].x * r, z[y].y * r, z[y].z * r, z[y].w * r);
+    const int64_t at = ((int64_t)g.row0 + row) * TL + 128 * y + 4 * lane;
+    if (a.z_bf16) store4(reinterpret_cast<bf16 *>(a.z) + at, v);
+    else store4(reinterpret_cast<float *>(a.z) + at, v);
+  }
 }
 
 bool tree_map(CUtensorMap *m, const void *ptr, int64_t d1, int64_t d2, int box_rows) {
@@ -841,9 +855,15 @@ cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ++*launches;
-  tree_combine_kernel<<<dim3(clusters, RC), 256, 0, s>>>(a, part, part_ml, merge);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters, 2 * RC / CROWS), cfg.blockDim = dim3(CNT), cfg.stream = s;
+  cudaLaunchAttribute early;  // its launch overlaps the attention kernel's end
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early, cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tree_combine_kernel, a, (const float *)part, (const float *)part_ml, (const Merge *)merge);
   ++*launches;
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace kda

@@ -77,6 +77,8 @@ _P = ctypes.POINTER(KdaParams)
 def load():
     """Loads libkda.so (built by hybrid_linear_attention_gb300.build.build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -188,9 +190,15 @@ def kda_params_default():
     return p
 
 
+_Tensor = torch.Tensor
+
+
 def _ptr(t, dtype=None, name="tensor"):
     if t is None:
         return None
+    if (isinstance(t, _Tensor) and t.is_cuda and t.is_contiguous()
+            and (dtype is None or t.dtype == dtype)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor or None")
     if not t.is_cuda:
@@ -511,7 +519,7 @@ def mla_decode(q_nope, q_rope, w_uk, w_uv, cache, lengths, gate_logit, q_cat, z,
 # ---- verifying a tree of drafted tokens -------------------------------------------------------
 
 def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
 
 
@@ -572,20 +580,26 @@ def mla_tree_workspace_size(n_seqs, total_nodes, H=64):
 
 def _paged(pool, page_table, lengths, n_seqs):
     """pool .. lengths of one layer ([n_pages, page_size, 576])."""
-    _shape(pool, (pool.shape[0], pool.shape[1], 576), "pool")
+    shape = pool.shape
+    if len(shape) != 3 or shape[2] != 576:
+        raise ValueError("pool: expected [n_pages, page_size, 576]")
     if page_table.shape[0] < n_seqs or lengths.shape[0] < n_seqs:
         raise ValueError("page_table, lengths: fewer rows than sequences")
-    return [_ptr(pool, torch.bfloat16, "pool"), pool.shape[0], pool.shape[1],
+    return [_ptr(pool, torch.bfloat16, "pool"), shape[0], shape[1],
             _ptr(page_table, torch.int32, "page_table"), page_table.shape[1],
             _ptr(lengths, torch.int32, "lengths")]
 
 
 def _paged_layers(pool, page_table, lengths, n_seqs):
     """pool .. lengths of all layers ([n_layers, n_pages, page_size, 576])."""
-    if pool.dim() != 4:
+    shape = pool.shape
+    if len(shape) != 4 or shape[3] != 576:
         raise ValueError("pool: expected [n_layers, n_pages, page_size, 576]")
-    one = _paged(pool[0], page_table, lengths, n_seqs)
-    return [_ptr(pool, torch.bfloat16, "pool"), pool.shape[0]] + one[1:]
+    if page_table.shape[0] < n_seqs or lengths.shape[0] < n_seqs:
+        raise ValueError("page_table, lengths: fewer rows than sequences")
+    return [_ptr(pool, torch.bfloat16, "pool"), shape[0], shape[1], shape[2],
+            _ptr(page_table, torch.int32, "page_table"), page_table.shape[1],
+            _ptr(lengths, torch.int32, "lengths")]
 
 
 _DTYPE = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
