@@ -192,8 +192,10 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ int64_t run_start(int64_t tiles, int w, int workers) { return tiles * w / workers; }
-
+// The first tile of worker w's run (a 64-bit division costs hundreds of cycles: only where needed).
+__device__ __forceinline__ int64_t run_start(int64_t tiles, int w, int workers) {
+  return tiles < (1 << 24) ? (int64_t)((uint32_t)tiles * (uint32_t)w / (uint32_t)workers) : tiles * w / workers;
+}
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     tree_attn_kernel(const TreeAttnArgs a, const __grid_constant__ TreeMaps maps, float *part, float *part_ml,
                      Merge *merge) {
@@ -259,7 +261,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     float best = INFINITY;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const float cost = (clusters >> g) ? (float)s_cost[g] / (float)(clusters >> g) * (g == 0 ? 1.f : g == 1 ? 0.93f : 0.87f) : INFINITY;
+      const float cost = (clusters >> g) ? __fdividef((float)s_cost[g] * (g == 0 ? 1.f : g == 1 ? 0.93f : 0.87f), (float)(clusters >> g))
+                                         : INFINITY;
       if (cost <= best) best = cost, group = 1 << g, workers = clusters >> g;
     }
   }
@@ -684,6 +687,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         uint8_t *stage = sm + OFF_P + warp * 4096;
         const bool bits = whole && a.z_bf16;
         const int col0 = 256 * ph + 128 * hf, first = 32 * (qw & 1);  // of the warp: latents, rows
+        const int width = bits ? 2 : 4;
+        // this lane's 16 bytes of the warp's first row: in z, or in this run's partial sums
+        char *dst = (whole ? reinterpret_cast<char *>(a.z) + ((int64_t)s.lo * a.H + r0 + first) * TL * width
+                           : reinterpret_cast<char *>(part) + ((size_t)slot * 2 * RC + RC * rank + first) * TL * 4) +
+                    col0 * width + 16 * (lane & 7);
 #pragma unroll 1
         for (int c = 0; c < 128; c += bits ? 64 : 32) {
           float z[32];
@@ -719,11 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
             const int r = 4 * x + (lane >> 3), piece = lane & 7;
             const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
             if (first + r < rows) {
-              const int64_t g = (int64_t)s.lo * a.H + r0 + first + r;  // row of the batch
-              char *dst = bits ? reinterpret_cast<char *>(reinterpret_cast<bf16 *>(a.z) + g * TL + col0 + c)
-                         : whole ? reinterpret_cast<char *>(reinterpret_cast<float *>(a.z) + g * TL + col0 + c)
-                                 : reinterpret_cast<char *>(part + ((size_t)slot * 2 * RC + RC * rank + first + r) * TL + col0 + c);
-              *reinterpret_cast<uint4 *>(dst + 16 * piece) = v;
+              *reinterpret_cast<uint4 *>(dst + (size_t)r * TL * width + c * width) = v;
             }
           }
           __syncwarp();
@@ -747,7 +751,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           const int64_t first_tile = begin - walk.t0;
           g.row0 = s.lo * a.H + 2 * RC * walk.rt;
           g.rows = s.W * a.H - 2 * RC * walk.rt < 2 * RC ? s.W * a.H - 2 * RC * walk.rt : 2 * RC;
-          g.first = (int)(((first_tile + 1) * workers - 1) / tiles);
+          g.first = (int)(((first_tile + 1) * workers - 1) / tiles);  // the last run that starts at or before it
           g.last = worker;
         }
         merge[cid] = g;
