@@ -26,6 +26,11 @@ namespace {
 __device__ __forceinline__ void l2_prefetch(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
+// Launched while the kernel before runs out; waits here until that one is complete.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
+}
+
 // 2^x, 1/x and the sigmoid on the special-function unit (relative errors about 2^-22)
 __device__ __forceinline__ float ex2_(float x) {
   float y;
@@ -203,8 +208,12 @@ constexpr size_t resident_floats() {
 // A CTA is small (four warps, no state held), so that seven share an SM, each in another of the phases
 // that the few barriers of a unit cut.  bf16 inputs come into shared memory by asynchronous copies
 // that run while the tree is worked out.
-// RESIDENT: with few units the state comes into shared memory the same way, all at once; read step by
-// step from L2 it would be most of a lone unit's time (one sequence x 12 nodes x 64 heads: MEASURED).
+// RESIDENT: with few units (no more than fit at a time) the state comes into shared memory the same
+// way, all at once; read step by step from L2 it would be most of a lone unit's time (one sequence x
+// 12 nodes x 64 heads: 19.7 us so, 16.2 resident).
+// Measured at 256 sequences x 6 to 8 nodes x 64 heads: 357 us (3.7 TB/s of what it must move, 1.36 GB
+// read from HBM), 14,000 warp instructions a unit at 55 % of the issue slots: issue and the phases'
+// latencies bound it, no longer the memory.  Five CTAs of 96 registers an SM took 419 us, eight 364.
 template <int D, typename IO, typename ST, bool RESIDENT>
 __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 : 7) : 1) tree_verify_kernel(const TreeArgs a) {
   constexpr int CW = VerifyShape<D>::CW, NT = VerifyShape<D>::NT, NJ = VerifyShape<D>::NJ, NW = NT / 32, XS = D + 4;
@@ -223,6 +232,7 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
   ST *s_S = reinterpret_cast<ST *>(smem + verify_smem_floats(WM, D, !EXACT));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  after_previous();
   const uint32_t H = a.H, units = (uint32_t)a.n_seqs * H;  // at most 65535 x 21845
   const size_t C = (size_t)3 * H * D;
 
@@ -518,7 +528,9 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
 // the tokens are staged in shared memory (k normalised, v, retention, strength) the warps need
 // nothing from each other.  A CTA takes `group` heads of a sequence at a time and stages all their
 // tokens together: the path is worked out once, and the warps go through the heads' states without
-// a barrier.  Bound by the state's bytes, read and written.
+// a barrier.  Bound by the state's bytes, read and written: 443 us for 256 sequences x 64 heads x 3.2
+// tokens, 5.1 TB/s (without the next group's inputs asked of L2 473; two CTAs of eight warps an SM are
+// what the registers hold, and they do not hide all of the staging).
 constexpr int AT = 8;  // path tokens staged at a time; a longer path goes head by head
 template <int D>
 constexpr size_t accept_smem(int group) {
@@ -533,6 +545,7 @@ __global__ void __launch_bounds__(2 * D, 2) tree_accept_kernel(const TreeArgs a,
   float *s_beta = smem + (size_t)group * AT * 3 * D;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cq = lane & 3, rg = lane >> 2, col = 16 * warp + 4 * cq;
+  after_previous();
   const int H = a.H;
   const uint32_t groups = (uint32_t)a.n_seqs * (uint32_t)H / group;  // at most 65535 x 21845
   const size_t C = (size_t)3 * H * D;
@@ -711,6 +724,17 @@ cudaError_t fitting(int threads, size_t smem, size_t smem_most, int64_t *ctas) {
   return cudaSuccess;
 }
 
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int64_t ctas, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early, cfg.numAttrs = 1, cfg.stream = s;
+  cfg.gridDim = dim3((unsigned)ctas), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 constexpr size_t SMEM_MOST = 220 * 1024;  // of a CTA, beside the kernels' static part
 template <int D, typename IO, typename ST>
 cudaError_t launch_typed(const TreeArgs &a, bool accept, cudaStream_t s) {
@@ -724,7 +748,7 @@ cudaError_t launch_typed(const TreeArgs &a, bool accept, cudaStream_t s) {
     // x 64 heads: 568 us one head at a time, 468 two, 505 four, whose paths differ too much in length)
     const int group = a.H % 2 == 0 && units / 2 >= 4 * fit ? 2 : 1;
     const int64_t groups = units / group;
-    kernel<<<(unsigned)(groups < fit ? groups : fit), 2 * D, accept_smem<D>(group), s>>>(a, group);
+    return launch(kernel, groups < fit ? groups : fit, 2 * D, accept_smem<D>(group), s, a, group);
   } else {
     constexpr bool staged = sizeof(IO) == 2;
     const size_t smem = verify_smem_floats(a.max_nodes, D, staged) * sizeof(float);
@@ -735,16 +759,14 @@ cudaError_t launch_typed(const TreeArgs &a, bool accept, cudaStream_t s) {
       cudaError_t e = fitting<kernel>(NT, smem + extra, SMEM_MOST, &fit);
       if (e != cudaSuccess) return e;
       if (units <= fit) {
-        kernel<<<(unsigned)units, NT, smem + extra, s>>>(a);
-        return cudaGetLastError();
+        return launch(kernel, units, NT, smem + extra, s, a);
       }
     }
     constexpr auto kernel = tree_verify_kernel<D, IO, ST, false>;
     cudaError_t e = fitting<kernel>(NT, smem, most, &fit);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(units < fit ? units : fit), NT, smem, s>>>(a);
+    return launch(kernel, units < fit ? units : fit, NT, smem, s, a);
   }
-  return cudaGetLastError();
 }
 
 template <int D>

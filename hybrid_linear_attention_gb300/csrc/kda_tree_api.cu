@@ -233,7 +233,7 @@ kda_status mla_pages_copy(void *pool, int n_layers, int n_pages, int page_size, 
   KDA_TRACE(TR_MLA_PAGES_COPY);
   kda_status st = check_cache(pool, n_layers, n_pages, page_size, false, nullptr, 0, nullptr);
   if (st != KDA_OK) return st;
-  if (n_copies < 0 || n_copies > 65535) return KDA_ERR_INVALID_ARG;
+  if (n_copies < 0 || n_copies > 8192) return KDA_ERR_INVALID_ARG;  // every entry is compared with every other
   if (n_copies == 0) return KDA_OK;
   if (!given(src) || !given(dst)) return KDA_ERR_INVALID_ARG;
   return done(kda::launch_pages_copy(cache_args(pool, n_layers, n_pages, page_size, nullptr, 0, nullptr), src, dst,

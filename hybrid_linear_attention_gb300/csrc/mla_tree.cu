@@ -25,8 +25,12 @@
 // by side.  One thread's products leave gaps (measured: with a wait and a commit every four of
 // them, 101 to 149 cycles a product instead of 64), two threads' fill each other's (64 cycles); one
 // thread's loads cost it about 450 cycles a slot, so two load.
-// That brings 272 KB to a CTA for 256 positions; TMA moves 41 bytes a cycle and SM from L2
-// (measured, 12 TB/s), the products need 64, so L2 is the bound, near 64 % of the tensor peak.
+// That brings 272 KB to a CTA for 256 positions; TMA moves about 41 bytes a cycle and SM from L2
+// (measured, 12 TB/s), the products at full rate would take 64, so L2 is the bound where the cache is
+// read by several row tiles: 4 sequences x 11 to 16 nodes x 65536 positions 281 us, 1.52 PFLOP/s, 78 %
+// of the measured bf16 peak.  With one node a sequence the same loop streams the cache: 256 sequences
+// of up to 4096 positions 207 us, 4.6 TB/s; there HBM's latency against the ring's depth bounds it
+// (asking L2 for coming tiles, by bulk prefetches or by threads, measured slower: 247 to 272 us).
 //
 // Work is dealt in tiles of 256 positions: clusters form groups of G that take G row tiles of a
 // sequence side by side (they read the same positions at the same time, so HBM sees them once),
@@ -234,6 +238,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
+  // launched while the kernel before runs out: nothing of global memory is read or written above
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
 
   // ---- the batch's tiles for groups of 1, 2, 4 and 8 clusters, and this cluster's run ----------
@@ -764,6 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   }
   if (lane == 0 && s_abort && a.err) atomicOr(a.err, ERR_MBAR_TIMEOUT);
   __syncwarp();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -777,7 +784,7 @@ constexpr int CNT = 256, CROWS = CNT / 32;
 __global__ void __launch_bounds__(CNT) tree_combine_kernel(const TreeAttnArgs a, const float *part, const float *part_ml,
                                                            const Merge *merge) {
   // launched while the attention kernel runs out: its results are there once this returns
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
   const Merge g = merge[blockIdx.x];
   const int row = CROWS * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= g.rows) return;
@@ -855,19 +862,19 @@ cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s
   float *part = reinterpret_cast<float *>(a.ws);
   float *part_ml = reinterpret_cast<float *>(reinterpret_cast<char *>(a.ws) + PART);
   Merge *merge = reinterpret_cast<Merge *>(reinterpret_cast<char *>(a.ws) + PART + PART_ML);
-  tree_attn_kernel<<<2 * clusters, NT, SMEM, s>>>(a, maps, part, part_ml, merge);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  ++*launches;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(clusters, 2 * RC / CROWS), cfg.blockDim = dim3(CNT), cfg.stream = s;
-  cudaLaunchAttribute early;  // its launch overlaps the attention kernel's end
+  cudaLaunchAttribute early;  // each launch overlaps the end of the kernel before
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early, cfg.numAttrs = 1;
+  cfg.attrs = &early, cfg.numAttrs = 1, cfg.stream = s;
+  cfg.gridDim = dim3(2 * clusters), cfg.blockDim = dim3(NT), cfg.dynamicSmemBytes = SMEM;
+  e = cudaLaunchKernelEx(&cfg, tree_attn_kernel, a, maps, part, part_ml, merge);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  cfg.gridDim = dim3(clusters, 2 * RC / CROWS), cfg.blockDim = dim3(CNT), cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, tree_combine_kernel, a, (const float *)part, (const float *)part_ml, (const Merge *)merge);
   ++*launches;
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return e;
 }
 
 }  // namespace kda
