@@ -103,6 +103,9 @@ kda_status kda_tree_verify(const kda_params *p, const void *x_raw, const void *c
                               const_cast<void *>(state), n_slots, slot_idx, cu_nodes, parent, n_seqs,
                               total_nodes);
   a.max_nodes = max_nodes;
+  // e^g below the normal fp32 range (2^-126) counts as 0: the kernel takes differences of sums of g along
+  // a path, which would be NaN of two infinities and drown a later node's g behind a huge one
+  if (a.g_min < -88.1f) a.g_min = -88.1f;
   a.gate = gate_logit, a.norm_w = norm_w, a.out = out;
   return done(kda::launch_tree(a, false, p->d_k, p->io_dtype == KDA_BF16, p->state_dtype == KDA_BF16, stream), 1);
 }

@@ -344,7 +344,8 @@ kda_status kda_state_accept(const kda_params* p, const void* step_states, int n_
  *   x_raw       [total_nodes, 3*H*d] io_dtype: raw q|k|v projections of the nodes; the
  *               convolution runs along each node's path, then into the tail.
  *   conv_w      [3*H*d, 4]; conv_state [n_slots, 3, 3*H*d] io_dtype (read only).
- *   g           [total_nodes, H, d] fp32 log-retention; beta [total_nodes, H] fp32.
+ *   g           [total_nodes, H, d] fp32 log-retention, clamped at p->g_min inside (and retentions
+ *               below 2^-126 count as 0); beta [total_nodes, H] fp32.
  *   state       [n_slots, H, d, d] state_dtype pool (read only); slot_idx [n_seqs] or NULL as in
  *               kda_decode_step (here two sequences may share a slot).
  *   cu_nodes    [n_seqs + 1] int32 (device): the nodes of sequence n are rows cu_nodes[n] ..

@@ -93,6 +93,21 @@ def test_verify_bf16_state_and_no_l2norm():
     assert out_error(verify(m, p), plain(m, p)[0]) <= tol(p)
 
 
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("chain", [True, False])
+def test_verify_retentions_of_zero(chain, io):
+    """Without a lower bound: a node that forgets its past, in some channels or in all.  One such node a
+    path: its sums stay under 2^8, whose half step 2^-17 enters at most 11 times, 6e-5 of a term."""
+    p = kda.params(H=2, g_min=-float("inf"), io_dtype=io)
+    m = make([11, 6], 2, 128, seed=305, chain=chain, io=io)
+    m["g"][2] = -float("inf")
+    m["g"][13] = torch.tensor([-0.1, -300.0, -1e6, -3e38, -88.0, -100.0, -0.5, -float("inf")]).repeat(16)
+    want = ref.kda_tree(m["x"], m["conv_w"], m["conv_state"], m["g"], m["beta"], m["state"], m["slots"], m["cu"],
+                        m["parent"], H=2, d=128, gate=m["gate"], norm_w=m["norm_w"], g_min=-float("inf"))[0]
+    assert out_error(verify(m, p, max_nodes=11), want) <= tol(p)
+    kda.kda_check_device_error()
+
+
 def test_verify_shared_slot():
     """Two drafts of one sequence: the pool state is only read."""
     p = kda.params(H=2)
