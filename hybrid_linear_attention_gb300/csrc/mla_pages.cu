@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(AC_NT)
     if (tid == 0) flag(c.err, ERR_BAD_SEQLEN);
     W = 0;
   }
-  const bool ok = last >= -1 && last < W && len >= 0;
+  const bool ok = last >= -1 && last < W && len >= 0 && len <= INT_MAX - 64;
   if (tid == 0 && !ok) flag(c.err, ERR_BAD_INDEX);
   const int nodes = ok ? last + 1 : 0;
   for (int i = tid; i < nodes; i += AC_NT) {

@@ -209,6 +209,27 @@ def test_rows_without_a_page_are_reported():
     assert status() == kda.KDA_ERR_BAD_INDEX and lengths.tolist() == [3, 4, -1]
 
 
+def test_accept_at_the_largest_length():
+    """A length whose sum with the path would pass 32 bits keeps its value and is reported."""
+    _gpu.lib()
+    pool = torch.zeros(1, 4, 16, 576, dtype=torch.bfloat16, device="cuda")
+    lengths = ref.i32([2**31 - 1, 3])
+    kda.mla_cache_accept(pool, ref.i32([[0], [1]]), lengths, ref.i32([0, 1, 2]), ref.i32([-1, -1]), ref.i32([0, 0]), lengths)
+    assert status() == kda.KDA_ERR_BAD_INDEX and lengths.tolist() == [2**31 - 1, 4]
+
+
+def test_reserve_more_entries_than_fit_on_chip():
+    """2500 entries: the notes are kept in the workspace; pages run out at the last ones."""
+    n = 2500
+    b = Both(n + 700, n, 2, 16, layers=1)
+    b.ws = torch.empty(kda.mla_pages_workspace_size(n), dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(31)
+    slots = [int(x) for x in rng.permutation(n)]
+    assert b.reserve(slots, [int(x) for x in rng.integers(0, 33, n)])
+    assert status() == kda.KDA_ERR_NO_PAGES
+    b.same()
+
+
 def test_a_verification_step_as_a_server_runs_it():
     """Two turns of: reserve, append the drafted rows, tree masks, latent attention and the KDA
     verify call, accept into both caches; a fork in between; everything against the plain forms."""
