@@ -518,6 +518,24 @@ def mla_decode(q_nope, q_rope, w_uk, w_uv, cache, lengths, gate_logit, q_cat, z,
 
 # ---- verifying a tree of drafted tokens -------------------------------------------------------
 
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _here(t, dtype, name):
+    """_ptr, of the current device's tensors only (the launch goes to its stream)."""
+    if (isinstance(t, _Tensor) and t.is_cuda and t.get_device() == _device() and t.is_contiguous()
+            and (dtype is None or t.dtype == dtype)):
+        return t.data_ptr()
+    p = _ptr(t, dtype, name)
+    if t is not None:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{_device()}")
+    return p
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
 def _shape(t, shape, name):
     if t is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
@@ -533,10 +551,10 @@ def _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, s
     _shape(beta, (total, H), "beta")
     _shape(state, (state.shape[0], H, d, d), "state")
     _shape(slot_idx, (n,), "slot_idx")
-    return [ctypes.byref(p), _ptr(x_raw, io, "x_raw"), _ptr(conv_w, io, "conv_w"),
-            _ptr(conv_state, io, "conv_state"), _ptr(g, f32, "g"), _ptr(beta, f32, "beta"),
-            _ptr(state, p.state_torch, "state"), state.shape[0], _ptr(slot_idx, i32, "slot_idx"),
-            _ptr(cu_nodes, i32, "cu_nodes"), _ptr(parent, i32, "parent"), n, total]
+    return [ctypes.byref(p), _here(x_raw, io, "x_raw"), _here(conv_w, io, "conv_w"),
+            _here(conv_state, io, "conv_state"), _here(g, f32, "g"), _here(beta, f32, "beta"),
+            _here(state, p.state_torch, "state"), state.shape[0], _here(slot_idx, i32, "slot_idx"),
+            _here(cu_nodes, i32, "cu_nodes"), _here(parent, i32, "parent"), n, total]
 
 
 def kda_tree_verify(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, out, *,
@@ -549,8 +567,8 @@ def kda_tree_verify(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, pare
     _shape(out, g.shape, "out")
     _shape(gate_logit, g.shape, "gate_logit")
     _shape(norm_w, (p.d_k,), "norm_w")
-    st = load().kda_tree_verify(*args, int(max_nodes), _ptr(gate_logit, io, "gate_logit"),
-                                _ptr(norm_w, torch.float32, "norm_w"), _ptr(out, io, "out"),
+    st = load().kda_tree_verify(*args, int(max_nodes), _here(gate_logit, io, "gate_logit"),
+                                _here(norm_w, torch.float32, "norm_w"), _here(out, io, "out"),
                                 _stream(stream))
     _check(st, "kda_tree_verify")
 
@@ -560,7 +578,7 @@ def kda_tree_accept(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, pare
     """The path to accept_node [n_seqs] (-1: none) replayed into the pool state and conv tail."""
     args = _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, slot_idx)
     _shape(accept_node, (cu_nodes.numel() - 1,), "accept_node")
-    st = load().kda_tree_accept(*args, _ptr(accept_node, torch.int32, "accept_node"),
+    st = load().kda_tree_accept(*args, _here(accept_node, torch.int32, "accept_node"),
                                 _stream(stream))
     _check(st, "kda_tree_accept")
 
@@ -568,9 +586,9 @@ def kda_tree_accept(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, pare
 def mla_tree_mask(parent, cu_nodes, mask, *, stream=None):
     """mask [nodes] int64: bit j = the node itself or its ancestor j, from parent [nodes]."""
     _shape(mask, parent.shape, "mask")
-    st = load().mla_tree_mask(_ptr(parent, torch.int32, "parent"),
-                              _ptr(cu_nodes, torch.int32, "cu_nodes"), cu_nodes.numel() - 1,
-                              parent.shape[0], _ptr(mask, torch.int64, "mask"), _stream(stream))
+    st = load().mla_tree_mask(_here(parent, torch.int32, "parent"),
+                              _here(cu_nodes, torch.int32, "cu_nodes"), cu_nodes.numel() - 1,
+                              parent.shape[0], _here(mask, torch.int64, "mask"), _stream(stream))
     _check(st, "mla_tree_mask")
 
 
@@ -585,9 +603,9 @@ def _paged(pool, page_table, lengths, n_seqs):
         raise ValueError("pool: expected [n_pages, page_size, 576]")
     if page_table.shape[0] < n_seqs or lengths.shape[0] < n_seqs:
         raise ValueError("page_table, lengths: fewer rows than sequences")
-    return [_ptr(pool, torch.bfloat16, "pool"), shape[0], shape[1],
-            _ptr(page_table, torch.int32, "page_table"), page_table.shape[1],
-            _ptr(lengths, torch.int32, "lengths")]
+    return [_here(pool, torch.bfloat16, "pool"), shape[0], shape[1],
+            _here(page_table, torch.int32, "page_table"), page_table.shape[1],
+            _here(lengths, torch.int32, "lengths")]
 
 
 def _paged_layers(pool, page_table, lengths, n_seqs):
@@ -597,9 +615,9 @@ def _paged_layers(pool, page_table, lengths, n_seqs):
         raise ValueError("pool: expected [n_layers, n_pages, page_size, 576]")
     if page_table.shape[0] < n_seqs or lengths.shape[0] < n_seqs:
         raise ValueError("page_table, lengths: fewer rows than sequences")
-    return [_ptr(pool, torch.bfloat16, "pool"), shape[0], shape[1], shape[2],
-            _ptr(page_table, torch.int32, "page_table"), page_table.shape[1],
-            _ptr(lengths, torch.int32, "lengths")]
+    return [_here(pool, torch.bfloat16, "pool"), shape[0], shape[1], shape[2],
+            _here(page_table, torch.int32, "page_table"), page_table.shape[1],
+            _here(lengths, torch.int32, "lengths")]
 
 
 _DTYPE = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
@@ -618,9 +636,9 @@ def mla_tree_latent(q_cat, pool, page_table, lengths, cu_nodes, z, *, mask=None,
         raise TypeError(f"z: expected float32 or bfloat16, got {z.dtype}")
     cache = _paged(pool, page_table, lengths, n)
     st = load().mla_tree_latent(
-        _ptr(q_cat, torch.bfloat16, "q_cat"), H, *cache,
-        _ptr(cu_nodes, torch.int32, "cu_nodes"), n, total, _ptr(mask, torch.int64, "mask"),
-        float(scale), _ptr(z, None, "z"), _DTYPE[z.dtype], *_ws(workspace), _stream(stream))
+        _here(q_cat, torch.bfloat16, "q_cat"), H, *cache,
+        _here(cu_nodes, torch.int32, "cu_nodes"), n, total, _here(mask, torch.int64, "mask"),
+        float(scale), _here(z, None, "z"), _DTYPE[z.dtype], _here(workspace, None, "workspace"), _bytes(workspace), _stream(stream))
     _check(st, "mla_tree_latent")
 
 
@@ -638,11 +656,11 @@ def mla_tree_decode(q_nope, q_rope, w_uk, w_uv, pool, page_table, lengths, cu_no
     _shape(w_uv, (64, 128, 512), "w_uv")
     _shape(mask, (total,), "mask")
     st = load().mla_tree_decode(
-        _ptr(q_nope, bf, "q_nope"), _ptr(q_rope, bf, "q_rope"), _ptr(w_uk, bf, "w_uk"),
-        _ptr(w_uv, bf, "w_uv"), *_paged(pool, page_table, lengths, n),
-        _ptr(cu_nodes, torch.int32, "cu_nodes"), n, total, _ptr(mask, torch.int64, "mask"),
-        _ptr(gate_logit, bf, "gate_logit"), float(scale), _ptr(q_cat, bf, "q_cat"),
-        _ptr(z, torch.float32, "z"), _ptr(out, bf, "out"), *_ws(workspace), _stream(stream))
+        _here(q_nope, bf, "q_nope"), _here(q_rope, bf, "q_rope"), _here(w_uk, bf, "w_uk"),
+        _here(w_uv, bf, "w_uv"), *_paged(pool, page_table, lengths, n),
+        _here(cu_nodes, torch.int32, "cu_nodes"), n, total, _here(mask, torch.int64, "mask"),
+        _here(gate_logit, bf, "gate_logit"), float(scale), _here(q_cat, bf, "q_cat"),
+        _here(z, torch.float32, "z"), _here(out, bf, "out"), _here(workspace, None, "workspace"), _bytes(workspace), _stream(stream))
     _check(st, "mla_tree_decode")
 
 
@@ -652,8 +670,8 @@ def mla_cache_append(pool, page_table, lengths, cu_rows, rows, *, stream=None):
     n = cu_rows.numel() - 1
     _shape(rows, (pool.shape[0], rows.shape[1], 576), "rows")
     st = load().mla_cache_append(
-        *_paged_layers(pool, page_table, lengths, n), _ptr(cu_rows, torch.int32, "cu_rows"), n,
-        rows.shape[1], _ptr(rows, torch.bfloat16, "rows"), _stream(stream))
+        *_paged_layers(pool, page_table, lengths, n), _here(cu_rows, torch.int32, "cu_rows"), n,
+        rows.shape[1], _here(rows, torch.bfloat16, "rows"), _stream(stream))
     _check(st, "mla_cache_append")
 
 
@@ -665,9 +683,9 @@ def mla_cache_accept(pool, page_table, lengths, cu_nodes, parent, accept_node, n
     if new_lengths.shape[0] < n:
         raise ValueError("new_lengths: fewer rows than sequences")
     st = load().mla_cache_accept(
-        *_paged_layers(pool, page_table, lengths, n), _ptr(cu_nodes, i32, "cu_nodes"), n,
-        parent.shape[0], _ptr(parent, i32, "parent"), _ptr(accept_node, i32, "accept_node"),
-        _ptr(new_lengths, i32, "new_lengths"), _stream(stream))
+        *_paged_layers(pool, page_table, lengths, n), _here(cu_nodes, i32, "cu_nodes"), n,
+        parent.shape[0], _here(parent, i32, "parent"), _here(accept_node, i32, "accept_node"),
+        _here(new_lengths, i32, "new_lengths"), _stream(stream))
     _check(st, "mla_cache_accept")
 
 
@@ -675,8 +693,8 @@ def mla_pages_copy(pool, src, dst, *, stream=None):
     """Pages src[i] copied to dst[i] in every layer of pool [n_layers, n_pages, page_size, 576]."""
     _shape(pool, (pool.shape[0], pool.shape[1], pool.shape[2], 576), "pool")
     _shape(dst, src.shape, "dst")
-    st = load().mla_pages_copy(_ptr(pool, torch.bfloat16, "pool"), *pool.shape[:3],
-                               _ptr(src, torch.int32, "src"), _ptr(dst, torch.int32, "dst"),
+    st = load().mla_pages_copy(_here(pool, torch.bfloat16, "pool"), *pool.shape[:3],
+                               _here(src, torch.int32, "src"), _here(dst, torch.int32, "dst"),
                                src.numel(), _stream(stream))
     _check(st, "mla_pages_copy")
 
@@ -689,15 +707,15 @@ def _book(refcount, page_table, held, lengths):
     i32 = torch.int32
     _shape(held, (page_table.shape[0],), "held")
     _shape(lengths, (page_table.shape[0],), "lengths")
-    return [_ptr(refcount, i32, "refcount"), _ptr(page_table, i32, "page_table"),
-            page_table.shape[1], _ptr(held, i32, "held"), _ptr(lengths, i32, "lengths"),
+    return [_here(refcount, i32, "refcount"), _here(page_table, i32, "page_table"),
+            page_table.shape[1], _here(held, i32, "held"), _here(lengths, i32, "lengths"),
             page_table.shape[0]]
 
 
 def mla_pages_free(refcount, page_table, held, lengths, slots, *, stream=None):
     """All pages of the sequences in slots released."""
     st = load().mla_pages_free(refcount.numel(), *_book(refcount, page_table, held, lengths),
-                               _ptr(slots, torch.int32, "slots"), slots.numel(), _stream(stream))
+                               _here(slots, torch.int32, "slots"), slots.numel(), _stream(stream))
     _check(st, "mla_pages_free")
 
 
@@ -708,9 +726,9 @@ def mla_pages_fork(pool, refcount, page_table, held, lengths, src, dst, *, works
     _shape(pool, (pool.shape[0], refcount.numel(), pool.shape[2], 576), "pool")
     _shape(dst, src.shape, "dst")
     st = load().mla_pages_fork(
-        _ptr(pool, torch.bfloat16, "pool"), *pool.shape[:3],
-        *_book(refcount, page_table, held, lengths), _ptr(src, i32, "src"), _ptr(dst, i32, "dst"),
-        src.numel(), *_ws(workspace), _stream(stream))
+        _here(pool, torch.bfloat16, "pool"), *pool.shape[:3],
+        *_book(refcount, page_table, held, lengths), _here(src, i32, "src"), _here(dst, i32, "dst"),
+        src.numel(), _here(workspace, None, "workspace"), _bytes(workspace), _stream(stream))
     _check(st, "mla_pages_fork")
 
 
@@ -721,6 +739,6 @@ def mla_pages_reserve(page_size, refcount, page_table, held, lengths, slots, ext
     _shape(extra, slots.shape, "extra")
     st = load().mla_pages_reserve(
         refcount.numel(), int(page_size), *_book(refcount, page_table, held, lengths),
-        _ptr(slots, i32, "slots"), _ptr(extra, i32, "extra"), slots.numel(), *_ws(workspace),
+        _here(slots, i32, "slots"), _here(extra, i32, "extra"), slots.numel(), _here(workspace, None, "workspace"), _bytes(workspace),
         _stream(stream))
     _check(st, "mla_pages_reserve")

@@ -112,8 +112,10 @@ kda_status mla_decode(const void* q_nope, const void* q_rope, const void* w_uk,
  * held        [n_slots] int32: pages that a sequence's table row holds.
  * Sequences that share a prefix share its full pages; a write never goes to a shared page as long
  * as the pages come from mla_pages_reserve and mla_pages_fork.  Free pages are taken in ascending
- * order, so the same calls always give the same tables.  No counterpart interface is printed on
- * the pages.
+ * order, so the same calls always give the same tables.  A sequence that is cut back into a page it
+ * shares must not be appended to (fork it first: the child's last page is a copy).  Calls that write
+ * the same tables run one after another (one stream, or events between them), each with a workspace
+ * that no other call in flight uses.  No counterpart interface is printed on the pages.
  */
 
 /*
@@ -249,7 +251,8 @@ kda_status mla_tree_latent(const void* q_cat, int H, const void* pool, int n_pag
  * mla_tree_latent with fp32 z, value up-projection and gate, one query row per node.
  *   q_nope [total_nodes, 64, 128], q_rope [total_nodes, 64, 64], gate_logit [total_nodes, 64],
  *   q_cat [total_nodes, 64, 576], z [total_nodes, 64, 512] fp32 and out [total_nodes, 64, 128]
- *   as mla_decode's with total_nodes for n_seqs; the rest as mla_tree_latent with H = 64.
+ *   as mla_decode's with total_nodes for n_seqs; the rest as mla_tree_latent with H = 64.  Rows of
+ *   no sequence keep their z, and their out is computed from it.
  */
 kda_status mla_tree_decode(const void* q_nope, const void* q_rope, const void* w_uk,
                            const void* w_uv, const void* pool, int n_pages, int page_size,

@@ -230,6 +230,15 @@ def test_reserve_more_entries_than_fit_on_chip():
     b.same()
 
 
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    b = Both(4, 2, 2, 16)
+    monkeypatch.setattr(kda, "_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        b.reserve([0], [3])
+    monkeypatch.undo()
+    b.same()
+
+
 def test_a_verification_step_as_a_server_runs_it():
     """Two turns of: reserve, append the drafted rows, tree masks, latent attention and the KDA
     verify call, accept into both caches; a fork in between; everything against the plain forms."""

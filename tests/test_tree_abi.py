@@ -117,6 +117,11 @@ def test_pages(lib):
     assert go(page=3) == UNSUPPORTED
 
 
+def test_page_copies_are_limited(lib):
+    go = lambda n: lib.mla_pages_copy(16, 9, 4, 64, 16, 16, n, None)  # noqa: E731
+    assert go(8193) == BAD and go(2**31 - 1) == BAD and go(0) == OK
+
+
 def test_the_binding_checks_shapes(lib):
     p = kda.params(H=2)
     t = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype)  # noqa: E731
