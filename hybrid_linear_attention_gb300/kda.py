@@ -518,22 +518,37 @@ def mla_decode(q_nope, q_rope, w_uk, w_uv, cache, lengths, gate_logit, q_cat, z,
 
 # ---- verifying a tree of drafted tokens -------------------------------------------------------
 
-_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _here(t, dtype, name):
-    """_ptr, of the current device's tensors only (the launch goes to its stream)."""
-    if (isinstance(t, _Tensor) and t.is_cuda and t.get_device() == _device() and t.is_contiguous()
-            and (dtype is None or t.dtype == dtype)):
-        return t.data_ptr()
+def _device():
+    try:
+        return _get_device()
+    except RuntimeError:  # no device: no tensor is on it
+        return -2
+
+
+def _here(t, dtype, name, dev):
+    """_ptr, of tensors on device `dev`, the current one, only: the launch goes to its stream."""
+    if t is None:
+        return None
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     p = _ptr(t, dtype, name)
-    if t is not None:
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{_device()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
     return p
 
 
-def _bytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+def _here_stream(stream, dev):
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+
+
+def _here_ws(t, dev):
+    return (None, 0) if t is None else (_here(t, t.dtype, "workspace", dev), t.nbytes)
 
 
 def _shape(t, shape, name):
@@ -541,7 +556,8 @@ def _shape(t, shape, name):
         raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
 
 
-def _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, slot_idx):
+def _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, slot_idx,
+               dev):
     io, i32, f32 = p.io_torch, torch.int32, torch.float32
     total, H, d, n = parent.shape[0], p.H, p.d_k, cu_nodes.numel() - 1
     _shape(x_raw, (total, 3 * H * d), "x_raw")
@@ -551,10 +567,11 @@ def _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, s
     _shape(beta, (total, H), "beta")
     _shape(state, (state.shape[0], H, d, d), "state")
     _shape(slot_idx, (n,), "slot_idx")
-    return [ctypes.byref(p), _here(x_raw, io, "x_raw"), _here(conv_w, io, "conv_w"),
-            _here(conv_state, io, "conv_state"), _here(g, f32, "g"), _here(beta, f32, "beta"),
-            _here(state, p.state_torch, "state"), state.shape[0], _here(slot_idx, i32, "slot_idx"),
-            _here(cu_nodes, i32, "cu_nodes"), _here(parent, i32, "parent"), n, total]
+    return [ctypes.byref(p), _here(x_raw, io, "x_raw", dev), _here(conv_w, io, "conv_w", dev),
+            _here(conv_state, io, "conv_state", dev), _here(g, f32, "g", dev),
+            _here(beta, f32, "beta", dev), _here(state, p.state_torch, "state", dev),
+            state.shape[0], _here(slot_idx, i32, "slot_idx", dev),
+            _here(cu_nodes, i32, "cu_nodes", dev), _here(parent, i32, "parent", dev), n, total]
 
 
 def kda_tree_verify(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, out, *,
@@ -562,33 +579,39 @@ def kda_tree_verify(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, pare
     """Outputs of every node of the drafted trees: x_raw [nodes, 3*H*d], g [nodes, H, d], beta
     [nodes, H], parent [nodes] and out [nodes, H, d] packed by cu_nodes [n_seqs + 1]; the pool
     state and the conv tails are only read."""
+    dev = _device()
     io = p.io_torch
-    args = _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, slot_idx)
+    args = _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, slot_idx,
+                      dev)
     _shape(out, g.shape, "out")
     _shape(gate_logit, g.shape, "gate_logit")
     _shape(norm_w, (p.d_k,), "norm_w")
-    st = load().kda_tree_verify(*args, int(max_nodes), _here(gate_logit, io, "gate_logit"),
-                                _here(norm_w, torch.float32, "norm_w"), _here(out, io, "out"),
-                                _stream(stream))
+    st = load().kda_tree_verify(*args, int(max_nodes), _here(gate_logit, io, "gate_logit", dev),
+                                _here(norm_w, torch.float32, "norm_w", dev),
+                                _here(out, io, "out", dev), _here_stream(stream, dev))
     _check(st, "kda_tree_verify")
 
 
 def kda_tree_accept(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, accept_node, *,
                     slot_idx=None, stream=None):
     """The path to accept_node [n_seqs] (-1: none) replayed into the pool state and conv tail."""
-    args = _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, slot_idx)
+    dev = _device()
+    args = _tree_args(p, x_raw, conv_w, conv_state, g, beta, state, cu_nodes, parent, slot_idx,
+                      dev)
     _shape(accept_node, (cu_nodes.numel() - 1,), "accept_node")
-    st = load().kda_tree_accept(*args, _here(accept_node, torch.int32, "accept_node"),
-                                _stream(stream))
+    st = load().kda_tree_accept(*args, _here(accept_node, torch.int32, "accept_node", dev),
+                                _here_stream(stream, dev))
     _check(st, "kda_tree_accept")
 
 
 def mla_tree_mask(parent, cu_nodes, mask, *, stream=None):
     """mask [nodes] int64: bit j = the node itself or its ancestor j, from parent [nodes]."""
+    dev = _device()
     _shape(mask, parent.shape, "mask")
-    st = load().mla_tree_mask(_here(parent, torch.int32, "parent"),
-                              _here(cu_nodes, torch.int32, "cu_nodes"), cu_nodes.numel() - 1,
-                              parent.shape[0], _here(mask, torch.int64, "mask"), _stream(stream))
+    st = load().mla_tree_mask(_here(parent, torch.int32, "parent", dev),
+                              _here(cu_nodes, torch.int32, "cu_nodes", dev), cu_nodes.numel() - 1,
+                              parent.shape[0], _here(mask, torch.int64, "mask", dev),
+                              _here_stream(stream, dev))
     _check(st, "mla_tree_mask")
 
 
@@ -596,28 +619,28 @@ def mla_tree_workspace_size(n_seqs, total_nodes, H=64):
     return int(load().mla_tree_workspace_size(int(n_seqs), int(total_nodes), int(H)))
 
 
-def _paged(pool, page_table, lengths, n_seqs):
+def _paged(pool, page_table, lengths, n_seqs, dev):
     """pool .. lengths of one layer ([n_pages, page_size, 576])."""
     shape = pool.shape
     if len(shape) != 3 or shape[2] != 576:
         raise ValueError("pool: expected [n_pages, page_size, 576]")
     if page_table.shape[0] < n_seqs or lengths.shape[0] < n_seqs:
         raise ValueError("page_table, lengths: fewer rows than sequences")
-    return [_here(pool, torch.bfloat16, "pool"), shape[0], shape[1],
-            _here(page_table, torch.int32, "page_table"), page_table.shape[1],
-            _here(lengths, torch.int32, "lengths")]
+    return [_here(pool, torch.bfloat16, "pool", dev), shape[0], shape[1],
+            _here(page_table, torch.int32, "page_table", dev), page_table.shape[1],
+            _here(lengths, torch.int32, "lengths", dev)]
 
 
-def _paged_layers(pool, page_table, lengths, n_seqs):
+def _paged_layers(pool, page_table, lengths, n_seqs, dev):
     """pool .. lengths of all layers ([n_layers, n_pages, page_size, 576])."""
     shape = pool.shape
     if len(shape) != 4 or shape[3] != 576:
         raise ValueError("pool: expected [n_layers, n_pages, page_size, 576]")
     if page_table.shape[0] < n_seqs or lengths.shape[0] < n_seqs:
         raise ValueError("page_table, lengths: fewer rows than sequences")
-    return [_here(pool, torch.bfloat16, "pool"), shape[0], shape[1], shape[2],
-            _here(page_table, torch.int32, "page_table"), page_table.shape[1],
-            _here(lengths, torch.int32, "lengths")]
+    return [_here(pool, torch.bfloat16, "pool", dev), shape[0], shape[1], shape[2],
+            _here(page_table, torch.int32, "page_table", dev), page_table.shape[1],
+            _here(lengths, torch.int32, "lengths", dev)]
 
 
 _DTYPE = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
@@ -628,17 +651,19 @@ def mla_tree_latent(q_cat, pool, page_table, lengths, cu_nodes, z, *, mask=None,
     """q_cat [nodes, H, 576] bf16, pool [n_pages, page_size, 576] bf16, page_table [n_seqs,
     max_pages], lengths [n_seqs], cu_nodes [n_seqs + 1], z [nodes, H, 512] fp32 or bf16, mask
     [nodes] int64 (None: a chain), workspace of mla_tree_workspace_size bytes."""
+    dev = _device()
     total, H, n = q_cat.shape[0], q_cat.shape[1], cu_nodes.numel() - 1
     _shape(q_cat, (total, H, 576), "q_cat")
     _shape(z, (total, H, 512), "z")
     _shape(mask, (total,), "mask")
     if z.dtype not in _DTYPE:
         raise TypeError(f"z: expected float32 or bfloat16, got {z.dtype}")
-    cache = _paged(pool, page_table, lengths, n)
+    cache = _paged(pool, page_table, lengths, n, dev)
     st = load().mla_tree_latent(
-        _here(q_cat, torch.bfloat16, "q_cat"), H, *cache,
-        _here(cu_nodes, torch.int32, "cu_nodes"), n, total, _here(mask, torch.int64, "mask"),
-        float(scale), _here(z, None, "z"), _DTYPE[z.dtype], _here(workspace, None, "workspace"), _bytes(workspace), _stream(stream))
+        _here(q_cat, torch.bfloat16, "q_cat", dev), H, *cache,
+        _here(cu_nodes, torch.int32, "cu_nodes", dev), n, total,
+        _here(mask, torch.int64, "mask", dev), float(scale), _here(z, z.dtype, "z", dev),
+        _DTYPE[z.dtype], *_here_ws(workspace, dev), _here_stream(stream, dev))
     _check(st, "mla_tree_latent")
 
 
@@ -646,6 +671,7 @@ def mla_tree_decode(q_nope, q_rope, w_uk, w_uv, pool, page_table, lengths, cu_no
                     q_cat, z, out, *, mask=None, scale=MLA_SCALE, workspace=None, stream=None):
     """One absorbed gated-MLA step for the nodes of drafted trees; q_cat and z are caller-owned
     intermediates."""
+    dev = _device()
     bf = torch.bfloat16
     total, n = q_nope.shape[0], cu_nodes.numel() - 1
     for t, tail, name in ((q_nope, (64, 128), "q_nope"), (q_rope, (64, 64), "q_rope"),
@@ -656,46 +682,52 @@ def mla_tree_decode(q_nope, q_rope, w_uk, w_uv, pool, page_table, lengths, cu_no
     _shape(w_uv, (64, 128, 512), "w_uv")
     _shape(mask, (total,), "mask")
     st = load().mla_tree_decode(
-        _here(q_nope, bf, "q_nope"), _here(q_rope, bf, "q_rope"), _here(w_uk, bf, "w_uk"),
-        _here(w_uv, bf, "w_uv"), *_paged(pool, page_table, lengths, n),
-        _here(cu_nodes, torch.int32, "cu_nodes"), n, total, _here(mask, torch.int64, "mask"),
-        _here(gate_logit, bf, "gate_logit"), float(scale), _here(q_cat, bf, "q_cat"),
-        _here(z, torch.float32, "z"), _here(out, bf, "out"), _here(workspace, None, "workspace"), _bytes(workspace), _stream(stream))
+        _here(q_nope, bf, "q_nope", dev), _here(q_rope, bf, "q_rope", dev),
+        _here(w_uk, bf, "w_uk", dev), _here(w_uv, bf, "w_uv", dev),
+        *_paged(pool, page_table, lengths, n, dev), _here(cu_nodes, torch.int32, "cu_nodes", dev),
+        n, total, _here(mask, torch.int64, "mask", dev), _here(gate_logit, bf, "gate_logit", dev),
+        float(scale), _here(q_cat, bf, "q_cat", dev), _here(z, torch.float32, "z", dev),
+        _here(out, bf, "out", dev), *_here_ws(workspace, dev), _here_stream(stream, dev))
     _check(st, "mla_tree_decode")
 
 
 def mla_cache_append(pool, page_table, lengths, cu_rows, rows, *, stream=None):
     """rows [n_layers, total, 576] written behind each sequence in pool [n_layers, n_pages,
     page_size, 576]; lengths stay."""
+    dev = _device()
     n = cu_rows.numel() - 1
     _shape(rows, (pool.shape[0], rows.shape[1], 576), "rows")
     st = load().mla_cache_append(
-        *_paged_layers(pool, page_table, lengths, n), _here(cu_rows, torch.int32, "cu_rows"), n,
-        rows.shape[1], _here(rows, torch.bfloat16, "rows"), _stream(stream))
+        *_paged_layers(pool, page_table, lengths, n, dev),
+        _here(cu_rows, torch.int32, "cu_rows", dev), n, rows.shape[1],
+        _here(rows, torch.bfloat16, "rows", dev), _here_stream(stream, dev))
     _check(st, "mla_cache_append")
 
 
 def mla_cache_accept(pool, page_table, lengths, cu_nodes, parent, accept_node, new_lengths, *,
                      stream=None):
     """The accepted paths' rows compacted; new_lengths [n_seqs] may be lengths."""
+    dev = _device()
     n, i32 = cu_nodes.numel() - 1, torch.int32
     _shape(accept_node, (n,), "accept_node")
     if new_lengths.shape[0] < n:
         raise ValueError("new_lengths: fewer rows than sequences")
     st = load().mla_cache_accept(
-        *_paged_layers(pool, page_table, lengths, n), _here(cu_nodes, i32, "cu_nodes"), n,
-        parent.shape[0], _here(parent, i32, "parent"), _here(accept_node, i32, "accept_node"),
-        _here(new_lengths, i32, "new_lengths"), _stream(stream))
+        *_paged_layers(pool, page_table, lengths, n, dev), _here(cu_nodes, i32, "cu_nodes", dev),
+        n, parent.shape[0], _here(parent, i32, "parent", dev),
+        _here(accept_node, i32, "accept_node", dev),
+        _here(new_lengths, i32, "new_lengths", dev), _here_stream(stream, dev))
     _check(st, "mla_cache_accept")
 
 
 def mla_pages_copy(pool, src, dst, *, stream=None):
     """Pages src[i] copied to dst[i] in every layer of pool [n_layers, n_pages, page_size, 576]."""
+    dev = _device()
     _shape(pool, (pool.shape[0], pool.shape[1], pool.shape[2], 576), "pool")
     _shape(dst, src.shape, "dst")
-    st = load().mla_pages_copy(_here(pool, torch.bfloat16, "pool"), *pool.shape[:3],
-                               _here(src, torch.int32, "src"), _here(dst, torch.int32, "dst"),
-                               src.numel(), _stream(stream))
+    st = load().mla_pages_copy(_here(pool, torch.bfloat16, "pool", dev), *pool.shape[:3],
+                               _here(src, torch.int32, "src", dev),
+                               _here(dst, torch.int32, "dst", dev), src.numel(), _here_stream(stream, dev))
     _check(st, "mla_pages_copy")
 
 
@@ -703,42 +735,47 @@ def mla_pages_workspace_size(n):
     return int(load().mla_pages_workspace_size(int(n)))
 
 
-def _book(refcount, page_table, held, lengths):
+def _book(refcount, page_table, held, lengths, dev):
     i32 = torch.int32
     _shape(held, (page_table.shape[0],), "held")
     _shape(lengths, (page_table.shape[0],), "lengths")
-    return [_here(refcount, i32, "refcount"), _here(page_table, i32, "page_table"),
-            page_table.shape[1], _here(held, i32, "held"), _here(lengths, i32, "lengths"),
+    return [_here(refcount, i32, "refcount", dev), _here(page_table, i32, "page_table", dev),
+            page_table.shape[1], _here(held, i32, "held", dev), _here(lengths, i32, "lengths", dev),
             page_table.shape[0]]
 
 
 def mla_pages_free(refcount, page_table, held, lengths, slots, *, stream=None):
     """All pages of the sequences in slots released."""
-    st = load().mla_pages_free(refcount.numel(), *_book(refcount, page_table, held, lengths),
-                               _here(slots, torch.int32, "slots"), slots.numel(), _stream(stream))
+    dev = _device()
+    st = load().mla_pages_free(refcount.numel(), *_book(refcount, page_table, held, lengths, dev),
+                               _here(slots, torch.int32, "slots", dev), slots.numel(),
+                               _here_stream(stream, dev))
     _check(st, "mla_pages_free")
 
 
 def mla_pages_fork(pool, refcount, page_table, held, lengths, src, dst, *, workspace=None,
                    stream=None):
     """Sequences dst become copies of src: full pages shared, a partly filled last one copied."""
+    dev = _device()
     i32 = torch.int32
     _shape(pool, (pool.shape[0], refcount.numel(), pool.shape[2], 576), "pool")
     _shape(dst, src.shape, "dst")
     st = load().mla_pages_fork(
-        _here(pool, torch.bfloat16, "pool"), *pool.shape[:3],
-        *_book(refcount, page_table, held, lengths), _here(src, i32, "src"), _here(dst, i32, "dst"),
-        src.numel(), _here(workspace, None, "workspace"), _bytes(workspace), _stream(stream))
+        _here(pool, torch.bfloat16, "pool", dev), *pool.shape[:3],
+        *_book(refcount, page_table, held, lengths, dev), _here(src, i32, "src", dev),
+        _here(dst, i32, "dst", dev), src.numel(), *_here_ws(workspace, dev),
+        _here_stream(stream, dev))
     _check(st, "mla_pages_fork")
 
 
 def mla_pages_reserve(page_size, refcount, page_table, held, lengths, slots, extra, *,
                       workspace=None, stream=None):
     """The pages that sequences `slots` lack for lengths + extra positions."""
+    dev = _device()
     i32 = torch.int32
     _shape(extra, slots.shape, "extra")
     st = load().mla_pages_reserve(
-        refcount.numel(), int(page_size), *_book(refcount, page_table, held, lengths),
-        _here(slots, i32, "slots"), _here(extra, i32, "extra"), slots.numel(), _here(workspace, None, "workspace"), _bytes(workspace),
-        _stream(stream))
+        refcount.numel(), int(page_size), *_book(refcount, page_table, held, lengths, dev),
+        _here(slots, i32, "slots", dev), _here(extra, i32, "extra", dev), slots.numel(),
+        *_here_ws(workspace, dev), _here_stream(stream, dev))
     _check(st, "mla_pages_reserve")
