@@ -85,7 +85,7 @@ enum {
 };
 
 struct TreeMaps {
-  CUtensorMap q, c;
+  CUtensorMap q, c, z, part;
 };
 // What the clusters leave for the combine kernel: partial sums [2 x clusters][128][512], their
 // (reference, normaliser) [..][128][2], and for every cluster the rows it completes.
@@ -141,6 +141,10 @@ __device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ void arrive_pair(uint32_t cluster_bar, uint32_t n = 1) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// the stores before the last one have read their shared memory
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
@@ -208,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_abort;
   __shared__ unsigned long long s_cost[4];
-  __shared__ int64_t s_scan[NT / 32];
+  __shared__ uint32_t s_scan[NT / 32];
   __shared__ int s_n, s_off, s_page[2][16];
   __shared__ float s_max[2][4][RC], s_sum[4][RC];
   const uint32_t raw = smem_u32(dyn);
@@ -219,42 +223,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   const uint32_t rank = cluster_rank();
   const int cid = blockIdx.x >> 1, clusters = gridDim.x >> 1;
   auto bar = [&](int i) { return smem_u32(&s_bar[i]); };
-  if (tid == 0) {
-    for (int i = 0; i < B_N; ++i) {
-      int n = 1;
-      if (i < B_EMPTY_S || i == B_QFULL) n = 2;                                        // a loader of each CTA
-      if (i == B_SFREE || i == B_SFREE + 1 || i == B_SCALED || i == B_ZFREE) n = 16;  // the softmax warps
-      if (i >= B_PFULL && i < B_PFREE) n = 4;                                         // two of each CTA
-      mbar_init(bar(i), n);
-    }
+  if (tid < B_N) {
+    const int i = tid;
+    int n = 1;
+    if (i < B_EMPTY_S || i == B_QFULL) n = 2;                                        // a loader of each CTA
+    if (i == B_SFREE || i == B_SFREE + 1 || i == B_SCALED || i == B_ZFREE) n = 16;  // the softmax warps
+    if (i >= B_PFULL && i < B_PFREE) n = 4;                                         // two of each CTA
+    mbar_init(bar(i), n);
     mbar_fence_init();
-    s_abort = 0;
-    s_n = 0;
-    s_off = 0;
   }
-  if (tid < 4) s_cost[tid] = 0;
-  if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(tid ? &maps.c : &maps.q) : "memory");
-  if (warp == 0) {
+  if (tid == 64) s_abort = 0, s_n = 0, s_off = 0;
+  if (tid >= 96 && tid < 100) s_cost[tid - 96] = 0;
+  if (tid >= 128 && tid < 132)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.q + (tid - 128)) : "memory");
+  if (warp == W_SCORE) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   // launched while the kernel before runs out: nothing of global memory is read or written above
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  Seq mine = {};
+  if (tid < a.n_seqs) mine = seq_of(a, tid, blockIdx.x == 0);
+  tc_fence_before();
   __syncthreads();
+  cluster_arrive();  // barriers and tensor memory are there in this CTA; waited for below
 
   // ---- the batch's tiles for groups of 1, 2, 4 and 8 clusters, and this cluster's run ----------
-  {
-    unsigned long long c[4] = {0, 0, 0, 0};
-    for (int n = tid; n < a.n_seqs; n += NT) {
-      const Seq s = seq_of(a, n, blockIdx.x == 0);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) c[g] += (unsigned long long)((s.row_tiles + (1 << g) - 1) >> g) * s.tiles;
+  for (int n0 = 0; n0 < a.n_seqs; n0 += NT) {
+    Seq s = mine;
+    if (n0 > 0) {
+      s.row_tiles = s.tiles = 0;
+      if (n0 + tid < a.n_seqs) s = seq_of(a, n0 + tid, blockIdx.x == 0);
     }
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) c[g] += __shfl_xor_sync(0xffffffffu, c[g], o);
-      if (lane == 0 && c[g]) atomicAdd(&s_cost[g], c[g]);
+    for (int g = 0; g < 4; ++g) {  // at most 64 x 2^20 tiles each: a warp's sum fits 32 bits
+      const uint32_t c = __reduce_add_sync(0xffffffffu, (uint32_t)((s.row_tiles + (1 << g) - 1) >> g) * (uint32_t)s.tiles);
+      if (lane == 0 && c) atomicAdd(&s_cost[g], (unsigned long long)c);
     }
   }
   __syncthreads();
@@ -274,21 +278,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   }
   const int64_t tiles = (int64_t)s_cost[31 - __clz(group)];
   if (tiles < workers) workers = (int)tiles;  // so every worker has a run
-  const int worker = cid / group, member = cid % group;
+  const int worker = cid >> (31 - __clz(group)), member = cid & (group - 1);
   const int64_t begin = worker < workers ? run_start(tiles, worker, workers) : 0;
   const int64_t stop = worker < workers ? run_start(tiles, worker + 1, workers) : 0;
   if (stop > begin) {  // the sequence that tile `begin` falls in
     int64_t before = 0;
     for (int n0 = 0; n0 < a.n_seqs && before <= begin; n0 += NT) {
-      int64_t cost = 0;
+      uint32_t cost = 0;
       if (n0 + tid < a.n_seqs) {
-        const Seq s = seq_of(a, n0 + tid, false);
-        cost = (int64_t)((s.row_tiles + group - 1) / group) * s.tiles;
+        const Seq s = n0 == 0 ? mine : seq_of(a, n0 + tid, false);
+        cost = (uint32_t)((s.row_tiles + group - 1) >> (31 - __clz(group))) * (uint32_t)s.tiles;
       }
-      int64_t x = cost;
+      uint32_t x = cost;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
       if (lane == 31) s_scan[warp] = x;
@@ -301,9 +305,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       __syncthreads();
     }
   }
-  tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  cluster_wait();
   tc_fence_after();
   const uint32_t tm = s_tmem;
   Walk walk;
@@ -687,56 +690,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         const float l = (s_sum[0][row] + s_sum[1][row]) + (s_sum[2][row] + s_sum[3][row]);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         tc_fence_after();
-        // the warp's [32 rows][128 latents], 128 bytes of each row at a time: through shared memory
-        // (the weights' place, free now), so that eight lanes write a row's 128 bytes together
-        // (a thread writing its own row's 16 bytes at a time took 10,000 cycles)
+        // the warp's [32 rows][128 latents], 64 bytes of each row at a time: through shared memory
+        // (the weights' place, free now) in two buffers, from where tile stores take them; threads
+        // where a store would pass the sequence's last row
         uint8_t *stage = sm + OFF_P + warp * 4096;
         const bool bits = whole && a.z_bf16;
         const int col0 = 256 * ph + 128 * hf, first = 32 * (qw & 1);  // of the warp: latents, rows
-        const int width = bits ? 2 : 4;
-        // this lane's 16 bytes of the warp's first row: in z, or in this run's partial sums
-        char *dst = (whole ? reinterpret_cast<char *>(a.z) + ((int64_t)s.lo * a.H + r0 + first) * TL * width
-                           : reinterpret_cast<char *>(part) + ((size_t)slot * 2 * RC + RC * rank + first) * TL * 4) +
-                    col0 * width + 16 * (lane & 7);
+        const int width = bits ? 2 : 4, cols = 64 / width;
+        const bool by_tile = !whole || first + 32 <= rows;
+        const int64_t row0 = whole ? (int64_t)s.lo * a.H + r0 + first : (int64_t)slot * 2 * RC + RC * rank + first;
+        const CUtensorMap *map = whole ? &maps.z : &maps.part;
+        auto put = [&](int half, int c, const uint4 (&v)[4]) {
+          if (lane == 0) bulk_wait_read1();
+          __syncwarp();
+          uint8_t *buf = stage + 2048 * half;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4 *>(buf + lane * 64 + ((x ^ (lane >> 1 & 3)) << 4)) = v[x];
+          if (by_tile) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(map, col0 + c, (int)row0, 0, smem_u32(buf));
+              bulk_commit();
+            }
+          } else {
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int r = 8 * x + (lane >> 2), piece = lane & 3;
+              const uint4 y = *reinterpret_cast<const uint4 *>(buf + r * 64 + ((piece ^ (r >> 1 & 3)) << 4));
+              if (first + r < rows)
+                *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(a.z) + ((row0 + r) * TL + col0 + c) * width + 16 * piece) = y;
+            }
+          }
+        };
 #pragma unroll 1
-        for (int c = 0; c < 128; c += bits ? 64 : 32) {
+        for (int c = 0; c < 128; c += 32) {
           float z[32];
           tmem_ld32(tm + lanes + TM_Z + 128 * hf + c, z);
           tmem_wait_ld();
           if (bits) {
-            float y[32];
-            tmem_ld32(tm + lanes + TM_Z + 128 * hf + c + 32, y);
-            tmem_wait_ld();
             auto pack = [&](float lo, float hi) {
               const __nv_bfloat162 b = __floats2bfloat162_rn(lo * inv, hi * inv);
               return *reinterpret_cast<const uint32_t *>(&b);
             };
+            uint4 v[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              *reinterpret_cast<uint4 *>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) = make_uint4(
-                  pack(z[8 * x], z[8 * x + 1]), pack(z[8 * x + 2], z[8 * x + 3]), pack(z[8 * x + 4], z[8 * x + 5]),
-                  pack(z[8 * x + 6], z[8 * x + 7]));
-              *reinterpret_cast<uint4 *>(stage + lane * 128 + (((x + 4) ^ (lane & 7)) << 4)) = make_uint4(
-                  pack(y[8 * x], y[8 * x + 1]), pack(y[8 * x + 2], y[8 * x + 3]), pack(y[8 * x + 4], y[8 * x + 5]),
-                  pack(y[8 * x + 6], y[8 * x + 7]));
-            }
+            for (int x = 0; x < 4; ++x)
+              v[x] = make_uint4(pack(z[8 * x], z[8 * x + 1]), pack(z[8 * x + 2], z[8 * x + 3]),
+                                pack(z[8 * x + 4], z[8 * x + 5]), pack(z[8 * x + 6], z[8 * x + 7]));
+            put(c >> 5 & 1, c, v);
           } else {
             const float f = whole ? inv : 1.f;
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              *reinterpret_cast<float4 *>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) =
-                  make_float4(z[4 * x] * f, z[4 * x + 1] * f, z[4 * x + 2] * f, z[4 * x + 3] * f);
-          }
-          __syncwarp();
+            for (int y = 0; y < 2; ++y) {
+              uint4 v[4];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int r = 4 * x + (lane >> 3), piece = lane & 7;
-            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
-            if (first + r < rows) {
-              *reinterpret_cast<uint4 *>(dst + (size_t)r * TL * width + c * width) = v;
+              for (int x = 0; x < 4; ++x)
+                v[x] = make_uint4(__float_as_uint(z[16 * y + 4 * x] * f), __float_as_uint(z[16 * y + 4 * x + 1] * f),
+                                  __float_as_uint(z[16 * y + 4 * x + 2] * f), __float_as_uint(z[16 * y + 4 * x + 3] * f));
+              put(y, c + cols * y, v);
             }
           }
-          __syncwarp();
         }
         if (!whole && quarter == 0) {
           float *ml = part_ml + ((size_t)slot * 2 * RC + RC * rank + row) * 2;
@@ -745,7 +761,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_pair(lead + 8 * B_ZFREE);
+        if (lane == 0) {
+          arrive_pair(lead + 8 * B_ZFREE);
+          bulk_wait_read0();  // the weights' place is free again
+        }
       }
       bar_sync(2, 288);  // (see warp 11)
       // what the combine kernel merges: a sequence's rows whose last tile is in this run and
@@ -767,6 +786,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       ++segs;
     }
     if (segs == 0 && rank == 0 && tid == 0) merge[cid].rows = 0;
+    if (lane == 0) bulk_wait0();
   }
   if (lane == 0 && s_abort && a.err) atomicOr(a.err, ERR_MBAR_TIMEOUT);
   __syncwarp();
@@ -774,7 +794,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == 0)
+  if (warp == W_SCORE)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u));
 }
 
@@ -820,15 +840,18 @@ __global__ void __launch_bounds__(CNT) tree_combine_kernel(const TreeAttnArgs a,
   }
 }
 
-bool tree_map(CUtensorMap *m, const void *ptr, int64_t d1, int64_t d2, int box_rows) {
+// [d2][d1][cols], the innermost contiguous, in boxes of box_cols x box_rows
+bool tree_map(CUtensorMap *m, const void *ptr, bool bits, int cols, int64_t d1, int64_t d2, int box_cols, int box_rows) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)TK, (cuuint64_t)d1, (cuuint64_t)d2};
-  cuuint64_t strides[2] = {(cuuint64_t)TK * 2, (cuuint64_t)d1 * TK * 2};
-  cuuint32_t bx[3] = {64, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, bx, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const int width = bits ? 2 : 4;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)d1, (cuuint64_t)d2};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * width, (cuuint64_t)d1 * cols * width};
+  cuuint32_t bx[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+  return fn(m, bits ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(ptr), dims,
+            strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_cols * width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr size_t PART = (size_t)MAX_CLUSTERS * 2 * 2 * RC * TL * sizeof(float);
@@ -844,8 +867,10 @@ cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s
   memset(&maps, 0, sizeof maps);
   const int64_t rows = a.total * a.H;
   const int box = a.c.page_size < 64 ? a.c.page_size : 64;
-  if (!tree_map(&maps.q, a.q, rows, 1, rows < RC ? (int)rows : RC) ||
-      !tree_map(&maps.c, a.c.pool, a.c.page_size, a.c.n_pages, box))
+  if (!tree_map(&maps.q, a.q, true, TK, rows, 1, 64, rows < RC ? (int)rows : RC) ||
+      !tree_map(&maps.c, a.c.pool, true, TK, a.c.page_size, a.c.n_pages, 64, box) ||
+      !tree_map(&maps.z, a.z, a.z_bf16, TL, rows, 1, a.z_bf16 ? 32 : 16, rows < 32 ? (int)rows : 32) ||
+      !tree_map(&maps.part, a.ws, false, TL, MAX_CLUSTERS * 2 * 2 * RC, 1, 16, 32))
     return cudaErrorInvalidValue;
   int dev = 0, nsm = 0;
   cudaError_t e = cudaGetDevice(&dev);
