@@ -255,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       s.row_tiles = s.tiles = 0;
       if (n0 + tid < a.n_seqs) s = seq_of(a, n0 + tid, blockIdx.x == 0);
     }
-#pragma unroll
+#pragma unroll 1  // (run once: its instructions come from L2, so few of them)
     for (int g = 0; g < 4; ++g) {  // at most 64 x 2^20 tiles each: a warp's sum fits 32 bits
       const uint32_t c = __reduce_add_sync(0xffffffffu, (uint32_t)((s.row_tiles + (1 << g) - 1) >> g) * (uint32_t)s.tiles);
       if (lane == 0 && c) atomicAdd(&s_cost[g], (unsigned long long)c);
@@ -266,28 +266,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   // it, but its clusters' tiles take less: they share HBM's reads (measured: 0.93 of a lone cluster's
   // time for two, 0.87 for four; 64 sequences x 6 to 8 nodes x 4096: 202 us alone, 180 in fours;
   // 100 x 4 to 5 nodes: 132 alone, 139 in twos).
-  int group = 1, workers = clusters;
+  int log_group = lane & 3;
   {
-    float best = INFINITY;
+    float cost = (clusters >> log_group)
+                     ? __fdividef((float)s_cost[log_group] * (log_group == 0 ? 1.f : log_group == 1 ? 0.93f : 0.87f),
+                                  (float)(clusters >> log_group))
+                     : INFINITY;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const float cost = (clusters >> g) ? __fdividef((float)s_cost[g] * (g == 0 ? 1.f : g == 1 ? 0.93f : 0.87f), (float)(clusters >> g))
-                                         : INFINITY;
-      if (cost <= best) best = cost, group = 1 << g, workers = clusters >> g;
+    for (int o = 1; o < 4; o <<= 1) {
+      const float c = __shfl_xor_sync(0xffffffffu, cost, o);
+      const int g = __shfl_xor_sync(0xffffffffu, log_group, o);
+      if (c < cost || (c == cost && g > log_group)) cost = c, log_group = g;
     }
   }
-  const int64_t tiles = (int64_t)s_cost[31 - __clz(group)];
-  if (tiles < workers) workers = (int)tiles;  // so every worker has a run
-  const int worker = cid >> (31 - __clz(group)), member = cid & (group - 1);
-  const int64_t begin = worker < workers ? run_start(tiles, worker, workers) : 0;
-  const int64_t stop = worker < workers ? run_start(tiles, worker + 1, workers) : 0;
+  const int group = 1 << log_group;
+  const int64_t tiles = (int64_t)s_cost[log_group];
+  // every worker has a run
+  const int workers = tiles < (clusters >> log_group) ? (int)tiles : clusters >> log_group;
+  const int worker = cid >> log_group, member = cid & (group - 1);
+  int64_t begin = 0, stop = 0;
+  if (worker < workers) {
+    const int64_t x = run_start(tiles, worker + (lane & 1), workers);
+    begin = __shfl_sync(0xffffffffu, x, 0), stop = __shfl_sync(0xffffffffu, x, 1);
+  }
   if (stop > begin) {  // the sequence that tile `begin` falls in
     int64_t before = 0;
     for (int n0 = 0; n0 < a.n_seqs && before <= begin; n0 += NT) {
       uint32_t cost = 0;
       if (n0 + tid < a.n_seqs) {
         const Seq s = n0 == 0 ? mine : seq_of(a, n0 + tid, false);
-        cost = (uint32_t)((s.row_tiles + group - 1) >> (31 - __clz(group))) * (uint32_t)s.tiles;
+        cost = (uint32_t)((s.row_tiles + group - 1) >> log_group) * (uint32_t)s.tiles;
       }
       uint32_t x = cost;
 #pragma unroll
@@ -297,11 +305,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       }
       if (lane == 31) s_scan[warp] = x;
       __syncthreads();
-      int64_t at = before;
-      for (int w = 0; w < warp; ++w) at += s_scan[w];
-      at += x - cost;
+      const uint32_t v = lane < NT / 32 ? s_scan[lane] : 0, v0 = lane < warp ? v : 0;  // sums in two halves: past 32 bits
+      const int64_t at = before + __reduce_add_sync(0xffffffffu, v0 & 0xffff) +
+                         ((int64_t)__reduce_add_sync(0xffffffffu, v0 >> 16) << 16) + (x - cost);
       if (at <= begin && begin < at + cost) s_n = n0 + tid, s_off = (int)(begin - at);
-      for (int w = 0; w < NT / 32; ++w) before += s_scan[w];
+      before += __reduce_add_sync(0xffffffffu, v & 0xffff) + ((int64_t)__reduce_add_sync(0xffffffffu, v >> 16) << 16);
       __syncthreads();
     }
   }
