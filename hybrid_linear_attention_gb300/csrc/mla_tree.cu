@@ -42,6 +42,7 @@
 
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 namespace kda {
 namespace {
@@ -379,38 +380,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         __syncwarp();
         if (elect()) {
           const int p0 = TILE * t;
-          if (scores) {
-            const int e0 = (128 * (int)rank) >> lb;
+          // a tile's loads, 64 positions in PER boxes
+          auto load = [&](auto PER) {
+            constexpr int per = decltype(PER)::value, rows = 64 / per;
+            if (scores) {
+              const int e0 = 2 * per * (int)rank;
+              int page[2 * per];
+#pragma unroll
+              for (int y = 0; y < 2 * per; ++y) page[y] = s_page[0][e0 + y];
 #pragma unroll 1
-            for (int kb = 0; kb < KB; ++kb) {
-              if (wait(empty + j, par)) {
-                announce();
-#pragma unroll 1
-                for (int y = 0; y < 2 * per; ++y)
-                  tma_pair_3d(ring + j * SLOT + y * box * 128, &maps.c, 64 * kb, (p0 + ((e0 + y) << lb)) & in_page,
-                              s_page[which][e0 + y], full0 + 8 * j, policy);
-              }
-              step();
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              const int g0 = p0 + 64 * (c >> 1), e0 = (64 * (c >> 1)) >> lb, ch = 256 * (int)rank + 128 * (c & 1);
-              const bool tail = g0 + 64 > walk.s.len && g0 < walk.s.end;  // warp 10 looks it over
-              if (wait(empty + j, par)) {
-                if (!tail) announce();
-                else mbar_expect_tx(bar(B_TAIL + j), SLOT);
-                const uint32_t done = (tail ? tail0 : full0) + 8 * j;
-#pragma unroll 1
-                for (int y = 0; y < per; ++y) {
-                  const int row = (p0 + ((e0 + y) << lb)) & in_page, pg = s_page[which][e0 + y];
-                  tma_pair_3d(ring + j * SLOT + y * box * 128, &maps.c, ch, row, pg, done, policy);
-                  tma_pair_3d(ring + j * SLOT + 8192 + y * box * 128, &maps.c, ch + 64, row, pg, done, policy);
+              for (int kb = 0; kb < KB; ++kb) {
+                if (wait(empty + j, par)) {
+                  announce();
+#pragma unroll
+                  for (int y = 0; y < 2 * per; ++y)
+                    tma_pair_3d(ring + j * SLOT + y * rows * 128, &maps.c, 64 * kb,
+                                per == 1 ? (p0 + 64 * (e0 + y)) & in_page : 0, page[y], full0 + 8 * j, policy);
                 }
+                step();
               }
-              step();
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                const int g0 = p0 + 64 * (c >> 1), e0 = per * (c >> 1), ch = 256 * (int)rank + 128 * (c & 1);
+                const bool tail = g0 + 64 > walk.s.len && g0 < walk.s.end;  // warp 10 looks it over
+                if (wait(empty + j, par)) {
+                  if (!tail) announce();
+                  else mbar_expect_tx(bar(B_TAIL + j), SLOT);
+                  const uint32_t done = (tail ? tail0 : full0) + 8 * j;
+                  const int row = per == 1 ? g0 & in_page : 0;
+#pragma unroll
+                  for (int y = 0; y < per; ++y) {
+                    const int page = s_page[1][e0 + y];
+                    tma_pair_3d(ring + j * SLOT + y * rows * 128, &maps.c, ch, row, page, done, policy);
+                    tma_pair_3d(ring + j * SLOT + 8192 + y * rows * 128, &maps.c, ch + 64, row, page, done, policy);
+                  }
+                }
+                step();
+              }
             }
-          }
+          };
+          if (per == 1) load(std::integral_constant<int, 1>{});
+          else if (per == 2) load(std::integral_constant<int, 2>{});
+          else load(std::integral_constant<int, 4>{});
         } else {
           for (int y = 0; y < (scores ? KB : 8); ++y) step();
         }
