@@ -148,11 +148,17 @@ __device__ __forceinline__ void ask_inputs(const TreeArgs &a, int row0, int rows
 }
 
 // shared memory of the verify kernel for at most W nodes (floats): k over q [2 W, whole tiles of
-// 16][D + 4], v, G (then S^T k) [W][D] each, then S^T q [W][D], A and B [W][W], which take the place of
-// the raw inputs [W + 3][3 D] where those are staged (bf16)
+// 16][D + 4], v, G (then S^T k) [W][D] each, then S^T q [W][D] and A and B of the pairs, which take the
+// place of the raw inputs [W + 3][3 D] where those are staged (bf16); the list of the pairs (node, itself or
+// an ancestor), 16 bits each
+__host__ __device__ constexpr size_t verify_pairs(int W) { return (size_t)W * (W + 1) / 2; }
+__host__ __device__ constexpr size_t verify_late_floats(int W, int D, bool staged) {
+  const size_t late = (size_t)W * D + 2 * verify_pairs(W), raw = staged ? ((size_t)(W + 3) * 3 * D + 1) / 2 : 0;
+  return late > raw ? late : raw;
+}
 __host__ __device__ constexpr size_t verify_smem_floats(int W, int D, bool staged) {
-  const size_t late = (size_t)W * D + (size_t)2 * W * W, raw = staged ? ((size_t)(W + 3) * 3 * D + 1) / 2 : 0;
-  const size_t all = (size_t)((2 * W + 15) / 16 * 16) * (D + 4) + (size_t)2 * W * D + (late > raw ? late : raw);
+  const size_t all = (size_t)((2 * W + 15) / 16 * 16) * (D + 4) + (size_t)2 * W * D + verify_late_floats(W, D, staged) +
+                     (verify_pairs(W) + 1) / 2;
   return (all + 3) / 4 * 4;  // what follows starts on 16 bytes
 }
 __device__ __forceinline__ void copy_async16(void *smem, const void *global) {
@@ -222,11 +228,12 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
   extern __shared__ __align__(16) float smem[];
   __shared__ int s_par[64];
   __shared__ __align__(16) int s_tap[64][4];  // a node's taps, oldest first: nodes, or -1 (newest) .. -3 of the tail
-  __shared__ unsigned long long s_anc[64];
+  __shared__ int s_off[65];  // the pairs of node i: s_off[i] .. s_off[i + 1] - 1, itself first
   __shared__ float s_beta[64], s_rn[128];
   const int WM = a.max_nodes;
   float *s_x = smem, *s_v = s_x + (2 * WM + 15) / 16 * 16 * XS, *s_g = s_v + WM * D, *s_o = s_g + WM * D,
-        *s_A = s_o + WM * D, *s_B = s_A + WM * WM;
+        *s_A = s_o + WM * D, *s_B = s_A + verify_pairs(WM);
+  uint16_t *s_pair = reinterpret_cast<uint16_t *>(s_o + verify_late_floats(WM, D, !EXACT));  // node << 6 | ancestor
   IO *s_raw = reinterpret_cast<IO *>(s_o);  // row 3 + i: node i, rows 0 .. 2 the tail
   constexpr int SS = D + 16 / (int)sizeof(ST);
   ST *s_S = reinterpret_cast<ST *>(smem + verify_smem_floats(WM, D, !EXACT));
@@ -278,16 +285,33 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
     }
     __syncthreads();
     for (int i = tid; i < W; i += NT) {
-      unsigned long long m = 0;
       int u = i;
 #pragma unroll
       for (int y = 3; y >= 0; --y) {
         s_tap[i][y] = u;
         u = u >= 0 ? s_par[u] : (u > -3 ? u - 1 : -3);
       }
-      for (int j = s_par[i]; j >= 0; j = s_par[j]) m |= 1ull << j;
-      s_anc[i] = m;
     }
+    if (warp == 0)
+      for (int i0 = 0, base = 0; i0 < W; i0 += 32) {
+        const int i = i0 + lane;
+        int cnt = 0;
+        if (i < W)
+          for (int j = i; j >= 0; j = s_par[j]) ++cnt;
+        int x = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        int k = base + x - cnt;
+        base += __shfl_sync(0xffffffffu, x, 31);
+        if (i < W) {
+          s_off[i] = k;
+          if (i == W - 1) s_off[W] = base;
+          for (int j = i; j >= 0; j = s_par[j]) s_pair[k++] = (uint16_t)(i << 6 | j);
+        }
+      }
     asm volatile("cp.async.wait_group %0;" ::"n"(RESIDENT ? 1 : 0) : "memory");
     __syncthreads();
 
@@ -342,46 +366,37 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
       if ((tid & 7) == 0) s_rn[x] = a.qk_l2norm ? rsqrtf(ss + a.l2_eps) : 1.f;
     }
     __syncthreads();
-    // ---- A and B over the (node, ancestor or itself) pairs: eight lanes a pair, every NT/8-th of
-    //      the running count of pairs to a group of lanes
+    // ---- A and B over the (node, ancestor or itself) pairs: eight lanes a pair
     {
-      const int sub = 4 * (tid & 7);
+      const int sub = 4 * (tid & 7), pairs = s_off[W];
       const unsigned eight = 0xffu << (lane & 24);
-      int at = tid >> 3;
-      for (int i = 0; i < W; ++i) {
-        unsigned long long m = s_anc[i] | (1ull << i);
-        const int cnt = __popcll(m);
-        int k = at;
-        for (int skipped = 0; k < cnt; k += NT / 8) {
-          for (; skipped < k; ++skipped) m &= m - 1;
-          const int j = __ffsll((long long)m) - 1;
-          float pa = 0.f, pb = 0.f;
+      for (int k = tid >> 3; k < pairs; k += NT / 8) {
+        const int i = s_pair[k] >> 6, j = s_pair[k] & 63;
+        float pa = 0.f, pb = 0.f;
 #pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            const int c = c0 + sub;
-            if (c < D) {
-              const float4 gi = *reinterpret_cast<const float4 *>(s_g + i * D + c),
-                           gj = *reinterpret_cast<const float4 *>(s_g + j * D + c);
-              const float4 kj = *reinterpret_cast<const float4 *>(s_x + j * XS + c),
-                           ki = *reinterpret_cast<const float4 *>(s_x + i * XS + c),
-                           qi = *reinterpret_cast<const float4 *>(s_x + (W + i) * XS + c);
-              const float e0 = ex2_(gi.x - gj.x) * kj.x, e1 = ex2_(gi.y - gj.y) * kj.y, e2 = ex2_(gi.z - gj.z) * kj.z,
-                          e3 = ex2_(gi.w - gj.w) * kj.w;
-              pa = fmaf(ki.x, e0, fmaf(ki.y, e1, fmaf(ki.z, e2, fmaf(ki.w, e3, pa))));
-              pb = fmaf(qi.x, e0, fmaf(qi.y, e1, fmaf(qi.z, e2, fmaf(qi.w, e3, pb))));
-            }
-          }
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) {
-            pa += __shfl_xor_sync(eight, pa, o);
-            pb += __shfl_xor_sync(eight, pb, o);
-          }
-          if (sub == 0) {
-            s_A[i * WM + j] = pa * s_rn[i] * s_rn[j];
-            s_B[i * WM + j] = pb * s_rn[W + i] * s_rn[j];
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          const int c = c0 + sub;
+          if (c < D) {
+            const float4 gi = *reinterpret_cast<const float4 *>(s_g + i * D + c),
+                         gj = *reinterpret_cast<const float4 *>(s_g + j * D + c);
+            const float4 kj = *reinterpret_cast<const float4 *>(s_x + j * XS + c),
+                         ki = *reinterpret_cast<const float4 *>(s_x + i * XS + c),
+                         qi = *reinterpret_cast<const float4 *>(s_x + (W + i) * XS + c);
+            const float e0 = ex2_(gi.x - gj.x) * kj.x, e1 = ex2_(gi.y - gj.y) * kj.y, e2 = ex2_(gi.z - gj.z) * kj.z,
+                        e3 = ex2_(gi.w - gj.w) * kj.w;
+            pa = fmaf(ki.x, e0, fmaf(ki.y, e1, fmaf(ki.z, e2, fmaf(ki.w, e3, pa))));
+            pb = fmaf(qi.x, e0, fmaf(qi.y, e1, fmaf(qi.z, e2, fmaf(qi.w, e3, pb))));
           }
         }
-        at = k - cnt;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          pa += __shfl_xor_sync(eight, pa, o);
+          pb += __shfl_xor_sync(eight, pb, o);
+        }
+        if (sub == 0) {
+          s_A[k] = pa * s_rn[i] * s_rn[j];
+          s_B[k] = pb * s_rn[W + i] * s_rn[j];
+        }
       }
     }
     __syncthreads();
@@ -488,10 +503,7 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
     for (int c = tid; c < D; c += NT)
       for (int i = 0; i < W; ++i) {
         float u = s_v[i * D + c] - s_g[i * D + c];
-        for (unsigned long long m = s_anc[i]; m; m &= m - 1) {
-          const int j = __ffsll((long long)m) - 1;
-          u = fmaf(-s_A[i * WM + j], s_v[j * D + c], u);
-        }
+        for (int k = s_off[i] + 1; k < s_off[i + 1]; ++k) u = fmaf(-s_A[k], s_v[(s_pair[k] & 63) * D + c], u);
         s_v[i * D + c] = s_beta[i] * u;
       }
     __syncthreads();
@@ -504,10 +516,9 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
         if (a.gate) z = load4(reinterpret_cast<const IO *>(a.gate) + row);
         if (a.gate && a.norm_w) w = load4(a.norm_w + c);
         o = *reinterpret_cast<const float4 *>(s_o + i * D + c);
-        for (unsigned long long m = s_anc[i] | (1ull << i); m; m &= m - 1) {
-          const int j = __ffsll((long long)m) - 1;
-          const float b = s_B[i * WM + j];
-          const float4 u = *reinterpret_cast<const float4 *>(s_v + j * D + c);
+        for (int k = s_off[i]; k < s_off[i + 1]; ++k) {
+          const float b = s_B[k];
+          const float4 u = *reinterpret_cast<const float4 *>(s_v + (s_pair[k] & 63) * D + c);
           o.x = fmaf(b, u.x, o.x), o.y = fmaf(b, u.y, o.y), o.z = fmaf(b, u.z, o.z), o.w = fmaf(b, u.w, o.w);
         }
         o.x *= a.scale, o.y *= a.scale, o.z *= a.scale, o.w *= a.scale;
