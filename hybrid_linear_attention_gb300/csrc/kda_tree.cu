@@ -115,10 +115,9 @@ struct Conv4 {
   }
 };
 
-// `bytes` from p on into L2, a line a thread
-__device__ __forceinline__ void ask_l2(const void *p, size_t bytes, int th, int nth) {
-  for (size_t off = (size_t)th * 128; off < bytes; off += (size_t)nth * 128)
-    l2_prefetch(reinterpret_cast<const char *>(p) + off);
+// `bytes` (a multiple of 16) from p on into L2, by one instruction
+__device__ __forceinline__ void ask_bulk(const void *p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // What a CTA will read of heads h .. h + HEADS - 1 of `rows` nodes of sequence n, into L2: the raw
@@ -210,18 +209,21 @@ constexpr size_t resident_floats() {
 // w loads columns 32 w + 4 g .. + 3 of its rows of S, which are its parts of the products' B operands,
 // straight from memory into registers, and gets columns 32 w + 8 t .. + 7 of X S.  With bf16 I/O both
 // operands are split into two bf16 parts and three products are added, good to about 2^-16 (an output
-// is rounded to 2^-9); with fp32 I/O into two tf32 parts, about 2^-21.
-// A CTA is small (four warps, no state held), so that seven share an SM, each in another of the phases
+// is rounded to 2^-8 of itself); with fp32 I/O into two tf32 parts, about 2^-21.
+// A CTA is small (four warps, no state held), so that eight share an SM, each in another of the phases
 // that the few barriers of a unit cut.  bf16 inputs come into shared memory by asynchronous copies
 // that run while the tree is worked out.
 // RESIDENT: with few units (no more than fit at a time) the state comes into shared memory the same
 // way, all at once; read step by step from L2 it would be most of a lone unit's time (one sequence x
-// 12 nodes x 64 heads: 19.7 us so, 16.2 resident).
-// Measured at 256 sequences x 6 to 8 nodes x 64 heads: 357 us (3.7 TB/s of what it must move, 1.36 GB
-// read from HBM), 14,000 warp instructions a unit at 55 % of the issue slots: issue and the phases'
-// latencies bound it, no longer the memory.  Five CTAs of 96 registers an SM took 419 us, eight 364.
+// 12 nodes x 64 heads: 19.7 us so, 16.2 resident, before the pairs were listed; 13.7 since).
+// Measured at 256 sequences x 6 to 8 nodes x 64 heads: 318 us, 4.2 TB/s of what it must move.  What is
+// not the state's product takes 186 us on its own (issue and the latencies of its short phases), the
+// product's loads from L2 most of the rest: more CTAs hide more of both (seven an SM 334 us, six 346, nine
+// spill: 356), which is also why deeper loads cost more than they give (two steps of the state in flight
+// through shared memory, five CTAs: 438 us; through registers: 363).  The state is asked of L2 by one bulk
+// prefetch a unit (325 us by a line a thread, 341 without).
 template <int D, typename IO, typename ST, bool RESIDENT>
-__global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 : 7) : 1) tree_verify_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 : 8) : 1) tree_verify_kernel(const TreeArgs a) {
   constexpr int CW = VerifyShape<D>::CW, NT = VerifyShape<D>::NT, NJ = VerifyShape<D>::NJ, NW = NT / 32, XS = D + 4;
   constexpr int CT = 3 * D / 4;  // threads of the convolution, four channels each
   constexpr bool EXACT = sizeof(IO) == 4;
@@ -270,7 +272,8 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
       for (int x = tid; x < D * D / P; x += NT) copy_async16(s_S + x / (D / P) * SS + x % (D / P) * P, src + (size_t)x * P);
       asm volatile("cp.async.commit_group;" ::: "memory");
     } else {
-      ask_l2(src, sizeof(ST) * D * D, tid, NT);  // needed a few phases on (any earlier, and L2 drops it again)
+      // needed a few phases on (any earlier, and L2 drops it again)
+      if (tid == 0) ask_bulk(src, sizeof(ST) * D * D);
     }
 
     // ---- the sequence's tree ---------------------------------------------------------------------
@@ -573,7 +576,7 @@ __global__ void __launch_bounds__(2 * D, 2) tree_accept_kernel(const TreeArgs a,
     }
     if (last < 0) continue;  // nothing accepted: state and tail stay
     ST *state = reinterpret_cast<ST *>(a.state) + ((size_t)slot * H + h0) * (size_t)D * D;
-    if (unit == blockIdx.x) ask_l2(state, sizeof(ST) * D * D, tid, NT);
+    if (unit == blockIdx.x && tid == 0) ask_bulk(state, sizeof(ST) * D * D);
     __syncthreads();  // the previous group's shared memory has been read
     for (int i = tid; i <= last; i += NT) {
       int p = a.parent[row0 + i];
@@ -640,14 +643,14 @@ __global__ void __launch_bounds__(2 * D, 2) tree_accept_kernel(const TreeArgs a,
         S[r][0] = x.x, S[r][1] = x.y, S[r][2] = x.z, S[r][3] = x.w;
       }
       if (y + 1 < group) {
-        ask_l2(state + (size_t)(y + 1) * D * D, sizeof(ST) * D * D, tid, NT);
+        if (tid == 0) ask_bulk(state + (size_t)(y + 1) * D * D, sizeof(ST) * D * D);
       } else if (unit + gridDim.x < groups) {  // the next group's first head
         const uint32_t nu = (unit + gridDim.x) * group;
         const int nn = (int)(nu / H), ns = a.slot_idx ? a.slot_idx[nn] : nn;
         int nrow0;
         const int nw = tree_nodes(a, nn, 64, nrow0, false), nl = a.accept[nn];
         if (ns >= 0 && ns < a.n_slots && nl >= 0 && nl < nw) {
-          ask_l2(reinterpret_cast<const ST *>(a.state) + ((size_t)ns * H + nu % H) * (size_t)D * D, sizeof(ST) * D * D, tid, NT);
+          if (tid == 0) ask_bulk(reinterpret_cast<const ST *>(a.state) + ((size_t)ns * H + nu % H) * (size_t)D * D, sizeof(ST) * D * D);
           if (group == 2) ask_inputs<D, IO, 2, 1>(a, nrow0, nl + 1, ns, (int)(nu % H), tid, NT);
           else ask_inputs<D, IO, 1, 1>(a, nrow0, nl + 1, ns, (int)(nu % H), tid, NT);
         }
