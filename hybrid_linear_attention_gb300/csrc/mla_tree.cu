@@ -24,12 +24,14 @@
 // an issuing warp each: while the softmax of tile t runs, S of t + 1 and Z of t - 1 are built side
 // by side.  One thread's products leave gaps (measured: with a wait and a commit every four of
 // them, 101 to 149 cycles a product instead of 64), two threads' fill each other's (64 cycles); one
-// thread's loads cost it about 450 cycles a slot, so two load.
-// That brings 272 KB to a CTA for 256 positions; TMA moves about 41 bytes a cycle and SM from L2
-// (measured, 12 TB/s), the products at full rate would take 64, so L2 is the bound where the cache is
-// read by several row tiles: 4 sequences x 11 to 16 nodes x 65536 positions 281 us, 1.52 PFLOP/s, 78 %
-// of the measured bf16 peak.  With one node a sequence the same loop streams the cache: 256 sequences
-// of up to 4096 positions 207 us, 4.6 TB/s; there HBM's latency against the ring's depth bounds it
+// thread's loads cost it about 450 cycles a slot, so two load, a slot's loads in a row without a lookup
+// between them (with one, pages of 16 positions were bound by it: 422 us for 283, pages of 64 278 for 266).
+// That brings 272 KB to a CTA for 256 positions, 64 bytes a cycle at the products' full rate; TMA moves 41
+// to 48 bytes a cycle and SM from L2, so L2 is the bound where the cache is read by several row tiles:
+// 4 sequences x 11 to 16 nodes x 65536 positions 266 us, 1.60 PFLOP/s, 83 % of the measured bf16 peak.
+// The rings' depth is what that rate needs: a slot less in either costs 11 to 35 %, one more (weights of
+// 128 positions at a time) gives back only what the smaller place for the weights costs.  With one node a
+// sequence the same loop streams the cache: 256 sequences of up to 4096 positions 200 us, 4.7 TB/s
 // (asking L2 for coming tiles, by bulk prefetches or by threads, measured slower: 247 to 272 us).
 //
 // Work is dealt in tiles of 256 positions: clusters form groups of G that take G row tiles of a
@@ -264,13 +266,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   }
   __syncthreads();
   // The group whose run takes the least time.  A larger one idles where row tiles do not divide by
-  // it, but its clusters' tiles take less: they share HBM's reads (measured: 0.93 of a lone cluster's
-  // time for two, 0.87 for four; 64 sequences x 6 to 8 nodes x 4096: 202 us alone, 180 in fours;
-  // 100 x 4 to 5 nodes: 132 alone, 139 in twos).
+  // it, but its clusters' tiles take less: they share HBM's reads (measured: 0.86 to 0.96 of a lone
+  // cluster's time for two, 0.73 to 0.83 for four; 64 sequences x 6 to 8 nodes x 4096: 190 us alone, 193 in
+  // twos, 165 in fours; 100 x 3 to 4 nodes: 169, 148, 235; 100 x 4 to 5 nodes: 204, 228, 241).
   int log_group = lane & 3;
   {
     float cost = (clusters >> log_group)
-                     ? __fdividef((float)s_cost[log_group] * (log_group == 0 ? 1.f : log_group == 1 ? 0.93f : 0.87f),
+                     ? __fdividef((float)s_cost[log_group] * (log_group == 0 ? 1.f : log_group == 1 ? 0.93f : 0.82f),
                                   (float)(clusters >> log_group))
                      : INFINITY;
 #pragma unroll
