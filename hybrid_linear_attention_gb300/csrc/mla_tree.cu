@@ -91,10 +91,10 @@ struct TreeMaps {
   CUtensorMap q, c, z, part;
 };
 // What the clusters leave for the combine kernel: partial sums [2 x clusters][128][512], their
-// (reference, normaliser) [..][128][2], and for every cluster the rows it completes.
+// (reference, normaliser) [..][128][2], and for every cluster the row tile that its run begins inside.
 struct Merge {
-  int row0, rows;           // rows that this cluster's first run completes (0: none)
-  int first, last;          // workers that hold parts of them
+  int row0, rows;           // the row tile (0 rows: the run begins with one)
+  int first, last;          // workers that hold parts of it
   int group, pad[3];
 };
 
@@ -181,19 +181,20 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnArgs &a, int n, bool tell) {
 struct Walk {
   int n, off;    // place in sequence n's (pass, tile) order (at most 2^26 tiles)
   int64_t left;  // tiles left
-  int group, member;
+  int log_group, member;
   Seq s;
   int rt, t0, t1;     // the current segment: row tile, tiles t0 .. t1 - 1
   __device__ __forceinline__ bool next(const TreeAttnArgs &a) {
     while (left > 0) {
       s = seq_of(a, n, false);
-      if (off >= (s.row_tiles + group - 1) / group * s.tiles) {
+      if (off >= ((s.row_tiles + (1 << log_group) - 1) >> log_group) * s.tiles) {
         ++n;
         off = 0;
         continue;
       }
-      t0 = off % s.tiles;
-      rt = off / s.tiles * group + member;
+      const int pass = off / s.tiles;
+      t0 = off - pass * s.tiles;
+      rt = (pass << log_group) + member;
       t1 = s.tiles - t0 < left ? s.tiles : t0 + (int)left;
       off += t1 - t0;
       left -= t1 - t0;
@@ -206,6 +207,11 @@ struct Walk {
 // The first tile of worker w's run (a 64-bit division costs hundreds of cycles: only where needed).
 __device__ __forceinline__ int64_t run_start(int64_t tiles, int w, int workers) {
   return tiles < (1 << 24) ? (int64_t)((uint32_t)tiles * (uint32_t)w / (uint32_t)workers) : tiles * w / workers;
+}
+// The worker whose run holds tile t: the last that starts at or before it.
+__device__ __forceinline__ int worker_of(int64_t tiles, int64_t t, int workers) {
+  const int64_t x = (t + 1) * workers - 1;
+  return ((x | tiles) >> 32) == 0 ? (int)((uint32_t)x / (uint32_t)tiles) : (int)(x / tiles);
 }
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     tree_attn_kernel(const TreeAttnArgs a, const __grid_constant__ TreeMaps maps, float *part, float *part_ml,
@@ -296,8 +302,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     int64_t before = 0;
     for (int n0 = 0; n0 < a.n_seqs && before <= begin; n0 += NT) {
       uint32_t cost = 0;
+      Seq s = mine;
       if (n0 + tid < a.n_seqs) {
-        const Seq s = n0 == 0 ? mine : seq_of(a, n0 + tid, false);
+        if (n0 > 0) s = seq_of(a, n0 + tid, false);
         cost = (uint32_t)((s.row_tiles + group - 1) >> log_group) * (uint32_t)s.tiles;
       }
       uint32_t x = cost;
@@ -311,17 +318,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       const uint32_t v = lane < NT / 32 ? s_scan[lane] : 0, v0 = lane < warp ? v : 0;  // sums in two halves: past 32 bits
       const int64_t at = before + __reduce_add_sync(0xffffffffu, v0 & 0xffff) +
                          ((int64_t)__reduce_add_sync(0xffffffffu, v0 >> 16) << 16) + (x - cost);
-      if (at <= begin && begin < at + cost) s_n = n0 + tid, s_off = (int)(begin - at);
+      if (at <= begin && begin < at + cost) {
+        const int off = (int)(begin - at);
+        s_n = n0 + tid, s_off = off;
+        if (rank == 0) {  // what the combine kernel merges with this worker's blocks
+          const int t0 = off % s.tiles, left = s.W * a.H - 2 * RC * (off / s.tiles * group + member);
+          Merge g;
+          g.group = group;
+          g.first = worker_of(tiles, begin - t0, workers), g.last = worker_of(tiles, begin - t0 + s.tiles - 1, workers);
+          g.row0 = (s.lo + s.W) * a.H - left;
+          g.rows = t0 == 0 || left <= 0 ? 0 : left < 2 * RC ? left : 2 * RC;
+          merge[cid] = g;
+        }
+      }
       before += __reduce_add_sync(0xffffffffu, v & 0xffff) + ((int64_t)__reduce_add_sync(0xffffffffu, v >> 16) << 16);
       __syncthreads();
     }
   }
+  if (stop <= begin && rank == 0 && tid == 0) merge[cid].rows = 0;
   __syncthreads();
   cluster_wait();
   tc_fence_after();
   const uint32_t tm = s_tmem;
   Walk walk;
-  walk.n = s_n, walk.off = s_off, walk.left = stop - begin, walk.group = group, walk.member = member;
+  walk.n = s_n, walk.off = s_off, walk.left = stop - begin, walk.log_group = log_group, walk.member = member;
   // A wait that runs out raises s_abort; from then on waits fail at once.  The softmax and load
   // warps then walk on to the end without waiting (they meet on named barriers, which all of them
   // have to reach), and the loader issues nothing more.
@@ -601,8 +621,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     const uint32_t lanes = (uint32_t)(32 * qw) << 16;
     const int lp = 31 - __clz(a.c.page_size);
     const uint32_t lead = map_shared_rank(bar(0), 0);
-    uint8_t *prow = sm + OFF_P + quarter * RC * 128 + row * 128;
-    int i = 0, segs = 0;
+    const uint32_t prow = sb + OFF_P + quarter * RC * 128 + row * 128;
+    int i = 0;
     while (walk.next(a)) {
       const int r0 = 2 * RC * walk.rt + RC * (int)rank;  // this CTA's first row of the sequence
       const int rows = walk.s.W * a.H - r0;              // and how many are there (may be <= 0)
@@ -697,7 +717,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         if (i > 0) wait(B_PFREE + quarter, (uint32_t)(i - 1));  // the last tile's weights are read
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4 *>(prow + ((c ^ (row & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + ((c ^ (row & 7)) << 4)), "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3]) : "memory");
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) arrive_pair(lead + 8 * (B_PFULL + quarter));
@@ -789,25 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         }
       }
       bar_sync(2, 288);  // (see warp 11)
-      // what the combine kernel merges: a sequence's rows whose last tile is in this run and
-      // whose first is not
-      if (segs == 0 && rank == 0 && tid == 0 && walk.t0 > 0) {
-        Merge g;
-        g.group = group, g.rows = 0, g.row0 = 0, g.first = g.last = 0;
-        if (walk.t1 == s.tiles) {
-          const int64_t first_tile = begin - walk.t0;
-          g.row0 = s.lo * a.H + 2 * RC * walk.rt;
-          g.rows = s.W * a.H - 2 * RC * walk.rt < 2 * RC ? s.W * a.H - 2 * RC * walk.rt : 2 * RC;
-          g.first = (int)(((first_tile + 1) * workers - 1) / tiles);  // the last run that starts at or before it
-          g.last = worker;
-        }
-        merge[cid] = g;
-      } else if (segs == 0 && rank == 0 && tid == 0) {
-        merge[cid].rows = 0;
-      }
-      ++segs;
     }
-    if (segs == 0 && rank == 0 && tid == 0) merge[cid].rows = 0;
     if (lane == 0) bulk_wait0();
   }
   if (lane == 0 && s_abort && a.err) atomicOr(a.err, ERR_MBAR_TIMEOUT);
@@ -820,42 +822,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u));
 }
 
-// z = sum_w 2^(m_w - M) Z_w / sum_w 2^(m_w - M) l_w over the workers w that hold parts of a row; a warp
-// a row, the parts' loads independent of the running sums.
-constexpr int CNT = 256, CROWS = CNT / 32;
+// z = sum_w 2^(m_w - M) Z_w / sum_w 2^(m_w - M) l_w over the workers w that hold parts of a row.  The blocks
+// of all workers but the first share a row tile's rows: with two workers a warp merges a row, with more
+// (a long sequence alone is cut into as many parts as there are workers) two to eight warps take a row's
+// parts in turn and add up in a fixed order (one sequence x 4 nodes x 16384 positions, 64 parts: 41 us
+// for both kernels with a warp a row by the last worker's blocks, 29 so; one x 1 x 65536 59 and 36).
+constexpr int CNT = 256, CW = CNT / 32, CY = 2 * RC / CW;
 __global__ void __launch_bounds__(CNT) tree_combine_kernel(const TreeAttnArgs a, const float *part, const float *part_ml,
                                                            const Merge *merge) {
+  __shared__ __align__(16) float s_z[CW][TL];
+  __shared__ float s_l[CW];
   // launched while the attention kernel runs out: its results are there once this returns
   asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
   const Merge g = merge[blockIdx.x];
-  const int row = CROWS * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= g.rows) return;
-  const int member = blockIdx.x % g.group;
-  // the first worker's part is the end of its run, the others' the beginning of theirs
-  auto slot = [&](int w) { return (size_t)(2 * (w * g.group + member) + (w == g.first ? 1 : 0)) * 2 * RC + row; };
-  float M = -INFINITY;
-  for (int w = g.first + lane; w <= g.last; w += 32) M = fmaxf(M, part_ml[slot(w) * 2]);
-  M = warp_max(M);
+  if (g.rows == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int first = g.first, last = g.last;
+  const int log_group = 31 - __clz(g.group), member = blockIdx.x & (g.group - 1);
+  const int sharers = last - first, mine = ((int)blockIdx.x >> log_group) - first - 1;
+  const int log_k = sharers >= 8 ? 3 : sharers >= 4 ? 2 : sharers >= 2 ? 1 : 0, k = 1 << log_k;  // warps a row
+  const int row = (((int)blockIdx.y * sharers + mine) << (3 - log_k)) + (warp >> log_k), slice = warp & (k - 1);
   float4 z[4] = {};
   float L = 0.f;
+  if (row < g.rows) {
+    // the first worker's part is the end of its run, the others' the beginning of theirs
+    auto slot = [&](int w) { return (size_t)(2 * (w * g.group + member) + (w == first ? 1 : 0)) * 2 * RC + row; };
+    float M = -INFINITY;
+    for (int w = first + lane; w <= last; w += 32) M = fmaxf(M, part_ml[slot(w) * 2]);
+    M = warp_max(M);
 #pragma unroll 2
-  for (int w = g.first; w <= g.last; ++w) {
-    const size_t s = slot(w);
-    const float m = part_ml[s * 2], l = part_ml[s * 2 + 1];
-    float4 x[4];
+    for (int w = first + slice; w <= last; w += k) {
+      const size_t s = slot(w);
+      const float m = part_ml[s * 2], l = part_ml[s * 2 + 1];
+      float4 x[4];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) x[y] = load4(part + s * TL + 128 * y + 4 * lane);
-    const float f = m == -INFINITY ? (l == 0.f ? 0.f : l) : exp2f(m - M);  // l NaN: the row is NaN
-    L = fmaf(f, l, L);
+      for (int y = 0; y < 4; ++y) x[y] = load4(part + s * TL + 128 * y + 4 * lane);
+      const float f = m == -INFINITY ? (l == 0.f ? 0.f : l) : exp2f(m - M);  // l NaN: the row is NaN
+      L = fmaf(f, l, L);
 #pragma unroll
-    for (int y = 0; y < 4; ++y)
-      z[y].x = fmaf(f, x[y].x, z[y].x), z[y].y = fmaf(f, x[y].y, z[y].y), z[y].z = fmaf(f, x[y].z, z[y].z),
-      z[y].w = fmaf(f, x[y].w, z[y].w);
+      for (int y = 0; y < 4; ++y)
+        z[y].x = fmaf(f, x[y].x, z[y].x), z[y].y = fmaf(f, x[y].y, z[y].y), z[y].z = fmaf(f, x[y].z, z[y].z),
+        z[y].w = fmaf(f, x[y].w, z[y].w);
+    }
   }
-  const float r = L == 0.f ? 0.f : 1.f / L;
+  if (k > 1) {
+    if (slice > 0) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) *reinterpret_cast<float4 *>(&s_z[warp][128 * y + 4 * lane]) = z[y];
+      if (lane == 0) s_l[warp] = L;
+    }
+    __syncthreads();
+    if (slice > 0) return;
+    for (int w = warp + 1; w < warp + k; ++w) {
+      L += s_l[w];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float4 x = *reinterpret_cast<const float4 *>(&s_z[w][128 * y + 4 * lane]);
+        z[y].x += x.x, z[y].y += x.y, z[y].z += x.z, z[y].w += x.w;
+      }
+    }
+  }
+  if (row >= g.rows) return;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
   for (int y = 0; y < 4; ++y) {
-    const float4 v = make_float4(z[y].x * r, z[y].y * r, z[y].z * r, z[y].w * r);
+    const float4 v = make_float4(z[y].x * inv, z[y].y * inv, z[y].z * inv, z[y].w * inv);
     const int64_t at = ((int64_t)g.row0 + row) * TL + 128 * y + 4 * lane;
     if (a.z_bf16) store4(reinterpret_cast<bf16 *>(a.z) + at, v);
     else store4(reinterpret_cast<float *>(a.z) + at, v);
@@ -918,7 +949,7 @@ cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s
   e = cudaLaunchKernelEx(&cfg, tree_attn_kernel, a, maps, part, part_ml, merge);
   if (e != cudaSuccess) return e;
   ++*launches;
-  cfg.gridDim = dim3(clusters, 2 * RC / CROWS), cfg.blockDim = dim3(CNT), cfg.dynamicSmemBytes = 0;
+  cfg.gridDim = dim3(clusters, CY), cfg.blockDim = dim3(CNT), cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, tree_combine_kernel, a, (const float *)part, (const float *)part_ml, (const Merge *)merge);
   ++*launches;
   return e;

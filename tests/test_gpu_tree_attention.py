@@ -133,6 +133,14 @@ def test_split_long_contexts():
     case.check(case.run(torch.float32), torch.float32)
 
 
+@pytest.mark.parametrize("w", [2, 11])
+@pytest.mark.parametrize("length", [500, 760, 1100, 1900, 4300, 21000])
+def test_merges_of_few_and_many_parts(length, w):
+    """A sequence alone is cut into as many parts as it has tiles, up to one a worker."""
+    case = Case([length], [w], H=16, seed=150 + w)
+    case.check(case.run())
+
+
 def test_many_short_sequences():
     rng = np.random.default_rng(5)
     case = Case([int(x) for x in rng.integers(0, 90, 300)], [int(x) for x in rng.integers(0, 4, 300)], H=16, page=16,
