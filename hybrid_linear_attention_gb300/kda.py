@@ -624,10 +624,11 @@ def _paged(pool, page_table, lengths, n_seqs, dev):
     shape = pool.shape
     if len(shape) != 3 or shape[2] != 576:
         raise ValueError("pool: expected [n_pages, page_size, 576]")
-    if page_table.shape[0] < n_seqs or lengths.shape[0] < n_seqs:
+    rows, max_pages = page_table.shape
+    if rows < n_seqs or lengths.shape[0] < n_seqs:
         raise ValueError("page_table, lengths: fewer rows than sequences")
     return [_here(pool, torch.bfloat16, "pool", dev), shape[0], shape[1],
-            _here(page_table, torch.int32, "page_table", dev), page_table.shape[1],
+            _here(page_table, torch.int32, "page_table", dev), max_pages,
             _here(lengths, torch.int32, "lengths", dev)]
 
 
@@ -636,10 +637,11 @@ def _paged_layers(pool, page_table, lengths, n_seqs, dev):
     shape = pool.shape
     if len(shape) != 4 or shape[3] != 576:
         raise ValueError("pool: expected [n_layers, n_pages, page_size, 576]")
-    if page_table.shape[0] < n_seqs or lengths.shape[0] < n_seqs:
+    rows, max_pages = page_table.shape
+    if rows < n_seqs or lengths.shape[0] < n_seqs:
         raise ValueError("page_table, lengths: fewer rows than sequences")
     return [_here(pool, torch.bfloat16, "pool", dev), shape[0], shape[1], shape[2],
-            _here(page_table, torch.int32, "page_table", dev), page_table.shape[1],
+            _here(page_table, torch.int32, "page_table", dev), max_pages,
             _here(lengths, torch.int32, "lengths", dev)]
 
 
@@ -737,11 +739,11 @@ def mla_pages_workspace_size(n):
 
 def _book(refcount, page_table, held, lengths, dev):
     i32 = torch.int32
-    _shape(held, (page_table.shape[0],), "held")
-    _shape(lengths, (page_table.shape[0],), "lengths")
-    return [_here(refcount, i32, "refcount", dev), _here(page_table, i32, "page_table", dev),
-            page_table.shape[1], _here(held, i32, "held", dev), _here(lengths, i32, "lengths", dev),
-            page_table.shape[0]]
+    n_slots, max_pages = page_table.shape
+    if held.shape != (n_slots,) or lengths.shape != (n_slots,):
+        raise ValueError(f"held, lengths: expected shape [{n_slots}]")
+    return (_here(refcount, i32, "refcount", dev), _here(page_table, i32, "page_table", dev),
+            max_pages, _here(held, i32, "held", dev), _here(lengths, i32, "lengths", dev), n_slots)
 
 
 def mla_pages_free(refcount, page_table, held, lengths, slots, *, stream=None):
