@@ -17,6 +17,7 @@
 // replayed afterwards (tree_accept_kernel), which reads and writes the state once.
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "kda_tc_ptx.cuh"
 
 #include <atomic>
 
@@ -541,28 +542,75 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
 // of columns 16 w + 4 cq .. + 3, so a column's sum over the key rows closes inside its warp, and once
 // the tokens are staged in shared memory (k normalised, v, retention, strength) the warps need
 // nothing from each other.  A CTA takes `group` heads of a sequence at a time and stages all their
-// tokens together: the path is worked out once, and the warps go through the heads' states without
-// a barrier.  Bound by the state's bytes, read and written: 443 us for 256 sequences x 64 heads x 3.2
-// tokens, 5.1 TB/s (without the next group's inputs asked of L2 473; two CTAs of eight warps an SM are
-// what the registers hold, and they do not hide all of the staging).
+// tokens together: the path is worked out once.  The next head's state comes into shared memory by bulk
+// copies from when this one's is in registers.  Bound by the state's bytes, read and written: 409 us for
+// 256 sequences x 64 heads x 3.2 tokens, 5.5 TB/s (443 with the next state only asked of L2; without the
+// next group's inputs asked of L2 457; two CTAs of eight warps an SM are what the registers hold, and they
+// do not hide all of the staging).
 constexpr int AT = 8;  // path tokens staged at a time; a longer path goes head by head
+// its shared memory: the staged tokens, then the next head's state, in eight parts (a lane group's rows each)
+// 64 bytes apart, so that a quarter of a warp reads 128 bytes of different banks
 template <int D>
+__host__ __device__ constexpr size_t accept_tokens(int group) {
+  return ((size_t)group * AT * (3 * D + 1) * sizeof(float) + 127) / 128 * 128;
+}
+template <int D, typename ST>
+__host__ __device__ constexpr size_t accept_part() {
+  return (size_t)D / 8 * D * sizeof(ST) + 64;
+}
+template <int D, typename ST>
 constexpr size_t accept_smem(int group) {
-  return (size_t)group * AT * (3 * D + 1) * sizeof(float);
+  return accept_tokens<D>(group) + 8 * accept_part<D, ST>();
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
 }
 template <int D, typename IO, typename ST>
 __global__ void __launch_bounds__(2 * D, 2) tree_accept_kernel(const TreeArgs a, int group) {
   constexpr int NT = 2 * D, R = D / 8;
   extern __shared__ __align__(16) float smem[];
   __shared__ int s_par[64], s_path[64], s_m;
+  __shared__ __align__(8) uint64_t s_bar;
   // [head of the group][token][k | v | retention][D], then the strengths
   float *s_beta = smem + (size_t)group * AT * 3 * D;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cq = lane & 3, rg = lane >> 2, col = 16 * warp + 4 * cq;
+  const uint32_t bar = tc::smem_u32(&s_bar);
+  uint8_t *s_state = reinterpret_cast<uint8_t *>(smem) + accept_tokens<D>(group);
+  if (tid == 0) {
+    tc::mbar_init(bar, 1);
+    tc::mbar_fence_init();
+  }
+  __syncthreads();
   after_previous();
   const int H = a.H;
   const uint32_t groups = (uint32_t)a.n_seqs * (uint32_t)H / group;  // at most 65535 x 21845
   const size_t C = (size_t)3 * H * D;
+
+  // the state of head h of slot `slot` on its way into shared memory (by one thread)
+  auto load_state = [&](int slot, int h) {
+    constexpr uint32_t bytes = D / 8 * D * sizeof(ST);
+    const uint8_t *src = reinterpret_cast<const uint8_t *>(a.state) + ((size_t)slot * H + h) * (8 * (size_t)bytes);
+    tc::mbar_expect_tx(bar, 8 * bytes);
+    for (int y = 0; y < 8; ++y)
+      bulk_load(tc::smem_u32(s_state) + y * (uint32_t)accept_part<D, ST>(), src + y * bytes, bytes, bar);
+  };
+  // the same of the first group from `unit` on that has something to accept
+  auto load_from = [&](uint32_t unit) {
+    for (; unit < groups; unit += gridDim.x) {
+      const int h = (int)(unit * group % H), n = (int)(unit * group / H), slot = a.slot_idx ? a.slot_idx[n] : n;
+      int row0;
+      const int W = tree_nodes(a, n, 64, row0, false), last = a.accept[n];
+      if (slot >= 0 && slot < a.n_slots && last >= 0 && last < W) {
+        load_state(slot, h);
+        return;
+      }
+    }
+  };
+  if (tid == 0) load_from(blockIdx.x);
+  uint32_t loads = 0;
 
   for (uint32_t unit = blockIdx.x; unit < groups; unit += gridDim.x) {
     const int h0 = (int)(unit * group % H), n = (int)(unit * group / H);
@@ -576,7 +624,6 @@ __global__ void __launch_bounds__(2 * D, 2) tree_accept_kernel(const TreeArgs a,
     }
     if (last < 0) continue;  // nothing accepted: state and tail stay
     ST *state = reinterpret_cast<ST *>(a.state) + ((size_t)slot * H + h0) * (size_t)D * D;
-    if (unit == blockIdx.x && tid == 0) ask_bulk(state, sizeof(ST) * D * D);
     __syncthreads();  // the previous group's shared memory has been read
     for (int i = tid; i <= last; i += NT) {
       int p = a.parent[row0 + i];
@@ -637,20 +684,27 @@ __global__ void __launch_bounds__(2 * D, 2) tree_accept_kernel(const TreeArgs a,
     for (int y = 0; y < group; ++y) {
       ST *st = state + (size_t)y * D * D + col;
       float S[R][4];
+      const bool here = tc::mbar_wait(bar, loads++ & 1);
+      const ST *from = reinterpret_cast<const ST *>(s_state + rg * accept_part<D, ST>()) + col;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float4 x = load4_stream(st + (size_t)(R * rg + r) * D);
+        const float4 x = load4(from + r * D);
         S[r][0] = x.x, S[r][1] = x.y, S[r][2] = x.z, S[r][3] = x.w;
       }
+      if (!__syncthreads_and(here)) {  // did not come: nothing is written
+        if (tid == 0 && a.err) atomicOr(a.err, ERR_MBAR_TIMEOUT);
+        for (int w = 0; w < 100; ++w) __nanosleep(10000);  // let the copies in flight land
+        return;
+      }
       if (y + 1 < group) {
-        if (tid == 0) ask_bulk(state + (size_t)(y + 1) * D * D, sizeof(ST) * D * D);
+        if (tid == 0) load_state(slot, h0 + y + 1);
       } else if (unit + gridDim.x < groups) {  // the next group's first head
+        if (tid == 0) load_from(unit + gridDim.x);
         const uint32_t nu = (unit + gridDim.x) * group;
         const int nn = (int)(nu / H), ns = a.slot_idx ? a.slot_idx[nn] : nn;
         int nrow0;
         const int nw = tree_nodes(a, nn, 64, nrow0, false), nl = a.accept[nn];
         if (ns >= 0 && ns < a.n_slots && nl >= 0 && nl < nw) {
-          if (tid == 0) ask_bulk(reinterpret_cast<const ST *>(a.state) + ((size_t)ns * H + nu % H) * (size_t)D * D, sizeof(ST) * D * D);
           if (group == 2) ask_inputs<D, IO, 2, 1>(a, nrow0, nl + 1, ns, (int)(nu % H), tid, NT);
           else ask_inputs<D, IO, 1, 1>(a, nrow0, nl + 1, ns, (int)(nu % H), tid, NT);
         }
@@ -756,13 +810,13 @@ cudaError_t launch_typed(const TreeArgs &a, bool accept, cudaStream_t s) {
   int64_t fit = 0;
   if (accept) {
     constexpr auto kernel = tree_accept_kernel<D, IO, ST>;
-    cudaError_t e = fitting<kernel>(2 * D, accept_smem<D>(2), accept_smem<D>(2), &fit);
+    cudaError_t e = fitting<kernel>(2 * D, accept_smem<D, ST>(2), accept_smem<D, ST>(2), &fit);
     if (e != cudaSuccess) return e;
     // two heads staged together where that leaves every CTA several groups (measured at 256 sequences
-    // x 64 heads: 568 us one head at a time, 468 two, 505 four, whose paths differ too much in length)
+    // x 64 heads: 470 us one head at a time, 409 two, 453 four)
     const int group = a.H % 2 == 0 && units / 2 >= 4 * fit ? 2 : 1;
     const int64_t groups = units / group;
-    return launch(kernel, groups < fit ? groups : fit, 2 * D, accept_smem<D>(group), s, a, group);
+    return launch(kernel, groups < fit ? groups : fit, 2 * D, accept_smem<D, ST>(group), s, a, group);
   } else {
     constexpr bool staged = sizeof(IO) == 2;
     const size_t smem = verify_smem_floats(a.max_nodes, D, staged) * sizeof(float);
