@@ -478,20 +478,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         const bool ok = warp_wait(B_TAIL + j, (looked >> j) & 1);
         looked ^= 1u << j;
         uint8_t *slot = sm + OFF_Z + j * SLOT;
-        const int piece = lane & 15;
-        // two rows at a time, 16 lanes each
-        for (int r0 = len > g0 ? len - g0 : 0; r0 < 64; r0 += 2) {
-          const int r = r0 + (lane >> 4);
-          uint4 *at = reinterpret_cast<uint4 *>(slot + (piece >> 3) * 8192 + (r & 63) * 128 + (((piece & 7) ^ (r & 7)) << 4));
-          bool bad = false;
-          if (g0 + r0 < end) {
-            auto odd = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
-            const uint4 v = *at;
-            bad = odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w);
+        const int piece = lane & 15, half = lane >> 4;  // 16 lanes a row
+        uint8_t *column = slot + (piece >> 3) * 8192;
+        auto place = [&](int r) { return reinterpret_cast<uint4 *>(column + r * 128 + (((piece & 7) ^ (r & 7)) << 4)); };
+        auto odd = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
+        const int first = len > g0 ? len - g0 : 0, stop = end - g0 < 64 ? end - g0 : 64;  // drafted rows
+        const uint32_t row_lanes = lane < 16 ? 0xffffu : 0xffff0000u;
+        for (int r0 = first; r0 < stop; r0 += 8) {  // eight of them at a time
+          uint4 v[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) v[y] = *place((r0 + 2 * y + half) & 63);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int r = r0 + 2 * y + half;
+            const bool bad = odd(v[y].x) || odd(v[y].y) || odd(v[y].z) || odd(v[y].w);
+            if ((__ballot_sync(0xffffffffu, bad) & row_lanes) && r < stop) *place(r) = make_uint4(0, 0, 0, 0);
           }
-          const uint32_t any = __ballot_sync(0xffffffffu, bad) & (lane < 16 ? 0xffffu : 0xffff0000u);
-          if (r < 64 && (any || g0 + r >= end)) *at = make_uint4(0, 0, 0, 0);
         }
+#pragma unroll 4
+        for (int r = stop + half; r < 64; r += 2) *place(r) = make_uint4(0, 0, 0, 0);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0 && ok) arrive_pair(map_shared_rank(bar(B_FULL_Z + j), 0));
