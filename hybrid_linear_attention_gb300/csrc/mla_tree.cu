@@ -31,7 +31,7 @@
 // 4 sequences x 11 to 16 nodes x 65536 positions 266 us, 1.60 PFLOP/s, 83 % of the measured bf16 peak.
 // The rings' depth is what that rate needs: a slot less in either costs 11 to 35 %, one more (weights of
 // 128 positions at a time) gives back only what the smaller place for the weights costs.  With one node a
-// sequence the same loop streams the cache: 256 sequences of up to 4096 positions 200 us, 4.7 TB/s
+// sequence the same loop streams the cache: 256 sequences of 2048 to 4096 positions 197 us, 4.8 TB/s
 // (asking L2 for coming tiles, by bulk prefetches or by threads, measured slower: 247 to 272 us).
 //
 // Work is dealt in tiles of 256 positions: clusters form groups of G that take G row tiles of a
@@ -462,7 +462,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     // ---- the queries of a segment, and the chunks of Z's operand that reach past the cached
     //      positions: rows behind the last drafted node and drafted rows with a value that is not
     //      finite become zeros there before the products may use them (their weight is 0 or NaN,
-    //      and 0 x NaN must not reach the rows that do not see them).
+    //      and 0 x NaN must not reach the rows that do not see them).  In short contexts every other
+    //      tile waits for this: eight rows' reads at a time (two took 194 us for 155 sequences x 25 nodes
+    //      x 32 heads, 526 positions, now 173).
     const uint32_t qfull0 = map_shared_rank(bar(B_QFULL), 0);
     int segs = 0, j0 = 0;      // the tile's first value slot
     uint32_t looked = 0;       // parity of B_TAIL + j
