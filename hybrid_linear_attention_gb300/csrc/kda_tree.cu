@@ -13,8 +13,13 @@
 //     o_i = scale (S^T (q_i e^{G_i}) + sum_{j in anc(i) + i} B_ij u_j)
 //     A_ij = sum_c k_ic k_jc e^{G_ic - G_jc},  B_ij = sum_c q_ic k_jc e^{G_ic - G_jc}
 // so the 64 KB state of a (sequence, head) is read once for the whole tree and no node's state
-// is ever stored; every exponent is a sum of log-retentions, at most 0.  The accepted path is
-// replayed afterwards (tree_accept_kernel), which reads and writes the state once.
+// is ever stored; every exponent is a sum of log-retentions, at most 0.  A G behind a past that was
+// forgotten is large (64 nodes at the clamp -5: 462 as a power of two), and the small retentions of later
+// nodes would be rounded at its size and come out of G_i - G_j wrong (up to 1e-2 of an output with g_min
+// near -88).  So G is kept as F - 16 - 32 N, F in fp32 within -16 .. 16 and N a whole number up to 255: a step
+// is rounded by 2^-21 at most (half an fp32 step below 16), whatever lies before it, N_i - N_j is exact, and down
+// to G = -32 N is 0.  The accepted path is replayed afterwards (tree_accept_kernel), which reads and writes the
+// state once.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "kda_tc_ptx.cuh"
@@ -148,22 +153,37 @@ __device__ __forceinline__ void ask_inputs(const TreeArgs &a, int row0, int rows
 }
 
 // shared memory of the verify kernel for at most W nodes (floats): k over q [2 W, whole tiles of
-// 16][D + 4], v, G (then S^T k) [W][D] each, then S^T q [W][D] and A and B of the pairs, which take the
-// place of the raw inputs [W + 3][3 D] where those are staged (bf16); the list of the pairs (node, itself or
-// an ancestor), 16 bits each
+// 16][D + 4], v, F (then S^T k) [W][D] each, the taps [W][4] and N (bytes) [W][D], then S^T q [W][D] and A and B
+// of the pairs, which take the place of the raw inputs [W + 3][3 D] where those are staged (bf16); parents,
+// first pairs [W + 1], strengths and norms [2 W]; the list of the pairs (node, itself or an ancestor), 16 bits each
 __host__ __device__ constexpr size_t verify_pairs(int W) { return (size_t)W * (W + 1) / 2; }
 __host__ __device__ constexpr size_t verify_late_floats(int W, int D, bool staged) {
   const size_t late = (size_t)W * D + 2 * verify_pairs(W), raw = staged ? ((size_t)(W + 3) * 3 * D + 1) / 2 : 0;
   return late > raw ? late : raw;
 }
 __host__ __device__ constexpr size_t verify_smem_floats(int W, int D, bool staged) {
-  const size_t all = (size_t)((2 * W + 15) / 16 * 16) * (D + 4) + (size_t)2 * W * D + verify_late_floats(W, D, staged) +
-                     (verify_pairs(W) + 1) / 2;
+  const size_t all = (size_t)((2 * W + 15) / 16 * 16) * (D + 4) + (size_t)2 * W * D + (size_t)W * (4 + D / 4) +
+                     verify_late_floats(W, D, staged) + (size_t)5 * W + 1 + (verify_pairs(W) + 1) / 2;
   return (all + 3) / 4 * 4;  // what follows starts on 16 bytes
 }
 __device__ __forceinline__ void copy_async16(void *smem, const void *global) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global)
                : "memory");
+}
+
+// F + 32 n for the n that brings F to -16 or above; returns n, at most 4 at a step (a retention of 0 counts as
+// 2^-127)
+constexpr float F_TOP = 16.f;
+__device__ __forceinline__ uint32_t wrap(float &f) {
+  const float n = fmaxf(floorf(fmaf(f, -0.03125f, 0.5f)), 0.f);
+  f = fmaf(n, 32.f, f);
+  return (uint32_t)n;
+}
+// f - 32 n of four channels, n in bytes
+__device__ __forceinline__ float4 unwrap(float4 f, uint32_t n) {
+  auto whole = [&](uint32_t which) { return __uint_as_float(__byte_perm(n, 0x4b000000u, which)) - 8388608.f; };  // 2^23 + byte
+  return make_float4(fmaf(whole(0x7540), -32.f, f.x), fmaf(whole(0x7541), -32.f, f.y), fmaf(whole(0x7542), -32.f, f.z),
+                     fmaf(whole(0x7543), -32.f, f.w));
 }
 
 // columns of the state that a warp of the verify kernel owns, and its threads: four warps of 32
@@ -216,8 +236,9 @@ constexpr size_t resident_floats() {
 // that run while the tree is worked out.
 // RESIDENT: with few units (no more than fit at a time) the state comes into shared memory the same
 // way, all at once; read step by step from L2 it would be most of a lone unit's time (one sequence x
-// 12 nodes x 64 heads: 19.7 us so, 16.2 resident, before the pairs were listed; 13.7 since).
-// Measured at 256 sequences x 6 to 8 nodes x 64 heads: 318 us, 4.2 TB/s of what it must move.  What is
+// 12 nodes x 64 heads: 19.7 us so, 16.2 resident, before the pairs were listed; 14.4 since).
+// Measured at 256 sequences x 6 to 8 nodes x 64 heads: 323 us, 4.1 TB/s of what it must move (318 with G as one
+// fp32 sum; a tree of 16 nodes 421 for 407, of 64, where most pairs reach past G = -32, 1421 for 1261).  What is
 // not the state's product takes 186 us on its own (issue and the latencies of its short phases), the
 // product's loads from L2 most of the rest: more CTAs hide more of both (seven an SM 334 us, six 346, nine
 // spill: 356), which is also why deeper loads cost more than they give (two steps of the state in flight
@@ -229,14 +250,15 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
   constexpr int CT = 3 * D / 4;  // threads of the convolution, four channels each
   constexpr bool EXACT = sizeof(IO) == 4;
   extern __shared__ __align__(16) float smem[];
-  __shared__ int s_par[64];
-  __shared__ __align__(16) int s_tap[64][4];  // a node's taps, oldest first: nodes, or -1 (newest) .. -3 of the tail
-  __shared__ int s_off[65];  // the pairs of node i: s_off[i] .. s_off[i + 1] - 1, itself first
-  __shared__ float s_beta[64], s_rn[128];
   const int WM = a.max_nodes;
-  float *s_x = smem, *s_v = s_x + (2 * WM + 15) / 16 * 16 * XS, *s_g = s_v + WM * D, *s_o = s_g + WM * D,
-        *s_A = s_o + WM * D, *s_B = s_A + verify_pairs(WM);
-  uint16_t *s_pair = reinterpret_cast<uint16_t *>(s_o + verify_late_floats(WM, D, !EXACT));  // node << 6 | ancestor
+  float *s_x = smem, *s_v = s_x + (2 * WM + 15) / 16 * 16 * XS, *s_g = s_v + WM * D;
+  int4 *s_tap = reinterpret_cast<int4 *>(s_g + WM * D);  // a node's taps, oldest first: nodes, or -1 (newest) .. -3 of the tail
+  uint32_t *s_n = reinterpret_cast<uint32_t *>(s_tap + WM);  // N of G, four channels a word
+  float *s_o = reinterpret_cast<float *>(s_n + WM * (D / 4)), *s_A = s_o + WM * D, *s_B = s_A + verify_pairs(WM);
+  int *s_par = reinterpret_cast<int *>(s_o + verify_late_floats(WM, D, !EXACT));
+  int *s_off = s_par + WM;  // the pairs of node i: s_off[i] .. s_off[i + 1] - 1, itself first
+  float *s_beta = reinterpret_cast<float *>(s_off + WM + 1), *s_rn = s_beta + WM;
+  uint16_t *s_pair = reinterpret_cast<uint16_t *>(s_rn + 2 * WM);  // node << 6 | ancestor
   IO *s_raw = reinterpret_cast<IO *>(s_o);  // row 3 + i: node i, rows 0 .. 2 the tail
   constexpr int SS = D + 16 / (int)sizeof(ST);
   ST *s_S = reinterpret_cast<ST *>(smem + verify_smem_floats(WM, D, !EXACT));
@@ -289,12 +311,13 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
     }
     __syncthreads();
     for (int i = tid; i < W; i += NT) {
-      int u = i;
+      int u = i, tap[4];
 #pragma unroll
       for (int y = 3; y >= 0; --y) {
-        s_tap[i][y] = u;
+        tap[y] = u;
         u = u >= 0 ? s_par[u] : (u > -3 ? u - 1 : -3);
       }
+      s_tap[i] = make_int4(tap[0], tap[1], tap[2], tap[3]);
     }
     if (warp == 0)
       for (int i0 = 0, base = 0; i0 < W; i0 += 32) {
@@ -322,6 +345,7 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
     // ---- q, k, v of every node after the convolution along its path (a thread four channels of a
     //      stream), beside them the retentions summed along the paths (the other threads, four
     //      channels each), as powers of two
+    uint32_t past = 0;
     if (tid < CT) {
       const int c4 = tid % (D / 4), st = tid / (D / 4);
       const size_t ch = (size_t)st * H * D + (size_t)h * D + 4 * c4;
@@ -331,7 +355,7 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
       const int ld = st == 2 ? D : XS;
       const IO *raw = s_raw + 9 * D + st * D + 4 * c4;
       for (int i = 0; i < W; ++i, dst += ld) {
-        const int4 tap = *reinterpret_cast<const int4 *>(s_tap[i]);
+        const int4 tap = s_tap[i];
         auto at = [&](int j) { return EXACT ? load4(tap_row<IO>(a, row0, slot, j, C) + ch) : load4(raw + j * 3 * D); };
         *reinterpret_cast<float4 *>(dst) = cw(at(tap.x), at(tap.y), at(tap.z), at(tap.w));
       }
@@ -342,11 +366,15 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
         const int p = s_par[i];
         float4 y = make_float4(fmaxf(x.x, a.g_min) * LOG2E, fmaxf(x.y, a.g_min) * LOG2E, fmaxf(x.z, a.g_min) * LOG2E,
                                fmaxf(x.w, a.g_min) * LOG2E);
-        if (p >= 0) {
-          const float4 z = *reinterpret_cast<const float4 *>(s_g + p * D + c);
-          y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
-        }
+        float4 z = make_float4(F_TOP, F_TOP, F_TOP, F_TOP);
+        uint32_t n = 0;
+        if (p >= 0) z = *reinterpret_cast<const float4 *>(s_g + p * D + c), n = s_n[(p * D + c) / 4];
+        y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+        if (fminf(fminf(y.x, y.y), fminf(y.z, y.w)) < -16.f)
+          n += wrap(y.x) | wrap(y.y) << 8 | wrap(y.z) << 16 | wrap(y.w) << 24;  // no byte passes 255
         *reinterpret_cast<float4 *>(s_g + i * D + c) = y;
+        s_n[(i * D + c) / 4] = n;
+        past |= n;
       }
     }
     if (unit + gridDim.x < units) {  // the next unit's inputs
@@ -356,7 +384,7 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
       const int nw = tree_nodes(a, nn, WM, nrow0, false);
       if (ns >= 0 && ns < a.n_slots && nw > 0) ask_inputs<D, IO, 1, 0>(a, nrow0, nw, ns, (int)(nu % H), tid, NT);
     }
-    __syncthreads();
+    const bool deep = __syncthreads_or(past);  // is there an N that is not 0
     // ---- the norms of k and q (eight lanes a row), kept as factors
     for (int x = tid >> 3; x < 2 * W; x += NT / 8) {
       float ss = 0.f;
@@ -386,8 +414,12 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
             const float4 kj = *reinterpret_cast<const float4 *>(s_x + j * XS + c),
                          ki = *reinterpret_cast<const float4 *>(s_x + i * XS + c),
                          qi = *reinterpret_cast<const float4 *>(s_x + (W + i) * XS + c);
-            const float e0 = ex2_(gi.x - gj.x) * kj.x, e1 = ex2_(gi.y - gj.y) * kj.y, e2 = ex2_(gi.z - gj.z) * kj.z,
-                        e3 = ex2_(gi.w - gj.w) * kj.w;
+            float4 d = make_float4(gi.x - gj.x, gi.y - gj.y, gi.z - gj.z, gi.w - gj.w);
+            if (deep) {
+              const uint32_t n = s_n[(i * D + c) / 4] - s_n[(j * D + c) / 4];  // N rises along a path: no borrow
+              if (n) d = unwrap(d, n);
+            }
+            const float e0 = ex2_(d.x) * kj.x, e1 = ex2_(d.y) * kj.y, e2 = ex2_(d.z) * kj.z, e3 = ex2_(d.w) * kj.w;
             pa = fmaf(ki.x, e0, fmaf(ki.y, e1, fmaf(ki.z, e2, fmaf(ki.w, e3, pa))));
             pb = fmaf(qi.x, e0, fmaf(qi.y, e1, fmaf(qi.z, e2, fmaf(qi.w, e3, pb))));
           }
@@ -408,14 +440,16 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
     // ---- X = k e^G over q e^G, a warp a row; with bf16 I/O as [D] high parts, then [D] low parts
     for (int x = warp; x < 2 * W; x += NW) {
       float *row = s_x + x * XS;
-      const float *G = s_g + (x < W ? x : x - W) * D;
+      const int node = x < W ? x : x - W;
       const float rn = s_rn[x];
       const int c = 4 * lane;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c < D) {
-        const float4 e = *reinterpret_cast<const float4 *>(G + c);
+        float4 e = *reinterpret_cast<const float4 *>(s_g + node * D + c);
+        if (deep) e = unwrap(e, s_n[(node * D + c) / 4]);
         y = *reinterpret_cast<const float4 *>(row + c);
-        y.x *= ex2_(e.x) * rn, y.y *= ex2_(e.y) * rn, y.z *= ex2_(e.z) * rn, y.w *= ex2_(e.w) * rn;
+        y.x *= ex2_(e.x - F_TOP) * rn, y.y *= ex2_(e.y - F_TOP) * rn, y.z *= ex2_(e.z - F_TOP) * rn,
+            y.w *= ex2_(e.w - F_TOP) * rn;
       }
       if (EXACT) {
         if (c < D) *reinterpret_cast<float4 *>(row + c) = y;

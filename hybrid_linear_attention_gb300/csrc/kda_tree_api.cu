@@ -104,7 +104,7 @@ kda_status kda_tree_verify(const kda_params *p, const void *x_raw, const void *c
                               total_nodes);
   a.max_nodes = max_nodes;
   // e^g below the normal fp32 range (2^-126) counts as 0: the kernel takes differences of sums of g along
-  // a path, which would be NaN of two infinities and drown a later node's g behind a huge one
+  // a path, which would be NaN of two infinities, and counts their multiples of 32 (64 nodes x 127.1 / 32) in a byte
   if (a.g_min < -88.1f) a.g_min = -88.1f;
   a.gate = gate_logit, a.norm_w = norm_w, a.out = out;
   return done(kda::launch_tree(a, false, p->d_k, p->io_dtype == KDA_BF16, p->state_dtype == KDA_BF16, stream), 1);

@@ -243,3 +243,38 @@ def test_captured_verify_and_accept_replay():
     assert out_error(out, want) <= tol(p)
     assert np.abs(keep["state"].double().cpu().numpy() - state).max() <= 1e-4 * np.sqrt((state ** 2).mean())
     assert np.array_equal(keep["conv_state"].double().cpu().numpy(), tail)
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("forget,nodes", [(-5.0, 8), (-5.0, 40), (-88.0, 11), (-88.0, 40)])
+@pytest.mark.parametrize("d", [16, 128])
+def test_verify_retains_after_forgetting(d, forget, nodes, io, gated):
+    """A chain of 64 that forgets strongly for some nodes and then hardly at all.  The log-retentions'
+    sum is held to 2^-21 a step (half a step of fp32 below 2^4), so a decay over 56 steps is off by at
+    most 56 * 2^-21 * ln 2 = 1.9e-5 of itself, wherever on the path the steps are."""
+    p = kda.params(H=2, d=d, io_dtype=io, g_min=forget)
+    m = make([64, 50], 2, d, seed=306, chain=True, io=io)
+    for lo in (0, 64):
+        m["g"][lo:lo + nodes] = forget
+        m["g"][lo + nodes:] = -0.013
+    want = ref.kda_tree(m["x"], m["conv_w"], m["conv_state"], m["g"], m["beta"], m["state"], m["slots"], m["cu"],
+                        m["parent"], H=2, d=d, gate=m["gate"] if gated else None,
+                        norm_w=m["norm_w"] if gated else None, g_min=forget)[0]
+    assert out_error(verify(m, p, gated=gated), want) <= tol(p)
+    kda.kda_check_device_error()
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+def test_verify_deep_trees_of_mixed_retentions(io):
+    """Channels that forget at different nodes of a branching tree, some at every other node."""
+    p = kda.params(H=3, io_dtype=io, g_min=-float("inf"))
+    m = make([64, 33, 5], 3, 128, seed=307, io=io)
+    g = torch.Generator().manual_seed(308)
+    kind = torch.randint(0, 6, m["g"].shape, generator=g)
+    kind[:, :, ::3] = 5
+    m["g"] = torch.tensor([-0.01, -0.3, -7.0, -40.0, -88.0, -0.02])[kind].contiguous()
+    want = ref.kda_tree(m["x"], m["conv_w"], m["conv_state"], m["g"], m["beta"], m["state"], m["slots"], m["cu"],
+                        m["parent"], H=3, d=128, gate=m["gate"], norm_w=m["norm_w"], g_min=-float("inf"))[0]
+    assert out_error(verify(m, p), want) <= tol(p)
+    kda.kda_check_device_error()
