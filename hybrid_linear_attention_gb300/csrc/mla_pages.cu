@@ -105,12 +105,13 @@ __global__ void __launch_bounds__(AP_NT) cache_append_kernel(const PagedCache c,
 
 // The accepted path's rows moved up to lengths[n], lengths[n] + 1, ..: step d of the path is
 // node path[d] >= d, so a thread that takes the steps in order never overwrites a row that one
-// of its later steps still has to read.
+// of its later steps still has to read.  The pages of all drafted positions are looked up beside the
+// parents: a path that needs one that is not there is refused whole, before a row is moved.
 constexpr int AC_LAYERS = 9, AC_NT = AC_LAYERS * ROW16;
 __global__ void __launch_bounds__(AC_NT)
     cache_accept_kernel(const PagedCache c, const int32_t *cu, int64_t total, const int32_t *parent,
                         const int32_t *accept, int32_t *new_lengths) {
-  __shared__ int s_par[64], s_path[64], s_m;
+  __shared__ int s_par[64], s_path[64], s_page[64], s_m;
   after_previous();
   const int n = blockIdx.x, tid = threadIdx.x;
   const int lo = cu[n], hi = cu[n + 1], last = accept[n], len = c.lengths[n];
@@ -129,13 +130,18 @@ __global__ void __launch_bounds__(AC_NT)
       p = -1;
     }
     s_par[i] = p;
+    s_page[i] = page_of(c, n, (int64_t)len + i);
   }
   __syncthreads();
   if (tid == 0) {
-    int m = 0;
-    for (int j = nodes - 1; j >= 0; j = s_par[j]) ++m;
-    s_m = m;
-    for (int j = nodes - 1; j >= 0; j = s_par[j]) s_path[--m] = j;
+    int steps = 0, missing = 0;
+    for (int j = nodes - 1; j >= 0; j = s_par[j]) ++steps;
+    for (int j = nodes - 1, d = steps; j >= 0; j = s_par[j]) {
+      s_path[--d] = j;
+      missing |= s_page[j] | s_page[d];  // a page that is not there is -1
+    }
+    s_m = missing < 0 ? 0 : steps;
+    if (missing < 0) flag(c.err, ERR_BAD_INDEX);
   }
   __syncthreads();
   const int m = s_m, piece = tid % ROW16;
@@ -144,24 +150,15 @@ __global__ void __launch_bounds__(AC_NT)
   for (int l = tid / ROW16; l < c.n_layers; l += AC_LAYERS)
     for (int d0 = same; d0 < m; d0 += 8) {
       uint4 x[8];
-      int to[8];
-#pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        to[y] = -1;
-        if (d0 + y < m) {
-          const int64_t a = (int64_t)len + s_path[d0 + y], b = (int64_t)len + d0 + y;
-          const int pa = page_of(c, n, a), pb = page_of(c, n, b);
-          if (pa >= 0 && pb >= 0) {
-            x[y] = pool_row(c, l, pa, (int)(a % c.page_size))[piece];
-            to[y] = pb;
-          } else if (piece == 0 && l == 0) {
-            flag(c.err, ERR_BAD_INDEX);
-          }
-        }
-      }
 #pragma unroll
       for (int y = 0; y < 8; ++y)
-        if (to[y] >= 0) pool_row(c, l, to[y], (int)(((int64_t)len + d0 + y) % c.page_size))[piece] = x[y];
+        if (d0 + y < m) {
+          const int from = s_path[d0 + y];
+          x[y] = pool_row(c, l, s_page[from], (len + from) % c.page_size)[piece];
+        }
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        if (d0 + y < m) pool_row(c, l, s_page[d0 + y], (len + d0 + y) % c.page_size)[piece] = x[y];
     }
   if (tid == 0) new_lengths[n] = ok ? len + m : len;
 }

@@ -137,8 +137,9 @@ kda_status mla_cache_append(void* pool, int n_layers, int n_pages, int page_size
  * every layer, and new_lengths[n] = lengths[n] + steps on the path.
  *   cu_nodes, parent, accept_node as kda_tree_accept (-1 accepts nothing);  new_lengths [n_seqs]
  *   int32 output, may be `lengths`.
- * Bit-exact moves.  A sequence with bad offsets, more than 64 nodes, or an accept_node outside -1
- * .. nodes - 1 keeps its rows and length and is reported, as is a position without a page.
+ * Bit-exact moves.  A sequence with bad offsets, more than 64 nodes, an accept_node outside -1 ..
+ * nodes - 1, or a path on which a node's position or the one that it moves to has no page keeps its rows
+ * and length and is reported.
  */
 kda_status mla_cache_accept(void* pool, int n_layers, int n_pages, int page_size,
                             const int32_t* page_table, int max_pages, const int32_t* lengths,

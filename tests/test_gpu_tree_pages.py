@@ -308,3 +308,32 @@ def test_a_verification_step_as_a_server_runs_it():
                 b.pool[:, b.model.table[i][t // page], t % page] = rows[:, m["cu"][i] + j]
             b.model.lengths[i] += len(path)
         b.same()
+
+
+@pytest.mark.parametrize("layers", [1, 11])
+def test_accept_over_a_missing_page_keeps_rows_and_length(layers):
+    """Pages of 16, lengths 14: nodes 0 and 1 on the sequence's first page, the others on its second.
+    Sequence 0 a chain over a page that is not there, 1 a path whose source page alone is missing,
+    2 a path that moves rows onto a missing page, 3 and 4 as they should be, 5 no path at all."""
+    _gpu.lib()
+    g = torch.Generator().manual_seed(61)
+    pool = torch.randn(layers, 16, 16, 576, generator=g).to(torch.bfloat16)
+    table = [[0, -1, 1], [2, 99, 3], [-1, 4, 5], [6, 7, 8], [9, 10, 11], [12, -1, -1]]
+    parents = [[-1, 0, 1, 2], [-1, 0, 1, 0], [-1, -1, 1, 2], [-1, 0, 0, 2], [-1, 0, 1, 2], [-1, 0, 1, 2]]
+    accept, lengths = [3, 3, 3, 3, 3, -1], [14] * 6
+    want, new = pool.clone(), list(lengths)
+    for b in (3, 4):
+        path = ref.path_to(parents[b], accept[b])
+        for d, i in enumerate(path):
+            (p, r), (p0, r0) = ((table[b][(14 + x) // 16], (14 + x) % 16) for x in (d, i))
+            want[:, p, r] = pool[:, p0, r0]
+        new[b] += len(path)
+    d_pool, out = pool.cuda(), ref.i32([-7] * 6)
+    kda.mla_cache_accept(d_pool, ref.i32(table), ref.i32(lengths), ref.i32([0, 4, 8, 12, 16, 20, 24]),
+                         ref.i32([p for q in parents for p in q]), ref.i32(accept), out)
+    assert status() == kda.KDA_ERR_BAD_INDEX
+    assert out.tolist() == new and torch.equal(d_pool.cpu(), want)
+    # a plain chain over a missing page alone is told of too
+    kda.mla_cache_accept(d_pool, ref.i32(table[:1]), ref.i32([14]), ref.i32([0, 4]), ref.i32(parents[0]), ref.i32([2]), out)
+    assert status() == kda.KDA_ERR_BAD_INDEX
+    assert out.tolist()[0] == 14 and torch.equal(d_pool.cpu(), want)
