@@ -387,16 +387,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       if (rank == 0) mbar_expect_tx(bar(full + j), 2 * SLOT);
       else arrive_pair(full0 + 8 * j);
     };
+    int limit = 0;  // tiles that begin before it have a position for this lane to look up
     auto lookup = [&](int t) {
-      const int pos = TILE * t + lane * box;
-      return lane * box < TILE && pos < walk.s.end ? a.c.table[(size_t)walk.n * a.c.max_pages + (pos >> lp)] : -2;
+      return TILE * t < limit ? a.c.table[(size_t)walk.n * a.c.max_pages + ((TILE * t + lane * box) >> lp)] : -2;
     };
     while (walk.next(a)) {
+      limit = lane * box < TILE ? walk.s.end - lane * box : 0;
       int ahead = lookup(walk.t0);
       for (int t = walk.t0; t < walk.t1; ++t) {
         const int page = ahead;
         if (t + 1 < walk.t1) ahead = lookup(t + 1);
-        if (scores && (page < 0 || page >= a.c.n_pages) && page != -2 && a.err) atomicOr(a.err, ERR_BAD_INDEX);
+        if (scores && (page < 0 || page >= a.c.n_pages) && TILE * t < limit && a.err) atomicOr(a.err, ERR_BAD_INDEX);
         // no page, or behind the last node: past the pool, where loads give zeros
         if (lane < 16) s_page[which][lane] = page >= 0 && page < a.c.n_pages ? page : a.c.n_pages;
         __syncwarp();

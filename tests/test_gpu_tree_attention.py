@@ -323,3 +323,42 @@ def test_masks_from_parents():
     with pytest.raises(kda.KdaError) as e:
         kda.kda_check_device_error()
     assert e.value.status == kda.KDA_ERR_BAD_INDEX and mask.tolist()[4] == 8
+
+
+@pytest.mark.parametrize("bad", [-2, -1, -2**31, 10**6])
+@pytest.mark.parametrize("page,where", [(16, 3), (64, 0), (64, 1), (256, 0)])
+def test_every_table_entry_that_names_no_page_is_reported(bad, page, where):
+    """Whatever the value: its positions are invisible and the call says so."""
+    case = Case([200, 130], [2, 3], H=4, page=page, seed=110)
+    want = case.expect()[0]
+    case.table[1][where] = bad
+    z = case.run(torch.float32)
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_check_device_error()
+    assert e.value.status == kda.KDA_ERR_BAD_INDEX
+    assert np.abs(z[:2] - want[:2]).max() <= 2.0**-6 * np.abs(want[:2]).max()
+    # sequence 1 without the page: its other positions as a shorter cache
+    hidden = range(where * page, (where + 1) * page)
+    keys = {t: torch.nan_to_num(case.pool[case.table[1][t // page], t % page], nan=0.0).double().numpy()
+            for t in range(133) if t not in hidden}
+    for i in range(3):
+        seen = [t for t in keys if t < 130 or (case.mask[2 + i] >> (t - 130)) & 1]
+        if not seen:
+            assert not z[2 + i].any()
+            continue
+        k = np.stack([keys[t] for t in seen])
+        s = case.q[2 + i].double().numpy() @ k.T * kda.MLA_SCALE
+        p = np.exp(s - s.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        unit, one = p @ np.abs(k[:, :512]), p @ k[:, :512]
+        size = (np.abs(case.q[2 + i].double().numpy()) @ np.abs(k).T).max(-1, keepdims=True) * kda.MLA_SCALE
+        assert (np.abs(z[2 + i] - one) <= 1.02 * (2.0**-8 + 584 * 2.0**-24 * size) * (unit + np.abs(one))).all()
+
+
+def test_entries_behind_the_last_position_are_not_read():
+    """The table past the pages in use may hold anything, and nothing is reported."""
+    case = Case([200, 130, 0], [2, 3, 1], H=4, page=16, seed=111)
+    for row in case.table:
+        row[:] = [p if p >= 0 else (-2, 10**6, -1)[i % 3] for i, p in enumerate(row)]
+    case.check(case.run())
+    kda.kda_check_device_error()
