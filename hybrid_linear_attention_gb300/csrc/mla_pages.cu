@@ -50,7 +50,9 @@ __device__ __forceinline__ void after_previous() {
 
 // Row t of sequence n's new rows goes to position lengths[n] + t.  A CTA takes four rows: 72 threads
 // read a row's 72 pieces of up to nine layers while a warp looks up where the row goes (32 sequences'
-// offsets at a step), then write them.
+// offsets at a step), then write them.  A sequence whose offsets are bad must not lead the search away
+// from the others' rows: a row that it finds no sequence for is looked for in all of them (so are rows of
+// no sequence).
 constexpr int AP_ROWS = 4, AP_NT = AP_ROWS * ROW16, AP_LAYERS = 9;
 __global__ void __launch_bounds__(AP_NT) cache_append_kernel(const PagedCache c, const int32_t *cu,
                                                              int n_seqs, int64_t total,
@@ -78,12 +80,20 @@ __global__ void __launch_bounds__(AP_NT) cache_append_kernel(const PagedCache c,
       hi = lo + (k + 1) * step < hi ? lo + (k + 1) * step : hi;
       lo += k * step;
     }
+    auto holds = [&](int n) {
+      const int64_t first = cu[n], end = cu[n + 1];
+      return first >= 0 && mine >= first && mine < end && end <= total;
+    };
+    bool found = holds(lo);
+    for (int n0 = 0; !found && n0 < n_seqs; n0 += 32) {
+      const unsigned m = __ballot_sync(0xffffffffu, n0 + lane < n_seqs && holds(n0 + lane));
+      if (m) found = true, lo = n0 + __ffs((int)m) - 1;
+    }
     if (lane == 0) {
-      const int64_t first = cu[lo], end = cu[lo + 1];
       int page = -2, row = 0;  // no sequence's row: not written
-      if (first >= 0 && mine >= first && mine < end && end <= total) {
+      if (found) {
         const int len = c.lengths[lo];
-        const int64_t pos = (int64_t)len + (mine - first);
+        const int64_t pos = (int64_t)len + (mine - cu[lo]);
         page = len < 0 ? -1 : page_of(c, lo, pos);
         row = (int)(pos % c.page_size);
         if (page < 0) flag(c.err, ERR_BAD_INDEX);

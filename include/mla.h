@@ -122,9 +122,10 @@ kda_status mla_decode(const void* q_nope, const void* q_rope, const void* w_uk,
  * mla_cache_append -- writes new rows (drafted tokens, or a prompt's) behind each sequence:
  * row cu_rows[n] + t of `rows` goes to position lengths[n] + t of sequence n, in every layer.
  *   rows        [n_layers, total_rows, 576] bf16;  cu_rows [n_seqs + 1] int32 (device).
- * Lengths are not changed.  Bit-exact copies.  Offsets outside [0, total_rows] or running
- * backwards are skipped and reported (KDA_ERR_BAD_SEQLENS); a position without a page is skipped
- * and reported (KDA_ERR_BAD_INDEX).  Rows of no sequence are not read into the pool.
+ * Lengths are not changed.  Bit-exact copies.  Sequences whose offsets fall outside [0, total_rows] or
+ * run backwards are skipped and reported (KDA_ERR_BAD_SEQLENS; a row that other sequences around them
+ * share goes to one of these); a position without a page is skipped and reported (KDA_ERR_BAD_INDEX).
+ * Rows of no sequence are not read into the pool.
  */
 kda_status mla_cache_append(void* pool, int n_layers, int n_pages, int page_size,
                             const int32_t* page_table, int max_pages, const int32_t* lengths,

@@ -337,3 +337,29 @@ def test_accept_over_a_missing_page_keeps_rows_and_length(layers):
     kda.mla_cache_accept(d_pool, ref.i32(table[:1]), ref.i32([14]), ref.i32([0, 4]), ref.i32(parents[0]), ref.i32([2]), out)
     assert status() == kda.KDA_ERR_BAD_INDEX
     assert out.tolist()[0] == 14 and torch.equal(d_pool.cpu(), want)
+
+
+@pytest.mark.parametrize("n", [3, 33, 100])
+def test_append_beside_bad_offsets(n):
+    """Offsets below 0, past the rows or running backwards lose their own sequences' rows alone."""
+    _gpu.lib()
+    g = torch.Generator().manual_seed(62 + n)
+    counts = [2 + i % 2 for i in range(n)]
+    cu = [0] + [int(x) for x in np.cumsum(counts)]
+    total = cu[-1]
+    for at, value in ((n // 2, -5), (n - 1, -1), (n // 2, total + 7), (1, 0), (n // 3, -2**31)):
+        bad = list(cu)
+        bad[at] = value
+        rows = torch.randn(2, total, 576, generator=g).to(torch.bfloat16)
+        want = torch.zeros(2, n, 16, 576, dtype=torch.bfloat16)
+        told = False
+        for b in range(n):
+            lo, hi = bad[b], bad[b + 1]
+            if lo < 0 or hi < lo or hi > total:
+                told = True
+                continue
+            want[:, b, 5:5 + hi - lo] = rows[:, lo:hi]
+        pool = torch.zeros(2, n, 16, 576, dtype=torch.bfloat16, device="cuda")
+        kda.mla_cache_append(pool, ref.i32([[b] for b in range(n)]), ref.i32([5] * n), ref.i32(bad), rows.cuda())
+        assert status() == (kda.KDA_ERR_BAD_SEQLENS if told else kda.KDA_OK), (at, value)
+        assert torch.equal(pool.cpu(), want), (at, value)
