@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(128) pages_free_kernel(PagedCache c, int32_t *
     const int h = atomicExch(&held[slot], 0);
     if (h < 0 || h > c.max_pages) flag(c.err, ERR_BAD_INDEX);
     s_held = h < 0 ? 0 : (h > c.max_pages ? c.max_pages : h);
-    if (h != 0) lengths[slot] = 0;
+    lengths[slot] = 0;
   }
   __syncthreads();
   for (int j = threadIdx.x; j < s_held; j += 128) {

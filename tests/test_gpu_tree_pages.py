@@ -363,3 +363,13 @@ def test_append_beside_bad_offsets(n):
         kda.mla_cache_append(pool, ref.i32([[b] for b in range(n)]), ref.i32([5] * n), ref.i32(bad), rows.cuda())
         assert status() == (kda.KDA_ERR_BAD_SEQLENS if told else kda.KDA_OK), (at, value)
         assert torch.equal(pool.cpu(), want), (at, value)
+
+
+def test_free_of_a_sequence_without_pages_clears_its_length():
+    b = Both(8, 3, 4, 16)
+    b.reserve([0], [20])
+    b.set_length(0, 20)
+    b.lengths[1] = 9  # set before any page was reserved
+    b.free([1, 0, 1])
+    assert status() == kda.KDA_OK
+    b.same()
