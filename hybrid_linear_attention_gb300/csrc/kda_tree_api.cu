@@ -28,6 +28,8 @@ kda_status done(cudaError_t e, int launches) {
 
 constexpr int64_t kMaxTreeRows = (int64_t)1 << 22;  // 65535 sequences of 64 nodes
 
+bool page_size_known(int n) { return n == 16 || n == 32 || n == 64 || n == 128 || n == 256; }
+
 // What the paged calls share; `tables`: the call reads or writes page tables and lengths.
 kda_status check_cache(const void *pool, int n_layers, int n_pages, int page_size, bool tables,
                        const int32_t *table, int max_pages, const int32_t *lengths) {
@@ -35,8 +37,7 @@ kda_status check_cache(const void *pool, int n_layers, int n_pages, int page_siz
     return KDA_ERR_INVALID_ARG;
   if (tables && (!given(table) || !given(lengths) || max_pages < 1 || max_pages > 1 << 20))
     return KDA_ERR_INVALID_ARG;
-  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
-    return KDA_ERR_UNSUPPORTED;
+  if (!page_size_known(page_size)) return KDA_ERR_UNSUPPORTED;
   if (n_pages > 1 << 26) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
@@ -282,7 +283,8 @@ kda_status mla_pages_reserve(int n_pages, int page_size, int32_t *refcount, int3
                              int32_t *held, const int32_t *lengths, int n_slots, const int32_t *slots,
                              const int32_t *extra, int n, void *workspace, size_t ws_bytes, cudaStream_t stream) {
   KDA_TRACE(TR_MLA_PAGES_RESERVE);
-  if (page_size < 1 || page_size > 256) return KDA_ERR_INVALID_ARG;
+  if (page_size < 1) return KDA_ERR_INVALID_ARG;
+  if (!page_size_known(page_size)) return KDA_ERR_UNSUPPORTED;
   kda_status st = check_pages(n_pages, refcount, page_table, max_pages, held, lengths, n_slots, n);
   if (st != KDA_OK || n == 0) return st;
   if (!given(slots) || !given(extra) || !optional(workspace)) return KDA_ERR_INVALID_ARG;

@@ -135,3 +135,11 @@ def test_the_binding_checks_shapes(lib):
     with pytest.raises(ValueError, match="n_layers"):
         kda.mla_cache_append(t(4, 16, 576), t(2, 3), t(2), t(3), t(4, 5, 576))
     assert kda.status_string(-8).startswith("KDA_ERR_NO_PAGES")
+
+
+def test_reserve_takes_the_page_sizes_of_the_pool(lib):
+    size = kda.mla_pages_workspace_size(3)
+    go = lambda page: lib.mla_pages_reserve(4, page, 16, 16, 2, 16, 16, 4, 16, 16, 3, 16, size, None)  # noqa: E731
+    assert go(0) == BAD and go(-16) == BAD
+    for page in (1, 8, 24, 48, 255, 512):
+        assert go(page) == UNSUPPORTED
