@@ -18,13 +18,15 @@
 // nodes would be rounded at its size and come out of G_i - G_j wrong (up to 1e-2 of an output with g_min
 // near -88).  So G is kept as F - 16 - 32 N, F in fp32 within -16 .. 16 and N a whole number up to 255: a step
 // is rounded by 2^-21 at most (half an fp32 step below 16), whatever lies before it, N_i - N_j is exact, and down
-// to G = -32 N is 0.  The accepted path is replayed afterwards (tree_accept_kernel), which reads and writes the
-// state once.
+// to G = -32 N is 0.  Trees so small that G cannot pass -64 (at the clamp -5: up to 8 nodes) keep one fp32 sum
+// G + 32, within -32 .. 32: 7 steps rounded by 2^-20 are no worse than 63 by 2^-21.  The accepted path is replayed
+// afterwards (tree_accept_kernel), which reads and writes the state once.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "kda_tc_ptx.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace kda {
 namespace {
@@ -152,17 +154,17 @@ __device__ __forceinline__ void ask_inputs(const TreeArgs &a, int row0, int rows
   }
 }
 
-// shared memory of the verify kernel for at most W nodes (floats): k over q [2 W, whole tiles of
-// 16][D + 4], v, F (then S^T k) [W][D] each, the taps [W][4] and N (bytes) [W][D], then S^T q [W][D] and A and B
-// of the pairs, which take the place of the raw inputs [W + 3][3 D] where those are staged (bf16); parents,
-// first pairs [W + 1], strengths and norms [2 W]; the list of the pairs (node, itself or an ancestor), 16 bits each
+// shared memory of the verify kernel for at most W nodes (floats): k over q [2 W][D + 4], v, F (then S^T k)
+// [W][D] each, the taps [W][4] and, with G split, N (bytes) [W][D], then S^T q [W][D] and A and B of the pairs,
+// which take the place of the raw inputs [W + 3][3 D] where those are staged (bf16); parents, first pairs [W + 1],
+// strengths and norms [2 W]; the list of the pairs (node, itself or an ancestor), 16 bits each
 __host__ __device__ constexpr size_t verify_pairs(int W) { return (size_t)W * (W + 1) / 2; }
 __host__ __device__ constexpr size_t verify_late_floats(int W, int D, bool staged) {
   const size_t late = (size_t)W * D + 2 * verify_pairs(W), raw = staged ? ((size_t)(W + 3) * 3 * D + 1) / 2 : 0;
   return late > raw ? late : raw;
 }
-__host__ __device__ constexpr size_t verify_smem_floats(int W, int D, bool staged) {
-  const size_t all = (size_t)((2 * W + 15) / 16 * 16) * (D + 4) + (size_t)2 * W * D + (size_t)W * (4 + D / 4) +
+__host__ __device__ constexpr size_t verify_smem_floats(int W, int D, bool staged, bool split) {
+  const size_t all = (size_t)2 * W * (D + 4) + (size_t)2 * W * D + (size_t)W * (4 + (split ? D / 4 : 0)) +
                      verify_late_floats(W, D, staged) + (size_t)5 * W + 1 + (verify_pairs(W) + 1) / 2;
   return (all + 3) / 4 * 4;  // what follows starts on 16 bytes
 }
@@ -173,7 +175,6 @@ __device__ __forceinline__ void copy_async16(void *smem, const void *global) {
 
 // F + 32 n for the n that brings F to -16 or above; returns n, at most 4 at a step (a retention of 0 counts as
 // 2^-127)
-constexpr float F_TOP = 16.f;
 __device__ __forceinline__ uint32_t wrap(float &f) {
   const float n = fmaxf(floorf(fmaf(f, -0.03125f, 0.5f)), 0.f);
   f = fmaf(n, 32.f, f);
@@ -234,34 +235,42 @@ constexpr size_t resident_floats() {
 // A CTA is small (four warps, no state held), so that eight share an SM, each in another of the phases
 // that the few barriers of a unit cut.  bf16 inputs come into shared memory by asynchronous copies
 // that run while the tree is worked out.
+// Forms, of x 64 heads:
 // RESIDENT: with few units (no more than fit at a time) the state comes into shared memory the same
 // way, all at once; read step by step from L2 it would be most of a lone unit's time (one sequence x
-// 12 nodes x 64 heads: 19.7 us so, 16.2 resident, before the pairs were listed; 14.4 since).
-// Measured at 256 sequences x 6 to 8 nodes x 64 heads: 323 us, 4.1 TB/s of what it must move (318 with G as one
-// fp32 sum; a tree of 16 nodes 421 for 407, of 64, where most pairs reach past G = -32, 1421 for 1261).  What is
+// 12 nodes: 19.7 us so, 16.2 resident, before the pairs were listed; 13.7 since).
+// LARGE: where shared memory holds five CTAs or fewer there are registers for the pair loop twice, with N and
+// without (32 sequences x up to 64 nodes 1268 us; 1411 with the capped forms' one loop; 128 x 16 406 and 425).
+// SHALLOW (one fp32 sum) and MANY: eight CTAs an SM, so 64 registers a thread and one pair loop that looks at N
+// only where a unit has one that is not 0 (256 x 8: 321 us SHALLOW, 327 MANY; with the loop twice 330 to 339).
+// Measured at 256 sequences x 6 to 8 nodes x 64 heads: 321 us, 4.1 TB/s of what it must move.  What is
 // not the state's product takes 186 us on its own (issue and the latencies of its short phases), the
 // product's loads from L2 most of the rest: more CTAs hide more of both (seven an SM 334 us, six 346, nine
 // spill: 356), which is also why deeper loads cost more than they give (two steps of the state in flight
 // through shared memory, five CTAs: 438 us; through registers: 363).  The state is asked of L2 by one bulk
 // prefetch a unit (325 us by a line a thread, 341 without).
-template <int D, typename IO, typename ST, bool RESIDENT>
-__global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 : 8) : 1) tree_verify_kernel(const TreeArgs a) {
+enum { SHALLOW_FORM, MANY_FORM, RESIDENT_FORM, LARGE_FORM };
+template <int D, typename IO, typename ST, int FORM>
+__global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (FORM == RESIDENT_FORM ? 2 : FORM == LARGE_FORM ? 5 : 8) : 1)
+    tree_verify_kernel(const TreeArgs a) {
+  constexpr bool RESIDENT = FORM == RESIDENT_FORM, SPLIT = FORM != SHALLOW_FORM, CAPPED = FORM == SHALLOW_FORM || FORM == MANY_FORM;
+  constexpr float F_TOP = SPLIT ? 16.f : 32.f;
   constexpr int CW = VerifyShape<D>::CW, NT = VerifyShape<D>::NT, NJ = VerifyShape<D>::NJ, NW = NT / 32, XS = D + 4;
   constexpr int CT = 3 * D / 4;  // threads of the convolution, four channels each
   constexpr bool EXACT = sizeof(IO) == 4;
   extern __shared__ __align__(16) float smem[];
   const int WM = a.max_nodes;
-  float *s_x = smem, *s_v = s_x + (2 * WM + 15) / 16 * 16 * XS, *s_g = s_v + WM * D;
+  float *s_x = smem, *s_v = s_x + 2 * WM * XS, *s_g = s_v + WM * D;
   int4 *s_tap = reinterpret_cast<int4 *>(s_g + WM * D);  // a node's taps, oldest first: nodes, or -1 (newest) .. -3 of the tail
   uint32_t *s_n = reinterpret_cast<uint32_t *>(s_tap + WM);  // N of G, four channels a word
-  float *s_o = reinterpret_cast<float *>(s_n + WM * (D / 4)), *s_A = s_o + WM * D, *s_B = s_A + verify_pairs(WM);
+  float *s_o = reinterpret_cast<float *>(s_n + (SPLIT ? WM * (D / 4) : 0)), *s_A = s_o + WM * D, *s_B = s_A + verify_pairs(WM);
   int *s_par = reinterpret_cast<int *>(s_o + verify_late_floats(WM, D, !EXACT));
   int *s_off = s_par + WM;  // the pairs of node i: s_off[i] .. s_off[i + 1] - 1, itself first
   float *s_beta = reinterpret_cast<float *>(s_off + WM + 1), *s_rn = s_beta + WM;
   uint16_t *s_pair = reinterpret_cast<uint16_t *>(s_rn + 2 * WM);  // node << 6 | ancestor
   IO *s_raw = reinterpret_cast<IO *>(s_o);  // row 3 + i: node i, rows 0 .. 2 the tail
   constexpr int SS = D + 16 / (int)sizeof(ST);
-  ST *s_S = reinterpret_cast<ST *>(smem + verify_smem_floats(WM, D, !EXACT));
+  ST *s_S = reinterpret_cast<ST *>(smem + verify_smem_floats(WM, D, !EXACT, SPLIT));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   after_previous();
@@ -368,13 +377,18 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
                                fmaxf(x.w, a.g_min) * LOG2E);
         float4 z = make_float4(F_TOP, F_TOP, F_TOP, F_TOP);
         uint32_t n = 0;
-        if (p >= 0) z = *reinterpret_cast<const float4 *>(s_g + p * D + c), n = s_n[(p * D + c) / 4];
+        if (p >= 0) {
+          z = *reinterpret_cast<const float4 *>(s_g + p * D + c);
+          if (SPLIT) n = s_n[(p * D + c) / 4];
+        }
         y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
-        if (fminf(fminf(y.x, y.y), fminf(y.z, y.w)) < -16.f)
-          n += wrap(y.x) | wrap(y.y) << 8 | wrap(y.z) << 16 | wrap(y.w) << 24;  // no byte passes 255
+        if (SPLIT) {
+          if (fminf(fminf(y.x, y.y), fminf(y.z, y.w)) < -16.f)
+            n += wrap(y.x) | wrap(y.y) << 8 | wrap(y.z) << 16 | wrap(y.w) << 24;  // no byte passes 255
+          s_n[(i * D + c) / 4] = n;
+          past |= n;
+        }
         *reinterpret_cast<float4 *>(s_g + i * D + c) = y;
-        s_n[(i * D + c) / 4] = n;
-        past |= n;
       }
     }
     if (unit + gridDim.x < units) {  // the next unit's inputs
@@ -384,7 +398,9 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
       const int nw = tree_nodes(a, nn, WM, nrow0, false);
       if (ns >= 0 && ns < a.n_slots && nw > 0) ask_inputs<D, IO, 1, 0>(a, nrow0, nw, ns, (int)(nu % H), tid, NT);
     }
-    const bool deep = __syncthreads_or(past);  // is there an N that is not 0
+    bool deep = false;  // is there an N that is not 0
+    if (SPLIT) deep = __syncthreads_or(past);
+    else __syncthreads();
     // ---- the norms of k and q (eight lanes a row), kept as factors
     for (int x = tid >> 3; x < 2 * W; x += NT / 8) {
       float ss = 0.f;
@@ -399,7 +415,7 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
     }
     __syncthreads();
     // ---- A and B over the (node, ancestor or itself) pairs: eight lanes a pair
-    {
+    auto pair_products = [&](auto DEEP) {
       const int sub = 4 * (tid & 7), pairs = s_off[W];
       const unsigned eight = 0xffu << (lane & 24);
       for (int k = tid >> 3; k < pairs; k += NT / 8) {
@@ -415,9 +431,9 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
                          ki = *reinterpret_cast<const float4 *>(s_x + i * XS + c),
                          qi = *reinterpret_cast<const float4 *>(s_x + (W + i) * XS + c);
             float4 d = make_float4(gi.x - gj.x, gi.y - gj.y, gi.z - gj.z, gi.w - gj.w);
-            if (deep) {
+            if (CAPPED ? deep : decltype(DEEP)::value) {
               const uint32_t n = s_n[(i * D + c) / 4] - s_n[(j * D + c) / 4];  // N rises along a path: no borrow
-              if (n) d = unwrap(d, n);
+              if (!CAPPED || n) d = unwrap(d, n);
             }
             const float e0 = ex2_(d.x) * kj.x, e1 = ex2_(d.y) * kj.y, e2 = ex2_(d.z) * kj.z, e3 = ex2_(d.w) * kj.w;
             pa = fmaf(ki.x, e0, fmaf(ki.y, e1, fmaf(ki.z, e2, fmaf(ki.w, e3, pa))));
@@ -434,7 +450,9 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
           s_B[k] = pb * s_rn[W + i] * s_rn[j];
         }
       }
-    }
+    };
+    if (!CAPPED && deep) pair_products(std::true_type{});
+    else pair_products(std::false_type{});
     __syncthreads();
     if (RESIDENT) asm volatile("cp.async.wait_group 0;" ::: "memory");
     // ---- X = k e^G over q e^G, a warp a row; with bf16 I/O as [D] high parts, then [D] low parts
@@ -474,8 +492,9 @@ __global__ void __launch_bounds__(VerifyShape<D>::NT, D == 128 ? (RESIDENT ? 2 :
         if (RESIDENT) load_cols_shared(x, mine + r * LD);
         else load_cols(x, mine + (size_t)r * LD);
       };
-      // lane l of ldmatrix names row l % 8 of block l / 8: rows 0-7 | 8-15, then 16 bytes on
-      const float *rows = s_x + (m0 + (lane & 7) + (lane >> 3 & 1) * 8) * XS + (lane >> 4) * 4;
+      // lane l of ldmatrix names row l % 8 of block l / 8: rows 0-7 | 8-15, then 16 bytes on; behind the
+      // last row that row is read again (its products are dropped)
+      const float *rows = s_x + min(m0 + (lane & 15), 2 * W - 1) * XS + (lane >> 4) * 4;
       if (EXACT) {
 #pragma unroll 4
         for (int s = 0; s < D / 8; ++s) {  // rows 8 s + t and 8 s + 4 + t
@@ -853,21 +872,29 @@ cudaError_t launch_typed(const TreeArgs &a, bool accept, cudaStream_t s) {
     return launch(kernel, groups < fit ? groups : fit, 2 * D, accept_smem<D, ST>(group), s, a, group);
   } else {
     constexpr bool staged = sizeof(IO) == 2;
-    const size_t smem = verify_smem_floats(a.max_nodes, D, staged) * sizeof(float);
-    const size_t most = verify_smem_floats(64, D, staged) * sizeof(float), extra = resident_floats<D, ST>() * sizeof(float);
     constexpr int NT = VerifyShape<D>::NT;
+    const size_t smem = verify_smem_floats(a.max_nodes, D, staged, true) * sizeof(float), extra = resident_floats<D, ST>() * sizeof(float);
     if (smem + extra <= SMEM_MOST) {
-      constexpr auto kernel = tree_verify_kernel<D, IO, ST, true>;
+      constexpr auto kernel = tree_verify_kernel<D, IO, ST, RESIDENT_FORM>;
       cudaError_t e = fitting<kernel>(NT, smem + extra, SMEM_MOST, &fit);
       if (e != cudaSuccess) return e;
       if (units <= fit) {
         return launch(kernel, units, NT, smem + extra, s, a);
       }
     }
-    constexpr auto kernel = tree_verify_kernel<D, IO, ST, false>;
-    cudaError_t e = fitting<kernel>(NT, smem, most, &fit);
-    if (e != cudaSuccess) return e;
-    return launch(kernel, units < fit ? units : fit, NT, smem, s, a);
+    auto go = [&](auto FORM) {
+      constexpr bool split = decltype(FORM)::value != SHALLOW_FORM;
+      constexpr size_t most = verify_smem_floats(64, D, staged, split) * sizeof(float);
+      constexpr auto kernel = tree_verify_kernel<D, IO, ST, decltype(FORM)::value>;
+      const size_t mine = verify_smem_floats(a.max_nodes, D, staged, split) * sizeof(float);
+      cudaError_t e = fitting<kernel>(NT, mine, most, &fit);
+      if (e != cudaSuccess) return e;
+      return launch(kernel, units < fit ? units : fit, NT, mine, s, a);
+    };
+    // see the kernel's comment; 1 KB of an SM's shared memory goes to each CTA beside its own
+    if (D == 128 && 6 * (smem + 1024) > 228 * 1024) return go(std::integral_constant<int, LARGE_FORM>{});
+    if (a.max_nodes * -a.g_min * LOG2E <= 64.f) return go(std::integral_constant<int, SHALLOW_FORM>{});
+    return go(std::integral_constant<int, MANY_FORM>{});
   }
 }
 

@@ -278,3 +278,38 @@ def test_verify_deep_trees_of_mixed_retentions(io):
                         m["parent"], H=3, d=128, gate=m["gate"], norm_w=m["norm_w"], g_min=-float("inf"))[0]
     assert out_error(verify(m, p), want) <= tol(p)
     kda.kda_check_device_error()
+
+
+@pytest.mark.parametrize("io,st", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("most", [1, 3, 8, 11, 12, 20])
+@pytest.mark.parametrize("d,n,H", [(128, 40, 16), (16, 90, 64)])
+def test_verify_of_many_units_in_every_form(d, n, H, most, io, st):
+    """More units than fit at a time, trees that are not a multiple of eight nodes, with the sums of the
+    log-retentions short enough for one fp32 number (the clamp at -5) and not (none, or strong forgetting)."""
+    rng = np.random.default_rng(most + d)
+    counts = [int(x) for x in rng.integers(0, most + 1, n)]
+    counts[3] = most
+    for g_min, strong in ((-5.0, -5.0), (-float("inf"), -80.0)):
+        p = kda.params(H=H, d=d, io_dtype=io, state_dtype=st, g_min=g_min)
+        m = make(counts, H, d, seed=600 + most, io=io, st=st, chain=most > 9)
+        kind = torch.rand(m["g"].shape, generator=torch.Generator().manual_seed(most))
+        m["g"] = torch.where(kind < 0.4, torch.tensor(strong), -0.05 * kind).contiguous()
+        want = ref.kda_tree(m["x"], m["conv_w"], m["conv_state"], m["g"], m["beta"], m["state"], m["slots"], m["cu"],
+                            m["parent"], H=H, d=d, g_min=g_min)[0]
+        assert out_error(verify(m, p, gated=False, max_nodes=most), want) <= tol(p)
+    kda.kda_check_device_error()
+
+
+@pytest.mark.parametrize("nodes,forget", [(17, 8), (17, 13), (12, 9), (11, 4), (8, 4), (8, 3)])
+def test_verify_shallow_trees_retain_after_forgetting(nodes, forget):
+    """Paths around the longest that one fp32 sum serves (8 nodes at the clamp -5): 7 steps off by 2^-20 each
+    (half a step of fp32 below 2^5) are 4.6e-6 of a decay, 16 steps of 2^-21 behind it 5.3e-6."""
+    for d, n, H in ((128, 40, 16), (16, 90, 64)):
+        p = kda.params(H=H, d=d, io_dtype=torch.float32)
+        m = make([nodes] * n, H, d, seed=610, chain=True, io=torch.float32)
+        g = m["g"].view(n, nodes, H, d)
+        g[:, :forget], g[:, forget:] = -5.0, -0.013
+        want = ref.kda_tree(m["x"], m["conv_w"], m["conv_state"], m["g"], m["beta"], m["state"], m["slots"], m["cu"],
+                            m["parent"], H=H, d=d)[0]
+        assert out_error(verify(m, p, gated=False, max_nodes=nodes), want) <= tol(p)
+    kda.kda_check_device_error()
