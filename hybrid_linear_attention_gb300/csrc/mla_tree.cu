@@ -28,11 +28,14 @@
 // between them (with one, pages of 16 positions were bound by it: 422 us for 283, pages of 64 278 for 266).
 // That brings 272 KB to a CTA for 256 positions, 64 bytes a cycle at the products' full rate; TMA moves 41
 // to 48 bytes a cycle and SM from L2, so L2 is the bound where the cache is read by several row tiles:
-// 4 sequences x 11 to 16 nodes x 65536 positions 266 us, 1.60 PFLOP/s, 83 % of the measured bf16 peak.
+// 4 sequences x 11 to 16 nodes x 65536 positions 266 us in bursts of ten, 1.60 PFLOP/s, 83 % of the measured bf16
+// peak; 290 to 304 us where calls follow one another for long (1.40 to 1.47 PFLOP/s: the power limit).
 // The rings' depth is what that rate needs: a slot less in either costs 11 to 35 %, one more (weights of
 // 128 positions at a time) gives back only what the smaller place for the weights costs.  With one node a
-// sequence the same loop streams the cache: 256 sequences of 2048 to 4096 positions 197 us, 4.8 TB/s
-// (asking L2 for coming tiles, by bulk prefetches or by threads, measured slower: 247 to 272 us).
+// sequence the same loop streams the cache: 256 sequences of 2048 to 4096 positions 198 us, 4.8 TB/s, and 202 to
+// 211 among other calls (asking L2 for coming tiles, by bulk prefetches or by threads, measured slower: 247 to
+// 272 us).  There every byte of the cache still comes into shared memory 1.85 times, for the scores and for the
+// values, and with 64 heads half of the products' rows are empty.
 //
 // Work is dealt in tiles of 256 positions: clusters form groups of G that take G row tiles of a
 // sequence side by side (they read the same positions at the same time, so HBM sees them once),
@@ -698,7 +701,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           const float e0 = ex2(fmaf(v[2 * c], a.scale_log2, -base)), e1 = ex2(fmaf(v[2 * c + 1], a.scale_log2, -base));
           const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
           w[c] = *reinterpret_cast<const uint32_t *>(&b);
-          // the normaliser sums the weights that the product uses
+          // weights are rounded to bf16, the product's operands (two parts each would double its time): 2^-8 of a
+          // weight at most, which averages out over the positions (a bf16 z is 1.7e-3 to 2.0e-3 off in RMS, where
+          // its own rounding is 1.7e-3).  The normaliser sums the weights that the product uses: they add up to one.
           ls += __uint_as_float(w[c] << 16) + __uint_as_float(w[c] & 0xffff0000u);
         }
         sum = sum * al + ls;

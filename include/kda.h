@@ -355,8 +355,9 @@ kda_status kda_state_accept(const kda_params* p, const void* step_states, int n_
  *   parent      [total_nodes] int32 (device): index of the parent within the sequence, smaller
  *               than the node's own, or -1.  Another value is taken as -1 and reported
  *               (KDA_ERR_BAD_INDEX).
- *   max_nodes   1..64: the most nodes of any sequence (a smaller value lets more of them run at
- *               a time).
+ *   max_nodes   1..64: the most nodes of any sequence.  It sizes the kernel's shared memory, so a
+ *               value well above the trees' costs time: 256 trees of 8 nodes x 64 heads take 347 us with 8
+ *               and 1315 with 64.
  *   gate_logit  [total_nodes, H, d] io_dtype or NULL; norm_w [d] fp32 or NULL, as kda_prefill.
  *   out         [total_nodes, H, d] io_dtype.  Rows of no sequence stay as they were.
  * total_nodes at most 2^22.  No counterpart interface is printed on the pages.

@@ -151,7 +151,8 @@ kda_status mla_cache_accept(void* pool, int n_layers, int n_pages, int page_size
 /*
  * mla_pages_copy -- copies page src[i] to page dst[i] in every layer, i < n_copies (at most
  * 8192; device int32 arrays).  An entry out of range, one whose target an earlier entry has, or
- * one whose target is a source of the call is skipped and reported (KDA_ERR_BAD_INDEX).
+ * one whose target is the source of another is skipped and reported (KDA_ERR_BAD_INDEX); a page named
+ * as its own target stays as it is.
  */
 kda_status mla_pages_copy(void* pool, int n_layers, int n_pages, int page_size,
                           const int32_t* src, const int32_t* dst, int n_copies,
