@@ -209,7 +209,7 @@ def prepare(case, seed):
         _prepare_sparse(s, d, case, lengths, n_pages)
         if own:
             from hybrid_linear_attention_gb300 import kda
-            s["ws"] = torch.empty(kda.mla_sparse_workspace_size(n, total, case["heads"], most, page), dtype=torch.uint8, device=DEV)
+            s["ws"] = torch.empty(kda.mla_sparse_workspace_size(n, total, case["heads"], most), dtype=torch.uint8, device=DEV)
     return s
 
 
