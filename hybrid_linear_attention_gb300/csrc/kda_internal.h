@@ -102,7 +102,42 @@ struct TreeAttnArgs {
   void *z;                     // [total, H, 512]
   int z_bf16;
   void *ws;                    // partial sums and the plan
+  float *lse;                  // [total, H] log of the sum of exp(score) over what a row sees, or nullptr
   int *err;
+};
+
+// What keys receive from all query rows of a sequence's step (mla_sums.cu).
+struct KeySumArgs {
+  PagedCache c;                // one layer; blocks: the pool is the pages' keys [n_pages, 576]
+  int n_seqs, H;
+  int64_t total;               // drafted nodes of the batch
+  float scale_log2;            // score scale x log2(e)
+  const void *q;               // [total, H, 576] bf16
+  const int32_t *cu_nodes;     // [n_seqs + 1]
+  const int64_t *mask;         // positions: as TreeAttnArgs
+  const float *node_weight;    // positions: [total] or nullptr (ones)
+  float *lse;                  // [total, H]
+  float *out;                  // [n_seqs, out_stride] positions: added to; blocks: written
+  int64_t out_stride;
+  float2 *part;                // blocks: (maximum, sum) of each row [total, H, part_stride] over half a tile
+  int64_t part_stride;
+  int *err;
+};
+
+// A selection of the largest values of each sequence (mla_select.cu).
+struct SelectArgs {
+  PagedCache c;                // page_size, table, lengths; the pool is not read
+  int n_seqs;
+  const float *values;         // [n_seqs, stride] of blocks or positions
+  int64_t stride;
+  int most, first, recent;     // taken in all; the first and the most recent always
+  int32_t *out;                // [n_seqs, out_stride] blocks: a page table; eviction: kept positions
+  int64_t out_stride;
+  int32_t *out_lengths;        // [n_seqs]
+  const int32_t *cu_nodes;     // blocks: [n_seqs + 1] drafted nodes, total in all
+  int64_t total;
+  const int32_t *refs;         // eviction: [n_pages] or nullptr
+  float *new_values;           // eviction: [n_seqs, stride], values (in place) or nullptr
 };
 
 struct ProArgs {
@@ -176,6 +211,14 @@ cudaError_t launch_pages_copy(const PagedCache &c, const int32_t *src, const int
 cudaError_t launch_pages_free(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots,
                               const int32_t *slots, int n, cudaStream_t s);
 size_t pages_ws_bytes(int n);
+cudaError_t launch_cache_weights(const KeySumArgs &a, cudaStream_t s);
+size_t block_scores_ws_bytes(int64_t total, int H, int max_pages);
+cudaError_t launch_block_scores(const KeySumArgs &a, void *ws, int *launches, cudaStream_t s);
+cudaError_t launch_block_keys(const PagedCache &c, const int32_t *from, int n_seqs, void *keys, cudaStream_t s);
+cudaError_t launch_block_select(const SelectArgs &a, cudaStream_t s);
+cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t s);
+cudaError_t launch_pages_trim(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots,
+                              const int32_t *slots, int n, cudaStream_t s);
 cudaError_t launch_pages_fork(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots,
                               const int32_t *src, const int32_t *dst, int n, void *ws,
                               cudaStream_t s);

@@ -1,4 +1,4 @@
-// kda_tree_api.cu -- the C ABI of the tree-verification calls (include/kda.h, include/mla.h):
+// kda_tree_api.cu -- the C ABI of the tree-verification and paged-cache calls (include/kda.h, include/mla.h):
 // host-side validation, then kernel launches, as kda_api.cu does for the rest.
 #include "../../include/kda.h"
 #include "../../include/mla.h"
@@ -181,6 +181,36 @@ kda_status mla_tree_latent(const void *q_cat, int H, const void *pool, int n_pag
   return done(e, launches);
 }
 
+kda_status mla_tree_latent_lse(const void *q_cat, int H, const void *pool, int n_pages, int page_size,
+                               const int32_t *page_table, int max_pages, const int32_t *lengths,
+                               const int32_t *cu_nodes, int n_seqs, int64_t total_nodes,
+                               const int64_t *mask, float scale, void *z, kda_dtype z_dtype, float *lse,
+                               void *workspace, size_t ws_bytes, cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_TREE_LATENT_LSE);
+  if (total_nodes > 0 && !given(lse)) return KDA_ERR_INVALID_ARG;
+  kda::TreeAttnArgs a;
+  kda_status st = tree_attention(q_cat, H, pool, n_pages, page_size, page_table, max_pages, lengths, cu_nodes,
+                                 n_seqs, total_nodes, mask, scale, z, z_dtype, workspace, ws_bytes, &a);
+  if (st != KDA_OK || total_nodes == 0) return st;
+  a.lse = lse;
+  int launches = 0;
+  const cudaError_t e = kda::launch_mla_tree(a, &launches, stream);
+  return done(e, launches);
+}
+
+// What the decode calls put around the attention: the projections see one query row per node.
+static kda_status node_projections(const void *q_nope, const void *q_rope, const void *w_uk, const void *w_uv,
+                                   const void *gate_logit, void *out, void *q_cat, float *z, int64_t total_nodes,
+                                   kda::MlaArgs *m) {
+  if (!given(q_nope) || !given(q_rope) || !given(w_uk) || !given(w_uv) || !given(gate_logit) || !given(out))
+    return KDA_ERR_INVALID_ARG;
+  std::memset(m, 0, sizeof *m);
+  m->B = (int)total_nodes;
+  m->q_nope = q_nope, m->q_rope = q_rope, m->w_uk = w_uk, m->w_uv = w_uv, m->gate = gate_logit;
+  m->q_cat = q_cat, m->z = z, m->out = out, m->err = kda::device_error();
+  return KDA_OK;
+}
+
 kda_status mla_tree_decode(const void *q_nope, const void *q_rope, const void *w_uk, const void *w_uv,
                            const void *pool, int n_pages, int page_size, const int32_t *page_table,
                            int max_pages, const int32_t *lengths, const int32_t *cu_nodes, int n_seqs,
@@ -189,16 +219,34 @@ kda_status mla_tree_decode(const void *q_nope, const void *q_rope, const void *w
                            cudaStream_t stream) {
   KDA_TRACE(TR_MLA_TREE_DECODE);
   kda::TreeAttnArgs a;
+  kda::MlaArgs m;
   kda_status st = tree_attention(q_cat, 64, pool, n_pages, page_size, page_table, max_pages, lengths, cu_nodes,
                                  n_seqs, total_nodes, mask, scale, z, KDA_F32, workspace, ws_bytes, &a);
   if (st != KDA_OK || total_nodes == 0) return st;
-  if (!given(q_nope) || !given(q_rope) || !given(w_uk) || !given(w_uv) || !given(gate_logit) || !given(out))
-    return KDA_ERR_INVALID_ARG;
-  kda::MlaArgs m;  // the projections see one query row per node
-  std::memset(&m, 0, sizeof m);
-  m.B = (int)total_nodes;
-  m.q_nope = q_nope, m.q_rope = q_rope, m.w_uk = w_uk, m.w_uv = w_uv, m.gate = gate_logit;
-  m.q_cat = q_cat, m.z = z, m.out = out, m.err = a.err;
+  st = node_projections(q_nope, q_rope, w_uk, w_uv, gate_logit, out, q_cat, z, total_nodes, &m);
+  if (st != KDA_OK) return st;
+  int launches = 0;
+  cudaError_t e = kda::launch_mla_absorb(m, stream);
+  if (e == cudaSuccess) e = kda::launch_mla_tree(a, &launches, stream);
+  if (e == cudaSuccess) e = kda::launch_mla_up_gate(m, stream);
+  return done(e, launches + 2);
+}
+
+kda_status mla_tree_decode_lse(const void *q_nope, const void *q_rope, const void *w_uk, const void *w_uv,
+                               const void *pool, int n_pages, int page_size, const int32_t *page_table,
+                               int max_pages, const int32_t *lengths, const int32_t *cu_nodes, int n_seqs,
+                               int64_t total_nodes, const int64_t *mask, const void *gate_logit, float scale,
+                               void *q_cat, float *z, void *out, float *lse, void *workspace, size_t ws_bytes,
+                               cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_TREE_DECODE_LSE);
+  kda::TreeAttnArgs a;
+  kda::MlaArgs m;
+  kda_status st = node_projections(q_nope, q_rope, w_uk, w_uv, gate_logit, out, q_cat, z, total_nodes, &m);
+  if (total_nodes > 0 && (st != KDA_OK || !given(lse))) return KDA_ERR_INVALID_ARG;
+  st = tree_attention(q_cat, 64, pool, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs, total_nodes,
+                      mask, scale, z, KDA_F32, workspace, ws_bytes, &a);
+  if (st != KDA_OK || total_nodes == 0) return st;
+  a.lse = lse;
   int launches = 0;
   cudaError_t e = kda::launch_mla_absorb(m, stream);
   if (e == cudaSuccess) e = kda::launch_mla_tree(a, &launches, stream);
@@ -291,6 +339,247 @@ kda_status mla_pages_reserve(int n_pages, int page_size, int32_t *refcount, int3
   if (!workspace || ws_bytes < kda::pages_ws_bytes(n)) return KDA_ERR_WORKSPACE;
   return done(kda::launch_pages_reserve(cache_args(nullptr, 1, n_pages, page_size, page_table, max_pages, lengths),
                                         refcount, held, n_slots, slots, extra, n, workspace, stream), 1);
+}
+
+kda_status mla_pages_trim(int n_pages, int page_size, int32_t *refcount, int32_t *page_table, int max_pages,
+                          int32_t *held, const int32_t *lengths, int n_slots, const int32_t *slots, int n,
+                          cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_PAGES_TRIM);
+  if (page_size < 1) return KDA_ERR_INVALID_ARG;
+  if (!page_size_known(page_size)) return KDA_ERR_UNSUPPORTED;
+  kda_status st = check_pages(n_pages, refcount, page_table, max_pages, held, lengths, n_slots, n);
+  if (st != KDA_OK || n == 0) return st;
+  if (!given(slots)) return KDA_ERR_INVALID_ARG;
+  return done(kda::launch_pages_trim(cache_args(nullptr, 1, n_pages, page_size, page_table, max_pages, lengths), refcount,
+                                     held, n_slots, slots, n, stream), 1);
+}
+
+// ---- long contexts -----------------------------------------------------------------------------
+
+// The checks that the two sums over query rows share; fills *a but for its results.
+static kda_status key_sums(const void *q_cat, int H, const void *keys, int n_pages, int page_size,
+                           const int32_t *page_table, int max_pages, const int32_t *lengths, const int32_t *cu_nodes,
+                           int n_seqs, int64_t total_nodes, float scale, kda::KeySumArgs *a) {
+  if (n_seqs < 0 || n_seqs > 65535 || total_nodes < 0 || total_nodes > kMaxTreeRows || H < 1 || H > 128)
+    return KDA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale < 1e30f)) return KDA_ERR_INVALID_ARG;
+  if (total_nodes == 0) return KDA_OK;
+  kda_status st = check_cache(keys, 1, n_pages, page_size, true, page_table, max_pages, lengths);
+  if (st != KDA_OK) return st;
+  if (n_seqs == 0 || !given(q_cat) || !given(cu_nodes)) return KDA_ERR_INVALID_ARG;
+  std::memset(a, 0, sizeof *a);
+  a->c = cache_args(keys, 1, n_pages, page_size, page_table, max_pages, lengths);
+  a->n_seqs = n_seqs, a->H = H, a->total = total_nodes;
+  a->scale_log2 = scale * 1.4426950408889634f;
+  a->q = q_cat, a->cu_nodes = cu_nodes, a->err = a->c.err;
+  return KDA_OK;
+}
+
+kda_status mla_cache_weights(const void *q_cat, int H, const void *pool, int n_pages, int page_size,
+                             const int32_t *page_table, int max_pages, const int32_t *lengths,
+                             const int32_t *cu_nodes, int n_seqs, int64_t total_nodes, const int64_t *mask,
+                             const float *node_weight, const float *lse, float scale, float *weights,
+                             int64_t weights_stride, cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_CACHE_WEIGHTS);
+  kda::KeySumArgs a;
+  kda_status st = key_sums(q_cat, H, pool, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
+                           total_nodes, scale, &a);
+  if (st != KDA_OK || total_nodes == 0) return st;
+  if (!optional(mask) || !optional(node_weight) || !given(lse) || !given(weights) || weights_stride < 1)
+    return KDA_ERR_INVALID_ARG;
+  if (!kda::mla_latent_supported()) return KDA_ERR_UNSUPPORTED;
+  a.mask = mask, a.node_weight = node_weight, a.lse = const_cast<float *>(lse);
+  a.out = weights, a.out_stride = weights_stride;
+  return done(kda::launch_cache_weights(a, stream), 1);
+}
+
+// What the selections share.
+static kda_status check_choice(int most, int first, int recent) {
+  return most < 1 || first < 0 || recent < 0 || first > most || recent > most - first ? KDA_ERR_INVALID_ARG : KDA_OK;
+}
+
+kda_status mla_cache_evict(void *pool, int n_layers, int n_pages, int page_size, const int32_t *page_table,
+                           int max_pages, const int32_t *lengths, const int32_t *refcount, int n_seqs,
+                           const float *weights, int64_t weights_stride, int budget, int first, int recent,
+                           int32_t *kept, int32_t *new_lengths, float *new_weights, cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_CACHE_EVICT);
+  if (n_seqs < 0 || n_seqs > 65535) return KDA_ERR_INVALID_ARG;
+  kda_status st = check_cache(pool, n_layers, n_pages, page_size, true, page_table, max_pages, lengths);
+  if (st == KDA_OK) st = check_choice(budget, first, recent);
+  if (st != KDA_OK || n_seqs == 0) return st;
+  if (!optional(refcount) || !given(weights) || weights_stride < 1 || !given(kept) || !given(new_lengths) ||
+      !optional(new_weights))
+    return KDA_ERR_INVALID_ARG;
+  kda::SelectArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.c = cache_args(pool, n_layers, n_pages, page_size, page_table, max_pages, lengths);
+  a.n_seqs = n_seqs, a.values = weights, a.stride = weights_stride;
+  a.most = budget, a.first = first, a.recent = recent;
+  a.out = kept, a.out_stride = budget, a.out_lengths = new_lengths;
+  a.refs = refcount, a.new_values = new_weights;
+  int launches = 0;
+  const cudaError_t e = kda::launch_cache_evict(a, &launches, stream);
+  return done(e, launches);
+}
+
+kda_status mla_block_keys(const void *pool, int n_layers, int n_pages, int page_size, const int32_t *page_table,
+                          int max_pages, const int32_t *from_lengths, const int32_t *lengths, int n_seqs, void *keys,
+                          cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_BLOCK_KEYS);
+  if (n_seqs < 0 || n_seqs > 65535) return KDA_ERR_INVALID_ARG;
+  kda_status st = check_cache(pool, n_layers, n_pages, page_size, true, page_table, max_pages, lengths);
+  if (st != KDA_OK || n_seqs == 0) return st;
+  if (!given(from_lengths) || !given(keys)) return KDA_ERR_INVALID_ARG;
+  return done(kda::launch_block_keys(cache_args(pool, n_layers, n_pages, page_size, page_table, max_pages, lengths),
+                                     from_lengths, n_seqs, keys, stream), 1);
+}
+
+size_t mla_block_scores_workspace_size(int64_t total_nodes, int H, int max_pages) {
+  if (total_nodes < 1 || total_nodes > kMaxTreeRows || H < 1 || H > 128 || max_pages < 1 || max_pages > 1 << 20) return 0;
+  return kda::block_scores_ws_bytes(total_nodes, H, max_pages);
+}
+
+// mla_block_scores but for the launch; fills *a.
+static kda_status block_scores(const void *q_cat, int H, const void *keys, int n_pages, int page_size,
+                               const int32_t *page_table, int max_pages, const int32_t *lengths, const int32_t *cu_nodes,
+                               int n_seqs, int64_t total_nodes, float scale, float *scores, int64_t scores_stride,
+                               void *workspace, size_t ws_bytes, kda::KeySumArgs *a) {
+  kda_status st = key_sums(q_cat, H, keys, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
+                           total_nodes, scale, a);
+  if (st != KDA_OK || total_nodes == 0) return st;
+  if (!given(scores) || scores_stride < max_pages || !optional(workspace)) return KDA_ERR_INVALID_ARG;
+  if (!workspace || ws_bytes < kda::block_scores_ws_bytes(total_nodes, H, max_pages)) return KDA_ERR_WORKSPACE;
+  a->out = scores, a->out_stride = scores_stride;
+  return KDA_OK;
+}
+
+kda_status mla_block_scores(const void *q_cat, int H, const void *keys, int n_pages, int page_size,
+                            const int32_t *page_table, int max_pages, const int32_t *lengths, const int32_t *cu_nodes,
+                            int n_seqs, int64_t total_nodes, float scale, float *scores, int64_t scores_stride,
+                            void *workspace, size_t ws_bytes, cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_BLOCK_SCORES);
+  kda::KeySumArgs a;
+  kda_status st = block_scores(q_cat, H, keys, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
+                               total_nodes, scale, scores, scores_stride, workspace, ws_bytes, &a);
+  if (st != KDA_OK || total_nodes == 0) return st;
+  if (!kda::mla_latent_supported()) return KDA_ERR_UNSUPPORTED;
+  int launches = 0;
+  const cudaError_t e = kda::launch_block_scores(a, workspace, &launches, stream);
+  return done(e, launches);
+}
+
+// mla_block_select but for the launch; fills *a.
+static kda_status block_select(const float *scores, int64_t scores_stride, int page_size, const int32_t *page_table,
+                               int max_pages, const int32_t *lengths, const int32_t *cu_nodes, int n_seqs,
+                               int64_t total_nodes, int blocks, int first, int recent, int32_t *sel_table, int sel_pages,
+                               int32_t *sel_lengths, kda::SelectArgs *a) {
+  if (n_seqs < 0 || n_seqs > 65535 || total_nodes < 0 || total_nodes > kMaxTreeRows || page_size < 1)
+    return KDA_ERR_INVALID_ARG;
+  if (!page_size_known(page_size)) return KDA_ERR_UNSUPPORTED;
+  if (check_choice(blocks, first, recent) != KDA_OK) return KDA_ERR_INVALID_ARG;
+  if (n_seqs == 0) return KDA_OK;
+  if (!given(scores) || !given(page_table) || max_pages < 1 || max_pages > 1 << 20 || scores_stride < max_pages ||
+      !given(lengths) || !given(cu_nodes) || !given(sel_table) || sel_pages < 1 || sel_pages > 1 << 20 || !given(sel_lengths))
+    return KDA_ERR_INVALID_ARG;
+  std::memset(a, 0, sizeof *a);
+  a->c = cache_args(nullptr, 1, 1, page_size, page_table, max_pages, lengths);
+  a->n_seqs = n_seqs, a->values = scores, a->stride = scores_stride;
+  a->most = blocks, a->first = first, a->recent = recent;
+  a->out = sel_table, a->out_stride = sel_pages, a->out_lengths = sel_lengths;
+  a->cu_nodes = cu_nodes, a->total = total_nodes;
+  return KDA_OK;
+}
+
+kda_status mla_block_select(const float *scores, int64_t scores_stride, int page_size, const int32_t *page_table,
+                            int max_pages, const int32_t *lengths, const int32_t *cu_nodes, int n_seqs,
+                            int64_t total_nodes, int blocks, int first, int recent, int32_t *sel_table, int sel_pages,
+                            int32_t *sel_lengths, cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_BLOCK_SELECT);
+  kda::SelectArgs a;
+  kda_status st = block_select(scores, scores_stride, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
+                               total_nodes, blocks, first, recent, sel_table, sel_pages, sel_lengths, &a);
+  if (st != KDA_OK || n_seqs == 0) return st;
+  return done(kda::launch_block_select(a, stream), 1);
+}
+
+size_t mla_sparse_workspace_size(int n_seqs, int64_t total_nodes, int H, int max_pages) {
+  const size_t scores = mla_block_scores_workspace_size(total_nodes, H, max_pages);
+  const size_t tree = mla_tree_workspace_size(n_seqs, total_nodes, H);
+  return scores == 0 || tree == 0 ? 0 : scores > tree ? scores : tree;
+}
+
+// The three parts of a sparse step; they follow one another, so they share the workspace.
+struct SparseStep {
+  kda::KeySumArgs scores;
+  kda::SelectArgs choice;
+  kda::TreeAttnArgs attention;
+  void *ws;
+};
+static kda_status sparse_step(const void *q_cat, int H, const void *pool, const void *keys, int n_pages, int page_size,
+                              const int32_t *page_table, int max_pages, const int32_t *lengths, const int32_t *cu_nodes,
+                              int n_seqs, int64_t total_nodes, const int64_t *mask, float scale, int blocks, int first,
+                              int recent, float *scores, int64_t scores_stride, int32_t *sel_table, int sel_pages,
+                              int32_t *sel_lengths, void *z, kda_dtype z_dtype, void *workspace, size_t ws_bytes,
+                              SparseStep *s) {
+  kda_status st = block_scores(q_cat, H, keys, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
+                               total_nodes, scale, scores, scores_stride, workspace, ws_bytes, &s->scores);
+  if (st != KDA_OK || total_nodes == 0) return st;
+  st = block_select(scores, scores_stride, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs, total_nodes, blocks,
+                    first, recent, sel_table, sel_pages, sel_lengths, &s->choice);
+  if (st != KDA_OK) return st;
+  s->ws = workspace;
+  return tree_attention(q_cat, H, pool, n_pages, page_size, sel_table, sel_pages, sel_lengths, cu_nodes, n_seqs,
+                        total_nodes, mask, scale, z, z_dtype, workspace, ws_bytes, &s->attention);
+}
+static cudaError_t launch_sparse(const SparseStep &s, int *launches, cudaStream_t stream) {
+  cudaError_t e = kda::launch_block_scores(s.scores, s.ws, launches, stream);
+  if (e != cudaSuccess) return e;
+  e = kda::launch_block_select(s.choice, stream);
+  if (e != cudaSuccess) return e;
+  int more = 0;
+  e = kda::launch_mla_tree(s.attention, &more, stream);
+  *launches += 1 + more;
+  return e;
+}
+
+kda_status mla_sparse_latent(const void *q_cat, int H, const void *pool, const void *keys, int n_pages, int page_size,
+                             const int32_t *page_table, int max_pages, const int32_t *lengths, const int32_t *cu_nodes,
+                             int n_seqs, int64_t total_nodes, const int64_t *mask, float scale, int blocks, int first,
+                             int recent, float *scores, int64_t scores_stride, int32_t *sel_table, int sel_pages,
+                             int32_t *sel_lengths, void *z, kda_dtype z_dtype, void *workspace, size_t ws_bytes,
+                             cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_SPARSE_LATENT);
+  SparseStep s;
+  kda_status st = sparse_step(q_cat, H, pool, keys, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
+                              total_nodes, mask, scale, blocks, first, recent, scores, scores_stride, sel_table, sel_pages,
+                              sel_lengths, z, z_dtype, workspace, ws_bytes, &s);
+  if (st != KDA_OK || total_nodes == 0) return st;
+  int launches = 0;
+  const cudaError_t e = launch_sparse(s, &launches, stream);
+  return done(e, launches);
+}
+
+kda_status mla_sparse_decode(const void *q_nope, const void *q_rope, const void *w_uk, const void *w_uv, const void *pool,
+                             const void *keys, int n_pages, int page_size, const int32_t *page_table, int max_pages,
+                             const int32_t *lengths, const int32_t *cu_nodes, int n_seqs, int64_t total_nodes,
+                             const int64_t *mask, const void *gate_logit, float scale, int blocks, int first, int recent,
+                             float *scores, int64_t scores_stride, int32_t *sel_table, int sel_pages,
+                             int32_t *sel_lengths, void *q_cat, float *z, void *out, void *workspace, size_t ws_bytes,
+                             cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_SPARSE_DECODE);
+  SparseStep s;
+  kda::MlaArgs m;
+  kda_status st = node_projections(q_nope, q_rope, w_uk, w_uv, gate_logit, out, q_cat, z, total_nodes, &m);
+  if (total_nodes > 0 && st != KDA_OK) return st;
+  st = sparse_step(q_cat, 64, pool, keys, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
+                   total_nodes, mask, scale, blocks, first, recent, scores, scores_stride, sel_table, sel_pages,
+                   sel_lengths, z, KDA_F32, workspace, ws_bytes, &s);
+  if (st != KDA_OK || total_nodes == 0) return st;
+  int launches = 0;
+  cudaError_t e = kda::launch_mla_absorb(m, stream);
+  if (e == cudaSuccess) e = launch_sparse(s, &launches, stream);
+  if (e == cudaSuccess) e = kda::launch_mla_up_gate(m, stream);
+  return done(e, launches + 2);
 }
 
 }  // extern "C"

@@ -1,0 +1,500 @@
+// mla_select.cu -- what of a long cache is read, and what of it is kept: the keys of full blocks, the
+// selection of the largest values of a row, the compaction of an evicted sequence's rows.
+//
+// A block is a page of the latent cache: sequences that share a prefix share its full pages, and so
+// the pages' keys.  The pages of the hybrid's sources name sparse reads without an interface ("Kimi
+// K3.1 Pro: Sparse Reads ...", the index that picks positions); what is computed here:
+//   key of a page      the mean of its rows, summed in fp32, rounded once to bf16;
+//   selection          of `count` values: the first and the most recent are always taken, of the
+//                      others the largest, among equals the lower index first, ascending;
+//   eviction           a sequence keeps the selected positions; its rows move up in every layer.
+// A selection is bound by latency: a cluster of CTAs takes a row of values, finds the value that the
+// last one taken has by four passes of 8 bits over order-preserving keys (counts in shared memory, added
+// up across the cluster), and writes what is taken by two prefix sums.  Every sum is of whole numbers, so
+// the result does not depend on the order.  The moves are bound by memory.
+#include "kda_common.cuh"
+#include "kda_internal.h"
+#include "kda_tc_ptx.cuh"
+
+#include <climits>
+
+namespace kda {
+namespace {
+
+using tc::cluster_rank;
+using tc::cluster_sync;
+
+constexpr int ROW16 = 576 * 2 / 16;  // 16-byte pieces of a row
+
+__device__ __forceinline__ void flag(int *err, int bit) {
+  if (err) atomicOr(err, bit);
+}
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ bool page_known(const PagedCache &c, int page) { return page >= 0 && page < c.n_pages; }
+
+// ---- block keys -------------------------------------------------------------------------------
+
+// Units (page, layer) of the pages that filled up, CTA b taking every gridDim.x-th page: 72 threads
+// take a row's pieces, four rows at a time, four loads in flight a thread; the four sums meet in
+// shared memory.
+constexpr int BK_ROWS = 4, BK_NT = BK_ROWS * ROW16, BK_SEQS = BK_NT;
+__global__ void __launch_bounds__(BK_NT) block_keys_kernel(const PagedCache c, const int32_t *from, int n_seqs, uint4 *keys) {
+  __shared__ int s_end[BK_SEQS], s_first[BK_SEQS], s_warp[BK_NT / 32];
+  __shared__ float s_sum[BK_ROWS][576];
+  after_previous();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, layer = blockIdx.y;
+  const int group = tid / ROW16, piece = tid - group * ROW16;
+  const int64_t room = (int64_t)c.max_pages * c.page_size;
+  int64_t before = 0;  // pages of the sequences before n0
+  for (int n0 = 0; n0 < n_seqs; n0 += BK_SEQS) {
+    const int n = n0 + tid;
+    int first = 0, count = 0;
+    if (n < n_seqs) {
+      const int f = from[n], t = c.lengths[n];
+      if (f < 0 || t < 0 || t > room) {
+        if (blockIdx.x == 0 && layer == 0) flag(c.err, ERR_BAD_INDEX);
+      } else if (t > f) {
+        first = f / c.page_size, count = t / c.page_size - first;
+      }
+    }
+    int x = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < BK_NT / 32; ++w) {
+      if (w < warp) x += s_warp[w];
+      all += s_warp[w];
+    }
+    s_end[tid] = x, s_first[tid] = first;  // at most 288 x 2^20 pages
+    __syncthreads();
+    const int begin = (int)((blockIdx.x + gridDim.x - before % gridDim.x) % gridDim.x);
+    for (int u = begin; u < all; u += gridDim.x) {
+      int lo = 0, hi = BK_SEQS - 1;  // the first sequence whose pages end behind u
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s_end[mid] > u) hi = mid;
+        else lo = mid + 1;
+      }
+      const int j = s_first[lo] + u - (lo > 0 ? s_end[lo - 1] : 0);
+      const int page = c.table[(size_t)(n0 + lo) * c.max_pages + j];
+      if (!page_known(c, page)) {
+        if (tid == 0 && layer == 0) flag(c.err, ERR_BAD_INDEX);
+        continue;
+      }
+      const uint4 *rows = reinterpret_cast<const uint4 *>(c.pool) + ((size_t)layer * c.n_pages + page) * c.page_size * ROW16 + piece;
+      float sum[8] = {};
+      auto add = [&](const uint4 &v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) sum[2 * y] += __uint_as_float(w[y] << 16), sum[2 * y + 1] += __uint_as_float(w[y] & 0xffff0000u);
+      };
+      for (int r = group; r < c.page_size; r += 4 * BK_ROWS) {  // pages hold 16 rows at least
+        uint4 v[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) v[y] = __ldcs(rows + (size_t)(r + BK_ROWS * y) * ROW16);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) add(v[y]);
+      }
+      __syncthreads();  // the sums of the page before are read
+#pragma unroll
+      for (int y = 0; y < 8; ++y) s_sum[group][8 * piece + y] = sum[y];
+      __syncthreads();
+      if (tid < ROW16) {
+        const float f = 1.f / c.page_size;  // a power of two
+        uint32_t w[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          float m[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int i = 8 * tid + 2 * y + z;
+            m[z] = ((s_sum[0][i] + s_sum[1][i]) + (s_sum[2][i] + s_sum[3][i])) * f;
+          }
+          const __nv_bfloat162 b = __floats2bfloat162_rn(m[0], m[1]);
+          w[y] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        keys[((size_t)layer * c.n_pages + page) * ROW16 + tid] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    before += all;
+    __syncthreads();
+  }
+}
+
+// ---- selection --------------------------------------------------------------------------------
+
+// A number whose order is the values': NaN below everything, -0 equal to 0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+
+constexpr int SEL_NT = 1024;
+template <bool EVICT>
+__global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
+  __shared__ int s_hist[2][256];
+  __shared__ int s_bins[256];
+  __shared__ uint32_t s_digit;
+  __shared__ int s_need;
+  __shared__ unsigned long long s_warp[SEL_NT / 32], s_all;  // taken for sure | equal to the threshold
+  __shared__ int s_gap, s_bad;
+  after_previous();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cs = (int)cluster_ctas(), rank = (int)cluster_rank(), n = blockIdx.x / cs;
+  const int page_size = a.c.page_size;
+  const int64_t room = (int64_t)a.c.max_pages * page_size;
+  const int len = a.c.lengths[n];
+  const float *value = a.values + (size_t)n * a.stride;
+  const int32_t *table = a.c.table + (size_t)n * a.c.max_pages;
+  int count, tail = 0;  // values; pages behind the full blocks
+  bool ok;
+  if (EVICT) {
+    ok = len >= 0 && len <= room && len <= a.stride;
+    count = len;
+  } else {
+    const int lo = a.cu_nodes[n], hi = a.cu_nodes[n + 1];
+    int W = hi - lo;
+    if (lo < 0 || hi < lo || hi > a.total || W > 64) {
+      if (rank == 0 && tid == 0) flag(a.c.err, ERR_BAD_SEQLEN);
+      W = 0;
+    }
+    count = len / page_size;
+    ok = len >= 0 && (int64_t)len + W <= room;
+    tail = ok ? (int)(((int64_t)len + W + page_size - 1) / page_size) - count : 0;
+    if (ok && W > 0) ok = (count < a.most ? count : a.most) + tail <= a.out_stride;
+    if (W == 0) ok = false;  // nothing to attend from: an empty selection, and no error
+    else if (!ok && rank == 0 && tid == 0) flag(a.c.err, ERR_BAD_INDEX);
+  }
+  int32_t *out = a.out + (size_t)n * a.out_stride;
+  if (!ok) {
+    for (int64_t j = rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT) out[j] = -1;
+    if (rank == 0 && tid == 0) {
+      if (EVICT) flag(a.c.err, ERR_BAD_INDEX);
+      a.out_lengths[n] = EVICT ? len : 0;
+    }
+    return;
+  }
+  const int most = a.most, take = count < most ? count : most;
+  const int lo = a.first, hi = count - a.recent;  // where values decide (count > most)
+  uint32_t threshold = 0;
+  int need = 0;  // of the values equal to it
+  // this thread's values, in order
+  const int per = (count + cs * SEL_NT - 1) / (cs * SEL_NT);
+  const int64_t j0 = (int64_t)(rank * SEL_NT + tid) * per;
+  const int begin = j0 < count ? (int)j0 : count, end = j0 + per < count ? (int)j0 + per : count;
+  const bool choose = count > most;
+  if (tid == 0) s_gap = INT_MAX, s_bad = 0;
+  if (choose) {
+    need = most - a.first - a.recent;
+    const int from = begin > lo ? begin : lo, to = end < hi ? end : hi;
+    if (need > 0) {
+#pragma unroll 1
+      for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        int *hist = s_hist[pass & 1];
+        if (tid < 256) hist[tid] = 0;
+        __syncthreads();
+        for (int j = from; j < to; ++j) {
+          const uint32_t k = order_key(value[j]);
+          if (pass == 0 || k >> (shift + 8) == threshold >> (shift + 8)) atomicAdd(&hist[k >> shift & 255], 1);
+        }
+        if (cs > 1) cluster_sync();
+        else __syncthreads();
+        if (tid < 256) {
+          int sum = 0;
+          for (int r = 0; r < cs; ++r) sum += *(cs > 1 ? (int *)tc::map_rank(hist + tid, r) : hist + tid);
+          s_bins[tid] = sum;
+        }
+        __syncthreads();
+        if (warp == 0) {  // lane l: bins 255 - 8 l down to 248 - 8 l
+          int v[8], sum = 0;
+#pragma unroll
+          for (int y = 0; y < 8; ++y) v[y] = s_bins[255 - 8 * lane - y], sum += v[y];
+          int x = sum;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          int above = x - sum;
+          if (above < need && x >= need) {
+            int y = 0;
+            while (above + v[y] < need) above += v[y], ++y;
+            s_digit = 255 - 8 * lane - y;
+            s_need = need - above;
+          }
+        }
+        __syncthreads();
+        threshold |= s_digit << shift;
+        need = s_need;
+      }
+    } else {
+      threshold = 0xffffffffu;  // no key reaches it
+    }
+  } else {
+    __syncthreads();
+  }
+  // how many are taken before this thread's
+  auto sort_of = [&](int j) {  // 2: taken, 1: equal to the threshold, 0: not
+    if (!choose || j < lo || j >= hi) return 2;
+    const uint32_t k = order_key(value[j]);
+    return k > threshold ? 2 : k == threshold && need > 0 ? 1 : 0;
+  };
+  unsigned long long mine = 0;
+  if (choose) {
+    int gap = INT_MAX;
+    for (int j = begin; j < end; ++j) {
+      const int s = sort_of(j);
+      mine += s == 2 ? 1ull << 32 : s;
+      if (s < 2 && gap == INT_MAX) gap = j;
+    }
+    unsigned long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    unsigned long long all = 0;
+    for (int w = 0; w < SEL_NT / 32; ++w) {
+      if (w < warp) x += s_warp[w];
+      all += s_warp[w];
+    }
+    if (tid == 0) s_all = all;
+    mine = x - mine;
+    if (cs > 1) {
+      cluster_sync();
+      for (int r = 0; r < rank; ++r) mine += *(unsigned long long *)tc::map_rank(&s_all, r);
+    }
+    if (EVICT) {
+      // the first position that is not taken: of the equal ones, those behind the last needed
+      int equal = (int)(uint32_t)mine;
+      gap = INT_MAX;
+      for (int j = begin; j < end && gap == INT_MAX; ++j) {
+        const int s = sort_of(j);
+        if (s == 0 || (s == 1 && equal++ >= need)) gap = j;
+      }
+      if (gap != INT_MAX) atomicMin(&s_gap, gap);
+      if (cs > 1) cluster_sync();
+      else __syncthreads();
+      gap = INT_MAX;
+      for (int r = 0; r < cs; ++r) {
+        const int g = *(cs > 1 ? (int *)tc::map_rank(&s_gap, r) : &s_gap);
+        gap = g < gap ? g : gap;
+      }
+      // every row from there on moves: its page has to be there, and nobody else's where it goes
+      int bad = 0;
+      for (int j = gap / page_size + rank * SEL_NT + tid; j <= (count - 1) / page_size; j += cs * SEL_NT) {
+        const int p = table[j];
+        if (!page_known(a.c, p)) bad = 1;
+        else if (a.refs && j <= (most - 1) / page_size && a.refs[p] > 1) bad = 1;
+      }
+      if (bad) s_bad = 1;
+      if (cs > 1) cluster_sync();
+      else __syncthreads();
+      bad = 0;
+      for (int r = 0; r < cs; ++r) bad |= *(cs > 1 ? (int *)tc::map_rank(&s_bad, r) : &s_bad);
+      if (bad) {  // the sequence stays as it is
+        for (int64_t j = rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT) out[j] = -1;
+        if (a.new_values && a.new_values != a.values)
+          for (int j = rank * SEL_NT + tid; j < count; j += cs * SEL_NT) a.new_values[(size_t)n * a.stride + j] = value[j];
+        if (rank == 0 && tid == 0) {
+          flag(a.c.err, ERR_BAD_INDEX);
+          a.out_lengths[n] = len;
+        }
+        if (cs > 1) cluster_sync();
+        return;
+      }
+    }
+  } else {
+    mine = (unsigned long long)begin << 32;
+  }
+  int taken = (int)(mine >> 32), equal = (int)(uint32_t)mine;
+  const bool aside = EVICT && a.new_values && a.new_values != a.values;
+  float *fresh = EVICT && a.new_values ? a.new_values + (size_t)n * a.stride : nullptr;
+  for (int j = begin; j < end; ++j) {
+    const int s = sort_of(j);
+    if (s == 2 || (s == 1 && equal < need)) {
+      const int at = taken + (equal < need ? equal : need);
+      out[at] = EVICT ? j : table[j];
+      if (aside) fresh[at] = value[j];
+    }
+    if (s == 2) ++taken;
+    else equal += s;
+  }
+  for (int64_t j = take + rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT)
+    out[j] = !EVICT && j < take + tail ? table[count + (j - take)] : -1;
+  if (EVICT) {
+    if (aside) {
+      for (int j = take + rank * SEL_NT + tid; j < count; j += cs * SEL_NT) fresh[j] = 0.f;
+    } else if (fresh && choose) {
+      // in place: a batch is read before it is written, and no later one reads what it wrote (a kept
+      // position is never before its new one)
+      if (cs > 1) cluster_sync();
+      else __syncthreads();
+      if (rank == 0) {
+        for (int b = 0; b < take; b += 4 * SEL_NT) {
+          float x[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int j = b + y * SEL_NT + tid;
+            if (j < take) x[y] = value[__ldcg(out + j)];
+          }
+          __syncthreads();
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int j = b + y * SEL_NT + tid;
+            if (j < take) fresh[j] = x[y];
+          }
+          __syncthreads();
+        }
+        for (int j = take + tid; j < count; j += SEL_NT) fresh[j] = 0.f;
+      }
+    }
+  }
+  if (rank == 0 && tid == 0) a.out_lengths[n] = EVICT ? take : (int)((int64_t)take * page_size + len % page_size);
+  if (cs > 1) cluster_sync();  // its shared memory is not read by the others any more
+}
+
+// Row kept[j] of each sequence moves to row j, in every layer: a CTA takes 128 bytes of the rows, 256
+// rows at a time, which are read before they are written; kept[j] >= j and both rise, so no later batch
+// reads a row that an earlier one wrote.  The next batch's places are looked up while one is copied.
+constexpr int MV_NT = 256, MV_U = 8, MV_ROWS = MV_NT / 8, MV_BATCH = MV_ROWS * MV_U;
+__global__ void __launch_bounds__(MV_NT) evict_rows_kernel(const PagedCache c, const int32_t *kept_all, int budget) {
+  after_previous();
+  const int n = blockIdx.z, layer = blockIdx.y, piece = blockIdx.x * 8 + (threadIdx.x & 7), r = threadIdx.x >> 3;
+  const int32_t *kept = kept_all + (size_t)n * budget;
+  if (kept[budget - 1] < budget) return;  // nothing moves (or the sequence is refused)
+  const int32_t *table = c.table + (size_t)n * c.max_pages;
+  uint4 *rows = reinterpret_cast<uint4 *>(c.pool) + (size_t)layer * c.n_pages * c.page_size * ROW16 + piece;
+  const int lp = 31 - __clz(c.page_size), in_page = c.page_size - 1;
+  int64_t from[MV_U], to[MV_U];
+  auto look = [&](int b) {
+    int k[MV_U];
+#pragma unroll
+    for (int y = 0; y < MV_U; ++y) {
+      const int j = b + y * MV_ROWS + r;
+      k[y] = j < budget ? kept[j] : 0;
+    }
+#pragma unroll
+    for (int y = 0; y < MV_U; ++y) {
+      const int j = b + y * MV_ROWS + r;
+      from[y] = -1;
+      if (k[y] > j) {
+        from[y] = ((int64_t)table[k[y] >> lp] << lp) + (k[y] & in_page);
+        to[y] = ((int64_t)table[j >> lp] << lp) + (j & in_page);
+      }
+    }
+  };
+  look(0);
+  for (int b = 0; b < budget; b += MV_BATCH) {
+    uint4 x[MV_U];
+    int64_t place[MV_U];
+#pragma unroll
+    for (int y = 0; y < MV_U; ++y) {
+      place[y] = from[y] < 0 ? -1 : to[y];
+      if (from[y] >= 0) x[y] = __ldcs(rows + from[y] * ROW16);
+    }
+    if (b + MV_BATCH < budget) look(b + MV_BATCH);
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < MV_U; ++y)
+      if (place[y] >= 0) __stcs(rows + place[y] * ROW16, x[y]);
+  }
+}
+
+// The pages of the listed sequences that lie wholly behind their lengths released.
+__global__ void __launch_bounds__(128) pages_trim_kernel(PagedCache c, int32_t *table, int32_t *refs, int32_t *held, int n_slots,
+                                                         const int32_t *slots) {
+  __shared__ int s_held, s_keep;
+  after_previous();
+  const int slot = slots[blockIdx.x];
+  if (slot < 0 || slot >= n_slots) {
+    if (threadIdx.x == 0) flag(c.err, ERR_BAD_INDEX);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    const int len = c.lengths[slot];
+    int keep = len < 0 ? INT_MAX : (int)(((int64_t)len + c.page_size - 1) / c.page_size);
+    const int h = atomicMin(&held[slot], keep);  // a sequence listed twice is cut once
+    if (len < 0 || h < 0 || h > c.max_pages || h < keep) flag(c.err, ERR_BAD_INDEX);
+    s_held = h < 0 ? 0 : (h > c.max_pages ? c.max_pages : h), s_keep = keep;
+  }
+  __syncthreads();
+  for (int j = s_keep < s_held ? s_keep + (int)threadIdx.x : s_held; j < s_held; j += 128) {
+    int32_t *e = table + (size_t)slot * c.max_pages + j;
+    const int p = *e;
+    if (!page_known(c, p)) {
+      flag(c.err, ERR_BAD_INDEX);
+    } else if (atomicSub(&refs[p], 1) <= 0) {  // held by nobody: the count goes back to 0
+      atomicAdd(&refs[p], 1);
+      flag(c.err, ERR_BAD_INDEX);
+    }
+    *e = -1;
+  }
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int cluster, int threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster, at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// CTAs of a selection: eight values a thread, as long as the GPU has room for the clusters.
+int select_ctas(int n_seqs, int64_t most_values) {
+  int cs = 1;
+  while (cs < 8 && most_values > (int64_t)cs * SEL_NT * 8 && (int64_t)n_seqs * cs * 2 <= 304) cs *= 2;
+  return cs;
+}
+
+}  // namespace
+
+cudaError_t launch_block_keys(const PagedCache &c, const int32_t *from, int n_seqs, void *keys, cudaStream_t s) {
+  const int ctas = 1064 / c.n_layers;  // seven an SM
+  return launch(block_keys_kernel, dim3(ctas < 1 ? 1 : ctas, c.n_layers), 1, BK_NT, s, c, from, n_seqs, static_cast<uint4 *>(keys));
+}
+
+cudaError_t launch_block_select(const SelectArgs &a, cudaStream_t s) {
+  const int cs = select_ctas(a.n_seqs, a.c.max_pages);
+  return launch(select_kernel<false>, dim3(a.n_seqs * cs), cs, SEL_NT, s, a);
+}
+
+cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t s) {
+  const int64_t room = (int64_t)a.c.max_pages * a.c.page_size;
+  const int cs = select_ctas(a.n_seqs, room < a.stride ? room : a.stride);
+  cudaError_t e = launch(select_kernel<true>, dim3(a.n_seqs * cs), cs, SEL_NT, s, a);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  e = launch(evict_rows_kernel, dim3(ROW16 / 8, a.c.n_layers, a.n_seqs), 1, MV_NT, s, a.c, a.out, a.most);
+  ++*launches;
+  return e;
+}
+
+cudaError_t launch_pages_trim(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots, const int32_t *slots, int n,
+                              cudaStream_t s) {
+  return launch(pages_trim_kernel, dim3(n), 1, 128, s, c, const_cast<int32_t *>(c.table), refs, held, n_slots, slots);
+}
+
+}  // namespace kda

@@ -1,0 +1,627 @@
+// mla_sums.cu -- the attention that cached positions, or the keys of blocks, receive from all query
+// rows of a sequence's step.
+//
+// With the absorbed form's scores ("Ling-3.1-flash: Grouped Routing and Two Different MLA Caches",
+// section "Why weight absorption keeps the same attention function") s_rt = scale q_r . [c_t ; r_t]
+// of the rows r (nodes x heads) and lse_r = ln sum_t exp(s_rt) over what row r sees,
+//     weights_t += sum_r u_r exp(s_rt - lse_r)        (positions; u_r: the weight of r's node)
+//     score_b    = sum_r exp(s_rb - lse_r)            (blocks: the keys are the pages' mean rows)
+// Blocks take two passes, lse first: each tile's maximum and sum of a row, merged by key_lse_kernel.
+//
+// The keys are the product's M side, D[256 keys x rows] = K Q^T on a pair of CTAs (cta_group::2, 128
+// keys each), so a thread owns a key: the sum over rows runs along its own columns of tensor memory,
+// in registers, in a fixed order, and what comes out is a number per key.  A key's garbage (no page, a
+// row past the end) stays in its own lane and is never used.  A tile's keys stay in shared memory,
+// 147 KB a CTA in nine blocks of 64 channels, while the step's rows pass by: up to 128 rows are
+// resident for a whole sequence (one-token decode: the cache streams through once, block by block, as
+// the products free the blocks), more stream through a ring in chunks of 256, which cost a CTA
+// 32 bytes a cycle at the products' full rate.
+#include "kda_common.cuh"
+#include "kda_internal.h"
+#include "mla_pair.cuh"
+
+#include <atomic>
+#include <cstring>
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int TK = 576, KB = TK / 64;
+constexpr int TILE = 256, KC = 128;    // keys of a tile, of a CTA
+constexpr int RES = 128, CHUNK = 256;  // rows: at most this many are resident; of a streamed chunk
+constexpr int NQ = 4;                  // slots of the rows' ring
+constexpr uint32_t SLOT = KC * 128;
+constexpr uint32_t OFF_K = 0, OFF_Q = KB * SLOT;
+constexpr uint32_t QBYTES = KB * (RES / 2) * 128;  // the ring takes NQ x 16 KB of them
+constexpr uint32_t SMEM = OFF_Q + QBYTES + 1024;
+static_assert(NQ * (CHUNK / 2) * 128 <= QBYTES, "the ring fits the resident rows' place");
+constexpr int W_KEYS = 8, W_ROWS = 9, W_MMA = 10, NT = 352;  // warps 0-7: sums
+constexpr int MAX_CLUSTERS = 80;  // of two CTAs (152 SMs: 76)
+
+// barriers; L: the leading CTA's are used by both
+enum {
+  B_KFULL = 0,              // L  a key block is there in both CTAs
+  B_KEMPTY = B_KFULL + KB,  //    the products have read it
+  B_QFULL = B_KEMPTY + KB,  // L  a slot of streamed rows
+  B_QEMPTY = B_QFULL + NQ,
+  B_RFULL = B_QEMPTY + NQ,  // L  the resident rows
+  B_REMPTY,
+  B_DFULL,                  //    a product is done (two buffers)
+  B_DFREE = B_DFULL + 2,    // L  and read
+  B_DRAIN = B_DFREE + 2, B_N
+};
+
+struct SumMaps {
+  CUtensorMap k, q16, q64;
+};
+
+struct Seq {
+  int lo, rows, len, keys, tiles, chunks;
+};
+template <bool BLOCKS>
+__device__ __forceinline__ Seq seq_of(const KeySumArgs &a, int n, bool tell) {
+  Seq s;
+  s.lo = a.cu_nodes[n];
+  const int hi = a.cu_nodes[n + 1];
+  int W = hi - s.lo;
+  if (s.lo < 0 || hi < s.lo || hi > a.total || W > 64) {
+    if (tell && a.err) atomicOr(a.err, ERR_BAD_SEQLEN);
+    W = 0;
+  }
+  s.len = a.c.lengths[n];
+  const int64_t room = (int64_t)a.c.max_pages * a.c.page_size;
+  const int64_t last = BLOCKS ? s.len : (int64_t)s.len + W;
+  if (W > 0 && (s.len < 0 || last > room || (!BLOCKS && last > a.out_stride))) {
+    if (tell && a.err) atomicOr(a.err, ERR_BAD_INDEX);
+    s.len = 0, W = 0;
+  }
+  s.rows = W * a.H;
+  s.keys = W == 0 ? 0 : BLOCKS ? s.len / a.c.page_size : s.len + W;
+  s.tiles = (s.keys + TILE - 1) / TILE;
+  s.chunks = s.rows <= RES ? 1 : (s.rows + CHUNK - 1) / CHUNK;
+  return s;
+}
+
+// This cluster's run of (tile, chunk) units; a tile belongs to the run that its first unit falls in.
+template <bool BLOCKS>
+struct Walk {
+  int n, t;          // the next tile
+  int64_t at, stop;  // its first unit; where the run ends
+  bool fresh = true;
+  Seq s;
+  int tile;
+  bool first, last;  // of the sequence's tiles in this run
+  __device__ __forceinline__ bool next(const KeySumArgs &a) {
+    while (at < stop) {
+      if (fresh) s = seq_of<BLOCKS>(a, n, false), first = true, fresh = false;
+      else first = false;
+      if (t >= s.tiles) {
+        if (++n >= a.n_seqs) return false;
+        t = 0, fresh = true;
+        continue;
+      }
+      tile = t++;
+      at += s.chunks;
+      last = t >= s.tiles || at >= stop;
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ int columns(const Seq &s, int chunk) {  // of a chunk's product, padded
+  const int r = s.rows - CHUNK * chunk;
+  return r >= CHUNK ? CHUNK : (r + 31) & ~31;
+}
+// four rows of the block keys, 64 channels each
+__device__ __forceinline__ void tma_pair_gather4(uint32_t dst, const CUtensorMap *map, int c0, int r0, int r1, int r2, int r3,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
+}
+// Sums over the warp's lanes of 16 columns: lane l gets column l & 15's.
+__device__ __forceinline__ float columns_sum(float (&v)[16], int lane) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) v[c] += __shfl_xor_sync(0xffffffffu, v[c], 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int c = 0; c < o; ++c) {
+      const bool up = lane & o;
+      const float keep = up ? v[c + o] : v[c], give = up ? v[c] : v[c + o];
+      v[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  return v[0];
+}
+__device__ __forceinline__ float lanes_max(float x) {  // (a NaN may be passed over: it shows in the sum)
+  const int i = __float_as_int(x);
+  const int m = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
+  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+}
+
+template <bool BLOCKS, bool LSE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
+    key_sums_kernel(const KeySumArgs a, const __grid_constant__ SumMaps maps) {
+  extern __shared__ uint8_t dyn[];
+  __shared__ __align__(8) uint64_t s_bar[B_N];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile uint32_t s_abort;
+  __shared__ unsigned long long s_total, s_scan[NT / 32];
+  __shared__ int s_n, s_t;
+  __shared__ long long s_at;
+  __shared__ float2 s_col[LSE ? 4 : 2][CHUNK];  // rows' (lse, weight); LSE: a quarter's (maximum, sum)
+  __shared__ uint8_t s_node[2][LSE ? 1 : CHUNK];
+  __shared__ float s_half[2][LSE ? 1 : KC];
+  const uint32_t raw = smem_u32(dyn);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int cid = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  auto bar = [&](int i) { return smem_u32(&s_bar[i]); };
+  if (tid < B_N) {
+    int n = 1;
+    if (tid < B_KEMPTY || (tid >= B_QFULL && tid < B_QEMPTY) || tid == B_RFULL) n = 2;  // a loader of each CTA
+    if (tid == B_DFREE || tid == B_DFREE + 1) n = 16;                                 // the sums' warps
+    mbar_init(bar(tid), n);
+    mbar_fence_init();
+  }
+  if (tid == 64) s_abort = 0, s_total = 0, s_n = 0, s_t = 0, s_at = 0;
+  if (tid >= 96 && tid < 99) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k + (tid - 96)) : "memory");
+  if (warp == W_MMA) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  // launched while the kernel before runs out: nothing of global memory is read or written above
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // barriers and tensor memory are there in this CTA; waited for below
+
+  // ---- this cluster's run of the batch's units -------------------------------------------------
+  {
+    unsigned long long mine = 0;
+    for (int n = tid; n < a.n_seqs; n += NT) {
+      const Seq s = seq_of<BLOCKS>(a, n, blockIdx.x == 0);
+      mine += (unsigned long long)s.tiles * s.chunks;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0 && mine) atomicAdd(&s_total, mine);
+  }
+  __syncthreads();
+  const long long total = (long long)s_total;
+  const long long begin = total * cid / clusters, stop = total * (cid + 1) / clusters;
+  if (stop > begin) {  // the first tile whose first unit is at or behind `begin`
+    long long before = 0;
+    for (int n0 = 0; n0 < a.n_seqs && before <= begin; n0 += NT) {
+      Seq s = {};
+      if (n0 + tid < a.n_seqs) s = seq_of<BLOCKS>(a, n0 + tid, false);
+      const long long cost = (long long)s.tiles * s.chunks;
+      long long x = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) s_scan[warp] = x;
+      __syncthreads();
+      long long ahead = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < NT / 32; ++w) {
+        const long long v = s_scan[w];
+        if (w < warp) ahead += v;
+        all += v;
+      }
+      const long long at = before + ahead + x - cost;
+      if (at <= begin && begin < at + cost) {
+        const int t = (int)((begin - at + s.chunks - 1) / s.chunks);
+        s_n = n0 + tid, s_t = t, s_at = at + (long long)t * s.chunks;
+      }
+      before += all;
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tm = s_tmem;
+  Walk<BLOCKS> walk;
+  walk.n = s_n, walk.t = s_t, walk.at = s_at, walk.stop = stop > begin ? stop : s_at;
+  // A wait that runs out raises s_abort; from then on waits fail at once.  The warps of the sums walk
+  // on to the end without waiting (they meet on a named barrier), the others issue nothing more.
+  auto wait = [&](int i, uint32_t parity) {
+#pragma unroll 1
+    for (long it = 0; it < kWaitLimit; ++it) {
+      if (mbar_try_wait(bar(i), parity & 1)) return true;
+      if (s_abort) return false;
+    }
+    s_abort = 1;
+    return false;
+  };
+  auto warp_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
+  // the leading CTA's barrier expects both CTAs' bytes; the other CTA only arrives (its bytes cannot
+  // come before the phase they belong to: its place was freed by that phase's products)
+  auto announce = [&](int i, uint32_t bytes) {
+    if (rank == 0) mbar_expect_tx(bar(i), 2 * bytes);
+    else arrive_pair(map_shared_rank(bar(i), 0));
+  };
+  const int lp = 31 - __clz(a.c.page_size);
+
+  if (warp == W_KEYS) {
+    // ---- key blocks: a lane a tile load ---------------------------------------------------------
+    const int box = a.c.page_size < 64 ? a.c.page_size : 64, lb = 31 - __clz(box), in_page = a.c.page_size - 1;
+    uint64_t policy;  // the cache's rows are read once
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    int tiles = 0;
+    while (walk.next(a)) {
+      const int p0 = TILE * walk.tile + KC * (int)rank;
+      const int32_t *row = a.c.table + (size_t)walk.n * a.c.max_pages;
+      auto known = [&](int page) { return page >= 0 && page < a.c.n_pages; };
+      int page[4];
+      if (BLOCKS) {  // blocks 4 lane ..; one without a page is not used: any row stands for it
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int b = p0 + 4 * lane + y;
+          page[y] = b < walk.s.keys ? row[b] : 0;
+          if (!known(page[y])) {
+            if (LSE && a.err) atomicOr(a.err, ERR_BAD_INDEX);
+            page[y] = 0;
+          }
+        }
+      } else {  // positions box lane ..; past the pool, where loads give zeros, for one without a page
+        const int p = p0 + (lane << lb);
+        const bool here = (lane << lb) < KC && p < walk.s.keys;
+        page[0] = here ? row[p >> lp] : a.c.n_pages;
+        if (!known(page[0])) {
+          if (here && a.err) atomicOr(a.err, ERR_BAD_INDEX);
+          page[0] = a.c.n_pages;
+        }
+      }
+#pragma unroll 1
+      for (int kb = 0; kb < KB; ++kb) {
+        if (tiles > 0 && !warp_wait(B_KEMPTY + kb, (uint32_t)(tiles - 1))) continue;
+        if (lane == 0) announce(B_KFULL + kb, SLOT);
+        __syncwarp();
+        const uint32_t full = map_shared_rank(bar(B_KFULL + kb), 0), dst = sb + OFF_K + kb * SLOT;
+        if (BLOCKS)
+          tma_pair_gather4(dst + lane * 512, &maps.k, 64 * kb, page[0], page[1], page[2], page[3], full);
+        else if ((lane << lb) < KC)
+          tma_pair_3d(dst + (lane << lb) * 128, &maps.k, 64 * kb, (p0 + (lane << lb)) & in_page, page[0], full, policy);
+      }
+      ++tiles;
+    }
+    if (tiles > 0)
+      for (int kb = 0; kb < KB; ++kb) wait(B_KEMPTY + kb, (uint32_t)(tiles - 1));  // read before the CTA may end
+    if (s_abort)  // a wait ran out: let the copies in flight land
+      for (int y = 0; y < 100; ++y) __nanosleep(10000);
+  } else if (warp == W_ROWS) {
+    // ---- query rows: resident for a sequence, or a chunk's 64 channels at a time -----------------
+    int segs = 0;      // resident uses so far
+    int j = 0, used = 0;
+    uint32_t par = 1;  // parity that a slot's last use ends (a fresh barrier counts as ended)
+    bool ring = false;  // the ring's slots hold what was read last
+    while (walk.next(a)) {
+      const int64_t row0 = (int64_t)walk.s.lo * a.H;
+      if (walk.s.rows <= RES) {
+        if (!walk.first) continue;
+        if (segs > 0) warp_wait(B_REMPTY, (uint32_t)(segs - 1));
+        if (ring) {  // every slot read
+          for (int y = 0; y < NQ && y < used; ++y) {
+            const int k = (j + NQ - 1 - y) % NQ;
+            warp_wait(B_QEMPTY + k, k < j ? par ^ 1 : par);
+          }
+          ring = false;
+        }
+        const int half = columns(walk.s, 0) / 2, boxes = half / 16;
+        if (lane == 0) announce(B_RFULL, (uint32_t)(KB * half * 128));
+        __syncwarp();
+        const uint32_t full = map_shared_rank(bar(B_RFULL), 0);
+        for (int x = lane; x < KB * boxes; x += 32) {
+          const int kb = x / boxes, b = x - kb * boxes;
+          if (!s_abort)
+            tma_pair_3d(sb + OFF_Q + kb * half * 128 + b * 2048, &maps.q16, 64 * kb, (int)(row0 + half * (int)rank + 16 * b), 0,
+                        full);
+        }
+        ++segs;
+      } else {
+        if (!ring && segs > 0) warp_wait(B_REMPTY, (uint32_t)(segs - 1));
+        ring = true;
+        for (int ch = 0; ch < walk.s.chunks; ++ch) {
+          const int half = columns(walk.s, ch) / 2;
+          const int64_t r = row0 + CHUNK * ch + half * (int)rank;
+#pragma unroll 1
+          for (int kb = 0; kb < KB; ++kb) {
+            if (warp_wait(B_QEMPTY + j, par)) {
+              if (lane == 0) announce(B_QFULL + j, (uint32_t)half * 128);
+              __syncwarp();
+              const uint32_t full = map_shared_rank(bar(B_QFULL + j), 0), dst = sb + OFF_Q + j * (CHUNK / 2) * 128;
+              if (half == CHUNK / 2) {
+                if (lane < 2) tma_pair_3d(dst + lane * 8192, &maps.q64, 64 * kb, (int)r + 64 * lane, 0, full);
+              } else if (lane < half / 16) {
+                tma_pair_3d(dst + lane * 2048, &maps.q16, 64 * kb, (int)r + 16 * lane, 0, full);
+              }
+            }
+            if (used < NQ) ++used;
+            if (++j == NQ) j = 0, par ^= 1;
+          }
+        }
+      }
+    }
+    if (segs > 0) wait(B_REMPTY, (uint32_t)(segs - 1));
+    for (int y = 0; y < used; ++y) {
+      const int k = (j + NQ - 1 - y) % NQ;
+      wait(B_QEMPTY + k, k < j ? par ^ 1 : par);
+    }
+    if (s_abort)
+      for (int y = 0; y < 100; ++y) __nanosleep(10000);
+  } else if (warp == W_MMA) {
+    // ---- products (one thread of the leading CTA) --------------------------------------------
+    if (rank == 0 && elect()) {
+      int i = 0, j = 0, tiles = 0, segs = 0;
+      uint32_t par = 0;
+      bool ok = true;
+      while (ok && walk.next(a)) {
+        const bool res = walk.s.rows <= RES;
+        if (res && walk.first && !(ok = wait(B_RFULL, (uint32_t)segs))) break;
+        for (int ch = 0; ch < walk.s.chunks && ok; ++ch, ++i) {
+          const int N = columns(walk.s, ch);
+          const uint32_t id = idesc(1, 256, (uint32_t)N, 0, 0), d = tm + CHUNK * (i & 1);
+          if (i >= 2 && !(ok = wait(B_DFREE + (i & 1), (uint32_t)((i >> 1) - 1)))) break;
+#pragma unroll 1
+          for (int kb = 0; kb < KB; ++kb) {
+            if (ch == 0 && !(ok = wait(B_KFULL + kb, (uint32_t)tiles))) break;
+            if (!res && !(ok = wait(B_QFULL + j, par))) break;
+            tc_fence_after();
+            const uint64_t ad = sdesc_sw128(sb + OFF_K + kb * SLOT, 16, 1024);
+            const uint64_t bd = sdesc_sw128(sb + OFF_Q + (res ? kb * (N / 2) * 128 : j * (CHUNK / 2) * 128), 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) mma2(d, ad + 2 * ks, bd + 2 * ks, id, kb > 0 || ks > 0);
+            if (!res) {
+              commit2(bar(B_QEMPTY + j));
+              if (++j == NQ) j = 0, par ^= 1;
+            }
+            if (ch == walk.s.chunks - 1) commit2(bar(B_KEMPTY + kb));
+          }
+          if (!ok) break;
+          commit2(bar(B_DFULL + (i & 1)));
+        }
+        if (ok && res && walk.last) {
+          commit2(bar(B_REMPTY));
+          ++segs;
+        }
+        ++tiles;
+      }
+      if (!ok) {  // a wait ran out: let the products in flight end
+        commit2(bar(B_DRAIN));
+        mbar_wait(bar(B_DRAIN), 0);
+      }
+    }
+  } else {
+    // ---- sums: lane l of tensor memory is the CTA's key l; warp w reads lanes 32 (w & 3) .. and
+    //      half w >> 2 of the columns
+    const int qw = warp & 3, hf = warp >> 2;
+    const uint32_t lanes = (uint32_t)(32 * qw) << 16;
+    const uint32_t lead = map_shared_rank(bar(0), 0);
+    int i = 0, loads = 0, tiles = 0;
+    while (walk.next(a)) {
+      const Seq s = walk.s;
+      const int p0 = TILE * walk.tile + KC * (int)rank, p = p0 + 32 * qw + lane;
+      // the nodes that see this thread's key, as bits
+      unsigned long long vis = 0;
+      if (p < s.keys) {
+        const int page = a.c.table[(size_t)walk.n * a.c.max_pages + (BLOCKS ? p : p >> lp)];
+        if (page >= 0 && page < a.c.n_pages) {
+          if (BLOCKS || p < s.len) {
+            vis = ~0ull;
+          } else {  // a drafted row
+            const int jn = p - s.len, W = s.keys - s.len;
+            for (int x = 0; x < W; ++x)
+              vis |= (unsigned long long)(a.mask ? (a.mask[s.lo + x] >> jn) & 1 : jn <= x) << x;
+          }
+        }
+      }
+      const bool none = __all_sync(0xffffffffu, vis == 0), whole = __all_sync(0xffffffffu, vis == ~0ull);
+      float *out = nullptr;
+      float old = 0.f;
+      if (!LSE && hf == 0 && (BLOCKS ? p < s.keys : vis != 0)) {
+        out = a.out + (size_t)walk.n * a.out_stride + p;
+        if (!BLOCKS) old = *out;
+      }
+      float acc = 0.f;
+      for (int ch = 0; ch < s.chunks; ++ch, ++i) {
+        const int N = columns(s, ch), c0 = hf * (N / 2), c1 = c0 + N / 2;
+        if (!LSE && (s.chunks > 1 || walk.first)) {
+          const int b = loads & 1, r = CHUNK * ch + tid;
+          float2 x = make_float2(0.f, 0.f);
+          int node = 0;
+          if (r < s.rows) {
+            node = r / a.H;
+            x.x = a.lse[(int64_t)s.lo * a.H + r] * 1.4426950408889634f;
+            x.y = a.node_weight ? a.node_weight[s.lo + node] : 1.f;
+            if (x.x == -INFINITY) x.y = 0.f;  // a row that sees nothing
+          }
+          s_col[b][tid] = x;
+          s_node[b][tid] = (uint8_t)node;
+          ++loads;
+          bar_sync(1, 256);  // two buffers: the next but one is written behind the next barrier
+        }
+        const int b = (loads - 1) & 1;
+        wait(B_DFULL + (i & 1), (uint32_t)(i >> 1));
+        tc_fence_after();
+        const uint32_t d = tm + lanes + CHUNK * (i & 1);
+        if (!LSE) {
+          if (!none) {
+#pragma unroll 2
+            for (int c = c0; c < c1; c += 16) {
+              float v[16];
+              tmem_ld16(d + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 16; ++y) {
+                const float2 x = s_col[b][c + y];
+                const float e = ex2(fmaf(v[y], a.scale_log2, -x.x));
+                if (x.y != 0.f && (whole || (vis >> s_node[b][c + y]) & 1)) acc = fmaf(x.y, e, acc);
+              }
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = c0; c < c1; c += 16) {
+            float v[16], top = 0.f;
+            tmem_ld16(d + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+              const float x = vis ? v[y] * a.scale_log2 : -INFINITY;
+              const float m = lanes_max(x);
+              if ((lane & 15) == y) top = m;
+              v[y] = ex2(x - (m == -INFINITY ? 0.f : m));
+            }
+            const float sum = columns_sum(v, lane);
+            if (lane < 16) s_col[qw][c + lane] = make_float2(top, sum);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_pair(lead + 8 * (B_DFREE + (i & 1)));
+        if (LSE) {
+          bar_sync(1, 256);
+          const int r = CHUNK * ch + tid;
+          if (r < s.rows && tid < N) {
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) m = fmaxf(m, s_col[x][tid].x);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float2 y = s_col[x][tid];
+              if (y.x != -INFINITY) l = fmaf(ex2(y.x - m), y.y, l);
+            }
+            a.part[((int64_t)s.lo * a.H + r) * a.part_stride + 2 * walk.tile + rank] = make_float2(m, l);
+          }
+          bar_sync(1, 256);
+        }
+      }
+      if (!LSE) {
+        if (hf == 1) s_half[tiles & 1][32 * qw + lane] = acc;
+        bar_sync(1, 256);  // two buffers here too
+        if (out) *out = old + (acc + s_half[tiles & 1][32 * qw + lane]);
+      }
+      ++tiles;
+    }
+  }
+  if (lane == 0 && s_abort && a.err) atomicOr(a.err, ERR_MBAR_TIMEOUT);
+  __syncwarp();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == W_MMA)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u));
+}
+
+// lse of each row over its sequence's blocks, from the tiles' (maximum, sum): a warp a row.
+constexpr int LNT = 256;
+__global__ void __launch_bounds__(LNT) key_lse_kernel(const KeySumArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
+  const Seq s = seq_of<true>(a, blockIdx.x, false);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = blockIdx.y * (LNT / 32) + warp; r < s.rows; r += gridDim.y * (LNT / 32)) {
+    const float2 *part = a.part + ((int64_t)s.lo * a.H + r) * a.part_stride;
+    float M = -INFINITY, L = 0.f;
+    for (int t = lane; t < 2 * s.tiles; t += 32) M = fmaxf(M, part[t].x);
+    M = warp_max(M);
+    for (int t = lane; t < 2 * s.tiles; t += 32)
+      if (part[t].x != -INFINITY) L = fmaf(ex2(part[t].x - M), part[t].y, L);
+    L = warp_sum(L);
+    if (lane == 0) a.lse[(int64_t)s.lo * a.H + r] = (M + log2f(L)) * 0.6931471805599453f;
+  }
+}
+
+// rows of the block keys, [n_pages][576], for gathers
+bool gather_map(CUtensorMap *m, const void *ptr, int64_t rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {TK, (cuuint64_t)rows}, strides[1] = {TK * 2};
+  cuuint32_t bx[2] = {64, 1}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BLOCKS, bool LSE>
+cudaError_t launch_sums(const KeySumArgs &a, const SumMaps &maps, cudaStream_t s) {
+  int dev = 0, nsm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int> sms[64];  // SMs of a device once the kernel is opted in there (idempotent if raced)
+  if (dev < 64) nsm = sms[dev].load();
+  if (nsm == 0) {
+    e = cudaFuncSetAttribute(key_sums_kernel<BLOCKS, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) sms[dev].store(nsm);
+  }
+  const int clusters = nsm / 2 < 1 ? 1 : (nsm / 2 < MAX_CLUSTERS ? nsm / 2 : MAX_CLUSTERS);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute early;  // each launch overlaps the end of the kernel before
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early, cfg.numAttrs = 1, cfg.stream = s;
+  cfg.gridDim = dim3(2 * clusters), cfg.blockDim = dim3(NT), cfg.dynamicSmemBytes = SMEM;
+  return cudaLaunchKernelEx(&cfg, key_sums_kernel<BLOCKS, LSE>, a, maps);
+}
+
+bool row_maps(const KeySumArgs &a, SumMaps *maps) {
+  const int64_t rows = a.total * a.H;
+  return tree_map(&maps->q16, a.q, true, TK, rows, 1, 64, 16) && tree_map(&maps->q64, a.q, true, TK, rows, 1, 64, 64);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_weights(const KeySumArgs &a, cudaStream_t s) {
+  SumMaps maps;
+  memset(&maps, 0, sizeof maps);
+  const int box = a.c.page_size < 64 ? a.c.page_size : 64;
+  if (!row_maps(a, &maps) || !tree_map(&maps.k, a.c.pool, true, TK, a.c.page_size, a.c.n_pages, 64, box))
+    return cudaErrorInvalidValue;
+  return launch_sums<false, false>(a, maps, s);
+}
+
+// rows' lse, then the tiles' (maximum, sum) of each: two for every 256 of a table row's blocks
+static int64_t score_tiles(int max_pages) { return 2 * (((int64_t)max_pages + TILE - 1) / TILE); }
+size_t block_scores_ws_bytes(int64_t total, int H, int max_pages) {
+  const size_t lse = ((size_t)total * H * sizeof(float) + 15) & ~(size_t)15;
+  return lse + (size_t)total * H * score_tiles(max_pages) * sizeof(float2);
+}
+
+cudaError_t launch_block_scores(const KeySumArgs &args, void *ws, int *launches, cudaStream_t s) {
+  KeySumArgs a = args;
+  a.lse = static_cast<float *>(ws);
+  a.part = reinterpret_cast<float2 *>(static_cast<char *>(ws) + (((size_t)a.total * a.H * sizeof(float) + 15) & ~(size_t)15));
+  a.part_stride = score_tiles(a.c.max_pages);
+  SumMaps maps;
+  memset(&maps, 0, sizeof maps);
+  if (!row_maps(a, &maps) || !gather_map(&maps.k, a.c.pool, a.c.n_pages)) return cudaErrorInvalidValue;
+  cudaError_t e = launch_sums<true, true>(a, maps, s);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early, cfg.numAttrs = 1, cfg.stream = s;
+  cfg.gridDim = dim3(a.n_seqs, 4), cfg.blockDim = dim3(LNT);
+  e = cudaLaunchKernelEx(&cfg, key_lse_kernel, (const KeySumArgs)a);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  e = launch_sums<true, false>(a, maps, s);
+  ++*launches;
+  return e;
+}
+
+}  // namespace kda

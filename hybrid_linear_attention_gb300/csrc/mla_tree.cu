@@ -43,7 +43,7 @@
 // sequence leaves partial sums, which tree_combine_kernel merges in a fixed order.
 #include "kda_common.cuh"
 #include "kda_internal.h"
-#include "kda_tc_ptx.cuh"
+#include "mla_pair.cuh"
 
 #include <atomic>
 #include <cstring>
@@ -100,60 +100,6 @@ struct Merge {
   int first, last;          // workers that hold parts of it
   int group, pad[3];
 };
-
-__device__ __forceinline__ bool elect() {  // one lane of the (whole) warp
-  uint32_t p;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-  return p != 0;
-}
-__device__ __forceinline__ float ex2(float x) {  // 2^x, relative error about 2^-22
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc));
-}
-// arrive on this barrier in both CTAs once the products issued so far are done
-__device__ __forceinline__ void commit2(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-// tile load into this CTA, completing on a barrier of the pair (shared::cluster address)
-__device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-      : "memory");
-}
-// the same with an L2 eviction policy
-__device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar,
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
-      : "memory");
-}
-// Arrive n times on a barrier of the pair (shared::cluster address).  What a thread wrote before is
-// in its own SM's shared and tensor memory, where the products read it: a CTA-scope release is
-// enough (a cluster-scope one costs the thread a fence of about a thousand cycles).
-__device__ __forceinline__ void arrive_pair(uint32_t cluster_bar, uint32_t n = 1) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// the stores before the last one have read their shared memory
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
-__device__ __forceinline__ void bar_sync(int id, int n) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
 
 // A sequence as the kernel sees it: rows of its nodes, visible positions, tiles.
 struct Seq {
@@ -216,9 +162,12 @@ __device__ __forceinline__ int worker_of(int64_t tiles, int64_t t, int workers) 
   const int64_t x = (t + 1) * workers - 1;
   return ((x | tiles) >> 32) == 0 ? (int)((uint32_t)x / (uint32_t)tiles) : (int)(x / tiles);
 }
+// LSE: a row's log-sum of exponentials is asked for too.  It comes from the weights before they are
+// rounded (the normaliser's rounded ones would put it off by up to 2^-9), in sums of its own.
+template <bool LSE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     tree_attn_kernel(const TreeAttnArgs a, const __grid_constant__ TreeMaps maps, float *part, float *part_ml,
-                     Merge *merge) {
+                     Merge *merge, float *part_e) {
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t s_bar[B_N];
   __shared__ uint32_t s_tmem;
@@ -226,7 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   __shared__ unsigned long long s_cost[4];
   __shared__ uint32_t s_scan[NT / 32];
   __shared__ int s_n, s_off, s_page[2][16];
-  __shared__ float s_max[2][4][RC], s_sum[4][RC];
+  __shared__ float s_max[2][4][RC], s_sum[4][RC], s_exp[4][LSE ? RC : 1];
   const uint32_t raw = smem_u32(dyn);
   const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
   uint8_t *sm = dyn + pad;
@@ -645,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         if (s.W < 64) seen &= (1ull << s.W) - 1;
         if (s.end == 0) seen = 0;  // a bad length: nothing is there
       }
-      float ref = -INFINITY, sum = 0.f;
+      float ref = -INFINITY, sum = 0.f, sum_e = 0.f;
       if (rows <= 0) i += walk.t1 - walk.t0;  // a row tile of one CTA: this one's products are not used
       for (int t = walk.t0; t < walk.t1 && rows > 0; ++t, ++i) {
         const int buf = i & 1;
@@ -694,11 +643,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           ref = m;
         }
         const float base = ref == -INFINITY ? 0.f : ref;
-        float ls = 0.f;
+        float ls = 0.f, le = 0.f;
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
           const float e0 = ex2(fmaf(v[2 * c], a.scale_log2, -base)), e1 = ex2(fmaf(v[2 * c + 1], a.scale_log2, -base));
+          if (LSE) le += e0 + e1;
           const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
           w[c] = *reinterpret_cast<const uint32_t *>(&b);
           // weights are rounded to bf16, the product's operands (two parts each would double its time): 2^-8 of a
@@ -707,6 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           ls += __uint_as_float(w[c] << 16) + __uint_as_float(w[c] & 0xffff0000u);
         }
         sum = sum * al + ls;
+        if (LSE) sum_e = sum_e * al + le;
         // the last tile's first products are done, so both CTAs have scaled Z for it: this tile's turn
         if (i > 0) wait(B_PFREE, (uint32_t)(i - 1));
         if (__any_sync(0xffffffffu, al != 1.f)) {
@@ -741,6 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       if (rows > 0) {
         wait(B_ZFULL, (uint32_t)(i - 1));
         s_sum[quarter][row] = sum;
+        if (LSE) s_exp[quarter][row] = sum_e;
         bar_sync(1, 256);
         const float l = (s_sum[0][row] + s_sum[1][row]) + (s_sum[2][row] + s_sum[3][row]);
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -814,6 +766,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           ml[0] = ref;
           ml[1] = l;
         }
+        if (LSE && quarter == 0 && row < rows) {
+          const float e = (s_exp[0][row] + s_exp[1][row]) + (s_exp[2][row] + s_exp[3][row]);
+          if (whole) a.lse[(int64_t)s.lo * a.H + r0 + row] = (ref + log2f(e)) * 0.6931471805599453f;
+          else part_e[(size_t)slot * 2 * RC + RC * rank + row] = e;
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -841,8 +798,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 // parts in turn and add up in a fixed order (one sequence x 4 nodes x 16384 positions, 64 parts: 41 us
 // for both kernels with a warp a row by the last worker's blocks, 29 so; one x 1 x 65536 59 and 36).
 constexpr int CNT = 256, CW = CNT / 32, CY = 2 * RC / CW;
+template <bool LSE>
 __global__ void __launch_bounds__(CNT) tree_combine_kernel(const TreeAttnArgs a, const float *part, const float *part_ml,
-                                                           const Merge *merge) {
+                                                           const Merge *merge, const float *part_e) {
   __shared__ __align__(16) float s_z[CW][TL];
   __shared__ float s_l[CW];
   // launched while the attention kernel runs out: its results are there once this returns
@@ -863,6 +821,16 @@ __global__ void __launch_bounds__(CNT) tree_combine_kernel(const TreeAttnArgs a,
     float M = -INFINITY;
     for (int w = first + lane; w <= last; w += 32) M = fmaxf(M, part_ml[slot(w) * 2]);
     M = warp_max(M);
+    if (LSE && slice == 0) {
+      float e = 0.f;
+      for (int w = first + lane; w <= last; w += 32) {
+        const size_t s = slot(w);
+        const float m = part_ml[s * 2];
+        e += m == -INFINITY ? (part_e[s] == 0.f ? 0.f : part_e[s]) : exp2f(m - M) * part_e[s];
+      }
+      e = warp_sum(e);
+      if (lane == 0) a.lse[(int64_t)g.row0 + row] = (M + log2f(e)) * 0.6931471805599453f;
+    }
 #pragma unroll 2
     for (int w = first + slice; w <= last; w += k) {
       const size_t s = slot(w);
@@ -906,28 +874,16 @@ __global__ void __launch_bounds__(CNT) tree_combine_kernel(const TreeAttnArgs a,
   }
 }
 
-// [d2][d1][cols], the innermost contiguous, in boxes of box_cols x box_rows
-bool tree_map(CUtensorMap *m, const void *ptr, bool bits, int cols, int64_t d1, int64_t d2, int box_cols, int box_rows) {
-  auto fn = tensor_map_encoder();
-  if (!fn) return false;
-  const int width = bits ? 2 : 4;
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)d1, (cuuint64_t)d2};
-  cuuint64_t strides[2] = {(cuuint64_t)cols * width, (cuuint64_t)d1 * cols * width};
-  cuuint32_t bx[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
-  return fn(m, bits ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(ptr), dims,
-            strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_cols * width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 constexpr size_t PART = (size_t)MAX_CLUSTERS * 2 * 2 * RC * TL * sizeof(float);
+constexpr size_t PART_E = (size_t)MAX_CLUSTERS * 2 * 2 * RC * sizeof(float);
 constexpr size_t PART_ML = (size_t)MAX_CLUSTERS * 2 * 2 * RC * 2 * sizeof(float);
 
 }  // namespace
 
-size_t mla_tree_ws_bytes(int, int64_t, int) { return PART + PART_ML + MAX_CLUSTERS * sizeof(Merge); }
+size_t mla_tree_ws_bytes(int, int64_t, int) { return PART + PART_ML + MAX_CLUSTERS * sizeof(Merge) + PART_E; }
 
-cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s) {
+template <bool LSE>
+static cudaError_t launch_tree_attention(const TreeAttnArgs &a, int *launches, cudaStream_t s) {
   *launches = 0;
   TreeMaps maps;
   memset(&maps, 0, sizeof maps);
@@ -944,7 +900,7 @@ cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s
   static std::atomic<int> sms[64];  // SMs of a device once the kernel is opted in there (idempotent if raced)
   if (dev < 64) nsm = sms[dev].load();
   if (nsm == 0) {
-    e = cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    e = cudaFuncSetAttribute(tree_attn_kernel<LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     if (dev < 64) sms[dev].store(nsm);
@@ -953,19 +909,25 @@ cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s
   float *part = reinterpret_cast<float *>(a.ws);
   float *part_ml = reinterpret_cast<float *>(reinterpret_cast<char *>(a.ws) + PART);
   Merge *merge = reinterpret_cast<Merge *>(reinterpret_cast<char *>(a.ws) + PART + PART_ML);
+  float *part_e = reinterpret_cast<float *>(merge + MAX_CLUSTERS);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute early;  // each launch overlaps the end of the kernel before
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early, cfg.numAttrs = 1, cfg.stream = s;
   cfg.gridDim = dim3(2 * clusters), cfg.blockDim = dim3(NT), cfg.dynamicSmemBytes = SMEM;
-  e = cudaLaunchKernelEx(&cfg, tree_attn_kernel, a, maps, part, part_ml, merge);
+  e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<LSE>, a, maps, part, part_ml, merge, part_e);
   if (e != cudaSuccess) return e;
   ++*launches;
   cfg.gridDim = dim3(clusters, CY), cfg.blockDim = dim3(CNT), cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, tree_combine_kernel, a, (const float *)part, (const float *)part_ml, (const Merge *)merge);
+  e = cudaLaunchKernelEx(&cfg, tree_combine_kernel<LSE>, a, (const float *)part, (const float *)part_ml, (const Merge *)merge,
+                         (const float *)part_e);
   ++*launches;
   return e;
+}
+
+cudaError_t launch_mla_tree(const TreeAttnArgs &a, int *launches, cudaStream_t s) {
+  return a.lse ? launch_tree_attention<true>(a, launches, s) : launch_tree_attention<false>(a, launches, s);
 }
 
 }  // namespace kda

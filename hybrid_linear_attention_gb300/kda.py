@@ -38,6 +38,9 @@ EXPORTS = (
     "mla_tree_latent", "mla_tree_decode", "mla_cache_append", "mla_cache_accept",
     "mla_pages_copy", "mla_pages_workspace_size", "mla_pages_free", "mla_pages_fork",
     "mla_pages_reserve",
+    "mla_tree_latent_lse", "mla_tree_decode_lse", "mla_cache_weights", "mla_cache_evict",
+    "mla_pages_trim", "mla_block_keys", "mla_block_scores_workspace_size", "mla_block_scores",
+    "mla_block_select", "mla_sparse_workspace_size", "mla_sparse_latent", "mla_sparse_decode",
 )
 
 
@@ -152,6 +155,30 @@ def load():
                                       _vp, _i32, _vp, _sz, _vp]),
             "mla_pages_reserve": (_i32, [_i32, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp,
                                          _i32, _vp, _sz, _vp]),
+        })
+        f32 = ctypes.c_float
+        choice = [_i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp]  # blocks .. sel_lengths
+        sig.update({
+            "mla_tree_latent_lse": (_i32, [_vp, _i32] + paged + [_vp, _i32, _i64, _vp, f32, _vp,
+                                                                 _i32, _vp, _vp, _sz, _vp]),
+            "mla_tree_decode_lse": (_i32, [_vp] * 4 + paged + [_vp, _i32, _i64, _vp, _vp, f32] +
+                                    [_vp] * 5 + [_sz, _vp]),
+            "mla_cache_weights": (_i32, [_vp, _i32] + paged + [_vp, _i32, _i64, _vp, _vp, _vp,
+                                                               f32, _vp, _i64, _vp]),
+            "mla_cache_evict": (_i32, layers + [_vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _vp,
+                                                _vp, _vp]),
+            "mla_pages_trim": (_i32, [_i32, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp]),
+            "mla_block_keys": (_i32, [_vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp]),
+            "mla_block_scores_workspace_size": (_sz, [_i64, _i32, _i32]),
+            "mla_block_scores": (_i32, [_vp, _i32] + paged + [_vp, _i32, _i64, f32, _vp, _i64, _vp,
+                                                              _sz, _vp]),
+            "mla_block_select": (_i32, [_vp, _i64, _i32, _vp, _i32, _vp, _vp, _i32, _i64, _i32,
+                                        _i32, _i32, _vp, _i32, _vp, _vp]),
+            "mla_sparse_workspace_size": (_sz, [_i32, _i64, _i32, _i32]),
+            "mla_sparse_latent": (_i32, [_vp, _i32, _vp] + paged + [_vp, _i32, _i64, _vp, f32] +
+                                  choice + [_vp, _i32, _vp, _sz, _vp]),
+            "mla_sparse_decode": (_i32, [_vp] * 5 + paged + [_vp, _i32, _i64, _vp, _vp, f32] +
+                                  choice + [_vp, _vp, _vp, _vp, _sz, _vp]),
         })
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -782,3 +809,234 @@ def mla_pages_reserve(page_size, refcount, page_table, held, lengths, slots, ext
         _here(slots, i32, "slots", dev), _here(extra, i32, "extra", dev), slots.numel(),
         *_here_ws(workspace, dev), _here_stream(stream, dev))
     _check(st, "mla_pages_reserve")
+
+
+# ---- long contexts: eviction by accumulated attention ------------------------------------------
+
+
+def mla_tree_latent_lse(q_cat, pool, page_table, lengths, cu_nodes, z, lse, *, mask=None,
+                        scale=MLA_SCALE, workspace=None, stream=None):
+    """mla_tree_latent that also writes lse [nodes, H] fp32, each row's log of the sum of exp(score)."""
+    dev = _device()
+    total, H, n = q_cat.shape[0], q_cat.shape[1], cu_nodes.numel() - 1
+    _shape(q_cat, (total, H, 576), "q_cat")
+    _shape(z, (total, H, 512), "z")
+    _shape(lse, (total, H), "lse")
+    _shape(mask, (total,), "mask")
+    if z.dtype not in _DTYPE:
+        raise TypeError(f"z: expected float32 or bfloat16, got {z.dtype}")
+    st = load().mla_tree_latent_lse(
+        _here(q_cat, torch.bfloat16, "q_cat", dev), H, *_paged(pool, page_table, lengths, n, dev),
+        _here(cu_nodes, torch.int32, "cu_nodes", dev), n, total,
+        _here(mask, torch.int64, "mask", dev), float(scale), _here(z, z.dtype, "z", dev),
+        _DTYPE[z.dtype], _here(lse, torch.float32, "lse", dev), *_here_ws(workspace, dev),
+        _here_stream(stream, dev))
+    _check(st, "mla_tree_latent_lse")
+
+
+def _decode_shapes(q_nope, q_rope, w_uk, w_uv, gate_logit, q_cat, z, out, mask):
+    total = q_nope.shape[0]
+    for t, tail, name in ((q_nope, (64, 128), "q_nope"), (q_rope, (64, 64), "q_rope"),
+                          (gate_logit, (64,), "gate_logit"), (q_cat, (64, 576), "q_cat"),
+                          (z, (64, 512), "z"), (out, (64, 128), "out")):
+        _shape(t, (total,) + tail, name)
+    _shape(w_uk, (64, 128, 512), "w_uk")
+    _shape(w_uv, (64, 128, 512), "w_uv")
+    _shape(mask, (total,), "mask")
+    return total
+
+
+def mla_tree_decode_lse(q_nope, q_rope, w_uk, w_uv, pool, page_table, lengths, cu_nodes, gate_logit,
+                        q_cat, z, out, lse, *, mask=None, scale=MLA_SCALE, workspace=None,
+                        stream=None):
+    """mla_tree_decode that also writes lse [nodes, 64] fp32."""
+    dev = _device()
+    bf, n = torch.bfloat16, cu_nodes.numel() - 1
+    total = _decode_shapes(q_nope, q_rope, w_uk, w_uv, gate_logit, q_cat, z, out, mask)
+    _shape(lse, (total, 64), "lse")
+    st = load().mla_tree_decode_lse(
+        _here(q_nope, bf, "q_nope", dev), _here(q_rope, bf, "q_rope", dev),
+        _here(w_uk, bf, "w_uk", dev), _here(w_uv, bf, "w_uv", dev),
+        *_paged(pool, page_table, lengths, n, dev), _here(cu_nodes, torch.int32, "cu_nodes", dev),
+        n, total, _here(mask, torch.int64, "mask", dev), _here(gate_logit, bf, "gate_logit", dev),
+        float(scale), _here(q_cat, bf, "q_cat", dev), _here(z, torch.float32, "z", dev),
+        _here(out, bf, "out", dev), _here(lse, torch.float32, "lse", dev),
+        *_here_ws(workspace, dev), _here_stream(stream, dev))
+    _check(st, "mla_tree_decode_lse")
+
+
+def mla_cache_weights(q_cat, pool, page_table, lengths, cu_nodes, lse, weights, *, mask=None,
+                      node_weight=None, scale=MLA_SCALE, stream=None):
+    """weights [n_seqs, positions] fp32 += the attention that each cached position gets from the rows
+    q_cat [nodes, H, 576], whose lse [nodes, H] mla_tree_latent_lse wrote; node_weight [nodes] fp32
+    (None: ones; 0: a node that does not count)."""
+    dev = _device()
+    f32, i32 = torch.float32, torch.int32
+    total, H, n = q_cat.shape[0], q_cat.shape[1], cu_nodes.numel() - 1
+    _shape(q_cat, (total, H, 576), "q_cat")
+    _shape(lse, (total, H), "lse")
+    _shape(mask, (total,), "mask")
+    _shape(node_weight, (total,), "node_weight")
+    if len(weights.shape) != 2 or weights.shape[0] < n:
+        raise ValueError("weights: expected [n_seqs, positions]")
+    st = load().mla_cache_weights(
+        _here(q_cat, torch.bfloat16, "q_cat", dev), H, *_paged(pool, page_table, lengths, n, dev),
+        _here(cu_nodes, i32, "cu_nodes", dev), n, total, _here(mask, torch.int64, "mask", dev),
+        _here(node_weight, f32, "node_weight", dev), _here(lse, f32, "lse", dev), float(scale),
+        _here(weights, f32, "weights", dev), weights.shape[1], _here_stream(stream, dev))
+    _check(st, "mla_cache_weights")
+
+
+def mla_cache_evict(pool, page_table, lengths, weights, kept, new_lengths, new_weights=None, *,
+                    first=0, recent=0, refcount=None, stream=None):
+    """Sequences cut to kept.shape[1] positions: the first, the recent and the heaviest others stay;
+    pool [n_layers, n_pages, page_size, 576] compacted, kept [n_seqs, budget], new_lengths (may be
+    lengths), new_weights like weights [n_seqs, positions] (may be weights)."""
+    dev = _device()
+    f32, i32 = torch.float32, torch.int32
+    n = kept.shape[0]
+    if len(kept.shape) != 2 or len(weights.shape) != 2 or weights.shape[0] < n:
+        raise ValueError("kept, weights: expected [n_seqs, budget] and [n_seqs, positions]")
+    if new_lengths.shape[0] < n:
+        raise ValueError("new_lengths: fewer rows than sequences")
+    _shape(new_weights, weights.shape, "new_weights")
+    _shape(refcount, (pool.shape[1],), "refcount")
+    st = load().mla_cache_evict(
+        *_paged_layers(pool, page_table, lengths, n, dev), _here(refcount, i32, "refcount", dev), n,
+        _here(weights, f32, "weights", dev), weights.shape[1], kept.shape[1], int(first),
+        int(recent), _here(kept, i32, "kept", dev), _here(new_lengths, i32, "new_lengths", dev),
+        _here(new_weights, f32, "new_weights", dev), _here_stream(stream, dev))
+    _check(st, "mla_cache_evict")
+
+
+def mla_pages_trim(page_size, refcount, page_table, held, lengths, slots, *, stream=None):
+    """The pages of sequences `slots` behind their lengths released."""
+    dev = _device()
+    st = load().mla_pages_trim(
+        refcount.numel(), int(page_size), *_book(refcount, page_table, held, lengths, dev),
+        _here(slots, torch.int32, "slots", dev), slots.numel(), _here_stream(stream, dev))
+    _check(st, "mla_pages_trim")
+
+
+# ---- long contexts: attention over chosen blocks -------------------------------------------------
+
+
+def mla_block_keys(pool, page_table, from_lengths, lengths, keys, *, stream=None):
+    """keys [n_layers, n_pages, 576]: the mean rows of the pages of pool [n_layers, n_pages,
+    page_size, 576] that filled up while from_lengths [n_seqs] grew to lengths."""
+    dev = _device()
+    n = from_lengths.shape[0]
+    _shape(keys, (pool.shape[0], pool.shape[1], 576), "keys")
+    layers = _paged_layers(pool, page_table, lengths, n, dev)
+    st = load().mla_block_keys(
+        *layers[:-1], _here(from_lengths, torch.int32, "from_lengths", dev), layers[-1], n,
+        _here(keys, torch.bfloat16, "keys", dev), _here_stream(stream, dev))
+    _check(st, "mla_block_keys")
+
+
+def mla_block_scores_workspace_size(total_nodes, H, max_pages):
+    return int(load().mla_block_scores_workspace_size(int(total_nodes), int(H), int(max_pages)))
+
+
+def _block_keys(keys, n_pages, dev):
+    _shape(keys, (n_pages, 576), "keys")
+    return _here(keys, torch.bfloat16, "keys", dev)
+
+
+def _scores(scores, n, dev):
+    if len(scores.shape) != 2 or scores.shape[0] < n:
+        raise ValueError("scores: expected [n_seqs, blocks]")
+    return _here(scores, torch.float32, "scores", dev), scores.shape[1]
+
+
+def _selection(sel_table, sel_lengths, n, dev):
+    if len(sel_table.shape) != 2 or sel_table.shape[0] < n or sel_lengths.shape[0] < n:
+        raise ValueError("sel_table, sel_lengths: fewer rows than sequences")
+    return (_here(sel_table, torch.int32, "sel_table", dev), sel_table.shape[1],
+            _here(sel_lengths, torch.int32, "sel_lengths", dev))
+
+
+def _tables(page_table, lengths, n, dev):
+    rows, max_pages = page_table.shape
+    if rows < n or lengths.shape[0] < n:
+        raise ValueError("page_table, lengths: fewer rows than sequences")
+    return (_here(page_table, torch.int32, "page_table", dev), max_pages,
+            _here(lengths, torch.int32, "lengths", dev))
+
+
+def mla_block_scores(q_cat, keys, page_size, page_table, lengths, cu_nodes, scores, *,
+                     scale=MLA_SCALE, workspace=None, stream=None):
+    """scores [n_seqs, blocks] fp32 of each sequence's full pages, by keys [n_pages, 576] (a layer's):
+    every row's softmax over the pages, summed over the rows q_cat [nodes, H, 576]."""
+    dev = _device()
+    total, H, n = q_cat.shape[0], q_cat.shape[1], cu_nodes.numel() - 1
+    _shape(q_cat, (total, H, 576), "q_cat")
+    st = load().mla_block_scores(
+        _here(q_cat, torch.bfloat16, "q_cat", dev), H, _block_keys(keys, keys.shape[0], dev),
+        keys.shape[0], int(page_size), *_tables(page_table, lengths, n, dev),
+        _here(cu_nodes, torch.int32, "cu_nodes", dev), n, total, float(scale),
+        *_scores(scores, n, dev), *_here_ws(workspace, dev), _here_stream(stream, dev))
+    _check(st, "mla_block_scores")
+
+
+def mla_block_select(scores, page_size, page_table, lengths, cu_nodes, sel_table, sel_lengths, *,
+                     blocks, total_nodes, first=0, recent=0, stream=None):
+    """sel_table [n_seqs, sel_pages], sel_lengths [n_seqs]: the page table and lengths of the `blocks`
+    full pages of the largest scores (the first and the recent always) and of what is behind them.
+    total_nodes: rows of the step's queries."""
+    dev = _device()
+    n = cu_nodes.numel() - 1
+    st = load().mla_block_select(
+        *_scores(scores, n, dev), int(page_size), *_tables(page_table, lengths, n, dev),
+        _here(cu_nodes, torch.int32, "cu_nodes", dev), n, int(total_nodes), int(blocks), int(first),
+        int(recent), *_selection(sel_table, sel_lengths, n, dev), _here_stream(stream, dev))
+    _check(st, "mla_block_select")
+
+
+def mla_sparse_workspace_size(n_seqs, total_nodes, H, max_pages):
+    return int(load().mla_sparse_workspace_size(int(n_seqs), int(total_nodes), int(H),
+                                                int(max_pages)))
+
+
+def mla_sparse_latent(q_cat, pool, keys, page_table, lengths, cu_nodes, scores, sel_table,
+                      sel_lengths, z, *, blocks, first=0, recent=0, mask=None, scale=MLA_SCALE,
+                      workspace=None, stream=None):
+    """mla_block_scores, mla_block_select and mla_tree_latent over the chosen pages."""
+    dev = _device()
+    total, H, n = q_cat.shape[0], q_cat.shape[1], cu_nodes.numel() - 1
+    _shape(q_cat, (total, H, 576), "q_cat")
+    _shape(z, (total, H, 512), "z")
+    _shape(mask, (total,), "mask")
+    if z.dtype not in _DTYPE:
+        raise TypeError(f"z: expected float32 or bfloat16, got {z.dtype}")
+    cache = _paged(pool, page_table, lengths, n, dev)
+    st = load().mla_sparse_latent(
+        _here(q_cat, torch.bfloat16, "q_cat", dev), H, cache[0],
+        _block_keys(keys, pool.shape[0], dev), *cache[1:],
+        _here(cu_nodes, torch.int32, "cu_nodes", dev), n, total,
+        _here(mask, torch.int64, "mask", dev), float(scale), int(blocks), int(first), int(recent),
+        *_scores(scores, n, dev), *_selection(sel_table, sel_lengths, n, dev),
+        _here(z, z.dtype, "z", dev), _DTYPE[z.dtype], *_here_ws(workspace, dev),
+        _here_stream(stream, dev))
+    _check(st, "mla_sparse_latent")
+
+
+def mla_sparse_decode(q_nope, q_rope, w_uk, w_uv, pool, keys, page_table, lengths, cu_nodes,
+                      gate_logit, scores, sel_table, sel_lengths, q_cat, z, out, *, blocks, first=0,
+                      recent=0, mask=None, scale=MLA_SCALE, workspace=None, stream=None):
+    """mla_tree_decode over the pages that mla_block_scores and mla_block_select choose."""
+    dev = _device()
+    bf, n = torch.bfloat16, cu_nodes.numel() - 1
+    total = _decode_shapes(q_nope, q_rope, w_uk, w_uv, gate_logit, q_cat, z, out, mask)
+    cache = _paged(pool, page_table, lengths, n, dev)
+    st = load().mla_sparse_decode(
+        _here(q_nope, bf, "q_nope", dev), _here(q_rope, bf, "q_rope", dev),
+        _here(w_uk, bf, "w_uk", dev), _here(w_uv, bf, "w_uv", dev), cache[0],
+        _block_keys(keys, pool.shape[0], dev), *cache[1:],
+        _here(cu_nodes, torch.int32, "cu_nodes", dev), n, total,
+        _here(mask, torch.int64, "mask", dev), _here(gate_logit, bf, "gate_logit", dev),
+        float(scale), int(blocks), int(first), int(recent), *_scores(scores, n, dev),
+        *_selection(sel_table, sel_lengths, n, dev), _here(q_cat, bf, "q_cat", dev),
+        _here(z, torch.float32, "z", dev), _here(out, bf, "out", dev), *_here_ws(workspace, dev),
+        _here_stream(stream, dev))
+    _check(st, "mla_sparse_decode")

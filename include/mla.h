@@ -265,6 +265,183 @@ kda_status mla_tree_decode(const void* q_nope, const void* q_rope, const void* w
                            float* z, void* out, void* workspace, size_t ws_bytes,
                            cudaStream_t stream);
 
+/* ---- long contexts: eviction by accumulated attention ----------------------------------------
+ *
+ * A sequence's positions are ranked by the attention that they received: mla_tree_latent_lse (or
+ * mla_tree_decode_lse) leaves each row's log-sum, mla_cache_weights adds what each position got to a
+ * running sum (in every latent layer that counts), mla_cache_evict keeps the heaviest positions of a
+ * sequence and moves their rows together in every layer, mla_pages_trim releases the pages behind
+ * them.  The rows' positional keys are as they were cached, so later queries are rotated by the
+ * token's own position, which is no longer the sequence's length.
+ */
+
+/*
+ * mla_tree_latent_lse, mla_tree_decode_lse -- mla_tree_latent and mla_tree_decode that also write
+ *   lse         [total_nodes, H] fp32: ln sum_t exp(s_t) over what the row sees, -infinity for a row
+ *               that sees nothing.  Summed in fp32 from the weights before they are rounded.
+ * All else as there; z and out are bit-identical to theirs.
+ */
+kda_status mla_tree_latent_lse(const void* q_cat, int H, const void* pool, int n_pages, int page_size,
+                               const int32_t* page_table, int max_pages, const int32_t* lengths,
+                               const int32_t* cu_nodes, int n_seqs, int64_t total_nodes,
+                               const int64_t* mask, float scale, void* z, kda_dtype z_dtype,
+                               float* lse, void* workspace, size_t ws_bytes, cudaStream_t stream);
+kda_status mla_tree_decode_lse(const void* q_nope, const void* q_rope, const void* w_uk,
+                               const void* w_uv, const void* pool, int n_pages, int page_size,
+                               const int32_t* page_table, int max_pages, const int32_t* lengths,
+                               const int32_t* cu_nodes, int n_seqs, int64_t total_nodes,
+                               const int64_t* mask, const void* gate_logit, float scale, void* q_cat,
+                               float* z, void* out, float* lse, void* workspace, size_t ws_bytes,
+                               cudaStream_t stream);
+
+/*
+ * mla_cache_weights -- weights[n][t] += sum_i u_i sum_h exp(s_iht - lse_ih) over the nodes i of
+ * sequence n that see position t (as mla_tree_latent: every cached position, and the drafted row of
+ * node j at position lengths[n] + j where bit j of mask[i] is set; NULL: a chain).
+ *   q_cat, H, pool .. lengths, cu_nodes, n_seqs, total_nodes, mask, scale as mla_tree_latent.
+ *   node_weight [total_nodes] fp32 u_i, or NULL (ones).  A node of weight 0 (a rejected draft)
+ *               adds nothing, whatever its row holds.
+ *   lse         [total_nodes, H] fp32 from mla_tree_latent_lse on the same arguments; a row whose lse is
+ *               -infinity adds nothing.
+ *   weights     [n_seqs, weights_stride] fp32, added to: positions 0 .. lengths[n] + nodes - 1; others
+ *               keep their values.
+ * Products with bf16 operands and fp32 accumulation; the sum over rows is in fp32 in a fixed order.
+ * Sequences with bad offsets or lengths (also more positions than weights_stride) are skipped and
+ * reported as there; a position whose page is out of range gets nothing and is reported.
+ */
+kda_status mla_cache_weights(const void* q_cat, int H, const void* pool, int n_pages, int page_size,
+                             const int32_t* page_table, int max_pages, const int32_t* lengths,
+                             const int32_t* cu_nodes, int n_seqs, int64_t total_nodes,
+                             const int64_t* mask, const float* node_weight, const float* lse,
+                             float scale, float* weights, int64_t weights_stride,
+                             cudaStream_t stream);
+
+/*
+ * mla_cache_evict -- cuts each sequence of more than `budget` positions to `budget`: it keeps its
+ * first `first` and its last `recent` positions and, of those between, the ones of the largest
+ * weights (among equals the lower position first; NaN counts as less than anything).  The kept rows
+ * move to positions 0 .. budget - 1 in their order, in every layer; shorter sequences stay as they are.
+ *   weights     [n_seqs, weights_stride] fp32.
+ *   budget      at least 1;  first, recent: at least 0, first + recent <= budget.
+ *   refcount    [n_pages] int32 or NULL: where given, a sequence whose kept rows would move into a page
+ *               that other sequences share is refused.
+ *   kept        [n_seqs, budget] int32 output: the kept positions in ascending order, then -1.
+ *   new_lengths [n_seqs] int32 output, may be `lengths`.
+ *   new_weights NULL, or [n_seqs, weights_stride] fp32: the kept positions' weights, then zeros up to
+ *               the old length, what is behind left as it was; may be `weights`, must not overlap it
+ *               otherwise.
+ * Bit-exact moves; pages stay held (mla_pages_trim).  There are no drafted rows at the time of the
+ * call.  A sequence with a bad length (below 0, more than the table row or weights_stride hold), a
+ * row that would move from or to a position without a page, or into a shared page keeps its rows, length
+ * and weights, has a `kept` row of -1 and is reported (KDA_ERR_BAD_INDEX).  Keys of pages that
+ * the rows moved into are written anew by mla_block_keys.
+ */
+kda_status mla_cache_evict(void* pool, int n_layers, int n_pages, int page_size,
+                           const int32_t* page_table, int max_pages, const int32_t* lengths,
+                           const int32_t* refcount, int n_seqs, const float* weights,
+                           int64_t weights_stride, int budget, int first, int recent,
+                           int32_t* kept, int32_t* new_lengths, float* new_weights,
+                           cudaStream_t stream);
+
+/*
+ * mla_pages_trim -- releases the pages of the sequences slots[0..n-1] that lie wholly behind their
+ * lengths: refcounts drop by one, table entries become -1, held the pages that are left.  A
+ * sequence listed twice is cut once.  Indices out of range, bad lengths, sequences that hold fewer pages
+ * than their length needs, table entries that name no page and counts that are already 0 are skipped
+ * and reported (KDA_ERR_BAD_INDEX).
+ */
+kda_status mla_pages_trim(int n_pages, int page_size, int32_t* refcount, int32_t* page_table,
+                          int max_pages, int32_t* held, const int32_t* lengths, int n_slots,
+                          const int32_t* slots, int n, cudaStream_t stream);
+
+/* ---- long contexts: attention over chosen blocks ------------------------------------------------
+ *
+ * A block is a page.  Every full page has a key, the mean of its rows; a step scores a sequence's
+ * full pages by their keys, keeps the best, and attends to those and to what is behind the last full
+ * page.  The choice is the sequence's: all its heads and drafted nodes read the same pages.  Keys go by
+ * page, so sequences that share pages share their keys, and a fork needs none of its own.
+ */
+
+/*
+ * mla_block_keys -- keys[layer][page] = mean of the page's rows (fp32 sum, rounded once), for the
+ * pages that filled up: sequence n's pages from_lengths[n] / page_size .. lengths[n] / page_size - 1, in
+ * every layer.  After mla_cache_append or mla_cache_accept with the lengths before and after.
+ *   keys        [n_layers, n_pages, 576] bf16;  from_lengths [n_seqs] int32 (from 0: all).
+ * Sequences with a bad length and pages out of range are skipped and reported (KDA_ERR_BAD_INDEX);
+ * from_lengths[n] >= lengths[n] is no work.
+ */
+kda_status mla_block_keys(const void* pool, int n_layers, int n_pages, int page_size,
+                          const int32_t* page_table, int max_pages, const int32_t* from_lengths,
+                          const int32_t* lengths, int n_seqs, void* keys, cudaStream_t stream);
+
+/* Device workspace of mla_block_scores; 0 for invalid arguments. */
+size_t mla_block_scores_workspace_size(int64_t total_nodes, int H, int max_pages);
+
+/*
+ * mla_block_scores -- scores[n][b] = sum over the rows r (nodes x heads) of sequence n's step of
+ * softmax_b(scale q_r . key_b), b over its full pages (b < lengths[n] / page_size).
+ *   q_cat, H, page_table .. lengths, cu_nodes, n_seqs, total_nodes, scale as mla_tree_latent.
+ *   keys        [n_pages, 576] bf16, the layer's.
+ *   scores      [n_seqs, scores_stride] fp32 (scores_stride >= max_pages); entries behind the full
+ *               pages keep their values.
+ *   workspace / ws_bytes: at least mla_block_scores_workspace_size() bytes, 16-byte aligned.
+ * Sequences without nodes or with bad offsets or lengths are skipped (and reported as there); a block
+ * whose page is out of range scores 0 and is reported.
+ */
+kda_status mla_block_scores(const void* q_cat, int H, const void* keys, int n_pages, int page_size,
+                            const int32_t* page_table, int max_pages, const int32_t* lengths,
+                            const int32_t* cu_nodes, int n_seqs, int64_t total_nodes, float scale,
+                            float* scores, int64_t scores_stride, void* workspace, size_t ws_bytes,
+                            cudaStream_t stream);
+
+/*
+ * mla_block_select -- the page table of what a step reads: of each sequence's full pages the first
+ * `first`, the last `recent` and those of the largest scores, `blocks` in all (among equals the earlier
+ * page; NaN counts as less than anything; all of them where there are no more), in their order; then the
+ * page in use and those of the drafted rows.
+ *   sel_table   [n_seqs, sel_pages] int32 output, -1 behind the last page;  sel_lengths [n_seqs] int32
+ *               output: the cached positions among them.  Both are what mla_tree_latent and
+ *               mla_tree_decode take as page_table and lengths.
+ *   blocks      at least 1;  first, recent: at least 0, first + recent <= blocks.
+ * A sequence without nodes gets an empty row; so does one with bad offsets or lengths or that needs more
+ * than sel_pages entries, which is reported.
+ */
+kda_status mla_block_select(const float* scores, int64_t scores_stride, int page_size,
+                            const int32_t* page_table, int max_pages, const int32_t* lengths,
+                            const int32_t* cu_nodes, int n_seqs, int64_t total_nodes, int blocks,
+                            int first, int recent, int32_t* sel_table, int sel_pages,
+                            int32_t* sel_lengths, cudaStream_t stream);
+
+/* Device workspace of mla_sparse_latent and mla_sparse_decode (H = 64); 0 for invalid arguments. */
+size_t mla_sparse_workspace_size(int n_seqs, int64_t total_nodes, int H, int max_pages);
+
+/*
+ * mla_sparse_latent -- mla_block_scores, mla_block_select and mla_tree_latent over the selection in
+ * one call.  keys is the layer's [n_pages, 576]; scores, sel_table and sel_lengths are caller-owned and
+ * hold what those calls write; workspace: at least mla_sparse_workspace_size() bytes.
+ */
+kda_status mla_sparse_latent(const void* q_cat, int H, const void* pool, const void* keys,
+                             int n_pages, int page_size, const int32_t* page_table, int max_pages,
+                             const int32_t* lengths, const int32_t* cu_nodes, int n_seqs,
+                             int64_t total_nodes, const int64_t* mask, float scale, int blocks,
+                             int first, int recent, float* scores, int64_t scores_stride,
+                             int32_t* sel_table, int sel_pages, int32_t* sel_lengths, void* z,
+                             kda_dtype z_dtype, void* workspace, size_t ws_bytes,
+                             cudaStream_t stream);
+
+/*
+ * mla_sparse_decode -- mla_tree_decode with mla_sparse_latent (H = 64, fp32 z) for mla_tree_latent.
+ */
+kda_status mla_sparse_decode(const void* q_nope, const void* q_rope, const void* w_uk,
+                             const void* w_uv, const void* pool, const void* keys, int n_pages,
+                             int page_size, const int32_t* page_table, int max_pages,
+                             const int32_t* lengths, const int32_t* cu_nodes, int n_seqs,
+                             int64_t total_nodes, const int64_t* mask, const void* gate_logit,
+                             float scale, int blocks, int first, int recent, float* scores,
+                             int64_t scores_stride, int32_t* sel_table, int sel_pages,
+                             int32_t* sel_lengths, void* q_cat, float* z, void* out,
+                             void* workspace, size_t ws_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
