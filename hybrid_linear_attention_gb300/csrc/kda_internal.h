@@ -116,7 +116,7 @@ struct KeySumArgs {
   const int32_t *cu_nodes;     // [n_seqs + 1]
   const int64_t *mask;         // positions: as TreeAttnArgs
   const float *node_weight;    // positions: [total] or nullptr (ones)
-  float *lse;                  // [total, H]
+  const float *lse;            // positions: [total, H]
   float *out;                  // [n_seqs, out_stride] positions: added to; blocks: written
   int64_t out_stride;
   float2 *part;                // blocks: (maximum, sum) of each row [total, H, part_stride] over half a tile

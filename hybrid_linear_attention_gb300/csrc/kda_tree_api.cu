@@ -388,7 +388,7 @@ kda_status mla_cache_weights(const void *q_cat, int H, const void *pool, int n_p
   if (!optional(mask) || !optional(node_weight) || !given(lse) || !given(weights) || weights_stride < 1)
     return KDA_ERR_INVALID_ARG;
   if (!kda::mla_latent_supported()) return KDA_ERR_UNSUPPORTED;
-  a.mask = mask, a.node_weight = node_weight, a.lse = const_cast<float *>(lse);
+  a.mask = mask, a.node_weight = node_weight, a.lse = lse;
   a.out = weights, a.out_stride = weights_stride;
   return done(kda::launch_cache_weights(a, stream), 1);
 }

@@ -6,7 +6,7 @@
 // of the rows r (nodes x heads) and lse_r = ln sum_t exp(s_rt) over what row r sees,
 //     weights_t += sum_r u_r exp(s_rt - lse_r)        (positions; u_r: the weight of r's node)
 //     score_b    = sum_r exp(s_rb - lse_r)            (blocks: the keys are the pages' mean rows)
-// Blocks take two passes, lse first: each tile's maximum and sum of a row, merged by key_lse_kernel.
+// Blocks take two passes: the first leaves each tile's maximum and sum of a row, the second merges them.
 //
 // The keys are the product's M side, D[256 keys x rows] = K Q^T on a pair of CTAs (cta_group::2, 128
 // keys each), so a thread owns a key: the sum over rows runs along its own columns of tensor memory,
@@ -115,14 +115,24 @@ __device__ __forceinline__ int columns(const Seq &s, int chunk) {  // of a chunk
   const int r = s.rows - CHUNK * chunk;
   return r >= CHUNK ? CHUNK : (r + 31) & ~31;
 }
-// four rows of the block keys, 64 channels each
-__device__ __forceinline__ void tma_pair_gather4(uint32_t dst, const CUtensorMap *map, int c0, int r0, int r1, int r2, int r3,
-                                                 uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-      : "memory");
+// The products drop bits of every partial sum (measured: a lone head's weights 1.1e-6 off), so where tensor
+// memory has room, a score is the sum of up to four of them over a part of the channels each, added in fp32.
+__device__ __forceinline__ int parts_of(int columns) { return columns <= CHUNK / 4 ? 4 : columns <= CHUNK / 2 ? 2 : 1; }
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// a barrier of the sums' warps that also tells whether any thread says so
+__device__ __forceinline__ bool bar_any(int id, int n, bool mine) {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %3, 0;\nbar.red.or.pred p, %1, %2, q;\nselp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(r)
+               : "r"(id), "r"(n), "r"((uint32_t)mine)
+               : "memory");
+  return r != 0;
 }
 // Sums over the warp's lanes of 16 columns: lane l gets column l & 15's.
 __device__ __forceinline__ float columns_sum(float (&v)[16], int lane) {
@@ -157,6 +167,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   __shared__ float2 s_col[LSE ? 4 : 2][CHUNK];  // rows' (lse, weight); LSE: a quarter's (maximum, sum)
   __shared__ uint8_t s_node[2][LSE ? 1 : CHUNK];
   __shared__ float s_half[2][LSE ? 1 : KC];
+  __shared__ int s_page[BLOCKS ? KC : 1];
   const uint32_t raw = smem_u32(dyn);
   const uint32_t sb = (raw + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -253,7 +264,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   const int lp = 31 - __clz(a.c.page_size);
 
   if (warp == W_KEYS) {
-    // ---- key blocks: a lane a tile load ---------------------------------------------------------
+    // ---- key blocks: positions a lane a tile load, blocks by 16-byte copies of their keys (gathers by
+    //      TMA, four rows each, took three times as long); a lane first looks four of them up
     const int box = a.c.page_size < 64 ? a.c.page_size : 64, lb = 31 - __clz(box), in_page = a.c.page_size - 1;
     uint64_t policy;  // the cache's rows are read once
     asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
@@ -262,36 +274,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       const int p0 = TILE * walk.tile + KC * (int)rank;
       const int32_t *row = a.c.table + (size_t)walk.n * a.c.max_pages;
       auto known = [&](int page) { return page >= 0 && page < a.c.n_pages; };
-      int page[4];
-      if (BLOCKS) {  // blocks 4 lane ..; one without a page is not used: any row stands for it
+      if (BLOCKS) {
+        const int rows = walk.s.keys - p0 < KC ? walk.s.keys - p0 : KC;  // (may be below 0)
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const int b = p0 + 4 * lane + y;
-          page[y] = b < walk.s.keys ? row[b] : 0;
-          if (!known(page[y])) {
+          const int r = 32 * y + lane;
+          int page = r < rows ? row[p0 + r] : 0;
+          if (!known(page)) {  // no page: any key stands for it
             if (LSE && a.err) atomicOr(a.err, ERR_BAD_INDEX);
-            page[y] = 0;
+            page = 0;
           }
+          s_page[r] = page;
         }
+        __syncwarp();
+        bool ok = true;
+#pragma unroll 1
+        for (int kb = 0; kb < KB; ++kb) {
+          if (tiles > 0) ok = ok && warp_wait(B_KEMPTY + kb, (uint32_t)(tiles - 1));
+          const uint32_t dst = sb + OFF_K + kb * SLOT;
+          const int piece = lane & 7;
+          const char *keys = reinterpret_cast<const char *>(a.c.pool) + 128 * kb + 16 * piece;
+          if (ok)
+#pragma unroll 4
+            for (int r = lane >> 3; r < rows; r += 4)
+              copy16(dst + r * 128 + ((piece ^ (r & 7)) << 4), keys + (size_t)s_page[r] * (TK * 2));
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        auto landed = [&](int kb) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0 && ok) arrive_pair(map_shared_rank(bar(B_KFULL + kb), 0));
+        };
+        copies_wait<8>(), landed(0), copies_wait<7>(), landed(1), copies_wait<6>(), landed(2);
+        copies_wait<5>(), landed(3), copies_wait<4>(), landed(4), copies_wait<3>(), landed(5);
+        copies_wait<2>(), landed(6), copies_wait<1>(), landed(7), copies_wait<0>(), landed(8);
+        __syncwarp();  // s_page is read
       } else {  // positions box lane ..; past the pool, where loads give zeros, for one without a page
         const int p = p0 + (lane << lb);
         const bool here = (lane << lb) < KC && p < walk.s.keys;
-        page[0] = here ? row[p >> lp] : a.c.n_pages;
-        if (!known(page[0])) {
+        int page = here ? row[p >> lp] : a.c.n_pages;
+        if (!known(page)) {
           if (here && a.err) atomicOr(a.err, ERR_BAD_INDEX);
-          page[0] = a.c.n_pages;
+          page = a.c.n_pages;
         }
-      }
 #pragma unroll 1
-      for (int kb = 0; kb < KB; ++kb) {
-        if (tiles > 0 && !warp_wait(B_KEMPTY + kb, (uint32_t)(tiles - 1))) continue;
-        if (lane == 0) announce(B_KFULL + kb, SLOT);
-        __syncwarp();
-        const uint32_t full = map_shared_rank(bar(B_KFULL + kb), 0), dst = sb + OFF_K + kb * SLOT;
-        if (BLOCKS)
-          tma_pair_gather4(dst + lane * 512, &maps.k, 64 * kb, page[0], page[1], page[2], page[3], full);
-        else if ((lane << lb) < KC)
-          tma_pair_3d(dst + (lane << lb) * 128, &maps.k, 64 * kb, (p0 + (lane << lb)) & in_page, page[0], full, policy);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (tiles > 0 && !warp_wait(B_KEMPTY + kb, (uint32_t)(tiles - 1))) continue;
+          if (lane == 0) announce(B_KFULL + kb, SLOT);
+          __syncwarp();
+          if ((lane << lb) < KC)
+            tma_pair_3d(sb + OFF_K + kb * SLOT + (lane << lb) * 128, &maps.k, 64 * kb, p & in_page, page,
+                        map_shared_rank(bar(B_KFULL + kb), 0), policy);
+        }
       }
       ++tiles;
     }
@@ -369,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         const bool res = walk.s.rows <= RES;
         if (res && walk.first && !(ok = wait(B_RFULL, (uint32_t)segs))) break;
         for (int ch = 0; ch < walk.s.chunks && ok; ++ch, ++i) {
-          const int N = columns(walk.s, ch);
+          const int N = columns(walk.s, ch), parts = parts_of(N);
           const uint32_t id = idesc(1, 256, (uint32_t)N, 0, 0), d = tm + CHUNK * (i & 1);
           if (i >= 2 && !(ok = wait(B_DFREE + (i & 1), (uint32_t)((i >> 1) - 1)))) break;
 #pragma unroll 1
@@ -377,10 +411,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
             if (ch == 0 && !(ok = wait(B_KFULL + kb, (uint32_t)tiles))) break;
             if (!res && !(ok = wait(B_QFULL + j, par))) break;
             tc_fence_after();
+            const int part = kb * parts / KB;
+            const bool fresh = kb == 0 || (kb - 1) * parts / KB < part;
             const uint64_t ad = sdesc_sw128(sb + OFF_K + kb * SLOT, 16, 1024);
             const uint64_t bd = sdesc_sw128(sb + OFF_Q + (res ? kb * (N / 2) * 128 : j * (CHUNK / 2) * 128), 16, 1024);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) mma2(d, ad + 2 * ks, bd + 2 * ks, id, kb > 0 || ks > 0);
+            for (int ks = 0; ks < 4; ++ks)
+              mma2(d + part * (CHUNK / parts), ad + 2 * ks, bd + 2 * ks, id, !fresh || ks > 0);
             if (!res) {
               commit2(bar(B_QEMPTY + j));
               if (++j == NQ) j = 0, par ^= 1;
@@ -408,6 +445,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     const uint32_t lanes = (uint32_t)(32 * qw) << 16;
     const uint32_t lead = map_shared_rank(bar(0), 0);
     int i = 0, loads = 0, tiles = 0;
+    bool skips = false;   // rows that add nothing are among the chunk's
+    float2 ahead = {};    // the next chunk's row of this thread
+    int ahead_node = 0;
+    auto row_of = [&](const Seq &s, int ch) {  // (lse in units of log 2, weight)
+      float2 x = make_float2(0.f, 0.f);
+      const int r = CHUNK * ch + tid;
+      if (r >= s.rows) return x;
+      ahead_node = r / a.H;
+      if (BLOCKS) {
+        // the tiles' (maximum, sum) of the row merged, four at a time
+        const float2 *part = a.part + ((int64_t)s.lo * a.H + r) * a.part_stride;
+        float M = -INFINITY, L = 0.f;
+        for (int t = 0; t < 2 * s.tiles; t += 4) {
+          float2 y[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) y[u] = t + u < 2 * s.tiles ? part[t + u] : make_float2(-INFINITY, 0.f);
+          const float m = fmaxf(M, fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x)));
+          if (M != -INFINITY) L *= ex2(M - m);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (y[u].x != -INFINITY) L = fmaf(ex2(y[u].x - m), y[u].y, L);
+          M = m;
+        }
+        x.x = M + log2f(L), x.y = 1.f;
+      } else {
+        x.x = a.lse[(int64_t)s.lo * a.H + r] * 1.4426950408889634f;
+        x.y = a.node_weight ? a.node_weight[s.lo + ahead_node] : 1.f;
+      }
+      if (x.x == -INFINITY) x.y = 0.f;  // a row that sees nothing
+      return x;
+    };
     while (walk.next(a)) {
       const Seq s = walk.s;
       const int p0 = TILE * walk.tile + KC * (int)rank, p = p0 + 32 * qw + lane;
@@ -434,38 +502,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       }
       float acc = 0.f;
       for (int ch = 0; ch < s.chunks; ++ch, ++i) {
-        const int N = columns(s, ch), c0 = hf * (N / 2), c1 = c0 + N / 2;
+        const int N = columns(s, ch), parts = parts_of(N), c0 = hf * (N / 2), c1 = c0 + N / 2;
         if (!LSE && (s.chunks > 1 || walk.first)) {
-          const int b = loads & 1, r = CHUNK * ch + tid;
-          float2 x = make_float2(0.f, 0.f);
-          int node = 0;
-          if (r < s.rows) {
-            node = r / a.H;
-            x.x = a.lse[(int64_t)s.lo * a.H + r] * 1.4426950408889634f;
-            x.y = a.node_weight ? a.node_weight[s.lo + node] : 1.f;
-            if (x.x == -INFINITY) x.y = 0.f;  // a row that sees nothing
-          }
+          if (walk.first && ch == 0) ahead = row_of(s, 0);
+          const float2 x = ahead;
+          const int b = loads & 1;
           s_col[b][tid] = x;
-          s_node[b][tid] = (uint8_t)node;
+          s_node[b][tid] = (uint8_t)ahead_node;
           ++loads;
-          bar_sync(1, 256);  // two buffers: the next but one is written behind the next barrier
+          skips = bar_any(1, 256, tid < N && x.y == 0.f);  // two buffers: the next but one is written behind the next barrier
+          if (s.chunks > 1) ahead = row_of(s, ch + 1 < s.chunks ? ch + 1 : 0);  // asked for while this one is summed
         }
         const int b = (loads - 1) & 1;
         wait(B_DFULL + (i & 1), (uint32_t)(i >> 1));
         tc_fence_after();
         const uint32_t d = tm + lanes + CHUNK * (i & 1);
+        // 16 columns' scores: asked for, and their parts added once they are there
+        auto ask = [&](int c, float (&v)[16]) { tmem_ld16(d + c, v); };
+        auto rest = [&](int c, float (&v)[16]) {
+          for (int x = 1; x < parts; ++x) {
+            float w[16];
+            tmem_ld16(d + x * (CHUNK / parts) + c, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) v[y] += w[y];
+          }
+        };
         if (!LSE) {
           if (!none) {
-#pragma unroll 2
-            for (int c = c0; c < c1; c += 16) {
-              float v[16];
-              tmem_ld16(d + c, v);
-              tmem_wait_ld();
+            float v[16], w[16];
+            auto sum = [&](const float (&v)[16], int c) {
+              const float4 *col = reinterpret_cast<const float4 *>(&s_col[b][c]);
+              if (whole && !skips) {
 #pragma unroll
-              for (int y = 0; y < 16; ++y) {
-                const float2 x = s_col[b][c + y];
-                const float e = ex2(fmaf(v[y], a.scale_log2, -x.x));
-                if (x.y != 0.f && (whole || (vis >> s_node[b][c + y]) & 1)) acc = fmaf(x.y, e, acc);
+                for (int y = 0; y < 8; ++y) {
+                  const float4 x = col[y];
+                  acc = fmaf(x.y, ex2(fmaf(v[2 * y], a.scale_log2, -x.x)), acc);
+                  acc = fmaf(x.w, ex2(fmaf(v[2 * y + 1], a.scale_log2, -x.z)), acc);
+                }
+              } else {
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                  const float2 x = s_col[b][c + y];
+                  const float e = ex2(fmaf(v[y], a.scale_log2, -x.x));
+                  if (x.y != 0.f && (vis >> s_node[b][c + y]) & 1) acc = fmaf(x.y, e, acc);
+                }
+              }
+            };
+            ask(c0, v);
+#pragma unroll 1
+            for (int c = c0; c < c1; c += 32) {  // 16 columns are read while 16 are summed
+              tmem_wait_ld();
+              rest(c, v);
+              if (c + 16 < c1) ask(c + 16, w);
+              sum(v, c);
+              if (c + 16 < c1) {
+                tmem_wait_ld();
+                rest(c + 16, w);
+                if (c + 32 < c1) ask(c + 32, v);
+                sum(w, c + 16);
               }
             }
           }
@@ -473,8 +568,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 #pragma unroll 1
           for (int c = c0; c < c1; c += 16) {
             float v[16], top = 0.f;
-            tmem_ld16(d + c, v);
+            ask(c, v);
             tmem_wait_ld();
+            rest(c, v);
 #pragma unroll
             for (int y = 0; y < 16; ++y) {
               const float x = vis ? v[y] * a.scale_log2 : -INFINITY;
@@ -524,35 +620,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u));
 }
 
-// lse of each row over its sequence's blocks, from the tiles' (maximum, sum): a warp a row.
-constexpr int LNT = 256;
-__global__ void __launch_bounds__(LNT) key_lse_kernel(const KeySumArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
-  const Seq s = seq_of<true>(a, blockIdx.x, false);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = blockIdx.y * (LNT / 32) + warp; r < s.rows; r += gridDim.y * (LNT / 32)) {
-    const float2 *part = a.part + ((int64_t)s.lo * a.H + r) * a.part_stride;
-    float M = -INFINITY, L = 0.f;
-    for (int t = lane; t < 2 * s.tiles; t += 32) M = fmaxf(M, part[t].x);
-    M = warp_max(M);
-    for (int t = lane; t < 2 * s.tiles; t += 32)
-      if (part[t].x != -INFINITY) L = fmaf(ex2(part[t].x - M), part[t].y, L);
-    L = warp_sum(L);
-    if (lane == 0) a.lse[(int64_t)s.lo * a.H + r] = (M + log2f(L)) * 0.6931471805599453f;
-  }
-}
-
-// rows of the block keys, [n_pages][576], for gathers
-bool gather_map(CUtensorMap *m, const void *ptr, int64_t rows) {
-  auto fn = tensor_map_encoder();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {TK, (cuuint64_t)rows}, strides[1] = {TK * 2};
-  cuuint32_t bx[2] = {64, 1}, es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, bx, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool BLOCKS, bool LSE>
 cudaError_t launch_sums(const KeySumArgs &a, const SumMaps &maps, cudaStream_t s) {
   int dev = 0, nsm = 0;
@@ -592,31 +659,21 @@ cudaError_t launch_cache_weights(const KeySumArgs &a, cudaStream_t s) {
   return launch_sums<false, false>(a, maps, s);
 }
 
-// rows' lse, then the tiles' (maximum, sum) of each: two for every 256 of a table row's blocks
+// the tiles' (maximum, sum) of each row: two for every 256 of a table row's blocks
 static int64_t score_tiles(int max_pages) { return 2 * (((int64_t)max_pages + TILE - 1) / TILE); }
 size_t block_scores_ws_bytes(int64_t total, int H, int max_pages) {
-  const size_t lse = ((size_t)total * H * sizeof(float) + 15) & ~(size_t)15;
-  return lse + (size_t)total * H * score_tiles(max_pages) * sizeof(float2);
+  return (size_t)total * H * score_tiles(max_pages) * sizeof(float2);
 }
 
 cudaError_t launch_block_scores(const KeySumArgs &args, void *ws, int *launches, cudaStream_t s) {
   KeySumArgs a = args;
-  a.lse = static_cast<float *>(ws);
-  a.part = reinterpret_cast<float2 *>(static_cast<char *>(ws) + (((size_t)a.total * a.H * sizeof(float) + 15) & ~(size_t)15));
+  a.part = static_cast<float2 *>(ws);
   a.part_stride = score_tiles(a.c.max_pages);
   SumMaps maps;
   memset(&maps, 0, sizeof maps);
-  if (!row_maps(a, &maps) || !gather_map(&maps.k, a.c.pool, a.c.n_pages)) return cudaErrorInvalidValue;
+  if (!row_maps(a, &maps)) return cudaErrorInvalidValue;
+  maps.k = maps.q16;  // not used: the keys come by copies
   cudaError_t e = launch_sums<true, true>(a, maps, s);
-  if (e != cudaSuccess) return e;
-  ++*launches;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early, cfg.numAttrs = 1, cfg.stream = s;
-  cfg.gridDim = dim3(a.n_seqs, 4), cfg.blockDim = dim3(LNT);
-  e = cudaLaunchKernelEx(&cfg, key_lse_kernel, (const KeySumArgs)a);
   if (e != cudaSuccess) return e;
   ++*launches;
   e = launch_sums<true, false>(a, maps, s);
