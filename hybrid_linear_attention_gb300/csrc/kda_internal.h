@@ -117,10 +117,8 @@ struct KeySumArgs {
   const int64_t *mask;         // positions: as TreeAttnArgs
   const float *node_weight;    // positions: [total] or nullptr (ones)
   const float *lse;            // positions: [total, H]
-  float *out;                  // [n_seqs, out_stride] positions: added to; blocks: written
-  int64_t out_stride;
-  float2 *part;                // blocks: (maximum, sum) of each row [total, H, part_stride] over half a tile
-  int64_t part_stride;
+  float *out;                  // positions: [n_seqs, out_stride], added to; blocks: the scores in
+  int64_t out_stride;          //   units of log 2, [total, H, out_stride]
   int *err;
 };
 
@@ -138,6 +136,11 @@ struct SelectArgs {
   int64_t total;
   const int32_t *refs;         // eviction: [n_pages] or nullptr
   float *new_values;           // eviction: [n_seqs, stride], values (in place) or nullptr
+  // blocks: where given, the values are computed first, from every row's scores
+  const float *rows;           // [total, H, rows_stride] in units of log 2
+  int64_t rows_stride;         // a multiple of 4
+  int H;
+  float *scores;               // the values, [n_seqs, stride]; out may be nullptr: no selection then
 };
 
 struct ProArgs {
@@ -212,8 +215,7 @@ cudaError_t launch_pages_free(const PagedCache &c, int32_t *refs, int32_t *held,
                               const int32_t *slots, int n, cudaStream_t s);
 size_t pages_ws_bytes(int n);
 cudaError_t launch_cache_weights(const KeySumArgs &a, cudaStream_t s);
-size_t block_scores_ws_bytes(int64_t total, int H, int max_pages);
-cudaError_t launch_block_scores(const KeySumArgs &a, void *ws, int *launches, cudaStream_t s);
+cudaError_t launch_block_products(const KeySumArgs &a, cudaStream_t s);
 cudaError_t launch_block_keys(const PagedCache &c, const int32_t *from, int n_seqs, void *keys, cudaStream_t s);
 cudaError_t launch_block_select(const SelectArgs &a, cudaStream_t s);
 cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t s);

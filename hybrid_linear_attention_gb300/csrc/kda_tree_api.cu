@@ -434,22 +434,29 @@ kda_status mla_block_keys(const void *pool, int n_layers, int n_pages, int page_
                                      from_lengths, n_seqs, keys, stream), 1);
 }
 
+// every row's scores of the blocks, rows a multiple of 16 bytes long
+static int64_t score_stride(int max_pages) { return ((int64_t)max_pages + 3) & ~(int64_t)3; }
+
 size_t mla_block_scores_workspace_size(int64_t total_nodes, int H, int max_pages) {
   if (total_nodes < 1 || total_nodes > kMaxTreeRows || H < 1 || H > 128 || max_pages < 1 || max_pages > 1 << 20) return 0;
-  return kda::block_scores_ws_bytes(total_nodes, H, max_pages);
+  return (size_t)total_nodes * H * score_stride(max_pages) * sizeof(float);
 }
 
-// mla_block_scores but for the launch; fills *a.
+// mla_block_scores but for the launches: the products (*a) and what makes scores of them (*s, which may
+// hold a selection).
 static kda_status block_scores(const void *q_cat, int H, const void *keys, int n_pages, int page_size,
                                const int32_t *page_table, int max_pages, const int32_t *lengths, const int32_t *cu_nodes,
                                int n_seqs, int64_t total_nodes, float scale, float *scores, int64_t scores_stride,
-                               void *workspace, size_t ws_bytes, kda::KeySumArgs *a) {
+                               void *workspace, size_t ws_bytes, kda::KeySumArgs *a, kda::SelectArgs *s) {
   kda_status st = key_sums(q_cat, H, keys, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
                            total_nodes, scale, a);
   if (st != KDA_OK || total_nodes == 0) return st;
   if (!given(scores) || scores_stride < max_pages || !optional(workspace)) return KDA_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < kda::block_scores_ws_bytes(total_nodes, H, max_pages)) return KDA_ERR_WORKSPACE;
-  a->out = scores, a->out_stride = scores_stride;
+  if (!workspace || ws_bytes < mla_block_scores_workspace_size(total_nodes, H, max_pages)) return KDA_ERR_WORKSPACE;
+  a->out = static_cast<float *>(workspace), a->out_stride = score_stride(max_pages);
+  s->c = a->c, s->n_seqs = n_seqs, s->cu_nodes = cu_nodes, s->total = total_nodes;
+  s->values = s->scores = scores, s->stride = scores_stride;
+  s->rows = a->out, s->rows_stride = a->out_stride, s->H = H;
   return KDA_OK;
 }
 
@@ -459,13 +466,15 @@ kda_status mla_block_scores(const void *q_cat, int H, const void *keys, int n_pa
                             void *workspace, size_t ws_bytes, cudaStream_t stream) {
   KDA_TRACE(TR_MLA_BLOCK_SCORES);
   kda::KeySumArgs a;
+  kda::SelectArgs s;
+  std::memset(&s, 0, sizeof s);
   kda_status st = block_scores(q_cat, H, keys, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
-                               total_nodes, scale, scores, scores_stride, workspace, ws_bytes, &a);
+                               total_nodes, scale, scores, scores_stride, workspace, ws_bytes, &a, &s);
   if (st != KDA_OK || total_nodes == 0) return st;
   if (!kda::mla_latent_supported()) return KDA_ERR_UNSUPPORTED;
-  int launches = 0;
-  const cudaError_t e = kda::launch_block_scores(a, workspace, &launches, stream);
-  return done(e, launches);
+  cudaError_t e = kda::launch_block_products(a, stream);
+  if (e == cudaSuccess) e = kda::launch_block_select(s, stream);
+  return done(e, 2);
 }
 
 // mla_block_select but for the launch; fills *a.
@@ -513,7 +522,6 @@ struct SparseStep {
   kda::KeySumArgs scores;
   kda::SelectArgs choice;
   kda::TreeAttnArgs attention;
-  void *ws;
 };
 static kda_status sparse_step(const void *q_cat, int H, const void *pool, const void *keys, int n_pages, int page_size,
                               const int32_t *page_table, int max_pages, const int32_t *lengths, const int32_t *cu_nodes,
@@ -521,24 +529,21 @@ static kda_status sparse_step(const void *q_cat, int H, const void *pool, const 
                               int recent, float *scores, int64_t scores_stride, int32_t *sel_table, int sel_pages,
                               int32_t *sel_lengths, void *z, kda_dtype z_dtype, void *workspace, size_t ws_bytes,
                               SparseStep *s) {
-  kda_status st = block_scores(q_cat, H, keys, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
-                               total_nodes, scale, scores, scores_stride, workspace, ws_bytes, &s->scores);
+  std::memset(&s->choice, 0, sizeof s->choice);
+  kda_status st = block_select(scores, scores_stride, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs, total_nodes,
+                               blocks, first, recent, sel_table, sel_pages, sel_lengths, &s->choice);
+  if (st != KDA_OK && total_nodes != 0) return st;
+  st = block_scores(q_cat, H, keys, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs, total_nodes, scale,
+                    scores, scores_stride, workspace, ws_bytes, &s->scores, &s->choice);
   if (st != KDA_OK || total_nodes == 0) return st;
-  st = block_select(scores, scores_stride, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs, total_nodes, blocks,
-                    first, recent, sel_table, sel_pages, sel_lengths, &s->choice);
-  if (st != KDA_OK) return st;
-  s->ws = workspace;
   return tree_attention(q_cat, H, pool, n_pages, page_size, sel_table, sel_pages, sel_lengths, cu_nodes, n_seqs,
                         total_nodes, mask, scale, z, z_dtype, workspace, ws_bytes, &s->attention);
 }
 static cudaError_t launch_sparse(const SparseStep &s, int *launches, cudaStream_t stream) {
-  cudaError_t e = kda::launch_block_scores(s.scores, s.ws, launches, stream);
-  if (e != cudaSuccess) return e;
-  e = kda::launch_block_select(s.choice, stream);
-  if (e != cudaSuccess) return e;
-  int more = 0;
-  e = kda::launch_mla_tree(s.attention, &more, stream);
-  *launches += 1 + more;
+  cudaError_t e = kda::launch_block_products(s.scores, stream);
+  if (e == cudaSuccess) e = kda::launch_block_select(s.choice, stream);
+  if (e == cudaSuccess) e = kda::launch_mla_tree(s.attention, launches, stream);
+  *launches += 2;
   return e;
 }
 

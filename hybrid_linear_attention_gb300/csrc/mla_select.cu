@@ -9,9 +9,10 @@
 //                      others the largest, among equals the lower index first, ascending;
 //   eviction           a sequence keeps the selected positions; its rows move up in every layer.
 // A selection is bound by latency: a cluster of CTAs takes a row of values, finds the value that the
-// last one taken has by four passes of 8 bits over order-preserving keys (counts in shared memory, added
-// up across the cluster), and writes what is taken by two prefix sums.  Every sum is of whole numbers, so
-// the result does not depend on the order.  The moves are bound by memory.
+// last one taken has by up to three passes of 11 bits over order-preserving keys (counts in shared memory,
+// added up across the cluster), and writes what is taken by prefix sums.  Every sum is of whole numbers, so
+// the result does not depend on the order.  Blocks' scores are summed up right before, by the same CTAs.
+// The moves are bound by memory.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "kda_tc_ptx.cuh"
@@ -143,14 +144,99 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
   return r;
 }
 
-constexpr int SEL_NT = 1024;
+constexpr int SEL_NT = 512, SEL_W = SEL_NT / 32, BINS = 2048;
+constexpr int SC_ROWS = 1024, SC_GROUP = 128;  // rows, blocks at a time
+
+// The scores of blocks begin .. end - 1, this CTA's, of a sequence's `rows` rows: each row's softmax over
+// all of the cluster's blocks, summed over the rows.
+struct ScoreSpace {
+  float2 ml[SC_ROWS];  // a row's (maximum, sum) over this CTA's blocks
+  float lse[SC_ROWS];  // and over all, in units of log 2
+  float part[SEL_W][SC_GROUP];
+};
+__device__ __forceinline__ void block_scores(const float *base, int64_t stride, int rows, int begin, int end, int cs, float *out,
+                                             ScoreSpace &s) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int r0 = 0; r0 < rows; r0 += SC_ROWS) {
+    const int count = rows - r0 < SC_ROWS ? rows - r0 : SC_ROWS;
+    // a warp two rows at a time, a lane eight of 256 blocks in flight of each
+    for (int r = warp; r < count; r += 2 * SEL_W) {
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int g = begin; g < end; g += 2 * SC_GROUP) {
+        float4 v[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // (up to three more values are read inside the row's stride, and not used)
+            const int b = g + SC_GROUP * h + 4 * lane;
+            v[k][h] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (b < end && r + SEL_W * k < count) v[k][h] = load4(base + (int64_t)(r0 + r + SEL_W * k) * stride + b);
+            if (b + 1 >= end) v[k][h].y = -INFINITY;
+            if (b + 2 >= end) v[k][h].z = -INFINITY;
+            if (b + 3 >= end) v[k][h].w = -INFINITY;
+          }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float4 x = v[k][0], y = v[k][1];
+          const float top = fmaxf(m[k], fmaxf(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w))));
+          const float t = top == -INFINITY ? 0.f : top;
+          l[k] = l[k] * exp2f(m[k] - t) + (((exp2f(x.x - t) + exp2f(x.y - t)) + (exp2f(x.z - t) + exp2f(x.w - t))) +
+                                           ((exp2f(y.x - t) + exp2f(y.y - t)) + (exp2f(y.z - t) + exp2f(y.w - t))));
+          m[k] = top;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float top = warp_max(m[k]);
+        const float sum = warp_sum(l[k] * exp2f(m[k] - (top == -INFINITY ? 0.f : top)));
+        if (lane == 0 && r + SEL_W * k < count) s.ml[r + SEL_W * k] = make_float2(top, sum);
+      }
+    }
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+    for (int r = tid; r < count; r += SEL_NT) {
+      float M = -INFINITY, L = 0.f;
+      for (int c = 0; c < cs; ++c) M = fmaxf(M, (cs > 1 ? (const float2 *)tc::map_rank(s.ml + r, c) : s.ml + r)->x);
+      for (int c = 0; c < cs; ++c) {
+        const float2 y = *(cs > 1 ? (const float2 *)tc::map_rank(s.ml + r, c) : s.ml + r);
+        L += y.x == -INFINITY ? y.y : exp2f(y.x - M) * y.y;  // (no block: 0, or NaN)
+      }
+      s.lse[r] = M == -INFINITY && L == 0.f ? 0.f : M + log2f(L);
+    }
+    if (cs > 1) cluster_sync();  // the others have read ml
+    else __syncthreads();
+    for (int g = begin; g < end; g += SC_GROUP) {
+      const int b = g + 4 * lane;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (b < end)  // (up to three more values are read inside the row's stride, and not used)
+#pragma unroll 4
+        for (int r = warp; r < count; r += SEL_W) {
+          const float4 x = load4(base + (int64_t)(r0 + r) * stride + b);
+          const float e = s.lse[r];
+          acc.x += exp2f(x.x - e), acc.y += exp2f(x.y - e), acc.z += exp2f(x.z - e), acc.w += exp2f(x.w - e);
+        }
+      store4(&s.part[warp][4 * lane], acc);
+      __syncthreads();
+      if (tid < SC_GROUP && g + tid < end) {
+        float sum = r0 == 0 ? 0.f : out[g + tid];
+#pragma unroll
+        for (int w = 0; w < SEL_W; ++w) sum += s.part[w][tid];
+        out[g + tid] = sum;
+      }
+      __syncthreads();
+    }
+  }
+}
+
 template <bool EVICT>
 __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
-  __shared__ int s_hist[2][256];
-  __shared__ int s_bins[256];
+  __shared__ __align__(16) union {
+    ScoreSpace scores;
+    int hist[2][BINS];
+  } s_u;
   __shared__ uint32_t s_digit;
-  __shared__ int s_need;
-  __shared__ unsigned long long s_warp[SEL_NT / 32], s_all;  // taken for sure | equal to the threshold
+  __shared__ int s_need, s_equal, s_sums[SEL_W];
+  __shared__ unsigned long long s_warp[SEL_W], s_all;  // taken for sure | equal to the threshold
   __shared__ int s_gap, s_bad;
   after_previous();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -160,8 +246,8 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
   const int len = a.c.lengths[n];
   const float *value = a.values + (size_t)n * a.stride;
   const int32_t *table = a.c.table + (size_t)n * a.c.max_pages;
-  int count, tail = 0;  // values; pages behind the full blocks
-  bool ok;
+  int count, tail = 0, row0 = 0, rows = 0;  // values; pages behind the full blocks; rows of scores
+  bool ok, fits = true;
   if (EVICT) {
     ok = len >= 0 && len <= room && len <= a.stride;
     count = len;
@@ -175,12 +261,26 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
     count = len / page_size;
     ok = len >= 0 && (int64_t)len + W <= room;
     tail = ok ? (int)(((int64_t)len + W + page_size - 1) / page_size) - count : 0;
-    if (ok && W > 0) ok = (count < a.most ? count : a.most) + tail <= a.out_stride;
+    row0 = lo * a.H, rows = W * a.H;
+    fits = !a.out || (count < a.most ? count : a.most) + tail <= a.out_stride;
     if (W == 0) ok = false;  // nothing to attend from: an empty selection, and no error
-    else if (!ok && rank == 0 && tid == 0) flag(a.c.err, ERR_BAD_INDEX);
+    else if (!(ok && fits) && rank == 0 && tid == 0) flag(a.c.err, ERR_BAD_INDEX);
+  }
+  // this CTA's values, and this thread's of them in order
+  const int width = ok ? ((count + cs - 1) / cs + 3) & ~3 : 0;
+  const int64_t c0 = (int64_t)rank * width;
+  const int cta_begin = c0 < count ? (int)c0 : count, cta_end = c0 + width < count ? (int)c0 + width : count;
+  if (!EVICT && a.rows && ok) {
+    block_scores(a.rows + (int64_t)row0 * a.rows_stride, a.rows_stride, rows, cta_begin, cta_end, cs,
+                 a.scores + (size_t)n * a.stride, s_u.scores);
+    __syncthreads();
+  }
+  if (!EVICT && !a.out) {
+    if (cs > 1) cluster_sync();  // its shared memory is not read by the others any more
+    return;
   }
   int32_t *out = a.out + (size_t)n * a.out_stride;
-  if (!ok) {
+  if (!ok || !fits) {
     for (int64_t j = rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT) out[j] = -1;
     if (rank == 0 && tid == 0) {
       if (EVICT) flag(a.c.err, ERR_BAD_INDEX);
@@ -192,10 +292,9 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
   const int lo = a.first, hi = count - a.recent;  // where values decide (count > most)
   uint32_t threshold = 0;
   int need = 0;  // of the values equal to it
-  // this thread's values, in order
-  const int per = (count + cs * SEL_NT - 1) / (cs * SEL_NT);
-  const int64_t j0 = (int64_t)(rank * SEL_NT + tid) * per;
-  const int begin = j0 < count ? (int)j0 : count, end = j0 + per < count ? (int)j0 + per : count;
+  const int per = (width + SEL_NT - 1) / SEL_NT;
+  const int begin = cta_begin + tid * per < cta_end ? cta_begin + tid * per : cta_end;
+  const int end = begin + per < cta_end ? begin + per : cta_end;
   const bool choose = count > most;
   if (tid == 0) s_gap = INT_MAX, s_bad = 0;
   if (choose) {
@@ -203,44 +302,50 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
     const int from = begin > lo ? begin : lo, to = end < hi ? end : hi;
     if (need > 0) {
 #pragma unroll 1
-      for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        int *hist = s_hist[pass & 1];
-        if (tid < 256) hist[tid] = 0;
+      for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, up = pass == 0 ? 31 : shift + 11, mask = pass == 2 ? 1023 : BINS - 1;
+        int *hist = s_u.hist[pass & 1];
+        for (int b = tid; b < BINS; b += SEL_NT) hist[b] = 0;
         __syncthreads();
         for (int j = from; j < to; ++j) {
           const uint32_t k = order_key(value[j]);
-          if (pass == 0 || k >> (shift + 8) == threshold >> (shift + 8)) atomicAdd(&hist[k >> shift & 255], 1);
+          if (pass == 0 || k >> up == threshold >> up) atomicAdd(&hist[k >> shift & mask], 1);
         }
         if (cs > 1) cluster_sync();
         else __syncthreads();
-        if (tid < 256) {
-          int sum = 0;
-          for (int r = 0; r < cs; ++r) sum += *(cs > 1 ? (int *)tc::map_rank(hist + tid, r) : hist + tid);
-          s_bins[tid] = sum;
+        // this thread's four bins, from the top
+        const int top = BINS - 1 - 4 * tid;
+        int v[4] = {}, sum = 0;
+        for (int r = 0; r < cs; ++r) {
+          const int4 x = *(cs > 1 ? (const int4 *)tc::map_rank(hist + top - 3, r) : (const int4 *)(hist + top - 3));
+          v[0] += x.w, v[1] += x.z, v[2] += x.y, v[3] += x.x;
         }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) sum += v[y];
+        int x = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (lane == 31) s_sums[warp] = x;
         __syncthreads();
-        if (warp == 0) {  // lane l: bins 255 - 8 l down to 248 - 8 l
-          int v[8], sum = 0;
 #pragma unroll
-          for (int y = 0; y < 8; ++y) v[y] = s_bins[255 - 8 * lane - y], sum += v[y];
-          int x = sum;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-          }
-          int above = x - sum;
-          if (above < need && x >= need) {
-            int y = 0;
-            while (above + v[y] < need) above += v[y], ++y;
-            s_digit = 255 - 8 * lane - y;
-            s_need = need - above;
-          }
+        for (int w = 0; w < SEL_W; ++w)
+          if (w < warp) x += s_sums[w];
+        int above = x - sum;
+        if (above < need && x >= need) {
+          int y = 0;
+          while (above + v[y] < need) above += v[y], ++y;
+          s_digit = top - y, s_need = need - above, s_equal = v[y];
         }
         __syncthreads();
         threshold |= s_digit << shift;
         need = s_need;
+        if (need == s_equal && threshold > 0) {  // all that begin so are taken
+          --threshold, need = 0;
+          break;
+        }
       }
     } else {
       threshold = 0xffffffffu;  // no key reaches it
@@ -271,7 +376,7 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
     unsigned long long all = 0;
-    for (int w = 0; w < SEL_NT / 32; ++w) {
+    for (int w = 0; w < SEL_W; ++w) {
       if (w < warp) x += s_warp[w];
       all += s_warp[w];
     }
@@ -462,10 +567,11 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int cluster, int threads, cu
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-// CTAs of a selection: eight values a thread, as long as the GPU has room for the clusters.
-int select_ctas(int n_seqs, int64_t most_values) {
+// CTAs of a selection: two values a thread, or 16384 rows' scores a CTA, as long as the GPU has room for
+// the clusters (two CTAs an SM).
+int select_ctas(int n_seqs, int64_t most_values, double scores) {
   int cs = 1;
-  while (cs < 8 && most_values > (int64_t)cs * SEL_NT * 8 && (int64_t)n_seqs * cs * 2 <= 304) cs *= 2;
+  while (cs < 8 && (most_values > (int64_t)cs * SEL_NT * 2 || scores > 16384. * cs) && (int64_t)n_seqs * cs * 2 <= 304) cs *= 2;
   return cs;
 }
 
@@ -477,13 +583,13 @@ cudaError_t launch_block_keys(const PagedCache &c, const int32_t *from, int n_se
 }
 
 cudaError_t launch_block_select(const SelectArgs &a, cudaStream_t s) {
-  const int cs = select_ctas(a.n_seqs, a.c.max_pages);
+  const int cs = select_ctas(a.n_seqs, a.c.max_pages, a.rows ? (double)a.total * a.H * a.c.max_pages / a.n_seqs : 0.);
   return launch(select_kernel<false>, dim3(a.n_seqs * cs), cs, SEL_NT, s, a);
 }
 
 cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t s) {
   const int64_t room = (int64_t)a.c.max_pages * a.c.page_size;
-  const int cs = select_ctas(a.n_seqs, room < a.stride ? room : a.stride);
+  const int cs = select_ctas(a.n_seqs, room < a.stride ? room : a.stride, 0.);
   cudaError_t e = launch(select_kernel<true>, dim3(a.n_seqs * cs), cs, SEL_NT, s, a);
   if (e != cudaSuccess) return e;
   ++*launches;

@@ -4,9 +4,9 @@
 // With the absorbed form's scores ("Ling-3.1-flash: Grouped Routing and Two Different MLA Caches",
 // section "Why weight absorption keeps the same attention function") s_rt = scale q_r . [c_t ; r_t]
 // of the rows r (nodes x heads) and lse_r = ln sum_t exp(s_rt) over what row r sees,
-//     weights_t += sum_r u_r exp(s_rt - lse_r)        (positions; u_r: the weight of r's node)
-//     score_b    = sum_r exp(s_rb - lse_r)            (blocks: the keys are the pages' mean rows)
-// Blocks take two passes: the first leaves each tile's maximum and sum of a row, the second merges them.
+//     weights_t += sum_r u_r exp(s_rt - lse_r)        (positions; u_r: the weight of r's node);
+// of blocks, whose keys are the pages' mean rows, the scores s_rb themselves are left for the selection
+// (mla_select.cu), which needs a row's sum over all of them first.
 //
 // The keys are the product's M side, D[256 keys x rows] = K Q^T on a pair of CTAs (cta_group::2, 128
 // keys each), so a thread owns a key: the sum over rows runs along its own columns of tensor memory,
@@ -37,7 +37,8 @@ constexpr uint32_t OFF_K = 0, OFF_Q = KB * SLOT;
 constexpr uint32_t QBYTES = KB * (RES / 2) * 128;  // the ring takes NQ x 16 KB of them
 constexpr uint32_t SMEM = OFF_Q + QBYTES + 1024;
 static_assert(NQ * (CHUNK / 2) * 128 <= QBYTES, "the ring fits the resident rows' place");
-constexpr int W_KEYS = 8, W_ROWS = 9, W_MMA = 10, NT = 352;  // warps 0-7: sums
+// warps 0-7 sum; of blocks, the last three load keys too
+constexpr int W_KEYS = 8, W_ROWS = 9, W_MMA = 10, NTP = 352, NTB = NTP + 96;
 constexpr int MAX_CLUSTERS = 80;  // of two CTAs (152 SMs: 76)
 
 // barriers; L: the leading CTA's are used by both
@@ -46,9 +47,9 @@ enum {
   B_KEMPTY = B_KFULL + KB,  //    the products have read it
   B_QFULL = B_KEMPTY + KB,  // L  a slot of streamed rows
   B_QEMPTY = B_QFULL + NQ,
-  B_RFULL = B_QEMPTY + NQ,  // L  the resident rows
-  B_REMPTY,
-  B_DFULL,                  //    a product is done (two buffers)
+  B_RFULL = B_QEMPTY + NQ,  // L  the resident rows (two)
+  B_REMPTY = B_RFULL + 2,
+  B_DFULL = B_REMPTY + 2,   //    a product is done (two buffers)
   B_DFREE = B_DFULL + 2,    // L  and read
   B_DRAIN = B_DFREE + 2, B_N
 };
@@ -72,7 +73,7 @@ __device__ __forceinline__ Seq seq_of(const KeySumArgs &a, int n, bool tell) {
   }
   s.len = a.c.lengths[n];
   const int64_t room = (int64_t)a.c.max_pages * a.c.page_size;
-  const int64_t last = BLOCKS ? s.len : (int64_t)s.len + W;
+  const int64_t last = (int64_t)s.len + W;
   if (W > 0 && (s.len < 0 || last > room || (!BLOCKS && last > a.out_stride))) {
     if (tell && a.err) atomicOr(a.err, ERR_BAD_INDEX);
     s.len = 0, W = 0;
@@ -134,29 +135,10 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool mine) {
                : "memory");
   return r != 0;
 }
-// Sums over the warp's lanes of 16 columns: lane l gets column l & 15's.
-__device__ __forceinline__ float columns_sum(float (&v)[16], int lane) {
-#pragma unroll
-  for (int c = 0; c < 16; ++c) v[c] += __shfl_xor_sync(0xffffffffu, v[c], 16);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-    for (int c = 0; c < o; ++c) {
-      const bool up = lane & o;
-      const float keep = up ? v[c + o] : v[c], give = up ? v[c] : v[c + o];
-      v[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-    }
-  return v[0];
-}
-__device__ __forceinline__ float lanes_max(float x) {  // (a NaN may be passed over: it shows in the sum)
-  const int i = __float_as_int(x);
-  const int m = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
-  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
-}
-
-template <bool BLOCKS, bool LSE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
+template <bool BLOCKS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 1)
     key_sums_kernel(const KeySumArgs a, const __grid_constant__ SumMaps maps) {
+  constexpr int NT = BLOCKS ? NTB : NTP;
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t s_bar[B_N];
   __shared__ uint32_t s_tmem;
@@ -164,10 +146,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   __shared__ unsigned long long s_total, s_scan[NT / 32];
   __shared__ int s_n, s_t;
   __shared__ long long s_at;
-  __shared__ float2 s_col[LSE ? 4 : 2][CHUNK];  // rows' (lse, weight); LSE: a quarter's (maximum, sum)
-  __shared__ uint8_t s_node[2][LSE ? 1 : CHUNK];
-  __shared__ float s_half[2][LSE ? 1 : KC];
-  __shared__ int s_page[BLOCKS ? KC : 1];
+  __shared__ float2 s_col[2][BLOCKS ? 1 : CHUNK];  // rows' (lse, weight)
+  __shared__ uint8_t s_node[2][BLOCKS ? 1 : CHUNK];
+  __shared__ float s_half[2][BLOCKS ? 1 : KC];
   const uint32_t raw = smem_u32(dyn);
   const uint32_t sb = (raw + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -176,7 +157,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   auto bar = [&](int i) { return smem_u32(&s_bar[i]); };
   if (tid < B_N) {
     int n = 1;
-    if (tid < B_KEMPTY || (tid >= B_QFULL && tid < B_QEMPTY) || tid == B_RFULL) n = 2;  // a loader of each CTA
+    if (tid < B_KEMPTY) n = BLOCKS ? 8 : 2;  // the loaders of both CTAs
+    if ((tid >= B_QFULL && tid < B_QEMPTY) || tid == B_RFULL || tid == B_RFULL + 1) n = 2;
     if (tid == B_DFREE || tid == B_DFREE + 1) n = 16;                                 // the sums' warps
     mbar_init(bar(tid), n);
     mbar_fence_init();
@@ -263,43 +245,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   };
   const int lp = 31 - __clz(a.c.page_size);
 
-  if (warp == W_KEYS) {
-    // ---- key blocks: positions a lane a tile load, blocks by 16-byte copies of their keys (gathers by
-    //      TMA, four rows each, took three times as long); a lane first looks four of them up
-    const int box = a.c.page_size < 64 ? a.c.page_size : 64, lb = 31 - __clz(box), in_page = a.c.page_size - 1;
-    uint64_t policy;  // the cache's rows are read once
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  if (warp == W_KEYS || (BLOCKS && warp > W_MMA)) {
+    // ---- key blocks: positions by tile loads, a lane each; blocks by 16-byte copies of their keys, 32 a
+    //      warp, the next tile's pages looked up meanwhile (gathers by TMA, four rows each, took three
+    //      times as long; one warp of copies twice)
+    auto known = [&](int page) { return page >= 0 && page < a.c.n_pages; };
     int tiles = 0;
-    while (walk.next(a)) {
-      const int p0 = TILE * walk.tile + KC * (int)rank;
-      const int32_t *row = a.c.table + (size_t)walk.n * a.c.max_pages;
-      auto known = [&](int page) { return page >= 0 && page < a.c.n_pages; };
-      if (BLOCKS) {
-        const int rows = walk.s.keys - p0 < KC ? walk.s.keys - p0 : KC;  // (may be below 0)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int r = 32 * y + lane;
-          int page = r < rows ? row[p0 + r] : 0;
-          if (!known(page)) {  // no page: any key stands for it
-            if (LSE && a.err) atomicOr(a.err, ERR_BAD_INDEX);
-            page = 0;
-          }
-          s_page[r] = page;
+    if constexpr (BLOCKS) {
+      const int mine = 32 * (warp == W_KEYS ? 0 : warp - W_MMA), piece = lane & 7;
+      auto look = [&]() {
+        const int b = TILE * walk.tile + KC * (int)rank + mine + lane;
+        int page = b < walk.s.keys ? a.c.table[(size_t)walk.n * a.c.max_pages + b] : 0;
+        if (!known(page)) {  // no page: any key stands for it
+          if (a.err) atomicOr(a.err, ERR_BAD_INDEX);
+          page = 0;
         }
-        __syncwarp();
-        bool ok = true;
+        return page;
+      };
+      bool more = walk.next(a), ok = true;
+      int page = more ? look() : 0;
+      while (more) {
+        const int rows = walk.s.keys - (TILE * walk.tile + KC * (int)rank + mine);  // (may be below 0)
+        const char *key[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          key[y] = reinterpret_cast<const char *>(a.c.pool) + (size_t)__shfl_sync(0xffffffffu, page, 4 * y + (lane >> 3)) * (TK * 2) +
+                   16 * piece;
 #pragma unroll 1
         for (int kb = 0; kb < KB; ++kb) {
           if (tiles > 0) ok = ok && warp_wait(B_KEMPTY + kb, (uint32_t)(tiles - 1));
-          const uint32_t dst = sb + OFF_K + kb * SLOT;
-          const int piece = lane & 7;
-          const char *keys = reinterpret_cast<const char *>(a.c.pool) + 128 * kb + 16 * piece;
+          const uint32_t dst = sb + OFF_K + kb * SLOT + mine * 128;
           if (ok)
-#pragma unroll 4
-            for (int r = lane >> 3; r < rows; r += 4)
-              copy16(dst + r * 128 + ((piece ^ (r & 7)) << 4), keys + (size_t)s_page[r] * (TK * 2));
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const int r = 4 * y + (lane >> 3);
+              if (r < rows) copy16(dst + r * 128 + ((piece ^ (r & 7)) << 4), key[y] + 128 * kb);
+            }
           asm volatile("cp.async.commit_group;" ::: "memory");
         }
+        more = walk.next(a);
+        if (more) page = look();
         auto landed = [&](int kb) {
           fence_proxy_async();
           __syncwarp();
@@ -308,12 +293,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         copies_wait<8>(), landed(0), copies_wait<7>(), landed(1), copies_wait<6>(), landed(2);
         copies_wait<5>(), landed(3), copies_wait<4>(), landed(4), copies_wait<3>(), landed(5);
         copies_wait<2>(), landed(6), copies_wait<1>(), landed(7), copies_wait<0>(), landed(8);
-        __syncwarp();  // s_page is read
-      } else {  // positions box lane ..; past the pool, where loads give zeros, for one without a page
-        const int p = p0 + (lane << lb);
+        ++tiles;
+      }
+    } else {
+      const int box = a.c.page_size < 64 ? a.c.page_size : 64, lb = 31 - __clz(box), in_page = a.c.page_size - 1;
+      uint64_t policy;  // the cache's rows are read once
+      asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+      while (walk.next(a)) {
+        const int p = TILE * walk.tile + KC * (int)rank + (lane << lb);
         const bool here = (lane << lb) < KC && p < walk.s.keys;
-        int page = here ? row[p >> lp] : a.c.n_pages;
-        if (!known(page)) {
+        int page = here ? a.c.table[(size_t)walk.n * a.c.max_pages + (p >> lp)] : a.c.n_pages;
+        if (!known(page)) {  // past the pool, where loads give zeros
           if (here && a.err) atomicOr(a.err, ERR_BAD_INDEX);
           page = a.c.n_pages;
         }
@@ -326,44 +316,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
             tma_pair_3d(sb + OFF_K + kb * SLOT + (lane << lb) * 128, &maps.k, 64 * kb, p & in_page, page,
                         map_shared_rank(bar(B_KFULL + kb), 0), policy);
         }
+        ++tiles;
       }
-      ++tiles;
     }
     if (tiles > 0)
       for (int kb = 0; kb < KB; ++kb) wait(B_KEMPTY + kb, (uint32_t)(tiles - 1));  // read before the CTA may end
     if (s_abort)  // a wait ran out: let the copies in flight land
       for (int y = 0; y < 100; ++y) __nanosleep(10000);
   } else if (warp == W_ROWS) {
-    // ---- query rows: resident for a sequence, or a chunk's 64 channels at a time -----------------
-    int segs = 0;      // resident uses so far
+    // ---- query rows: resident for a sequence, or a chunk's 64 channels at a time.  Up to 64 resident
+    //      rows take half of the place, so that the next sequence's are loaded meanwhile; the k-th
+    //      resident sequence uses the barriers k & 1.
+    int segs = 0;
+    bool wide = false;  // the last one took the whole place
     int j = 0, used = 0;
-    uint32_t par = 1;  // parity that a slot's last use ends (a fresh barrier counts as ended)
+    uint32_t par = 1;   // parity that a slot's last use ends (a fresh barrier counts as ended)
     bool ring = false;  // the ring's slots hold what was read last
+    auto seg_done = [&](int k) {
+      if (k >= 0) warp_wait(B_REMPTY + (k & 1), (uint32_t)(k >> 1));
+    };
     while (walk.next(a)) {
       const int64_t row0 = (int64_t)walk.s.lo * a.H;
       if (walk.s.rows <= RES) {
         if (!walk.first) continue;
-        if (segs > 0) warp_wait(B_REMPTY, (uint32_t)(segs - 1));
+        const int half = columns(walk.s, 0) / 2, boxes = half / 16;
+        const bool whole = 2 * half > RES / 2;
+        seg_done(segs - 2);
+        if (whole || wide) seg_done(segs - 1);
+        wide = whole;
         if (ring) {  // every slot read
-          for (int y = 0; y < NQ && y < used; ++y) {
+          for (int y = 0; y < used; ++y) {
             const int k = (j + NQ - 1 - y) % NQ;
             warp_wait(B_QEMPTY + k, k < j ? par ^ 1 : par);
           }
           ring = false;
         }
-        const int half = columns(walk.s, 0) / 2, boxes = half / 16;
-        if (lane == 0) announce(B_RFULL, (uint32_t)(KB * half * 128));
+        const int b = segs & 1;
+        const uint32_t place = sb + OFF_Q + (whole || b == 0 ? 0 : QBYTES / 2);
+        if (lane == 0) announce(B_RFULL + b, (uint32_t)(KB * half * 128));
         __syncwarp();
-        const uint32_t full = map_shared_rank(bar(B_RFULL), 0);
+        const uint32_t full = map_shared_rank(bar(B_RFULL + b), 0);
         for (int x = lane; x < KB * boxes; x += 32) {
-          const int kb = x / boxes, b = x - kb * boxes;
+          const int kb = x / boxes, y = x - kb * boxes;
           if (!s_abort)
-            tma_pair_3d(sb + OFF_Q + kb * half * 128 + b * 2048, &maps.q16, 64 * kb, (int)(row0 + half * (int)rank + 16 * b), 0,
-                        full);
+            tma_pair_3d(place + kb * half * 128 + y * 2048, &maps.q16, 64 * kb, (int)(row0 + half * (int)rank + 16 * y), 0, full);
         }
         ++segs;
       } else {
-        if (!ring && segs > 0) warp_wait(B_REMPTY, (uint32_t)(segs - 1));
+        if (!ring) seg_done(segs - 1);
         ring = true;
         for (int ch = 0; ch < walk.s.chunks; ++ch) {
           const int half = columns(walk.s, ch) / 2;
@@ -386,7 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         }
       }
     }
-    if (segs > 0) wait(B_REMPTY, (uint32_t)(segs - 1));
+    seg_done(segs - 2);
+    seg_done(segs - 1);
     for (int y = 0; y < used; ++y) {
       const int k = (j + NQ - 1 - y) % NQ;
       wait(B_QEMPTY + k, k < j ? par ^ 1 : par);
@@ -401,7 +402,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       bool ok = true;
       while (ok && walk.next(a)) {
         const bool res = walk.s.rows <= RES;
-        if (res && walk.first && !(ok = wait(B_RFULL, (uint32_t)segs))) break;
+        if (res && walk.first && !(ok = wait(B_RFULL + (segs & 1), (uint32_t)(segs >> 1)))) break;
+        const uint32_t place = sb + OFF_Q + (columns(walk.s, 0) > RES / 2 || !(segs & 1) ? 0 : QBYTES / 2);
         for (int ch = 0; ch < walk.s.chunks && ok; ++ch, ++i) {
           const int N = columns(walk.s, ch), parts = parts_of(N);
           const uint32_t id = idesc(1, 256, (uint32_t)N, 0, 0), d = tm + CHUNK * (i & 1);
@@ -414,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
             const int part = kb * parts / KB;
             const bool fresh = kb == 0 || (kb - 1) * parts / KB < part;
             const uint64_t ad = sdesc_sw128(sb + OFF_K + kb * SLOT, 16, 1024);
-            const uint64_t bd = sdesc_sw128(sb + OFF_Q + (res ? kb * (N / 2) * 128 : j * (CHUNK / 2) * 128), 16, 1024);
+            const uint64_t bd = sdesc_sw128(res ? place + kb * (N / 2) * 128 : sb + OFF_Q + j * (CHUNK / 2) * 128, 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               mma2(d + part * (CHUNK / parts), ad + 2 * ks, bd + 2 * ks, id, !fresh || ks > 0);
@@ -428,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           commit2(bar(B_DFULL + (i & 1)));
         }
         if (ok && res && walk.last) {
-          commit2(bar(B_REMPTY));
+          commit2(bar(B_REMPTY + (segs & 1)));
           ++segs;
         }
         ++tiles;
@@ -453,26 +455,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       const int r = CHUNK * ch + tid;
       if (r >= s.rows) return x;
       ahead_node = r / a.H;
-      if (BLOCKS) {
-        // the tiles' (maximum, sum) of the row merged, four at a time
-        const float2 *part = a.part + ((int64_t)s.lo * a.H + r) * a.part_stride;
-        float M = -INFINITY, L = 0.f;
-        for (int t = 0; t < 2 * s.tiles; t += 4) {
-          float2 y[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) y[u] = t + u < 2 * s.tiles ? part[t + u] : make_float2(-INFINITY, 0.f);
-          const float m = fmaxf(M, fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x)));
-          if (M != -INFINITY) L *= ex2(M - m);
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (y[u].x != -INFINITY) L = fmaf(ex2(y[u].x - m), y[u].y, L);
-          M = m;
-        }
-        x.x = M + log2f(L), x.y = 1.f;
-      } else {
-        x.x = a.lse[(int64_t)s.lo * a.H + r] * 1.4426950408889634f;
-        x.y = a.node_weight ? a.node_weight[s.lo + ahead_node] : 1.f;
-      }
+      x.x = a.lse[(int64_t)s.lo * a.H + r] * 1.4426950408889634f;
+      x.y = a.node_weight ? a.node_weight[s.lo + ahead_node] : 1.f;
       if (x.x == -INFINITY) x.y = 0.f;  // a row that sees nothing
       return x;
     };
@@ -493,17 +477,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           }
         }
       }
-      const bool none = __all_sync(0xffffffffu, vis == 0), whole = __all_sync(0xffffffffu, vis == ~0ull);
+      const bool none = __all_sync(0xffffffffu, BLOCKS ? p >= s.keys : vis == 0), whole = __all_sync(0xffffffffu, vis == ~0ull);
       float *out = nullptr;
       float old = 0.f;
-      if (!LSE && hf == 0 && (BLOCKS ? p < s.keys : vis != 0)) {
+      if (!BLOCKS && hf == 0 && vis != 0) {
         out = a.out + (size_t)walk.n * a.out_stride + p;
-        if (!BLOCKS) old = *out;
+        old = *out;
       }
       float acc = 0.f;
       for (int ch = 0; ch < s.chunks; ++ch, ++i) {
         const int N = columns(s, ch), parts = parts_of(N), c0 = hf * (N / 2), c1 = c0 + N / 2;
-        if (!LSE && (s.chunks > 1 || walk.first)) {
+        if (!BLOCKS && (s.chunks > 1 || walk.first)) {
           if (walk.first && ch == 0) ahead = row_of(s, 0);
           const float2 x = ahead;
           const int b = loads & 1;
@@ -528,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
             for (int y = 0; y < 16; ++y) v[y] += w[y];
           }
         };
-        if (!LSE) {
+        if (!BLOCKS) {
           if (!none) {
             float v[16], w[16];
             auto sum = [&](const float (&v)[16], int c) {
@@ -564,45 +548,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
               }
             }
           }
-        } else {
+        } else if (!none) {
 #pragma unroll 1
           for (int c = c0; c < c1; c += 16) {
-            float v[16], top = 0.f;
+            float v[16];
             ask(c, v);
             tmem_wait_ld();
             rest(c, v);
+            const int r = CHUNK * ch + c;
+            float *to = a.out + ((int64_t)s.lo * a.H + r) * a.out_stride + p;
 #pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              const float x = vis ? v[y] * a.scale_log2 : -INFINITY;
-              const float m = lanes_max(x);
-              if ((lane & 15) == y) top = m;
-              v[y] = ex2(x - (m == -INFINITY ? 0.f : m));
-            }
-            const float sum = columns_sum(v, lane);
-            if (lane < 16) s_col[qw][c + lane] = make_float2(top, sum);
+            for (int y = 0; y < 16; ++y)
+              if (r + y < s.rows && p < s.keys) to[y * a.out_stride] = vis ? v[y] * a.scale_log2 : -INFINITY;
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_pair(lead + 8 * (B_DFREE + (i & 1)));
-        if (LSE) {
-          bar_sync(1, 256);
-          const int r = CHUNK * ch + tid;
-          if (r < s.rows && tid < N) {
-            float m = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) m = fmaxf(m, s_col[x][tid].x);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float2 y = s_col[x][tid];
-              if (y.x != -INFINITY) l = fmaf(ex2(y.x - m), y.y, l);
-            }
-            a.part[((int64_t)s.lo * a.H + r) * a.part_stride + 2 * walk.tile + rank] = make_float2(m, l);
-          }
-          bar_sync(1, 256);
-        }
       }
-      if (!LSE) {
+      if (!BLOCKS) {
         if (hf == 1) s_half[tiles & 1][32 * qw + lane] = acc;
         bar_sync(1, 256);  // two buffers here too
         if (out) *out = old + (acc + s_half[tiles & 1][32 * qw + lane]);
@@ -620,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u));
 }
 
-template <bool BLOCKS, bool LSE>
+template <bool BLOCKS>
 cudaError_t launch_sums(const KeySumArgs &a, const SumMaps &maps, cudaStream_t s) {
   int dev = 0, nsm = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -628,7 +592,7 @@ cudaError_t launch_sums(const KeySumArgs &a, const SumMaps &maps, cudaStream_t s
   static std::atomic<int> sms[64];  // SMs of a device once the kernel is opted in there (idempotent if raced)
   if (dev < 64) nsm = sms[dev].load();
   if (nsm == 0) {
-    e = cudaFuncSetAttribute(key_sums_kernel<BLOCKS, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    e = cudaFuncSetAttribute(key_sums_kernel<BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     if (dev < 64) sms[dev].store(nsm);
@@ -639,8 +603,8 @@ cudaError_t launch_sums(const KeySumArgs &a, const SumMaps &maps, cudaStream_t s
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early, cfg.numAttrs = 1, cfg.stream = s;
-  cfg.gridDim = dim3(2 * clusters), cfg.blockDim = dim3(NT), cfg.dynamicSmemBytes = SMEM;
-  return cudaLaunchKernelEx(&cfg, key_sums_kernel<BLOCKS, LSE>, a, maps);
+  cfg.gridDim = dim3(2 * clusters), cfg.blockDim = dim3(BLOCKS ? NTB : NTP), cfg.dynamicSmemBytes = SMEM;
+  return cudaLaunchKernelEx(&cfg, key_sums_kernel<BLOCKS>, a, maps);
 }
 
 bool row_maps(const KeySumArgs &a, SumMaps *maps) {
@@ -656,29 +620,15 @@ cudaError_t launch_cache_weights(const KeySumArgs &a, cudaStream_t s) {
   const int box = a.c.page_size < 64 ? a.c.page_size : 64;
   if (!row_maps(a, &maps) || !tree_map(&maps.k, a.c.pool, true, TK, a.c.page_size, a.c.n_pages, 64, box))
     return cudaErrorInvalidValue;
-  return launch_sums<false, false>(a, maps, s);
+  return launch_sums<false>(a, maps, s);
 }
 
-// the tiles' (maximum, sum) of each row: two for every 256 of a table row's blocks
-static int64_t score_tiles(int max_pages) { return 2 * (((int64_t)max_pages + TILE - 1) / TILE); }
-size_t block_scores_ws_bytes(int64_t total, int H, int max_pages) {
-  return (size_t)total * H * score_tiles(max_pages) * sizeof(float2);
-}
-
-cudaError_t launch_block_scores(const KeySumArgs &args, void *ws, int *launches, cudaStream_t s) {
-  KeySumArgs a = args;
-  a.part = static_cast<float2 *>(ws);
-  a.part_stride = score_tiles(a.c.max_pages);
+cudaError_t launch_block_products(const KeySumArgs &a, cudaStream_t s) {
   SumMaps maps;
   memset(&maps, 0, sizeof maps);
   if (!row_maps(a, &maps)) return cudaErrorInvalidValue;
   maps.k = maps.q16;  // not used: the keys come by copies
-  cudaError_t e = launch_sums<true, true>(a, maps, s);
-  if (e != cudaSuccess) return e;
-  ++*launches;
-  e = launch_sums<true, false>(a, maps, s);
-  ++*launches;
-  return e;
+  return launch_sums<true>(a, maps, s);
 }
 
 }  // namespace kda
