@@ -17,6 +17,7 @@
 #include "kda_internal.h"
 #include "kda_tc_ptx.cuh"
 
+#include <atomic>
 #include <climits>
 
 namespace kda {
@@ -476,50 +477,73 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
   if (cs > 1) cluster_sync();  // its shared memory is not read by the others any more
 }
 
-// Row kept[j] of each sequence moves to row j, in every layer: a CTA takes 128 bytes of the rows, 256
-// rows at a time, which are read before they are written; kept[j] >= j and both rise, so no later batch
-// reads a row that an earlier one wrote.  The next batch's places are looked up while one is copied.
-constexpr int MV_NT = 256, MV_U = 8, MV_ROWS = MV_NT / 8, MV_BATCH = MV_ROWS * MV_U;
-__global__ void __launch_bounds__(MV_NT) evict_rows_kernel(const PagedCache c, const int32_t *kept_all, int budget) {
+// Row kept[j] of each sequence moves to row j, in every layer.  A CTA takes 128 bytes of the rows, 128
+// rows at a time, through a ring in shared memory of which all but one batch are on their way: a batch is
+// written once all of its reads, and so those of the batches before, are done.  kept[j] >= j and both
+// rise, so no later batch reads a row that an earlier one wrote.  A thread writes what it read itself; the
+// places of a batch are looked up one ahead of its reads.
+constexpr int MV_NT = 256, MV_U = 4, MV_ROWS = MV_NT / 8, MV_BATCH = MV_ROWS * MV_U, MV_STAGES = 4;
+constexpr int MV_SMEM = MV_STAGES * MV_BATCH * 128;
+__global__ void __launch_bounds__(MV_NT, 3) evict_rows_kernel(const PagedCache c, const int32_t *kept_all, int budget) {
+  extern __shared__ uint4 ring[];  // [stage][MV_U][MV_NT]
   after_previous();
-  const int n = blockIdx.z, layer = blockIdx.y, piece = blockIdx.x * 8 + (threadIdx.x & 7), r = threadIdx.x >> 3;
+  const int n = blockIdx.z, layer = blockIdx.y, tid = threadIdx.x, piece = blockIdx.x * 8 + (tid & 7), r = tid >> 3;
   const int32_t *kept = kept_all + (size_t)n * budget;
   if (kept[budget - 1] < budget) return;  // nothing moves (or the sequence is refused)
   const int32_t *table = c.table + (size_t)n * c.max_pages;
   uint4 *rows = reinterpret_cast<uint4 *>(c.pool) + (size_t)layer * c.n_pages * c.page_size * ROW16 + piece;
   const int lp = 31 - __clz(c.page_size), in_page = c.page_size - 1;
-  int64_t from[MV_U], to[MV_U];
+  const int batches = (budget + MV_BATCH - 1) / MV_BATCH;
+  int64_t from[MV_U];  // of the next batch to read; -1: the row stays where it is
   auto look = [&](int b) {
     int k[MV_U];
 #pragma unroll
     for (int y = 0; y < MV_U; ++y) {
-      const int j = b + y * MV_ROWS + r;
+      const int j = b * MV_BATCH + y * MV_ROWS + r;
       k[y] = j < budget ? kept[j] : 0;
+      if (k[y] <= j) k[y] = -1;
     }
 #pragma unroll
-    for (int y = 0; y < MV_U; ++y) {
-      const int j = b + y * MV_ROWS + r;
-      from[y] = -1;
-      if (k[y] > j) {
-        from[y] = ((int64_t)table[k[y] >> lp] << lp) + (k[y] & in_page);
-        to[y] = ((int64_t)table[j >> lp] << lp) + (j & in_page);
-      }
-    }
+    for (int y = 0; y < MV_U; ++y) from[y] = k[y] < 0 ? -1 : ((int64_t)table[k[y] >> lp] << lp) + (k[y] & in_page);
   };
-  look(0);
-  for (int b = 0; b < budget; b += MV_BATCH) {
-    uint4 x[MV_U];
-    int64_t place[MV_U];
-#pragma unroll
-    for (int y = 0; y < MV_U; ++y) {
-      place[y] = from[y] < 0 ? -1 : to[y];
-      if (from[y] >= 0) x[y] = __ldcs(rows + from[y] * ROW16);
-    }
-    if (b + MV_BATCH < budget) look(b + MV_BATCH);
-    __syncthreads();
+  uint32_t moves = 0;  // MV_U bits a batch of the ring, the next one to be written lowest
+  auto read = [&](int b) {
+    uint4 *to = ring + (b % MV_STAGES) * (MV_U * MV_NT) + tid;
 #pragma unroll
     for (int y = 0; y < MV_U; ++y)
-      if (place[y] >= 0) __stcs(rows + place[y] * ROW16, x[y]);
+      if (b < batches && from[y] >= 0) {
+        moves |= 1u << ((MV_STAGES - 1) * MV_U + y);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to + y * MV_NT)),
+                     "l"(__cvta_generic_to_global(rows + from[y] * ROW16))
+                     : "memory");
+      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  look(0);
+#pragma unroll 1
+  for (int b = 0; b < MV_STAGES - 1; ++b) {
+    read(b);
+    moves >>= MV_U;
+    if (b + 1 < batches) look(b + 1);
+  }
+#pragma unroll 1
+  for (int b = 0; b < batches; ++b) {
+    read(b + MV_STAGES - 1);
+    if (b + MV_STAGES < batches) look(b + MV_STAGES);
+    int to[MV_U];
+#pragma unroll
+    for (int y = 0; y < MV_U; ++y) {
+      const int j = b * MV_BATCH + y * MV_ROWS + r;
+      to[y] = moves >> y & 1 ? table[j >> lp] : 0;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(MV_STAGES - 1) : "memory");
+    __syncthreads();
+    const uint4 *x = ring + (b % MV_STAGES) * (MV_U * MV_NT) + tid;
+#pragma unroll
+    for (int y = 0; y < MV_U; ++y)
+      if (moves >> y & 1)
+        __stcs(rows + (((int64_t)to[y] << lp) + ((b * MV_BATCH + y * MV_ROWS + r) & in_page)) * ROW16, x[y * MV_NT]);
+    moves >>= MV_U;
   }
 }
 
@@ -555,9 +579,9 @@ __global__ void __launch_bounds__(128) pages_trim_kernel(PagedCache c, int32_t *
 }
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, int cluster, int threads, cudaStream_t s, A... args) {
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int cluster, int threads, int smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.stream = s;
+  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -579,28 +603,37 @@ int select_ctas(int n_seqs, int64_t most_values, double scores) {
 
 cudaError_t launch_block_keys(const PagedCache &c, const int32_t *from, int n_seqs, void *keys, cudaStream_t s) {
   const int ctas = 1064 / c.n_layers;  // seven an SM
-  return launch(block_keys_kernel, dim3(ctas < 1 ? 1 : ctas, c.n_layers), 1, BK_NT, s, c, from, n_seqs, static_cast<uint4 *>(keys));
+  return launch(block_keys_kernel, dim3(ctas < 1 ? 1 : ctas, c.n_layers), 1, BK_NT, 0, s, c, from, n_seqs, static_cast<uint4 *>(keys));
 }
 
 cudaError_t launch_block_select(const SelectArgs &a, cudaStream_t s) {
   const int cs = select_ctas(a.n_seqs, a.c.max_pages, a.rows ? (double)a.total * a.H * a.c.max_pages / a.n_seqs : 0.);
-  return launch(select_kernel<false>, dim3(a.n_seqs * cs), cs, SEL_NT, s, a);
+  return launch(select_kernel<false>, dim3(a.n_seqs * cs), cs, SEL_NT, 0, s, a);
 }
 
 cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t s) {
   const int64_t room = (int64_t)a.c.max_pages * a.c.page_size;
   const int cs = select_ctas(a.n_seqs, room < a.stride ? room : a.stride, 0.);
-  cudaError_t e = launch(select_kernel<true>, dim3(a.n_seqs * cs), cs, SEL_NT, s, a);
+  cudaError_t e = launch(select_kernel<true>, dim3(a.n_seqs * cs), cs, SEL_NT, 0, s, a);
   if (e != cudaSuccess) return e;
   ++*launches;
-  e = launch(evict_rows_kernel, dim3(ROW16 / 8, a.c.n_layers, a.n_seqs), 1, MV_NT, s, a.c, a.out, a.most);
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<bool> opted[64];  // devices where the kernel may use its shared memory (idempotent if raced)
+  if (dev >= 64 || !opted[dev].load()) {
+    e = cudaFuncSetAttribute(evict_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MV_SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) opted[dev].store(true);
+  }
+  e = launch(evict_rows_kernel, dim3(ROW16 / 8, a.c.n_layers, a.n_seqs), 1, MV_NT, MV_SMEM, s, a.c, a.out, a.most);
   ++*launches;
   return e;
 }
 
 cudaError_t launch_pages_trim(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots, const int32_t *slots, int n,
                               cudaStream_t s) {
-  return launch(pages_trim_kernel, dim3(n), 1, 128, s, c, const_cast<int32_t *>(c.table), refs, held, n_slots, slots);
+  return launch(pages_trim_kernel, dim3(n), 1, 128, 0, s, c, const_cast<int32_t *>(c.table), refs, held, n_slots, slots);
 }
 
 }  // namespace kda

@@ -59,8 +59,12 @@ struct SumMaps {
 };
 
 struct Seq {
-  int lo, rows, len, keys, tiles, chunks;
+  int lo, rows, len, keys, tiles;
+  uint32_t live;  // chunks that hold a node that counts (8192 rows: 32 at most)
+  __device__ __forceinline__ int chunks() const { return __popc(live); }
 };
+// the live chunk behind chunk ch (-1: the first), or -1
+__device__ __forceinline__ int next_chunk(const Seq &s, int ch) { return __ffs((int)(ch < 0 ? s.live : s.live & (~1u << ch))) - 1; }
 template <bool BLOCKS>
 __device__ __forceinline__ Seq seq_of(const KeySumArgs &a, int n, bool tell) {
   Seq s;
@@ -80,8 +84,17 @@ __device__ __forceinline__ Seq seq_of(const KeySumArgs &a, int n, bool tell) {
   }
   s.rows = W * a.H;
   s.keys = W == 0 ? 0 : BLOCKS ? s.len / a.c.page_size : s.len + W;
+  const int chunks = s.rows <= RES ? 1 : (s.rows + CHUNK - 1) / CHUNK;
+  s.live = ~0u >> (32 - chunks);
+  if (!BLOCKS && a.node_weight) {
+    s.live = 0;
+#pragma unroll 8
+    for (int i = 0; i < W; ++i)
+      if (a.node_weight[s.lo + i] != 0.f)
+        s.live |= chunks == 1 ? 1u : (~0u << (i * a.H / CHUNK)) & (~0u >> (31 - ((i + 1) * a.H - 1) / CHUNK));
+    if (s.live == 0) s.keys = 0;
+  }
   s.tiles = (s.keys + TILE - 1) / TILE;
-  s.chunks = s.rows <= RES ? 1 : (s.rows + CHUNK - 1) / CHUNK;
   return s;
 }
 
@@ -104,7 +117,7 @@ struct Walk {
         continue;
       }
       tile = t++;
-      at += s.chunks;
+      at += s.chunks();
       last = t >= s.tiles || at >= stop;
       return true;
     }
@@ -126,15 +139,6 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// a barrier of the sums' warps that also tells whether any thread says so
-__device__ __forceinline__ bool bar_any(int id, int n, bool mine) {
-  uint32_t r;
-  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %3, 0;\nbar.red.or.pred p, %1, %2, q;\nselp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(r)
-               : "r"(id), "r"(n), "r"((uint32_t)mine)
-               : "memory");
-  return r != 0;
-}
 template <bool BLOCKS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 1)
     key_sums_kernel(const KeySumArgs a, const __grid_constant__ SumMaps maps) {
@@ -146,8 +150,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   __shared__ unsigned long long s_total, s_scan[NT / 32];
   __shared__ int s_n, s_t;
   __shared__ long long s_at;
-  __shared__ float2 s_col[2][BLOCKS ? 1 : CHUNK];  // rows' (lse, weight)
-  __shared__ uint8_t s_node[2][BLOCKS ? 1 : CHUNK];
+  __shared__ __align__(16) float2 s_col[2][BLOCKS ? 2 : CHUNK];  // rows' (lse, weight)
+  __shared__ __align__(16) uint8_t s_node[2][BLOCKS ? 16 : CHUNK];
+  __shared__ uint32_t s_counts[2][8];  // bits of the rows that count
   __shared__ float s_half[2][BLOCKS ? 1 : KC];
   const uint32_t raw = smem_u32(dyn);
   const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -180,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     unsigned long long mine = 0;
     for (int n = tid; n < a.n_seqs; n += NT) {
       const Seq s = seq_of<BLOCKS>(a, n, blockIdx.x == 0);
-      mine += (unsigned long long)s.tiles * s.chunks;
+      mine += (unsigned long long)s.tiles * s.chunks();
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -194,7 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     for (int n0 = 0; n0 < a.n_seqs && before <= begin; n0 += NT) {
       Seq s = {};
       if (n0 + tid < a.n_seqs) s = seq_of<BLOCKS>(a, n0 + tid, false);
-      const long long cost = (long long)s.tiles * s.chunks;
+      const long long cost = (long long)s.tiles * s.chunks();
       long long x = cost;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -212,8 +217,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
       }
       const long long at = before + ahead + x - cost;
       if (at <= begin && begin < at + cost) {
-        const int t = (int)((begin - at + s.chunks - 1) / s.chunks);
-        s_n = n0 + tid, s_t = t, s_at = at + (long long)t * s.chunks;
+        const int t = (int)((begin - at + s.chunks() - 1) / s.chunks());
+        s_n = n0 + tid, s_t = t, s_at = at + (long long)t * s.chunks();
       }
       before += all;
       __syncthreads();
@@ -365,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
       } else {
         if (!ring) seg_done(segs - 1);
         ring = true;
-        for (int ch = 0; ch < walk.s.chunks; ++ch) {
+        for (int ch = next_chunk(walk.s, -1); ch >= 0; ch = next_chunk(walk.s, ch)) {
           const int half = columns(walk.s, ch) / 2;
           const int64_t r = row0 + CHUNK * ch + half * (int)rank;
 #pragma unroll 1
@@ -404,13 +409,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         const bool res = walk.s.rows <= RES;
         if (res && walk.first && !(ok = wait(B_RFULL + (segs & 1), (uint32_t)(segs >> 1)))) break;
         const uint32_t place = sb + OFF_Q + (columns(walk.s, 0) > RES / 2 || !(segs & 1) ? 0 : QBYTES / 2);
-        for (int ch = 0; ch < walk.s.chunks && ok; ++ch, ++i) {
+        bool fill = true;  // the tile's keys are waited for
+        for (int ch = next_chunk(walk.s, -1), then; ch >= 0 && ok; ch = then, ++i) {
+          then = next_chunk(walk.s, ch);
           const int N = columns(walk.s, ch), parts = parts_of(N);
           const uint32_t id = idesc(1, 256, (uint32_t)N, 0, 0), d = tm + CHUNK * (i & 1);
           if (i >= 2 && !(ok = wait(B_DFREE + (i & 1), (uint32_t)((i >> 1) - 1)))) break;
 #pragma unroll 1
           for (int kb = 0; kb < KB; ++kb) {
-            if (ch == 0 && !(ok = wait(B_KFULL + kb, (uint32_t)tiles))) break;
+            if (fill && !(ok = wait(B_KFULL + kb, (uint32_t)tiles))) break;
             if (!res && !(ok = wait(B_QFULL + j, par))) break;
             tc_fence_after();
             const int part = kb * parts / KB;
@@ -424,8 +431,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
               commit2(bar(B_QEMPTY + j));
               if (++j == NQ) j = 0, par ^= 1;
             }
-            if (ch == walk.s.chunks - 1) commit2(bar(B_KEMPTY + kb));
+            if (then < 0) commit2(bar(B_KEMPTY + kb));
           }
+          fill = false;
           if (!ok) break;
           commit2(bar(B_DFULL + (i & 1)));
         }
@@ -447,7 +455,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     const uint32_t lanes = (uint32_t)(32 * qw) << 16;
     const uint32_t lead = map_shared_rank(bar(0), 0);
     int i = 0, loads = 0, tiles = 0;
-    bool skips = false;   // rows that add nothing are among the chunk's
     float2 ahead = {};    // the next chunk's row of this thread
     int ahead_node = 0;
     auto row_of = [&](const Seq &s, int ch) {  // (lse in units of log 2, weight)
@@ -485,17 +492,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         old = *out;
       }
       float acc = 0.f;
-      for (int ch = 0; ch < s.chunks; ++ch, ++i) {
+      const int head = next_chunk(s, -1);
+      for (int ch = head, then; ch >= 0; ch = then, ++i) {
+        then = next_chunk(s, ch);
         const int N = columns(s, ch), parts = parts_of(N), c0 = hf * (N / 2), c1 = c0 + N / 2;
-        if (!BLOCKS && (s.chunks > 1 || walk.first)) {
-          if (walk.first && ch == 0) ahead = row_of(s, 0);
+        if (!BLOCKS && (s.rows > RES || walk.first)) {
+          if (walk.first && ch == head) ahead = row_of(s, ch);
           const float2 x = ahead;
           const int b = loads & 1;
           s_col[b][tid] = x;
           s_node[b][tid] = (uint8_t)ahead_node;
+          const uint32_t counts = __ballot_sync(0xffffffffu, x.y != 0.f);
+          if (lane == 0) s_counts[b][warp] = counts;
           ++loads;
-          skips = bar_any(1, 256, tid < N && x.y == 0.f);  // two buffers: the next but one is written behind the next barrier
-          if (s.chunks > 1) ahead = row_of(s, ch + 1 < s.chunks ? ch + 1 : 0);  // asked for while this one is summed
+          bar_sync(1, 256);  // two buffers: the next but one is written behind the next barrier
+          if (s.rows > RES) ahead = row_of(s, then >= 0 ? then : head);  // asked for while this one is summed
         }
         const int b = (loads - 1) & 1;
         wait(B_DFULL + (i & 1), (uint32_t)(i >> 1));
@@ -517,19 +528,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
             float v[16], w[16];
             auto sum = [&](const float (&v)[16], int c) {
               const float4 *col = reinterpret_cast<const float4 *>(&s_col[b][c]);
-              if (whole && !skips) {
+              const uint32_t counts = s_counts[b][c >> 5] >> (c & 16) & 0xffff;
+              if (counts == 0) return;
+              if (whole && counts == 0xffff) {
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {
                   const float4 x = col[y];
                   acc = fmaf(x.y, ex2(fmaf(v[2 * y], a.scale_log2, -x.x)), acc);
                   acc = fmaf(x.w, ex2(fmaf(v[2 * y + 1], a.scale_log2, -x.z)), acc);
                 }
-              } else {
+              } else if (whole) {
 #pragma unroll
                 for (int y = 0; y < 16; ++y) {
                   const float2 x = s_col[b][c + y];
                   const float e = ex2(fmaf(v[y], a.scale_log2, -x.x));
-                  if (x.y != 0.f && (vis >> s_node[b][c + y]) & 1) acc = fmaf(x.y, e, acc);
+                  if (counts >> y & 1) acc = fmaf(x.y, e, acc);
+                }
+              } else {
+                const uint4 nodes = *reinterpret_cast<const uint4 *>(&s_node[b][c]);
+                const uint32_t word[4] = {nodes.x, nodes.y, nodes.z, nodes.w};
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                  const float4 x = col[y >> 1];
+                  const float lse = y & 1 ? x.z : x.x, u = y & 1 ? x.w : x.y;
+                  const float e = ex2(fmaf(v[y], a.scale_log2, -lse));
+                  const uint32_t node = word[y >> 2] >> (8 * (y & 3)) & 63;
+                  const uint32_t bit = (node & 32 ? (uint32_t)(vis >> 32) : (uint32_t)vis) >> (node & 31) & 1;
+                  if ((counts >> y & 1) && bit) acc = fmaf(u, e, acc);
                 }
               }
             };
