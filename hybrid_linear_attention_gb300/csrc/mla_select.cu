@@ -38,16 +38,28 @@ __device__ __forceinline__ bool page_known(const PagedCache &c, int page) { retu
 
 // ---- block keys -------------------------------------------------------------------------------
 
-// Units (page, layer) of the pages that filled up, CTA b taking every gridDim.x-th page: 72 threads
-// take a row's pieces, four rows at a time, four loads in flight a thread; the four sums meet in
-// shared memory.
-constexpr int BK_ROWS = 4, BK_NT = BK_ROWS * ROW16, BK_SEQS = BK_NT;
-__global__ void __launch_bounds__(BK_NT) block_keys_kernel(const PagedCache c, const int32_t *from, int n_seqs, uint4 *keys) {
+// Units (page, layer) of the pages that filled up, CTA b taking every gridDim.x-th page.  A warp brings the
+// pages in, 16 rows a bulk copy, through a ring in shared memory; 72 threads take a row's pieces, four rows
+// at a time, and their four sums meet in shared memory.
+constexpr int BK_ROWS = 4, BK_SUM = BK_ROWS * ROW16, BK_NT = BK_SUM + 32, BK_SEQS = BK_NT, BK_U = 4, BK_RING = 3;
+constexpr int BK_SLOT = BK_U * BK_SUM * 16, BK_SMEM = BK_RING * BK_SLOT;
+__global__ void __launch_bounds__(BK_NT, 3) block_keys_kernel(const PagedCache c, const int32_t *from, int n_seqs, bf16 *keys) {
+  extern __shared__ __align__(128) uint4 ring[];  // [BK_RING][16 rows]
   __shared__ int s_end[BK_SEQS], s_first[BK_SEQS], s_warp[BK_NT / 32];
-  __shared__ float s_sum[BK_ROWS][576];
-  after_previous();
+  __shared__ __align__(16) float s_sum[BK_ROWS][576];
+  __shared__ __align__(8) uint64_t s_full[BK_RING], s_empty[BK_RING];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, layer = blockIdx.y;
-  const int group = tid / ROW16, piece = tid - group * ROW16;
+  const int steps = c.page_size / (BK_U * BK_ROWS);
+  const bool loads = warp == BK_SUM / 32;
+  if (tid < BK_RING) {
+    tc::mbar_init(tc::smem_u32(&s_full[tid]), 1);
+    tc::mbar_init(tc::smem_u32(&s_empty[tid]), BK_SUM / 32);
+    tc::mbar_fence_init();
+  }
+  int slot = 0;
+  uint32_t par = 0;  // of the slot's next filling
+  bool ok = true;    // no wait has run out
+  after_previous();
   const int64_t room = (int64_t)c.max_pages * c.page_size;
   int64_t before = 0;  // pages of the sequences before n0
   for (int n0 = 0; n0 < n_seqs; n0 += BK_SEQS) {
@@ -77,57 +89,78 @@ __global__ void __launch_bounds__(BK_NT) block_keys_kernel(const PagedCache c, c
     }
     s_end[tid] = x, s_first[tid] = first;  // at most 288 x 2^20 pages
     __syncthreads();
-    const int begin = (int)((blockIdx.x + gridDim.x - before % gridDim.x) % gridDim.x);
-    for (int u = begin; u < all; u += gridDim.x) {
+    // page of unit u; past the last unit, or where there is none: -1
+    auto look = [&](int u) {
+      if (u >= all) return -1;
       int lo = 0, hi = BK_SEQS - 1;  // the first sequence whose pages end behind u
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (s_end[mid] > u) hi = mid;
         else lo = mid + 1;
       }
-      const int j = s_first[lo] + u - (lo > 0 ? s_end[lo - 1] : 0);
-      const int page = c.table[(size_t)(n0 + lo) * c.max_pages + j];
-      if (!page_known(c, page)) {
+      return c.table[(size_t)(n0 + lo) * c.max_pages + s_first[lo] + u - (lo > 0 ? s_end[lo - 1] : 0)];
+    };
+    const uint4 *pool = reinterpret_cast<const uint4 *>(c.pool) + (size_t)layer * c.n_pages * c.page_size * ROW16;
+    const int begin = (int)((blockIdx.x + gridDim.x - before % gridDim.x) % gridDim.x);
+    int page = look(begin);
+    for (int u = begin; u < all; u += gridDim.x) {
+      const int mine = page;
+      page = look(u + gridDim.x);
+      if (!page_known(c, mine)) {
         if (tid == 0 && layer == 0) flag(c.err, ERR_BAD_INDEX);
         continue;
       }
-      const uint4 *rows = reinterpret_cast<const uint4 *>(c.pool) + ((size_t)layer * c.n_pages + page) * c.page_size * ROW16 + piece;
-      float sum[8] = {};
-      auto add = [&](const uint4 &v) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) sum[2 * y] += __uint_as_float(w[y] << 16), sum[2 * y + 1] += __uint_as_float(w[y] & 0xffff0000u);
-      };
-      for (int r = group; r < c.page_size; r += 4 * BK_ROWS) {  // pages hold 16 rows at least
-        uint4 v[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) v[y] = __ldcs(rows + (size_t)(r + BK_ROWS * y) * ROW16);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) add(v[y]);
-      }
-      __syncthreads();  // the sums of the page before are read
-#pragma unroll
-      for (int y = 0; y < 8; ++y) s_sum[group][8 * piece + y] = sum[y];
-      __syncthreads();
-      if (tid < ROW16) {
-        const float f = 1.f / c.page_size;  // a power of two
-        uint32_t w[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          float m[2];
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const int i = 8 * tid + 2 * y + z;
-            m[z] = ((s_sum[0][i] + s_sum[1][i]) + (s_sum[2][i] + s_sum[3][i])) * f;
+      if (loads) {
+        if (lane == 0)
+          for (int s = 0; s < steps; ++s) {
+            const uint32_t full = tc::smem_u32(&s_full[slot]);
+            if (ok) ok = tc::mbar_wait(tc::smem_u32(&s_empty[slot]), par ^ 1);
+            if (ok) {
+              tc::mbar_expect_tx(full, BK_SLOT);
+              asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                               tc::smem_u32(ring) + slot * BK_SLOT),
+                           "l"(__cvta_generic_to_global(pool + ((size_t)mine * c.page_size + s * (BK_U * BK_ROWS)) * ROW16)),
+                           "r"(BK_SLOT), "r"(full)
+                           : "memory");
+            }
+            if (++slot == BK_RING) slot = 0, par ^= 1;
           }
-          const __nv_bfloat162 b = __floats2bfloat162_rn(m[0], m[1]);
-          w[y] = *reinterpret_cast<const uint32_t *>(&b);
-        }
-        keys[((size_t)layer * c.n_pages + page) * ROW16 + tid] = make_uint4(w[0], w[1], w[2], w[3]);
+        __syncwarp();
+        continue;
       }
+      float sum[8] = {};
+#pragma unroll 1
+      for (int s = 0; s < steps; ++s) {
+        if (ok) ok = tc::mbar_wait(tc::smem_u32(&s_full[slot]), par);
+#pragma unroll
+        for (int x = 0; x < BK_U; ++x) {
+          const uint4 v = ring[(slot * BK_U + x) * BK_SUM + tid];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) sum[2 * y] += __uint_as_float(w[y] << 16), sum[2 * y + 1] += __uint_as_float(w[y] & 0xffff0000u);
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&s_empty[slot]));
+        if (++slot == BK_RING) slot = 0, par ^= 1;
+      }
+      const int group = tid / ROW16, piece = tid - group * ROW16;
+      asm volatile("bar.sync 1, %0;" ::"n"(BK_SUM) : "memory");  // the sums of the page before are read
+      store4(&s_sum[group][8 * piece], make_float4(sum[0], sum[1], sum[2], sum[3]));
+      store4(&s_sum[group][8 * piece + 4], make_float4(sum[4], sum[5], sum[6], sum[7]));
+      asm volatile("bar.sync 1, %0;" ::"n"(BK_SUM) : "memory");
+      // two channels a thread
+      const float2 g0 = load2(&s_sum[0][2 * tid]), g1 = load2(&s_sum[1][2 * tid]), g2 = load2(&s_sum[2][2 * tid]), g3 = load2(&s_sum[3][2 * tid]);
+      const float f = 1.f / c.page_size;  // a power of two
+      if (ok)
+        store2(keys + ((size_t)layer * c.n_pages + mine) * 576 + 2 * tid,
+               make_float2(((g0.x + g1.x) + (g2.x + g3.x)) * f, ((g0.y + g1.y) + (g2.y + g3.y)) * f));
     }
     before += all;
     __syncthreads();
+  }
+  if (!ok) {  // let the copies in flight land
+    flag(c.err, ERR_MBAR_TIMEOUT);
+    for (int y = 0; y < 100; ++y) __nanosleep(10000);
   }
 }
 
@@ -229,16 +262,24 @@ __device__ __forceinline__ void block_scores(const float *base, int64_t stride, 
   }
 }
 
+// What a CTA tells the others of its cluster.
+struct SelectEnd {
+  unsigned long long taken;  // taken for sure << 32 | equal to the threshold
+  int gap, bad;              // the first value that is not taken; the last page that must not move
+};
+
 template <bool EVICT>
 __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
+  constexpr int HELD = EVICT ? 16 : 4;  // values of a thread that stay in registers
   __shared__ __align__(16) union {
     ScoreSpace scores;
     int hist[2][BINS];
   } s_u;
   __shared__ uint32_t s_digit;
   __shared__ int s_need, s_equal, s_sums[SEL_W];
-  __shared__ unsigned long long s_warp[SEL_W], s_all;  // taken for sure | equal to the threshold
-  __shared__ int s_gap, s_bad;
+  __shared__ unsigned long long s_warp[SEL_W];
+  __shared__ SelectEnd s_end;
+  __shared__ int s_gap;
   after_previous();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cs = (int)cluster_ctas(), rank = (int)cluster_rank(), n = blockIdx.x / cs;
@@ -297,10 +338,36 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
   const int begin = cta_begin + tid * per < cta_end ? cta_begin + tid * per : cta_end;
   const int end = begin + per < cta_end ? begin + per : cta_end;
   const bool choose = count > most;
-  if (tid == 0) s_gap = INT_MAX, s_bad = 0;
+  // the keys of this thread's values in order, from registers where they fit
+  uint32_t held[HELD];
+  const bool fit = per <= HELD;
+  if (choose && fit) {
+    float x[HELD];
+#pragma unroll
+    for (int y = 0; y < HELD; ++y) x[y] = begin + y < end ? value[begin + y] : 0.f;
+#pragma unroll
+    for (int y = 0; y < HELD; ++y) held[y] = order_key(x[y]);
+  }
+  auto each = [&](auto &&f) {
+    if (fit) {
+#pragma unroll
+      for (int y = 0; y < HELD; ++y)
+        if (begin + y < end) f(begin + y, held[y]);
+    } else {
+#pragma unroll 4
+      for (int j = begin; j < end; ++j) f(j, order_key(value[j]));
+    }
+  };
+  // eviction: the last page that is not there, or is shared and would be written
+  int last_bad = -1;
+  if (EVICT && choose)
+    for (int j = rank * SEL_NT + tid; j <= (count - 1) / page_size; j += cs * SEL_NT) {
+      const int p = table[j];
+      if (!page_known(a.c, p) || (a.refs && j <= (most - 1) / page_size && a.refs[p] > 1)) last_bad = j;
+    }
+  if (tid == 0) s_end.taken = 0, s_end.gap = INT_MAX, s_end.bad = -1, s_gap = INT_MAX;
   if (choose) {
     need = most - a.first - a.recent;
-    const int from = begin > lo ? begin : lo, to = end < hi ? end : hi;
     if (need > 0) {
 #pragma unroll 1
       for (int pass = 0; pass < 3; ++pass) {
@@ -308,10 +375,9 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
         int *hist = s_u.hist[pass & 1];
         for (int b = tid; b < BINS; b += SEL_NT) hist[b] = 0;
         __syncthreads();
-        for (int j = from; j < to; ++j) {
-          const uint32_t k = order_key(value[j]);
-          if (pass == 0 || k >> up == threshold >> up) atomicAdd(&hist[k >> shift & mask], 1);
-        }
+        each([&](int j, uint32_t k) {
+          if (j >= lo && j < hi && (pass == 0 || k >> up == threshold >> up)) atomicAdd(&hist[k >> shift & mask], 1);
+        });
         if (cs > 1) cluster_sync();
         else __syncthreads();
         // this thread's four bins, from the top
@@ -350,24 +416,20 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
       }
     } else {
       threshold = 0xffffffffu;  // no key reaches it
+      __syncthreads();
     }
-  } else {
-    __syncthreads();
   }
-  // how many are taken before this thread's
-  auto sort_of = [&](int j) {  // 2: taken, 1: equal to the threshold, 0: not
-    if (!choose || j < lo || j >= hi) return 2;
-    const uint32_t k = order_key(value[j]);
-    return k > threshold ? 2 : k == threshold && need > 0 ? 1 : 0;
-  };
+  // 2: taken, 1: equal to the threshold (the first `need` of these are taken), 0: not
+  auto sort_of = [&](int j, uint32_t k) { return !choose || j < lo || j >= hi || k > threshold ? 2 : k == threshold && need > 0 ? 1 : 0; };
+  // how many are taken, and equal, before this thread's values
   unsigned long long mine = 0;
   if (choose) {
-    int gap = INT_MAX;
-    for (int j = begin; j < end; ++j) {
-      const int s = sort_of(j);
+    int gap = INT_MAX;  // the first that is not taken for sure
+    each([&](int j, uint32_t k) {
+      const int s = sort_of(j, k);
       mine += s == 2 ? 1ull << 32 : s;
-      if (s < 2 && gap == INT_MAX) gap = j;
-    }
+      if (s == 0 && gap == INT_MAX) gap = j;
+    });
     unsigned long long x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -375,57 +437,52 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
       if (lane >= o) x += y;
     }
     if (lane == 31) s_warp[warp] = x;
+    if (EVICT) {
+      gap = __reduce_min_sync(0xffffffffu, gap), last_bad = __reduce_max_sync(0xffffffffu, last_bad);
+      if (lane == 0 && gap != INT_MAX) atomicMin(&s_end.gap, gap);
+      if (lane == 0 && last_bad >= 0) atomicMax(&s_end.bad, last_bad);
+    }
     __syncthreads();
     unsigned long long all = 0;
+#pragma unroll
     for (int w = 0; w < SEL_W; ++w) {
       if (w < warp) x += s_warp[w];
       all += s_warp[w];
     }
-    if (tid == 0) s_all = all;
+    if (tid == 0) s_end.taken = all;
     mine = x - mine;
-    if (cs > 1) {
-      cluster_sync();
-      for (int r = 0; r < rank; ++r) mine += *(unsigned long long *)tc::map_rank(&s_all, r);
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+    gap = INT_MAX, last_bad = -1;
+    for (int r = 0; r < cs; ++r) {
+      const SelectEnd *e = cs > 1 ? (const SelectEnd *)tc::map_rank(&s_end, r) : &s_end;
+      if (r < rank) mine += e->taken;
+      if (EVICT) gap = e->gap < gap ? e->gap : gap, last_bad = e->bad > last_bad ? e->bad : last_bad;
     }
-    if (EVICT) {
-      // the first position that is not taken: of the equal ones, those behind the last needed
-      int equal = (int)(uint32_t)mine;
-      gap = INT_MAX;
-      for (int j = begin; j < end && gap == INT_MAX; ++j) {
-        const int s = sort_of(j);
-        if (s == 0 || (s == 1 && equal++ >= need)) gap = j;
-      }
-      if (gap != INT_MAX) atomicMin(&s_gap, gap);
+    if (EVICT && need > 0) {  // of the equal ones the first behind those that are taken
+      int equal = (int)(uint32_t)mine, here = INT_MAX;
+      each([&](int j, uint32_t k) {
+        if (sort_of(j, k) == 1 && equal++ >= need && here == INT_MAX) here = j;
+      });
+      if (here != INT_MAX) atomicMin(&s_gap, here);
       if (cs > 1) cluster_sync();
       else __syncthreads();
-      gap = INT_MAX;
       for (int r = 0; r < cs; ++r) {
         const int g = *(cs > 1 ? (int *)tc::map_rank(&s_gap, r) : &s_gap);
         gap = g < gap ? g : gap;
       }
-      // every row from there on moves: its page has to be there, and nobody else's where it goes
-      int bad = 0;
-      for (int j = gap / page_size + rank * SEL_NT + tid; j <= (count - 1) / page_size; j += cs * SEL_NT) {
-        const int p = table[j];
-        if (!page_known(a.c, p)) bad = 1;
-        else if (a.refs && j <= (most - 1) / page_size && a.refs[p] > 1) bad = 1;
+    }
+    // rows behind the first gap move: their pages have to be there, and nobody else's where they go
+    if (EVICT && last_bad >= gap / page_size) {  // the sequence stays as it is
+      for (int64_t j = rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT) out[j] = -1;
+      if (a.new_values && a.new_values != a.values)
+        for (int j = rank * SEL_NT + tid; j < count; j += cs * SEL_NT) a.new_values[(size_t)n * a.stride + j] = value[j];
+      if (rank == 0 && tid == 0) {
+        flag(a.c.err, ERR_BAD_INDEX);
+        a.out_lengths[n] = len;
       }
-      if (bad) s_bad = 1;
       if (cs > 1) cluster_sync();
-      else __syncthreads();
-      bad = 0;
-      for (int r = 0; r < cs; ++r) bad |= *(cs > 1 ? (int *)tc::map_rank(&s_bad, r) : &s_bad);
-      if (bad) {  // the sequence stays as it is
-        for (int64_t j = rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT) out[j] = -1;
-        if (a.new_values && a.new_values != a.values)
-          for (int j = rank * SEL_NT + tid; j < count; j += cs * SEL_NT) a.new_values[(size_t)n * a.stride + j] = value[j];
-        if (rank == 0 && tid == 0) {
-          flag(a.c.err, ERR_BAD_INDEX);
-          a.out_lengths[n] = len;
-        }
-        if (cs > 1) cluster_sync();
-        return;
-      }
+      return;
     }
   } else {
     mine = (unsigned long long)begin << 32;
@@ -433,8 +490,8 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
   int taken = (int)(mine >> 32), equal = (int)(uint32_t)mine;
   const bool aside = EVICT && a.new_values && a.new_values != a.values;
   float *fresh = EVICT && a.new_values ? a.new_values + (size_t)n * a.stride : nullptr;
-  for (int j = begin; j < end; ++j) {
-    const int s = sort_of(j);
+  auto put = [&](int j, uint32_t k) {
+    const int s = sort_of(j, k);
     if (s == 2 || (s == 1 && equal < need)) {
       const int at = taken + (equal < need ? equal : need);
       out[at] = EVICT ? j : table[j];
@@ -442,7 +499,10 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
     }
     if (s == 2) ++taken;
     else equal += s;
-  }
+  };
+  if (choose) each(put);
+  else
+    for (int j = begin; j < end; ++j) put(j, 0);
   for (int64_t j = take + rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT)
     out[j] = !EVICT && j < take + tail ? table[count + (j - take)] : -1;
   if (EVICT) {
@@ -600,6 +660,17 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int cluster, int threads, in
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// Lets a kernel use that much shared memory on this device; done[device] once it may (idempotent if raced).
+template <typename K>
+cudaError_t opt_in(K kernel, int smem, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev].load())) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && dev < 64) done[dev].store(true);
+  return e;
+}
+
 // CTAs of a selection: two values a thread, or 16384 rows' scores a CTA, as long as the GPU has room for
 // the clusters (two CTAs an SM).
 int select_ctas(int n_seqs, int64_t most_values, double scores) {
@@ -611,8 +682,11 @@ int select_ctas(int n_seqs, int64_t most_values, double scores) {
 }  // namespace
 
 cudaError_t launch_block_keys(const PagedCache &c, const int32_t *from, int n_seqs, void *keys, cudaStream_t s) {
-  const int ctas = 1064 / c.n_layers;  // seven an SM
-  return launch(block_keys_kernel, dim3(ctas < 1 ? 1 : ctas, c.n_layers), 1, BK_NT, 0, s, c, from, n_seqs, static_cast<uint4 *>(keys));
+  static std::atomic<bool> opted[64];
+  const cudaError_t e = opt_in(block_keys_kernel, BK_SMEM, opted);
+  if (e != cudaSuccess) return e;
+  const int ctas = 456 / c.n_layers;  // three an SM
+  return launch(block_keys_kernel, dim3(ctas < 1 ? 1 : ctas, c.n_layers), 1, BK_NT, BK_SMEM, s, c, from, n_seqs, static_cast<bf16 *>(keys));
 }
 
 cudaError_t launch_block_select(const SelectArgs &a, cudaStream_t s) {
@@ -626,15 +700,9 @@ cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t 
   cudaError_t e = launch(select_kernel<true>, dim3(a.n_seqs * cs), cs, SEL_NT, 0, s, a);
   if (e != cudaSuccess) return e;
   ++*launches;
-  int dev = 0;
-  e = cudaGetDevice(&dev);
+  static std::atomic<bool> opted[64];
+  e = opt_in(evict_rows_kernel, MV_SMEM, opted);
   if (e != cudaSuccess) return e;
-  static std::atomic<bool> opted[64];  // devices where the kernel may use its shared memory (idempotent if raced)
-  if (dev >= 64 || !opted[dev].load()) {
-    e = cudaFuncSetAttribute(evict_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MV_SMEM);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) opted[dev].store(true);
-  }
   e = launch(evict_rows_kernel, dim3(ROW16 / MV_PIECES, a.c.n_layers, a.n_seqs), 1, MV_NT, MV_SMEM, s, a.c, a.out, a.most);
   ++*launches;
   return e;
