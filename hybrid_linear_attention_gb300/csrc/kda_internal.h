@@ -119,6 +119,8 @@ struct KeySumArgs {
   const float *lse;            // positions: [total, H]
   float *out;                  // positions: [n_seqs, out_stride], added to; blocks: the scores in
   int64_t out_stride;          //   units of log 2, [total, H, out_stride]
+  float2 *part;                // blocks: [total, H, part_stride] (maximum, sum) of each row over 32 blocks
+  int64_t part_stride;
   int *err;
 };
 
@@ -139,6 +141,8 @@ struct SelectArgs {
   // blocks: where given, the values are computed first, from every row's scores
   const float *rows;           // [total, H, rows_stride] in units of log 2
   int64_t rows_stride;         // a multiple of 4
+  const float2 *parts;         // [total, H, parts_stride] (maximum, sum) over 32 blocks
+  int64_t parts_stride;
   int H;
   float *scores;               // the values, [n_seqs, stride]; out may be nullptr: no selection then
 };
@@ -217,7 +221,7 @@ size_t pages_ws_bytes(int n);
 cudaError_t launch_cache_weights(const KeySumArgs &a, cudaStream_t s);
 cudaError_t launch_block_products(const KeySumArgs &a, cudaStream_t s);
 cudaError_t launch_block_keys(const PagedCache &c, const int32_t *from, int n_seqs, void *keys, cudaStream_t s);
-cudaError_t launch_block_select(const SelectArgs &a, cudaStream_t s);
+cudaError_t launch_block_select(const SelectArgs &a, int *launches, cudaStream_t s);
 cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t s);
 cudaError_t launch_pages_trim(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots,
                               const int32_t *slots, int n, cudaStream_t s);

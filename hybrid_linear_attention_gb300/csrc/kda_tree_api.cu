@@ -434,12 +434,13 @@ kda_status mla_block_keys(const void *pool, int n_layers, int n_pages, int page_
                                      from_lengths, n_seqs, keys, stream), 1);
 }
 
-// every row's scores of the blocks, rows a multiple of 16 bytes long
+// every row's scores of the blocks, rows a multiple of 16 bytes long, and its (maximum, sum) over every 32
 static int64_t score_stride(int max_pages) { return ((int64_t)max_pages + 3) & ~(int64_t)3; }
+static int64_t part_stride(int max_pages) { return ((int64_t)max_pages + 31) / 32; }
 
 size_t mla_block_scores_workspace_size(int64_t total_nodes, int H, int max_pages) {
   if (total_nodes < 1 || total_nodes > kMaxTreeRows || H < 1 || H > 128 || max_pages < 1 || max_pages > 1 << 20) return 0;
-  return (size_t)total_nodes * H * score_stride(max_pages) * sizeof(float);
+  return (size_t)total_nodes * H * (score_stride(max_pages) * sizeof(float) + part_stride(max_pages) * sizeof(float2));
 }
 
 // mla_block_scores but for the launches: the products (*a) and what makes scores of them (*s, which may
@@ -454,9 +455,10 @@ static kda_status block_scores(const void *q_cat, int H, const void *keys, int n
   if (!given(scores) || scores_stride < max_pages || !optional(workspace)) return KDA_ERR_INVALID_ARG;
   if (!workspace || ws_bytes < mla_block_scores_workspace_size(total_nodes, H, max_pages)) return KDA_ERR_WORKSPACE;
   a->out = static_cast<float *>(workspace), a->out_stride = score_stride(max_pages);
+  a->part = reinterpret_cast<float2 *>(a->out + total_nodes * H * a->out_stride), a->part_stride = part_stride(max_pages);
   s->c = a->c, s->n_seqs = n_seqs, s->cu_nodes = cu_nodes, s->total = total_nodes;
   s->values = s->scores = scores, s->stride = scores_stride;
-  s->rows = a->out, s->rows_stride = a->out_stride, s->H = H;
+  s->rows = a->out, s->rows_stride = a->out_stride, s->parts = a->part, s->parts_stride = a->part_stride, s->H = H;
   return KDA_OK;
 }
 
@@ -472,9 +474,10 @@ kda_status mla_block_scores(const void *q_cat, int H, const void *keys, int n_pa
                                total_nodes, scale, scores, scores_stride, workspace, ws_bytes, &a, &s);
   if (st != KDA_OK || total_nodes == 0) return st;
   if (!kda::mla_latent_supported()) return KDA_ERR_UNSUPPORTED;
+  int launches = 0;
   cudaError_t e = kda::launch_block_products(a, stream);
-  if (e == cudaSuccess) e = kda::launch_block_select(s, stream);
-  return done(e, 2);
+  if (e == cudaSuccess) e = kda::launch_block_select(s, &launches, stream);
+  return done(e, launches + 1);
 }
 
 // mla_block_select but for the launch; fills *a.
@@ -508,7 +511,9 @@ kda_status mla_block_select(const float *scores, int64_t scores_stride, int page
   kda_status st = block_select(scores, scores_stride, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs,
                                total_nodes, blocks, first, recent, sel_table, sel_pages, sel_lengths, &a);
   if (st != KDA_OK || n_seqs == 0) return st;
-  return done(kda::launch_block_select(a, stream), 1);
+  int launches = 0;
+  const cudaError_t e = kda::launch_block_select(a, &launches, stream);
+  return done(e, launches);
 }
 
 size_t mla_sparse_workspace_size(int n_seqs, int64_t total_nodes, int H, int max_pages) {
@@ -541,9 +546,10 @@ static kda_status sparse_step(const void *q_cat, int H, const void *pool, const 
 }
 static cudaError_t launch_sparse(const SparseStep &s, int *launches, cudaStream_t stream) {
   cudaError_t e = kda::launch_block_products(s.scores, stream);
-  if (e == cudaSuccess) e = kda::launch_block_select(s.choice, stream);
+  int more = 0;
+  if (e == cudaSuccess) e = kda::launch_block_select(s.choice, &more, stream);
   if (e == cudaSuccess) e = kda::launch_mla_tree(s.attention, launches, stream);
-  *launches += 2;
+  *launches += more + 1;
   return e;
 }
 

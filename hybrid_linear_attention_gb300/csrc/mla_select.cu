@@ -180,96 +180,137 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
 
 constexpr int SEL_NT = 512, SEL_W = SEL_NT / 32, BINS = 2048;
 constexpr int SC_ROWS = 1024, SC_GROUP = 128;  // rows, blocks at a time
+constexpr int MAX_CS = 8;                      // CTAs of a cluster
+static_assert(SEL_W == 16, "the groups' warps are counted in powers of two");
 
-// The scores of blocks begin .. end - 1, this CTA's, of a sequence's `rows` rows: each row's softmax over
-// all of the cluster's blocks, summed over the rows.
+// The scores of blocks begin .. end - 1 of a sequence with `rows` rows from row0 on: each row's softmax over
+// all of its blocks, summed over the rows, to `out` and, where given, to `here`.
 struct ScoreSpace {
-  float2 ml[SC_ROWS];  // a row's (maximum, sum) over this CTA's blocks
-  float lse[SC_ROWS];  // and over all, in units of log 2
+  float lse[SC_ROWS];  // of rows, in units of log 2
   float part[SEL_W][SC_GROUP];
 };
-__device__ __forceinline__ void block_scores(const float *base, int64_t stride, int rows, int begin, int end, int cs, float *out,
+__device__ __forceinline__ void block_scores(const SelectArgs &a, int row0, int rows, int count, int begin, int end, float *out, float *here,
                                              ScoreSpace &s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int groups = (end - begin + SC_GROUP - 1) / SC_GROUP, pieces = (count + 31) / 32;
+  const int log_gp = groups <= 1 ? 0 : groups <= 2 ? 1 : groups <= 4 ? 2 : groups <= 8 ? 3 : 4;  // groups side by side
+  const int share = SEL_W >> log_gp, sub = warp & (share - 1);                                    // warps of a group
   for (int r0 = 0; r0 < rows; r0 += SC_ROWS) {
-    const int count = rows - r0 < SC_ROWS ? rows - r0 : SC_ROWS;
-    // a warp two rows at a time, a lane eight of 256 blocks in flight of each
-    for (int r = warp; r < count; r += 2 * SEL_W) {
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-      for (int g = begin; g < end; g += 2 * SC_GROUP) {
-        float4 v[2][2];
+    const int n = rows - r0 < SC_ROWS ? rows - r0 : SC_ROWS;
+    const float *at = a.rows + (int64_t)(row0 + r0) * a.rows_stride;
+    // four rows' scores of this thread's blocks (up to three more are read inside a row's stride, and not used)
+    auto load = [&](int r, int b, float4 (&x)[4]) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+      for (int y = 0; y < 4; ++y)
+        x[y] = r + y * share < n && b < end ? load4(at + (int64_t)(r + y * share) * a.rows_stride + b)
+                                            : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    };
+    float4 ahead[4];  // the first of them are on their way while the log-sums are merged
+    load(sub, begin + (warp >> (4 - log_gp)) * SC_GROUP + 4 * lane, ahead);
+    // a row's log-sum by a warp, four rows on their way
+    const float2 *part = a.parts + (int64_t)(row0 + r0) * a.parts_stride;
+    for (int r = warp; r < n; r += 4 * SEL_W) {
+      float M[4], L[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // (up to three more values are read inside the row's stride, and not used)
-            const int b = g + SC_GROUP * h + 4 * lane;
-            v[k][h] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (b < end && r + SEL_W * k < count) v[k][h] = load4(base + (int64_t)(r0 + r + SEL_W * k) * stride + b);
-            if (b + 1 >= end) v[k][h].y = -INFINITY;
-            if (b + 2 >= end) v[k][h].z = -INFINITY;
-            if (b + 3 >= end) v[k][h].w = -INFINITY;
-          }
+      for (int k = 0; k < 4; ++k) M[k] = -INFINITY, L[k] = 0.f;
+      for (int p = lane; p < pieces; p += 32) {
+        float2 x[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float4 x = v[k][0], y = v[k][1];
-          const float top = fmaxf(m[k], fmaxf(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w))));
-          const float t = top == -INFINITY ? 0.f : top;
-          l[k] = l[k] * exp2f(m[k] - t) + (((exp2f(x.x - t) + exp2f(x.y - t)) + (exp2f(x.z - t) + exp2f(x.w - t))) +
-                                           ((exp2f(y.x - t) + exp2f(y.y - t)) + (exp2f(y.z - t) + exp2f(y.w - t))));
-          m[k] = top;
+        for (int k = 0; k < 4; ++k)
+          x[k] = r + k * SEL_W < n ? part[(int64_t)(r + k * SEL_W) * a.parts_stride + p] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float top = fmaxf(M[k], x[k].x), t = top == -INFINITY ? 0.f : top;
+          L[k] = L[k] * exp2f(M[k] - t) + exp2f(x[k].x - t) * x[k].y, M[k] = top;
         }
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float top = warp_max(m[k]);
-        const float sum = warp_sum(l[k] * exp2f(m[k] - (top == -INFINITY ? 0.f : top)));
-        if (lane == 0 && r + SEL_W * k < count) s.ml[r + SEL_W * k] = make_float2(top, sum);
+      for (int k = 0; k < 4; ++k) {
+        const float top = warp_max(M[k]);
+        const float sum = warp_sum(L[k] * exp2f(M[k] - (top == -INFINITY ? 0.f : top)));
+        if (lane == 0 && r + k * SEL_W < n) s.lse[r + k * SEL_W] = top == -INFINITY && sum == 0.f ? 0.f : top + log2f(sum);
       }
     }
-    if (cs > 1) cluster_sync();
-    else __syncthreads();
-    for (int r = tid; r < count; r += SEL_NT) {
-      float M = -INFINITY, L = 0.f;
-      for (int c = 0; c < cs; ++c) M = fmaxf(M, (cs > 1 ? (const float2 *)tc::map_rank(s.ml + r, c) : s.ml + r)->x);
-      for (int c = 0; c < cs; ++c) {
-        const float2 y = *(cs > 1 ? (const float2 *)tc::map_rank(s.ml + r, c) : s.ml + r);
-        L += y.x == -INFINITY ? y.y : exp2f(y.x - M) * y.y;  // (no block: 0, or NaN)
-      }
-      s.lse[r] = M == -INFINITY && L == 0.f ? 0.f : M + log2f(L);
-    }
-    if (cs > 1) cluster_sync();  // the others have read ml
-    else __syncthreads();
-    for (int g = begin; g < end; g += SC_GROUP) {
-      const int b = g + 4 * lane;
+    __syncthreads();
+    for (int g0 = 0; g0 < groups; g0 += 1 << log_gp) {
+      const int b = begin + (g0 + (warp >> (4 - log_gp))) * SC_GROUP + 4 * lane;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (b < end)  // (up to three more values are read inside the row's stride, and not used)
-#pragma unroll 4
-        for (int r = warp; r < count; r += SEL_W) {
-          const float4 x = load4(base + (int64_t)(r0 + r) * stride + b);
-          const float e = s.lse[r];
-          acc.x += exp2f(x.x - e), acc.y += exp2f(x.y - e), acc.z += exp2f(x.z - e), acc.w += exp2f(x.w - e);
+      if (b < end)
+        for (int r = sub; r < n; r += 4 * share) {
+          float4 x[4];
+          if (g0 == 0 && r == sub) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) x[y] = ahead[y];
+          } else {
+            load(r, b, x);
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float e = r + y * share < n ? s.lse[r + y * share] : 0.f;
+            acc.x += exp2f(x[y].x - e), acc.y += exp2f(x[y].y - e), acc.z += exp2f(x[y].z - e), acc.w += exp2f(x[y].w - e);
+          }
         }
       store4(&s.part[warp][4 * lane], acc);
       __syncthreads();
-      if (tid < SC_GROUP && g + tid < end) {
-        float sum = r0 == 0 ? 0.f : out[g + tid];
-#pragma unroll
-        for (int w = 0; w < SEL_W; ++w) sum += s.part[w][tid];
-        out[g + tid] = sum;
+      for (int t = tid; t < SC_GROUP << log_gp; t += SEL_NT) {
+        const int g = t / SC_GROUP, o = begin + g0 * SC_GROUP + t;
+        if (o >= end) break;
+        float sum = r0 == 0 ? 0.f : out[o];
+        for (int w = 0; w < share; ++w) sum += s.part[g * share + w][t % SC_GROUP];
+        out[o] = sum;
+        if (here) here[o] = sum;
       }
       __syncthreads();
     }
   }
 }
 
+// The step of a sequence as the two kernels of blocks see it; false: nothing is done for it (told once).
+struct BlockStep {
+  int lo, W, len, full;
+};
+__device__ __forceinline__ bool step_of(const SelectArgs &a, int n, bool tell, BlockStep &s) {
+  s.lo = a.cu_nodes[n], s.len = a.c.lengths[n];
+  const int hi = a.cu_nodes[n + 1];
+  s.W = hi - s.lo, s.full = s.len / a.c.page_size;
+  if (s.lo < 0 || hi < s.lo || hi > a.total || s.W > 64) {
+    if (tell) flag(a.c.err, ERR_BAD_SEQLEN);
+    return false;
+  }
+  if (s.W == 0) return false;  // nothing to attend from, and no error
+  if (s.len < 0 || (int64_t)s.len + s.W > (int64_t)a.c.max_pages * a.c.page_size) {
+    if (tell) flag(a.c.err, ERR_BAD_INDEX);
+    return false;
+  }
+  return true;
+}
+
+// Scores of SC_WIDE blocks a CTA, where a sequence may have more than one CTA takes along with its selection.
+constexpr int SC_WIDE = 4 * SC_GROUP;
+__global__ void __launch_bounds__(SEL_NT, 2) block_scores_kernel(const SelectArgs a) {
+  __shared__ __align__(16) ScoreSpace s_space;
+  after_previous();
+  const int n = blockIdx.y, begin = blockIdx.x * SC_WIDE;
+  BlockStep s;
+  if (!step_of(a, n, blockIdx.x == 0 && threadIdx.x == 0, s) || begin >= s.full) return;
+  block_scores(a, s.lo * a.H, s.W * a.H, s.full, begin, s.full < begin + SC_WIDE ? s.full : begin + SC_WIDE,
+               a.scores + (size_t)n * a.stride, nullptr, s_space);
+}
+
+// p in CTA r of the cluster
+template <typename T>
+__device__ __forceinline__ const T *of_cta(const T *p, int r, int cs) {
+  return cs > 1 ? reinterpret_cast<const T *>(tc::map_rank(p, r)) : p;
+}
+
 // What a CTA tells the others of its cluster.
-struct SelectEnd {
+struct __align__(16) SelectEnd {
   unsigned long long taken;  // taken for sure << 32 | equal to the threshold
   int gap, bad;              // the first value that is not taken; the last page that must not move
 };
 
 template <bool EVICT>
-__global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
   constexpr int HELD = EVICT ? 16 : 4;  // values of a thread that stay in registers
   __shared__ __align__(16) union {
     ScoreSpace scores;
@@ -280,6 +321,7 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
   __shared__ unsigned long long s_warp[SEL_W];
   __shared__ SelectEnd s_end;
   __shared__ int s_gap;
+  __shared__ __align__(16) float s_scores[EVICT ? 4 : SC_WIDE];  // computed here
   after_previous();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cs = (int)cluster_ctas(), rank = (int)cluster_rank(), n = blockIdx.x / cs;
@@ -288,39 +330,29 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
   const int len = a.c.lengths[n];
   const float *value = a.values + (size_t)n * a.stride;
   const int32_t *table = a.c.table + (size_t)n * a.c.max_pages;
-  int count, tail = 0, row0 = 0, rows = 0;  // values; pages behind the full blocks; rows of scores
+  int count, tail = 0;  // values; pages behind the full blocks
   bool ok, fits = true;
   if (EVICT) {
     ok = len >= 0 && len <= room && len <= a.stride;
     count = len;
   } else {
-    const int lo = a.cu_nodes[n], hi = a.cu_nodes[n + 1];
-    int W = hi - lo;
-    if (lo < 0 || hi < lo || hi > a.total || W > 64) {
-      if (rank == 0 && tid == 0) flag(a.c.err, ERR_BAD_SEQLEN);
-      W = 0;
+    BlockStep s;
+    ok = step_of(a, n, rank == 0 && tid == 0, s);
+    count = s.full;
+    if (ok) {
+      tail = (int)(((int64_t)len + s.W + page_size - 1) / page_size) - count;
+      fits = (count < a.most ? count : a.most) + tail <= a.out_stride;
+      if (!fits && rank == 0 && tid == 0) flag(a.c.err, ERR_BAD_INDEX);
+      if (a.rows) {  // (a cluster of one CTA then)
+        block_scores(a, s.lo * a.H, s.W * a.H, count, 0, count, a.scores + (size_t)n * a.stride, s_scores, s_u.scores);
+        value = s_scores;
+      }
     }
-    count = len / page_size;
-    ok = len >= 0 && (int64_t)len + W <= room;
-    tail = ok ? (int)(((int64_t)len + W + page_size - 1) / page_size) - count : 0;
-    row0 = lo * a.H, rows = W * a.H;
-    fits = !a.out || (count < a.most ? count : a.most) + tail <= a.out_stride;
-    if (W == 0) ok = false;  // nothing to attend from: an empty selection, and no error
-    else if (!(ok && fits) && rank == 0 && tid == 0) flag(a.c.err, ERR_BAD_INDEX);
   }
-  // this CTA's values, and this thread's of them in order
+  // this CTA's values
   const int width = ok ? ((count + cs - 1) / cs + 3) & ~3 : 0;
   const int64_t c0 = (int64_t)rank * width;
   const int cta_begin = c0 < count ? (int)c0 : count, cta_end = c0 + width < count ? (int)c0 + width : count;
-  if (!EVICT && a.rows && ok) {
-    block_scores(a.rows + (int64_t)row0 * a.rows_stride, a.rows_stride, rows, cta_begin, cta_end, cs,
-                 a.scores + (size_t)n * a.stride, s_u.scores);
-    __syncthreads();
-  }
-  if (!EVICT && !a.out) {
-    if (cs > 1) cluster_sync();  // its shared memory is not read by the others any more
-    return;
-  }
   int32_t *out = a.out + (size_t)n * a.out_stride;
   if (!ok || !fits) {
     for (int64_t j = rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT) out[j] = -1;
@@ -334,19 +366,38 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
   const int lo = a.first, hi = count - a.recent;  // where values decide (count > most)
   uint32_t threshold = 0;
   int need = 0;  // of the values equal to it
-  const int per = (width + SEL_NT - 1) / SEL_NT;
+  const int per0 = (width + SEL_NT - 1) / SEL_NT, per = per0 > 1 ? (per0 + 3) & ~3 : per0;
   const int begin = cta_begin + tid * per < cta_end ? cta_begin + tid * per : cta_end;
   const int end = begin + per < cta_end ? begin + per : cta_end;
   const bool choose = count > most;
   // the keys of this thread's values in order, from registers where they fit
-  uint32_t held[HELD];
+  uint32_t held[HELD] = {};
   const bool fit = per <= HELD;
   if (choose && fit) {
     float x[HELD];
+    if (per > 1 && (reinterpret_cast<uintptr_t>(value) & 15) == 0) {  // begin is a multiple of four then
 #pragma unroll
-    for (int y = 0; y < HELD; ++y) x[y] = begin + y < end ? value[begin + y] : 0.f;
+      for (int y = 0; y < HELD; y += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (begin + y + 3 < end) v = load4(value + begin + y);
+        else if (begin + y < end) {
+          v.x = value[begin + y];
+          if (begin + y + 1 < end) v.y = value[begin + y + 1];
+          if (begin + y + 2 < end) v.z = value[begin + y + 2];
+        }
+        x[y] = v.x, x[y + 1] = v.y, x[y + 2] = v.z, x[y + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int y = 0; y < HELD; ++y) x[y] = begin + y < end ? value[begin + y] : 0.f;
+    }
 #pragma unroll
     for (int y = 0; y < HELD; ++y) held[y] = order_key(x[y]);
+  }
+  int named[EVICT ? 1 : HELD];  // blocks: their pages
+  if (!EVICT && fit) {
+#pragma unroll
+    for (int y = 0; y < HELD; ++y) named[EVICT ? 0 : y] = begin + y < end ? table[begin + y] : -1;
   }
   auto each = [&](auto &&f) {
     if (fit) {
@@ -383,10 +434,12 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
         // this thread's four bins, from the top
         const int top = BINS - 1 - 4 * tid;
         int v[4] = {}, sum = 0;
-        for (int r = 0; r < cs; ++r) {
-          const int4 x = *(cs > 1 ? (const int4 *)tc::map_rank(hist + top - 3, r) : (const int4 *)(hist + top - 3));
-          v[0] += x.w, v[1] += x.z, v[2] += x.y, v[3] += x.x;
-        }
+        int4 bins[MAX_CS];
+#pragma unroll
+        for (int r = 0; r < MAX_CS; ++r)
+          bins[r] = r < cs ? *of_cta(reinterpret_cast<const int4 *>(hist + top - 3), r, cs) : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < MAX_CS; ++r) v[0] += bins[r].w, v[1] += bins[r].z, v[2] += bins[r].y, v[3] += bins[r].x;
 #pragma unroll
         for (int y = 0; y < 4; ++y) sum += v[y];
         int x = sum;
@@ -454,11 +507,16 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
     if (cs > 1) cluster_sync();
     else __syncthreads();
     gap = INT_MAX, last_bad = -1;
-    for (int r = 0; r < cs; ++r) {
-      const SelectEnd *e = cs > 1 ? (const SelectEnd *)tc::map_rank(&s_end, r) : &s_end;
-      if (r < rank) mine += e->taken;
-      if (EVICT) gap = e->gap < gap ? e->gap : gap, last_bad = e->bad > last_bad ? e->bad : last_bad;
-    }
+    SelectEnd ends[MAX_CS];
+#pragma unroll
+    for (int r = 0; r < MAX_CS; ++r)
+      if (r < cs) ends[r] = *of_cta(&s_end, r, cs);
+#pragma unroll
+    for (int r = 0; r < MAX_CS; ++r)
+      if (r < cs) {
+        if (r < rank) mine += ends[r].taken;
+        if (EVICT) gap = min(gap, ends[r].gap), last_bad = max(last_bad, ends[r].bad);
+      }
     if (EVICT && need > 0) {  // of the equal ones the first behind those that are taken
       int equal = (int)(uint32_t)mine, here = INT_MAX;
       each([&](int j, uint32_t k) {
@@ -467,10 +525,9 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
       if (here != INT_MAX) atomicMin(&s_gap, here);
       if (cs > 1) cluster_sync();
       else __syncthreads();
-      for (int r = 0; r < cs; ++r) {
-        const int g = *(cs > 1 ? (int *)tc::map_rank(&s_gap, r) : &s_gap);
-        gap = g < gap ? g : gap;
-      }
+#pragma unroll
+      for (int r = 0; r < MAX_CS; ++r)
+        if (r < cs) gap = min(gap, *of_cta(&s_gap, r, cs));
     }
     // rows behind the first gap move: their pages have to be there, and nobody else's where they go
     if (EVICT && last_bad >= gap / page_size) {  // the sequence stays as it is
@@ -490,19 +547,24 @@ __global__ void __launch_bounds__(SEL_NT) select_kernel(const SelectArgs a) {
   int taken = (int)(mine >> 32), equal = (int)(uint32_t)mine;
   const bool aside = EVICT && a.new_values && a.new_values != a.values;
   float *fresh = EVICT && a.new_values ? a.new_values + (size_t)n * a.stride : nullptr;
-  auto put = [&](int j, uint32_t k) {
+  auto put = [&](int j, uint32_t k, int page) {
     const int s = sort_of(j, k);
     if (s == 2 || (s == 1 && equal < need)) {
       const int at = taken + (equal < need ? equal : need);
-      out[at] = EVICT ? j : table[j];
-      if (aside) fresh[at] = value[j];
+      out[at] = EVICT ? j : page;
+      // the value again from its key, but for zeros, of which there are two, and NaN
+      if (aside) fresh[at] = !choose || k == 0 || k == 0x80000000u ? value[j] : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
     }
     if (s == 2) ++taken;
     else equal += s;
   };
-  if (choose) each(put);
-  else
-    for (int j = begin; j < end; ++j) put(j, 0);
+  if (fit) {
+#pragma unroll
+    for (int y = 0; y < HELD; ++y)
+      if (begin + y < end) put(begin + y, held[y], named[EVICT ? 0 : y]);
+  } else {
+    for (int j = begin; j < end; ++j) put(j, choose ? order_key(value[j]) : 0, EVICT ? 0 : table[j]);
+  }
   for (int64_t j = take + rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT)
     out[j] = !EVICT && j < take + tail ? table[count + (j - take)] : -1;
   if (EVICT) {
@@ -671,11 +733,12 @@ cudaError_t opt_in(K kernel, int smem, std::atomic<bool> (&done)[64]) {
   return e;
 }
 
-// CTAs of a selection: two values a thread, or 16384 rows' scores a CTA, as long as the GPU has room for
-// the clusters (two CTAs an SM).
-int select_ctas(int n_seqs, int64_t most_values, double scores) {
+// CTAs of a selection: one for up to 16 values a thread (an exchange between the CTAs of a cluster costs
+// about as much as 16 values: 4 sequences x 65536 take 18 us by clusters of eight, 64 x 4096 10 by one CTA each and 16 by
+// four), as long as the GPU has room for the clusters (two CTAs an SM).
+int select_ctas(int n_seqs, int64_t most_values) {
   int cs = 1;
-  while (cs < 8 && (most_values > (int64_t)cs * SEL_NT * 2 || scores > 16384. * cs) && (int64_t)n_seqs * cs * 2 <= 304) cs *= 2;
+  while (cs < MAX_CS && most_values > (int64_t)cs * SEL_NT * 16 && (int64_t)n_seqs * cs * 2 <= 304) cs *= 2;
   return cs;
 }
 
@@ -689,14 +752,23 @@ cudaError_t launch_block_keys(const PagedCache &c, const int32_t *from, int n_se
   return launch(block_keys_kernel, dim3(ctas < 1 ? 1 : ctas, c.n_layers), 1, BK_NT, BK_SMEM, s, c, from, n_seqs, static_cast<bf16 *>(keys));
 }
 
-cudaError_t launch_block_select(const SelectArgs &a, cudaStream_t s) {
-  const int cs = select_ctas(a.n_seqs, a.c.max_pages, a.rows ? (double)a.total * a.H * a.c.max_pages / a.n_seqs : 0.);
+cudaError_t launch_block_select(const SelectArgs &args, int *launches, cudaStream_t s) {
+  SelectArgs a = args;
+  if (a.rows && (a.c.max_pages > SC_WIDE || !a.out)) {
+    const cudaError_t e = launch(block_scores_kernel, dim3((a.c.max_pages + SC_WIDE - 1) / SC_WIDE, a.n_seqs), 1, SEL_NT, 0, s, a);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    if (!a.out) return e;
+    a.rows = nullptr;  // the scores are there
+  }
+  const int cs = select_ctas(a.n_seqs, a.c.max_pages);
+  ++*launches;
   return launch(select_kernel<false>, dim3(a.n_seqs * cs), cs, SEL_NT, 0, s, a);
 }
 
 cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t s) {
   const int64_t room = (int64_t)a.c.max_pages * a.c.page_size;
-  const int cs = select_ctas(a.n_seqs, room < a.stride ? room : a.stride, 0.);
+  const int cs = select_ctas(a.n_seqs, room < a.stride ? room : a.stride);
   cudaError_t e = launch(select_kernel<true>, dim3(a.n_seqs * cs), cs, SEL_NT, 0, s, a);
   if (e != cudaSuccess) return e;
   ++*launches;

@@ -6,7 +6,7 @@
 // of the rows r (nodes x heads) and lse_r = ln sum_t exp(s_rt) over what row r sees,
 //     weights_t += sum_r u_r exp(s_rt - lse_r)        (positions; u_r: the weight of r's node);
 // of blocks, whose keys are the pages' mean rows, the scores s_rb themselves are left for the selection
-// (mla_select.cu), which needs a row's sum over all of them first.
+// (mla_select.cu), with each row's maximum and sum over every 32 of them.
 //
 // The keys are the product's M side, D[256 keys x rows] = K Q^T on a pair of CTAs (cta_group::2, 128
 // keys each), so a thread owns a key: the sum over rows runs along its own columns of tensor memory,
@@ -139,6 +139,26 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Sums over the warp's lanes of 16 columns: lane l gets column l & 15's.
+__device__ __forceinline__ float columns_sum(float (&v)[16], int lane) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) v[c] += __shfl_xor_sync(0xffffffffu, v[c], 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int c = 0; c < o; ++c) {
+      const bool up = lane & o;
+      const float keep = up ? v[c + o] : v[c], give = up ? v[c] : v[c + o];
+      v[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  return v[0];
+}
+__device__ __forceinline__ float lanes_max(float x) {  // (a NaN may be passed over: it shows in the sum)
+  const int i = __float_as_int(x);
+  const int m = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
+  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+}
+
 template <bool BLOCKS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 1)
     key_sums_kernel(const KeySumArgs a, const __grid_constant__ SumMaps maps) {
@@ -581,10 +601,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
             tmem_wait_ld();
             rest(c, v);
             const int r = CHUNK * ch + c;
-            float *to = a.out + ((int64_t)s.lo * a.H + r) * a.out_stride + p;
+            const int64_t row = (int64_t)s.lo * a.H + r;
+            float *to = a.out + row * a.out_stride + p;
+            float top = 0.f;
 #pragma unroll
-            for (int y = 0; y < 16; ++y)
-              if (r + y < s.rows && p < s.keys) to[y * a.out_stride] = vis ? v[y] * a.scale_log2 : -INFINITY;
+            for (int y = 0; y < 16; ++y) {
+              const float x = vis ? v[y] * a.scale_log2 : -INFINITY;
+              if (r + y < s.rows && p < s.keys) to[y * a.out_stride] = x;
+              const float m = lanes_max(x);
+              if ((lane & 15) == y) top = m;
+              v[y] = ex2(x - (m == -INFINITY ? 0.f : m));
+            }
+            const float sum = columns_sum(v, lane);
+            if (lane < 16 && r + lane < s.rows) a.part[(row + lane) * a.part_stride + (p >> 5)] = make_float2(top, sum);
           }
         }
         tc_fence_before();
