@@ -20,7 +20,8 @@ const char *const kTraceNames[TR_COUNT] = {
     "kda_check_device_error", "kda_wait_probe", "kda_tree_verify", "kda_tree_accept",
     "mla_tree_mask", "mla_tree_latent", "mla_tree_decode", "mla_cache_append", "mla_cache_accept",
     "mla_pages_copy", "mla_pages_free", "mla_pages_fork", "mla_pages_reserve",
-    "mla_tree_latent_lse", "mla_tree_decode_lse", "mla_cache_weights", "mla_cache_evict",
+    "mla_tree_latent_lse", "mla_tree_decode_lse", "mla_cache_weights", "mla_weights_accept",
+    "mla_cache_evict",
     "mla_pages_trim", "mla_block_keys", "mla_block_scores", "mla_block_select",
     "mla_sparse_latent", "mla_sparse_decode"};
 }  // namespace kda

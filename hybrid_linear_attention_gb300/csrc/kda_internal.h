@@ -223,6 +223,9 @@ cudaError_t launch_block_products(const KeySumArgs &a, cudaStream_t s);
 cudaError_t launch_block_keys(const PagedCache &c, const int32_t *from, int n_seqs, void *keys, cudaStream_t s);
 cudaError_t launch_block_select(const SelectArgs &a, int *launches, cudaStream_t s);
 cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t s);
+cudaError_t launch_weights_accept(float *weights, int64_t stride, const int32_t *lengths, const int32_t *cu,
+                                  int n_seqs, int64_t total, const int32_t *parent, const int32_t *accept,
+                                  int *err, cudaStream_t s);
 cudaError_t launch_pages_trim(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots,
                               const int32_t *slots, int n, cudaStream_t s);
 cudaError_t launch_pages_fork(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots,

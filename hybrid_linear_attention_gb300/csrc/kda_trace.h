@@ -15,7 +15,7 @@ enum TraceId {
   TR_WAIT_PROBE, TR_TREE_VERIFY, TR_TREE_ACCEPT, TR_MLA_TREE_MASK, TR_MLA_TREE_LATENT,
   TR_MLA_TREE_DECODE, TR_MLA_CACHE_APPEND, TR_MLA_CACHE_ACCEPT, TR_MLA_PAGES_COPY, TR_MLA_PAGES_FREE,
   TR_MLA_PAGES_FORK, TR_MLA_PAGES_RESERVE, TR_MLA_TREE_LATENT_LSE, TR_MLA_TREE_DECODE_LSE, TR_MLA_CACHE_WEIGHTS,
-  TR_MLA_CACHE_EVICT, TR_MLA_PAGES_TRIM, TR_MLA_BLOCK_KEYS, TR_MLA_BLOCK_SCORES, TR_MLA_BLOCK_SELECT,
+  TR_MLA_WEIGHTS_ACCEPT, TR_MLA_CACHE_EVICT, TR_MLA_PAGES_TRIM, TR_MLA_BLOCK_KEYS, TR_MLA_BLOCK_SCORES, TR_MLA_BLOCK_SELECT,
   TR_MLA_SPARSE_LATENT, TR_MLA_SPARSE_DECODE, TR_COUNT
 };
 extern const char *const kTraceNames[TR_COUNT];

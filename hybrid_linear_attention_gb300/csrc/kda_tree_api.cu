@@ -393,6 +393,18 @@ kda_status mla_cache_weights(const void *q_cat, int H, const void *pool, int n_p
   return done(kda::launch_cache_weights(a, stream), 1);
 }
 
+kda_status mla_weights_accept(float *weights, int64_t weights_stride, const int32_t *lengths, const int32_t *cu_nodes,
+                              int n_seqs, int64_t total_nodes, const int32_t *parent, const int32_t *accept_node,
+                              cudaStream_t stream) {
+  KDA_TRACE(TR_MLA_WEIGHTS_ACCEPT);
+  if (n_seqs < 0 || n_seqs > 65535 || total_nodes < 0 || total_nodes > kMaxTreeRows) return KDA_ERR_INVALID_ARG;
+  if (n_seqs == 0 || total_nodes == 0) return KDA_OK;
+  if (!given(weights) || weights_stride < 1 || !given(lengths) || !given(cu_nodes) || !given(parent) || !given(accept_node))
+    return KDA_ERR_INVALID_ARG;
+  return done(kda::launch_weights_accept(weights, weights_stride, lengths, cu_nodes, n_seqs, total_nodes, parent, accept_node,
+                                         kda::device_error(), stream), 1);
+}
+
 // What the selections share.
 static kda_status check_choice(int most, int first, int recent) {
   return most < 1 || first < 0 || recent < 0 || first > most || recent > most - first ? KDA_ERR_INVALID_ARG : KDA_OK;

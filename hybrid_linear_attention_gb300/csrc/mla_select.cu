@@ -678,6 +678,42 @@ __global__ void __launch_bounds__(MV_NT, 3) evict_rows_kernel(const PagedCache c
   }
 }
 
+// The weights of an accepted path's nodes to the places of its steps, those of the other nodes to 0.
+__global__ void __launch_bounds__(64) weights_accept_kernel(float *weights, int64_t stride, const int32_t *lengths, const int32_t *cu,
+                                                            int64_t total, const int32_t *parent, const int32_t *accept, int *err) {
+  __shared__ int s_par[64], s_path[64], s_m;
+  after_previous();
+  const int n = blockIdx.x, tid = threadIdx.x, lo = cu[n], hi = cu[n + 1], W = hi - lo, last = accept[n], len = lengths[n];
+  if (lo < 0 || hi < lo || hi > total || W > 64) {
+    if (tid == 0) flag(err, ERR_BAD_SEQLEN);
+    return;
+  }
+  if (last < -1 || last >= W || len < 0 || (int64_t)len + W > stride) {
+    if (tid == 0) flag(err, ERR_BAD_INDEX);
+    return;
+  }
+  if (tid <= last) {
+    int p = parent[lo + tid];
+    if (p < -1 || p >= tid) {
+      flag(err, ERR_BAD_INDEX);
+      p = -1;
+    }
+    s_par[tid] = p;
+  }
+  float *w = weights + (size_t)n * stride + len;
+  __syncthreads();
+  if (tid == 0) {
+    int steps = 0;
+    for (int j = last; j >= 0; j = s_par[j]) ++steps;
+    s_m = steps;
+    for (int j = last; j >= 0; j = s_par[j]) s_path[--steps] = j;
+  }
+  __syncthreads();
+  const float x = tid < s_m ? w[s_path[tid]] : 0.f;
+  __syncthreads();
+  if (tid < W) w[tid] = x;
+}
+
 // The pages of the listed sequences that lie wholly behind their lengths released.
 __global__ void __launch_bounds__(128) pages_trim_kernel(PagedCache c, int32_t *table, int32_t *refs, int32_t *held, int n_slots,
                                                          const int32_t *slots) {
@@ -778,6 +814,11 @@ cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t 
   e = launch(evict_rows_kernel, dim3(ROW16 / MV_PIECES, a.c.n_layers, a.n_seqs), 1, MV_NT, MV_SMEM, s, a.c, a.out, a.most);
   ++*launches;
   return e;
+}
+
+cudaError_t launch_weights_accept(float *weights, int64_t stride, const int32_t *lengths, const int32_t *cu, int n_seqs,
+                                  int64_t total, const int32_t *parent, const int32_t *accept, int *err, cudaStream_t s) {
+  return launch(weights_accept_kernel, dim3(n_seqs), 1, 64, 0, s, weights, stride, lengths, cu, total, parent, accept, err);
 }
 
 cudaError_t launch_pages_trim(const PagedCache &c, int32_t *refs, int32_t *held, int n_slots, const int32_t *slots, int n,

@@ -38,7 +38,8 @@ EXPORTS = (
     "mla_tree_latent", "mla_tree_decode", "mla_cache_append", "mla_cache_accept",
     "mla_pages_copy", "mla_pages_workspace_size", "mla_pages_free", "mla_pages_fork",
     "mla_pages_reserve",
-    "mla_tree_latent_lse", "mla_tree_decode_lse", "mla_cache_weights", "mla_cache_evict",
+    "mla_tree_latent_lse", "mla_tree_decode_lse", "mla_cache_weights", "mla_weights_accept",
+    "mla_cache_evict",
     "mla_pages_trim", "mla_block_keys", "mla_block_scores_workspace_size", "mla_block_scores",
     "mla_block_select", "mla_sparse_workspace_size", "mla_sparse_latent", "mla_sparse_decode",
 )
@@ -165,6 +166,7 @@ def load():
                                     [_vp] * 5 + [_sz, _vp]),
             "mla_cache_weights": (_i32, [_vp, _i32] + paged + [_vp, _i32, _i64, _vp, _vp, _vp,
                                                                f32, _vp, _i64, _vp]),
+            "mla_weights_accept": (_i32, [_vp, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _vp]),
             "mla_cache_evict": (_i32, layers + [_vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _vp,
                                                 _vp, _vp]),
             "mla_pages_trim": (_i32, [_i32, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp]),
@@ -885,6 +887,22 @@ def mla_cache_weights(q_cat, pool, page_table, lengths, cu_nodes, lse, weights, 
         _here(node_weight, f32, "node_weight", dev), _here(lse, f32, "lse", dev), float(scale),
         _here(weights, f32, "weights", dev), weights.shape[1], _here_stream(stream, dev))
     _check(st, "mla_cache_weights")
+
+
+def mla_weights_accept(weights, lengths, cu_nodes, parent, accept_node, *, stream=None):
+    """The weights of accepted paths moved as mla_cache_accept moves their rows (lengths as before it);
+    those of the other drafted positions become 0."""
+    dev = _device()
+    n, i32 = cu_nodes.numel() - 1, torch.int32
+    _shape(accept_node, (n,), "accept_node")
+    if len(weights.shape) != 2 or weights.shape[0] < n or lengths.shape[0] < n:
+        raise ValueError("weights, lengths: fewer rows than sequences")
+    st = load().mla_weights_accept(
+        _here(weights, torch.float32, "weights", dev), weights.shape[1],
+        _here(lengths, i32, "lengths", dev), _here(cu_nodes, i32, "cu_nodes", dev), n,
+        parent.shape[0], _here(parent, i32, "parent", dev),
+        _here(accept_node, i32, "accept_node", dev), _here_stream(stream, dev))
+    _check(st, "mla_weights_accept")
 
 
 def mla_cache_evict(pool, page_table, lengths, weights, kept, new_lengths, new_weights=None, *,

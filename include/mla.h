@@ -317,6 +317,22 @@ kda_status mla_cache_weights(const void* q_cat, int H, const void* pool, int n_p
                              cudaStream_t stream);
 
 /*
+ * mla_weights_accept -- what mla_cache_accept does to the rows, for the weights of drafted trees: the
+ * weight of the accepted path's step d (0 = root), at position lengths[n] + its node, moves to
+ * lengths[n] + d; those of the other drafted positions become 0.  Called with the lengths before the
+ * acceptance.  (A chain of which a prefix is accepted needs no such call.)
+ *   weights, weights_stride, lengths as mla_cache_weights;  cu_nodes, parent, accept_node as
+ *   mla_cache_accept.
+ * A sequence with bad offsets or more than 64 nodes (KDA_ERR_BAD_SEQLENS), an accept_node outside
+ * -1 .. nodes - 1, or a length below 0 or with which the nodes pass weights_stride (KDA_ERR_BAD_INDEX) keeps
+ * its weights and is reported; a bad parent is reported and counts as none.
+ */
+kda_status mla_weights_accept(float* weights, int64_t weights_stride, const int32_t* lengths,
+                              const int32_t* cu_nodes, int n_seqs, int64_t total_nodes,
+                              const int32_t* parent, const int32_t* accept_node,
+                              cudaStream_t stream);
+
+/*
  * mla_cache_evict -- cuts each sequence of more than `budget` positions to `budget`: it keeps its
  * first `first` and its last `recent` positions and, of those between, the ones of the largest
  * weights (among equals the lower position first; NaN counts as less than anything).  The kept rows
@@ -324,7 +340,7 @@ kda_status mla_cache_weights(const void* q_cat, int H, const void* pool, int n_p
  *   weights     [n_seqs, weights_stride] fp32.
  *   budget      at least 1;  first, recent: at least 0, first + recent <= budget.
  *   refcount    [n_pages] int32 or NULL: where given, a sequence whose kept rows would move into a page
- *               that other sequences share is refused.
+ *               that other sequences share is refused; without it the caller answers for that.
  *   kept        [n_seqs, budget] int32 output: the kept positions in ascending order, then -1.
  *   new_lengths [n_seqs] int32 output, may be `lengths`.
  *   new_weights NULL, or [n_seqs, weights_stride] fp32: the kept positions' weights, then zeros up to

@@ -235,3 +235,53 @@ def test_decode_with_lse_gives_the_same_bits():
     kda.kda_check_device_error()
     assert torch.equal(q[0], q[1]) and torch.equal(z[0], z[1]) and torch.equal(out[0], out[1])
     assert torch.equal(lse[0], lse[1]) and torch.equal(z[1], z[2])
+
+
+def test_all_nodes_rejected_is_no_work():
+    case = Case([500, 90], [6, 3], H=64, seed=31)
+    got = run_weights(case, true_lse(case), node_weight=[0.0, -0.0] * 4 + [0.0])
+    kda.kda_check_device_error()
+    assert (got == 0.5).all()
+
+
+@pytest.mark.parametrize("H", [1, 5, 64, 100])
+def test_chunks_without_a_node_that_counts(H):
+    """Any pattern of weights over 64 nodes: chunks of 256 rows begin and end inside nodes."""
+    case = Case([300], [64], H=H, seed=32)
+    given = true_lse(case)
+    for pattern in (0x1, 1 << 63, 0x00F0000000000F00, 0xAAAAAAAAAAAAAAAA):
+        u = [float((pattern >> i) & 1) for i in range(64)]
+        check_weights(case, run_weights(case, given, node_weight=u), given, node_weight=u)
+
+
+def test_accepted_weights_follow_their_rows():
+    _gpu.lib()
+    rng = np.random.default_rng(40)
+    counts = [64, 1, 9, 0, 33, 5, 4, 7]
+    cu = [0] + [int(x) for x in np.cumsum(counts)]
+    parents = [ref.random_parents(rng, w) for w in counts]
+    accept = [63, -1, 5, -1, 20, 0, 3, 6]
+    lengths = [100, 7, 0, 50, 190, 30, -1, 219]
+    w = torch.rand(8, 224, generator=torch.Generator().manual_seed(2))
+    want = w.clone()
+    for n, (x, k) in enumerate(zip(lengths, counts)):
+        if n in (6, 7):  # a length below 0, nodes past the row's end
+            continue
+        path = ref.path_to(parents[n], accept[n])
+        want[n, x:x + k] = 0
+        want[n, x:x + len(path)] = w[n, [x + j for j in path]]
+    got = w.cuda()
+    kda.mla_weights_accept(got, ref.i32(lengths), ref.i32(cu), ref.i32([p for q in parents for p in q]), ref.i32(accept))
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_check_device_error()
+    assert e.value.status == kda.KDA_ERR_BAD_INDEX
+    assert torch.equal(got.cpu(), want)
+    got = w.cuda()
+    bad = list(accept)
+    bad[0], bad[2] = 64, -2
+    kda.mla_weights_accept(got[:3], ref.i32(lengths[:3]), ref.i32(cu[:3] + [1000]), ref.i32([-1] * cu[3]), ref.i32(bad[:3]))
+    with pytest.raises(kda.KdaError):
+        kda.kda_check_device_error()
+    want = w.clone()
+    want[1, 7] = 0
+    assert torch.equal(got.cpu(), want)

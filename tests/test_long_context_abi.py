@@ -12,7 +12,7 @@ CHOICE = ["blocks", "first", "recent", "scores", "stride", "sel", "sel_pages", "
 D = dict(q=16, H=64, pool=16, keys=16, layers=2, n_pages=4, page=64, table=16, max_pages=2, lengths=16, cu=16, n=2, total=5,
          mask=None, scale=0.1, z=16, zt=0, lse=16, ws=16, wsb=1 << 40, stream=None, u=None, w=16, stride=128, refs=None,
          budget=10, first=1, recent=2, kept=16, new_lengths=16, new_w=None, held=16, slots=16, n_slots=4, refcount=16,
-         before=16, scores=16, blocks=8, sel=16, sel_pages=12, cut=16, qn=16, qr=16, uk=16, uv=16, gate=16, out=16)
+         before=16, parent=16, accept=16, scores=16, blocks=8, sel=16, sel_pages=12, cut=16, qn=16, qr=16, uk=16, uv=16, gate=16, out=16)
 
 
 @pytest.fixture(scope="module")
@@ -60,6 +60,15 @@ def test_cache_weights(go):
     assert go(name, order, total=-1) == BAD and go(name, order, total=2**22 + 1) == BAD and go(name, order, n=0) == BAD
     assert go(name, order, scale=0.0) == BAD and go(name, order, scale=float("nan")) == BAD
     assert go(name, order, total=0, q=None) == OK
+
+
+def test_weights_accept(go):
+    order = ["w", "stride", "lengths", "cu", "n", "total", "parent", "accept", "stream"]
+    name = "mla_weights_accept"
+    pointers(go, name, order, ("w", "lengths", "cu", "parent", "accept"))
+    assert go(name, order, stride=0) == BAD and go(name, order, n=-1) == BAD and go(name, order, n=65536) == BAD
+    assert go(name, order, total=-1) == BAD and go(name, order, total=2**22 + 1) == BAD
+    assert go(name, order, total=0, w=None) == OK and go(name, order, n=0, w=None) == OK
 
 
 def test_cache_evict(go):
