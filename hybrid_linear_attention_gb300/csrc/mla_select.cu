@@ -285,15 +285,15 @@ __device__ __forceinline__ bool step_of(const SelectArgs &a, int n, bool tell, B
   return true;
 }
 
-// Scores of SC_WIDE blocks a CTA, where a sequence may have more than one CTA takes along with its selection.
+// Scores of `width` blocks a CTA, where a sequence may have more than one CTA takes along with its selection.
 constexpr int SC_WIDE = 4 * SC_GROUP;
-__global__ void __launch_bounds__(SEL_NT, 2) block_scores_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(SEL_NT, 2) block_scores_kernel(const SelectArgs a, int width) {
   __shared__ __align__(16) ScoreSpace s_space;
   after_previous();
-  const int n = blockIdx.y, begin = blockIdx.x * SC_WIDE;
+  const int n = blockIdx.y, begin = blockIdx.x * width;
   BlockStep s;
   if (!step_of(a, n, blockIdx.x == 0 && threadIdx.x == 0, s) || begin >= s.full) return;
-  block_scores(a, s.lo * a.H, s.W * a.H, s.full, begin, s.full < begin + SC_WIDE ? s.full : begin + SC_WIDE,
+  block_scores(a, s.lo * a.H, s.W * a.H, s.full, begin, s.full < begin + width ? s.full : begin + width,
                a.scores + (size_t)n * a.stride, nullptr, s_space);
 }
 
@@ -790,8 +790,13 @@ cudaError_t launch_block_keys(const PagedCache &c, const int32_t *from, int n_se
 
 cudaError_t launch_block_select(const SelectArgs &args, int *launches, cudaStream_t s) {
   SelectArgs a = args;
-  if (a.rows && (a.c.max_pages > SC_WIDE || !a.out)) {
-    const cudaError_t e = launch(block_scores_kernel, dim3((a.c.max_pages + SC_WIDE - 1) / SC_WIDE, a.n_seqs), 1, SEL_NT, 0, s, a);
+  // one CTA takes its sequence's scores along where they are few
+  const double scores = (double)a.total * a.H * a.c.max_pages / a.n_seqs;
+  if (a.rows && (a.c.max_pages > SC_WIDE || scores > 16384. || !a.out)) {
+    int width = SC_GROUP;  // as narrow as one wave of CTAs allows
+    while (width < SC_WIDE && (double)((a.c.max_pages + width - 1) / width) * a.n_seqs > 304.) width *= 2;
+    const cudaError_t e =
+        launch(block_scores_kernel, dim3((a.c.max_pages + width - 1) / width, a.n_seqs), 1, SEL_NT, 0, s, a, width);
     if (e != cudaSuccess) return e;
     ++*launches;
     if (!a.out) return e;

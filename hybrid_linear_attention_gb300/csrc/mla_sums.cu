@@ -22,6 +22,7 @@
 
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 namespace kda {
 namespace {
@@ -29,11 +30,16 @@ namespace {
 using namespace tc;
 
 constexpr int TK = 576, KB = TK / 64;
-constexpr int TILE = 256, KC = 128;    // keys of a tile, of a CTA
 constexpr int RES = 128, CHUNK = 256;  // rows: at most this many are resident; of a streamed chunk
 constexpr int NQ = 4;                  // slots of the rows' ring
-constexpr uint32_t SLOT = KC * 128;
-constexpr uint32_t OFF_K = 0, OFF_Q = KB * SLOT;
+// Keys: positions 128 a CTA (M = 256), in one buffer of nine blocks; blocks 64 (M = 128: each CTA's lanes 64 ..
+// hold the upper half of the rows' columns), in two, as their tiles are few and their latency counts
+template <bool BLOCKS>
+struct Keys {
+  static constexpr int KC = BLOCKS ? 64 : 128, TILE = 2 * KC, BUFS = BLOCKS ? 2 : 1;
+  static constexpr uint32_t SLOT = KC * 128;
+};
+constexpr uint32_t OFF_K = 0, OFF_Q = KB * 128 * 128;
 constexpr uint32_t QBYTES = KB * (RES / 2) * 128;  // the ring takes NQ x 16 KB of them
 constexpr uint32_t SMEM = OFF_Q + QBYTES + 1024;
 static_assert(NQ * (CHUNK / 2) * 128 <= QBYTES, "the ring fits the resident rows' place");
@@ -43,14 +49,14 @@ constexpr int MAX_CLUSTERS = 80;  // of two CTAs (152 SMs: 76)
 
 // barriers; L: the leading CTA's are used by both
 enum {
-  B_KFULL = 0,              // L  a key block is there in both CTAs
-  B_KEMPTY = B_KFULL + KB,  //    the products have read it
-  B_QFULL = B_KEMPTY + KB,  // L  a slot of streamed rows
+  B_KFULL = 0,                  // L  a key block is there in both CTAs (of two buffers)
+  B_KEMPTY = B_KFULL + 2 * KB,  //    the products have read it
+  B_QFULL = B_KEMPTY + 2 * KB,  // L  a slot of streamed rows
   B_QEMPTY = B_QFULL + NQ,
-  B_RFULL = B_QEMPTY + NQ,  // L  the resident rows (two)
+  B_RFULL = B_QEMPTY + NQ,      // L  the resident rows (two)
   B_REMPTY = B_RFULL + 2,
-  B_DFULL = B_REMPTY + 2,   //    a product is done (two buffers)
-  B_DFREE = B_DFULL + 2,    // L  and read
+  B_DFULL = B_REMPTY + 2,       //    a product is done (two buffers)
+  B_DFREE = B_DFULL + 2,        // L  and read
   B_DRAIN = B_DFREE + 2, B_N
 };
 
@@ -94,7 +100,7 @@ __device__ __forceinline__ Seq seq_of(const KeySumArgs &a, int n, bool tell) {
         s.live |= chunks == 1 ? 1u : (~0u << (i * a.H / CHUNK)) & (~0u >> (31 - ((i + 1) * a.H - 1) / CHUNK));
     if (s.live == 0) s.keys = 0;
   }
-  s.tiles = (s.keys + TILE - 1) / TILE;
+  s.tiles = (s.keys + Keys<BLOCKS>::TILE - 1) / Keys<BLOCKS>::TILE;
   return s;
 }
 
@@ -125,13 +131,19 @@ struct Walk {
   }
 };
 
+template <bool BLOCKS>
 __device__ __forceinline__ int columns(const Seq &s, int chunk) {  // of a chunk's product, padded
+  constexpr int pad = BLOCKS ? 63 : 31;
   const int r = s.rows - CHUNK * chunk;
-  return r >= CHUNK ? CHUNK : (r + 31) & ~31;
+  return r >= CHUNK ? CHUNK : (r + pad) & ~pad;
 }
 // The products drop bits of every partial sum (measured: a lone head's weights 1.1e-6 off), so where tensor
 // memory has room, a score is the sum of up to four of them over a part of the channels each, added in fp32.
-__device__ __forceinline__ int parts_of(int columns) { return columns <= CHUNK / 4 ? 4 : columns <= CHUNK / 2 ? 2 : 1; }
+template <bool BLOCKS>
+__device__ __forceinline__ int parts_of(int columns) {
+  const int wide = BLOCKS ? columns / 2 : columns;  // of tensor memory
+  return wide <= CHUNK / 4 ? 4 : wide <= CHUNK / 2 ? 2 : 1;
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
 }
@@ -162,7 +174,8 @@ __device__ __forceinline__ float lanes_max(float x) {  // (a NaN may be passed o
 template <bool BLOCKS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 1)
     key_sums_kernel(const KeySumArgs a, const __grid_constant__ SumMaps maps) {
-  constexpr int NT = BLOCKS ? NTB : NTP;
+  constexpr int NT = BLOCKS ? NTB : NTP, KC = Keys<BLOCKS>::KC, TILE = Keys<BLOCKS>::TILE, BUFS = Keys<BLOCKS>::BUFS;
+  constexpr uint32_t SLOT = Keys<BLOCKS>::SLOT;
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t s_bar[B_N];
   __shared__ uint32_t s_tmem;
@@ -277,49 +290,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     auto known = [&](int page) { return page >= 0 && page < a.c.n_pages; };
     int tiles = 0;
     if constexpr (BLOCKS) {
-      const int mine = 32 * (warp == W_KEYS ? 0 : warp - W_MMA), piece = lane & 7;
+      const int mine = 16 * (warp == W_KEYS ? 0 : warp - W_MMA), piece = lane & 7;
+      int page = 0, rows = 0;  // of the next tile: this lane's page, the warp's keys (may be below 0)
       auto look = [&]() {
-        const int b = TILE * walk.tile + KC * (int)rank + mine + lane;
-        int page = b < walk.s.keys ? a.c.table[(size_t)walk.n * a.c.max_pages + b] : 0;
+        const int b = TILE * walk.tile + KC * (int)rank + mine;
+        rows = walk.s.keys - b;
+        page = lane < 16 && lane < rows ? a.c.table[(size_t)walk.n * a.c.max_pages + b + lane] : 0;
+      };
+      auto landed = [&](int t, auto BEHIND) {  // tile t's blocks, BEHIND groups after them
+        auto one = [&](int kb) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) arrive_pair(map_shared_rank(bar(B_KFULL + (t & 1) * KB + kb), 0));
+        };
+        constexpr int n = decltype(BEHIND)::value;
+        copies_wait<n + 8>(), one(0), copies_wait<n + 7>(), one(1), copies_wait<n + 6>(), one(2);
+        copies_wait<n + 5>(), one(3), copies_wait<n + 4>(), one(4), copies_wait<n + 3>(), one(5);
+        copies_wait<n + 2>(), one(6), copies_wait<n + 1>(), one(7), copies_wait<n>(), one(8);
+      };
+      bool more = walk.next(a), ok = true;
+      if (more) look();
+      while (more) {
         if (!known(page)) {  // no page: any key stands for it
           if (a.err) atomicOr(a.err, ERR_BAD_INDEX);
           page = 0;
         }
-        return page;
-      };
-      bool more = walk.next(a), ok = true;
-      int page = more ? look() : 0;
-      while (more) {
-        const int rows = walk.s.keys - (TILE * walk.tile + KC * (int)rank + mine);  // (may be below 0)
-        const char *key[8];
+        const char *key[4];
 #pragma unroll
-        for (int y = 0; y < 8; ++y)
+        for (int y = 0; y < 4; ++y)
           key[y] = reinterpret_cast<const char *>(a.c.pool) + (size_t)__shfl_sync(0xffffffffu, page, 4 * y + (lane >> 3)) * (TK * 2) +
                    16 * piece;
 #pragma unroll 1
         for (int kb = 0; kb < KB; ++kb) {
-          if (tiles > 0) ok = ok && warp_wait(B_KEMPTY + kb, (uint32_t)(tiles - 1));
-          const uint32_t dst = sb + OFF_K + kb * SLOT + mine * 128;
+          if (tiles > 1) ok = ok && warp_wait(B_KEMPTY + (tiles & 1) * KB + kb, (uint32_t)((tiles >> 1) - 1));
+          const uint32_t dst = sb + OFF_K + ((tiles & 1) * KB + kb) * SLOT + mine * 128;
           if (ok)
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
+            for (int y = 0; y < 4; ++y) {
               const int r = 4 * y + (lane >> 3);
               if (r < rows) copy16(dst + r * 128 + ((piece ^ (r & 7)) << 4), key[y] + 128 * kb);
             }
           asm volatile("cp.async.commit_group;" ::: "memory");
         }
         more = walk.next(a);
-        if (more) page = look();
-        auto landed = [&](int kb) {
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0 && ok) arrive_pair(map_shared_rank(bar(B_KFULL + kb), 0));
-        };
-        copies_wait<8>(), landed(0), copies_wait<7>(), landed(1), copies_wait<6>(), landed(2);
-        copies_wait<5>(), landed(3), copies_wait<4>(), landed(4), copies_wait<3>(), landed(5);
-        copies_wait<2>(), landed(6), copies_wait<1>(), landed(7), copies_wait<0>(), landed(8);
+        if (more) look();
+        if (tiles > 0 && ok) landed(tiles - 1, std::integral_constant<int, KB>{});
         ++tiles;
       }
+      if (tiles > 0 && ok) landed(tiles - 1, std::integral_constant<int, 0>{});
     } else {
       const int box = a.c.page_size < 64 ? a.c.page_size : 64, lb = 31 - __clz(box), in_page = a.c.page_size - 1;
       uint64_t policy;  // the cache's rows are read once
@@ -344,8 +362,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         ++tiles;
       }
     }
-    if (tiles > 0)
-      for (int kb = 0; kb < KB; ++kb) wait(B_KEMPTY + kb, (uint32_t)(tiles - 1));  // read before the CTA may end
+    for (int t = tiles > BUFS ? tiles - BUFS : 0; t < tiles; ++t)  // read before the CTA may end
+      for (int kb = 0; kb < KB; ++kb) wait(B_KEMPTY + t % BUFS * KB + kb, (uint32_t)(t / BUFS));
     if (s_abort)  // a wait ran out: let the copies in flight land
       for (int y = 0; y < 100; ++y) __nanosleep(10000);
   } else if (warp == W_ROWS) {
@@ -364,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
       const int64_t row0 = (int64_t)walk.s.lo * a.H;
       if (walk.s.rows <= RES) {
         if (!walk.first) continue;
-        const int half = columns(walk.s, 0) / 2, boxes = half / 16;
+        const int half = columns<BLOCKS>(walk.s, 0) / 2, boxes = half / 16;
         const bool whole = 2 * half > RES / 2;
         seg_done(segs - 2);
         if (whole || wide) seg_done(segs - 1);
@@ -391,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         if (!ring) seg_done(segs - 1);
         ring = true;
         for (int ch = next_chunk(walk.s, -1); ch >= 0; ch = next_chunk(walk.s, ch)) {
-          const int half = columns(walk.s, ch) / 2;
+          const int half = columns<BLOCKS>(walk.s, ch) / 2;
           const int64_t r = row0 + CHUNK * ch + half * (int)rank;
 #pragma unroll 1
           for (int kb = 0; kb < KB; ++kb) {
@@ -428,21 +446,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
       while (ok && walk.next(a)) {
         const bool res = walk.s.rows <= RES;
         if (res && walk.first && !(ok = wait(B_RFULL + (segs & 1), (uint32_t)(segs >> 1)))) break;
-        const uint32_t place = sb + OFF_Q + (columns(walk.s, 0) > RES / 2 || !(segs & 1) ? 0 : QBYTES / 2);
+        const uint32_t place = sb + OFF_Q + (columns<BLOCKS>(walk.s, 0) > RES / 2 || !(segs & 1) ? 0 : QBYTES / 2);
         bool fill = true;  // the tile's keys are waited for
         for (int ch = next_chunk(walk.s, -1), then; ch >= 0 && ok; ch = then, ++i) {
           then = next_chunk(walk.s, ch);
-          const int N = columns(walk.s, ch), parts = parts_of(N);
-          const uint32_t id = idesc(1, 256, (uint32_t)N, 0, 0), d = tm + CHUNK * (i & 1);
+          const int N = columns<BLOCKS>(walk.s, ch), parts = parts_of<BLOCKS>(N);
+          const uint32_t id = idesc(1, TILE, (uint32_t)N, 0, 0), d = tm + CHUNK * (i & 1);
           if (i >= 2 && !(ok = wait(B_DFREE + (i & 1), (uint32_t)((i >> 1) - 1)))) break;
 #pragma unroll 1
           for (int kb = 0; kb < KB; ++kb) {
-            if (fill && !(ok = wait(B_KFULL + kb, (uint32_t)tiles))) break;
+            const int block = tiles % BUFS * KB + kb;
+            if (fill && !(ok = wait(B_KFULL + block, (uint32_t)(tiles / BUFS)))) break;
             if (!res && !(ok = wait(B_QFULL + j, par))) break;
             tc_fence_after();
             const int part = kb * parts / KB;
             const bool fresh = kb == 0 || (kb - 1) * parts / KB < part;
-            const uint64_t ad = sdesc_sw128(sb + OFF_K + kb * SLOT, 16, 1024);
+            const uint64_t ad = sdesc_sw128(sb + OFF_K + block * SLOT, 16, 1024);
             const uint64_t bd = sdesc_sw128(res ? place + kb * (N / 2) * 128 : sb + OFF_Q + j * (CHUNK / 2) * 128, 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
@@ -451,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
               commit2(bar(B_QEMPTY + j));
               if (++j == NQ) j = 0, par ^= 1;
             }
-            if (then < 0) commit2(bar(B_KEMPTY + kb));
+            if (then < 0) commit2(bar(B_KEMPTY + block));
           }
           fill = false;
           if (!ok) break;
@@ -489,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     };
     while (walk.next(a)) {
       const Seq s = walk.s;
-      const int p0 = TILE * walk.tile + KC * (int)rank, p = p0 + 32 * qw + lane;
+      const int p = TILE * walk.tile + KC * (int)rank + (BLOCKS ? 32 * (qw & 1) : 32 * qw) + lane;
       // the nodes that see this thread's key, as bits
       unsigned long long vis = 0;
       if (p < s.keys) {
@@ -515,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
       const int head = next_chunk(s, -1);
       for (int ch = head, then; ch >= 0; ch = then, ++i) {
         then = next_chunk(s, ch);
-        const int N = columns(s, ch), parts = parts_of(N), c0 = hf * (N / 2), c1 = c0 + N / 2;
+        const int N = columns<BLOCKS>(s, ch), parts = parts_of<BLOCKS>(N), share = BLOCKS ? N / 4 : N / 2, c0 = hf * share, c1 = c0 + share;
         if (!BLOCKS && (s.rows > RES || walk.first)) {
           if (walk.first && ch == head) ahead = row_of(s, ch);
           const float2 x = ahead;
@@ -600,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
             ask(c, v);
             tmem_wait_ld();
             rest(c, v);
-            const int r = CHUNK * ch + c;
+            const int r = CHUNK * ch + (qw >> 1) * (N / 2) + c;
             const int64_t row = (int64_t)s.lo * a.H + r;
             float *to = a.out + row * a.out_stride + p;
             float top = 0.f;
