@@ -22,7 +22,6 @@
 
 #include <atomic>
 #include <cstring>
-#include <type_traits>
 
 namespace kda {
 namespace {
@@ -50,8 +49,8 @@ constexpr int MAX_CLUSTERS = 80;  // of two CTAs (152 SMs: 76)
 // barriers; L: the leading CTA's are used by both
 enum {
   B_KFULL = 0,                  // L  a key block is there in both CTAs (of two buffers)
-  B_KEMPTY = B_KFULL + 2 * KB,  //    the products have read it
-  B_QFULL = B_KEMPTY + 2 * KB,  // L  a slot of streamed rows
+  B_KEMPTY = B_KFULL + 2 * KB,  //    the products have read it; of blocks, a buffer of them
+  B_QFULL = B_KEMPTY + KB,      // L  a slot of streamed rows
   B_QEMPTY = B_QFULL + NQ,
   B_RFULL = B_QEMPTY + NQ,      // L  the resident rows (two)
   B_REMPTY = B_RFULL + 2,
@@ -131,6 +130,11 @@ struct Walk {
   }
 };
 
+// The first unit of cluster c's run (a 64-bit division costs hundreds of cycles: only where needed).
+__device__ __forceinline__ long long run_start(long long units, int c, int clusters) {
+  return units < (1 << 24) ? (long long)((uint32_t)units * (uint32_t)c / (uint32_t)clusters) : units * c / clusters;
+}
+
 template <bool BLOCKS>
 __device__ __forceinline__ int columns(const Seq &s, int chunk) {  // of a chunk's product, padded
   constexpr int pad = BLOCKS ? 63 : 31;
@@ -180,7 +184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   __shared__ __align__(8) uint64_t s_bar[B_N];
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_abort;
-  __shared__ unsigned long long s_total, s_scan[NT / 32];
+  __shared__ long long s_scan[NT / 32];
   __shared__ int s_n, s_t;
   __shared__ long long s_at;
   __shared__ __align__(16) float2 s_col[2][BLOCKS ? 2 : CHUNK];  // rows' (lse, weight)
@@ -201,7 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     mbar_init(bar(tid), n);
     mbar_fence_init();
   }
-  if (tid == 64) s_abort = 0, s_total = 0, s_n = 0, s_t = 0, s_at = 0;
+  if (tid == 64) s_abort = 0, s_n = 0, s_t = 0, s_at = 0;
   if (tid >= 96 && tid < 99) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k + (tid - 96)) : "memory");
   if (warp == W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
@@ -213,48 +217,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   __syncthreads();
   cluster_arrive();  // barriers and tensor memory are there in this CTA; waited for below
 
-  // ---- this cluster's run of the batch's units -------------------------------------------------
-  {
-    unsigned long long mine = 0;
-    for (int n = tid; n < a.n_seqs; n += NT) {
-      const Seq s = seq_of<BLOCKS>(a, n, blockIdx.x == 0);
-      mine += (unsigned long long)s.tiles * s.chunks();
+  // ---- this cluster's run of the batch's units: sequences' units summed up, a thread each --------
+  Seq mine = {};       // of the first NT sequences
+  long long at = 0;    // units before this thread's sequence
+  auto sum_up = [&](const Seq &s, long long &before) {  // returns the units before it, adds all to `before`
+    const long long cost = (long long)s.tiles * s.chunks();
+    long long x = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    x += before - cost;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0 && mine) atomicAdd(&s_total, mine);
+    for (int w = 0; w < NT / 32; ++w) {
+      const long long v = s_scan[w];
+      if (w < warp) x += v;
+      before += v;
+    }
+    return x;
+  };
+  long long total = 0;
+  for (int n0 = 0; n0 < a.n_seqs; n0 += NT) {
+    Seq s = {};
+    if (n0 + tid < a.n_seqs) s = seq_of<BLOCKS>(a, n0 + tid, blockIdx.x == 0);
+    const long long x = sum_up(s, total);
+    if (n0 == 0) mine = s, at = x;
+    else __syncthreads();
   }
-  __syncthreads();
-  const long long total = (long long)s_total;
-  const long long begin = total * cid / clusters, stop = total * (cid + 1) / clusters;
+  const long long begin = run_start(total, cid, clusters), stop = run_start(total, cid + 1, clusters);
   if (stop > begin) {  // the first tile whose first unit is at or behind `begin`
-    long long before = 0;
-    for (int n0 = 0; n0 < a.n_seqs && before <= begin; n0 += NT) {
-      Seq s = {};
-      if (n0 + tid < a.n_seqs) s = seq_of<BLOCKS>(a, n0 + tid, false);
-      const long long cost = (long long)s.tiles * s.chunks();
-      long long x = cost;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+    auto claim = [&](const Seq &s, long long at, int n) {
+      const int chunks = s.chunks();
+      if (at <= begin && begin < at + (long long)s.tiles * chunks) {
+        const int t = (int)(begin - at + chunks - 1) / chunks;  // (a sequence has at most 2^26 units)
+        s_n = n, s_t = t, s_at = at + (long long)t * chunks;
       }
-      if (lane == 31) s_scan[warp] = x;
-      __syncthreads();
-      long long ahead = 0, all = 0;
-#pragma unroll
-      for (int w = 0; w < NT / 32; ++w) {
-        const long long v = s_scan[w];
-        if (w < warp) ahead += v;
-        all += v;
+    };
+    claim(mine, at, tid);
+    if (a.n_seqs > NT) {
+      long long before = 0;
+      for (int n0 = 0; n0 < a.n_seqs && before <= begin; n0 += NT) {
+        Seq s = {};
+        if (n0 + tid < a.n_seqs) s = seq_of<BLOCKS>(a, n0 + tid, false);
+        __syncthreads();
+        const long long x = sum_up(s, before);
+        if (n0 > 0) claim(s, x, n0 + tid);
       }
-      const long long at = before + ahead + x - cost;
-      if (at <= begin && begin < at + cost) {
-        const int t = (int)((begin - at + s.chunks() - 1) / s.chunks());
-        s_n = n0 + tid, s_t = t, s_at = at + (long long)t * s.chunks();
-      }
-      before += all;
-      __syncthreads();
     }
   }
   __syncthreads();
@@ -297,16 +308,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         rows = walk.s.keys - b;
         page = lane < 16 && lane < rows ? a.c.table[(size_t)walk.n * a.c.max_pages + b + lane] : 0;
       };
-      auto landed = [&](int t, auto BEHIND) {  // tile t's blocks, BEHIND groups after them
-        auto one = [&](int kb) {
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) arrive_pair(map_shared_rank(bar(B_KFULL + (t & 1) * KB + kb), 0));
-        };
-        constexpr int n = decltype(BEHIND)::value;
-        copies_wait<n + 8>(), one(0), copies_wait<n + 7>(), one(1), copies_wait<n + 6>(), one(2);
-        copies_wait<n + 5>(), one(3), copies_wait<n + 4>(), one(4), copies_wait<n + 3>(), one(5);
-        copies_wait<n + 2>(), one(6), copies_wait<n + 1>(), one(7), copies_wait<n>(), one(8);
+      auto landed = [&](int kb) {
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive_pair(map_shared_rank(bar(B_KFULL + (tiles & 1) * KB + kb), 0));
       };
       bool more = walk.next(a), ok = true;
       if (more) look();
@@ -322,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
                    16 * piece;
 #pragma unroll 1
         for (int kb = 0; kb < KB; ++kb) {
-          if (tiles > 1) ok = ok && warp_wait(B_KEMPTY + (tiles & 1) * KB + kb, (uint32_t)((tiles >> 1) - 1));
+          if (tiles > 1 && kb == 0) ok = ok && warp_wait(B_KEMPTY + (tiles & 1), (uint32_t)((tiles >> 1) - 1));
           const uint32_t dst = sb + OFF_K + ((tiles & 1) * KB + kb) * SLOT + mine * 128;
           if (ok)
 #pragma unroll
@@ -334,10 +339,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         }
         more = walk.next(a);
         if (more) look();
-        if (tiles > 0 && ok) landed(tiles - 1, std::integral_constant<int, KB>{});
+        if (ok) {
+          copies_wait<8>(), landed(0), copies_wait<7>(), landed(1), copies_wait<6>(), landed(2);
+          copies_wait<5>(), landed(3), copies_wait<4>(), landed(4), copies_wait<3>(), landed(5);
+          copies_wait<2>(), landed(6), copies_wait<1>(), landed(7), copies_wait<0>(), landed(8);
+        }
         ++tiles;
       }
-      if (tiles > 0 && ok) landed(tiles - 1, std::integral_constant<int, 0>{});
     } else {
       const int box = a.c.page_size < 64 ? a.c.page_size : 64, lb = 31 - __clz(box), in_page = a.c.page_size - 1;
       uint64_t policy;  // the cache's rows are read once
@@ -362,8 +370,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         ++tiles;
       }
     }
-    for (int t = tiles > BUFS ? tiles - BUFS : 0; t < tiles; ++t)  // read before the CTA may end
-      for (int kb = 0; kb < KB; ++kb) wait(B_KEMPTY + t % BUFS * KB + kb, (uint32_t)(t / BUFS));
+    // read before the CTA may end
+    if (BLOCKS)
+      for (int t = tiles > 2 ? tiles - 2 : 0; t < tiles; ++t) wait(B_KEMPTY + (t & 1), (uint32_t)(t >> 1));
+    else if (tiles > 0)
+      for (int kb = 0; kb < KB; ++kb) wait(B_KEMPTY + kb, (uint32_t)(tiles - 1));
     if (s_abort)  // a wait ran out: let the copies in flight land
       for (int y = 0; y < 100; ++y) __nanosleep(10000);
   } else if (warp == W_ROWS) {
@@ -453,12 +464,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
           const int N = columns<BLOCKS>(walk.s, ch), parts = parts_of<BLOCKS>(N);
           const uint32_t id = idesc(1, TILE, (uint32_t)N, 0, 0), d = tm + CHUNK * (i & 1);
           if (i >= 2 && !(ok = wait(B_DFREE + (i & 1), (uint32_t)((i >> 1) - 1)))) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int kb = 0; kb < KB; ++kb) {
             const int block = tiles % BUFS * KB + kb;
             if (fill && !(ok = wait(B_KFULL + block, (uint32_t)(tiles / BUFS)))) break;
             if (!res && !(ok = wait(B_QFULL + j, par))) break;
-            tc_fence_after();
             const int part = kb * parts / KB;
             const bool fresh = kb == 0 || (kb - 1) * parts / KB < part;
             const uint64_t ad = sdesc_sw128(sb + OFF_K + block * SLOT, 16, 1024);
@@ -470,10 +481,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
               commit2(bar(B_QEMPTY + j));
               if (++j == NQ) j = 0, par ^= 1;
             }
-            if (then < 0) commit2(bar(B_KEMPTY + block));
+            if (!BLOCKS && then < 0) commit2(bar(B_KEMPTY + kb));
           }
           fill = false;
           if (!ok) break;
+          if (BLOCKS && then < 0) commit2(bar(B_KEMPTY + (tiles & 1)));
           commit2(bar(B_DFULL + (i & 1)));
         }
         if (ok && res && walk.last) {
@@ -554,13 +566,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         // 16 columns' scores: asked for, and their parts added once they are there
         auto ask = [&](int c, float (&v)[16]) { tmem_ld16(d + c, v); };
         auto rest = [&](int c, float (&v)[16]) {
-          for (int x = 1; x < parts; ++x) {
-            float w[16];
-            tmem_ld16(d + x * (CHUNK / parts) + c, w);
-            tmem_wait_ld();
+          if (!BLOCKS) {
+            for (int x = 1; x < parts; ++x) {
+              float w[16];
+              tmem_ld16(d + x * (CHUNK / parts) + c, w);
+              tmem_wait_ld();
 #pragma unroll
-            for (int y = 0; y < 16; ++y) v[y] += w[y];
+              for (int y = 0; y < 16; ++y) v[y] += w[y];
+            }
+            return;
           }
+          float w[3][16];  // at once: there is one group of columns, mostly
+#pragma unroll
+          for (int x = 1; x < 4; ++x)
+            if (x < parts) tmem_ld16(d + x * (CHUNK / parts) + c, w[x - 1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 1; x < 4; ++x)
+            if (x < parts) {
+#pragma unroll
+              for (int y = 0; y < 16; ++y) v[y] += w[x - 1][y];
+            }
         };
         if (!BLOCKS) {
           if (!none) {
