@@ -48,8 +48,8 @@ constexpr int MAX_CLUSTERS = 80;  // of two CTAs (152 SMs: 76)
 
 // barriers; L: the leading CTA's are used by both
 enum {
-  B_KFULL = 0,                  // L  a key block is there in both CTAs (of two buffers)
-  B_KEMPTY = B_KFULL + 2 * KB,  //    the products have read it; of blocks, a buffer of them
+  B_KFULL = 0,                  // L  a key block is there in both CTAs; of blocks, a buffer of them
+  B_KEMPTY = B_KFULL + KB,      //    the products have read it
   B_QFULL = B_KEMPTY + KB,      // L  a slot of streamed rows
   B_QEMPTY = B_QFULL + NQ,
   B_RFULL = B_QEMPTY + NQ,      // L  the resident rows (two)
@@ -60,7 +60,7 @@ enum {
 };
 
 struct SumMaps {
-  CUtensorMap k, q16, q64;
+  CUtensorMap k, q16, q32, q64;  // query rows in boxes of 16, 32 and 64
 };
 
 struct Seq {
@@ -206,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     mbar_fence_init();
   }
   if (tid == 64) s_abort = 0, s_n = 0, s_t = 0, s_at = 0;
-  if (tid >= 96 && tid < 99) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k + (tid - 96)) : "memory");
+  if (tid >= 96 && tid < 100) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k + (tid - 96)) : "memory");
   if (warp == W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -308,11 +308,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         rows = walk.s.keys - b;
         page = lane < 16 && lane < rows ? a.c.table[(size_t)walk.n * a.c.max_pages + b + lane] : 0;
       };
-      auto landed = [&](int kb) {
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) arrive_pair(map_shared_rank(bar(B_KFULL + (tiles & 1) * KB + kb), 0));
-      };
       bool more = walk.next(a), ok = true;
       if (more) look();
       while (more) {
@@ -340,9 +335,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         more = walk.next(a);
         if (more) look();
         if (ok) {
-          copies_wait<8>(), landed(0), copies_wait<7>(), landed(1), copies_wait<6>(), landed(2);
-          copies_wait<5>(), landed(3), copies_wait<4>(), landed(4), copies_wait<3>(), landed(5);
-          copies_wait<2>(), landed(6), copies_wait<1>(), landed(7), copies_wait<0>(), landed(8);
+          copies_wait<0>();
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) arrive_pair(map_shared_rank(bar(B_KFULL + (tiles & 1)), 0));
         }
         ++tiles;
       }
@@ -393,7 +389,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
       const int64_t row0 = (int64_t)walk.s.lo * a.H;
       if (walk.s.rows <= RES) {
         if (!walk.first) continue;
-        const int half = columns<BLOCKS>(walk.s, 0) / 2, boxes = half / 16;
+        const int half = columns<BLOCKS>(walk.s, 0) / 2;
+        const int box = half % 64 == 0 ? 64 : half % 32 == 0 ? 32 : 16, boxes = half / box;  // few loads: each costs the warp
+        const CUtensorMap *map = box == 64 ? &maps.q64 : box == 32 ? &maps.q32 : &maps.q16;
         const bool whole = 2 * half > RES / 2;
         seg_done(segs - 2);
         if (whole || wide) seg_done(segs - 1);
@@ -413,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         for (int x = lane; x < KB * boxes; x += 32) {
           const int kb = x / boxes, y = x - kb * boxes;
           if (!s_abort)
-            tma_pair_3d(place + kb * half * 128 + y * 2048, &maps.q16, 64 * kb, (int)(row0 + half * (int)rank + 16 * y), 0, full);
+            tma_pair_3d(place + kb * half * 128 + y * box * 128, map, 64 * kb, (int)(row0 + half * (int)rank + box * y), 0, full);
         }
         ++segs;
       } else {
@@ -468,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
 #pragma unroll 1
           for (int kb = 0; kb < KB; ++kb) {
             const int block = tiles % BUFS * KB + kb;
-            if (fill && !(ok = wait(B_KFULL + block, (uint32_t)(tiles / BUFS)))) break;
+            if (fill && (!BLOCKS || kb == 0) && !(ok = wait(B_KFULL + (BLOCKS ? tiles & 1 : kb), (uint32_t)(tiles / BUFS)))) break;
             if (!res && !(ok = wait(B_QFULL + j, par))) break;
             const int part = kb * parts / KB;
             const bool fresh = kb == 0 || (kb - 1) * parts / KB < part;
@@ -708,7 +706,8 @@ cudaError_t launch_sums(const KeySumArgs &a, const SumMaps &maps, cudaStream_t s
 
 bool row_maps(const KeySumArgs &a, SumMaps *maps) {
   const int64_t rows = a.total * a.H;
-  return tree_map(&maps->q16, a.q, true, TK, rows, 1, 64, 16) && tree_map(&maps->q64, a.q, true, TK, rows, 1, 64, 64);
+  return tree_map(&maps->q16, a.q, true, TK, rows, 1, 64, 16) && tree_map(&maps->q32, a.q, true, TK, rows, 1, 64, 32) &&
+         tree_map(&maps->q64, a.q, true, TK, rows, 1, 64, 64);
 }
 
 }  // namespace
