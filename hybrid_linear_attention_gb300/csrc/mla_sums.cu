@@ -45,6 +45,7 @@ static_assert(NQ * (CHUNK / 2) * 128 <= QBYTES, "the ring fits the resident rows
 // warps 0-7 sum; of blocks, the last three load keys too
 constexpr int W_KEYS = 8, W_ROWS = 9, W_MMA = 10, NTP = 352, NTB = NTP + 96;
 constexpr int MAX_CLUSTERS = 80;  // of two CTAs (152 SMs: 76)
+constexpr int KNOWN = 32;         // sequences of a run that are looked at once
 
 // barriers; L: the leading CTA's are used by both
 enum {
@@ -109,12 +110,14 @@ struct Walk {
   int n, t;          // the next tile
   int64_t at, stop;  // its first unit; where the run ends
   bool fresh = true;
+  const Seq *known;      // of sequences n0 .. in shared memory (a look at global memory takes longer than a tile)
+  int n0, knowns;
   Seq s;
   int tile;
   bool first, last;  // of the sequence's tiles in this run
   __device__ __forceinline__ bool next(const KeySumArgs &a) {
     while (at < stop) {
-      if (fresh) s = seq_of<BLOCKS>(a, n, false), first = true, fresh = false;
+      if (fresh) s = n - n0 < knowns ? known[n - n0] : seq_of<BLOCKS>(a, n, false), first = true, fresh = false;
       else first = false;
       if (t >= s.tiles) {
         if (++n >= a.n_seqs) return false;
@@ -186,6 +189,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   __shared__ volatile uint32_t s_abort;
   __shared__ long long s_scan[NT / 32];
   __shared__ int s_n, s_t;
+  __shared__ Seq s_known[KNOWN];
   __shared__ long long s_at;
   __shared__ __align__(16) float2 s_col[2][BLOCKS ? 2 : CHUNK];  // rows' (lse, weight)
   __shared__ __align__(16) uint8_t s_node[2][BLOCKS ? 16 : CHUNK];
@@ -269,10 +273,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     }
   }
   __syncthreads();
+  if (tid >= s_n && tid < s_n + KNOWN) s_known[tid - s_n] = mine;
+  __syncthreads();
   cluster_wait();
   tc_fence_after();
   const uint32_t tm = s_tmem;
   Walk<BLOCKS> walk;
+  walk.known = s_known, walk.n0 = s_n, walk.knowns = s_n + KNOWN <= NT ? KNOWN : s_n < NT ? NT - s_n : 0;
   walk.n = s_n, walk.t = s_t, walk.at = s_at, walk.stop = stop > begin ? stop : s_at;
   // A wait that runs out raises s_abort; from then on waits fail at once.  The warps of the sums walk
   // on to the end without waiting (they meet on a named barrier), the others issue nothing more.
