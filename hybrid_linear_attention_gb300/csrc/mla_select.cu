@@ -422,7 +422,8 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
     if (need > 0) {
 #pragma unroll 1
       for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, up = pass == 0 ? 31 : shift + 11, mask = pass == 2 ? 1023 : BINS - 1;
+        // bits 31 .. 21, 20 .. 10 and 9 .. 0; the bits above them are known
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, up = pass == 2 ? 10 : 21, mask = pass == 2 ? 1023 : BINS - 1;
         int *hist = s_u.hist[pass & 1];
         for (int b = tid; b < BINS; b += SEL_NT) hist[b] = 0;
         __syncthreads();

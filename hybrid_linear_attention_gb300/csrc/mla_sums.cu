@@ -13,9 +13,16 @@
 // in registers, in a fixed order, and what comes out is a number per key.  A key's garbage (no page, a
 // row past the end) stays in its own lane and is never used.  A tile's keys stay in shared memory,
 // 147 KB a CTA in nine blocks of 64 channels, while the step's rows pass by: up to 128 rows are
-// resident for a whole sequence (one-token decode: the cache streams through once, block by block, as
-// the products free the blocks), more stream through a ring in chunks of 256, which cost a CTA
-// 32 bytes a cycle at the products' full rate.
+// resident for a whole sequence, more come in chunks of 128; chunks of nodes that do not count are
+// passed over.
+//
+// What bounds it.  One node a sequence: the cache's bytes, which stream through once, block by block, as
+// the products free the blocks (256 sequences of 2048 to 4096 positions, 64 heads: 137 us, 6.8 TB/s, the copy
+// rate).  Many nodes: rows x positions x 1152 flop on the tensor cores; a chunk's 36 products of 64 cycles take
+// about 3,600, as its rows' way through the shared memory that the keys leave (74 KB, no more than the chunk)
+// shows (8 sequences x 22 to 32 nodes x 8192 to 16384 positions: 158 us where all count, 1.33 PFLOP/s; chunks of
+// 256 rows, with a buffer of tensor memory each and so one sum over all channels, took 147 us and were up to
+// 1.4e-6 off).  Few positions: latency, a launch of 8 us.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "mla_pair.cuh"
@@ -29,8 +36,9 @@ namespace {
 using namespace tc;
 
 constexpr int TK = 576, KB = TK / 64;
-constexpr int RES = 128, CHUNK = 256;  // rows: at most this many are resident; of a streamed chunk
-constexpr int NQ = 4;                  // slots of the rows' ring
+constexpr int CHUNK = 128;             // rows of a product: as many are resident, more are streamed
+constexpr int NQ = 3, QK = 3;          // rows come in groups of blocks: their slots, blocks of a group
+constexpr int DCOLS = 256;             // columns of tensor memory of a product (two of them)
 // Keys: positions 128 a CTA (M = 256), in one buffer of nine blocks; blocks 64 (M = 128: each CTA's lanes 64 ..
 // hold the upper half of the rows' columns), in two, as their tiles are few and their latency counts
 template <bool BLOCKS>
@@ -39,11 +47,14 @@ struct Keys {
   static constexpr uint32_t SLOT = KC * 128;
 };
 constexpr uint32_t OFF_K = 0, OFF_Q = KB * 128 * 128;
-constexpr uint32_t QBYTES = KB * (RES / 2) * 128;  // the ring takes NQ x 16 KB of them
+constexpr uint32_t QSLOT = QK * (CHUNK / 2) * 128, QBYTES = KB * (CHUNK / 2) * 128;
 constexpr uint32_t SMEM = OFF_Q + QBYTES + 1024;
-static_assert(NQ * (CHUNK / 2) * 128 <= QBYTES, "the ring fits the resident rows' place");
-// warps 0-7 sum; of blocks, the last three load keys too
-constexpr int W_KEYS = 8, W_ROWS = 9, W_MMA = 10, NTP = 352, NTB = NTP + 96;
+static_assert(NQ * QSLOT <= QBYTES && KB % QK == 0, "the ring fits the resident rows' place");
+// warps 0-7 sum, 8 loads keys, 9 rows, 10 and 11 issue the products of the blocks 0 1 3 4 6 and 2 5 7 8 of
+// channels, so that both are done with a group of rows' blocks before the next (one thread issues a product in 80 cycles at best, and its waits show: a chunk of 128 rows in 3,580
+// cycles instead of the 2,300 of the products, window of 8 x 32 nodes x 16384 181 us); of blocks, the last three
+// load keys too
+constexpr int W_KEYS = 8, W_ROWS = 9, W_MMA = 10, NTP = 384, NTB = NTP + 96;
 constexpr int MAX_CLUSTERS = 80;  // of two CTAs (152 SMs: 76)
 constexpr int KNOWN = 32;         // sequences of a run that are looked at once
 
@@ -57,20 +68,21 @@ enum {
   B_REMPTY = B_RFULL + 2,
   B_DFULL = B_REMPTY + 2,       //    a product is done (two buffers)
   B_DFREE = B_DFULL + 2,        // L  and read
-  B_DRAIN = B_DFREE + 2, B_N
+  B_DRAIN = B_DFREE + 2, B_N = B_DRAIN + 2
 };
 
 struct SumMaps {
-  CUtensorMap k, q16, q32, q64;  // query rows in boxes of 16, 32 and 64
+  CUtensorMap k, q[4];  // query rows in boxes of 16, 32, 48 and 64, three blocks of channels each
 };
 
 struct Seq {
   int lo, rows, len, keys, tiles;
-  uint32_t live;  // chunks that hold a node that counts (8192 rows: 32 at most)
-  __device__ __forceinline__ int chunks() const { return __popc(live); }
+  unsigned long long live;  // chunks that hold a node that counts (8192 rows: 64 at most)
+  // of a tile, in chunks' products: its keys' way into shared memory takes as long as three
+  __device__ __forceinline__ int cost() const { return max(__popcll(live), 3); }
 };
 // the live chunk behind chunk ch (-1: the first), or -1
-__device__ __forceinline__ int next_chunk(const Seq &s, int ch) { return __ffs((int)(ch < 0 ? s.live : s.live & (~1u << ch))) - 1; }
+__device__ __forceinline__ int next_chunk(const Seq &s, int ch) { return __ffsll((long long)(ch < 0 ? s.live : s.live & (~1ull << ch))) - 1; }
 template <bool BLOCKS>
 __device__ __forceinline__ Seq seq_of(const KeySumArgs &a, int n, bool tell) {
   Seq s;
@@ -90,21 +102,27 @@ __device__ __forceinline__ Seq seq_of(const KeySumArgs &a, int n, bool tell) {
   }
   s.rows = W * a.H;
   s.keys = W == 0 ? 0 : BLOCKS ? s.len / a.c.page_size : s.len + W;
-  const int chunks = s.rows <= RES ? 1 : (s.rows + CHUNK - 1) / CHUNK;
-  s.live = ~0u >> (32 - chunks);
+  const int chunks = s.rows <= CHUNK ? 1 : (s.rows + CHUNK - 1) / CHUNK;
+  s.live = ~0ull >> (64 - chunks);
   if (!BLOCKS && a.node_weight) {
     s.live = 0;
-#pragma unroll 8
-    for (int i = 0; i < W; ++i)
-      if (a.node_weight[s.lo + i] != 0.f)
-        s.live |= chunks == 1 ? 1u : (~0u << (i * a.H / CHUNK)) & (~0u >> (31 - ((i + 1) * a.H - 1) / CHUNK));
+    for (int i0 = 0; i0 < W; i0 += 16) {  // sixteen on their way
+      float u[16];
+#pragma unroll
+      for (int y = 0; y < 16; ++y) u[y] = i0 + y < W ? a.node_weight[s.lo + i0 + y] : 0.f;
+#pragma unroll
+      for (int y = 0; y < 16; ++y) {
+        const int i = i0 + y;
+        if (u[y] != 0.f) s.live |= chunks == 1 ? 1ull : (~0ull << (i * a.H / CHUNK)) & (~0ull >> (63 - ((i + 1) * a.H - 1) / CHUNK));
+      }
+    }
     if (s.live == 0) s.keys = 0;
   }
   s.tiles = (s.keys + Keys<BLOCKS>::TILE - 1) / Keys<BLOCKS>::TILE;
   return s;
 }
 
-// This cluster's run of (tile, chunk) units; a tile belongs to the run that its first unit falls in.
+// This cluster's run of the batch's units, a tile's cost each; a tile belongs to the run that its first unit falls in.
 template <bool BLOCKS>
 struct Walk {
   int n, t;          // the next tile
@@ -125,7 +143,7 @@ struct Walk {
         continue;
       }
       tile = t++;
-      at += s.chunks();
+      at += s.cost();
       last = t >= s.tiles || at >= stop;
       return true;
     }
@@ -144,12 +162,12 @@ __device__ __forceinline__ int columns(const Seq &s, int chunk) {  // of a chunk
   const int r = s.rows - CHUNK * chunk;
   return r >= CHUNK ? CHUNK : (r + pad) & ~pad;
 }
-// The products drop bits of every partial sum (measured: a lone head's weights 1.1e-6 off), so where tensor
-// memory has room, a score is the sum of up to four of them over a part of the channels each, added in fp32.
+// The products drop bits of every partial sum (measured: weights up to 1.4e-6 off), so a score is the sum of two
+// or, where tensor memory has room, four of them over a part of the channels each, added in fp32.
 template <bool BLOCKS>
 __device__ __forceinline__ int parts_of(int columns) {
   const int wide = BLOCKS ? columns / 2 : columns;  // of tensor memory
-  return wide <= CHUNK / 4 ? 4 : wide <= CHUNK / 2 ? 2 : 1;
+  return wide <= DCOLS / 4 ? 4 : 2;
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
@@ -193,7 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   __shared__ long long s_at;
   __shared__ __align__(16) float2 s_col[2][BLOCKS ? 2 : CHUNK];  // rows' (lse, weight)
   __shared__ __align__(16) uint8_t s_node[2][BLOCKS ? 16 : CHUNK];
-  __shared__ uint32_t s_counts[2][8];  // bits of the rows that count
+  __shared__ uint32_t s_counts[2][CHUNK / 32];  // bits of the rows that count
   __shared__ float s_half[2][BLOCKS ? 1 : KC];
   const uint32_t raw = smem_u32(dyn);
   const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -203,14 +221,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   auto bar = [&](int i) { return smem_u32(&s_bar[i]); };
   if (tid < B_N) {
     int n = 1;
-    if (tid < B_KEMPTY) n = BLOCKS ? 8 : 2;  // the loaders of both CTAs
-    if ((tid >= B_QFULL && tid < B_QEMPTY) || tid == B_RFULL || tid == B_RFULL + 1) n = 2;
+    if (tid < B_KEMPTY) n = BLOCKS ? 8 : 2;              // the loaders of both CTAs
+    else if (tid < B_QFULL) n = BLOCKS ? 2 : 1;          // the issuing warps that read it
+    else if (tid < B_QEMPTY) n = 2;
+    else if (tid < B_DFREE) n = 2;
     if (tid == B_DFREE || tid == B_DFREE + 1) n = 16;                                 // the sums' warps
     mbar_init(bar(tid), n);
     mbar_fence_init();
   }
   if (tid == 64) s_abort = 0, s_n = 0, s_t = 0, s_at = 0;
-  if (tid >= 96 && tid < 100) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k + (tid - 96)) : "memory");
+  if (tid >= 96 && tid < 101) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k + (tid - 96)) : "memory");
   if (warp == W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -225,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   Seq mine = {};       // of the first NT sequences
   long long at = 0;    // units before this thread's sequence
   auto sum_up = [&](const Seq &s, long long &before) {  // returns the units before it, adds all to `before`
-    const long long cost = (long long)s.tiles * s.chunks();
+    const long long cost = (long long)s.tiles * s.cost();
     long long x = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -254,10 +274,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   const long long begin = run_start(total, cid, clusters), stop = run_start(total, cid + 1, clusters);
   if (stop > begin) {  // the first tile whose first unit is at or behind `begin`
     auto claim = [&](const Seq &s, long long at, int n) {
-      const int chunks = s.chunks();
-      if (at <= begin && begin < at + (long long)s.tiles * chunks) {
-        const int t = (int)(begin - at + chunks - 1) / chunks;  // (a sequence has at most 2^26 units)
-        s_n = n, s_t = t, s_at = at + (long long)t * chunks;
+      const int cost = s.cost();
+      if (at <= begin && begin < at + (long long)s.tiles * cost) {
+        const int t = (int)(begin - at + cost - 1) / cost;  // (a sequence has at most 2^26 units)
+        s_n = n, s_t = t, s_at = at + (long long)t * cost;
       }
     };
     claim(mine, at, tid);
@@ -301,14 +321,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   };
   const int lp = 31 - __clz(a.c.page_size);
 
-  if (warp == W_KEYS || (BLOCKS && warp > W_MMA)) {
+  if (warp == W_KEYS || (BLOCKS && warp > W_MMA + 1)) {
     // ---- key blocks: positions by tile loads, a lane each; blocks by 16-byte copies of their keys, 32 a
     //      warp, the next tile's pages looked up meanwhile (gathers by TMA, four rows each, took three
     //      times as long; one warp of copies twice)
     auto known = [&](int page) { return page >= 0 && page < a.c.n_pages; };
     int tiles = 0;
     if constexpr (BLOCKS) {
-      const int mine = 16 * (warp == W_KEYS ? 0 : warp - W_MMA), piece = lane & 7;
+      const int mine = 16 * (warp == W_KEYS ? 0 : warp - W_MMA - 1), piece = lane & 7;
       int page = 0, rows = 0;  // of the next tile: this lane's page, the warp's keys (may be below 0)
       auto look = [&]() {
         const int b = TILE * walk.tile + KC * (int)rank + mine;
@@ -381,117 +401,105 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     if (s_abort)  // a wait ran out: let the copies in flight land
       for (int y = 0; y < 100; ++y) __nanosleep(10000);
   } else if (warp == W_ROWS) {
-    // ---- query rows: resident for a sequence, or a chunk's 64 channels at a time.  Up to 64 resident
+    // ---- query rows: resident for a sequence, or a chunk's three blocks of channels at a time.  Up to 64 resident
     //      rows take half of the place, so that the next sequence's are loaded meanwhile; the k-th
     //      resident sequence uses the barriers k & 1.
-    int segs = 0;
+    int segs = 0, streamed = 0;
     bool wide = false;  // the last one took the whole place
-    int j = 0, used = 0;
-    uint32_t par = 1;   // parity that a slot's last use ends (a fresh barrier counts as ended)
-    bool ring = false;  // the ring's slots hold what was read last
+    bool ring = false;  // a chunk's slots hold what was read last
     auto seg_done = [&](int k) {
       if (k >= 0) warp_wait(B_REMPTY + (k & 1), (uint32_t)(k >> 1));
     };
+    auto load = [&](int full, uint32_t dst, int g, int64_t row, int half) {  // a group of blocks
+      if (lane == 0) {
+        announce(full, (uint32_t)(QK * half * 128));
+        tma_pair_3d(dst, &maps.q[half / 16 - 1], 0, (int)row, QK * g, map_shared_rank(bar(full), 0));
+      }
+      __syncwarp();
+    };
     while (walk.next(a)) {
       const int64_t row0 = (int64_t)walk.s.lo * a.H;
-      if (walk.s.rows <= RES) {
+      if (walk.s.rows <= CHUNK) {
         if (!walk.first) continue;
         const int half = columns<BLOCKS>(walk.s, 0) / 2;
-        const int box = half % 64 == 0 ? 64 : half % 32 == 0 ? 32 : 16, boxes = half / box;  // few loads: each costs the warp
-        const CUtensorMap *map = box == 64 ? &maps.q64 : box == 32 ? &maps.q32 : &maps.q16;
-        const bool whole = 2 * half > RES / 2;
+        const bool whole = 2 * half > CHUNK / 2;
         seg_done(segs - 2);
         if (whole || wide) seg_done(segs - 1);
         wide = whole;
-        if (ring) {  // every slot read
-          for (int y = 0; y < used; ++y) {
-            const int k = (j + NQ - 1 - y) % NQ;
-            warp_wait(B_QEMPTY + k, k < j ? par ^ 1 : par);
-          }
-          ring = false;
-        }
+        if (ring)
+          for (int g = 0; g < NQ; ++g) warp_wait(B_QEMPTY + g, (uint32_t)(streamed - 1));
+        ring = false;
         const int b = segs & 1;
         const uint32_t place = sb + OFF_Q + (whole || b == 0 ? 0 : QBYTES / 2);
-        if (lane == 0) announce(B_RFULL + b, (uint32_t)(KB * half * 128));
-        __syncwarp();
-        const uint32_t full = map_shared_rank(bar(B_RFULL + b), 0);
-        for (int x = lane; x < KB * boxes; x += 32) {
-          const int kb = x / boxes, y = x - kb * boxes;
-          if (!s_abort)
-            tma_pair_3d(place + kb * half * 128 + y * box * 128, map, 64 * kb, (int)(row0 + half * (int)rank + box * y), 0, full);
+        if (!s_abort) {
+          if (lane == 0) {
+            announce(B_RFULL + b, (uint32_t)(KB * half * 128));
+            for (int g = 0; g < NQ; ++g)
+              tma_pair_3d(place + g * QK * half * 128, &maps.q[half / 16 - 1], 0, (int)(row0 + half * (int)rank), QK * g,
+                          map_shared_rank(bar(B_RFULL + b), 0));
+          }
+          __syncwarp();
         }
         ++segs;
       } else {
         if (!ring) seg_done(segs - 1);
         ring = true;
-        for (int ch = next_chunk(walk.s, -1); ch >= 0; ch = next_chunk(walk.s, ch)) {
+        for (int ch = next_chunk(walk.s, -1); ch >= 0; ch = next_chunk(walk.s, ch), ++streamed) {
           const int half = columns<BLOCKS>(walk.s, ch) / 2;
-          const int64_t r = row0 + CHUNK * ch + half * (int)rank;
 #pragma unroll 1
-          for (int kb = 0; kb < KB; ++kb) {
-            if (warp_wait(B_QEMPTY + j, par)) {
-              if (lane == 0) announce(B_QFULL + j, (uint32_t)half * 128);
-              __syncwarp();
-              const uint32_t full = map_shared_rank(bar(B_QFULL + j), 0), dst = sb + OFF_Q + j * (CHUNK / 2) * 128;
-              if (half == CHUNK / 2) {
-                if (lane < 2) tma_pair_3d(dst + lane * 8192, &maps.q64, 64 * kb, (int)r + 64 * lane, 0, full);
-              } else if (lane < half / 16) {
-                tma_pair_3d(dst + lane * 2048, &maps.q16, 64 * kb, (int)r + 16 * lane, 0, full);
-              }
-            }
-            if (used < NQ) ++used;
-            if (++j == NQ) j = 0, par ^= 1;
-          }
+          for (int g = 0; g < NQ; ++g)
+            if (streamed == 0 || warp_wait(B_QEMPTY + g, (uint32_t)(streamed - 1)))
+              load(B_QFULL + g, sb + OFF_Q + g * QSLOT, g, row0 + CHUNK * ch + half * (int)rank, half);
         }
       }
     }
     seg_done(segs - 2);
     seg_done(segs - 1);
-    for (int y = 0; y < used; ++y) {
-      const int k = (j + NQ - 1 - y) % NQ;
-      wait(B_QEMPTY + k, k < j ? par ^ 1 : par);
-    }
+    if (streamed > 0)
+      for (int g = 0; g < NQ; ++g) wait(B_QEMPTY + g, (uint32_t)(streamed - 1));
     if (s_abort)
       for (int y = 0; y < 100; ++y) __nanosleep(10000);
-  } else if (warp == W_MMA) {
-    // ---- products (one thread of the leading CTA) --------------------------------------------
+  } else if (warp == W_MMA || warp == W_MMA + 1) {
+    // ---- products (a thread each of two warps of the leading CTA: their partial sums are apart) ----
     if (rank == 0 && elect()) {
-      int i = 0, j = 0, tiles = 0, segs = 0;
-      uint32_t par = 0;
+      const int which = warp - W_MMA, blocks = which == 0 ? 5 : 4;
+      const uint32_t order = which == 0 ? 0x64310u : 0x8752u;  // a block a digit
+      int i = 0, tiles = 0, segs = 0, streamed = 0;
       bool ok = true;
       while (ok && walk.next(a)) {
-        const bool res = walk.s.rows <= RES;
+        const bool res = walk.s.rows <= CHUNK;
         if (res && walk.first && !(ok = wait(B_RFULL + (segs & 1), (uint32_t)(segs >> 1)))) break;
-        const uint32_t place = sb + OFF_Q + (columns<BLOCKS>(walk.s, 0) > RES / 2 || !(segs & 1) ? 0 : QBYTES / 2);
-        bool fill = true;  // the tile's keys are waited for
+        const uint32_t place = sb + OFF_Q + (!res || columns<BLOCKS>(walk.s, 0) > CHUNK / 2 || !(segs & 1) ? 0 : QBYTES / 2);
+        if (BLOCKS && !(ok = wait(B_KFULL + (tiles & 1), (uint32_t)(tiles >> 1)))) break;
+        bool fill = !BLOCKS;  // the tile's keys are waited for
         for (int ch = next_chunk(walk.s, -1), then; ch >= 0 && ok; ch = then, ++i) {
           then = next_chunk(walk.s, ch);
           const int N = columns<BLOCKS>(walk.s, ch), parts = parts_of<BLOCKS>(N);
-          const uint32_t id = idesc(1, TILE, (uint32_t)N, 0, 0), d = tm + CHUNK * (i & 1);
+          const uint32_t id = idesc(1, TILE, (uint32_t)N, 0, 0), d = tm + DCOLS * (i & 1);
           if (i >= 2 && !(ok = wait(B_DFREE + (i & 1), (uint32_t)((i >> 1) - 1)))) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int kb = 0; kb < KB; ++kb) {
-            const int block = tiles % BUFS * KB + kb;
-            if (fill && (!BLOCKS || kb == 0) && !(ok = wait(B_KFULL + (BLOCKS ? tiles & 1 : kb), (uint32_t)(tiles / BUFS)))) break;
-            if (!res && !(ok = wait(B_QFULL + j, par))) break;
-            const int part = kb * parts / KB;
-            const bool fresh = kb == 0 || (kb - 1) * parts / KB < part;
-            const uint64_t ad = sdesc_sw128(sb + OFF_K + block * SLOT, 16, 1024);
-            const uint64_t bd = sdesc_sw128(res ? place + kb * (N / 2) * 128 : sb + OFF_Q + j * (CHUNK / 2) * 128, 16, 1024);
+          for (int x = 0; x < blocks; ++x) {
+            const int kb = order >> (4 * x) & 15, behind = x + 1 < blocks ? order >> (4 * x + 4) & 15 : KB;
+            const int ahead = x > 0 ? order >> (4 * x - 4) & 15 : -QK;
+            if (fill && !(ok = wait(B_KFULL + kb, (uint32_t)tiles))) break;
+            if (!res && (ahead < 0 || ahead / QK < kb / QK) && !(ok = wait(B_QFULL + kb / QK, (uint32_t)streamed))) break;
+            // its part of the sum: half of them are each warp's, which takes three blocks or two to one of two
+            const int part = which * (parts >> 1) + (parts == 4 && x >= 3 - which ? 1 : 0);
+            const bool fresh = x == 0 || (parts == 4 && x == 3 - which);
+            const uint64_t ad = sdesc_sw128(sb + OFF_K + (tiles % BUFS * KB + kb) * SLOT, 16, 1024);
+            const uint64_t bd = sdesc_sw128(res ? place + kb * (N / 2) * 128 : place + kb / QK * QSLOT + kb % QK * (N / 2) * 128, 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma2(d + part * (CHUNK / parts), ad + 2 * ks, bd + 2 * ks, id, !fresh || ks > 0);
-            if (!res) {
-              commit2(bar(B_QEMPTY + j));
-              if (++j == NQ) j = 0, par ^= 1;
-            }
+              mma2(d + part * (DCOLS / parts), ad + 2 * ks, bd + 2 * ks, id, !fresh || ks > 0);
+            if (!res && behind / QK > kb / QK) commit2(bar(B_QEMPTY + kb / QK));
             if (!BLOCKS && then < 0) commit2(bar(B_KEMPTY + kb));
           }
           fill = false;
           if (!ok) break;
           if (BLOCKS && then < 0) commit2(bar(B_KEMPTY + (tiles & 1)));
           commit2(bar(B_DFULL + (i & 1)));
+          if (!res) ++streamed;
         }
         if (ok && res && walk.last) {
           commit2(bar(B_REMPTY + (segs & 1)));
@@ -500,8 +508,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         ++tiles;
       }
       if (!ok) {  // a wait ran out: let the products in flight end
-        commit2(bar(B_DRAIN));
-        mbar_wait(bar(B_DRAIN), 0);
+        commit2(bar(B_DRAIN + which));
+        mbar_wait(bar(B_DRAIN + which), 0);
       }
     }
   } else {
@@ -516,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     auto row_of = [&](const Seq &s, int ch) {  // (lse in units of log 2, weight)
       float2 x = make_float2(0.f, 0.f);
       const int r = CHUNK * ch + tid;
-      if (r >= s.rows) return x;
+      if (tid >= CHUNK || r >= s.rows) return x;
       ahead_node = r / a.H;
       x.x = a.lse[(int64_t)s.lo * a.H + r] * 1.4426950408889634f;
       x.y = a.node_weight ? a.node_weight[s.lo + ahead_node] : 1.f;
@@ -552,39 +560,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
       for (int ch = head, then; ch >= 0; ch = then, ++i) {
         then = next_chunk(s, ch);
         const int N = columns<BLOCKS>(s, ch), parts = parts_of<BLOCKS>(N), share = BLOCKS ? N / 4 : N / 2, c0 = hf * share, c1 = c0 + share;
-        if (!BLOCKS && (s.rows > RES || walk.first)) {
+        if (!BLOCKS && (s.rows > CHUNK || walk.first)) {
           if (walk.first && ch == head) ahead = row_of(s, ch);
           const float2 x = ahead;
           const int b = loads & 1;
-          s_col[b][tid] = x;
-          s_node[b][tid] = (uint8_t)ahead_node;
-          const uint32_t counts = __ballot_sync(0xffffffffu, x.y != 0.f);
-          if (lane == 0) s_counts[b][warp] = counts;
+          if (tid < CHUNK) {
+            s_col[b][tid] = x;
+            s_node[b][tid] = (uint8_t)ahead_node;
+            const uint32_t counts = __ballot_sync(0xffffffffu, x.y != 0.f);
+            if (lane == 0) s_counts[b][warp] = counts;
+          }
           ++loads;
           bar_sync(1, 256);  // two buffers: the next but one is written behind the next barrier
-          if (s.rows > RES) ahead = row_of(s, then >= 0 ? then : head);  // asked for while this one is summed
+          if (s.rows > CHUNK) ahead = row_of(s, then >= 0 ? then : head);  // asked for while this one is summed
         }
         const int b = (loads - 1) & 1;
         wait(B_DFULL + (i & 1), (uint32_t)(i >> 1));
         tc_fence_after();
-        const uint32_t d = tm + lanes + CHUNK * (i & 1);
+        const uint32_t d = tm + lanes + DCOLS * (i & 1);
         // 16 columns' scores: asked for, and their parts added once they are there
         auto ask = [&](int c, float (&v)[16]) { tmem_ld16(d + c, v); };
         auto rest = [&](int c, float (&v)[16]) {
-          if (!BLOCKS) {
-            for (int x = 1; x < parts; ++x) {
-              float w[16];
-              tmem_ld16(d + x * (CHUNK / parts) + c, w);
-              tmem_wait_ld();
-#pragma unroll
-              for (int y = 0; y < 16; ++y) v[y] += w[y];
-            }
-            return;
-          }
-          float w[3][16];  // at once: there is one group of columns, mostly
+          float w[3][16];
 #pragma unroll
           for (int x = 1; x < 4; ++x)
-            if (x < parts) tmem_ld16(d + x * (CHUNK / parts) + c, w[x - 1]);
+            if (x < parts) tmem_ld16(d + x * (DCOLS / parts) + c, w[x - 1]);
           tmem_wait_ld();
 #pragma unroll
           for (int x = 1; x < 4; ++x)
@@ -711,10 +711,19 @@ cudaError_t launch_sums(const KeySumArgs &a, const SumMaps &maps, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, key_sums_kernel<BLOCKS>, a, maps);
 }
 
+// query rows as [9 blocks of 64 channels][rows], so that a load brings several blocks
 bool row_maps(const KeySumArgs &a, SumMaps *maps) {
-  const int64_t rows = a.total * a.H;
-  return tree_map(&maps->q16, a.q, true, TK, rows, 1, 64, 16) && tree_map(&maps->q32, a.q, true, TK, rows, 1, 64, 32) &&
-         tree_map(&maps->q64, a.q, true, TK, rows, 1, 64, 64);
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  for (int i = 0; i < 4; ++i) {
+    cuuint64_t dims[3] = {64, (cuuint64_t)(a.total * a.H), KB}, strides[2] = {TK * 2, 128};
+    cuuint32_t bx[3] = {64, (cuuint32_t)(16 * (i + 1)), QK}, es[3] = {1, 1, 1};
+    if (fn(&maps->q[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, bx, es,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
 }
 
 }  // namespace
@@ -732,7 +741,7 @@ cudaError_t launch_block_products(const KeySumArgs &a, cudaStream_t s) {
   SumMaps maps;
   memset(&maps, 0, sizeof maps);
   if (!row_maps(a, &maps)) return cudaErrorInvalidValue;
-  maps.k = maps.q16;  // not used: the keys come by copies
+  maps.k = maps.q[0];  // not used: the keys come by copies
   return launch_sums<true>(a, maps, s);
 }
 

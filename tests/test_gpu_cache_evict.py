@@ -38,8 +38,9 @@ class Cache:
             self.w = torch.randint(0, 4, (n, width), generator=g).float() - 1.0
         elif kind == "same":
             self.w = torch.full((n, width), 0.25)
-        else:  # close together: the low bits decide
-            self.w = 1.0 + torch.randint(0, 300, (n, width), generator=g).float() * 2.0**-23
+        else:  # close together: the last bits decide, over any number of them
+            most = {"close": 300, "near": 6000, "apart": 1 << 16}[kind]
+            self.w = 1.0 + torch.randint(0, most, (n, width), generator=g).float() * 2.0**-23
 
     def run(self, budget, *, first=0, recent=0, refs="own", new="aside", in_place_lengths=False):
         _gpu.lib()
@@ -76,7 +77,7 @@ class Cache:
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
-@pytest.mark.parametrize("kind", ["random", "ties", "same", "close"])
+@pytest.mark.parametrize("kind", ["random", "ties", "same", "close", "near", "apart"])
 def test_ragged_lengths(page, kind):
     c = Cache([0, 1, 39, 40, 41, 63, 64, 300, 700, 1025], page=page, seed=page, kind=kind)
     for budget, first, recent in ((40, 0, 0), (40, 4, 8), (40, 40, 0), (40, 0, 40), (1, 0, 0), (64, 3, 60), (2000, 1, 1)):
@@ -98,12 +99,25 @@ def self_lengths(c, new):
     return d
 
 
+@pytest.mark.parametrize("kind", ["ties", "near", "apart", "random"])
 @pytest.mark.parametrize("n,length", [(1, 9000), (2, 20001), (1, 70001), (40, 9000)])
-def test_long_sequences_by_clusters(n, length):
-    """One to eight CTAs a sequence, with many equal weights among them."""
-    c = Cache([length - 7 * i for i in range(n)], layers=1, page=64, seed=n, kind="ties")
+def test_long_sequences_by_clusters(n, length, kind):
+    """One to eight CTAs a sequence, with many equal weights or such as differ in their last bits."""
+    c = Cache([length - 7 * i for i in range(n)], layers=1, page=64, seed=n, kind=kind)
     for budget in (length // 3, length - 400):
         c.check(c.run(budget, first=4, recent=32, new="own"), budget, first=4, recent=32, new="own")
+
+
+@pytest.mark.parametrize("bit", range(0, 32, 3))
+def test_every_bit_counts(bit):
+    """Weights that differ in a few neighbouring bits alone, whichever they are."""
+    c = Cache([900, 333], layers=1, seed=bit)
+    g = torch.Generator().manual_seed(bit)
+    span = min(4, 32 - bit)
+    low = torch.randint(0, 1 << span, c.w.shape, generator=g) << bit
+    c.w = (low ^ 0x3F800000 if bit < 22 else low).to(torch.int64).to(torch.int32).view(torch.float32)
+    for budget in (100, 200, 320):
+        c.check(c.run(budget, recent=7), budget, recent=7)
 
 
 def test_special_values():
