@@ -19,10 +19,9 @@
 // What bounds it.  One node a sequence: the cache's bytes, which stream through once, block by block, as
 // the products free the blocks (256 sequences of 2048 to 4096 positions, 64 heads: 137 us, 6.8 TB/s, the copy
 // rate).  Many nodes: rows x positions x 1152 flop on the tensor cores; a chunk's 36 products of 64 cycles take
-// about 3,600, as its rows' way through the shared memory that the keys leave (74 KB, no more than the chunk)
-// shows (8 sequences x 22 to 32 nodes x 8192 to 16384 positions: 158 us where all count, 1.33 PFLOP/s; chunks of
-// 256 rows, with a buffer of tensor memory each and so one sum over all channels, took 147 us and were up to
-// 1.4e-6 off).  Few positions: latency, a launch of 8 us.
+// about 2,900, with the epilogue beside them (8 sequences x 22 to 32 nodes x 8192 to 16384 positions: 150 us where
+// all count, 1.40 PFLOP/s; chunks of 256 rows, whose products fill a buffer of tensor memory each and so are one
+// sum over all channels, took 147 us and were up to 1.4e-6 off).  Few positions: latency, a launch of 8 us.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "mla_pair.cuh"
@@ -37,7 +36,7 @@ using namespace tc;
 
 constexpr int TK = 576, KB = TK / 64;
 constexpr int CHUNK = 128;             // rows of a product: as many are resident, more are streamed
-constexpr int NQ = 3, QK = 3;          // rows come in groups of blocks: their slots, blocks of a group
+constexpr int NQ = KB, QK = 3;         // rows' slots, a block each; resident rows come by threes of blocks
 constexpr int DCOLS = 256;             // columns of tensor memory of a product (two of them)
 // Keys: positions 128 a CTA (M = 256), in one buffer of nine blocks; blocks 64 (M = 128: each CTA's lanes 64 ..
 // hold the upper half of the rows' columns), in two, as their tiles are few and their latency counts
@@ -47,14 +46,14 @@ struct Keys {
   static constexpr uint32_t SLOT = KC * 128;
 };
 constexpr uint32_t OFF_K = 0, OFF_Q = KB * 128 * 128;
-constexpr uint32_t QSLOT = QK * (CHUNK / 2) * 128, QBYTES = KB * (CHUNK / 2) * 128;
+constexpr uint32_t QSLOT = (CHUNK / 2) * 128, QBYTES = KB * (CHUNK / 2) * 128;
 constexpr uint32_t SMEM = OFF_Q + QBYTES + 1024;
-static_assert(NQ * QSLOT <= QBYTES && KB % QK == 0, "the ring fits the resident rows' place");
-// warps 0-7 sum, 8 loads keys, 9 rows, 10 and 11 issue the products of the blocks 0 1 3 4 6 and 2 5 7 8 of
-// channels, so that both are done with a group of rows' blocks before the next (one thread issues a product in 80 cycles at best, and its waits show: a chunk of 128 rows in 3,580
-// cycles instead of the 2,300 of the products, window of 8 x 32 nodes x 16384 181 us); of blocks, the last three
-// load keys too
-constexpr int W_KEYS = 8, W_ROWS = 9, W_MMA = 10, NTP = 384, NTB = NTP + 96;
+static_assert(NQ * QSLOT <= QBYTES && KB % QK == 0, "a chunk fits the resident rows' place");
+// warps 0-7 sum, 8 loads keys, 9 rows, 10 and 11 issue the products of the even and of the odd blocks of
+// channels; of blocks, the last three load keys too, of positions the last two rows.  A thread issues a product in
+// 80 cycles at best, waits come on top; a load costs its thread some 450 (the window above: 181 us with one
+// issuing warp, 200 with two and one for the rows' loads, 150 so).
+constexpr int W_KEYS = 8, W_ROWS = 9, W_MMA = 10, W_MORE = 12, NTP = 448, NTB = 480;
 constexpr int MAX_CLUSTERS = 80;  // of two CTAs (152 SMs: 76)
 constexpr int KNOWN = 32;         // sequences of a run that are looked at once
 
@@ -72,7 +71,7 @@ enum {
 };
 
 struct SumMaps {
-  CUtensorMap k, q[4];  // query rows in boxes of 16, 32, 48 and 64, three blocks of channels each
+  CUtensorMap k, q[4], q3[4];  // query rows in boxes of 16, 32, 48 and 64, one and three blocks of channels each
 };
 
 struct Seq {
@@ -224,13 +223,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     if (tid < B_KEMPTY) n = BLOCKS ? 8 : 2;              // the loaders of both CTAs
     else if (tid < B_QFULL) n = BLOCKS ? 2 : 1;          // the issuing warps that read it
     else if (tid < B_QEMPTY) n = 2;
+    else if (tid < B_RFULL) n = 1;
     else if (tid < B_DFREE) n = 2;
     if (tid == B_DFREE || tid == B_DFREE + 1) n = 16;                                 // the sums' warps
     mbar_init(bar(tid), n);
     mbar_fence_init();
   }
   if (tid == 64) s_abort = 0, s_n = 0, s_t = 0, s_at = 0;
-  if (tid >= 96 && tid < 101) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k + (tid - 96)) : "memory");
+  if (tid >= 96 && tid < 105) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k + (tid - 96)) : "memory");
   if (warp == W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -321,14 +321,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   };
   const int lp = 31 - __clz(a.c.page_size);
 
-  if (warp == W_KEYS || (BLOCKS && warp > W_MMA + 1)) {
+  if (warp == W_KEYS || (BLOCKS && warp >= W_MORE)) {
     // ---- key blocks: positions by tile loads, a lane each; blocks by 16-byte copies of their keys, 32 a
     //      warp, the next tile's pages looked up meanwhile (gathers by TMA, four rows each, took three
     //      times as long; one warp of copies twice)
     auto known = [&](int page) { return page >= 0 && page < a.c.n_pages; };
     int tiles = 0;
     if constexpr (BLOCKS) {
-      const int mine = 16 * (warp == W_KEYS ? 0 : warp - W_MMA - 1), piece = lane & 7;
+      const int mine = 16 * (warp == W_KEYS ? 0 : warp - W_MORE + 1), piece = lane & 7;
       int page = 0, rows = 0;  // of the next tile: this lane's page, the warp's keys (may be below 0)
       auto look = [&]() {
         const int b = TILE * walk.tile + KC * (int)rank + mine;
@@ -400,27 +400,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
       for (int kb = 0; kb < KB; ++kb) wait(B_KEMPTY + kb, (uint32_t)(tiles - 1));
     if (s_abort)  // a wait ran out: let the copies in flight land
       for (int y = 0; y < 100; ++y) __nanosleep(10000);
-  } else if (warp == W_ROWS) {
-    // ---- query rows: resident for a sequence, or a chunk's three blocks of channels at a time.  Up to 64 resident
+  } else if (warp == W_ROWS || (!BLOCKS && warp >= W_MORE)) {
+    // ---- query rows: resident for a sequence, or a chunk's blocks of channels one by one.  Up to 64 resident
     //      rows take half of the place, so that the next sequence's are loaded meanwhile; the k-th
     //      resident sequence uses the barriers k & 1.
+    const int which = warp == W_ROWS ? 0 : warp - W_MORE + 1, loaders = BLOCKS ? 1 : 3;
     int segs = 0, streamed = 0;
     bool wide = false;  // the last one took the whole place
     bool ring = false;  // a chunk's slots hold what was read last
     auto seg_done = [&](int k) {
       if (k >= 0) warp_wait(B_REMPTY + (k & 1), (uint32_t)(k >> 1));
     };
-    auto load = [&](int full, uint32_t dst, int g, int64_t row, int half) {  // a group of blocks
-      if (lane == 0) {
-        announce(full, (uint32_t)(QK * half * 128));
-        tma_pair_3d(dst, &maps.q[half / 16 - 1], 0, (int)row, QK * g, map_shared_rank(bar(full), 0));
-      }
-      __syncwarp();
-    };
     while (walk.next(a)) {
       const int64_t row0 = (int64_t)walk.s.lo * a.H;
       if (walk.s.rows <= CHUNK) {
         if (!walk.first) continue;
+        if (which > 0) {
+          ring = false;
+          ++segs;
+          continue;
+        }
         const int half = columns<BLOCKS>(walk.s, 0) / 2;
         const bool whole = 2 * half > CHUNK / 2;
         seg_done(segs - 2);
@@ -434,8 +433,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         if (!s_abort) {
           if (lane == 0) {
             announce(B_RFULL + b, (uint32_t)(KB * half * 128));
-            for (int g = 0; g < NQ; ++g)
-              tma_pair_3d(place + g * QK * half * 128, &maps.q[half / 16 - 1], 0, (int)(row0 + half * (int)rank), QK * g,
+            for (int kb = 0; kb < KB; kb += QK)
+              tma_pair_3d(place + kb * half * 128, &maps.q3[half / 16 - 1], 0, (int)(row0 + half * (int)rank), kb,
                           map_shared_rank(bar(B_RFULL + b), 0));
           }
           __syncwarp();
@@ -447,9 +446,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         for (int ch = next_chunk(walk.s, -1); ch >= 0; ch = next_chunk(walk.s, ch), ++streamed) {
           const int half = columns<BLOCKS>(walk.s, ch) / 2;
 #pragma unroll 1
-          for (int g = 0; g < NQ; ++g)
-            if (streamed == 0 || warp_wait(B_QEMPTY + g, (uint32_t)(streamed - 1)))
-              load(B_QFULL + g, sb + OFF_Q + g * QSLOT, g, row0 + CHUNK * ch + half * (int)rank, half);
+          for (int kb = which; kb < KB; kb += loaders)
+            if (streamed == 0 || warp_wait(B_QEMPTY + kb, (uint32_t)(streamed - 1))) {
+              if (lane == 0) {
+                announce(B_QFULL + kb, (uint32_t)half * 128);
+                tma_pair_3d(sb + OFF_Q + kb * QSLOT, &maps.q[half / 16 - 1], 0, (int)(row0 + CHUNK * ch + half * (int)rank), kb,
+                            map_shared_rank(bar(B_QFULL + kb), 0));
+              }
+              __syncwarp();
+            }
         }
       }
     }
@@ -463,7 +468,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     // ---- products (a thread each of two warps of the leading CTA: their partial sums are apart) ----
     if (rank == 0 && elect()) {
       const int which = warp - W_MMA, blocks = which == 0 ? 5 : 4;
-      const uint32_t order = which == 0 ? 0x64310u : 0x8752u;  // a block a digit
       int i = 0, tiles = 0, segs = 0, streamed = 0;
       bool ok = true;
       while (ok && walk.next(a)) {
@@ -480,19 +484,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
           tc_fence_after();
 #pragma unroll 1
           for (int x = 0; x < blocks; ++x) {
-            const int kb = order >> (4 * x) & 15, behind = x + 1 < blocks ? order >> (4 * x + 4) & 15 : KB;
-            const int ahead = x > 0 ? order >> (4 * x - 4) & 15 : -QK;
+            const int kb = 2 * x + which;
             if (fill && !(ok = wait(B_KFULL + kb, (uint32_t)tiles))) break;
-            if (!res && (ahead < 0 || ahead / QK < kb / QK) && !(ok = wait(B_QFULL + kb / QK, (uint32_t)streamed))) break;
+            if (!res && !(ok = wait(B_QFULL + kb, (uint32_t)streamed))) break;
             // its part of the sum: half of them are each warp's, which takes three blocks or two to one of two
             const int part = which * (parts >> 1) + (parts == 4 && x >= 3 - which ? 1 : 0);
             const bool fresh = x == 0 || (parts == 4 && x == 3 - which);
             const uint64_t ad = sdesc_sw128(sb + OFF_K + (tiles % BUFS * KB + kb) * SLOT, 16, 1024);
-            const uint64_t bd = sdesc_sw128(res ? place + kb * (N / 2) * 128 : place + kb / QK * QSLOT + kb % QK * (N / 2) * 128, 16, 1024);
+            const uint64_t bd = sdesc_sw128(place + kb * (res ? (N / 2) * 128 : QSLOT), 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               mma2(d + part * (DCOLS / parts), ad + 2 * ks, bd + 2 * ks, id, !fresh || ks > 0);
-            if (!res && behind / QK > kb / QK) commit2(bar(B_QEMPTY + kb / QK));
+            if (!res) commit2(bar(B_QEMPTY + kb));
             if (!BLOCKS && then < 0) commit2(bar(B_KEMPTY + kb));
           }
           fill = false;
@@ -578,24 +581,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
         wait(B_DFULL + (i & 1), (uint32_t)(i >> 1));
         tc_fence_after();
         const uint32_t d = tm + lanes + DCOLS * (i & 1);
-        // 16 columns' scores: asked for, and their parts added once they are there
-        auto ask = [&](int c, float (&v)[16]) { tmem_ld16(d + c, v); };
-        auto rest = [&](int c, float (&v)[16]) {
+        // 16 columns' scores, in `parts` parts: asked for, and added up once they are there
+        auto ask = [&](int c, int part, float (&v)[16]) { tmem_ld16(d + part * (DCOLS / parts) + c, v); };
+        auto add = [&](float (&v)[16], const float (&w)[16]) {
+#pragma unroll
+          for (int y = 0; y < 16; ++y) v[y] += w[y];
+        };
+        auto all_of_four = [&](int c, float (&v)[16]) {
           float w[3][16];
-#pragma unroll
-          for (int x = 1; x < 4; ++x)
-            if (x < parts) tmem_ld16(d + x * (DCOLS / parts) + c, w[x - 1]);
+          ask(c, 0, v), ask(c, 1, w[0]), ask(c, 2, w[1]), ask(c, 3, w[2]);
           tmem_wait_ld();
-#pragma unroll
-          for (int x = 1; x < 4; ++x)
-            if (x < parts) {
-#pragma unroll
-              for (int y = 0; y < 16; ++y) v[y] += w[x - 1][y];
-            }
+          add(v, w[0]), add(w[1], w[2]), add(v, w[1]);
         };
         if (!BLOCKS) {
           if (!none) {
-            float v[16], w[16];
             auto sum = [&](const float (&v)[16], int c) {
               const float4 *col = reinterpret_cast<const float4 *>(&s_col[b][c]);
               const uint32_t counts = s_counts[b][c >> 5] >> (c & 16) & 0xffff;
@@ -628,28 +627,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
                 }
               }
             };
-            ask(c0, v);
+            if (parts == 4) {
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 32) {  // 16 columns are read while 16 are summed
-              tmem_wait_ld();
-              rest(c, v);
-              if (c + 16 < c1) ask(c + 16, w);
-              sum(v, c);
-              if (c + 16 < c1) {
+              for (int c = c0; c < c1; c += 16) {
+                float v[16];
+                all_of_four(c, v);
+                sum(v, c);
+              }
+            } else {
+              float v[2][16], w[2][16];
+              ask(c0, 0, v[0]), ask(c0, 1, v[1]);
+#pragma unroll 1
+              for (int c = c0; c < c1; c += 32) {  // 16 columns are read while 16 are summed
                 tmem_wait_ld();
-                rest(c + 16, w);
-                if (c + 32 < c1) ask(c + 32, v);
-                sum(w, c + 16);
+                if (c + 16 < c1) ask(c + 16, 0, w[0]), ask(c + 16, 1, w[1]);
+                add(v[0], v[1]);
+                sum(v[0], c);
+                if (c + 16 < c1) {
+                  tmem_wait_ld();
+                  if (c + 32 < c1) ask(c + 32, 0, v[0]), ask(c + 32, 1, v[1]);
+                  add(w[0], w[1]);
+                  sum(w[0], c + 16);
+                }
               }
             }
           }
         } else if (!none) {
 #pragma unroll 1
           for (int c = c0; c < c1; c += 16) {
-            float v[16];
-            ask(c, v);
-            tmem_wait_ld();
-            rest(c, v);
+            float v[16];  // (never more than 128 rows: four parts)
+            all_of_four(c, v);
             const int r = CHUNK * ch + (qw >> 1) * (N / 2) + c;
             const int64_t row = (int64_t)s.lo * a.H + r;
             float *to = a.out + row * a.out_stride + p;
@@ -715,10 +722,10 @@ cudaError_t launch_sums(const KeySumArgs &a, const SumMaps &maps, cudaStream_t s
 bool row_maps(const KeySumArgs &a, SumMaps *maps) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     cuuint64_t dims[3] = {64, (cuuint64_t)(a.total * a.H), KB}, strides[2] = {TK * 2, 128};
-    cuuint32_t bx[3] = {64, (cuuint32_t)(16 * (i + 1)), QK}, es[3] = {1, 1, 1};
-    if (fn(&maps->q[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, bx, es,
+    cuuint32_t bx[3] = {64, (cuuint32_t)(16 * (i % 4 + 1)), (cuuint32_t)(i < 4 ? 1 : QK)}, es[3] = {1, 1, 1};
+    if (fn(i < 4 ? &maps->q[i] : &maps->q3[i - 4], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, bx, es,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return false;
