@@ -184,11 +184,12 @@ constexpr int MAX_CS = 8;                      // CTAs of a cluster
 static_assert(SEL_W == 16, "the groups' warps are counted in powers of two");
 
 // The scores of blocks begin .. end - 1 of a sequence with `rows` rows from row0 on: each row's softmax over
-// all of its blocks, summed over the rows, to `out` and, where given, to `here`.
+// all of its blocks, U of them on their way, summed over the rows, to `out` and, where given, to `here`.
 struct ScoreSpace {
   float lse[SC_ROWS];  // of rows, in units of log 2
   float part[SEL_W][SC_GROUP];
 };
+template <int U>
 __device__ __forceinline__ void block_scores(const SelectArgs &a, int row0, int rows, int count, int begin, int end, float *out, float *here,
                                              ScoreSpace &s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -198,34 +199,34 @@ __device__ __forceinline__ void block_scores(const SelectArgs &a, int row0, int 
   for (int r0 = 0; r0 < rows; r0 += SC_ROWS) {
     const int n = rows - r0 < SC_ROWS ? rows - r0 : SC_ROWS;
     const float *at = a.rows + (int64_t)(row0 + r0) * a.rows_stride;
-    // four rows' scores of this thread's blocks (up to three more are read inside a row's stride, and not used)
-    auto load = [&](int r, int b, float4 (&x)[4]) {
+    // U rows' scores of this thread's blocks (up to three more are read inside a row's stride, and not used)
+    auto load = [&](int r, int b, float4 (&x)[U]) {
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
+      for (int y = 0; y < U; ++y)
         x[y] = r + y * share < n && b < end ? load4(at + (int64_t)(r + y * share) * a.rows_stride + b)
                                             : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     };
-    float4 ahead[4];  // the first of them are on their way while the log-sums are merged
+    float4 ahead[U];  // the first of them are on their way while the log-sums are merged
     load(sub, begin + (warp >> (4 - log_gp)) * SC_GROUP + 4 * lane, ahead);
-    // a row's log-sum by a warp, four rows on their way
+    // a row's log-sum by a warp, U rows on their way
     const float2 *part = a.parts + (int64_t)(row0 + r0) * a.parts_stride;
-    for (int r = warp; r < n; r += 4 * SEL_W) {
-      float M[4], L[4];
+    for (int r = warp; r < n; r += U * SEL_W) {
+      float M[U], L[U];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) M[k] = -INFINITY, L[k] = 0.f;
+      for (int k = 0; k < U; ++k) M[k] = -INFINITY, L[k] = 0.f;
       for (int p = lane; p < pieces; p += 32) {
-        float2 x[4];
+        float2 x[U];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < U; ++k)
           x[k] = r + k * SEL_W < n ? part[(int64_t)(r + k * SEL_W) * a.parts_stride + p] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < U; ++k) {
           const float top = fmaxf(M[k], x[k].x), t = top == -INFINITY ? 0.f : top;
           L[k] = L[k] * exp2f(M[k] - t) + exp2f(x[k].x - t) * x[k].y, M[k] = top;
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < U; ++k) {
         const float top = warp_max(M[k]);
         const float sum = warp_sum(L[k] * exp2f(M[k] - (top == -INFINITY ? 0.f : top)));
         if (lane == 0 && r + k * SEL_W < n) s.lse[r + k * SEL_W] = top == -INFINITY && sum == 0.f ? 0.f : top + log2f(sum);
@@ -236,16 +237,16 @@ __device__ __forceinline__ void block_scores(const SelectArgs &a, int row0, int 
       const int b = begin + (g0 + (warp >> (4 - log_gp))) * SC_GROUP + 4 * lane;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       if (b < end)
-        for (int r = sub; r < n; r += 4 * share) {
-          float4 x[4];
+        for (int r = sub; r < n; r += U * share) {
+          float4 x[U];
           if (g0 == 0 && r == sub) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) x[y] = ahead[y];
+            for (int y = 0; y < U; ++y) x[y] = ahead[y];
           } else {
             load(r, b, x);
           }
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
+          for (int y = 0; y < U; ++y) {
             const float e = r + y * share < n ? s.lse[r + y * share] : 0.f;
             acc.x += exp2f(x[y].x - e), acc.y += exp2f(x[y].y - e), acc.z += exp2f(x[y].z - e), acc.w += exp2f(x[y].w - e);
           }
@@ -287,13 +288,14 @@ __device__ __forceinline__ bool step_of(const SelectArgs &a, int n, bool tell, B
 
 // Scores of `width` blocks a CTA, where a sequence may have more than one CTA takes along with its selection.
 constexpr int SC_WIDE = 4 * SC_GROUP;
-__global__ void __launch_bounds__(SEL_NT, 2) block_scores_kernel(const SelectArgs a, int width) {
+template <int U>
+__global__ void __launch_bounds__(SEL_NT, U > 4 ? 1 : 2) block_scores_kernel(const SelectArgs a, int width) {
   __shared__ __align__(16) ScoreSpace s_space;
   after_previous();
   const int n = blockIdx.y, begin = blockIdx.x * width;
   BlockStep s;
   if (!step_of(a, n, blockIdx.x == 0 && threadIdx.x == 0, s) || begin >= s.full) return;
-  block_scores(a, s.lo * a.H, s.W * a.H, s.full, begin, s.full < begin + width ? s.full : begin + width,
+  block_scores<U>(a, s.lo * a.H, s.W * a.H, s.full, begin, s.full < begin + width ? s.full : begin + width,
                a.scores + (size_t)n * a.stride, nullptr, s_space);
 }
 
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
       fits = (count < a.most ? count : a.most) + tail <= a.out_stride;
       if (!fits && rank == 0 && tid == 0) flag(a.c.err, ERR_BAD_INDEX);
       if (a.rows) {  // (a cluster of one CTA then)
-        block_scores(a, s.lo * a.H, s.W * a.H, count, 0, count, a.scores + (size_t)n * a.stride, s_scores, s_u.scores);
+        block_scores<4>(a, s.lo * a.H, s.W * a.H, count, 0, count, a.scores + (size_t)n * a.stride, s_scores, s_u.scores);
         value = s_scores;
       }
     }
@@ -794,10 +796,14 @@ cudaError_t launch_block_select(const SelectArgs &args, int *launches, cudaStrea
   // one CTA takes its sequence's scores along where they are few
   const double scores = (double)a.total * a.H * a.c.max_pages / a.n_seqs;
   if (a.rows && (a.c.max_pages > SC_WIDE || scores > 16384. || !a.out)) {
-    int width = SC_GROUP;  // as narrow as one wave of CTAs allows
-    while (width < SC_WIDE && (double)((a.c.max_pages + width - 1) / width) * a.n_seqs > 304.) width *= 2;
-    const cudaError_t e =
-        launch(block_scores_kernel, dim3((a.c.max_pages + width - 1) / width, a.n_seqs), 1, SEL_NT, 0, s, a, width);
+    // as narrow as one wave of CTAs allows: of one an SM with eight rows on their way (16 x 4 nodes, 512 blocks: the
+    // step 68 us, with four 71), else of two with four (256 x 1, 64 blocks: the call 18 us, with eight 23)
+    auto ctas = [&](int w) { return (double)((a.c.max_pages + w - 1) / w) * a.n_seqs; };
+    const bool few = ctas(SC_WIDE) <= 152.;
+    int width = SC_GROUP;
+    while (width < SC_WIDE && ctas(width) > (few ? 152. : 304.)) width *= 2;
+    const cudaError_t e = launch(few ? block_scores_kernel<8> : block_scores_kernel<4>,
+                                 dim3((a.c.max_pages + width - 1) / width, a.n_seqs), 1, SEL_NT, 0, s, a, width);
     if (e != cudaSuccess) return e;
     ++*launches;
     if (!a.out) return e;
