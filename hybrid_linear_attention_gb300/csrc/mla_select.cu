@@ -8,10 +8,11 @@
 //   selection          of `count` values: the first and the most recent are always taken, of the
 //                      others the largest, among equals the lower index first, ascending;
 //   eviction           a sequence keeps the selected positions; its rows move up in every layer.
-// A selection is bound by latency: a cluster of CTAs takes a row of values, finds the value that the
+// A selection is bound by latency: a CTA or a cluster of them takes a row of values, finds the value that the
 // last one taken has by up to three passes of 11 bits over order-preserving keys (counts in shared memory,
 // added up across the cluster), and writes what is taken by prefix sums.  Every sum is of whole numbers, so
-// the result does not depend on the order.  Blocks' scores are summed up right before, by the same CTAs.
+// the result does not depend on the order.  Blocks' scores are summed up right before, by the same CTA or, where
+// they are many, by a launch of their own.
 // The moves are bound by memory.
 #include "kda_common.cuh"
 #include "kda_internal.h"
@@ -607,8 +608,8 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
 // written once all of its reads, and so those of the batches before, are done.  kept[j] >= j and both
 // rise, so no later batch reads a row that an earlier one wrote.  A thread writes what it read itself; the
 // places of a batch are looked up two ahead of its reads.  (64 sequences of 2048 to 4096 positions cut to 2048,
-// nine layers: 440 us with the selection, 6.2 TB/s, 91 % of the copy rate; with the lookups on the way 540.  Wider
-// slices leave long sequences to fewer CTAs: 4 sequences cut to 16384 261 us, with 384 bytes 436, whole rows 819.)
+// nine layers: 435 us with the selection, 6.3 TB/s, 92 % of the copy rate; with the lookups on the way 540.  Wider
+// slices leave long sequences to fewer CTAs: 4 sequences cut to 16384 250 us, with 384 bytes 436, whole rows 819.)
 constexpr int MV_PIECES = 8, MV_ROWS = 36, MV_NT = MV_ROWS * MV_PIECES, MV_U = 4, MV_BATCH = MV_ROWS * MV_U, MV_STAGES = 4;
 constexpr int MV_SMEM = MV_STAGES * MV_BATCH * MV_PIECES * 16;
 __global__ void __launch_bounds__(MV_NT, 3) evict_rows_kernel(const PagedCache c, const int32_t *kept_all, int budget) {
@@ -773,8 +774,8 @@ cudaError_t opt_in(K kernel, int smem, std::atomic<bool> (&done)[64]) {
 }
 
 // CTAs of a selection: one for up to 16 values a thread (an exchange between the CTAs of a cluster costs
-// about as much as 16 values: 4 sequences x 65536 take 18 us by clusters of eight, 64 x 4096 10 by one CTA each and 16 by
-// four), as long as the GPU has room for the clusters (two CTAs an SM).
+// about as much as 16 values: 64 x 4096 take 10 us by one CTA each and 13 by four; 4 x 65536 by clusters of eight
+// 18), as long as the GPU has room for the clusters (two CTAs an SM).
 int select_ctas(int n_seqs, int64_t most_values) {
   int cs = 1;
   while (cs < MAX_CS && most_values > (int64_t)cs * SEL_NT * 16 && (int64_t)n_seqs * cs * 2 <= 304) cs *= 2;

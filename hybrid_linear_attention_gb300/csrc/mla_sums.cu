@@ -322,9 +322,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   const int lp = 31 - __clz(a.c.page_size);
 
   if (warp == W_KEYS || (BLOCKS && warp >= W_MORE)) {
-    // ---- key blocks: positions by tile loads, a lane each; blocks by 16-byte copies of their keys, 32 a
-    //      warp, the next tile's pages looked up meanwhile (gathers by TMA, four rows each, took three
-    //      times as long; one warp of copies twice)
+    // ---- key blocks: positions by tile loads, a lane each; blocks by 16-byte copies of their keys, 16 a
+    //      warp, the next tile's pages looked up meanwhile (gathers by TMA, four rows each, took
+    //      three times as long)
     auto known = [&](int page) { return page >= 0 && page < a.c.n_pages; };
     int tiles = 0;
     if constexpr (BLOCKS) {

@@ -108,6 +108,13 @@ def test_long_sequences_by_clusters(n, length, kind):
         c.check(c.run(budget, first=4, recent=32, new="own"), budget, first=4, recent=32, new="own")
 
 
+@pytest.mark.parametrize("width", [1025, 1026, 1027, 1039])
+def test_rows_of_weights_of_any_width(width):
+    c = Cache([1025, 700, 1, 999], layers=1, seed=width, width=width)
+    for budget in (1, 130, 513, 1024):
+        c.check(c.run(budget, first=1, new="own"), budget, first=1, new="own")
+
+
 @pytest.mark.parametrize("bit", range(0, 32, 3))
 def test_every_bit_counts(bit):
     """Weights that differ in a few neighbouring bits alone, whichever they are."""

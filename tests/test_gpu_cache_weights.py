@@ -285,3 +285,57 @@ def test_accepted_weights_follow_their_rows():
     want = w.clone()
     want[1, 7] = 0
     assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("length", [0, 5, 300])
+def test_one_row(length):
+    """One head of one node in the whole batch."""
+    case = Case([length], [1], H=1, page=16, seed=7)
+    given = true_lse(case)
+    check_weights(case, run_weights(case, given), given)
+    _, lse = run_lse(case)
+    check_lse(case, lse)
+
+
+def test_rows_of_any_width_and_padding_behind_the_last_sequence():
+    """weights rows that are no multiple of 16 bytes; query rows of no sequence behind the last."""
+    case = Case([100, 61], [2, 1], H=16, page=16, seed=8)
+    given = true_lse(case)
+    check_weights(case, run_weights(case, given, width=103), given)
+    case.q = torch.cat([case.q, torch.full_like(case.q, float("nan"))])
+    padded = torch.cat([given, torch.full_like(given, float("nan"))])
+    case.mask = case.mask + [0, 0, 0]
+    got = run_weights(case, padded, width=103)
+    kda.kda_check_device_error()
+    case.q, case.mask = case.q[:3], case.mask[:3]
+    check_weights(case, got, given)
+
+
+def test_a_pool_beyond_four_gigabytes():
+    _gpu.lib()
+    n_pages, page, H, length = 70000, 64, 16, 200
+    g = torch.Generator().manual_seed(3)
+    rows = torch.randn(4 * page, 576, generator=g).to(torch.bfloat16)
+    table = [n_pages - 1, 2, n_pages - 3, 5]
+    pool = torch.zeros(n_pages, page, 576, dtype=torch.bfloat16, device="cuda")
+    pool[table] = rows.view(4, page, 576).cuda()
+    q = torch.randn(1, H, 576, generator=g).to(torch.bfloat16)
+    paged = rows[None, :length + 1].contiguous()
+    given = torch.tensor(long.lse(q, paged, [[0]], [length], [0, 1], None, kda.MLA_SCALE)[0]).float()
+    want, tol = long.weights(q, paged, [[0]], [length], [0, 1], None, None, given.double().numpy(), kda.MLA_SCALE, 256)
+    w = torch.zeros(1, 256, device="cuda")
+    args = (pool, ref.i32([table]), ref.i32([length]))
+    kda.mla_cache_weights(q.cuda(), *args, ref.i32([0, 1]), given.cuda(), w)
+    assert (np.abs(w.double().cpu().numpy() - want) <= tol + 2.0**-24 * want).all()
+    keys = torch.zeros(1, n_pages, 576, dtype=torch.bfloat16, device="cuda")
+    kda.mla_block_keys(pool[None], args[1], ref.i32([256]), ref.i32([256]), keys)  # nothing filled up since
+    assert not keys.any()
+    kda.mla_block_keys(pool[None], args[1], ref.i32([0]), ref.i32([256]), keys)
+    mean = rows.double().view(4, page, 576).mean(1)
+    assert ((keys[0, table].double().cpu() - mean).abs() <= 2.0**-8 * mean.abs() + 1e-5).all()
+    kept, cut = torch.zeros(1, 90, dtype=torch.int32, device="cuda"), ref.i32([0])
+    kda.mla_cache_evict(pool[None], *args[1:], w, kept, cut, recent=9)
+    kda.kda_check_device_error()
+    chosen = long.choose(w[0].tolist(), length, 0, 9, 90)
+    assert kept[0].tolist() == chosen
+    assert torch.equal(pool[table[:2]].view(-1, 576)[:90].cpu(), rows[chosen])

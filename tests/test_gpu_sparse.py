@@ -123,6 +123,15 @@ def test_scores_of_wide_trees_and_many_sequences():
     check_scores(run_scores(b[0], b[1], 16, b[2], lengths, b[3]), b[0], b[1], 16, b[2], lengths, b[3])
 
 
+def test_scores_of_one_row_and_of_a_thousand_sequences():
+    b = block_batch([700], [1], H=1, page=16, seed=5)
+    check_scores(run_scores(b[0], b[1], 16, b[2], [700], b[3]), b[0], b[1], 16, b[2], [700], b[3])
+    rng = np.random.default_rng(5)
+    lengths = [int(x) for x in rng.integers(0, 200, 1000)]
+    b = block_batch(lengths, [1] * 1000, H=3, page=16, seed=5)
+    check_scores(run_scores(b[0], b[1], 16, b[2], lengths, b[3]), b[0], b[1], 16, b[2], lengths, b[3])
+
+
 def test_scores_report_what_is_bad():
     lengths, counts = [640, 640, 640], [1, 1, 1]
     q, keys, table, cu = block_batch(lengths, counts, seed=6)
