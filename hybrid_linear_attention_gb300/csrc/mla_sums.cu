@@ -156,7 +156,7 @@ __device__ __forceinline__ long long run_start(long long units, int c, int clust
 }
 
 template <bool BLOCKS>
-__device__ __forceinline__ int columns(const Seq &s, int chunk) {  // of a chunk's product, padded
+__host__ __device__ __forceinline__ int columns(const Seq &s, int chunk) {  // of a chunk's product, padded
   constexpr int pad = BLOCKS ? 63 : 31;
   const int r = s.rows - CHUNK * chunk;
   return r >= CHUNK ? CHUNK : (r + pad) & ~pad;
@@ -230,7 +230,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     mbar_fence_init();
   }
   if (tid == 64) s_abort = 0, s_n = 0, s_t = 0, s_at = 0;
-  if (tid >= 96 && tid < 105) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k + (tid - 96)) : "memory");
+  if (tid >= 96 && (tid == 96 ? !BLOCKS : tid < 105 && a.total * a.H > CHUNK))  // the maps that there are
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k + (tid - 96)) : "memory");
   if (warp == W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -718,12 +719,19 @@ cudaError_t launch_sums(const KeySumArgs &a, const SumMaps &maps, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, key_sums_kernel<BLOCKS>, a, maps);
 }
 
-// query rows as [9 blocks of 64 channels][rows], so that a load brings several blocks
+// query rows as [9 blocks of 64 channels][rows], so that a load brings several blocks; a batch of few rows needs the
+// small boxes alone (each map costs the host some 0.2 us)
+template <bool BLOCKS>
 bool row_maps(const KeySumArgs &a, SumMaps *maps) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
+  const int64_t rows = a.total * a.H;
+  const bool streams = rows > CHUNK;
+  Seq all = {};
+  all.rows = streams ? CHUNK : (int)rows;
   for (int i = 0; i < 8; ++i) {
-    cuuint64_t dims[3] = {64, (cuuint64_t)(a.total * a.H), KB}, strides[2] = {TK * 2, 128};
+    if (i < 4 ? !streams : 16 * (i - 3) > columns<BLOCKS>(all, 0) / 2) continue;
+    cuuint64_t dims[3] = {64, (cuuint64_t)rows, KB}, strides[2] = {TK * 2, 128};
     cuuint32_t bx[3] = {64, (cuuint32_t)(16 * (i % 4 + 1)), (cuuint32_t)(i < 4 ? 1 : QK)}, es[3] = {1, 1, 1};
     if (fn(i < 4 ? &maps->q[i] : &maps->q3[i - 4], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, bx, es,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -739,7 +747,7 @@ cudaError_t launch_cache_weights(const KeySumArgs &a, cudaStream_t s) {
   SumMaps maps;
   memset(&maps, 0, sizeof maps);
   const int box = a.c.page_size < 64 ? a.c.page_size : 64;
-  if (!row_maps(a, &maps) || !tree_map(&maps.k, a.c.pool, true, TK, a.c.page_size, a.c.n_pages, 64, box))
+  if (!row_maps<false>(a, &maps) || !tree_map(&maps.k, a.c.pool, true, TK, a.c.page_size, a.c.n_pages, 64, box))
     return cudaErrorInvalidValue;
   return launch_sums<false>(a, maps, s);
 }
@@ -747,8 +755,7 @@ cudaError_t launch_cache_weights(const KeySumArgs &a, cudaStream_t s) {
 cudaError_t launch_block_products(const KeySumArgs &a, cudaStream_t s) {
   SumMaps maps;
   memset(&maps, 0, sizeof maps);
-  if (!row_maps(a, &maps)) return cudaErrorInvalidValue;
-  maps.k = maps.q[0];  // not used: the keys come by copies
+  if (!row_maps<true>(a, &maps)) return cudaErrorInvalidValue;  // (no map of the keys: they come by copies)
   return launch_sums<true>(a, maps, s);
 }
 
