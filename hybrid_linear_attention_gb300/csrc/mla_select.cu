@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
   const int begin = cta_begin + tid * per < cta_end ? cta_begin + tid * per : cta_end;
   const int end = begin + per < cta_end ? begin + per : cta_end;
   const bool choose = count > most;
+  const int page_ahead = EVICT && choose && rank * SEL_NT + tid <= (count - 1) / page_size ? table[rank * SEL_NT + tid] : 0;
   // the keys of this thread's values in order, from registers where they fit
   uint32_t held[HELD] = {};
   const bool fit = per <= HELD;
@@ -412,13 +413,10 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
       for (int j = begin; j < end; ++j) f(j, order_key(value[j]));
     }
   };
-  // eviction: the last page that is not there, or is shared and would be written
-  int last_bad = -1;
-  if (EVICT && choose)
-    for (int j = rank * SEL_NT + tid; j <= (count - 1) / page_size; j += cs * SEL_NT) {
-      const int p = table[j];
-      if (!page_known(a.c, p) || (a.refs && j <= (most - 1) / page_size && a.refs[p] > 1)) last_bad = j;
-    }
+  // eviction: a page of the sequence's and its count, asked for now and looked at behind the counting
+  const int last_page = EVICT && choose ? (count - 1) / page_size : -1, first_look = rank * SEL_NT + tid;
+  const int page0 = first_look <= last_page ? page_ahead : 0;
+  const int ref0 = first_look <= last_page && a.refs && page_known(a.c, page0) ? a.refs[page0] : 0;
   if (tid == 0) s_end.taken = 0, s_end.gap = INT_MAX, s_end.bad = -1, s_gap = INT_MAX;
   if (choose) {
     need = most - a.first - a.recent;
@@ -495,6 +493,12 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
     }
     if (lane == 31) s_warp[warp] = x;
     if (EVICT) {
+      // the last page that is not there, or is shared and would be written
+      int last_bad = -1;
+      for (int j = first_look, p = page0, r = ref0; j <= last_page; j += cs * SEL_NT) {
+        if (j != first_look) p = table[j], r = a.refs && page_known(a.c, p) ? a.refs[p] : 0;
+        if (!page_known(a.c, p) || (r > 1 && j <= (most - 1) / page_size)) last_bad = j;
+      }
       gap = __reduce_min_sync(0xffffffffu, gap), last_bad = __reduce_max_sync(0xffffffffu, last_bad);
       if (lane == 0 && gap != INT_MAX) atomicMin(&s_end.gap, gap);
       if (lane == 0 && last_bad >= 0) atomicMax(&s_end.bad, last_bad);
@@ -510,7 +514,8 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
     mine = x - mine;
     if (cs > 1) cluster_sync();
     else __syncthreads();
-    gap = INT_MAX, last_bad = -1;
+    gap = INT_MAX;
+    int last_bad = -1;
     SelectEnd ends[MAX_CS];
 #pragma unroll
     for (int r = 0; r < MAX_CS; ++r)
@@ -618,7 +623,7 @@ __global__ void __launch_bounds__(MV_NT, 3) evict_rows_kernel(const PagedCache c
   const int n = blockIdx.z, layer = blockIdx.y, tid = threadIdx.x, r = tid / MV_PIECES;
   const int piece = blockIdx.x * MV_PIECES + tid % MV_PIECES;
   const int32_t *kept = kept_all + (size_t)n * budget;
-  if (kept[budget - 1] < budget) return;  // nothing moves (or the sequence is refused)
+  const int last = kept[budget - 1];
   const int32_t *table = c.table + (size_t)n * c.max_pages;
   uint4 *rows = reinterpret_cast<uint4 *>(c.pool) + (size_t)layer * c.n_pages * c.page_size * ROW16 + piece;
   const int lp = 31 - __clz(c.page_size), in_page = c.page_size - 1;
@@ -655,15 +660,29 @@ __global__ void __launch_bounds__(MV_NT, 3) evict_rows_kernel(const PagedCache c
       }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  look(0, then);
-  look_pages(0);
-  look(1, then);
-#pragma unroll 1
-  for (int b = 0; b < MV_STAGES - 1; ++b) {
-    read(b);
-    moves >>= MV_U;
-    look_pages(b + 1);
-    look(b + 2, then);
+  {  // the first batches' places all at once
+    int k[MV_STAGES + 1][MV_U], p[MV_STAGES][MV_U];
+#pragma unroll
+    for (int b = 0; b <= MV_STAGES; ++b) look(b, k[b]);
+    if (last < budget) return;  // nothing moves (or the sequence is refused)
+#pragma unroll
+    for (int b = 0; b < MV_STAGES; ++b)
+#pragma unroll
+      for (int y = 0; y < MV_U; ++y) {
+        if (k[b][y] <= row_of(b, y)) k[b][y] = -1;
+        p[b][y] = k[b][y] >= 0 ? table[k[b][y] >> lp] : 0;
+      }
+#pragma unroll
+    for (int b = 0; b < MV_STAGES; ++b) {
+#pragma unroll
+      for (int y = 0; y < MV_U; ++y) at[y] = k[b][y], page[y] = p[b][y];
+      if (b < MV_STAGES - 1) {
+        read(b);
+        moves >>= MV_U;
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < MV_U; ++y) then[y] = k[MV_STAGES][y];
   }
   look_to(0);
 #pragma unroll 1
