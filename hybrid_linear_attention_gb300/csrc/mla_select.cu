@@ -608,16 +608,18 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
   if (cs > 1) cluster_sync();  // its shared memory is not read by the others any more
 }
 
-// Row kept[j] of each sequence moves to row j, in every layer.  A CTA takes 128 bytes of the rows, 144
-// rows at a time, through a ring in shared memory of which all but one batch are on their way: a batch is
+// Row kept[j] of each sequence moves to row j, in every layer.  A CTA takes 128 bytes of the rows (64 or 32
+// where the GPU has room for as many CTAs at once: one sequence of 1024, nine layers, 15.0 us, with 128 17.1), 144
+// rows at a time (288, 576), through a ring in shared memory of which all but one batch are on their way: a batch is
 // written once all of its reads, and so those of the batches before, are done.  kept[j] >= j and both
 // rise, so no later batch reads a row that an earlier one wrote.  A thread writes what it read itself; the
 // places of a batch are looked up two ahead of its reads.  (64 sequences of 2048 to 4096 positions cut to 2048,
 // nine layers: 435 us with the selection, 6.3 TB/s, 92 % of the copy rate; with the lookups on the way 540.  Wider
 // slices leave long sequences to fewer CTAs: 4 sequences cut to 16384 250 us, with 384 bytes 436, whole rows 819.)
-constexpr int MV_PIECES = 8, MV_ROWS = 36, MV_NT = MV_ROWS * MV_PIECES, MV_U = 4, MV_BATCH = MV_ROWS * MV_U, MV_STAGES = 4;
-constexpr int MV_SMEM = MV_STAGES * MV_BATCH * MV_PIECES * 16;
+constexpr int MV_NT = 288, MV_U = 4, MV_STAGES = 4, MV_SMEM = MV_STAGES * MV_U * MV_NT * 16;
+template <int MV_PIECES>
 __global__ void __launch_bounds__(MV_NT, 3) evict_rows_kernel(const PagedCache c, const int32_t *kept_all, int budget) {
+  constexpr int MV_ROWS = MV_NT / MV_PIECES, MV_BATCH = MV_ROWS * MV_U;
   extern __shared__ uint4 ring[];  // [stage][MV_U][MV_NT]
   after_previous();
   const int n = blockIdx.z, layer = blockIdx.y, tid = threadIdx.x, r = tid / MV_PIECES;
@@ -840,10 +842,15 @@ cudaError_t launch_cache_evict(const SelectArgs &a, int *launches, cudaStream_t 
   cudaError_t e = launch(select_kernel<true>, dim3(a.n_seqs * cs), cs, SEL_NT, 0, s, a);
   if (e != cudaSuccess) return e;
   ++*launches;
-  static std::atomic<bool> opted[64];
-  e = opt_in(evict_rows_kernel, MV_SMEM, opted);
-  if (e != cudaSuccess) return e;
-  e = launch(evict_rows_kernel, dim3(ROW16 / MV_PIECES, a.c.n_layers, a.n_seqs), 1, MV_NT, MV_SMEM, s, a.c, a.out, a.most);
+  static std::atomic<bool> opted[3][64];
+  auto move = [&](auto kernel, int pieces, std::atomic<bool> (&done)[64]) {
+    const cudaError_t e = opt_in(kernel, MV_SMEM, done);
+    return e != cudaSuccess ? e : launch(kernel, dim3(ROW16 / pieces, a.c.n_layers, a.n_seqs), 1, MV_NT, MV_SMEM, s, a.c, a.out, a.most);
+  };
+  const int64_t units = (int64_t)a.n_seqs * a.c.n_layers;  // three CTAs an SM
+  e = units * (ROW16 / 2) <= 456   ? move(evict_rows_kernel<2>, 2, opted[0])
+      : units * (ROW16 / 4) <= 456 ? move(evict_rows_kernel<4>, 4, opted[1])
+                                   : move(evict_rows_kernel<8>, 8, opted[2]);
   ++*launches;
   return e;
 }
