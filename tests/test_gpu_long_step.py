@@ -208,6 +208,55 @@ def test_two_steps_at_once_on_two_streams():
         assert all(torch.equal(a, b) for a, b in zip(s.results(), w))
 
 
+def test_calls_in_a_row_share_their_buffers():
+    """Layer after layer with one selection, one score buffer and one workspace, and eviction after eviction
+    with one list of kept positions: each launch overlaps the end of the one before, and sees what it wrote."""
+    _gpu.lib()
+    g = torch.Generator(device="cuda").manual_seed(11)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    n, page, blocks, layers = 24, 32, 5, 6
+    lengths = [int(x) for x in np.random.default_rng(1).integers(200, 900, n)]
+    most = 30
+    table = torch.arange(n * most, dtype=torch.int32, device="cuda").view(n, most)
+    pool, q = r(layers, n * most, page, 576).to(torch.bfloat16), r(layers, n, 16, 576).to(torch.bfloat16)
+    keys = pool.float().mean(2).to(torch.bfloat16)
+    size = kda.mla_sparse_workspace_size(n, n, 16, most)
+    new = lambda: (torch.zeros(n, most, device="cuda"), torch.zeros(n, blocks + 3, dtype=torch.int32, device="cuda"),  # noqa: E731
+                   torch.zeros(n, dtype=torch.int32, device="cuda"), torch.empty(size, dtype=torch.uint8, device="cuda"))
+    cu, lens = ref.i32(list(range(n + 1))), ref.i32(lengths)
+
+    def step(y, z, scores, sel, cut, ws):
+        kda.mla_sparse_latent(q[y], pool[y], keys[y], table, lens, cu, scores, sel, cut, z, blocks=blocks, workspace=ws)
+
+    want = [torch.zeros(n, 16, 512, device="cuda") for _ in range(layers)]
+    for y in range(layers):
+        step(y, want[y], *new())
+        torch.cuda.synchronize()
+    shared = new()
+    for _ in range(20):
+        got = [torch.zeros(n, 16, 512, device="cuda") for _ in range(layers)]
+        torch.cuda.synchronize()
+        for y in range(layers):
+            step(y, got[y], *shared)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    weights = [torch.rand(n, most * page, generator=g, device="cuda") for _ in range(layers)]
+    pools = [r(1, n * most, page, 576).to(torch.bfloat16) for _ in range(layers)]
+    first = [p.clone() for p in pools]
+    kept, cut, moved = torch.zeros(n, 150, dtype=torch.int32, device="cuda"), torch.zeros_like(lens), torch.zeros_like(weights[0])
+    for y in range(layers):
+        kda.mla_cache_evict(pools[y], table, lens, weights[y], kept, cut, moved, recent=8)
+        torch.cuda.synchronize()
+    for _ in range(20):
+        again = [p.clone() for p in first]
+        torch.cuda.synchronize()
+        for y in range(layers):
+            kda.mla_cache_evict(again[y], table, lens, weights[y], kept, cut, moved, recent=8)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(again, pools))
+    kda.kda_check_device_error()
+
+
 def test_wrong_shapes_types_and_devices_are_refused():
     _gpu.lib()
     s = Step()
