@@ -181,6 +181,7 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
 
 constexpr int SEL_NT = 512, SEL_W = SEL_NT / 32, BINS = 2048;
 constexpr int SC_ROWS = 1024, SC_GROUP = 128;  // rows, blocks at a time
+constexpr int FEW = 16;                        // parts of a row's sum that a thread takes
 constexpr int MAX_CS = 8;                      // CTAs of a cluster
 static_assert(SEL_W == 16, "the groups' warps are counted in powers of two");
 
@@ -209,9 +210,23 @@ __device__ __forceinline__ void block_scores(const SelectArgs &a, int row0, int 
     };
     float4 ahead[U];  // the first of them are on their way while the log-sums are merged
     load(sub, begin + (warp >> (4 - log_gp)) * SC_GROUP + 4 * lane, ahead);
-    // a row's log-sum by a warp, U rows on their way
     const float2 *part = a.parts + (int64_t)(row0 + r0) * a.parts_stride;
-    for (int r = warp; r < n; r += U * SEL_W) {
+    // a row's log-sum by a thread where its parts are few, all of them on their way (16 x 4 rows of 64 heads,
+    // 256 to 512 blocks: the scores 22 -> 17 us) ...
+    for (int r = tid; pieces <= FEW && r < n; r += SEL_NT) {
+      float2 x[FEW];
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int p = 0; p < FEW; ++p) x[p] = p < pieces ? part[(int64_t)r * a.parts_stride + p] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int p = 0; p < FEW; ++p) M = fmaxf(M, x[p].x);
+      const float t = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int p = 0; p < FEW; ++p) L = fmaf(exp2f(x[p].x - t), x[p].y, L);
+      s.lse[r] = M == -INFINITY && L == 0.f ? 0.f : M + log2f(L);
+    }
+    // ... else by a warp, U rows on their way
+    for (int r = warp; pieces > FEW && r < n; r += U * SEL_W) {
       float M[U], L[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) M[k] = -INFINITY, L[k] = 0.f;
