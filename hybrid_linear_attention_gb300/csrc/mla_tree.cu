@@ -126,6 +126,13 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnArgs &a, int n, bool tell) {
   return s;
 }
 
+// Chunks of 64 positions of tile t that hold any (at least one: the first product writes Z).  Those behind
+// a sequence's last position are neither loaded for Z nor multiplied; their weights are 0.
+__device__ __forceinline__ int chunks_of(int end, int t) {
+  const int n = (end - TILE * t + 63) >> 6;
+  return n < 1 ? 1 : n > 4 ? 4 : n;
+}
+
 // This cluster's run of tiles, cut at the sequences' ends; every warp role walks it on its own.
 struct Walk {
   int n, off;    // place in sequence n's (pass, tile) order (at most 2^26 tiles)
@@ -347,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       limit = lane * box < TILE ? walk.s.end - lane * box : 0;
       int ahead = lookup(walk.t0);
       for (int t = walk.t0; t < walk.t1; ++t) {
-        const int page = ahead;
+        const int page = ahead, pieces = scores ? KB : 2 * chunks_of(walk.s.end, t);
         if (t + 1 < walk.t1) ahead = lookup(t + 1);
         if (scores && (page < 0 || page >= a.c.n_pages) && TILE * t < limit && a.err) atomicOr(a.err, ERR_BAD_INDEX);
         // no page, or behind the last node: past the pool, where loads give zeros
@@ -376,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
               }
             } else {
 #pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
+              for (int c = 0; c < pieces; ++c) {
                 const int g0 = p0 + 64 * (c >> 1), e0 = per * (c >> 1), ch = 256 * (int)rank + 128 * (c & 1);
                 const bool tail = g0 + 64 > walk.s.len && g0 < walk.s.end;  // warp 10 looks it over
                 if (wait(empty + j, par)) {
@@ -399,7 +406,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           else if (per == 2) load(std::integral_constant<int, 2>{});
           else load(std::integral_constant<int, 4>{});
         } else {
-          for (int y = 0; y < (scores ? KB : 8); ++y) step();
+          for (int y = 0; y < (scores ? KB : 8); ++y)
+            if (y < pieces) step();
         }
         __syncwarp();
       }
@@ -424,10 +432,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     int len1 = -1, end1 = 0, t1 = 0;
     auto look = [&](int len, int end, int t) {
       const int first = j0;
-      j0 = (j0 + 8) % NZ;
+      const int chunks = 2 * chunks_of(end, t);
+      j0 = (j0 + chunks) % NZ;
       if (TILE * (t + 1) <= len) return;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < chunks; ++c) {
         const int g0 = TILE * t + 64 * (c >> 1), j = (first + c) % NZ;
         if (g0 + 64 <= len || g0 >= end) continue;
         const bool ok = warp_wait(B_TAIL + j, (looked >> j) & 1);
@@ -521,10 +530,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       while (ok && walk.next(a)) {
         for (int t = walk.t0; t < walk.t1 && ok; ++t, ++i) {
           const bool first = t == walk.t0;
+          const int chunks = chunks_of(walk.s.end, t);
           if (!(ok = wait(B_SCALED, (uint32_t)i))) break;
           if (first && segs > 0 && !(ok = wait(B_ZFREE, (uint32_t)(segs - 1)))) break;
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {  // 64 positions, one half of the latents and then the other
+          for (int c = 0; c < 2 * chunks; ++c) {  // 64 positions, one half of the latents and then the other
             const int pc = c >> 1, h = c & 1;
             if (h == 0 && !(ok = wait(B_PFULL + pc, (uint32_t)i))) break;
             if (!(ok = wait(B_FULL_Z + j, par))) break;
@@ -538,6 +548,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
             if (h == 1) commit2(bar(B_PFREE + pc));
             if (++j == NZ) j = 0, par ^= 1;
           }
+#pragma unroll 1
+          for (int pc = chunks; pc < 4 && ok; ++pc)
+            if ((ok = wait(B_PFULL + pc, (uint32_t)i))) commit2(bar(B_PFREE + pc));
           if (!ok) break;
           commit2(bar(B_ZFULL));
         }
