@@ -127,7 +127,8 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnArgs &a, int n, bool tell) {
 }
 
 // Chunks of 64 positions of tile t that hold any (at least one: the first product writes Z).  Those behind
-// a sequence's last position are neither loaded for Z nor multiplied; their weights are 0.
+// a sequence's last position are neither loaded for Z nor multiplied, as their weights are 0 (256 sequences x
+// 1057 positions: 96 -> 91 us; leaving out the scores' loads there too slows every tile's: 64 x 8 nodes 157 -> 160).
 __device__ __forceinline__ int chunks_of(int end, int t) {
   const int n = (end - TILE * t + 63) >> 6;
   return n < 1 ? 1 : n > 4 ? 4 : n;
@@ -405,14 +406,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           if (per == 1) load(std::integral_constant<int, 1>{});
           else if (per == 2) load(std::integral_constant<int, 2>{});
           else load(std::integral_constant<int, 4>{});
-        } else {
-          for (int y = 0; y < (scores ? KB : 8); ++y)
-            if (y < pieces) step();
         }
         __syncwarp();
       }
     }
-    // every slot read before the CTA may end
+    // every slot read before the CTA may end (only the loading thread counted them: the same one is elected each time)
+    if (!elect()) j = 0, par = 0;
+    j = __reduce_add_sync(0xffffffffu, j), par = __reduce_add_sync(0xffffffffu, par);
     for (int y = 0; y < slots; ++y) {
       wait(empty + j, par);
       step();
