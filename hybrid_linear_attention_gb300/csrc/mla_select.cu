@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
 // written once all of its reads, and so those of the batches before, are done.  kept[j] >= j and both
 // rise, so no later batch reads a row that an earlier one wrote.  A thread writes what it read itself; the
 // places of a batch are looked up two ahead of its reads.  (64 sequences of 2048 to 4096 positions cut to 2048,
-// nine layers: 435 us with the selection, 6.3 TB/s, 92 % of the copy rate; with the lookups on the way 540.  Wider
+// nine layers: 430 us with the selection, 6.3 TB/s, 93 % of the copy rate; with the lookups on the way 540.  Wider
 // slices leave long sequences to fewer CTAs: 4 sequences cut to 16384 250 us, with 384 bytes 436, whole rows 819.)
 constexpr int MV_NT = 288, MV_U = 4, MV_STAGES = 4, MV_SMEM = MV_STAGES * MV_U * MV_NT * 16;
 template <int MV_PIECES>

@@ -32,7 +32,7 @@
 // peak; 290 to 304 us where calls follow one another for long (1.40 to 1.47 PFLOP/s: the power limit).
 // The rings' depth is what that rate needs: a slot less in either costs 11 to 35 %, one more (weights of
 // 128 positions at a time) gives back only what the smaller place for the weights costs.  With one node a
-// sequence the same loop streams the cache: 256 sequences of 2048 to 4096 positions 198 us, 4.8 TB/s, and 202 to
+// sequence the same loop streams the cache: 256 sequences of 2048 to 4096 positions 196 us, 4.8 TB/s, and 202 to
 // 211 among other calls (asking L2 for coming tiles, by bulk prefetches or by threads, measured slower: 247 to
 // 272 us).  There every byte of the cache still comes into shared memory 1.85 times, for the scores and for the
 // values, and with 64 heads half of the products' rows are empty.
