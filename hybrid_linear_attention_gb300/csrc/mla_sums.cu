@@ -22,6 +22,7 @@
 // about 2,900, with the epilogue beside them (8 sequences x 22 to 32 nodes x 8192 to 16384 positions: 150 us where
 // all count, 1.40 PFLOP/s; chunks of 256 rows, whose products fill a buffer of tensor memory each and so are one
 // sum over all channels, took 147 us and were up to 1.4e-6 off).  Few positions: latency, a launch of 8 us.
+#include "batch_sums.h"
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "mla_pair.cuh"
@@ -171,6 +172,21 @@ __device__ __forceinline__ int parts_of(int columns) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
 }
+// The CTA as sum_pass sees it.
+struct Threads {
+  int w, lane;
+  __device__ __forceinline__ int warp() const { return w; }
+  __device__ __forceinline__ bool last_lane() const { return lane == 31; }
+  __device__ __forceinline__ void barrier() const { __syncthreads(); }
+  __device__ __forceinline__ long long inclusive(long long x) const {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  }
+};
 template <int N>
 __device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -204,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   __shared__ __align__(8) uint64_t s_bar[B_N];
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_abort;
-  __shared__ long long s_scan[NT / 32];
+  __shared__ PassSums<NT / 32> s_scan;
   __shared__ int s_n, s_t;
   __shared__ Seq s_known[KNOWN];
   __shared__ long long s_at;
@@ -245,24 +261,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
   // ---- this cluster's run of the batch's units: sequences' units summed up, a thread each --------
   Seq mine = {};       // of the first NT sequences
   long long at = 0;    // units before this thread's sequence
+  int passes = 0;
   auto sum_up = [&](const Seq &s, long long &before) {  // returns the units before it, adds all to `before`
-    const long long cost = (long long)s.tiles * s.cost();
-    long long x = cost;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    x += before - cost;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-      const long long v = s_scan[w];
-      if (w < warp) x += v;
-      before += v;
-    }
-    return x;
+    return sum_pass(Threads{warp, lane}, s_scan, passes, (long long)s.tiles * s.cost(), before);
   };
   long long total = 0;
   for (int n0 = 0; n0 < a.n_seqs; n0 += NT) {
@@ -270,7 +271,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
     if (n0 + tid < a.n_seqs) s = seq_of<BLOCKS>(a, n0 + tid, blockIdx.x == 0);
     const long long x = sum_up(s, total);
     if (n0 == 0) mine = s, at = x;
-    else __syncthreads();
   }
   const long long begin = run_start(total, cid, clusters), stop = run_start(total, cid + 1, clusters);
   if (stop > begin) {  // the first tile whose first unit is at or behind `begin`
@@ -287,7 +287,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BLOCKS ? NTB : NTP, 
       for (int n0 = 0; n0 < a.n_seqs && before <= begin; n0 += NT) {
         Seq s = {};
         if (n0 + tid < a.n_seqs) s = seq_of<BLOCKS>(a, n0 + tid, false);
-        __syncthreads();
         const long long x = sum_up(s, before);
         if (n0 > 0) claim(s, x, n0 + tid);
       }
