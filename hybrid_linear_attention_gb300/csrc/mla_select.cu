@@ -324,7 +324,7 @@ __device__ __forceinline__ const T *of_cta(const T *p, int r, int cs) {
 // What a CTA tells the others of its cluster.
 struct __align__(16) SelectEnd {
   unsigned long long taken;  // taken for sure << 32 | equal to the threshold
-  int gap, bad;              // the first value that is not taken; the last page that must not move
+  int gap, bad;              // the first value that is not taken; the last page that may not be read or written
 };
 
 template <bool EVICT>
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
   __shared__ int s_need, s_equal, s_sums[SEL_W];
   __shared__ unsigned long long s_warp[SEL_W];
   __shared__ SelectEnd s_end;
-  __shared__ int s_gap;
+  __shared__ int s_gap, s_refuse;
   __shared__ __align__(16) float s_scores[EVICT ? 4 : SC_WIDE];  // computed here
   after_previous();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
   const int last_page = EVICT && choose ? (count - 1) / page_size : -1, first_look = rank * SEL_NT + tid;
   const int page0 = first_look <= last_page ? page_ahead : 0;
   const int ref0 = first_look <= last_page && a.refs && page_known(a.c, page0) ? a.refs[page0] : 0;
-  if (tid == 0) s_end.taken = 0, s_end.gap = INT_MAX, s_end.bad = -1, s_gap = INT_MAX;
+  if (tid == 0) s_end.taken = 0, s_end.gap = INT_MAX, s_end.bad = -1, s_gap = INT_MAX, s_refuse = 0;
   if (choose) {
     need = most - a.first - a.recent;
     if (need > 0) {
@@ -553,8 +553,30 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
       for (int r = 0; r < MAX_CS; ++r)
         if (r < cs) gap = min(gap, *of_cta(&s_gap, r, cs));
     }
-    // rows behind the first gap move: their pages have to be there, and nobody else's where they go
-    if (EVICT && last_bad >= gap / page_size) {  // the sequence stays as it is
+    // Rows behind the first gap move: their pages have to be there, and nobody else's where they go.  A page that is
+    // not there, or shared, behind the gap is seldom, and only then it is asked whether such a row needs it: from
+    // positions `gap` .. on where the rows go, and from each kept one behind it.
+    bool refused = false;
+    if (EVICT && last_bad >= gap / page_size) {
+      bool bad = false;
+      for (int j = gap / page_size + first_look; gap < most && j <= (most - 1) / page_size; j += cs * SEL_NT) {
+        const int p = table[j];
+        bad |= !page_known(a.c, p) || (a.refs && a.refs[p] > 1);
+      }
+      int equal = (int)(uint32_t)mine;
+      each([&](int j, uint32_t k) {
+        const int s = sort_of(j, k);
+        if (j > gap && (s == 2 || (s == 1 && equal < need))) bad |= !page_known(a.c, table[j / page_size]);
+        equal += s == 1;
+      });
+      if (bad) s_refuse = 1;
+      if (cs > 1) cluster_sync();
+      else __syncthreads();
+#pragma unroll
+      for (int r = 0; r < MAX_CS; ++r)
+        if (r < cs) refused |= *of_cta(&s_refuse, r, cs) != 0;
+    }
+    if (refused) {  // the sequence stays as it is
       for (int64_t j = rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT) out[j] = -1;
       if (a.new_values && a.new_values != a.values)
         for (int j = rank * SEL_NT + tid; j < count; j += cs * SEL_NT) a.new_values[(size_t)n * a.stride + j] = value[j];
