@@ -374,6 +374,8 @@ __global__ void __launch_bounds__(SEL_NT, 2) select_kernel(const SelectArgs a) {
   int32_t *out = a.out + (size_t)n * a.out_stride;
   if (!ok || !fits) {
     for (int64_t j = rank * SEL_NT + tid; j < a.out_stride; j += cs * SEL_NT) out[j] = -1;
+    if (EVICT && a.new_values && a.new_values != a.values)  // how many of them count is not known: the whole row
+      for (int64_t j = rank * SEL_NT + tid; j < a.stride; j += cs * SEL_NT) a.new_values[(size_t)n * a.stride + j] = value[j];
     if (rank == 0 && tid == 0) {
       if (EVICT) flag(a.c.err, ERR_BAD_INDEX);
       a.out_lengths[n] = EVICT ? len : 0;

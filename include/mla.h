@@ -350,7 +350,8 @@ kda_status mla_weights_accept(float* weights, int64_t weights_stride, const int3
  * call.  A sequence with a bad length (below 0, more than the table row or weights_stride hold), a
  * row that would move from or to a position without a page, or into a shared page keeps its rows, length
  * and weights, has a `kept` row of -1 and is reported (KDA_ERR_BAD_INDEX); other pages may be missing or
- * shared.  Keys of pages that the rows moved into are written anew by mla_block_keys.
+ * shared.  A new_weights of its own gets such a sequence's weights up to its length, the whole row where that is
+ * bad.  Keys of pages that the rows moved into are written anew by mla_block_keys.
  */
 kda_status mla_cache_evict(void* pool, int n_layers, int n_pages, int page_size,
                            const int32_t* page_table, int max_pages, const int32_t* lengths,
