@@ -547,9 +547,12 @@ static kda_status sparse_step(const void *q_cat, int H, const void *pool, const 
                               int32_t *sel_lengths, void *z, kda_dtype z_dtype, void *workspace, size_t ws_bytes,
                               SparseStep *s) {
   std::memset(&s->choice, 0, sizeof s->choice);
-  kda_status st = block_select(scores, scores_stride, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs, total_nodes,
-                               blocks, first, recent, sel_table, sel_pages, sel_lengths, &s->choice);
-  if (st != KDA_OK && total_nodes != 0) return st;
+  if (check_choice(blocks, first, recent) != KDA_OK) return KDA_ERR_INVALID_ARG;  // without nodes too
+  kda_status st = KDA_OK;
+  if (total_nodes != 0)
+    st = block_select(scores, scores_stride, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs, total_nodes, blocks, first,
+                      recent, sel_table, sel_pages, sel_lengths, &s->choice);
+  if (st != KDA_OK) return st;
   st = block_scores(q_cat, H, keys, n_pages, page_size, page_table, max_pages, lengths, cu_nodes, n_seqs, total_nodes, scale,
                     scores, scores_stride, workspace, ws_bytes, &s->scores, &s->choice);
   if (st != KDA_OK || total_nodes == 0) return st;

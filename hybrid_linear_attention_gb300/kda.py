@@ -1019,7 +1019,8 @@ def mla_sparse_workspace_size(n_seqs, total_nodes, H, max_pages):
 def mla_sparse_latent(q_cat, pool, keys, page_table, lengths, cu_nodes, scores, sel_table,
                       sel_lengths, z, *, blocks, first=0, recent=0, mask=None, scale=MLA_SCALE,
                       workspace=None, stream=None):
-    """mla_block_scores, mla_block_select and mla_tree_latent over the chosen pages."""
+    """mla_block_scores, mla_block_select and mla_tree_latent over the chosen pages.  Without nodes nothing
+    is written, the selection neither."""
     dev = _device()
     total, H, n = q_cat.shape[0], q_cat.shape[1], cu_nodes.numel() - 1
     _shape(q_cat, (total, H, 576), "q_cat")

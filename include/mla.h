@@ -435,7 +435,9 @@ size_t mla_sparse_workspace_size(int n_seqs, int64_t total_nodes, int H, int max
 /*
  * mla_sparse_latent -- mla_block_scores, mla_block_select and mla_tree_latent over the selection in
  * one call.  keys is the layer's [n_pages, 576]; scores, sel_table and sel_lengths are caller-owned and
- * hold what those calls write; workspace: at least mla_sparse_workspace_size() bytes.
+ * hold what those calls write; workspace: at least mla_sparse_workspace_size() bytes.  A call without nodes
+ * (total_nodes = 0) launches nothing: z, scores, sel_table and sel_lengths stay as they were
+ * (mla_block_select, on its own, then writes empty rows).
  */
 kda_status mla_sparse_latent(const void* q_cat, int H, const void* pool, const void* keys,
                              int n_pages, int page_size, const int32_t* page_table, int max_pages,
