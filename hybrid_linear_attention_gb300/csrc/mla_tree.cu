@@ -69,7 +69,8 @@ constexpr uint32_t TM_Z = 0, TM_S = 256;  // Z: two products of 128 columns; S: 
 // and looks over a sequence's last chunks, 11 arrives for the softmax warps of a CTA without rows, 12
 // and 13 issue the score and the value products
 constexpr int W_LOAD_S = 8, W_LOAD_Z = 9, W_HELP = 10, W_TELL = 11, W_SCORE = 12, W_VALUE = 13, NT = 448;
-constexpr int MAX_CLUSTERS = 80;     // of two CTAs (152 SMs: 76)
+constexpr int PLACES = 80;           // for partial sums, of a pair of CTAs each; the last one's holds sums of exponentials
+constexpr int MAX_CLUSTERS = PLACES - 1;  // of two CTAs (152 SMs: 76)
 constexpr float LAZY = 8.f;          // log2 of how far a row's scores may rise above its reference
 
 // barriers; L: the leading CTA's are used by both
@@ -887,13 +888,15 @@ __global__ void __launch_bounds__(CNT) tree_combine_kernel(const TreeAttnArgs a,
   }
 }
 
-constexpr size_t PART = (size_t)MAX_CLUSTERS * 2 * 2 * RC * TL * sizeof(float);
-constexpr size_t PART_E = (size_t)MAX_CLUSTERS * 2 * 2 * RC * sizeof(float);
-constexpr size_t PART_ML = (size_t)MAX_CLUSTERS * 2 * 2 * RC * 2 * sizeof(float);
+constexpr size_t PART_1 = (size_t)2 * 2 * RC * TL * sizeof(float), PART = PLACES * PART_1;
+constexpr size_t PART_ML = (size_t)PLACES * 2 * 2 * RC * 2 * sizeof(float);
+// the rows' sums of exponentials lie where no cluster leaves partial sums, so the calls that leave log-sums need no
+// more workspace than the others
+static_assert((size_t)MAX_CLUSTERS * 2 * 2 * RC * sizeof(float) <= PART_1, "the last place holds them");
 
 }  // namespace
 
-size_t mla_tree_ws_bytes(int, int64_t, int) { return PART + PART_ML + MAX_CLUSTERS * sizeof(Merge) + PART_E; }
+size_t mla_tree_ws_bytes(int, int64_t, int) { return PART + PART_ML + PLACES * sizeof(Merge); }
 
 template <bool LSE>
 static cudaError_t launch_tree_attention(const TreeAttnArgs &a, int *launches, cudaStream_t s) {
@@ -905,7 +908,7 @@ static cudaError_t launch_tree_attention(const TreeAttnArgs &a, int *launches, c
   if (!tree_map(&maps.q, a.q, true, TK, rows, 1, 64, rows < RC ? (int)rows : RC) ||
       !tree_map(&maps.c, a.c.pool, true, TK, a.c.page_size, a.c.n_pages, 64, box) ||
       !tree_map(&maps.z, a.z, a.z_bf16, TL, rows, 1, a.z_bf16 ? 32 : 16, rows < 32 ? (int)rows : 32) ||
-      !tree_map(&maps.part, a.ws, false, TL, MAX_CLUSTERS * 2 * 2 * RC, 1, 16, 32))
+      !tree_map(&maps.part, a.ws, false, TL, PLACES * 2 * 2 * RC, 1, 16, 32))
     return cudaErrorInvalidValue;
   int dev = 0, nsm = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -922,7 +925,7 @@ static cudaError_t launch_tree_attention(const TreeAttnArgs &a, int *launches, c
   float *part = reinterpret_cast<float *>(a.ws);
   float *part_ml = reinterpret_cast<float *>(reinterpret_cast<char *>(a.ws) + PART);
   Merge *merge = reinterpret_cast<Merge *>(reinterpret_cast<char *>(a.ws) + PART + PART_ML);
-  float *part_e = reinterpret_cast<float *>(merge + MAX_CLUSTERS);
+  float *part_e = reinterpret_cast<float *>(reinterpret_cast<char *>(a.ws) + MAX_CLUSTERS * PART_1);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute early;  // each launch overlaps the end of the kernel before
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
