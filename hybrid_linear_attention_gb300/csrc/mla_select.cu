@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(BK_NT, 3) block_keys_kernel(const PagedCache c
       if (w < warp) x += s_warp[w];
       all += s_warp[w];
     }
-    s_end[tid] = x, s_first[tid] = first;  // at most 288 x 2^20 pages
+    s_end[tid] = x, s_first[tid] = first;  // at most 320 x 2^20 pages
     __syncthreads();
     // page of unit u; past the last unit, or where there is none: -1
     auto look = [&](int u) {

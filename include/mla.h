@@ -211,8 +211,8 @@ kda_status mla_pages_reserve(int n_pages, int page_size, int32_t* refcount, int3
 kda_status mla_tree_mask(const int32_t* parent, const int32_t* cu_nodes, int n_seqs,
                          int64_t total_nodes, int64_t* mask, cudaStream_t stream);
 
-/* Device workspace of mla_tree_latent and mla_tree_decode (H heads; 64 for mla_tree_decode);
- * 0 for invalid arguments. */
+/* Device workspace of mla_tree_latent and mla_tree_decode, and of those with lse (H heads; 64 for
+ * mla_tree_decode); 0 for invalid arguments. */
 size_t mla_tree_workspace_size(int n_seqs, int64_t total_nodes, int H);
 
 /*
@@ -325,7 +325,8 @@ kda_status mla_cache_weights(const void* q_cat, int H, const void* pool, int n_p
  *   mla_cache_accept.
  * A sequence with bad offsets or more than 64 nodes (KDA_ERR_BAD_SEQLENS), an accept_node outside
  * -1 .. nodes - 1, or a length below 0 or with which the nodes pass weights_stride (KDA_ERR_BAD_INDEX) keeps
- * its weights and is reported; a bad parent is reported and counts as none.
+ * its weights and is reported; a bad parent is reported and counts as none.  Pages are not looked at: of a
+ * path that mla_cache_accept refuses for a page that is not there the weights move all the same.
  */
 kda_status mla_weights_accept(float* weights, int64_t weights_stride, const int32_t* lengths,
                               const int32_t* cu_nodes, int n_seqs, int64_t total_nodes,
